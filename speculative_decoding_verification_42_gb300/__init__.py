@@ -8,11 +8,16 @@ raises.
 
 ``Verifier`` is a convenience wrapper that takes torch tensors (device memory
 and the current CUDA stream come from PyTorch) and calls the same entry points.
+``TreeCache`` (tree.py) does the same for the operators around the verify step,
+declared in ``include/spec_tree.h``.
 """
 from __future__ import annotations
 
 import ctypes as C
 import os
+
+from . import tree as _tree
+from .tree import *  # noqa: F401,F403  (the operators of include/spec_tree.h)
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libspec_verify.so")
@@ -25,11 +30,12 @@ SPEC_DRAFT_LOGITS, SPEC_DRAFT_PROBS = 0, 1
 SPEC_ROW_OK, SPEC_ROW_BAD_TOKEN, SPEC_ROW_BAD_K, SPEC_ROW_NONFINITE, \
     SPEC_ROW_ZERO_RESIDUAL = range(5)
 
-# every function the header declares (checked by the tests)
+# every function the headers declare (checked by the tests)
 ABI_FUNCTIONS = ("spec_verify_create", "spec_verify_run", "spec_draft_sample",
                  "spec_verify_destroy", "spec_verify_status_string", "spec_verify_run_noalloc",
                  "spec_verify_set_profiling", "spec_lmhead_logits", "spec_verify_run_early_exit",
-                 "spec_verify_check", "spec_verify_inject_fault", "spec_verify_set_allocator")
+                 "spec_verify_check", "spec_verify_inject_fault", "spec_verify_set_allocator") + \
+    _tree.TREE_FUNCTIONS
 SPEC_FAULT_NONE, SPEC_FAULT_STALL_STREAM = 0, 1
 
 # spec_alloc_fn / spec_release_fn of spec_verify_set_allocator
@@ -112,6 +118,7 @@ def load_library(path: str | None = None) -> C.CDLL:
     L.spec_verify_inject_fault.restype = C.c_int
     L.spec_verify_set_allocator.argtypes = [SPEC_ALLOC_FN, SPEC_RELEASE_FN, C.c_void_p]
     L.spec_verify_set_allocator.restype = C.c_int
+    _tree.bind(L)
     if path is None:
         _lib = L
     return L

@@ -16,7 +16,8 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libspec_verify.so")
 BUILD_DIR = os.path.join(HERE, "_build")
-SOURCES = ["sv_rows.cu", "sv_sample.cu", "sv_api.cu", "sv_noalloc.cu", "sv_lmhead.cu"]
+SOURCES = ["sv_rows.cu", "sv_sample.cu", "sv_api.cu", "sv_noalloc.cu", "sv_lmhead.cu",
+           "sv_tree_api.cu", "sv_tree_rows.cu", "sv_tree_attend.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE,
               "-Xptxas", "-warn-spills"]
@@ -31,7 +32,7 @@ def _nvcc() -> str:
 
 def _deps():
     files = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
-    files.append(os.path.join(INCLUDE, "spec_verify.h"))
+    files += [os.path.join(INCLUDE, f) for f in os.listdir(INCLUDE)]
     files.append(os.path.abspath(__file__))
     return files
 

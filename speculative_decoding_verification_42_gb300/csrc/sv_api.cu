@@ -9,6 +9,7 @@
 #include <mutex>
 #include <new>
 
+#include "sv_host.h"
 #include "sv_internal.cuh"
 #include "spec_verify.h"
 
@@ -44,10 +45,7 @@ struct spec_verify {
     int32_t* prof_launches;
     float* logits;        // the LM head's output (SPEC_TARGET_HIDDEN_LMHEAD), else NULL
     int fault;            // spec_verify_inject_fault: the fault armed for the next run
-    // where the workspace came from (NULL: cudaMalloc / cudaFree)
-    spec_alloc_fn alloc_fn;
-    spec_release_fn release_fn;
-    void* alloc_ctx;
+    Workspace mem;        // where the workspace came from
 };
 
 namespace {
@@ -56,22 +54,6 @@ int elem_size(int dtype) { return dtype == SPEC_BF16 ? 2 : 4; }
 int seg_elems(int dtype) { return SEG_BYTES / elem_size(dtype); }
 int chunk_elems(int dtype) { return CHUNK_BYTES / elem_size(dtype); }
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
-
-struct DeviceGuard {
-    int prev = -1;
-    bool ok = false;
-    explicit DeviceGuard(int dev)
-    {
-        if (cudaGetDevice(&prev) != cudaSuccess) return;
-        ok = (prev == dev) || cudaSetDevice(dev) == cudaSuccess;
-    }
-    ~DeviceGuard()
-    {
-        if (prev >= 0) cudaSetDevice(prev);
-    }
-};
-
-bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 
 // spec_verify_set_allocator: the functions later handles take their workspace from
 struct AllocHook {
@@ -243,6 +225,50 @@ void use_key_histograms(Params& p, int dtype, bool vec)
 
 }  // namespace
 
+namespace sv {
+
+spec_status workspace_take(Workspace* w, int device, size_t bytes)
+{
+    {
+        AllocHook& hook = alloc_hook();
+        std::lock_guard<std::mutex> lock(hook.mu);
+        *w = Workspace{nullptr, hook.alloc, hook.release, hook.ctx};
+    }
+    void* base = nullptr;
+    if (w->alloc_fn) {
+        if (w->alloc_fn(w->ctx, (uint64_t)bytes, device, &base) != 0 || !base) return SPEC_ERR_OOM;
+        if ((uintptr_t)base & 255u) {  // the sub-buffers need 256-byte alignment
+            w->release_fn(w->ctx, base, device);
+            return SPEC_ERR_INVALID_ARG;
+        }
+    } else if (cudaMalloc(&base, bytes) != cudaSuccess) {
+        cudaGetLastError();
+        return SPEC_ERR_OOM;
+    }
+    if (cudaMemset(base, 0, bytes) != cudaSuccess) {
+        if (w->alloc_fn) w->release_fn(w->ctx, base, device);
+        else cudaFree(base);
+        return SPEC_ERR_CUDA;
+    }
+    w->base = base;
+    return SPEC_OK;
+}
+
+spec_status workspace_give(Workspace* w, int device)
+{
+    spec_status st = SPEC_OK;
+    if (w->base && w->release_fn) {
+        if (cudaDeviceSynchronize() != cudaSuccess) st = SPEC_ERR_CUDA;
+        w->release_fn(w->ctx, w->base, device);
+    } else if (w->base && cudaFree(w->base) != cudaSuccess) {
+        st = SPEC_ERR_CUDA;
+    }
+    w->base = nullptr;
+    return st;
+}
+
+}  // namespace sv
+
 extern "C" {
 
 const char* spec_verify_status_string(spec_status s)
@@ -306,36 +332,12 @@ spec_status spec_verify_create(const spec_verify_config* cfg, spec_verify_t* out
         return SPEC_ERR_INVALID_ARG;
     }
     h->ws_bytes = layout_workspace(h, nullptr);
-    {
-        AllocHook& hook = alloc_hook();
-        std::lock_guard<std::mutex> lock(hook.mu);
-        h->alloc_fn = hook.alloc;
-        h->release_fn = hook.release;
-        h->alloc_ctx = hook.ctx;
-    }
-    void* base = nullptr;
-    if (h->alloc_fn) {
-        if (h->alloc_fn(h->alloc_ctx, (uint64_t)h->ws_bytes, cfg->device, &base) != 0 || !base) {
-            delete h;
-            return SPEC_ERR_OOM;
-        }
-        if ((uintptr_t)base & 255u) {  // the sub-buffers need 256-byte alignment
-            h->release_fn(h->alloc_ctx, base, cfg->device);
-            delete h;
-            return SPEC_ERR_INVALID_ARG;
-        }
-    } else if (cudaMalloc(&base, h->ws_bytes) != cudaSuccess) {
-        cudaGetLastError();
+    const spec_status st = workspace_take(&h->mem, cfg->device, h->ws_bytes);
+    if (st != SPEC_OK) {
         delete h;
-        return SPEC_ERR_OOM;
+        return st;
     }
-    if (cudaMemset(base, 0, h->ws_bytes) != cudaSuccess) {
-        if (h->alloc_fn) h->release_fn(h->alloc_ctx, base, cfg->device);
-        else cudaFree(base);
-        delete h;
-        return SPEC_ERR_CUDA;
-    }
-    layout_workspace(h, base);
+    layout_workspace(h, h->mem.base);
     *out = h;
     return SPEC_OK;
 }
@@ -582,12 +584,7 @@ spec_status spec_verify_destroy(spec_verify_t h)
     {
         DeviceGuard g(h->cfg.device);
         if (!g.ok) st = SPEC_ERR_CUDA;
-        if (h->ws && h->release_fn) {
-            if (cudaDeviceSynchronize() != cudaSuccess) st = SPEC_ERR_CUDA;
-            h->release_fn(h->alloc_ctx, h->ws, h->cfg.device);
-        } else if (h->ws && cudaFree(h->ws) != cudaSuccess) {
-            st = SPEC_ERR_CUDA;
-        }
+        if (workspace_give(&h->mem, h->cfg.device) != SPEC_OK) st = SPEC_ERR_CUDA;
     }
     delete h;
     return st;
