@@ -195,8 +195,9 @@ spec_status spec_tree_append(spec_tree_t h, const spec_tree_append_args* a, void
  * row and lse = -inf; so has every node of a sequence with ctx < 0, n outside
  * [0, T] or ctx + n beyond the table.  Scores, sums and outputs accumulate in
  * fp32; the probabilities are rounded to the 16-bit type before they meet V.
- * SPEC_ERR_UNSUPPORTED when q, the cache, out or lse is not on 16 bytes or a
- * stride is not a multiple of 8 elements (or is beyond 2^36). */
+ * SPEC_ERR_UNSUPPORTED when q, the cache, out or lse is not on 16 bytes, a
+ * stride is not a multiple of 8 elements (or is beyond 2^36), or is 0 for a
+ * dimension larger than 1. */
 typedef struct {
     spec_tree_rows q;
     spec_tree_cache cache;

@@ -28,6 +28,7 @@
 #include <algorithm>
 
 #include "sv_internal.cuh"
+#include "sv_tcgen.cuh"
 #include "spec_verify.h"
 
 namespace sv {
@@ -343,14 +344,9 @@ __global__ void __launch_bounds__(LM_THREADS, 1)
 // ------------------------------------------------------------------------- //
 // host side                                                                 //
 // ------------------------------------------------------------------------- //
-using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                 const cuuint64_t*, const cuuint32_t*, const cuuint32_t*,
-                                 CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion,
-                                 CUtensorMapFloatOOBfill);
-
-static EncodeTiled encoder()
+EncodeTiledFn tensor_map_encoder()
 {
-    static EncodeTiled fn = nullptr;
+    static EncodeTiledFn fn = nullptr;
     if (!fn) {
         void* p = nullptr;
         cudaDriverEntryPointQueryResult q;
@@ -358,7 +354,7 @@ static EncodeTiled encoder()
                 cudaSuccess ||
             q != cudaDriverEntryPointSuccess)
             return nullptr;
-        fn = reinterpret_cast<EncodeTiled>(p);
+        fn = reinterpret_cast<EncodeTiledFn>(p);
     }
     return fn;
 }
@@ -368,7 +364,7 @@ static EncodeTiled encoder()
 static bool bf16_map(CUtensorMap* map, const void* ptr, int64_t rows, int64_t cols, int box_cols,
                      int box_rows)
 {
-    EncodeTiled enc = encoder();
+    EncodeTiledFn enc = tensor_map_encoder();
     if (!enc) return false;
     const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
     const cuuint64_t strides[1] = {(cuuint64_t)cols * 2};

@@ -86,8 +86,6 @@ struct TreeAppendParams {
     void* q_out;
 };
 
-// where a CTA's range of key tiles begins inside a work item, for the merge of
-// the item's parts
 struct TreeAttendParams {
     TreeShape s;
     TreeRows q;
@@ -112,7 +110,11 @@ struct TreeKeepParams {
 
 cudaError_t launch_tree_plan(TreePlanParams p, int num_sms, cudaStream_t s);
 cudaError_t launch_tree_append(const TreeAppendParams& p, int dtype, cudaStream_t s);
-cudaError_t launch_tree_attend(const TreeAttendParams& p, int dtype, int num_sms, cudaStream_t s);
+// bytes of workspace for `ctas` CTAs, and where in it the (m, l) and the cuts begin
+size_t tree_attend_bytes(int D, int ctas, size_t* ml_at, size_t* cut_at);
+// err: bit 0 set when a bounded wait ran out; stall: issue no copy
+cudaError_t launch_tree_attend(const TreeAttendParams& p, int dtype, int num_sms, void* ws, unsigned* err, bool stall,
+                               cudaStream_t s);
 cudaError_t launch_tree_keep(const TreeKeepParams& p, cudaStream_t s);
 
 // 16-bit element types: unpacking two of a word, packing, converting

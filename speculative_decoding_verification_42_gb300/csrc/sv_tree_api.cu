@@ -16,7 +16,8 @@ struct spec_tree {
     int num_sms;
     int fault;  // spec_tree_inject_fault: the fault armed for the next attend
     Workspace mem;
-    unsigned* err;
+    unsigned* err;   // bounded waits that ran out (0 = none)
+    void* parts;     // partial sums of spec_tree_attend
 };
 
 namespace {
@@ -78,13 +79,15 @@ spec_status spec_tree_create(const spec_tree_config* cfg, spec_tree_t* out)
     h->cfg = *cfg;
     while ((1 << h->page_log2) < cfg->page_size) ++h->page_log2;
     spec_status st = SPEC_ERR_CUDA;
+    size_t at;
     if (cudaDeviceGetAttribute(&h->num_sms, cudaDevAttrMultiProcessorCount, cfg->device) == cudaSuccess)
-        st = workspace_take(&h->mem, cfg->device, 256);
+        st = workspace_take(&h->mem, cfg->device, 256 + tree_attend_bytes(cfg->head_dim, h->num_sms, &at, &at));
     if (st != SPEC_OK) {
         delete h;
         return st;
     }
     h->err = (unsigned*)h->mem.base;
+    h->parts = (char*)h->mem.base + 256;
     *out = h;
     return SPEC_OK;
 }
@@ -196,6 +199,12 @@ spec_status spec_tree_attend(spec_tree_t h, const spec_tree_attend_args* a, void
         return SPEC_ERR_INVALID_ARG;
     if (!rows_ok(a->q) || !cache_ok(a->cache) || !aligned16(a->out) || !aligned16(a->lse))
         return SPEC_ERR_UNSUPPORTED;
+    // tensor maps: a stride of 0 only where there is one element
+    const spec_tree_config& c = h->cfg;
+    if ((a->batch > 1 && !a->q.seq_stride) || (a->tokens > 1 && !a->q.token_stride) ||
+        (c.q_heads > 1 && !a->q.head_stride) || (c.num_pages > 1 && !a->cache.page_stride) ||
+        (c.page_size > 1 && !a->cache.token_stride) || (c.kv_heads > 1 && !a->cache.head_stride))
+        return SPEC_ERR_UNSUPPORTED;
     DeviceGuard g(h->cfg.device);
     if (!g.ok) return SPEC_ERR_CUDA;
     TreeAttendParams p = {};
@@ -208,7 +217,9 @@ spec_status spec_tree_attend(spec_tree_t h, const spec_tree_attend_args* a, void
     p.scale = a->scale;
     p.out = a->out;
     p.lse = a->lse;
-    return launched(launch_tree_attend(p, h->cfg.dtype, h->num_sms, (cudaStream_t)stream));
+    const bool stall = h->fault == SPEC_FAULT_STALL_STREAM;
+    h->fault = SPEC_FAULT_NONE;
+    return launched(launch_tree_attend(p, h->cfg.dtype, h->num_sms, h->parts, h->err, stall, (cudaStream_t)stream));
 }
 
 spec_status spec_tree_keep(spec_tree_t h, const spec_tree_keep_args* a, void* stream)

@@ -386,6 +386,23 @@ def test_attend_is_deterministic_and_stream_ordered(sv):
     tc.close()
 
 
+def test_stalled_attend_reports_and_recovers(sv):
+    import torch
+    rng = np.random.default_rng(12)
+    tc = _tc(sv, 1, 2, 4, 2, 64, 16, 8, 8)
+    kc, vc = _layout(rng, 8, 16, 2, 64, "bf16", "tokens")
+    args = (_rand(rng, (1, 2, 4, 64), "bf16"), kc, vc, _i32([np.arange(8)]), _i32([100]), _i32([2]))
+    first = tc.attend(*args)
+    assert tc.check() == sv.SPEC_OK
+    sv.spec_tree_inject_fault(tc.h, sv.SPEC_FAULT_STALL_STREAM)
+    tc.attend(*args)
+    assert tc.check() == sv.SPEC_ERR_TIMEOUT and tc.check() == sv.SPEC_OK
+    second = tc.attend(*args)
+    assert tc.check() == sv.SPEC_OK
+    assert torch.equal(first["out"], second["out"]) and torch.equal(first["lse"], second["lse"])
+    tc.close()
+
+
 # --------------------------------------------------------------------------- #
 # keep                                                                         #
 # --------------------------------------------------------------------------- #
