@@ -48,6 +48,7 @@ constexpr int ATT_ROWS = 128;                 // rows of a row tile: M of the MM
 constexpr int ATT_SMEM = 227 * 1024;          // shared memory of a CTA
 constexpr int ATT_MISC = 2048;                // of it: barriers and small tables
 constexpr uint32_t ATT_TMEM_COLS = 512;
+constexpr uint32_t ATT_WAIT_POLLS = 1u << 17;  // limit of a wait: some seconds (a poll sleeps for microseconds)
 constexpr uint32_t ATT_STALL_POLLS = 4096;    // SPEC_FAULT_STALL_STREAM
 constexpr float ATT_LAZY = 8.f;               // log2 growth of the maximum that O takes unscaled
 
@@ -59,6 +60,7 @@ struct Att {                                  // DP: head size rounded up to 64
     static constexpr int UNIT = KT * DP * 2;         // bytes of a K or V tile
     static constexpr int QB = ATT_ROWS * DP * 2;     // bytes of a row tile of Q
     static constexpr int STAGES = (ATT_SMEM - 1024 - ATT_MISC - NS * QB) / UNIT;
+    static constexpr int KS = (STAGES + 1) / 2, VS = STAGES / 2;  // of them for keys, for values
     static constexpr int SMEM = 1024 + NS * QB + STAGES * UNIT + ATT_MISC;
     static constexpr int THREADS = 128 + 128 * NS;
     __host__ __device__ static constexpr uint32_t s_col(int s) { return 128u * s; }
@@ -67,15 +69,16 @@ struct Att {                                  // DP: head size rounded up to 64
 };
 
 struct __align__(16) AttMisc {
-    uint64_t full[16], empty[16];  // ring stages: copied; read by the MMAs
-    uint64_t clean[16];            // the stage's value tile may meet the MMAs
+    uint64_t k_full[8], k_empty[8];  // key tiles: copied; read by the MMAs
+    uint64_t v_full[8], v_empty[8];  // value tiles
+    uint64_t v_clean[8];             // the value tile may meet the MMAs
     uint64_t q_full[2], q_empty[2];
     uint64_t s_full[2];            // scores of the stream's unit are in tensor memory
     uint64_t p_ready[2];           // its probabilities are (and O is scaled)
     uint64_t o_full[2], o_empty[2];  // the segment's O is complete; has been read
     uint64_t ml_full, ml_empty;    // stream 1's (m, l) for the join
     uint64_t drain;
-    uint32_t nf[16][4];            // value rows of the stage with non-finite elements
+    uint32_t nf[8][4];             // value rows of the tile with non-finite elements
     float2 ml[ATT_ROWS];
     int64_t scan[16];
     int64_t total;
@@ -200,15 +203,6 @@ struct AttWork {
     int32_t stall;
 };
 
-// ring position of the K and V tiles of tile t of a segment of nt tiles: the
-// order in which the MMAs read them.  With two streams on alternate tiles the
-// scores run one tile further ahead of the values.
-__device__ __forceinline__ int att_kpos(int t, bool ahead) { return ahead ? (t == 0 ? 0 : 2 * t - 1) : 2 * t; }
-__device__ __forceinline__ int att_vpos(int t, int nt, bool ahead)
-{
-    return ahead ? (t == nt - 1 ? 2 * nt - 1 : 2 * t + 2) : 2 * t + 1;
-}
-
 __device__ __forceinline__ bool att_wait(uint64_t* bar, uint32_t parity, const volatile int32_t* failed, uint32_t limit)
 {
     for (uint32_t i = 0; i < limit; ++i) {
@@ -250,24 +244,29 @@ __global__ void __launch_bounds__(Att<DP>::THREADS, 1)
 {
     using A = Att<DP>;
     using H = Half2<F16>;
-    constexpr int KT = A::KT, NS = A::NS, NH = A::NH, STAGES = A::STAGES;
+    constexpr int KT = A::KT, NS = A::NS, NH = A::NH, KS = A::KS, VS = A::VS;
     extern __shared__ unsigned char att_raw[];
     const uint32_t raw = smem_u32(att_raw);
     unsigned char* const q_smem = att_raw + (((raw + 1023u) & ~1023u) - raw);
-    unsigned char* const ring = q_smem + NS * A::QB;
-    AttMisc& ms = *reinterpret_cast<AttMisc*>(ring + STAGES * A::UNIT);
+    unsigned char* const k_smem = q_smem + NS * A::QB;
+    unsigned char* const v_smem = k_smem + KS * A::UNIT;
+    AttMisc& ms = *reinterpret_cast<AttMisc*>(v_smem + VS * A::UNIT);
     const TreeAttendParams& p = w.p;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const uint32_t limit = w.stall ? ATT_STALL_POLLS : WAIT_LIMIT;
+    const uint32_t limit = w.stall ? ATT_STALL_POLLS : ATT_WAIT_POLLS;
     const volatile int32_t* failed = &ms.failed;
 
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (warp == 0) tmem_alloc(&ms.tmem, ATT_TMEM_COLS);
     if (tid == 32) {
-        for (int i = 0; i < STAGES; ++i) {
-            mbar_init(&ms.full[i], 1);
-            mbar_init(&ms.empty[i], 1);
-            mbar_init(&ms.clean[i], 2);
+        for (int i = 0; i < KS; ++i) {
+            mbar_init(&ms.k_full[i], 1);
+            mbar_init(&ms.k_empty[i], 1);
+        }
+        for (int i = 0; i < VS; ++i) {
+            mbar_init(&ms.v_full[i], 1);
+            mbar_init(&ms.v_empty[i], 1);
+            mbar_init(&ms.v_clean[i], 2);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&ms.q_full[i], 1);
@@ -334,35 +333,47 @@ __global__ void __launch_bounds__(Att<DP>::THREADS, 1)
 
     if (warp == 0) {
         // ---------------- producer: pages of K and V, and the rows of Q
-        uint32_t idx = 0, qi = 0;  // ring units and Q tiles so far
-        auto unit = [&](const CUtensorMap* map, int kb) {
-            const uint32_t st = idx % STAGES;
-            if (idx >= STAGES)
-                ok = ok && __all_sync(0xffffffffu, att_wait(&ms.empty[st], (idx / STAGES - 1) & 1, failed, limit));
+        uint32_t ki = 0, vi = 0, qi = 0;  // key tiles, value tiles and row tiles of Q so far
+        auto tile = [&](const CUtensorMap* map, int kb, unsigned char* dst, uint64_t* full, uint64_t* empty,
+                        bool reused, uint32_t parity) {
+            if (reused) ok = ok && __all_sync(0xffffffffu, att_wait(empty, parity, failed, limit));
             if (!ok || w.stall) return;
             const int boxes = (min(KT, it.limit - kb) + w.page_box - 1) / w.page_box;
-            if (lane == 0) mbar_arrive_expect_tx(&ms.full[st], (uint32_t)(boxes * w.page_box * 128 * NH));
+            if (lane == 0) mbar_arrive_expect_tx(full, (uint32_t)(boxes * w.page_box * 128 * NH));
             __syncwarp();
-            unsigned char* dst = ring + st * A::UNIT;
             for (int i = lane; i < boxes; i += 32) {
                 const int key = kb + i * w.page_box;
                 const int page = __ldg(p.table + (int64_t)it.b * p.s.width + (key >> p.s.page_log2));
                 for (int h = 0; h < NH; ++h)
                     tma_4d(dst + (h * KT + i * w.page_box) * 128, map, h * 64, it.hk,
-                           key & ((1 << p.s.page_log2) - 1), page, &ms.full[st]);
+                           key & ((1 << p.s.page_log2) - 1), page, full);
             }
-            ++idx;
+        };
+        auto keys = [&](int t) {
+            const uint32_t st = ki % KS;
+            if (ok)
+                tile(&map_k, (it.tile0 + t) * KT, k_smem + st * A::UNIT, &ms.k_full[st], &ms.k_empty[st], ki >= KS,
+                     (ki / KS - 1) & 1);
+            if (ok && !w.stall) ++ki;
+        };
+        auto values = [&](int t) {
+            const uint32_t st = vi % VS;
+            if (ok)
+                tile(&map_v, (it.tile0 + t) * KT, v_smem + st * A::UNIT, &ms.v_full[st], &ms.v_empty[st], vi >= VS,
+                     (vi / VS - 1) & 1);
+            if (ok && !w.stall) ++vi;
         };
         for (; ok && it.more(); it.next(p, w.g)) {
-            const bool ahead = NS == 2 && !it.dual;
-            const int nt = it.tiles();
-            unit(&map_k, it.tile0 * KT);
-            for (int s = 0; s < (it.dual ? 2 : 1); ++s, ++qi) {
+            // two streams on alternate tiles: the scores run one tile further ahead
+            const int nt = it.tiles(), lead = NS == 2 && !it.dual ? 1 : 0;
+            keys(0);
+            for (int s = 0; s < (it.dual ? 2 : 1); ++s) {
                 const uint32_t qb = qi % NS;
                 if (qi >= NS)
                     ok = ok &&
                          __all_sync(0xffffffffu, att_wait(&ms.q_empty[qb], (qi / NS - 1) & 1, failed, limit));
-                if (!ok || w.stall) continue;
+                if (!ok || w.stall) break;
+                ++qi;
                 if (lane == 0) {
                     mbar_arrive_expect_tx(&ms.q_full[qb], (uint32_t)(w.q_box * w.g.G * 128 * NH));
                     for (int h = 0; h < NH; ++h)
@@ -370,34 +381,24 @@ __global__ void __launch_bounds__(Att<DP>::THREADS, 1)
                                it.t0 + s * w.g.tpt, it.b, &ms.q_full[qb]);
                 }
             }
-            if (ahead) {
-                for (int t = 1; ok && t < nt; ++t) {
-                    unit(&map_k, (it.tile0 + t) * KT);
-                    if (ok) unit(&map_v, (it.tile0 + t - 1) * KT);
-                }
-                if (ok) unit(&map_v, (it.tile0 + nt - 1) * KT);
-            } else {
-                for (int t = 0; ok && t < nt; ++t) {
-                    if (t > 0) unit(&map_k, (it.tile0 + t) * KT);
-                    if (ok) unit(&map_v, (it.tile0 + t) * KT);
-                }
+            for (int t = 0; ok && t < nt; ++t) {
+                for (int k = t == 0 ? 1 : t + lead; k <= min(t + lead, nt - 1); ++k) keys(k);
+                values(t);
             }
             if (w.stall) break;
         }
         // drain: every tile and row tile of Q has been read by the MMAs, so no
         // copy or commit is still on its way when the CTA leaves
-        if (!w.stall) {
-            for (uint32_t i = idx > STAGES ? idx - STAGES : 0; ok && i < idx; ++i)
-                ok = att_wait(&ms.empty[i % STAGES], (i / STAGES) & 1, failed, limit);
-            for (uint32_t i = qi > NS ? qi - NS : 0; ok && i < qi; ++i)
-                ok = att_wait(&ms.q_empty[i % NS], (i / NS) & 1, failed, limit);
-        }
+        const uint32_t k0 = ki > KS ? ki - KS : 0, v0 = vi > VS ? vi - VS : 0, q0 = qi > NS ? qi - NS : 0;
+        for (uint32_t i = k0; ok && i < ki; ++i) ok = att_wait(&ms.k_empty[i % KS], (i / KS) & 1, failed, limit);
+        for (uint32_t i = v0; ok && i < vi; ++i) ok = att_wait(&ms.v_empty[i % VS], (i / VS) & 1, failed, limit);
+        for (uint32_t i = q0; ok && i < qi; ++i) ok = att_wait(&ms.q_empty[i % NS], (i / NS) & 1, failed, limit);
         if (!ok) {
             // a role gave up: at least every copy issued has landed
             if (lane == 0) ms.failed = 1;
-            for (uint32_t i = idx > STAGES ? idx - STAGES : 0; i < idx; ++i)
-                mbar_wait(&ms.full[i % STAGES], (i / STAGES) & 1);
-            for (uint32_t i = qi > NS ? qi - NS : 0; i < qi; ++i) mbar_wait(&ms.q_full[i % NS], (i / NS) & 1);
+            for (uint32_t i = k0; i < ki; ++i) mbar_wait_n(&ms.k_full[i % KS], (i / KS) & 1, limit);
+            for (uint32_t i = v0; i < vi; ++i) mbar_wait_n(&ms.v_full[i % VS], (i / VS) & 1, limit);
+            for (uint32_t i = q0; i < qi; ++i) mbar_wait_n(&ms.q_full[i % NS], (i / NS) & 1, limit);
         }
     } else if (warp == 1) {
         if (lane == 0) {
@@ -406,34 +407,34 @@ __global__ void __launch_bounds__(Att<DP>::THREADS, 1)
             constexpr uint32_t ID_O = umma_idesc(F16, true, ATT_ROWS, DP);
             uint32_t base = 0, qi = 0;
             uint32_t n_unit[2] = {0, 0}, n_seg[2] = {0, 0};  // units and segments of each stream so far
-            const uint32_t ring_u = smem_u32(ring), q_u = smem_u32(q_smem);
+            const uint32_t k_u = smem_u32(k_smem), v_u = smem_u32(v_smem), q_u = smem_u32(q_smem);
             for (; ok && it.more(); it.next(p, w.g)) {
-                const bool dual = it.dual, ahead = NS == 2 && !dual;
+                const bool dual = it.dual;
                 const int nt = it.tiles(), units = dual ? 2 * nt : nt;
                 auto scores = [&](int u) {
                     const int s = NS == 2 ? u & 1 : 0, t = dual ? u >> 1 : u;
-                    const uint32_t i = base + att_kpos(t, ahead), st = i % STAGES;
+                    const uint32_t i = base + t, st = i % KS;
                     const uint32_t q = (qi + (dual ? s : 0)), qb = q % NS;
-                    if (!dual || s == 0) ok = ok && att_wait(&ms.full[st], (i / STAGES) & 1, failed, limit);
+                    if (!dual || s == 0) ok = ok && att_wait(&ms.k_full[st], (i / KS) & 1, failed, limit);
                     if (t == 0 && (dual || u == 0))
                         ok = ok && att_wait(&ms.q_full[qb], (q / NS) & 1, failed, limit);
                     if (!ok) return;
                     tmem_fence_after();
-                    const uint32_t ka = ring_u + st * A::UNIT, qa = q_u + qb * A::QB;
+                    const uint32_t ka = k_u + st * A::UNIT, qa = q_u + qb * A::QB;
 #pragma unroll
                     for (int k = 0; k < DP / 16; ++k)
                         umma_ss(tmem + A::s_col(s),
                                 umma_desc(qa + (k / 4) * ATT_ROWS * 128 + (k % 4) * 32, 16, 1024),
                                 umma_desc(ka + (k / 4) * KT * 128 + (k % 4) * 32, 16, 1024), ID_S, k > 0);
                     umma_commit(&ms.s_full[s]);
-                    if (!dual || s == 1) umma_commit(&ms.empty[st]);
+                    if (!dual || s == 1) umma_commit(&ms.k_empty[st]);
                     if (t == nt - 1) umma_commit(&ms.q_empty[qb]);
                 };
                 auto values = [&](int u) {
                     const int s = NS == 2 ? u & 1 : 0, t = dual ? u >> 1 : u;
-                    const uint32_t i = base + att_vpos(t, nt, ahead), st = i % STAGES;
+                    const uint32_t i = base + t, st = i % VS;
                     const bool first = u < NS;
-                    if (!dual || s == 0) ok = ok && att_wait(&ms.clean[st], (i / STAGES) & 1, failed, limit);
+                    if (!dual || s == 0) ok = ok && att_wait(&ms.v_clean[st], (i / VS) & 1, failed, limit);
                     if (first && n_seg[s] > 0)
                         ok = ok && att_wait(&ms.o_empty[s], (n_seg[s] - 1) & 1, failed, limit);
                     ok = ok && att_wait(&ms.p_ready[s], n_unit[s] & 1, failed, limit);
@@ -441,12 +442,12 @@ __global__ void __launch_bounds__(Att<DP>::THREADS, 1)
                     ++n_unit[s];
                     if (first) ++n_seg[s];
                     tmem_fence_after();
-                    const uint32_t va = ring_u + st * A::UNIT;
+                    const uint32_t va = v_u + st * A::UNIT;
 #pragma unroll
                     for (int k = 0; k < KT / 16; ++k)
                         umma_ts(tmem + A::o_col(s), tmem + A::s_col(s) + k * 8,
                                 umma_desc(va + k * 2048, KT * 128, 1024), ID_O, !first || k > 0);
-                    if (!dual || s == 1) umma_commit(&ms.empty[st]);
+                    if (!dual || s == 1) umma_commit(&ms.v_empty[st]);
                     if (u + NS >= units) umma_commit(&ms.o_full[s]);
                 };
                 for (int u = 0; ok && u < min(NS, units); ++u) scores(u);
@@ -454,13 +455,13 @@ __global__ void __launch_bounds__(Att<DP>::THREADS, 1)
                     values(u);
                     if (ok && u + NS < units) scores(u + NS);
                 }
-                base += 2 * nt;
+                base += nt;
                 qi += dual ? 2 : 1;
             }
             if (!ok) {
                 ms.failed = 1;
                 umma_commit(&ms.drain);  // no MMA is in flight when the CTA leaves
-                mbar_wait(&ms.drain, 0);
+                mbar_wait_n(&ms.drain, 0, limit);
             }
         }
         __syncwarp();
@@ -480,12 +481,11 @@ __global__ void __launch_bounds__(Att<DP>::THREADS, 1)
         const int r0 = (warp - 2) * HALF;
         uint32_t base = 0;
         for (; ok && it.more(); it.next(p, w.g)) {
-            const bool ahead = NS == 2 && !it.dual;
             const int nt = it.tiles(), end = it.ctx + it.n;
             for (int t = 0; ok && t < nt; ++t) {
-                const uint32_t i = base + att_vpos(t, nt, ahead), st = i % STAGES;
+                const uint32_t i = base + t, st = i % VS;
                 const int kb = (it.tile0 + t) * KT;
-                ok = __all_sync(0xffffffffu, att_wait(&ms.full[st], (i / STAGES) & 1, failed, limit));
+                ok = __all_sync(0xffffffffu, att_wait(&ms.v_full[st], (i / VS) & 1, failed, limit));
                 if (!ok) break;
                 if (kb + KT > it.mask_from) {
                     uint32_t* nf = ms.nf[st] + (warp - 2) * (HALF / 32);
@@ -497,7 +497,7 @@ __global__ void __launch_bounds__(Att<DP>::THREADS, 1)
                         if (key < it.mask_from) continue;
 #pragma unroll
                         for (int h = 0; h < NH; ++h) {
-                            uint4* a = (uint4*)(ring + st * A::UNIT + (h * KT + r) * 128) + (lane & 7);
+                            uint4* a = (uint4*)(v_smem + st * A::UNIT + (h * KT + r) * 128) + (lane & 7);
                             uint4 x = key < end ? *a : make_uint4(0, 0, 0, 0);
                             uint32_t* xs = &x.x;
                             bool dirty = key >= end;
@@ -515,9 +515,9 @@ __global__ void __launch_bounds__(Att<DP>::THREADS, 1)
                     fence_async_smem();
                     __syncwarp();
                 }
-                if (lane == 0) mbar_arrive(&ms.clean[st]);
+                if (lane == 0) mbar_arrive(&ms.v_clean[st]);
             }
-            base += 2 * nt;
+            base += nt;
         }
         if (!ok && lane == 0) ms.failed = 1;
     } else {
@@ -541,7 +541,7 @@ __global__ void __launch_bounds__(Att<DP>::THREADS, 1)
         }
         uint32_t base = 0, n_unit = 0, n_seg[2] = {0, 0}, n_ml = 0;
         for (; ok && it.more(); it.next(p, w.g)) {
-            const bool dual = it.dual, ahead = NS == 2 && !dual;
+            const bool dual = it.dual;
             const int nt = it.tiles(), units = dual ? 2 * nt : nt;
             const int tbase = it.t0 + (dual ? s * w.g.tpt : 0);
             const int rows = min(w.g.tpt, it.t0 + it.ntok - tbase) * G;
@@ -593,8 +593,8 @@ __global__ void __launch_bounds__(Att<DP>::THREADS, 1)
                     uint32_t x[KT];
                     tmem_ld<KT>(s_addr, x);
                     if (kb + KT > it.mask_from) {
-                        const uint32_t i = base + att_vpos(tile, nt, ahead), st = i % STAGES;
-                        ok = __all_sync(0xffffffffu, att_wait(&ms.clean[st], (i / STAGES) & 1, failed, limit));
+                        const uint32_t i = base + tile, st = i % VS;
+                        ok = __all_sync(0xffffffffu, att_wait(&ms.v_clean[st], (i / VS) & 1, failed, limit));
                         if (!ok) break;
                         uint32_t some = 0;
 #pragma unroll
@@ -651,7 +651,7 @@ __global__ void __launch_bounds__(Att<DP>::THREADS, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&ms.p_ready[s]);
             }
-            base += 2 * nt;
+            base += nt;
             if (!ok) break;
 
             // ---- the segment's end: O of the streams with units

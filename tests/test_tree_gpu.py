@@ -283,6 +283,15 @@ def _attend_case(sv, rng, B, T, Hq, Hkv, D, page, ctx, n, dtype, kind="tokens", 
     # one long sequence: split over many CTAs
     (1, 3, 2, 1, 64, 16, [20011], [3], "bf16", "tokens", "random"),
     (2, 8, 8, 1, 128, 64, [9000, 5], [8, 8], "bf16", "tokens", "random"),
+    # more key tiles than SMs: ranges of several tiles and several items
+    (24, 3, 16, 8, 128, 16, [(i * 97) % 1500 for i in range(24)], [1 + i % 3 for i in range(24)], "bf16", "tokens",
+     "random"),
+    (12, 70, 16, 8, 128, 16, [(i * 131) % 1300 for i in range(12)], [70 - i for i in range(12)], "bf16", "heads",
+     "random"),
+    (20, 4, 16, 8, 64, 32, [(i * 211) % 2100 for i in range(20)], [1 + i % 4 for i in range(20)], "f16", "tokens", None),
+    (14, 5, 12, 6, 256, 16, [(i * 173) % 1100 for i in range(14)], [1 + i % 5 for i in range(14)], "bf16", "pairs",
+     "random"),
+    (6, 150, 8, 8, 80, 8, [(i * 311) % 900 for i in range(6)], [150 - 20 * i for i in range(6)], "f16", "tokens", None),
 ])
 def test_attend(sv, B, T, Hq, Hkv, D, page, ctx, n, dtype, kind, tree):
     from parity_util import report
