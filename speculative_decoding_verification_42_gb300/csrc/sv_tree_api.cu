@@ -209,6 +209,7 @@ spec_status spec_tree_attend(spec_tree_t h, const spec_tree_attend_args* a, void
     if (!g.ok) return SPEC_ERR_CUDA;
     TreeAttendParams p = {};
     p.s = shape(h, a->batch, a->tokens, a->ctx_len, a->n_tokens);
+    if (!tree_attend_fits(p.s)) return SPEC_ERR_UNSUPPORTED;
     p.q = rows(a->q);
     p.c = cache(a->cache);
     p.table = a->block_table;

@@ -80,10 +80,8 @@ struct __align__(16) AttMisc {
     uint64_t drain;
     uint32_t nf[8][4];             // value rows of the tile with non-finite elements
     float2 ml[ATT_ROWS];
-    int64_t scan[16];
-    int64_t total;
-    int64_t first;                 // tiles of the start sequence before the range
-    int32_t first_b;
+    int32_t scan[16];
+    int32_t first, first_b;        // the range's first sequence, and its cost before the range
     uint32_t tmem;
     int32_t failed;
 };
@@ -94,37 +92,61 @@ static_assert(sizeof(AttMisc) <= ATT_MISC, "barriers and tables fit");
 // ------------------------------------------------------------------------- //
 struct AttGeom {
     int G, tpt, group;  // heads per key head, nodes per row tile, nodes per item
-    int KT;
     int Hkv;
 };
 
-// key tiles of item `rp` of a sequence: a chain's rows see nothing past their
-// last node
+// The ranges are equal in cost, not in tiles: an item costs its key tiles and
+// ATT_ITEM_COST more (its first scores, its masked tile and its output).
+constexpr int ATT_ITEM_COST = 1;
+
+// keys that some row of item `rp` of a sequence sees: a chain's rows see
+// nothing past their last node
 __device__ __forceinline__ int att_limit(const TreeAttendParams& p, const AttGeom& g, int ctx, int n, int rp)
 {
     return ctx + (p.mask ? n : min(n, (rp + 1) * g.group));
 }
-__device__ __forceinline__ int att_tiles(const TreeAttendParams& p, const AttGeom& g, int ctx, int n, int rp)
+template <int KT>
+__device__ __forceinline__ int att_cost(const TreeAttendParams& p, const AttGeom& g, int ctx, int n, int rp)
 {
-    return (att_limit(p, g, ctx, n, rp) + g.KT - 1) / g.KT;
+    return (att_limit(p, g, ctx, n, rp) + KT - 1) / KT + ATT_ITEM_COST;
 }
-// key tiles of all items of one key head of a sequence
-__device__ __forceinline__ int64_t att_head_tiles(const TreeAttendParams& p, const AttGeom& g, int ctx, int n)
+// cost of all items of one key head of a sequence
+template <int KT>
+__device__ __forceinline__ int att_head_cost(const TreeAttendParams& p, const AttGeom& g, int ctx, int n)
 {
+    if (n <= g.group) return n ? att_cost<KT>(p, g, ctx, n, 0) : 0;
     const int nrp = (n + g.group - 1) / g.group;
-    if (p.mask || nrp <= 1) return (int64_t)nrp * (n ? att_tiles(p, g, ctx, n, 0) : 0);
-    int64_t t = 0;
-    for (int rp = 0; rp < nrp; ++rp) t += att_tiles(p, g, ctx, n, rp);
+    if (p.mask) return nrp * att_cost<KT>(p, g, ctx, n, 0);
+    int t = 0;
+    for (int rp = 0; rp < nrp; ++rp) t += att_cost<KT>(p, g, ctx, n, rp);
     return t;
 }
 
+// `total` cut into `ctas` ranges that differ by one at most
+struct AttSplit {
+    int total, ctas, q, r;
+    __device__ __forceinline__ AttSplit(int total_, int ctas_) : total(total_), ctas(min(ctas_, total_))
+    {
+        q = ctas ? total / ctas : 0;
+        r = total - q * ctas;
+    }
+    __device__ __forceinline__ int start(int c) const { return c * q + min(c, r); }
+    __device__ __forceinline__ int owner(int x) const
+    {
+        const int wide = r * (q + 1);
+        return x < wide ? x / (q + 1) : r + (x - wide) / q;
+    }
+};
+
 // the segments of a CTA: parts of items, in order of (sequence, key head, group)
+template <int KT>
 struct AttIter {
-    int64_t pos, end;           // key tiles in the order of all items
+    int pos, end;               // cost positions in the order of all items
     int b, hk, rp;              // the item
-    int ctx, n, nrp;
+    int at;                     // cost position of its begin
+    int ctx, n;
     int t0, ntok;               // its first node and nodes
-    int ntiles, tile0, tile1;   // its key tiles, and this segment's
+    int ntiles, tile0, tile1;   // its key tiles, and this segment's (none: tile0 >= tile1)
     int limit;                  // keys any of its rows may see
     int mask_from;              // keys below are seen by all its rows
     bool dual;                  // two row tiles
@@ -136,50 +158,54 @@ struct AttIter {
         ntok = min(g.group, n - t0);
         dual = ntok > g.tpt;
         limit = att_limit(p, g, ctx, n, rp);
-        ntiles = (limit + g.KT - 1) / g.KT;
+        ntiles = (limit + KT - 1) / KT;
         mask_from = p.mask ? ctx : ctx + t0 + 1;
-        tile1 = (int)min((int64_t)ntiles, tile0 + (end - pos));
+        tile0 = max(pos - at - ATT_ITEM_COST, 0);
+        tile1 = min(end - at - ATT_ITEM_COST, ntiles);
     }
-    __device__ __forceinline__ void load_seq(const TreeAttendParams& p, const AttGeom& g)
+    __device__ __forceinline__ void load_seq(const TreeAttendParams& p)
     {
         const SeqLen l = tree_len(p.s, b);
         ctx = l.ctx;
         n = l.n;
-        nrp = (n + g.group - 1) / g.group;
     }
-    // off: tiles of sequence b0 before the range
-    __device__ __forceinline__ void start(const TreeAttendParams& p, const AttGeom& g, int64_t pos0, int64_t end0,
-                                          int b0, int64_t off)
+    // off: cost of sequence b0 before the range
+    __device__ __forceinline__ void start(const TreeAttendParams& p, const AttGeom& g, int pos0, int end0, int b0,
+                                          int off)
     {
         pos = pos0;
         end = end0;
         if (!more()) return;
         b = b0;
-        load_seq(p, g);
-        const int64_t per_head = att_head_tiles(p, g, ctx, n);
-        hk = (int)(off / per_head);
+        load_seq(p);
+        const int per_head = att_head_cost<KT>(p, g, ctx, n);
+        hk = off / per_head;
         off -= hk * per_head;
         rp = 0;
-        for (int t; off >= (t = att_tiles(p, g, ctx, n, rp)); ++rp) off -= t;
-        tile0 = (int)off;
+        if (n > g.group)
+            for (int t; off >= (t = att_cost<KT>(p, g, ctx, n, rp)); ++rp) off -= t;
+        at = pos - off;
         load_item(p, g);
+        if (tile0 >= tile1) next(p, g);
     }
     __device__ __forceinline__ void next(const TreeAttendParams& p, const AttGeom& g)
     {
-        pos += tile1 - tile0;
-        if (!more()) return;
-        tile0 = 0;
-        if (++rp == nrp) {
-            rp = 0;
-            if (++hk == g.Hkv) {
-                hk = 0;
-                do {
-                    ++b;
-                    load_seq(p, g);
-                } while (n == 0);
+        do {
+            at += ntiles + ATT_ITEM_COST;
+            pos = at;
+            if (!more()) return;
+            if ((++rp) * g.group >= n) {
+                rp = 0;
+                if (++hk == g.Hkv) {
+                    hk = 0;
+                    do {
+                        ++b;
+                        load_seq(p);
+                    } while (n == 0);
+                }
             }
-        }
-        load_item(p, g);
+            load_item(p, g);
+        } while (tile0 >= tile1);
     }
     __device__ __forceinline__ int tiles() const { return tile1 - tile0; }
     __device__ __forceinline__ bool whole() const { return tile0 == 0 && tile1 == ntiles; }
@@ -257,6 +283,11 @@ __global__ void __launch_bounds__(Att<DP>::THREADS, 1)
     const volatile int32_t* failed = &ms.failed;
 
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (tid == 64) {
+        tma_prefetch_map(&map_k);
+        tma_prefetch_map(&map_q);
+        tma_prefetch_map(&map_v);
+    }
     if (warp == 0) tmem_alloc(&ms.tmem, ATT_TMEM_COLS);
     if (tid == 32) {
         for (int i = 0; i < KS; ++i) {
@@ -282,37 +313,38 @@ __global__ void __launch_bounds__(Att<DP>::THREADS, 1)
         ms.failed = 0;
         fence_barrier_init();
     }
-    // ---- this CTA's range: a scan of the sequences' tiles
+    // ---- this CTA's range: a scan of the sequences' costs
+    int total = 0;
     {
         const int per = (p.s.B + A::THREADS - 1) / A::THREADS;
         const int s0 = min(p.s.B, tid * per), s1 = min(p.s.B, s0 + per);
-        int64_t sum = 0;
+        int sum = 0;
         for (int b = s0; b < s1; ++b) {
             const SeqLen l = tree_len(p.s, b);
-            sum += w.g.Hkv * att_head_tiles(p, w.g, l.ctx, l.n);
+            sum += w.g.Hkv * att_head_cost<KT>(p, w.g, l.ctx, l.n);
         }
-        int64_t inc = sum;
+        int inc = sum;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int64_t v = __shfl_up_sync(0xffffffffu, inc, o);
+            const int v = __shfl_up_sync(0xffffffffu, inc, o);
             if (lane >= o) inc += v;
         }
         if (lane == 31) ms.scan[warp] = inc;
         __syncthreads();
-        int64_t before = inc - sum, total = 0;
+        int before = inc - sum;
+#pragma unroll
         for (int i = 0; i < A::THREADS / 32; ++i) {
-            if (i < warp) before += ms.scan[i];
-            total += ms.scan[i];
+            const int v = ms.scan[i];
+            if (i < warp) before += v;
+            total += v;
         }
-        const int64_t ctas = min((int64_t)gridDim.x, total);  // every one of them has a tile
-        const int64_t pos0 = (int)blockIdx.x < ctas ? total * blockIdx.x / ctas : 0;
-        if (tid == 0) ms.total = total;
+        const AttSplit split(total, gridDim.x);
+        const int pos0 = split.start(blockIdx.x);
         if (sum > 0 && pos0 >= before && pos0 < before + sum) {
-            int b = s0;
-            int64_t off = pos0 - before;
+            int b = s0, off = pos0 - before;
             for (;; ++b) {
                 const SeqLen l = tree_len(p.s, b);
-                const int64_t t = w.g.Hkv * att_head_tiles(p, w.g, l.ctx, l.n);
+                const int t = w.g.Hkv * att_head_cost<KT>(p, w.g, l.ctx, l.n);
                 if (off < t) break;
                 off -= t;
             }
@@ -324,16 +356,30 @@ __global__ void __launch_bounds__(Att<DP>::THREADS, 1)
     __syncthreads();
     tmem_fence_after();
     const uint32_t tmem = ms.tmem;
-    const int64_t total = ms.total, ctas = min((int64_t)gridDim.x, total);
-    const bool busy = (int)blockIdx.x < ctas;
-    const int64_t pos0 = busy ? total * blockIdx.x / ctas : 0, end0 = busy ? total * (blockIdx.x + 1) / ctas : 0;
-    AttIter it;
-    it.start(p, w.g, pos0, end0, ms.first_b, ms.first);
+    const AttSplit split(total, gridDim.x);
+    const bool busy = (int)blockIdx.x < split.ctas;
+    AttIter<KT> it;
+    it.start(p, w.g, busy ? split.start(blockIdx.x) : 0, busy ? split.start(blockIdx.x + 1) : 0, ms.first_b, ms.first);
     bool ok = true;
 
     if (warp == 0) {
         // ---------------- producer: pages of K and V, and the rows of Q
         uint32_t ki = 0, vi = 0, qi = 0;  // key tiles, value tiles and row tiles of Q so far
+        // page ids come 32 at a time, one load per block of the table row and one
+        // block ahead: a lookup per tile would put its latency between the copies
+        int blk = -2, prev = 0, cur = 0, ahead = 0;  // of the item's row: ids of blocks blk - 1, blk, blk + 1
+        auto ids = [&](int k) {
+            const int i = k * 32 + lane, pages = (it.limit + (1 << p.s.page_log2) - 1) >> p.s.page_log2;
+            return i < pages ? __ldg(p.table + (int64_t)it.b * p.s.width + i) : -1;
+        };
+        auto seek = [&](int kb) {  // called for the keys, which run ahead of the values by a tile at most
+            const int k = (kb >> p.s.page_log2) >> 5;
+            if (k == blk) return;
+            prev = cur;
+            cur = k == blk + 1 ? ahead : ids(k);
+            ahead = ids(k + 1);
+            blk = k;
+        };
         auto tile = [&](const CUtensorMap* map, int kb, unsigned char* dst, uint64_t* full, uint64_t* empty,
                         bool reused, uint32_t parity) {
             if (reused) ok = ok && __all_sync(0xffffffffu, att_wait(empty, parity, failed, limit));
@@ -341,16 +387,17 @@ __global__ void __launch_bounds__(Att<DP>::THREADS, 1)
             const int boxes = (min(KT, it.limit - kb) + w.page_box - 1) / w.page_box;
             if (lane == 0) mbar_arrive_expect_tx(full, (uint32_t)(boxes * w.page_box * 128 * NH));
             __syncwarp();
-            for (int i = lane; i < boxes; i += 32) {
-                const int key = kb + i * w.page_box;
-                const int page = __ldg(p.table + (int64_t)it.b * p.s.width + (key >> p.s.page_log2));
+            // a tile's pages (at most 16) lie in one block
+            const int key = kb + lane * w.page_box, first = kb >> p.s.page_log2;
+            const int page = __shfl_sync(0xffffffffu, first >> 5 == blk ? cur : prev, (key >> p.s.page_log2) & 31);
+            if (lane < boxes)
                 for (int h = 0; h < NH; ++h)
-                    tma_4d(dst + (h * KT + i * w.page_box) * 128, map, h * 64, it.hk,
+                    tma_4d(dst + (h * KT + lane * w.page_box) * 128, map, h * 64, it.hk,
                            key & ((1 << p.s.page_log2) - 1), page, full);
-            }
         };
         auto keys = [&](int t) {
             const uint32_t st = ki % KS;
+            seek((it.tile0 + t) * KT);
             if (ok)
                 tile(&map_k, (it.tile0 + t) * KT, k_smem + st * A::UNIT, &ms.k_full[st], &ms.k_empty[st], ki >= KS,
                      (ki / KS - 1) & 1);
@@ -366,6 +413,7 @@ __global__ void __launch_bounds__(Att<DP>::THREADS, 1)
         for (; ok && it.more(); it.next(p, w.g)) {
             // two streams on alternate tiles: the scores run one tile further ahead
             const int nt = it.tiles(), lead = NS == 2 && !it.dual ? 1 : 0;
+            blk = -2;
             keys(0);
             for (int s = 0; s < (it.dual ? 2 : 1); ++s) {
                 const uint32_t qb = qi % NS;
@@ -468,12 +516,14 @@ __global__ void __launch_bounds__(Att<DP>::THREADS, 1)
     } else if (warp < 4) {
         // ---------------- cleaning warps: half of each value tile's rows each
         if (warp == 2 && lane == 0) {
+            // the item's first tile lies in an earlier range: the one before it, or
+            // the cut is not the first of the item
             AttCut cut{-1, 0, 0, 0, 0, 0};
-            if (busy && it.tile0 > 0) {
-                const int64_t i0 = pos0 - it.tile0, i1 = i0 + it.ntiles;
-                const int c = blockIdx.x;
-                if (i0 >= total * (c - 1) / ctas)
-                    cut = AttCut{c - 1, (int)((i1 * ctas - 1) / total), it.b, it.hk, it.t0, it.ntok * w.g.G};
+            if (it.more() && it.tile0 > 0) {
+                const int first = split.owner(it.at + ATT_ITEM_COST);
+                if (first == (int)blockIdx.x - 1)
+                    cut = AttCut{first, split.owner(it.at + ATT_ITEM_COST + it.ntiles - 1), it.b, it.hk, it.t0,
+                                 it.ntok * w.g.G};
             }
             w.cuts[blockIdx.x] = cut;
         }
@@ -528,15 +578,15 @@ __global__ void __launch_bounds__(Att<DP>::THREADS, 1)
         const int T = p.s.T, Hq = p.s.Hq, D = p.s.D, G = w.g.G;
         // nodes that do not exist: zero rows
         {
-            const int64_t rows = (int64_t)p.s.B * T, ws = (int64_t)gridDim.x * NS * 4;
-            const int64_t per = (rows + ws - 1) / ws, r0 = ((int64_t)blockIdx.x * NS * 4 + warp - 4) * per;
-            for (int64_t r = r0; r < min(rows, r0 + per); ++r) {
-                const int b = (int)(r / T);
-                if (r - (int64_t)b * T < tree_len(p.s, b).n) continue;
-                uint4* o = (uint4*)((char*)p.out + r * Hq * D * 2);
+            const int rows = p.s.B * T, ws = gridDim.x * NS * 4, per = (rows + ws - 1) / ws;
+            const int r0 = min(rows, ((int)blockIdx.x * NS * 4 + warp - 4) * per), r1 = min(rows, r0 + per);
+            for (int r = r0, b = r0 / T; r < r1; ++r) {
+                if (r >= (b + 1) * T) ++b;
+                if (r - b * T < tree_len(p.s, b).n) continue;
+                uint4* o = (uint4*)((char*)p.out + (int64_t)r * Hq * D * 2);
                 for (int i = lane; i < Hq * D / 8; i += 32) o[i] = make_uint4(0, 0, 0, 0);
                 if (p.lse)
-                    for (int i = lane; i < Hq; i += 32) p.lse[r * Hq + i] = -INFINITY;
+                    for (int i = lane; i < Hq; i += 32) p.lse[(int64_t)r * Hq + i] = -INFINITY;
             }
         }
         uint32_t base = 0, n_unit = 0, n_seg[2] = {0, 0}, n_ml = 0;
@@ -590,27 +640,49 @@ __global__ void __launch_bounds__(Att<DP>::THREADS, 1)
                 if (active) {
                     // every earlier P V of the stream is complete: the scores were issued after it
                     if (pend_kb >= 0) add_nonfinite();
-                    uint32_t x[KT];
-                    tmem_ld<KT>(s_addr, x);
                     if (kb + KT > it.mask_from) {
+                        // hidden scores become -inf in tensor memory, before the passes over them
                         const uint32_t i = base + tile, st = i % VS;
                         ok = __all_sync(0xffffffffu, att_wait(&ms.v_clean[st], (i / VS) & 1, failed, limit));
                         if (!ok) break;
                         uint32_t some = 0;
-#pragma unroll
+#pragma unroll 1
                         for (int y = 0; y < KT / 32; ++y) {
                             const uint32_t see = att_sees(p, it.b, t, it.ctx, it.n, kb + 32 * y);
-                            pend[y] = see & *(volatile uint32_t*)&ms.nf[st][y];
-                            some |= pend[y];
+                            if (__all_sync(0xffffffffu, see == ~0u)) continue;
+                            some |= see & *(volatile uint32_t*)&ms.nf[st][y];
+                            uint32_t x[32];
+                            tmem_ld<32>(s_addr + 32 * y, x);
 #pragma unroll
                             for (int k = 0; k < 32; ++k)
-                                if (!((see >> k) & 1u)) x[32 * y + k] = 0xFF800000u;
+                                if (!((see >> k) & 1u)) x[k] = 0xFF800000u;
+                            tmem_st<32>(s_addr + 32 * y, x);
                         }
-                        pend_kb = __any_sync(0xffffffffu, some) ? kb : -1;
+                        tmem_wait_st();
+                        pend_kb = -1;
+                        if (__any_sync(0xffffffffu, some)) {
+                            pend_kb = kb;
+#pragma unroll
+                            for (int y = 0; y < KT / 32; ++y)
+                                pend[y] = att_sees(p, it.b, t, it.ctx, it.n, kb + 32 * y) &
+                                          *(volatile uint32_t*)&ms.nf[st][y];
+                        }
                     }
+                    // the row's maximum, then its exponentials: two passes over the
+                    // scores in tensor memory take fewer registers than one that
+                    // holds all of them, and no spills
                     float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                    for (int k = 0; k < KT; ++k) mx[k & 3] = fmaxf(mx[k & 3], __uint_as_float(x[k]));
+                    for (int y = 0; y < KT; y += 64) {
+                        uint32_t x[64];
+                        tmem_ld<64>(s_addr + y, x);
+#pragma unroll
+                        for (int k = 0; k < 64; k += 8)
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)
+                                mx[j] = fmaxf(mx[j], fmaxf(__uint_as_float(x[k + 2 * j]),
+                                                           __uint_as_float(x[k + 2 * j + 1])));
+                    }
                     const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
                     // O and l stay in units of the old maximum while the new one is
                     // less than 2^8 above it: p then stays below 2^8
@@ -630,21 +702,24 @@ __global__ void __launch_bounds__(Att<DP>::THREADS, 1)
                         }
                     }
                     const float mc = m == -INFINITY ? 0.f : m * c;
-                    float sum[2] = {0.f, 0.f};
+                    const uint64_t c2 = pack2(c, c), mc2 = pack2(-mc, -mc);
+                    uint64_t sum[2] = {0ull, 0ull};  // two pairs of partial sums
 #pragma unroll
-                    for (int y = 0; y < KT / 32; ++y) {
-                        uint32_t pk[16];
+                    for (int y = 0; y < KT; y += 64) {
+                        uint32_t x[64];
+                        tmem_ld<64>(s_addr + y, x);
 #pragma unroll
-                        for (int k = 0; k < 16; ++k) {
-                            const float a = ex2_fast(fmaf(__uint_as_float(x[32 * y + 2 * k]), c, -mc));
-                            const float e = ex2_fast(fmaf(__uint_as_float(x[32 * y + 2 * k + 1]), c, -mc));
-                            sum[0] += a;
-                            sum[1] += e;
-                            pk[k] = H::pack(a, e);
+                        for (int k = 0; k < 32; ++k) {
+                            float2 e = unpack2(fma2(pack2u(x[2 * k], x[2 * k + 1]), c2, mc2));
+                            e.x = ex2_fast(e.x);
+                            e.y = ex2_fast(e.y);
+                            sum[k & 1] = add2(sum[k & 1], pack2(e.x, e.y));
+                            x[k] = H::pack(e.x, e.y);
                         }
-                        tmem_st<16>(s_addr + 16 * y, pk);
+                        tmem_st<32>(s_addr + y / 2, *reinterpret_cast<uint32_t(*)[32]>(&x));
                     }
-                    l += sum[0] + sum[1];
+                    const float2 sums = unpack2(add2(sum[0], sum[1]));
+                    l += sums.x + sums.y;
                     tmem_wait_st();
                 }
                 tmem_fence_before();
@@ -704,30 +779,39 @@ __global__ void __launch_bounds__(Att<DP>::THREADS, 1)
                 const int64_t orow = ((int64_t)it.b * T + t) * Hq + head;
                 const int64_t slot = (int64_t)blockIdx.x * 2 + (it.tile0 > 0 ? 0 : 1);
                 const int prow = (dual ? s * ATT_ROWS : 0) + row;
-                for (int d = 0; d < D; d += 16) {
-                    uint32_t o[16];
-                    tmem_ld<16>(o_addr + d, o);
-                    float y[16];
-#pragma unroll
-                    for (int k = 0; k < 16; ++k) y[k] = __uint_as_float(o[k]) * f0;
+#pragma unroll 1
+                for (int d = 0; d < D; d += 32) {
+                    uint32_t o[32];
+                    float y[32];
                     if (join) {
-                        tmem_ld<16>(tmem + A::o_col(NS - 1) + lanes + d, o);
+                        uint32_t o1[32];
+                        tmem_ld_2x32(o_addr + d, tmem + A::o_col(NS - 1) + lanes + d, o, o1);
 #pragma unroll
-                        for (int k = 0; k < 16; ++k) y[k] += __uint_as_float(o[k]) * f1;
+                        for (int k = 0; k < 32; ++k)
+                            y[k] = __uint_as_float(o[k]) * f0 + __uint_as_float(o1[k]) * f1;
+                    } else {
+                        tmem_ld<32>(o_addr + d, o);
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) y[k] = __uint_as_float(o[k]) * f0;
                     }
                     if (!mine) continue;
                     if (whole) {
-                        uint32_t h[8];
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) h[k] = none ? 0u : H::pack(y[2 * k], y[2 * k + 1]);
                         uint4* o16 = (uint4*)((char*)p.out + (orow * D + d) * 2);
-                        o16[0] = make_uint4(h[0], h[1], h[2], h[3]);
-                        o16[1] = make_uint4(h[4], h[5], h[6], h[7]);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            if (d + 8 * k < D)
+                                o16[k] = none ? make_uint4(0, 0, 0, 0)
+                                              : make_uint4(H::pack(y[8 * k], y[8 * k + 1]),
+                                                           H::pack(y[8 * k + 2], y[8 * k + 3]),
+                                                           H::pack(y[8 * k + 4], y[8 * k + 5]),
+                                                           H::pack(y[8 * k + 6], y[8 * k + 7]));
                     } else {
                         float4* o32 = (float4*)w.part_o + (slot * (DP / 4) + d / 4) * (NS * ATT_ROWS) + prow;
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            o32[k * NS * ATT_ROWS] = make_float4(y[4 * k], y[4 * k + 1], y[4 * k + 2], y[4 * k + 3]);
+                        for (int k = 0; k < 8; ++k)
+                            if (d + 4 * k < D)
+                                o32[k * NS * ATT_ROWS] =
+                                    make_float4(y[4 * k], y[4 * k + 1], y[4 * k + 2], y[4 * k + 3]);
                     }
                 }
                 if (mine && whole && p.lse) p.lse[orow] = none ? -INFINITY : fmaf(mr, p.scale, logf(ll));
@@ -884,7 +968,6 @@ static cudaError_t att_launch(AttWork w, int num_sms, cudaStream_t s)
     });
     if (e != cudaSuccess) return e;
     const TreeShape& sh = w.p.s;
-    w.g.KT = A::KT;
     w.g.group = A::NS * w.g.tpt;
     w.page_box = min(1 << sh.page_log2, A::KT);
     w.q_box = min(w.g.tpt, sh.T);
@@ -908,6 +991,14 @@ static cudaError_t att_launch(AttWork w, int num_sms, cudaStream_t s)
     cfg.attrs = at;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, k_tree_combine<F16>, w, DP, A::NS * ATT_ROWS);
+}
+
+bool tree_attend_fits(const TreeShape& sh)
+{
+    const int64_t kt = sh.D <= 128 ? 128 : 64, group = (sh.D <= 128 ? 2 : 1) * (ATT_ROWS / (sh.Hq / sh.Hkv));
+    const int64_t groups = (sh.T + group - 1) / group;
+    const int64_t tiles = (((int64_t)sh.width << sh.page_log2) + kt - 1) / kt + ATT_ITEM_COST;
+    return (double)sh.B * sh.Hkv * groups * tiles < 2147483648.0;
 }
 
 cudaError_t launch_tree_attend(const TreeAttendParams& p, int dtype, int num_sms, void* ws, unsigned* err, bool stall,
