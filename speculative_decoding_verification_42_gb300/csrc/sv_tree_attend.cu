@@ -16,14 +16,15 @@
 //  * Rows are tiles of 128: floor(128 / G) nodes times G heads, the M of the
 //    MMA, whatever their number: the tensor pipe has time for 128 rows while
 //    the keys stream, so few rows need no other form.
-//  * Work items are (sequence, key head, group of row tiles).  All items' key
+//  * Work items are (key head, sequence, group of row tiles).  All items' key
 //    tiles in a row are cut into equal ranges, one per SM, whatever the batch:
 //    a long cache with few rows fills the machine, a ragged batch is balanced,
 //    and the lengths are read on the GPU.  An item cut by a range's end leaves
-//    partial sums (O, m, l) that k_tree_combine joins.
-//  * A CTA has one producer warp (tensor-map copies of whole pages into a ring
-//    of 128-byte-swizzled key and value tiles), one MMA thread, two cleaning
-//    warps and one or two softmax warpgroups, a thread per row.  With heads up
+//    partial sums (O, m, l) that k_tree_combine joins.  The key head comes
+//    first, so that the SMs of all heads go through the same pages together.
+//  * A CTA has two producer warps (tensor-map copies of whole pages into rings
+//    of 128-byte-swizzled key and value tiles), an MMA warp and one or two
+//    softmax warpgroups, a thread per row.  With heads up
 //    to 128 elements two streams of (S, O) share tensor memory's 512 columns:
 //    an item of one row tile gives its even key tiles to one and its odd ones
 //    to the other (own m, l, O; joined at the end), an item of two row tiles
@@ -34,7 +35,7 @@
 // What a row does not see must not touch it, whatever it holds: scores are
 // replaced by -inf before the maximum, but P V multiplies hidden values by a
 // zero probability, and 0 x NaN is NaN.  In the tiles that some row sees only
-// in part the cleaning warps zero the rows beyond the sequence and every
+// in part the softmax warps zero the rows beyond the sequence and every
 // non-finite value in shared memory; rows that see a node with such values
 // (rare) add them afterwards.
 #include <math.h>
@@ -71,14 +72,14 @@ struct Att {                                  // DP: head size rounded up to 64
 struct __align__(16) AttMisc {
     uint64_t k_full[8], k_empty[8];  // key tiles: copied; read by the MMAs
     uint64_t v_full[8], v_empty[8];  // value tiles
-    uint64_t v_clean[8];             // the value tile may meet the MMAs
+    uint64_t v_clean[8];             // a masked value tile may meet the MMAs
     uint64_t q_full[2], q_empty[2];
     uint64_t s_full[2];            // scores of the stream's unit are in tensor memory
     uint64_t p_ready[2];           // its probabilities are (and O is scaled)
     uint64_t o_full[2], o_empty[2];  // the segment's O is complete; has been read
     uint64_t ml_full, ml_empty;    // stream 1's (m, l) for the join
     uint64_t drain;
-    uint32_t nf[8][4];             // value rows of the tile with non-finite elements
+    uint32_t nf[8][4];             // (masked) value rows of the tile with non-finite elements
     float2 ml[ATT_ROWS];
     int32_t scan[16];
     int32_t first, first_b;        // the range's first sequence, and its cost before the range
@@ -138,7 +139,7 @@ struct AttSplit {
     }
 };
 
-// the segments of a CTA: parts of items, in order of (sequence, key head, group)
+// the segments of a CTA: parts of items, in order of (key head, sequence, group)
 template <int KT>
 struct AttIter {
     int pos, end;               // cost positions in the order of all items
@@ -169,18 +170,16 @@ struct AttIter {
         ctx = l.ctx;
         n = l.n;
     }
-    // off: cost of sequence b0 before the range
-    __device__ __forceinline__ void start(const TreeAttendParams& p, const AttGeom& g, int pos0, int end0, int b0,
-                                          int off)
+    // head0: key head of the range's begin; off: cost of sequence b0 before it
+    __device__ __forceinline__ void start(const TreeAttendParams& p, const AttGeom& g, int pos0, int end0, int head0,
+                                          int b0, int off)
     {
         pos = pos0;
         end = end0;
         if (!more()) return;
+        hk = head0;
         b = b0;
         load_seq(p);
-        const int per_head = att_head_cost<KT>(p, g, ctx, n);
-        hk = off / per_head;
-        off -= hk * per_head;
         rp = 0;
         if (n > g.group)
             for (int t; off >= (t = att_cost<KT>(p, g, ctx, n, rp)); ++rp) off -= t;
@@ -196,18 +195,20 @@ struct AttIter {
             if (!more()) return;
             if ((++rp) * g.group >= n) {
                 rp = 0;
-                if (++hk == g.Hkv) {
-                    hk = 0;
-                    do {
-                        ++b;
-                        load_seq(p);
-                    } while (n == 0);
-                }
+                do {
+                    if (++b == p.s.B) {
+                        b = 0;
+                        ++hk;
+                    }
+                    load_seq(p);
+                } while (n == 0);
             }
             load_item(p, g);
         } while (tile0 >= tile1);
     }
     __device__ __forceinline__ int tiles() const { return tile1 - tile0; }
+    // the segment's first tile that some row sees only in part
+    __device__ __forceinline__ int first_masked() const { return max(0, mask_from / KT - tile0); }
     __device__ __forceinline__ bool whole() const { return tile0 == 0 && tile1 == ntiles; }
 };
 
@@ -263,6 +264,16 @@ __device__ __forceinline__ bool att_nonfinite(uint16_t h)
     return (h & e) == e;
 }
 
+// zeroes the non-finite ones of a word's two values; true when there was one
+template <bool F16>
+__device__ __forceinline__ bool clean_word(uint32_t& v)
+{
+    const bool lo = att_nonfinite<F16>((uint16_t)v), hi = att_nonfinite<F16>((uint16_t)(v >> 16));
+    if (lo) v &= 0xFFFF0000u;
+    if (hi) v &= 0x0000FFFFu;
+    return lo || hi;
+}
+
 template <bool F16, int DP>
 __global__ void __launch_bounds__(Att<DP>::THREADS, 1)
     k_tree_attend(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
@@ -297,7 +308,7 @@ __global__ void __launch_bounds__(Att<DP>::THREADS, 1)
         for (int i = 0; i < VS; ++i) {
             mbar_init(&ms.v_full[i], 1);
             mbar_init(&ms.v_empty[i], 1);
-            mbar_init(&ms.v_clean[i], 2);
+            mbar_init(&ms.v_clean[i], 4 * NS);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&ms.q_full[i], 1);
@@ -314,14 +325,14 @@ __global__ void __launch_bounds__(Att<DP>::THREADS, 1)
         fence_barrier_init();
     }
     // ---- this CTA's range: a scan of the sequences' costs
-    int total = 0;
+    int total = 0, per_head = 0, head0 = 0;
     {
         const int per = (p.s.B + A::THREADS - 1) / A::THREADS;
         const int s0 = min(p.s.B, tid * per), s1 = min(p.s.B, s0 + per);
         int sum = 0;
         for (int b = s0; b < s1; ++b) {
             const SeqLen l = tree_len(p.s, b);
-            sum += w.g.Hkv * att_head_cost<KT>(p, w.g, l.ctx, l.n);
+            sum += att_head_cost<KT>(p, w.g, l.ctx, l.n);
         }
         int inc = sum;
 #pragma unroll
@@ -338,13 +349,16 @@ __global__ void __launch_bounds__(Att<DP>::THREADS, 1)
             if (i < warp) before += v;
             total += v;
         }
-        const AttSplit split(total, gridDim.x);
-        const int pos0 = split.start(blockIdx.x);
-        if (sum > 0 && pos0 >= before && pos0 < before + sum) {
-            int b = s0, off = pos0 - before;
+        per_head = total;
+        total *= w.g.Hkv;
+        const int pos0 = AttSplit(total, gridDim.x).start(blockIdx.x);
+        head0 = per_head ? pos0 / per_head : 0;
+        const int in_head = pos0 - head0 * per_head;
+        if (sum > 0 && in_head >= before && in_head < before + sum) {
+            int b = s0, off = in_head - before;
             for (;; ++b) {
                 const SeqLen l = tree_len(p.s, b);
-                const int t = w.g.Hkv * att_head_cost<KT>(p, w.g, l.ctx, l.n);
+                const int t = att_head_cost<KT>(p, w.g, l.ctx, l.n);
                 if (off < t) break;
                 off -= t;
             }
@@ -359,165 +373,164 @@ __global__ void __launch_bounds__(Att<DP>::THREADS, 1)
     const AttSplit split(total, gridDim.x);
     const bool busy = (int)blockIdx.x < split.ctas;
     AttIter<KT> it;
-    it.start(p, w.g, busy ? split.start(blockIdx.x) : 0, busy ? split.start(blockIdx.x + 1) : 0, ms.first_b, ms.first);
+    it.start(p, w.g, busy ? split.start(blockIdx.x) : 0, busy ? split.start(blockIdx.x + 1) : 0, head0,
+             ms.first_b, ms.first);
     bool ok = true;
 
-    if (warp == 0) {
-        // ---------------- producer: pages of K and V, and the rows of Q
-        uint32_t ki = 0, vi = 0, qi = 0;  // key tiles, value tiles and row tiles of Q so far
+    if (warp == 0 || warp == 2) {
+        // ---------------- producers: warp 0 keys and the rows of Q, warp 2 values
+        const bool is_k = warp == 0;
+        const CUtensorMap* map = is_k ? &map_k : &map_v;
+        unsigned char* const ring = is_k ? k_smem : v_smem;
+        uint64_t *const full = is_k ? ms.k_full : ms.v_full, *const empty = is_k ? ms.k_empty : ms.v_empty;
+        const uint32_t stages = is_k ? KS : VS;
+        uint32_t n = 0, st = 0, round = 0, qi = 0;  // tiles so far, the next one's stage; row tiles of Q
         // page ids come 32 at a time, one load per block of the table row and one
         // block ahead: a lookup per tile would put its latency between the copies
-        int blk = -2, prev = 0, cur = 0, ahead = 0;  // of the item's row: ids of blocks blk - 1, blk, blk + 1
+        int blk = -2, cur = 0, ahead = 0;  // ids of blocks blk and blk + 1 of the item's row
         auto ids = [&](int k) {
             const int i = k * 32 + lane, pages = (it.limit + (1 << p.s.page_log2) - 1) >> p.s.page_log2;
             return i < pages ? __ldg(p.table + (int64_t)it.b * p.s.width + i) : -1;
         };
-        auto seek = [&](int kb) {  // called for the keys, which run ahead of the values by a tile at most
-            const int k = (kb >> p.s.page_log2) >> 5;
-            if (k == blk) return;
-            prev = cur;
-            cur = k == blk + 1 ? ahead : ids(k);
-            ahead = ids(k + 1);
-            blk = k;
-        };
-        auto tile = [&](const CUtensorMap* map, int kb, unsigned char* dst, uint64_t* full, uint64_t* empty,
-                        bool reused, uint32_t parity) {
-            if (reused) ok = ok && __all_sync(0xffffffffu, att_wait(empty, parity, failed, limit));
+        auto copy = [&](int t) {
+            const int kb = (it.tile0 + t) * KT, first = kb >> p.s.page_log2;
+            if ((first >> 5) != blk) {
+                cur = (first >> 5) == blk + 1 ? ahead : ids(first >> 5);
+                blk = first >> 5;
+                ahead = ids(blk + 1);
+            }
+            if (n >= stages) ok = ok && __all_sync(0xffffffffu, att_wait(&empty[st], (round - 1) & 1, failed, limit));
             if (!ok || w.stall) return;
             const int boxes = (min(KT, it.limit - kb) + w.page_box - 1) / w.page_box;
-            if (lane == 0) mbar_arrive_expect_tx(full, (uint32_t)(boxes * w.page_box * 128 * NH));
-            __syncwarp();
+            if (lane == 0) mbar_arrive_expect_tx(&full[st], (uint32_t)(boxes * w.page_box * 128 * NH));
             // a tile's pages (at most 16) lie in one block
-            const int key = kb + lane * w.page_box, first = kb >> p.s.page_log2;
-            const int page = __shfl_sync(0xffffffffu, first >> 5 == blk ? cur : prev, (key >> p.s.page_log2) & 31);
+            const int key = kb + lane * w.page_box;
+            const int page = __shfl_sync(0xffffffffu, cur, (key >> p.s.page_log2) & 31);
+            unsigned char* dst = ring + st * A::UNIT + lane * w.page_box * 128;
             if (lane < boxes)
                 for (int h = 0; h < NH; ++h)
-                    tma_4d(dst + (h * KT + lane * w.page_box) * 128, map, h * 64, it.hk,
-                           key & ((1 << p.s.page_log2) - 1), page, full);
+                    tma_4d(dst + h * KT * 128, map, h * 64, it.hk, key & ((1 << p.s.page_log2) - 1), page, &full[st]);
+            ++n;
+            if (++st == stages) st = 0, ++round;
         };
-        auto keys = [&](int t) {
-            const uint32_t st = ki % KS;
-            seek((it.tile0 + t) * KT);
-            if (ok)
-                tile(&map_k, (it.tile0 + t) * KT, k_smem + st * A::UNIT, &ms.k_full[st], &ms.k_empty[st], ki >= KS,
-                     (ki / KS - 1) & 1);
-            if (ok && !w.stall) ++ki;
-        };
-        auto values = [&](int t) {
-            const uint32_t st = vi % VS;
-            if (ok)
-                tile(&map_v, (it.tile0 + t) * KT, v_smem + st * A::UNIT, &ms.v_full[st], &ms.v_empty[st], vi >= VS,
-                     (vi / VS - 1) & 1);
-            if (ok && !w.stall) ++vi;
-        };
-        for (; ok && it.more(); it.next(p, w.g)) {
-            // two streams on alternate tiles: the scores run one tile further ahead
-            const int nt = it.tiles(), lead = NS == 2 && !it.dual ? 1 : 0;
+        for (; ok && it.more() && !w.stall; it.next(p, w.g)) {
+            const int nt = it.tiles();
             blk = -2;
-            keys(0);
-            for (int s = 0; s < (it.dual ? 2 : 1); ++s) {
-                const uint32_t qb = qi % NS;
-                if (qi >= NS)
-                    ok = ok &&
-                         __all_sync(0xffffffffu, att_wait(&ms.q_empty[qb], (qi / NS - 1) & 1, failed, limit));
-                if (!ok || w.stall) break;
-                ++qi;
-                if (lane == 0) {
-                    mbar_arrive_expect_tx(&ms.q_full[qb], (uint32_t)(w.q_box * w.g.G * 128 * NH));
-                    for (int h = 0; h < NH; ++h)
-                        tma_4d(q_smem + qb * A::QB + h * ATT_ROWS * 128, &map_q, h * 64, it.hk * w.g.G,
-                               it.t0 + s * w.g.tpt, it.b, &ms.q_full[qb]);
+            copy(0);
+            if (is_k)
+                for (int s = 0; s < (it.dual ? 2 : 1); ++s) {
+                    const uint32_t qb = qi % NS;
+                    if (qi >= NS)
+                        ok = ok &&
+                             __all_sync(0xffffffffu, att_wait(&ms.q_empty[qb], (qi / NS - 1) & 1, failed, limit));
+                    if (!ok) break;
+                    ++qi;
+                    if (lane == 0) {
+                        mbar_arrive_expect_tx(&ms.q_full[qb], (uint32_t)(w.q_box * w.g.G * 128 * NH));
+                        for (int h = 0; h < NH; ++h)
+                            tma_4d(q_smem + qb * A::QB + h * ATT_ROWS * 128, &map_q, h * 64, it.hk * w.g.G,
+                                   it.t0 + s * w.g.tpt, it.b, &ms.q_full[qb]);
+                    }
                 }
-            }
-            for (int t = 0; ok && t < nt; ++t) {
-                for (int k = t == 0 ? 1 : t + lead; k <= min(t + lead, nt - 1); ++k) keys(k);
-                values(t);
-            }
-            if (w.stall) break;
+            for (int t = 1; ok && t < nt; ++t) copy(t);
         }
         // drain: every tile and row tile of Q has been read by the MMAs, so no
         // copy or commit is still on its way when the CTA leaves
-        const uint32_t k0 = ki > KS ? ki - KS : 0, v0 = vi > VS ? vi - VS : 0, q0 = qi > NS ? qi - NS : 0;
-        for (uint32_t i = k0; ok && i < ki; ++i) ok = att_wait(&ms.k_empty[i % KS], (i / KS) & 1, failed, limit);
-        for (uint32_t i = v0; ok && i < vi; ++i) ok = att_wait(&ms.v_empty[i % VS], (i / VS) & 1, failed, limit);
+        const uint32_t n0 = n > stages ? n - stages : 0, q0 = qi > NS ? qi - NS : 0;
+        for (uint32_t i = n0; ok && i < n; ++i) ok = att_wait(&empty[i % stages], (i / stages) & 1, failed, limit);
         for (uint32_t i = q0; ok && i < qi; ++i) ok = att_wait(&ms.q_empty[i % NS], (i / NS) & 1, failed, limit);
         if (!ok) {
             // a role gave up: at least every copy issued has landed
             if (lane == 0) ms.failed = 1;
-            for (uint32_t i = k0; i < ki; ++i) mbar_wait_n(&ms.k_full[i % KS], (i / KS) & 1, limit);
-            for (uint32_t i = v0; i < vi; ++i) mbar_wait_n(&ms.v_full[i % VS], (i / VS) & 1, limit);
+            for (uint32_t i = n0; i < n; ++i) mbar_wait_n(&full[i % stages], (i / stages) & 1, limit);
             for (uint32_t i = q0; i < qi; ++i) mbar_wait_n(&ms.q_full[i % NS], (i / NS) & 1, limit);
         }
     } else if (warp == 1) {
-        if (lane == 0) {
-            // ---------------- MMA issuer
-            constexpr uint32_t ID_S = umma_idesc(F16, false, ATT_ROWS, KT);
-            constexpr uint32_t ID_O = umma_idesc(F16, true, ATT_ROWS, DP);
-            uint32_t base = 0, qi = 0;
-            uint32_t n_unit[2] = {0, 0}, n_seg[2] = {0, 0};  // units and segments of each stream so far
-            const uint32_t k_u = smem_u32(k_smem), v_u = smem_u32(v_smem), q_u = smem_u32(q_smem);
-            for (; ok && it.more(); it.next(p, w.g)) {
-                const bool dual = it.dual;
-                const int nt = it.tiles(), units = dual ? 2 * nt : nt;
-                auto scores = [&](int u) {
-                    const int s = NS == 2 ? u & 1 : 0, t = dual ? u >> 1 : u;
-                    const uint32_t i = base + t, st = i % KS;
-                    const uint32_t q = (qi + (dual ? s : 0)), qb = q % NS;
-                    if (!dual || s == 0) ok = ok && att_wait(&ms.k_full[st], (i / KS) & 1, failed, limit);
-                    if (t == 0 && (dual || u == 0))
-                        ok = ok && att_wait(&ms.q_full[qb], (q / NS) & 1, failed, limit);
-                    if (!ok) return;
-                    tmem_fence_after();
-                    const uint32_t ka = k_u + st * A::UNIT, qa = q_u + qb * A::QB;
+        // ---------------- MMA issuer: the whole warp waits, one lane issues
+        constexpr uint32_t ID_S = umma_idesc(F16, false, ATT_ROWS, KT);
+        constexpr uint32_t ID_O = umma_idesc(F16, true, ATT_ROWS, DP);
+        uint32_t base = 0, qi = 0, cleaned = 0;  // cleaned: bit per stage, phases of v_clean so far
+        uint32_t n_unit[2] = {0, 0}, n_seg[2] = {0, 0};  // units and segments of each stream so far
+        // descriptors: Q and K are K-major with 8-row groups 1024 bytes apart; V is
+        // N-major, 64-column boxes KT rows apart, 8-row groups 1024 bytes apart
+        const uint64_t q_desc = umma_desc(smem_u32(q_smem), 16, 1024), k_desc = umma_desc(smem_u32(k_smem), 16, 1024);
+        const uint64_t v_desc = umma_desc(smem_u32(v_smem), KT * 128, 1024);
+        auto wait = [&](uint64_t* bar, uint32_t parity) {
+            ok = ok && __all_sync(0xffffffffu, att_wait(bar, parity & 1, failed, limit));
+        };
+        for (; ok && it.more(); it.next(p, w.g)) {
+            const bool dual = it.dual;
+            const int nt = it.tiles(), units = dual ? 2 * nt : nt, masked = it.first_masked();
+            auto scores = [&](int u) {
+                const int s = NS == 2 ? u & 1 : 0, t = dual ? u >> 1 : u;
+                const uint32_t i = base + t, st = i % KS;
+                const uint32_t q = qi + (dual ? s : 0), qb = q % NS;
+                if (!dual || s == 0) wait(&ms.k_full[st], i / KS);
+                if (t == 0 && (dual || u == 0)) wait(&ms.q_full[qb], q / NS);
+                if (!ok) return;
+                tmem_fence_after();
+                if (elect_one()) {
+                    const uint64_t a = q_desc + qb * (A::QB / 16), b = k_desc + st * (A::UNIT / 16);
 #pragma unroll
                     for (int k = 0; k < DP / 16; ++k)
-                        umma_ss(tmem + A::s_col(s),
-                                umma_desc(qa + (k / 4) * ATT_ROWS * 128 + (k % 4) * 32, 16, 1024),
-                                umma_desc(ka + (k / 4) * KT * 128 + (k % 4) * 32, 16, 1024), ID_S, k > 0);
+                        umma_ss(tmem + A::s_col(s), a + ((k / 4) * ATT_ROWS * 128 + (k % 4) * 32) / 16,
+                                b + ((k / 4) * KT * 128 + (k % 4) * 32) / 16, ID_S, k > 0);
                     umma_commit(&ms.s_full[s]);
                     if (!dual || s == 1) umma_commit(&ms.k_empty[st]);
                     if (t == nt - 1) umma_commit(&ms.q_empty[qb]);
-                };
-                auto values = [&](int u) {
-                    const int s = NS == 2 ? u & 1 : 0, t = dual ? u >> 1 : u;
-                    const uint32_t i = base + t, st = i % VS;
-                    const bool first = u < NS;
-                    if (!dual || s == 0) ok = ok && att_wait(&ms.v_clean[st], (i / VS) & 1, failed, limit);
-                    if (first && n_seg[s] > 0)
-                        ok = ok && att_wait(&ms.o_empty[s], (n_seg[s] - 1) & 1, failed, limit);
-                    ok = ok && att_wait(&ms.p_ready[s], n_unit[s] & 1, failed, limit);
-                    if (!ok) return;
-                    ++n_unit[s];
-                    if (first) ++n_seg[s];
-                    tmem_fence_after();
-                    const uint32_t va = v_u + st * A::UNIT;
+                }
+                __syncwarp();
+            };
+            auto values = [&](int u) {
+                const int s = NS == 2 ? u & 1 : 0, t = dual ? u >> 1 : u;
+                const uint32_t i = base + t, st = i % VS;
+                const bool first = u < NS;
+                if (!dual || s == 0) {
+                    if (t >= masked) {
+                        wait(&ms.v_clean[st], cleaned >> st);
+                        cleaned ^= 1u << st;
+                    } else {
+                        wait(&ms.v_full[st], i / VS);
+                    }
+                }
+                if (first && n_seg[s] > 0) wait(&ms.o_empty[s], n_seg[s] - 1);
+                wait(&ms.p_ready[s], n_unit[s]);
+                if (!ok) return;
+                ++n_unit[s];
+                if (first) ++n_seg[s];
+                tmem_fence_after();
+                if (elect_one()) {
+                    const uint64_t b = v_desc + st * (A::UNIT / 16);
 #pragma unroll
                     for (int k = 0; k < KT / 16; ++k)
-                        umma_ts(tmem + A::o_col(s), tmem + A::s_col(s) + k * 8,
-                                umma_desc(va + k * 2048, KT * 128, 1024), ID_O, !first || k > 0);
+                        umma_ts(tmem + A::o_col(s), tmem + A::s_col(s) + k * 8, b + k * 128, ID_O, !first || k > 0);
                     if (!dual || s == 1) umma_commit(&ms.v_empty[st]);
                     if (u + NS >= units) umma_commit(&ms.o_full[s]);
-                };
-                for (int u = 0; ok && u < min(NS, units); ++u) scores(u);
-                for (int u = 0; ok && u < units; ++u) {
-                    values(u);
-                    if (ok && u + NS < units) scores(u + NS);
                 }
-                base += nt;
-                qi += dual ? 2 : 1;
+                __syncwarp();
+            };
+            for (int u = 0; ok && u < min(NS, units); ++u) scores(u);
+            for (int u = 0; ok && u < units; ++u) {
+                values(u);
+                if (ok && u + NS < units) scores(u + NS);
             }
-            if (!ok) {
+            base += nt;
+            qi += dual ? 2 : 1;
+        }
+        if (!ok) {
+            // no MMA is in flight when the CTA leaves (one lane issued them all: the
+            // election takes the same lane of a full warp every time)
+            if (elect_one()) {
                 ms.failed = 1;
-                umma_commit(&ms.drain);  // no MMA is in flight when the CTA leaves
+                umma_commit(&ms.drain);
                 mbar_wait_n(&ms.drain, 0, limit);
             }
+            __syncwarp();
         }
-        __syncwarp();
-    } else if (warp < 4) {
-        // ---------------- cleaning warps: half of each value tile's rows each
-        if (warp == 2 && lane == 0) {
-            // the item's first tile lies in an earlier range: the one before it, or
-            // the cut is not the first of the item
+    } else if (warp == 3) {
+        // ---------------- this range's first item, where it began in an earlier
+        // range: the one before it, or the cut is not the first of the item
+        if (lane == 0) {
             AttCut cut{-1, 0, 0, 0, 0, 0};
             if (it.more() && it.tile0 > 0) {
                 const int first = split.owner(it.at + ATT_ITEM_COST);
@@ -527,49 +540,6 @@ __global__ void __launch_bounds__(Att<DP>::THREADS, 1)
             }
             w.cuts[blockIdx.x] = cut;
         }
-        constexpr int HALF = KT / 2;
-        const int r0 = (warp - 2) * HALF;
-        uint32_t base = 0;
-        for (; ok && it.more(); it.next(p, w.g)) {
-            const int nt = it.tiles(), end = it.ctx + it.n;
-            for (int t = 0; ok && t < nt; ++t) {
-                const uint32_t i = base + t, st = i % VS;
-                const int kb = (it.tile0 + t) * KT;
-                ok = __all_sync(0xffffffffu, att_wait(&ms.v_full[st], (i / VS) & 1, failed, limit));
-                if (!ok) break;
-                if (kb + KT > it.mask_from) {
-                    uint32_t* nf = ms.nf[st] + (warp - 2) * (HALF / 32);
-                    if (lane < HALF / 32) nf[lane] = 0;
-                    __syncwarp();
-                    // eight lanes per 128-byte row of a box
-                    for (int r = r0 + (lane >> 3); r < r0 + HALF; r += 4) {
-                        const int key = kb + r;
-                        if (key < it.mask_from) continue;
-#pragma unroll
-                        for (int h = 0; h < NH; ++h) {
-                            uint4* a = (uint4*)(v_smem + st * A::UNIT + (h * KT + r) * 128) + (lane & 7);
-                            uint4 x = key < end ? *a : make_uint4(0, 0, 0, 0);
-                            uint32_t* xs = &x.x;
-                            bool dirty = key >= end;
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                if (att_nonfinite<F16>((uint16_t)xs[k])) xs[k] &= 0xFFFF0000u, dirty = true;
-                                if (att_nonfinite<F16>((uint16_t)(xs[k] >> 16))) xs[k] &= 0xFFFFu, dirty = true;
-                            }
-                            if (dirty) {
-                                *a = x;
-                                if (key < end) atomicOr(&ms.nf[st][r >> 5], 1u << (r & 31));
-                            }
-                        }
-                    }
-                    fence_async_smem();
-                    __syncwarp();
-                }
-                if (lane == 0) mbar_arrive(&ms.v_clean[st]);
-            }
-            base += nt;
-        }
-        if (!ok && lane == 0) ms.failed = 1;
     } else {
         // ---------------- softmax: warpgroup s, thread = row
         const int s = (warp - 4) >> 2, row = (warp & 3) * 32 + lane;
@@ -589,7 +559,7 @@ __global__ void __launch_bounds__(Att<DP>::THREADS, 1)
                     for (int i = lane; i < Hq; i += 32) p.lse[(int64_t)r * Hq + i] = -INFINITY;
             }
         }
-        uint32_t base = 0, n_unit = 0, n_seg[2] = {0, 0}, n_ml = 0;
+        uint32_t base = 0, n_unit = 0, n_seg[2] = {0, 0}, n_ml = 0, cleaned = 0;
         for (; ok && it.more(); it.next(p, w.g)) {
             const bool dual = it.dual;
             const int nt = it.tiles(), units = dual ? 2 * nt : nt;
@@ -601,8 +571,44 @@ __global__ void __launch_bounds__(Att<DP>::THREADS, 1)
             float m = -INFINITY, l = 0.f;
             uint32_t pend[KT / 32] = {};  // seen keys with non-finite values, of the tile at pend_kb
             int pend_kb = -1;
+            int masked = it.first_masked();  // later: the first masked tile not counted in `cleaned`
             const uint32_t o_addr = tmem + A::o_col(s) + lanes, s_addr = tmem + A::s_col(s) + lanes;
 
+            // the rows of a masked value tile beyond the sequence become 0, and so does
+            // what is not finite (noted in nf); the warpgroups share the tile where
+            // both read it.  Eight lanes per 128-byte row of a box.
+            auto clean = [&](uint32_t st, int kb, bool shared) {
+                const int per = shared ? KT / 8 : KT / 4, r0 = ((shared ? s * 4 : 0) + (warp & 3)) * per;
+                uint32_t bits = 0;
+#pragma unroll 1
+                for (int i = 0; i < per; i += 4) {
+                    const int r = r0 + i + (lane >> 3), key = kb + r;
+                    bool found = false;
+                    if (key >= it.mask_from) {
+#pragma unroll
+                        for (int h = 0; h < NH; ++h) {
+                            uint4* a = (uint4*)(v_smem + st * A::UNIT + (h * KT + r) * 128) + (lane & 7);
+                            if (key >= it.ctx + it.n) {
+                                *a = make_uint4(0, 0, 0, 0);
+                                continue;
+                            }
+                            uint4 x = *a;
+                            const bool bad = clean_word<F16>(x.x) | clean_word<F16>(x.y) | clean_word<F16>(x.z) |
+                                             clean_word<F16>(x.w);
+                            if (bad) *a = x;
+                            found = found || bad;
+                        }
+                    }
+                    const uint32_t v = __ballot_sync(0xffffffffu, found);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if ((v >> (8 * j)) & 0xFFu) bits |= 1u << (i + j);
+                }
+                fence_async_smem();
+                if (lane < per / 16) ((uint16_t*)ms.nf[st])[r0 / 16 + lane] = (uint16_t)(bits >> (16 * lane));
+                __syncwarp();
+                if (lane == 0) mbar_arrive_n(&ms.v_clean[st], NS == 2 && !shared ? 2 : 1);
+            };
             // O += the non-finite values of pend's keys (the MMA saw zeros there)
             auto add_nonfinite = [&]() {
                 for (int x = 0; x < KT / 32; ++x) {
@@ -637,20 +643,30 @@ __global__ void __launch_bounds__(Att<DP>::THREADS, 1)
                 if (!ok) break;
                 ++n_unit;
                 tmem_fence_after();
+                const uint32_t vi = base + tile, vst = vi % VS;
+                const bool part = kb + KT > it.mask_from;
+                if (part) {
+                    // phases of v_clean of the tiles before this one (the other stream's)
+                    for (; masked < tile; ++masked) cleaned ^= 1u << ((base + masked) % VS);
+                    ++masked;
+                    ok = __all_sync(0xffffffffu, att_wait(&ms.v_full[vst], (vi / VS) & 1, failed, limit));
+                    if (!ok) break;
+                    clean(vst, kb, dual);
+                    ok = __all_sync(0xffffffffu, att_wait(&ms.v_clean[vst], (cleaned >> vst) & 1, failed, limit));
+                    if (!ok) break;
+                    cleaned ^= 1u << vst;
+                }
                 if (active) {
                     // every earlier P V of the stream is complete: the scores were issued after it
                     if (pend_kb >= 0) add_nonfinite();
-                    if (kb + KT > it.mask_from) {
+                    if (part) {
                         // hidden scores become -inf in tensor memory, before the passes over them
-                        const uint32_t i = base + tile, st = i % VS;
-                        ok = __all_sync(0xffffffffu, att_wait(&ms.v_clean[st], (i / VS) & 1, failed, limit));
-                        if (!ok) break;
                         uint32_t some = 0;
 #pragma unroll 1
                         for (int y = 0; y < KT / 32; ++y) {
                             const uint32_t see = att_sees(p, it.b, t, it.ctx, it.n, kb + 32 * y);
                             if (__all_sync(0xffffffffu, see == ~0u)) continue;
-                            some |= see & *(volatile uint32_t*)&ms.nf[st][y];
+                            some |= see & *(volatile uint32_t*)&ms.nf[vst][y];
                             uint32_t x[32];
                             tmem_ld<32>(s_addr + 32 * y, x);
 #pragma unroll
@@ -665,7 +681,7 @@ __global__ void __launch_bounds__(Att<DP>::THREADS, 1)
 #pragma unroll
                             for (int y = 0; y < KT / 32; ++y)
                                 pend[y] = att_sees(p, it.b, t, it.ctx, it.n, kb + 32 * y) &
-                                          *(volatile uint32_t*)&ms.nf[st][y];
+                                          *(volatile uint32_t*)&ms.nf[vst][y];
                         }
                     }
                     // the row's maximum, then its exponentials: two passes over the
@@ -726,6 +742,7 @@ __global__ void __launch_bounds__(Att<DP>::THREADS, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&ms.p_ready[s]);
             }
+            for (; masked < nt; ++masked) cleaned ^= 1u << ((base + masked) % VS);
             base += nt;
             if (!ok) break;
 
