@@ -22,9 +22,11 @@
 //    and the lengths are read on the GPU.  An item cut by a range's end leaves
 //    partial sums (O, m, l) that k_tree_combine joins.  The key head comes
 //    first, so that the SMs of all heads go through the same pages together.
-//  * A CTA has two producer warps (tensor-map copies of whole pages into rings
-//    of 128-byte-swizzled key and value tiles), an MMA warp and one or two
-//    softmax warpgroups, a thread per row.  With heads up
+//  * A CTA has a scheduling warp (it walks the range and hands the others one
+//    segment of an item at a time, which keeps that state out of their
+//    registers), two producer warps (tensor-map copies of whole pages into
+//    rings of 128-byte-swizzled key and value tiles), an MMA warp and one or
+//    two softmax warpgroups, a thread per row.  With heads up
 //    to 128 elements two streams of (S, O) share tensor memory's 512 columns:
 //    an item of one row tile gives its even key tiles to one and its odd ones
 //    to the other (own m, l, O; joined at the end), an item of two row tiles
@@ -40,6 +42,8 @@
 // (rare) add them afterwards.
 #include <math.h>
 
+#include <algorithm>
+
 #include "sv_tcgen.cuh"
 #include "sv_tree.cuh"
 
@@ -49,6 +53,7 @@ constexpr int ATT_ROWS = 128;                 // rows of a row tile: M of the MM
 constexpr int ATT_SMEM = 227 * 1024;          // shared memory of a CTA
 constexpr int ATT_MISC = 2048;                // of it: barriers and small tables
 constexpr uint32_t ATT_TMEM_COLS = 512;
+constexpr int ATT_SEGS = 4;                   // segments handed out ahead
 constexpr uint32_t ATT_WAIT_POLLS = 1u << 17;  // limit of a wait: some seconds (a poll sleeps for microseconds)
 constexpr uint32_t ATT_STALL_POLLS = 4096;    // SPEC_FAULT_STALL_STREAM
 constexpr float ATT_LAZY = 8.f;               // log2 growth of the maximum that O takes unscaled
@@ -69,6 +74,18 @@ struct Att {                                  // DP: head size rounded up to 64
     static_assert(STAGES >= 4 && SMEM <= ATT_SMEM, "the ring fits");
 };
 
+// one segment: the key tiles tile0 .. tile0 + nt - 1 of an item (nt = 0: the range's end)
+struct __align__(16) AttSeg {
+    int32_t b, hk;
+    int32_t ctx, n;
+    int32_t t0, ntok;           // the item's first node, and nodes
+    int32_t tile0, nt;
+    int32_t limit;              // keys any of its rows may see
+    int32_t mask_from;          // keys below are seen by all its rows
+    int32_t dual;               // two row tiles
+    int32_t whole;              // all of the item's tiles
+};
+
 struct __align__(16) AttMisc {
     uint64_t k_full[8], k_empty[8];  // key tiles: copied; read by the MMAs
     uint64_t v_full[8], v_empty[8];  // value tiles
@@ -78,7 +95,9 @@ struct __align__(16) AttMisc {
     uint64_t p_ready[2];           // its probabilities are (and O is scaled)
     uint64_t o_full[2], o_empty[2];  // the segment's O is complete; has been read
     uint64_t ml_full, ml_empty;    // stream 1's (m, l) for the join
+    uint64_t seg_full[ATT_SEGS], seg_empty[ATT_SEGS];
     uint64_t drain;
+    AttSeg seg[ATT_SEGS];
     uint32_t nf[8][4];             // (masked) value rows of the tile with non-finite elements
     float2 ml[ATT_ROWS];
     int32_t scan[16];
@@ -148,19 +167,15 @@ struct AttIter {
     int ctx, n;
     int t0, ntok;               // its first node and nodes
     int ntiles, tile0, tile1;   // its key tiles, and this segment's (none: tile0 >= tile1)
-    int limit;                  // keys any of its rows may see
-    int mask_from;              // keys below are seen by all its rows
-    bool dual;                  // two row tiles
+    int limit;                  // keys some of its rows see
 
     __device__ __forceinline__ bool more() const { return pos < end; }
     __device__ __forceinline__ void load_item(const TreeAttendParams& p, const AttGeom& g)
     {
         t0 = rp * g.group;
         ntok = min(g.group, n - t0);
-        dual = ntok > g.tpt;
         limit = att_limit(p, g, ctx, n, rp);
         ntiles = (limit + KT - 1) / KT;
-        mask_from = p.mask ? ctx : ctx + t0 + 1;
         tile0 = max(pos - at - ATT_ITEM_COST, 0);
         tile1 = min(end - at - ATT_ITEM_COST, ntiles);
     }
@@ -206,10 +221,6 @@ struct AttIter {
             load_item(p, g);
         } while (tile0 >= tile1);
     }
-    __device__ __forceinline__ int tiles() const { return tile1 - tile0; }
-    // the segment's first tile that some row sees only in part
-    __device__ __forceinline__ int first_masked() const { return max(0, mask_from / KT - tile0); }
-    __device__ __forceinline__ bool whole() const { return tile0 == 0 && tile1 == ntiles; }
 };
 
 // an item's tiles cut by the start of CTA c's range; c is the first such cut
@@ -264,6 +275,13 @@ __device__ __forceinline__ bool att_nonfinite(uint16_t h)
     return (h & e) == e;
 }
 
+// the segment's first tile that some row sees only in part
+template <int KT>
+__device__ __forceinline__ int att_first_masked(const AttSeg& sg)
+{
+    return max(0, sg.mask_from / KT - sg.tile0);
+}
+
 // zeroes the non-finite ones of a word's two values; true when there was one
 template <bool F16>
 __device__ __forceinline__ bool clean_word(uint32_t& v)
@@ -272,6 +290,78 @@ __device__ __forceinline__ bool clean_word(uint32_t& v)
     if (lo) v &= 0xFFFF0000u;
     if (hi) v &= 0x0000FFFFu;
     return lo || hi;
+}
+
+// One warp's part of cleaning a masked value tile (keys from kb on): rows from
+// key `end` on become 0, and so does what is not finite, noted in nf.  A tile
+// that both warpgroups read is shared between them.  Eight lanes per 128-byte
+// row of a box.
+template <bool F16, int DP>
+__device__ __forceinline__ void att_clean(AttMisc& ms, unsigned char* v_smem, uint32_t st, int kb, int from, int end,
+                                          bool shared, int s, int quarter, int lane)
+{
+    using A = Att<DP>;
+    const int per = shared ? A::KT / 8 : A::KT / 4, r0 = ((shared ? s * 4 : 0) + quarter) * per;
+    uint32_t bits = 0;
+#pragma unroll 4
+    for (int i = 0; i < per; i += 4) {
+        const int r = r0 + i + (lane >> 3), key = kb + r;
+        bool found = false;
+        if (key >= from) {
+#pragma unroll
+            for (int h = 0; h < A::NH; ++h) {
+                uint4* a = (uint4*)(v_smem + st * A::UNIT + (h * A::KT + r) * 128) + (lane & 7);
+                if (key >= end) {
+                    *a = make_uint4(0, 0, 0, 0);
+                    continue;
+                }
+                uint4 x = *a;
+                const bool bad = clean_word<F16>(x.x) | clean_word<F16>(x.y) | clean_word<F16>(x.z) |
+                                 clean_word<F16>(x.w);
+                if (bad) *a = x;
+                found = found || bad;
+            }
+        }
+        const uint32_t v = __ballot_sync(0xffffffffu, found);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if ((v >> (8 * j)) & 0xFFu) bits |= 1u << (i + j);
+    }
+    fence_async_smem();
+    if (lane < per / 16) ((uint16_t*)ms.nf[st])[r0 / 16 + lane] = (uint16_t)(bits >> (16 * lane));
+    __syncwarp();
+    if (lane == 0) mbar_arrive_n(&ms.v_clean[st], A::NS == 2 && !shared ? 2 : 1);
+}
+
+// O += the non-finite values of the keys kb + i whose bits i are set in rows' words
+template <bool F16, int KT>
+__device__ __noinline__ void att_add_nonfinite(const TreeAttendParams& p, uint4 rows, int b, int hk, int kb,
+                                               uint32_t o_addr)
+{
+#pragma unroll 1
+    for (int y = 0; y < KT / 32; ++y) {
+        const uint32_t mine = y == 0 ? rows.x : y == 1 ? rows.y : y == 2 ? rows.z : rows.w;
+        for (uint32_t any = __reduce_or_sync(0xffffffffu, mine); any; any &= any - 1) {
+            const int bit = __ffs(any) - 1, key = kb + 32 * y + bit;
+            const int page = __ldg(p.table + (int64_t)b * p.s.width + (key >> p.s.page_log2));
+            if (page < 0 || page >= p.s.num_pages) continue;
+            const uint16_t* v = (const uint16_t*)p.c.v + page * p.c.page +
+                                (key & ((1 << p.s.page_log2) - 1)) * p.c.token + hk * p.c.head;
+#pragma unroll 1
+            for (int d = 0; d < p.s.D; d += 16) {
+                uint32_t o[16];
+                tmem_ld<16>(o_addr + d, o);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const uint16_t e = __ldg(v + d + i);
+                    if (att_nonfinite<F16>(e) && ((mine >> bit) & 1u))
+                        o[i] = __float_as_uint(__uint_as_float(o[i]) + Half2<F16>::one(e));
+                }
+                tmem_st<16>(o_addr + d, o);
+            }
+            tmem_wait_st();
+        }
+    }
 }
 
 template <bool F16, int DP>
@@ -317,6 +407,10 @@ __global__ void __launch_bounds__(Att<DP>::THREADS, 1)
             mbar_init(&ms.p_ready[i], 4);
             mbar_init(&ms.o_full[i], 1);
             mbar_init(&ms.o_empty[i], 4);
+        }
+        for (int i = 0; i < ATT_SEGS; ++i) {
+            mbar_init(&ms.seg_full[i], 1);
+            mbar_init(&ms.seg_empty[i], 3 + 4 * NS);
         }
         mbar_init(&ms.ml_full, 4);
         mbar_init(&ms.ml_empty, 4);
@@ -370,75 +464,128 @@ __global__ void __launch_bounds__(Att<DP>::THREADS, 1)
     __syncthreads();
     tmem_fence_after();
     const uint32_t tmem = ms.tmem;
-    const AttSplit split(total, gridDim.x);
-    const bool busy = (int)blockIdx.x < split.ctas;
-    AttIter<KT> it;
-    it.start(p, w.g, busy ? split.start(blockIdx.x) : 0, busy ? split.start(blockIdx.x + 1) : 0, head0,
-             ms.first_b, ms.first);
     bool ok = true;
+    auto wait = [&](uint64_t* bar, uint32_t parity) {  // whole warp
+        ok = ok && __all_sync(0xffffffffu, att_wait(bar, parity & 1u, failed, limit));
+    };
+    // the k-th segment; done with it
+    auto segment = [&](uint32_t k) -> const AttSeg& {
+        wait(&ms.seg_full[k % ATT_SEGS], k / ATT_SEGS);
+        return ms.seg[k % ATT_SEGS];
+    };
+    auto release = [&](uint32_t k) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ms.seg_empty[k % ATT_SEGS]);
+    };
 
-    if (warp == 0 || warp == 2) {
+    if (warp == 3) {
+        // ---------------- scheduler
+        const AttSplit split(total, gridDim.x);
+        const bool busy = (int)blockIdx.x < split.ctas;
+        AttIter<KT> it;
+        it.start(p, w.g, busy ? split.start(blockIdx.x) : 0, busy ? split.start(blockIdx.x + 1) : 0, head0,
+                 ms.first_b, ms.first);
+        // an item that began in an earlier range: the one before it, or this cut
+        // is not the first of the item
+        AttCut cut{-1, 0, 0, 0, 0, 0};
+        if (it.more() && it.tile0 > 0) {
+            const int first = split.owner(it.at + ATT_ITEM_COST);
+            if (first == (int)blockIdx.x - 1)
+                cut = AttCut{first, split.owner(it.at + ATT_ITEM_COST + it.ntiles - 1), it.b, it.hk, it.t0,
+                             it.ntok * w.g.G};
+        }
+        for (uint32_t k = 0; ok; ++k) {
+            const uint32_t slot = k % ATT_SEGS;
+            if (k >= ATT_SEGS) wait(&ms.seg_empty[slot], k / ATT_SEGS - 1);
+            if (!ok) break;
+            const bool more = it.more();
+            if (lane == 0) {
+                AttSeg& sg = ms.seg[slot];
+                sg.nt = more ? it.tile1 - it.tile0 : 0;
+                if (more) {
+                    sg.b = it.b;
+                    sg.hk = it.hk;
+                    sg.ctx = it.ctx;
+                    sg.n = it.n;
+                    sg.t0 = it.t0;
+                    sg.ntok = it.ntok;
+                    sg.tile0 = it.tile0;
+                    sg.limit = it.limit;
+                    sg.mask_from = p.mask ? it.ctx : it.ctx + it.t0 + 1;
+                    sg.dual = it.ntok > w.g.tpt;
+                    sg.whole = it.tile0 == 0 && it.tile1 == it.ntiles;
+                }
+                mbar_arrive(&ms.seg_full[slot]);
+                if (k == 0) w.cuts[blockIdx.x] = cut;
+            }
+            __syncwarp();
+            if (!more) break;
+            it.next(p, w.g);
+        }
+        if (!ok && lane == 0) ms.failed = 1;
+    } else if (warp == 0 || warp == 2) {
         // ---------------- producers: warp 0 keys and the rows of Q, warp 2 values
         const bool is_k = warp == 0;
         const CUtensorMap* map = is_k ? &map_k : &map_v;
         unsigned char* const ring = is_k ? k_smem : v_smem;
         uint64_t *const full = is_k ? ms.k_full : ms.v_full, *const empty = is_k ? ms.k_empty : ms.v_empty;
         const uint32_t stages = is_k ? KS : VS;
+        const int page_mask = (1 << p.s.page_log2) - 1;
         uint32_t n = 0, st = 0, round = 0, qi = 0;  // tiles so far, the next one's stage; row tiles of Q
-        // page ids come 32 at a time, one load per block of the table row and one
-        // block ahead: a lookup per tile would put its latency between the copies
-        int blk = -2, cur = 0, ahead = 0;  // ids of blocks blk and blk + 1 of the item's row
-        auto ids = [&](int k) {
-            const int i = k * 32 + lane, pages = (it.limit + (1 << p.s.page_log2) - 1) >> p.s.page_log2;
-            return i < pages ? __ldg(p.table + (int64_t)it.b * p.s.width + i) : -1;
-        };
-        auto copy = [&](int t) {
-            const int kb = (it.tile0 + t) * KT, first = kb >> p.s.page_log2;
-            if ((first >> 5) != blk) {
-                cur = (first >> 5) == blk + 1 ? ahead : ids(first >> 5);
-                blk = first >> 5;
-                ahead = ids(blk + 1);
-            }
-            if (n >= stages) ok = ok && __all_sync(0xffffffffu, att_wait(&empty[st], (round - 1) & 1, failed, limit));
-            if (!ok || w.stall) return;
-            const int boxes = (min(KT, it.limit - kb) + w.page_box - 1) / w.page_box;
-            if (lane == 0) mbar_arrive_expect_tx(&full[st], (uint32_t)(boxes * w.page_box * 128 * NH));
-            // a tile's pages (at most 16) lie in one block
-            const int key = kb + lane * w.page_box;
-            const int page = __shfl_sync(0xffffffffu, cur, (key >> p.s.page_log2) & 31);
-            unsigned char* dst = ring + st * A::UNIT + lane * w.page_box * 128;
-            if (lane < boxes)
-                for (int h = 0; h < NH; ++h)
-                    tma_4d(dst + h * KT * 128, map, h * 64, it.hk, key & ((1 << p.s.page_log2) - 1), page, &full[st]);
-            ++n;
-            if (++st == stages) st = 0, ++round;
-        };
-        for (; ok && it.more() && !w.stall; it.next(p, w.g)) {
-            const int nt = it.tiles();
-            blk = -2;
-            copy(0);
-            if (is_k)
-                for (int s = 0; s < (it.dual ? 2 : 1); ++s) {
+        for (uint32_t k = 0; ok && !w.stall; ++k) {
+            const AttSeg& sg = segment(k);
+            const int nt = sg.nt, b = sg.b, hk = sg.hk, tile0 = sg.tile0, last_key = sg.limit;
+            if (!ok || nt == 0) break;
+            // page ids come 32 at a time, one load per block of the table row and one
+            // block ahead: a lookup per tile would put its latency between the copies
+            const int32_t* table = p.table + (int64_t)b * p.s.width;
+            const int pages = (last_key + page_mask) >> p.s.page_log2;
+            auto ids = [&](int blk) {
+                const int i = blk * 32 + lane;
+                return i < pages ? __ldg(table + i) : -1;
+            };
+            int blk = (tile0 * KT >> p.s.page_log2) >> 5, cur = ids(blk), ahead = ids(blk + 1);
+            for (int t = 0; t < nt; ++t) {
+                const int kb = (tile0 + t) * KT, first = kb >> p.s.page_log2;
+                if ((first >> 5) != blk) {
+                    ++blk;
+                    cur = ahead;
+                    ahead = ids(blk + 1);
+                }
+                if (n >= stages) wait(&empty[st], round - 1);
+                if (!ok) break;
+                const int boxes = (min(KT, last_key - kb) + w.page_box - 1) / w.page_box;
+                if (lane == 0) mbar_arrive_expect_tx(&full[st], (uint32_t)(boxes * w.page_box * 128 * NH));
+                // a tile's pages (at most 16) lie in one block
+                const int key = kb + lane * w.page_box;
+                const int page = __shfl_sync(0xffffffffu, cur, (key >> p.s.page_log2) & 31);
+                unsigned char* dst = ring + st * A::UNIT + lane * w.page_box * 128;
+                if (lane < boxes)
+                    for (int h = 0; h < NH; ++h)
+                        tma_4d(dst + h * KT * 128, map, h * 64, hk, key & page_mask, page, &full[st]);
+                ++n;
+                if (++st == stages) st = 0, ++round;
+                if (t > 0 || !is_k) continue;
+                for (int s = 0; s <= sg.dual; ++s) {
                     const uint32_t qb = qi % NS;
-                    if (qi >= NS)
-                        ok = ok &&
-                             __all_sync(0xffffffffu, att_wait(&ms.q_empty[qb], (qi / NS - 1) & 1, failed, limit));
+                    if (qi >= NS) wait(&ms.q_empty[qb], qi / NS - 1);
                     if (!ok) break;
                     ++qi;
                     if (lane == 0) {
                         mbar_arrive_expect_tx(&ms.q_full[qb], (uint32_t)(w.q_box * w.g.G * 128 * NH));
                         for (int h = 0; h < NH; ++h)
-                            tma_4d(q_smem + qb * A::QB + h * ATT_ROWS * 128, &map_q, h * 64, it.hk * w.g.G,
-                                   it.t0 + s * w.g.tpt, it.b, &ms.q_full[qb]);
+                            tma_4d(q_smem + qb * A::QB + h * ATT_ROWS * 128, &map_q, h * 64, hk * w.g.G,
+                                   sg.t0 + s * w.g.tpt, b, &ms.q_full[qb]);
                     }
                 }
-            for (int t = 1; ok && t < nt; ++t) copy(t);
+            }
+            release(k);
         }
         // drain: every tile and row tile of Q has been read by the MMAs, so no
         // copy or commit is still on its way when the CTA leaves
         const uint32_t n0 = n > stages ? n - stages : 0, q0 = qi > NS ? qi - NS : 0;
-        for (uint32_t i = n0; ok && i < n; ++i) ok = att_wait(&empty[i % stages], (i / stages) & 1, failed, limit);
-        for (uint32_t i = q0; ok && i < qi; ++i) ok = att_wait(&ms.q_empty[i % NS], (i / NS) & 1, failed, limit);
+        for (uint32_t i = n0; ok && i < n; ++i) wait(&empty[i % stages], i / stages);
+        for (uint32_t i = q0; ok && i < qi; ++i) wait(&ms.q_empty[i % NS], i / NS);
         if (!ok) {
             // a role gave up: at least every copy issued has landed
             if (lane == 0) ms.failed = 1;
@@ -455,12 +602,13 @@ __global__ void __launch_bounds__(Att<DP>::THREADS, 1)
         // N-major, 64-column boxes KT rows apart, 8-row groups 1024 bytes apart
         const uint64_t q_desc = umma_desc(smem_u32(q_smem), 16, 1024), k_desc = umma_desc(smem_u32(k_smem), 16, 1024);
         const uint64_t v_desc = umma_desc(smem_u32(v_smem), KT * 128, 1024);
-        auto wait = [&](uint64_t* bar, uint32_t parity) {
-            ok = ok && __all_sync(0xffffffffu, att_wait(bar, parity & 1, failed, limit));
-        };
-        for (; ok && it.more(); it.next(p, w.g)) {
-            const bool dual = it.dual;
-            const int nt = it.tiles(), units = dual ? 2 * nt : nt, masked = it.first_masked();
+        for (uint32_t k = 0; ok; ++k) {
+            const AttSeg& sg = segment(k);
+            const int nt = sg.nt;
+            if (!ok || nt == 0) break;
+            const bool dual = sg.dual != 0;
+            const int units = dual ? 2 * nt : nt, masked = att_first_masked<KT>(sg);
+            release(k);
             auto scores = [&](int u) {
                 const int s = NS == 2 ? u & 1 : 0, t = dual ? u >> 1 : u;
                 const uint32_t i = base + t, st = i % KS;
@@ -472,9 +620,9 @@ __global__ void __launch_bounds__(Att<DP>::THREADS, 1)
                 if (elect_one()) {
                     const uint64_t a = q_desc + qb * (A::QB / 16), b = k_desc + st * (A::UNIT / 16);
 #pragma unroll
-                    for (int k = 0; k < DP / 16; ++k)
-                        umma_ss(tmem + A::s_col(s), a + ((k / 4) * ATT_ROWS * 128 + (k % 4) * 32) / 16,
-                                b + ((k / 4) * KT * 128 + (k % 4) * 32) / 16, ID_S, k > 0);
+                    for (int x = 0; x < DP / 16; ++x)
+                        umma_ss(tmem + A::s_col(s), a + ((x / 4) * ATT_ROWS * 128 + (x % 4) * 32) / 16,
+                                b + ((x / 4) * KT * 128 + (x % 4) * 32) / 16, ID_S, x > 0);
                     umma_commit(&ms.s_full[s]);
                     if (!dual || s == 1) umma_commit(&ms.k_empty[st]);
                     if (t == nt - 1) umma_commit(&ms.q_empty[qb]);
@@ -502,8 +650,8 @@ __global__ void __launch_bounds__(Att<DP>::THREADS, 1)
                 if (elect_one()) {
                     const uint64_t b = v_desc + st * (A::UNIT / 16);
 #pragma unroll
-                    for (int k = 0; k < KT / 16; ++k)
-                        umma_ts(tmem + A::o_col(s), tmem + A::s_col(s) + k * 8, b + k * 128, ID_O, !first || k > 0);
+                    for (int x = 0; x < KT / 16; ++x)
+                        umma_ts(tmem + A::o_col(s), tmem + A::s_col(s) + x * 8, b + x * 128, ID_O, !first || x > 0);
                     if (!dual || s == 1) umma_commit(&ms.v_empty[st]);
                     if (u + NS >= units) umma_commit(&ms.o_full[s]);
                 }
@@ -527,23 +675,11 @@ __global__ void __launch_bounds__(Att<DP>::THREADS, 1)
             }
             __syncwarp();
         }
-    } else if (warp == 3) {
-        // ---------------- this range's first item, where it began in an earlier
-        // range: the one before it, or the cut is not the first of the item
-        if (lane == 0) {
-            AttCut cut{-1, 0, 0, 0, 0, 0};
-            if (it.more() && it.tile0 > 0) {
-                const int first = split.owner(it.at + ATT_ITEM_COST);
-                if (first == (int)blockIdx.x - 1)
-                    cut = AttCut{first, split.owner(it.at + ATT_ITEM_COST + it.ntiles - 1), it.b, it.hk, it.t0,
-                                 it.ntok * w.g.G};
-            }
-            w.cuts[blockIdx.x] = cut;
-        }
     } else {
         // ---------------- softmax: warpgroup s, thread = row
         const int s = (warp - 4) >> 2, row = (warp & 3) * 32 + lane;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t o_addr = tmem + A::o_col(s) + lanes, s_addr = tmem + A::s_col(s) + lanes;
         const float c = p.scale * 1.4426950408889634f;
         const int T = p.s.T, Hq = p.s.Hq, D = p.s.D, G = w.g.G;
         // nodes that do not exist: zero rows
@@ -559,160 +695,85 @@ __global__ void __launch_bounds__(Att<DP>::THREADS, 1)
                     for (int i = lane; i < Hq; i += 32) p.lse[(int64_t)r * Hq + i] = -INFINITY;
             }
         }
-        uint32_t base = 0, n_unit = 0, n_seg[2] = {0, 0}, n_ml = 0, cleaned = 0;
-        for (; ok && it.more(); it.next(p, w.g)) {
-            const bool dual = it.dual;
-            const int nt = it.tiles(), units = dual ? 2 * nt : nt;
-            const int tbase = it.t0 + (dual ? s * w.g.tpt : 0);
-            const int rows = min(w.g.tpt, it.t0 + it.ntok - tbase) * G;
+        uint32_t base = 0, n_unit = 0, cleaned = 0;  // tiles, own units, phases of v_clean (bit per stage)
+        uint32_t n_seg0 = 0, n_seg1 = 0, n_ml = 0;   // segments of each stream, joins
+        for (uint32_t k = 0; ok; ++k) {
+            const AttSeg& sg = segment(k);
+            const int nt = sg.nt;
+            if (!ok || nt == 0) break;
+            const bool dual = sg.dual != 0;
+            const int t_first = sg.t0 + (dual ? s * w.g.tpt : 0);
+            const int rows = min(w.g.tpt, sg.t0 + sg.ntok - t_first) * G;
             const bool active = (warp & 3) * 32 < rows;
-            const int t = min(tbase + row / G, it.n - 1);  // rows past the last are computed, never stored
-            const bool mine = row < rows;
             float m = -INFINITY, l = 0.f;
-            uint32_t pend[KT / 32] = {};  // seen keys with non-finite values, of the tile at pend_kb
-            int pend_kb = -1;
-            int masked = it.first_masked();  // later: the first masked tile not counted in `cleaned`
-            const uint32_t o_addr = tmem + A::o_col(s) + lanes, s_addr = tmem + A::s_col(s) + lanes;
+            int masked = att_first_masked<KT>(sg);  // later: the first masked tile not counted in `cleaned`
 
-            // the rows of a masked value tile beyond the sequence become 0, and so does
-            // what is not finite (noted in nf); the warpgroups share the tile where
-            // both read it.  Eight lanes per 128-byte row of a box.
-            auto clean = [&](uint32_t st, int kb, bool shared) {
-                const int per = shared ? KT / 8 : KT / 4, r0 = ((shared ? s * 4 : 0) + (warp & 3)) * per;
-                uint32_t bits = 0;
-#pragma unroll 1
-                for (int i = 0; i < per; i += 4) {
-                    const int r = r0 + i + (lane >> 3), key = kb + r;
-                    bool found = false;
-                    if (key >= it.mask_from) {
+            for (int tile = dual ? 0 : s; tile < nt && ok; tile += dual ? 1 : NS) {
+                const bool part = tile >= masked;
+                const int kb = (sg.tile0 + tile) * KT;
+                uint32_t see[KT / 32];
+                if (part) {
+                    // on their way while the scores are computed
+                    const int t = min(t_first + row / G, sg.n - 1);  // rows past the last are never stored
 #pragma unroll
-                        for (int h = 0; h < NH; ++h) {
-                            uint4* a = (uint4*)(v_smem + st * A::UNIT + (h * KT + r) * 128) + (lane & 7);
-                            if (key >= it.ctx + it.n) {
-                                *a = make_uint4(0, 0, 0, 0);
-                                continue;
-                            }
-                            uint4 x = *a;
-                            const bool bad = clean_word<F16>(x.x) | clean_word<F16>(x.y) | clean_word<F16>(x.z) |
-                                             clean_word<F16>(x.w);
-                            if (bad) *a = x;
-                            found = found || bad;
-                        }
-                    }
-                    const uint32_t v = __ballot_sync(0xffffffffu, found);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        if ((v >> (8 * j)) & 0xFFu) bits |= 1u << (i + j);
+                    for (int y = 0; y < KT / 32; ++y) see[y] = att_sees(p, sg.b, t, sg.ctx, sg.n, kb + 32 * y);
                 }
-                fence_async_smem();
-                if (lane < per / 16) ((uint16_t*)ms.nf[st])[r0 / 16 + lane] = (uint16_t)(bits >> (16 * lane));
-                __syncwarp();
-                if (lane == 0) mbar_arrive_n(&ms.v_clean[st], NS == 2 && !shared ? 2 : 1);
-            };
-            // O += the non-finite values of pend's keys (the MMA saw zeros there)
-            auto add_nonfinite = [&]() {
-                for (int x = 0; x < KT / 32; ++x) {
-                    uint32_t any = __reduce_or_sync(0xffffffffu, pend[x]);
-                    for (; any; any &= any - 1) {
-                        const int bit = __ffs(any) - 1, key = pend_kb + 32 * x + bit;
-                        const int page = __ldg(p.table + (int64_t)it.b * p.s.width + (key >> p.s.page_log2));
-                        if (page < 0 || page >= p.s.num_pages) continue;
-                        const uint16_t* v = (const uint16_t*)p.c.v + page * p.c.page +
-                                            (key & ((1 << p.s.page_log2) - 1)) * p.c.token + it.hk * p.c.head;
-                        for (int d = 0; d < D; d += 16) {
-                            uint32_t o[16];
-                            tmem_ld<16>(o_addr + d, o);
-#pragma unroll
-                            for (int k = 0; k < 16; ++k) {
-                                const uint16_t e = __ldg(v + d + k);
-                                if (att_nonfinite<F16>(e) && ((pend[x] >> bit) & 1u))
-                                    o[k] = __float_as_uint(__uint_as_float(o[k]) + H::one(e));
-                            }
-                            tmem_st<16>(o_addr + d, o);
-                        }
-                        tmem_wait_st();
-                    }
-                    pend[x] = 0;
-                }
-                pend_kb = -1;
-            };
-
-            for (int u = s; u < units && ok; u += NS) {
-                const int tile = dual ? u >> 1 : u, kb = (it.tile0 + tile) * KT;
-                ok = __all_sync(0xffffffffu, att_wait(&ms.s_full[s], n_unit & 1, failed, limit));
-                if (!ok) break;
+                wait(&ms.s_full[s], n_unit);
                 ++n_unit;
+                if (!ok) break;
                 tmem_fence_after();
-                const uint32_t vi = base + tile, vst = vi % VS;
-                const bool part = kb + KT > it.mask_from;
                 if (part) {
                     // phases of v_clean of the tiles before this one (the other stream's)
                     for (; masked < tile; ++masked) cleaned ^= 1u << ((base + masked) % VS);
                     ++masked;
-                    ok = __all_sync(0xffffffffu, att_wait(&ms.v_full[vst], (vi / VS) & 1, failed, limit));
+                    const uint32_t vi = base + tile, vst = vi % VS;
+                    wait(&ms.v_full[vst], vi / VS);
                     if (!ok) break;
-                    clean(vst, kb, dual);
-                    ok = __all_sync(0xffffffffu, att_wait(&ms.v_clean[vst], (cleaned >> vst) & 1, failed, limit));
+                    att_clean<F16, DP>(ms, v_smem, vst, kb, sg.mask_from, sg.ctx + sg.n, dual, s, warp & 3, lane);
+                    wait(&ms.v_clean[vst], cleaned >> vst);
                     if (!ok) break;
                     cleaned ^= 1u << vst;
                 }
                 if (active) {
-                    // every earlier P V of the stream is complete: the scores were issued after it
-                    if (pend_kb >= 0) add_nonfinite();
+                    // hidden scores become -inf in tensor memory; then the row's maximum,
+                    // found by the loads, and its exponentials.  Loops and two passes over
+                    // tensor memory keep the code and the registers few: the first pass of
+                    // a CTA through every path waits for its instructions.
                     if (part) {
-                        // hidden scores become -inf in tensor memory, before the passes over them
-                        uint32_t some = 0;
 #pragma unroll 1
                         for (int y = 0; y < KT / 32; ++y) {
-                            const uint32_t see = att_sees(p, it.b, t, it.ctx, it.n, kb + 32 * y);
-                            if (__all_sync(0xffffffffu, see == ~0u)) continue;
-                            some |= see & *(volatile uint32_t*)&ms.nf[vst][y];
+                            const uint32_t sees = y == 0 ? see[0] : y == 1 ? see[1] : y == 2 ? see[KT / 32 - 2]
+                                                                                          : see[KT / 32 - 1];
                             uint32_t x[32];
                             tmem_ld<32>(s_addr + 32 * y, x);
 #pragma unroll
-                            for (int k = 0; k < 32; ++k)
-                                if (!((see >> k) & 1u)) x[k] = 0xFF800000u;
+                            for (int i = 0; i < 32; ++i)
+                                if (!((sees >> i) & 1u)) x[i] = 0xFF800000u;
                             tmem_st<32>(s_addr + 32 * y, x);
                         }
                         tmem_wait_st();
-                        pend_kb = -1;
-                        if (__any_sync(0xffffffffu, some)) {
-                            pend_kb = kb;
-#pragma unroll
-                            for (int y = 0; y < KT / 32; ++y)
-                                pend[y] = att_sees(p, it.b, t, it.ctx, it.n, kb + 32 * y) &
-                                          *(volatile uint32_t*)&ms.nf[vst][y];
-                        }
                     }
-                    // the row's maximum, then its exponentials: two passes over the
-                    // scores in tensor memory take fewer registers than one that
-                    // holds all of them, and no spills
-                    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
+                    float top = -INFINITY;
+#pragma unroll 1
                     for (int y = 0; y < KT; y += 64) {
                         uint32_t x[64];
-                        tmem_ld<64>(s_addr + y, x);
-#pragma unroll
-                        for (int k = 0; k < 64; k += 8)
-#pragma unroll
-                            for (int j = 0; j < 4; ++j)
-                                mx[j] = fmaxf(mx[j], fmaxf(__uint_as_float(x[k + 2 * j]),
-                                                           __uint_as_float(x[k + 2 * j + 1])));
+                        top = fmaxf(top, tmem_ld_max<64>(s_addr + y, x));
                     }
-                    const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
                     // O and l stay in units of the old maximum while the new one is
-                    // less than 2^8 above it: p then stays below 2^8
+                    // less than 2^8 above it: p then stays below 2^8.  Every earlier
+                    // P V of the stream is complete: the scores were issued after it.
                     const bool grow = top * c > m * c + ATT_LAZY || (m == -INFINITY && top > m);
                     if (__any_sync(0xffffffffu, grow)) {
                         const float f = grow ? ex2_fast((m - top) * c) : 1.f;
                         if (grow) m = top;
                         l *= f;
-                        if (u >= NS) {
+                        if (tile >= (dual ? 1 : NS)) {
+#pragma unroll 1
                             for (int d = 0; d < D; d += 16) {
                                 uint32_t o[16];
                                 tmem_ld<16>(o_addr + d, o);
 #pragma unroll
-                                for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+                                for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
                                 tmem_st<16>(o_addr + d, o);
                             }
                         }
@@ -720,17 +781,17 @@ __global__ void __launch_bounds__(Att<DP>::THREADS, 1)
                     const float mc = m == -INFINITY ? 0.f : m * c;
                     const uint64_t c2 = pack2(c, c), mc2 = pack2(-mc, -mc);
                     uint64_t sum[2] = {0ull, 0ull};  // two pairs of partial sums
-#pragma unroll
+#pragma unroll 1
                     for (int y = 0; y < KT; y += 64) {
                         uint32_t x[64];
                         tmem_ld<64>(s_addr + y, x);
 #pragma unroll
-                        for (int k = 0; k < 32; ++k) {
-                            float2 e = unpack2(fma2(pack2u(x[2 * k], x[2 * k + 1]), c2, mc2));
+                        for (int i = 0; i < 32; ++i) {
+                            float2 e = unpack2(fma2(pack2u(x[2 * i], x[2 * i + 1]), c2, mc2));
                             e.x = ex2_fast(e.x);
                             e.y = ex2_fast(e.y);
-                            sum[k & 1] = add2(sum[k & 1], pack2(e.x, e.y));
-                            x[k] = H::pack(e.x, e.y);
+                            sum[i & 1] = add2(sum[i & 1], pack2(e.x, e.y));
+                            x[i] = H::pack(e.x, e.y);
                         }
                         tmem_st<32>(s_addr + y / 2, *reinterpret_cast<uint32_t(*)[32]>(&x));
                     }
@@ -738,36 +799,48 @@ __global__ void __launch_bounds__(Att<DP>::THREADS, 1)
                     l += sums.x + sums.y;
                     tmem_wait_st();
                 }
+                uint32_t some = 0;  // seen keys with non-finite values
+                if (part) {
+#pragma unroll
+                    for (int y = 0; y < KT / 32; ++y)
+                        some |= see[y] &= *(volatile uint32_t*)&ms.nf[(base + tile) % VS][y];
+                }
                 tmem_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&ms.p_ready[s]);
+                if (part && __any_sync(0xffffffffu, active && some)) {
+                    // rare: once P V is done (it saw zeros there), O += those values
+                    const uint32_t vi = base + tile;
+                    wait(&ms.v_empty[vi % VS], vi / VS);
+                    if (!ok) break;
+                    tmem_fence_after();
+                    att_add_nonfinite<F16, KT>(p, make_uint4(see[0], see[1], see[KT / 32 - 2], see[KT / 32 - 1]), sg.b,
+                                               sg.hk, kb, o_addr);
+                }
             }
             for (; masked < nt; ++masked) cleaned ^= 1u << ((base + masked) % VS);
             base += nt;
             if (!ok) break;
 
             // ---- the segment's end: O of the streams with units
-            const int units1 = dual ? nt : units / 2;  // of stream 1 (NS == 2)
-            const bool join = NS == 2 && !dual && units1 > 0;  // one row tile in two streams
-            const bool has = s == 0 || units1 > 0;
-            if (has)
-                ok = __all_sync(0xffffffffu, att_wait(&ms.o_full[s], n_seg[s] & 1, failed, limit));
+            const bool two = dual || nt > 1;           // stream 1 has some
+            const bool join = NS == 2 && !dual && two;  // one row tile in two streams
+            if (s == 0 || two) wait(&ms.o_full[s], s == 0 ? n_seg0 : n_seg1);
             if (!ok) break;
             tmem_fence_after();
-            if (has && active && pend_kb >= 0) add_nonfinite();
+            float m1 = -INFINITY, l1 = 0.f;
             if (join && s == 1) {
                 // stream 1 hands its maximum and sum over; its O stays until stream 0 has read it
-                if (n_ml > 0) ok = __all_sync(0xffffffffu, att_wait(&ms.ml_empty, (n_ml - 1) & 1, failed, limit));
+                if (n_ml > 0) wait(&ms.ml_empty, n_ml - 1);
                 if (!ok) break;
                 ms.ml[row] = make_float2(m, l);
                 tmem_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&ms.ml_full);
             }
-            float m1 = -INFINITY, l1 = 0.f;
             if (join && s == 0) {
-                ok = __all_sync(0xffffffffu, att_wait(&ms.o_full[1], n_seg[1] & 1, failed, limit) &&
-                                                 att_wait(&ms.ml_full, n_ml & 1, failed, limit));
+                wait(&ms.o_full[1], n_seg1);
+                wait(&ms.ml_full, n_ml);
                 if (!ok) break;
                 tmem_fence_after();
                 const float2 o = ms.ml[row];
@@ -776,65 +849,64 @@ __global__ void __launch_bounds__(Att<DP>::THREADS, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&ms.ml_empty);
             }
-            if (join) ++n_ml;
-            ++n_seg[0];
-            if (units1 > 0) ++n_seg[1];
-            if (active && (s == 0 || dual)) {
-                const float mm = fmaxf(m, m1), mr = mm == -INFINITY ? 0.f : mm;
-                float f0 = ex2_fast((m - mr) * c), f1 = ex2_fast((m1 - mr) * c);
-                if (m == -INFINITY) f0 = 0.f;
-                if (m1 == -INFINITY) f1 = 0.f;
-                // a NaN sum stays NaN; an infinite maximum (0 x inf above) too
-                float ll = l * f0 + (join ? l1 * f1 : 0.f);
-                const bool none = ll == 0.f, whole = it.whole();
-                if (whole) {
-                    const float inv = none ? 0.f : 1.f / ll;
-                    f0 *= inv;
-                    f1 *= inv;
-                }
-                const int head = it.hk * G + row % G;
-                const int64_t orow = ((int64_t)it.b * T + t) * Hq + head;
-                const int64_t slot = (int64_t)blockIdx.x * 2 + (it.tile0 > 0 ? 0 : 1);
-                const int prow = (dual ? s * ATT_ROWS : 0) + row;
-#pragma unroll 1
-                for (int d = 0; d < D; d += 32) {
-                    uint32_t o[32];
-                    float y[32];
-                    if (join) {
-                        uint32_t o1[32];
-                        tmem_ld_2x32(o_addr + d, tmem + A::o_col(NS - 1) + lanes + d, o, o1);
-#pragma unroll
-                        for (int k = 0; k < 32; ++k)
-                            y[k] = __uint_as_float(o[k]) * f0 + __uint_as_float(o1[k]) * f1;
-                    } else {
-                        tmem_ld<32>(o_addr + d, o);
-#pragma unroll
-                        for (int k = 0; k < 32; ++k) y[k] = __uint_as_float(o[k]) * f0;
-                    }
-                    if (!mine) continue;
-                    if (whole) {
-                        uint4* o16 = (uint4*)((char*)p.out + (orow * D + d) * 2);
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            if (d + 8 * k < D)
-                                o16[k] = none ? make_uint4(0, 0, 0, 0)
-                                              : make_uint4(H::pack(y[8 * k], y[8 * k + 1]),
-                                                           H::pack(y[8 * k + 2], y[8 * k + 3]),
-                                                           H::pack(y[8 * k + 4], y[8 * k + 5]),
-                                                           H::pack(y[8 * k + 6], y[8 * k + 7]));
-                    } else {
-                        float4* o32 = (float4*)w.part_o + (slot * (DP / 4) + d / 4) * (NS * ATT_ROWS) + prow;
-#pragma unroll
-                        for (int k = 0; k < 8; ++k)
-                            if (d + 4 * k < D)
-                                o32[k * NS * ATT_ROWS] =
-                                    make_float4(y[4 * k], y[4 * k + 1], y[4 * k + 2], y[4 * k + 3]);
-                    }
-                }
-                if (mine && whole && p.lse) p.lse[orow] = none ? -INFINITY : fmaf(mr, p.scale, logf(ll));
-                if (mine && !whole) w.part_ml[slot * NS * ATT_ROWS + prow] = make_float2(mm, ll);
-            }
+            n_ml += join;
+            n_seg0 += 1;
+            n_seg1 += two;
             if (s == 0 || dual) {
+                if (active) {
+                    const float mm = fmaxf(m, m1), mr = mm == -INFINITY ? 0.f : mm;
+                    float f0 = m == -INFINITY ? 0.f : ex2_fast((m - mr) * c);
+                    float f1 = m1 == -INFINITY ? 0.f : ex2_fast((m1 - mr) * c);
+                    // a NaN sum stays NaN, and so does that of an infinite maximum
+                    const float ll = l * f0 + (join ? l1 * f1 : 0.f);
+                    const bool none = ll == 0.f, whole = sg.whole != 0, mine = row < rows;
+                    if (whole) {
+                        const float inv = none ? 0.f : 1.f / ll;
+                        f0 *= inv;
+                        f1 *= inv;
+                    }
+                    const int node = row / G;
+                    const int64_t orow = ((int64_t)sg.b * T + t_first + node) * Hq + sg.hk * G + row - node * G;
+                    const int64_t slot = (int64_t)blockIdx.x * 2 + (sg.tile0 > 0 ? 0 : 1);
+                    const int prow = (dual ? s * ATT_ROWS : 0) + row;
+#pragma unroll 1
+                    for (int d = 0; d < D; d += 32) {
+                        uint32_t o[32];
+                        if (join) {
+                            uint32_t o1[32];
+                            tmem_ld_2x32(o_addr + d, tmem + A::o_col(NS - 1) + lanes + d, o, o1);
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                o[i] = __float_as_uint(__uint_as_float(o[i]) * f0 + __uint_as_float(o1[i]) * f1);
+                        } else {
+                            tmem_ld<32>(o_addr + d, o);
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f0);
+                        }
+                        auto y = [&](int i) { return __uint_as_float(o[i]); };
+                        if (!mine) continue;
+                        if (whole) {
+                            uint4* o16 = (uint4*)((char*)p.out + (orow * D + d) * 2);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                if (d + 8 * i < D)
+                                    o16[i] = none ? make_uint4(0, 0, 0, 0)
+                                                  : make_uint4(H::pack(y(8 * i), y(8 * i + 1)),
+                                                               H::pack(y(8 * i + 2), y(8 * i + 3)),
+                                                               H::pack(y(8 * i + 4), y(8 * i + 5)),
+                                                               H::pack(y(8 * i + 6), y(8 * i + 7)));
+                        } else {
+                            float4* o32 = (float4*)w.part_o + (slot * (DP / 4) + d / 4) * (NS * ATT_ROWS) + prow;
+#pragma unroll
+                            for (int i = 0; i < 8; ++i)
+                                if (d + 4 * i < D)
+                                    o32[i * NS * ATT_ROWS] =
+                                        make_float4(y(4 * i), y(4 * i + 1), y(4 * i + 2), y(4 * i + 3));
+                        }
+                    }
+                    if (mine && whole && p.lse) p.lse[orow] = none ? -INFINITY : fmaf(mr, p.scale, logf(ll));
+                    if (mine && !whole) w.part_ml[slot * NS * ATT_ROWS + prow] = make_float2(mm, ll);
+                }
                 tmem_fence_before();
                 __syncwarp();
                 if (lane == 0) {
@@ -842,6 +914,7 @@ __global__ void __launch_bounds__(Att<DP>::THREADS, 1)
                     if (join) mbar_arrive(&ms.o_empty[1]);
                 }
             }
+            release(k);
         }
         if (!ok && lane == 0) ms.failed = 1;
     }
@@ -856,89 +929,180 @@ __global__ void __launch_bounds__(Att<DP>::THREADS, 1)
 // k_tree_combine                                                            //
 // ------------------------------------------------------------------------- //
 // Joins the parts of an item cut between CTAs: out = sum_i 2^(m_i - m) O_i /
-// sum_i 2^(m_i - m) l_i.  Grid (cut, 32 rows, 32 columns); a thread has one row,
-// four columns and one in eight of the parts, or all parts of few.
-constexpr int COMB_THREADS = 256;
+// sum_i 2^(m_i - m) l_i (m here in log2 units).  Lane = row, and a task is 32
+// rows by 32 columns of a cut: for a warp where the parts are few, all loads of
+// a thread independent; for a CTA where they are many (few items, long
+// caches), 8 columns, every eighth part a warp's and the warps' sums joined in
+// shared memory.  The CTAs find their tasks in the list of cuts, since only
+// the GPU knows which ranges cut items.
+constexpr int COMB_THREADS = 256, COMB_CUTS = 512, COMB_CTAS_PER_SM = 4;
+constexpr int COMB_FEW = 8;
+
+// tasks of the cuts up to each, of one kind: cols columns a task
+__device__ __forceinline__ int comb_scan(const AttWork& w, int n_cuts, bool many, int cols, int* ends, int* scan)
+{
+    const int tid = threadIdx.x, lane = tid & 31, g = tid >> 5;
+    int before = 0;
+    for (int i0 = 0; i0 < n_cuts; i0 += COMB_THREADS) {
+        const int i = i0 + tid;
+        int t = 0;
+        if (i < n_cuts) {
+            const AttCut cut = w.cuts[i];
+            if (cut.first >= 0 && (cut.last - cut.first + 1 > COMB_FEW) == many)
+                t = ((cut.rows + 31) / 32) * ((w.p.s.D + cols - 1) / cols);
+        }
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, t, o);
+            if (lane >= o) t += v;
+        }
+        if (lane == 31) scan[g] = t;
+        __syncthreads();
+        int add = before;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const int v = scan[k];
+            if (k < g) add += v;
+            before += v;
+        }
+        if (i < n_cuts) ends[i] = t + add;
+        __syncthreads();
+    }
+    return before;
+}
 
 template <bool F16>
-__global__ void __launch_bounds__(COMB_THREADS) k_tree_combine(const AttWork w, int DP, int prows)
+__global__ void __launch_bounds__(COMB_THREADS, COMB_CTAS_PER_SM)
+    k_tree_combine(const AttWork w, int n_cuts, int DP, int prows)
 {
     using H = Half2<F16>;
-    __shared__ float4 part[8][32];
-    __shared__ float2 part_ml[8][32];
+    __shared__ float4 acc_s[8][2][32];
+    __shared__ float2 ml_s[8][32];
+    __shared__ int ends[COMB_CUTS];
+    __shared__ int scan[8];
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const AttCut cut = w.cuts[blockIdx.x + 1];
-    const int r = blockIdx.y * 32 + (threadIdx.x & 31), g8 = threadIdx.x >> 5;
-    if (cut.first < 0 || (int)blockIdx.y * 32 >= cut.rows) return;
     const TreeAttendParams& p = w.p;
+    const int lane = threadIdx.x & 31, g = threadIdx.x >> 5;
+    const int D = p.s.D, G = w.g.G, first_rows = w.g.tpt * G;
     const float c = p.scale * 1.4426950408889634f;
-    const int G = w.g.G, D = p.s.D;
+    auto weight = [&](float m, float ref) { return m == -INFINITY ? 0.f : ex2_fast((m - ref) * c); };
+    auto slot = [](const AttCut& cut, int i) { return (int64_t)(cut.first + i) * 2 + (i == 0 ? 1 : 0); };
+    // the cut of a task (the first whose tasks end past it), and the task's number in it
+    auto find = [&](int& task) {
+        int lo = 0, hi = n_cuts - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi) / 2;
+            if (ends[mid] > task) hi = mid;
+            else lo = mid + 1;
+        }
+        if (lo) task -= ends[lo - 1];
+        return w.cuts[lo];
+    };
     // rows of the second row tile lie behind the first's 128
-    const int first_rows = w.g.tpt * G, pr = r < first_rows ? r : ATT_ROWS + r - first_rows;
-    const bool on = r < cut.rows;
-    const int64_t orow = ((int64_t)cut.b * p.s.T + cut.t0 + r / G) * p.s.Hq + cut.hk * G + r % G;
-    const int n = cut.last - cut.first + 1;
-    auto slot = [&](int i) { return (int64_t)(cut.first + i) * 2 + (i == 0 ? 1 : 0); };
-    auto ml = [&](int i) { return on ? w.part_ml[slot(i) * prows + pr] : make_float2(-INFINITY, 0.f); };
-    auto weight = [&](float m, float top) { return m == -INFINITY ? 0.f : ex2_fast((m - top) * c); };
-    const int step = n > 8 ? 8 : 1, i0 = n > 8 ? g8 : 0;
-    float top = -INFINITY;
-    for (int i = i0; i < n; i += step) top = fmaxf(top, ml(i).x);
-    if (step == 8) {
-        part_ml[g8][threadIdx.x & 31].x = top;
-        __syncthreads();
-        for (int k = 0; k < 8; ++k) top = fmaxf(top, part_ml[k][threadIdx.x & 31].x);
-        __syncthreads();
-    }
-    const float ref = top == -INFINITY ? 0.f : top;
-    float l = 0.f;
-    for (int i = i0; i < n; i += step) {
-        const float2 v = ml(i);
-        l += v.y * weight(v.x, ref);
-    }
-    if (step == 8) {
-        part_ml[g8][threadIdx.x & 31].y = l;
-        __syncthreads();
-        l = 0.f;
-        for (int k = 0; k < 8; ++k) l += part_ml[k][threadIdx.x & 31].y;
-    }
-    const bool none = l == 0.f;
-    const float inv = none ? 0.f : 1.f / l;
-    auto store = [&](int col4, float4 y) {
-        if (!on || col4 * 4 >= D) return;
-        uint2 h = make_uint2(H::pack(y.x * inv, y.y * inv), H::pack(y.z * inv, y.w * inv));
-        if (none) h = make_uint2(0, 0);
-        *(uint2*)((char*)p.out + (orow * D + col4 * 4) * 2) = h;
+    auto part_row = [&](int r) { return r < first_rows ? r : ATT_ROWS + r - first_rows; };
+    auto out_row = [&](const AttCut& cut, int r) {
+        const int node = r / G;
+        return ((int64_t)cut.b * p.s.T + cut.t0 + node) * p.s.Hq + cut.hk * G + r - node * G;
     };
-    auto sum = [&](int col4, int from, int by) {
-        float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (on && col4 * 4 < D)
-#pragma unroll 4
-            for (int i = from; i < n; i += by) {
-                const float f = weight(ml(i).x, ref);
-                const float4 v = ((const float4*)w.part_o)[(slot(i) * (DP / 4) + col4) * prows + pr];
-                y.x += f * v.x, y.y += f * v.y, y.z += f * v.z, y.w += f * v.w;
-            }
-        return y;
-    };
-    if (step == 1) {
-        store(blockIdx.z * 8 + g8, sum(blockIdx.z * 8 + g8, 0, 1));
-    } else {
-        for (int k = 0; k < 8; ++k) {
-            __syncthreads();
-            part[g8][threadIdx.x & 31] = sum(blockIdx.z * 8 + k, g8, 8);
-            __syncthreads();
-            if (g8 == 0) {
-                float4 y = part[0][threadIdx.x];
-                for (int x = 1; x < 8; ++x) {
-                    const float4 v = part[x][threadIdx.x];
-                    y.x += v.x, y.y += v.y, y.z += v.z, y.w += v.w;
+
+    // ---- few parts: a warp per task
+    const int few = comb_scan(w, n_cuts, false, 32, ends, scan), c32 = (D + 31) / 32;
+    for (int task0 = blockIdx.x * 8 + g; task0 < few; task0 += gridDim.x * 8) {
+        int task = task0;
+        const AttCut cut = find(task);
+        const int n = cut.last - cut.first + 1, rb = task / c32, col4 = (task - rb * c32) * 8;
+        const int r = rb * 32 + lane, pr = part_row(r);
+        if (r >= cut.rows) continue;
+        float top = -INFINITY, l = 0.f;
+        for (int i = 0; i < n; ++i) top = fmaxf(top, w.part_ml[slot(cut, i) * prows + pr].x);
+        const float ref = top == -INFINITY ? 0.f : top;
+        float4 acc[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int i = 0; i < n; ++i) {
+            const float2 v = w.part_ml[slot(cut, i) * prows + pr];
+            const float f = weight(v.x, ref);
+            l += v.y * f;
+            const float4* src = (const float4*)w.part_o + (slot(cut, i) * (DP / 4) + col4) * prows + pr;
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                if ((col4 + k) * 4 < D) {
+                    const float4 o = src[k * prows];
+                    acc[k].x += f * o.x, acc[k].y += f * o.y, acc[k].z += f * o.z, acc[k].w += f * o.w;
                 }
-                store(blockIdx.z * 8 + k, y);
+        }
+        const bool none = l == 0.f;
+        const float inv = none ? 0.f : 1.f / l;
+        const int64_t orow = out_row(cut, r);
+        uint4* o16 = (uint4*)((char*)p.out + (orow * D + col4 * 4) * 2);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const float4 a = acc[2 * k], b = acc[2 * k + 1];
+            if ((col4 + 2 * k) * 4 < D)
+                o16[k] = none ? make_uint4(0, 0, 0, 0)
+                              : make_uint4(H::pack(a.x * inv, a.y * inv), H::pack(a.z * inv, a.w * inv),
+                                           H::pack(b.x * inv, b.y * inv), H::pack(b.z * inv, b.w * inv));
+        }
+        if (p.lse && col4 == 0) p.lse[orow] = none ? -INFINITY : fmaf(ref, p.scale, logf(l));
+    }
+    __syncthreads();
+
+    // ---- many parts: a CTA per task
+    const int many = comb_scan(w, n_cuts, true, 8, ends, scan), c8 = D / 8;
+    for (int task0 = blockIdx.x; task0 < many; task0 += gridDim.x) {
+        int task = task0;
+        const AttCut cut = find(task);
+        const int n = cut.last - cut.first + 1, rb = task / c8, col4 = (task - rb * c8) * 2;
+        const int r = min(rb * 32 + lane, cut.rows - 1), pr = part_row(r);
+        float top = -INFINITY, l = 0.f;
+#pragma unroll 4
+        for (int i = g; i < n; i += 8) top = fmaxf(top, w.part_ml[slot(cut, i) * prows + pr].x);
+        const float own = top == -INFINITY ? 0.f : top;
+        float4 acc[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+#pragma unroll 4
+        for (int i = g; i < n; i += 8) {
+            const float2 v = w.part_ml[slot(cut, i) * prows + pr];
+            const float f = weight(v.x, own);
+            l += v.y * f;
+            const float4* src = (const float4*)w.part_o + (slot(cut, i) * (DP / 4) + col4) * prows + pr;
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const float4 o = src[k * prows];
+                acc[k].x += f * o.x, acc[k].y += f * o.y, acc[k].z += f * o.z, acc[k].w += f * o.w;
             }
         }
+        ml_s[g][lane] = make_float2(top, l);
+        acc_s[g][0][lane] = acc[0];
+        acc_s[g][1][lane] = acc[1];
+        __syncthreads();
+        if (g < 2) {  // warp g joins its four columns
+            top = -INFINITY;
+            l = 0.f;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) top = fmaxf(top, ml_s[k][lane].x);
+            const float ref = top == -INFINITY ? 0.f : top;
+            float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const float2 v = ml_s[k][lane];
+                const float f = weight(v.x, ref);
+                const float4 o = acc_s[k][g][lane];
+                l += v.y * f;
+                y.x += f * o.x, y.y += f * o.y, y.z += f * o.z, y.w += f * o.w;
+            }
+            const bool none = l == 0.f;
+            const float inv = none ? 0.f : 1.f / l;
+            if (rb * 32 + lane < cut.rows) {
+                const int64_t orow = out_row(cut, r);
+                *(uint2*)((char*)p.out + (orow * D + (col4 + g) * 4) * 2) =
+                    none ? make_uint2(0, 0)
+                         : make_uint2(H::pack(y.x * inv, y.y * inv), H::pack(y.z * inv, y.w * inv));
+                if (p.lse && col4 == 0 && g == 0)
+                    p.lse[orow] = none ? -INFINITY : fmaf(ref, p.scale, logf(l));
+            }
+        }
+        __syncthreads();  // the tables are reused
     }
-    if (p.lse && on && g8 == 0 && blockIdx.z == 0) p.lse[orow] = none ? -INFINITY : fmaf(ref, p.scale, logf(l));
 }
 
 // ------------------------------------------------------------------------- //
@@ -995,19 +1159,21 @@ static cudaError_t att_launch(AttWork w, int num_sms, cudaStream_t s)
         !att_map(&mk, F16, w.p.c.k, sh.D, cd, cs, 1, w.page_box) ||
         !att_map(&mv, F16, w.p.c.v, sh.D, cd, cs, 1, w.page_box))
         return cudaErrorInvalidValue;
+    num_sms = std::min(num_sms, COMB_CUTS);
     k_tree_attend<F16, DP><<<num_sms, A::THREADS, A::SMEM, s>>>(mq, mk, mv, w);
     if ((e = cudaGetLastError()) != cudaSuccess || num_sms == 1) return e;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
-    const int rows = min(w.g.group, sh.T) * w.g.G;
-    cfg.gridDim = dim3((unsigned)num_sms - 1, (unsigned)((rows + 31) / 32), (unsigned)((sh.D + 31) / 32));
+    // no more CTAs than there may be tasks
+    const int64_t tasks = (int64_t)num_sms * ((min(w.g.group, sh.T) * w.g.G + 31) / 32) * ((sh.D + 7) / 8);
+    cfg.gridDim = dim3((unsigned)std::min<int64_t>(tasks, (int64_t)num_sms * COMB_CTAS_PER_SM));
     cfg.blockDim = dim3(COMB_THREADS);
     cfg.stream = s;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, k_tree_combine<F16>, w, DP, A::NS * ATT_ROWS);
+    return cudaLaunchKernelEx(&cfg, k_tree_combine<F16>, w, num_sms, DP, A::NS * ATT_ROWS);
 }
 
 bool tree_attend_fits(const TreeShape& sh)
