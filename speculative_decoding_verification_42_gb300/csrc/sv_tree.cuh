@@ -110,8 +110,9 @@ struct TreeKeepParams {
 
 cudaError_t launch_tree_plan(TreePlanParams p, int num_sms, cudaStream_t s);
 cudaError_t launch_tree_append(const TreeAppendParams& p, int dtype, cudaStream_t s);
-// bytes of workspace for `ctas` CTAs, and where in it the (m, l) and the cuts begin
-size_t tree_attend_bytes(int D, int ctas, size_t* ml_at, size_t* cut_at);
+// bytes of workspace (zeroed before the first call) for `ctas` CTAs, and where
+// in it the (m, l) and the joins begin
+size_t tree_attend_bytes(int D, int ctas, size_t* ml_at, size_t* join_at);
 // key tiles of a call are counted in 32 bits
 bool tree_attend_fits(const TreeShape& s);
 // err: bit 0 set when a bounded wait ran out; stall: issue no copy

@@ -223,18 +223,30 @@ struct AttIter {
     }
 };
 
-// an item's tiles cut by the start of CTA c's range; c is the first such cut
-struct __align__(16) AttCut {
-    int32_t first, last;  // CTAs with parts of it; first < 0: nothing to join here
+// A task of k_tree_combine: some rows and columns (number `sub` of its item's
+// tasks) of an item whose tiles the CTAs first .. last share.
+struct __align__(16) AttJoin {
+    int32_t first, last;
     int32_t b, hk, t0, rows;
+    int32_t sub;
+    int32_t pad;
 };
+// few parts: a task is 8 warps times 32 rows by 32 columns; many: 32 rows by 8
+constexpr int ATT_FEW = 8;
+__host__ __device__ __forceinline__ int att_join_tasks(int parts, int rows, int D)
+{
+    const int rb = (rows + 31) / 32;
+    return parts <= ATT_FEW ? (rb * ((D + 31) / 32) + 7) / 8 : rb * (D / 8);
+}
 
 struct AttWork {
     TreeAttendParams p;
     AttGeom g;
     float* part_o;      // [2 * CTAs][DP / 4][NS * 128] float4: O of a part, per 4 columns all rows
     float2* part_ml;    // [2 * CTAs][NS * 128]: (m, l) of a part's rows
-    AttCut* cuts;       // [CTAs]
+    AttJoin* joins;     // the tasks of k_tree_combine
+    unsigned* n_joins;  // their number; back at 0 after it
+    unsigned* n_done;   // its CTAs that are done
     unsigned* err;
     int32_t page_box;   // tokens of one copied box: min(page, KT)
     int32_t q_box;      // nodes of one copied box of Q
@@ -485,15 +497,6 @@ __global__ void __launch_bounds__(Att<DP>::THREADS, 1)
         AttIter<KT> it;
         it.start(p, w.g, busy ? split.start(blockIdx.x) : 0, busy ? split.start(blockIdx.x + 1) : 0, head0,
                  ms.first_b, ms.first);
-        // an item that began in an earlier range: the one before it, or this cut
-        // is not the first of the item
-        AttCut cut{-1, 0, 0, 0, 0, 0};
-        if (it.more() && it.tile0 > 0) {
-            const int first = split.owner(it.at + ATT_ITEM_COST);
-            if (first == (int)blockIdx.x - 1)
-                cut = AttCut{first, split.owner(it.at + ATT_ITEM_COST + it.ntiles - 1), it.b, it.hk, it.t0,
-                             it.ntok * w.g.G};
-        }
         for (uint32_t k = 0; ok; ++k) {
             const uint32_t slot = k % ATT_SEGS;
             if (k >= ATT_SEGS) wait(&ms.seg_empty[slot], k / ATT_SEGS - 1);
@@ -516,10 +519,23 @@ __global__ void __launch_bounds__(Att<DP>::THREADS, 1)
                     sg.whole = it.tile0 == 0 && it.tile1 == it.ntiles;
                 }
                 mbar_arrive(&ms.seg_full[slot]);
-                if (k == 0) w.cuts[blockIdx.x] = cut;
             }
             __syncwarp();
             if (!more) break;
+            if (k == 0 && it.tile0 > 0) {
+                // the item began in an earlier range.  Where that is the one before,
+                // this is the first cut of the item, and its join is announced here.
+                const int first = split.owner(it.at + ATT_ITEM_COST);
+                if (first == (int)blockIdx.x - 1) {
+                    const int last = split.owner(it.at + ATT_ITEM_COST + it.ntiles - 1), rows = it.ntok * w.g.G;
+                    const int tasks = att_join_tasks(last - first + 1, rows, p.s.D);
+                    unsigned at = 0;
+                    if (lane == 0) at = atomicAdd(w.n_joins, (unsigned)tasks);
+                    at = __shfl_sync(0xffffffffu, at, 0);
+                    for (int i = lane; i < tasks; i += 32)
+                        w.joins[at + i] = AttJoin{first, last, it.b, it.hk, it.t0, rows, i, 0};
+                }
+            }
             it.next(p, w.g);
         }
         if (!ok && lane == 0) ms.failed = 1;
@@ -929,148 +945,97 @@ __global__ void __launch_bounds__(Att<DP>::THREADS, 1)
 // k_tree_combine                                                            //
 // ------------------------------------------------------------------------- //
 // Joins the parts of an item cut between CTAs: out = sum_i 2^(m_i - m) O_i /
-// sum_i 2^(m_i - m) l_i (m here in log2 units).  Lane = row, and a task is 32
-// rows by 32 columns of a cut: for a warp where the parts are few, all loads of
-// a thread independent; for a CTA where they are many (few items, long
-// caches), 8 columns, every eighth part a warp's and the warps' sums joined in
-// shared memory.  The CTAs find their tasks in the list of cuts, since only
-// the GPU knows which ranges cut items.
-constexpr int COMB_THREADS = 256, COMB_CUTS = 512, COMB_CTAS_PER_SM = 4;
-constexpr int COMB_FEW = 8;
-
-// tasks of the cuts up to each, of one kind: cols columns a task
-__device__ __forceinline__ int comb_scan(const AttWork& w, int n_cuts, bool many, int cols, int* ends, int* scan)
-{
-    const int tid = threadIdx.x, lane = tid & 31, g = tid >> 5;
-    int before = 0;
-    for (int i0 = 0; i0 < n_cuts; i0 += COMB_THREADS) {
-        const int i = i0 + tid;
-        int t = 0;
-        if (i < n_cuts) {
-            const AttCut cut = w.cuts[i];
-            if (cut.first >= 0 && (cut.last - cut.first + 1 > COMB_FEW) == many)
-                t = ((cut.rows + 31) / 32) * ((w.p.s.D + cols - 1) / cols);
-        }
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int v = __shfl_up_sync(0xffffffffu, t, o);
-            if (lane >= o) t += v;
-        }
-        if (lane == 31) scan[g] = t;
-        __syncthreads();
-        int add = before;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            const int v = scan[k];
-            if (k < g) add += v;
-            before += v;
-        }
-        if (i < n_cuts) ends[i] = t + add;
-        __syncthreads();
-    }
-    return before;
-}
+// sum_i 2^(m_i - m) l_i (m here in log2 units).  Lane = row.  Where the parts
+// are few a warp takes 32 rows by 32 columns, all loads of a thread
+// independent; where they are many (few items, long caches) a CTA takes 32
+// rows by 8 columns, every eighth part a warp's, and the warps' sums meet in
+// shared memory.  The tasks are those that k_tree_attend announced: only the
+// GPU knows which ranges cut items.  Parts are summed in their order, whatever
+// the order of the tasks.
+constexpr int COMB_THREADS = 256, COMB_CTAS_PER_SM = 4;
 
 template <bool F16>
 __global__ void __launch_bounds__(COMB_THREADS, COMB_CTAS_PER_SM)
-    k_tree_combine(const AttWork w, int n_cuts, int DP, int prows)
+    k_tree_combine(const AttWork w, int DP, int prows)
 {
     using H = Half2<F16>;
     __shared__ float4 acc_s[8][2][32];
     __shared__ float2 ml_s[8][32];
-    __shared__ int ends[COMB_CUTS];
-    __shared__ int scan[8];
-    asm volatile("griddepcontrol.wait;" ::: "memory");
     const TreeAttendParams& p = w.p;
     const int lane = threadIdx.x & 31, g = threadIdx.x >> 5;
     const int D = p.s.D, G = w.g.G, first_rows = w.g.tpt * G;
     const float c = p.scale * 1.4426950408889634f;
     auto weight = [&](float m, float ref) { return m == -INFINITY ? 0.f : ex2_fast((m - ref) * c); };
-    auto slot = [](const AttCut& cut, int i) { return (int64_t)(cut.first + i) * 2 + (i == 0 ? 1 : 0); };
-    // the cut of a task (the first whose tasks end past it), and the task's number in it
-    auto find = [&](int& task) {
-        int lo = 0, hi = n_cuts - 1;
-        while (lo < hi) {
-            const int mid = (lo + hi) / 2;
-            if (ends[mid] > task) hi = mid;
-            else lo = mid + 1;
-        }
-        if (lo) task -= ends[lo - 1];
-        return w.cuts[lo];
-    };
-    // rows of the second row tile lie behind the first's 128
-    auto part_row = [&](int r) { return r < first_rows ? r : ATT_ROWS + r - first_rows; };
-    auto out_row = [&](const AttCut& cut, int r) {
-        const int node = r / G;
-        return ((int64_t)cut.b * p.s.T + cut.t0 + node) * p.s.Hq + cut.hk * G + r - node * G;
-    };
-
-    // ---- few parts: a warp per task
-    const int few = comb_scan(w, n_cuts, false, 32, ends, scan), c32 = (D + 31) / 32;
-    for (int task0 = blockIdx.x * 8 + g; task0 < few; task0 += gridDim.x * 8) {
-        int task = task0;
-        const AttCut cut = find(task);
-        const int n = cut.last - cut.first + 1, rb = task / c32, col4 = (task - rb * c32) * 8;
-        const int r = rb * 32 + lane, pr = part_row(r);
-        if (r >= cut.rows) continue;
-        float top = -INFINITY, l = 0.f;
-        for (int i = 0; i < n; ++i) top = fmaxf(top, w.part_ml[slot(cut, i) * prows + pr].x);
-        const float ref = top == -INFINITY ? 0.f : top;
-        float4 acc[8];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int tasks = (int)__ldcg(w.n_joins);
+    for (int task = blockIdx.x; task < tasks; task += gridDim.x) {
+        const AttJoin jn = w.joins[task];
+        const int n = jn.last - jn.first + 1;
+        auto slot = [&](int i) { return (int64_t)(jn.first + i) * 2 + (i == 0 ? 1 : 0); };
+        // rows of the second row tile lie behind the first's 128
+        auto part_row = [&](int r) { return r < first_rows ? r : ATT_ROWS + r - first_rows; };
+        auto out_row = [&](int r) {
+            const int node = r / G;
+            return ((int64_t)jn.b * p.s.T + jn.t0 + node) * p.s.Hq + jn.hk * G + r - node * G;
+        };
+        if (n <= ATT_FEW) {
+            const int c32 = (D + 31) / 32, sub = jn.sub * 8 + g, rb = sub / c32, col4 = (sub - rb * c32) * 8;
+            const int r = rb * 32 + lane, pr = part_row(r);
+            if (r >= jn.rows) continue;
+            float top = -INFINITY, l = 0.f;
+            for (int i = 0; i < n; ++i) top = fmaxf(top, w.part_ml[slot(i) * prows + pr].x);
+            const float ref = top == -INFINITY ? 0.f : top;
+            float4 acc[8];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int i = 0; i < n; ++i) {
-            const float2 v = w.part_ml[slot(cut, i) * prows + pr];
-            const float f = weight(v.x, ref);
-            l += v.y * f;
-            const float4* src = (const float4*)w.part_o + (slot(cut, i) * (DP / 4) + col4) * prows + pr;
+            for (int k = 0; k < 8; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+            for (int i = 0; i < n; ++i) {
+                const float2 v = w.part_ml[slot(i) * prows + pr];
+                const float f = weight(v.x, ref);
+                l += v.y * f;
+                const float4* src = (const float4*)w.part_o + (slot(i) * (DP / 4) + col4) * prows + pr;
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-                if ((col4 + k) * 4 < D) {
-                    const float4 o = src[k * prows];
-                    acc[k].x += f * o.x, acc[k].y += f * o.y, acc[k].z += f * o.z, acc[k].w += f * o.w;
-                }
-        }
-        const bool none = l == 0.f;
-        const float inv = none ? 0.f : 1.f / l;
-        const int64_t orow = out_row(cut, r);
-        uint4* o16 = (uint4*)((char*)p.out + (orow * D + col4 * 4) * 2);
+                for (int k = 0; k < 8; ++k)
+                    if ((col4 + k) * 4 < D) {
+                        const float4 o = src[k * prows];
+                        acc[k].x += f * o.x, acc[k].y += f * o.y, acc[k].z += f * o.z, acc[k].w += f * o.w;
+                    }
+            }
+            const bool none = l == 0.f;
+            const float inv = none ? 0.f : 1.f / l;
+            const int64_t orow = out_row(r);
+            uint4* o16 = (uint4*)((char*)p.out + (orow * D + col4 * 4) * 2);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const float4 a = acc[2 * k], b = acc[2 * k + 1];
-            if ((col4 + 2 * k) * 4 < D)
-                o16[k] = none ? make_uint4(0, 0, 0, 0)
-                              : make_uint4(H::pack(a.x * inv, a.y * inv), H::pack(a.z * inv, a.w * inv),
-                                           H::pack(b.x * inv, b.y * inv), H::pack(b.z * inv, b.w * inv));
+            for (int k = 0; k < 4; ++k) {
+                const float4 a = acc[2 * k], b = acc[2 * k + 1];
+                if ((col4 + 2 * k) * 4 < D)
+                    o16[k] = none ? make_uint4(0, 0, 0, 0)
+                                  : make_uint4(H::pack(a.x * inv, a.y * inv), H::pack(a.z * inv, a.w * inv),
+                                               H::pack(b.x * inv, b.y * inv), H::pack(b.z * inv, b.w * inv));
+            }
+            if (p.lse && col4 == 0) p.lse[orow] = none ? -INFINITY : fmaf(ref, p.scale, logf(l));
+            continue;
         }
-        if (p.lse && col4 == 0) p.lse[orow] = none ? -INFINITY : fmaf(ref, p.scale, logf(l));
-    }
-    __syncthreads();
-
-    // ---- many parts: a CTA per task
-    const int many = comb_scan(w, n_cuts, true, 8, ends, scan), c8 = D / 8;
-    for (int task0 = blockIdx.x; task0 < many; task0 += gridDim.x) {
-        int task = task0;
-        const AttCut cut = find(task);
-        const int n = cut.last - cut.first + 1, rb = task / c8, col4 = (task - rb * c8) * 2;
-        const int r = min(rb * 32 + lane, cut.rows - 1), pr = part_row(r);
+        const int c8 = D / 8, rb = jn.sub / c8, col4 = (jn.sub - rb * c8) * 2;
+        const int r = min(rb * 32 + lane, jn.rows - 1), pr = part_row(r);
         float top = -INFINITY, l = 0.f;
 #pragma unroll 4
-        for (int i = g; i < n; i += 8) top = fmaxf(top, w.part_ml[slot(cut, i) * prows + pr].x);
+        for (int i = g; i < n; i += 8) top = fmaxf(top, w.part_ml[slot(i) * prows + pr].x);
         const float own = top == -INFINITY ? 0.f : top;
         float4 acc[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
 #pragma unroll 4
         for (int i = g; i < n; i += 8) {
-            const float2 v = w.part_ml[slot(cut, i) * prows + pr];
+            const float2 v = w.part_ml[slot(i) * prows + pr];
             const float f = weight(v.x, own);
             l += v.y * f;
-            const float4* src = (const float4*)w.part_o + (slot(cut, i) * (DP / 4) + col4) * prows + pr;
+            const float4* src = (const float4*)w.part_o + (slot(i) * (DP / 4) + col4) * prows + pr;
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
                 const float4 o = src[k * prows];
                 acc[k].x += f * o.x, acc[k].y += f * o.y, acc[k].z += f * o.z, acc[k].w += f * o.w;
             }
         }
+        __syncthreads();  // the tables of the task before have been read
         ml_s[g][lane] = make_float2(top, l);
         acc_s[g][0][lane] = acc[0];
         acc_s[g][1][lane] = acc[1];
@@ -1092,8 +1057,8 @@ __global__ void __launch_bounds__(COMB_THREADS, COMB_CTAS_PER_SM)
             }
             const bool none = l == 0.f;
             const float inv = none ? 0.f : 1.f / l;
-            if (rb * 32 + lane < cut.rows) {
-                const int64_t orow = out_row(cut, r);
+            if (rb * 32 + lane < jn.rows) {
+                const int64_t orow = out_row(r);
                 *(uint2*)((char*)p.out + (orow * D + (col4 + g) * 4) * 2) =
                     none ? make_uint2(0, 0)
                          : make_uint2(H::pack(y.x * inv, y.y * inv), H::pack(y.z * inv, y.w * inv));
@@ -1101,8 +1066,9 @@ __global__ void __launch_bounds__(COMB_THREADS, COMB_CTAS_PER_SM)
                     p.lse[orow] = none ? -INFINITY : fmaf(ref, p.scale, logf(l));
             }
         }
-        __syncthreads();  // the tables are reused
     }
+    // the last CTA to finish leaves the list empty
+    if (threadIdx.x == 0 && atomicInc(w.n_done, gridDim.x - 1) == gridDim.x - 1) *w.n_joins = 0;
 }
 
 // ------------------------------------------------------------------------- //
@@ -1111,15 +1077,16 @@ __global__ void __launch_bounds__(COMB_THREADS, COMB_CTAS_PER_SM)
 static int att_dp(int D) { return (D + 63) / 64 * 64; }
 static int att_part_rows(int DP) { return (DP <= 128 ? 2 : 1) * ATT_ROWS; }
 
-// workspace: partial O, (m, l) and cuts of `ctas` CTAs
-size_t tree_attend_bytes(int D, int ctas, size_t* ml_at, size_t* cut_at)
+// workspace: partial O, (m, l) and joins of `ctas` CTAs, and the joins' two counters
+size_t tree_attend_bytes(int D, int ctas, size_t* ml_at, size_t* join_at)
 {
     const int DP = att_dp(D);
     const size_t slots = 2 * (size_t)ctas, o = slots * att_part_rows(DP) * DP * sizeof(float);
     const size_t ml = slots * att_part_rows(DP) * sizeof(float2);
     *ml_at = o;
-    *cut_at = o + ml;
-    return o + ml + (size_t)ctas * sizeof(AttCut);
+    *join_at = o + ml;
+    const int most = att_join_tasks(ATT_FEW + 1, att_part_rows(DP), DP);  // of a cut
+    return o + ml + 16 + (size_t)ctas * most * sizeof(AttJoin);
 }
 
 // a tensor [d3, d2, d1, D] of 16-bit elements as a 4-D map with boxes of 64
@@ -1159,21 +1126,20 @@ static cudaError_t att_launch(AttWork w, int num_sms, cudaStream_t s)
         !att_map(&mk, F16, w.p.c.k, sh.D, cd, cs, 1, w.page_box) ||
         !att_map(&mv, F16, w.p.c.v, sh.D, cd, cs, 1, w.page_box))
         return cudaErrorInvalidValue;
-    num_sms = std::min(num_sms, COMB_CUTS);
     k_tree_attend<F16, DP><<<num_sms, A::THREADS, A::SMEM, s>>>(mq, mk, mv, w);
     if ((e = cudaGetLastError()) != cudaSuccess || num_sms == 1) return e;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
-    // no more CTAs than there may be tasks
-    const int64_t tasks = (int64_t)num_sms * ((min(w.g.group, sh.T) * w.g.G + 31) / 32) * ((sh.D + 7) / 8);
-    cfg.gridDim = dim3((unsigned)std::min<int64_t>(tasks, (int64_t)num_sms * COMB_CTAS_PER_SM));
+    cfg.gridDim = dim3((unsigned)(num_sms * COMB_CTAS_PER_SM));
     cfg.blockDim = dim3(COMB_THREADS);
     cfg.stream = s;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, k_tree_combine<F16>, w, num_sms, DP, A::NS * ATT_ROWS);
+    e = cudaLaunchKernelEx(&cfg, k_tree_combine<F16>, w, DP, A::NS * ATT_ROWS);
+    if (e != cudaSuccess) cudaMemsetAsync(w.n_joins, 0, sizeof(unsigned), s);  // nobody empties the list
+    return e;
 }
 
 bool tree_attend_fits(const TreeShape& sh)
@@ -1187,8 +1153,8 @@ bool tree_attend_fits(const TreeShape& sh)
 cudaError_t launch_tree_attend(const TreeAttendParams& p, int dtype, int num_sms, void* ws, unsigned* err, bool stall,
                                cudaStream_t s)
 {
-    size_t ml_at, cut_at;
-    tree_attend_bytes(p.s.D, num_sms, &ml_at, &cut_at);
+    size_t ml_at, join_at;
+    tree_attend_bytes(p.s.D, num_sms, &ml_at, &join_at);
     AttWork w = {};
     w.p = p;
     w.g.G = p.s.Hq / p.s.Hkv;
@@ -1196,7 +1162,9 @@ cudaError_t launch_tree_attend(const TreeAttendParams& p, int dtype, int num_sms
     w.g.Hkv = p.s.Hkv;
     w.part_o = (float*)ws;
     w.part_ml = (float2*)((char*)ws + ml_at);
-    w.cuts = (AttCut*)((char*)ws + cut_at);
+    w.n_joins = (unsigned*)((char*)ws + join_at);
+    w.n_done = w.n_joins + 1;
+    w.joins = (AttJoin*)((char*)ws + join_at + 16);
     w.err = err;
     w.stall = stall;
     const bool f16 = dtype == SPEC_F16;

@@ -143,13 +143,14 @@ class TreeCache:
     free pages, caches) are the caller's; the cache of a layer is a pair of
     tensors [num_pages, page_size, kv_heads, head_dim] of one layout, any
     strides with a contiguous last dimension.  ``new_pool`` makes the state of
-    an empty pool."""
+    an empty pool.  Small calls are bound by the host, so the checks here are
+    kept short: plain attributes, one pass over each tensor."""
 
     def __init__(self, *, max_batch: int, max_tokens: int, q_heads: int, kv_heads: int,
                  head_dim: int, dtype, page_size: int, num_pages: int, table_width: int,
                  device: int | None = None):
         import torch
-        from . import SPEC_BF16, SPEC_F32
+        from . import SPEC_BF16, SPEC_F32, load_library
         self.h = None
         types = {"bf16": torch.bfloat16, "f16": torch.float16, "f32": torch.float32}
         self.dtype = types.get(dtype, dtype)
@@ -161,6 +162,15 @@ class TreeCache:
         self.cfg = spec_tree_config(self.device, max_batch, max_tokens, q_heads, kv_heads,
                                     head_dim, code, page_size, num_pages, table_width)
         self.h = spec_tree_create(self.cfg)
+        self._lib = load_library()
+        self._dev = torch.device("cuda", self.device)
+        self._hq, self._hkv, self._d = q_heads, kv_heads, head_dim
+        self._pages, self._width, self._max_tokens = num_pages, table_width, max_tokens
+        self._cache_shape = (num_pages, page_size, kv_heads, head_dim)
+        self._scale = head_dim ** -0.5
+        # the argument records of the calls, filled anew by each (one handle, one caller at a time)
+        self._plan_args, self._append_args = spec_tree_plan_args(), spec_tree_append_args()
+        self._attend_args, self._keep_args = spec_tree_attend_args(), spec_tree_keep_args()
 
     def close(self):
         if self.h is not None and self.h.value:
@@ -174,74 +184,72 @@ class TreeCache:
             pass
 
     # ---- argument checks --------------------------------------------------- #
-    def _ints(self, t, shape, what, dtype=None):
-        import torch
-        if t is None:
-            return None
-        if t.dtype != (dtype or torch.int32) or tuple(t.shape) != shape or not t.is_contiguous():
-            raise ValueError(f"{what} must be a contiguous {dtype or torch.int32} tensor of shape "
-                             f"{shape}, got {t.dtype} {tuple(t.shape)}")
-        self._on_device(t, what)
+    def _tensor(self, t, shape, dtype, what):
+        """The address of a contiguous tensor of this shape and type on the handle's device."""
+        if t.shape != shape or t.dtype is not dtype or t.device != self._dev or not t.is_contiguous():
+            raise ValueError(f"{what} must be a contiguous {dtype} tensor of shape {shape} on "
+                             f"{self._dev}, got {t.dtype} {tuple(t.shape)} on {t.device}")
         return t.data_ptr()
 
-    def _on_device(self, t, what):
-        if t.device.type != "cuda" or t.device.index != self.device:
-            raise ValueError(f"{what} is on {t.device}, the handle on cuda:{self.device}")
-
-    def _rows(self, t, heads, what):
-        if t.dtype != self.dtype or t.dim() != 4 or t.shape[2] != heads or \
-                t.shape[3] != self.cfg.head_dim:
-            raise ValueError(f"{what} must be {self.dtype} [B, T, {heads}, {self.cfg.head_dim}], "
-                             f"got {t.dtype} {tuple(t.shape)}")
-        self._on_device(t, what)
-        return spec_tree_rows(t.data_ptr(), *self._strides(t, (0, 1, 2), what))
-
-    @staticmethod
-    def _strides(t, dims, what):
-        if t.shape[-1] > 1 and t.stride(-1) != 1:
+    def _rows(self, rec, t, shape, what):
+        """Fill a spec_tree_rows with a [B, T, heads, head_dim] tensor of any strides."""
+        if t.shape != shape or t.dtype is not self.dtype or t.device != self._dev:
+            raise ValueError(f"{what} must be {self.dtype} {shape} on {self._dev}, got {t.dtype} "
+                             f"{tuple(t.shape)} on {t.device}")
+        st = t.stride()
+        if st[3] != 1:
             raise ValueError(f"the last dimension of {what} must be contiguous")
+        rec.ptr = t.data_ptr()
         # the stride of a dimension of size 1 is never used
-        return [t.stride(d) if t.shape[d] > 1 else 0 for d in dims]
+        rec.seq_stride = st[0] if shape[0] > 1 else 0
+        rec.token_stride = st[1] if shape[1] > 1 else 0
+        rec.head_stride = st[2] if shape[2] > 1 else 0
 
-    def _cache(self, k, v, layered):
-        c = self.cfg
-        want = (c.num_pages, c.page_size, c.kv_heads, c.head_dim)
-        for t, what in ((k, "k_cache"), (v, "v_cache")):
-            if t.dtype != self.dtype or tuple(t.shape[-4:]) != want or t.dim() not in (4, 4 + layered):
-                raise ValueError(f"{what} must be {self.dtype} {want}, got {t.dtype} {tuple(t.shape)}")
-            self._on_device(t, what)
-        strides = self._strides(k, (-4, -3, -2), "k_cache")
-        layer = k.stride(0) if k.dim() == 5 and k.shape[0] > 1 else 0
-        if self._strides(v, (-4, -3, -2), "v_cache") != strides or v.shape != k.shape or \
-                (layer and v.stride(0) != layer):
+    def _cache(self, rec, k, v, layered=False):
+        """Fill a spec_tree_cache with the K and V tensors of one layer or (layered) of several."""
+        shape, st = k.shape, k.stride()
+        if v.shape != shape or (v.stride() != st and
+                                any(a != b for a, b, n in zip(st, v.stride(), shape) if n > 1)):
             raise ValueError("k_cache and v_cache must have the same shape and strides")
-        return spec_tree_cache(k.data_ptr(), v.data_ptr(), *strides, layer,
-                               k.shape[0] if k.dim() == 5 else 1)
+        many = layered and len(shape) == 5
+        if (shape[1:] if many else shape) != self._cache_shape or k.dtype is not self.dtype or \
+                v.dtype is not self.dtype or k.device != self._dev or v.device != self._dev:
+            raise ValueError(f"the caches must be {self.dtype} {self._cache_shape} on {self._dev}, "
+                             f"got {k.dtype} and {v.dtype} {tuple(shape)} on {k.device}")
+        if st[-1] != 1:
+            raise ValueError("the last dimension of the caches must be contiguous")
+        size = self._cache_shape
+        rec.k, rec.v = k.data_ptr(), v.data_ptr()
+        rec.page_stride = st[-4] if size[0] > 1 else 0
+        rec.token_stride = st[-3] if size[1] > 1 else 0
+        rec.head_stride = st[-2] if size[2] > 1 else 0
+        rec.layers = shape[0] if many else 1
+        rec.layer_stride = st[0] if many and shape[0] > 1 else 0
 
     def _stream(self, stream):
-        import torch
-        s = stream if stream is not None else torch.cuda.current_stream(self.device)
-        return s.cuda_stream
+        if stream is None:
+            import torch
+            stream = torch.cuda.current_stream(self.device)
+        return stream.cuda_stream
 
-    def _out(self, t, shape, dtype, what):
-        import torch
-        if t is None:
-            return torch.empty(shape, dtype=dtype, device=f"cuda:{self.device}")
-        if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
-            raise ValueError(f"{what} must be a contiguous {dtype} tensor of shape {tuple(shape)}")
-        self._on_device(t, what)
-        return t
+    def _out(self, out, key, shape, dtype):
+        """The caller's output tensor (checked), or a new one."""
+        if out is None or key not in out:
+            import torch
+            return torch.empty(shape, dtype=dtype, device=self._dev)
+        self._tensor(out[key], shape, dtype, f"out['{key}']")
+        return out[key]
 
     # ---- the operators ------------------------------------------------------ #
     def new_pool(self, batch: int) -> dict:
         """The plan's state of an empty cache: block_table, held, ring and
         free_pages, every page free."""
         import torch
-        c, dev = self.cfg, f"cuda:{self.device}"
-        return dict(block_table=torch.full((batch, c.table_width), -1, dtype=torch.int32, device=dev),
-                    held=torch.zeros(batch, dtype=torch.int32, device=dev),
-                    ring=torch.tensor([0, c.num_pages], dtype=torch.int64, device=dev),
-                    free_pages=torch.arange(c.num_pages, dtype=torch.int32, device=dev))
+        i32, dev = torch.int32, self._dev
+        return dict(block_table=torch.full((batch, self._width), -1, dtype=i32, device=dev),
+                    held=torch.zeros(batch, dtype=i32, device=dev),
+                    ring=torch.tensor([0, self._pages], dtype=torch.int64, device=dev),
+                    free_pages=torch.arange(self._pages, dtype=i32, device=dev))
 
     def plan(self, ctx_len, n_tokens, held, ring, free_pages, block_table, *, parents=None,
              max_tokens: int | None = None, out: dict | None = None, stream=None) -> dict:
@@ -250,30 +258,29 @@ class TreeCache:
         returns held, ring, slot_map, positions, row_status (and tree_mask with
         parents).  T is parents.shape[1], or max_tokens for chains."""
         import torch
+        i32, a = torch.int32, self._plan_args
         B = ctx_len.shape[0]
-        T = parents.shape[1] if parents is not None else int(max_tokens or self.cfg.max_tokens)
-        out = out or {}
-        i32 = torch.int32
-        res = dict(held=self._out(out.get("held"), (B,), i32, "out['held']"),
-                   ring=self._out(out.get("ring"), (2,), torch.int64, "out['ring']"),
-                   slot_map=self._out(out.get("slot_map"), (B, T), i32, "out['slot_map']"),
-                   positions=self._out(out.get("positions"), (B, T), i32, "out['positions']"),
-                   row_status=self._out(out.get("row_status"), (B,), i32, "out['row_status']"))
+        T = parents.shape[1] if parents is not None else int(max_tokens or self._max_tokens)
+        b, bt = (B,), (B, T)
+        res = dict(held=self._out(out, "held", b, i32), ring=self._out(out, "ring", (2,), torch.int64),
+                   slot_map=self._out(out, "slot_map", bt, i32),
+                   positions=self._out(out, "positions", bt, i32),
+                   row_status=self._out(out, "row_status", b, i32))
+        a.parents = a.tree_mask = None
         if parents is not None:
-            res["tree_mask"] = self._out(out.get("tree_mask"), (B, T, -(-T // 32)), i32,
-                                         "out['tree_mask']")
-        c = self.cfg
-        args = spec_tree_plan_args(
-            self._ints(ctx_len, (B,), "ctx_len"), self._ints(n_tokens, (B,), "n_tokens"),
-            self._ints(parents, (B, T), "parents"), self._ints(held, (B,), "held"),
-            self._ints(ring, (2,), "ring", torch.int64),
-            self._ints(free_pages, (c.num_pages,), "free_pages"),
-            self._ints(block_table, (B, c.table_width), "block_table"), B, T,
-            res["held"].data_ptr(), res["ring"].data_ptr(), res["slot_map"].data_ptr(),
-            res["positions"].data_ptr(),
-            res["tree_mask"].data_ptr() if parents is not None else None,
-            res["row_status"].data_ptr())
-        spec_tree_plan(self.h, args, self._stream(stream))
+            mask = res["tree_mask"] = self._out(out, "tree_mask", (B, T, (T + 31) // 32), i32)
+            a.parents, a.tree_mask = self._tensor(parents, bt, i32, "parents"), mask.data_ptr()
+        a.ctx_len = self._tensor(ctx_len, b, i32, "ctx_len")
+        a.n_tokens = None if n_tokens is None else self._tensor(n_tokens, b, i32, "n_tokens")
+        a.held = self._tensor(held, b, i32, "held")
+        a.ring = self._tensor(ring, (2,), torch.int64, "ring")
+        a.free_pages = self._tensor(free_pages, (self._pages,), i32, "free_pages")
+        a.block_table = self._tensor(block_table, (B, self._width), i32, "block_table")
+        a.batch, a.tokens = B, T
+        a.held_out, a.ring_out = res["held"].data_ptr(), res["ring"].data_ptr()
+        a.slot_map, a.positions = res["slot_map"].data_ptr(), res["positions"].data_ptr()
+        a.row_status = res["row_status"].data_ptr()
+        _check(self._lib.spec_tree_plan(self.h, a, self._stream(stream)), "spec_tree_plan")
         return res
 
     def append(self, q, k, v, k_cache, v_cache, slot_map, positions=None, n_tokens=None, *,
@@ -283,33 +290,32 @@ class TreeCache:
         new q [B, T, q_heads, head_dim].  cos_sin: float32 [positions, rot_dim],
         rot_dim / 2 cosines, then as many sines."""
         import torch
-        c = self.cfg
+        i32, a, d, hkv = torch.int32, self._append_args, self._d, self._hkv
         B, T = q.shape[:2]
-        if tuple(k.shape[:2]) != (B, T) or tuple(v.shape[:2]) != (B, T):
-            raise ValueError("q, k and v must have the same batch and tokens")
-        for w, what in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-            if w is not None and (w.dtype != self.dtype or tuple(w.shape) != (c.head_dim,) or
-                                  not w.is_contiguous()):
-                raise ValueError(f"{what} must be a contiguous {self.dtype} tensor [{c.head_dim}]")
-        if cos_sin is not None and (cos_sin.dtype != torch.float32 or cos_sin.dim() != 2 or
-                                    not cos_sin.is_contiguous() or positions is None):
-            raise ValueError("cos_sin must be a contiguous float32 tensor [positions, rot_dim], "
-                             "with positions given")
-        for t, what in ((q_weight, "q_weight"), (k_weight, "k_weight"), (cos_sin, "cos_sin")):
-            if t is not None:
-                self._on_device(t, what)
-        out = self._out(out, (B, T, c.q_heads, c.head_dim), self.dtype, "out")
-        table_len, rot = cos_sin.shape if cos_sin is not None else (0, 0)
-        args = spec_tree_append_args(
-            self._rows(q, c.q_heads, "q"), self._rows(k, c.kv_heads, "k"),
-            self._rows(v, c.kv_heads, "v"), self._cache(k_cache, v_cache, False),
-            self._ints(slot_map, (B, T), "slot_map"), self._ints(positions, (B, T), "positions"),
-            self._ints(n_tokens, (B,), "n_tokens"),
-            q_weight.data_ptr() if q_weight is not None else None,
-            k_weight.data_ptr() if k_weight is not None else None,
-            cos_sin.data_ptr() if cos_sin is not None else None, table_len, rot,
-            int(interleaved), float(eps), B, T, out.data_ptr())
-        spec_tree_append(self.h, args, self._stream(stream))
+        shape, bt = (B, T, self._hq, d), (B, T)
+        self._rows(a.q, q, shape, "q")
+        self._rows(a.k, k, (B, T, hkv, d), "k")
+        self._rows(a.v, v, (B, T, hkv, d), "v")
+        self._cache(a.cache, k_cache, v_cache)
+        a.slot_map = self._tensor(slot_map, bt, i32, "slot_map")
+        a.positions = None if positions is None else self._tensor(positions, bt, i32, "positions")
+        a.n_tokens = None if n_tokens is None else self._tensor(n_tokens, (B,), i32, "n_tokens")
+        a.q_weight = None if q_weight is None else self._tensor(q_weight, (d,), self.dtype, "q_weight")
+        a.k_weight = None if k_weight is None else self._tensor(k_weight, (d,), self.dtype, "k_weight")
+        a.cos_sin, a.table_len, a.rot_dim = None, 0, 0
+        if cos_sin is not None:
+            if cos_sin.dim() != 2 or positions is None:
+                raise ValueError("cos_sin must be a float32 tensor [positions, rot_dim], with "
+                                 "positions given")
+            a.cos_sin = self._tensor(cos_sin, cos_sin.shape, torch.float32, "cos_sin")
+            a.table_len, a.rot_dim = cos_sin.shape
+        a.interleaved, a.eps, a.batch, a.tokens = bool(interleaved), eps, B, T
+        if out is None:
+            out = torch.empty(shape, dtype=self.dtype, device=self._dev)
+            a.q_out = out.data_ptr()
+        else:
+            a.q_out = self._tensor(out, shape, self.dtype, "out")
+        _check(self._lib.spec_tree_append(self.h, a, self._stream(stream)), "spec_tree_append")
         return out
 
     def attend(self, q, k_cache, v_cache, block_table, ctx_len, n_tokens=None, *, tree_mask=None,
@@ -319,21 +325,24 @@ class TreeCache:
         over context and chain); scale defaults to head_dim ** -0.5.  Returns
         out [B, T, q_heads, head_dim] and, with lse, lse [B, T, q_heads]."""
         import torch
-        c = self.cfg
+        i32, a = torch.int32, self._attend_args
         B, T = q.shape[:2]
-        out = out or {}
-        res = dict(out=self._out(out.get("out"), (B, T, c.q_heads, c.head_dim), self.dtype,
-                                 "out['out']"))
+        shape = (B, T, self._hq, self._d)
+        self._rows(a.q, q, shape, "q")
+        self._cache(a.cache, k_cache, v_cache)
+        a.block_table = self._tensor(block_table, (B, self._width), i32, "block_table")
+        a.ctx_len = self._tensor(ctx_len, (B,), i32, "ctx_len")
+        a.n_tokens = None if n_tokens is None else self._tensor(n_tokens, (B,), i32, "n_tokens")
+        a.tree_mask = None if tree_mask is None else \
+            self._tensor(tree_mask, (B, T, (T + 31) // 32), i32, "tree_mask")
+        a.scale, a.batch, a.tokens = self._scale if scale is None else scale, B, T
+        o = self._out(out, "out", shape, self.dtype)
+        res = {"out": o}
+        a.out, a.lse = o.data_ptr(), None
         if lse:
-            res["lse"] = self._out(out.get("lse"), (B, T, c.q_heads), torch.float32, "out['lse']")
-        args = spec_tree_attend_args(
-            self._rows(q, c.q_heads, "q"), self._cache(k_cache, v_cache, False),
-            self._ints(block_table, (B, c.table_width), "block_table"),
-            self._ints(ctx_len, (B,), "ctx_len"), self._ints(n_tokens, (B,), "n_tokens"),
-            self._ints(tree_mask, (B, T, -(-T // 32)), "tree_mask"),
-            float(c.head_dim ** -0.5 if scale is None else scale), B, T, res["out"].data_ptr(),
-            res["lse"].data_ptr() if lse else None)
-        spec_tree_attend(self.h, args, self._stream(stream))
+            e = res["lse"] = self._out(out, "lse", shape[:3], torch.float32)
+            a.lse = e.data_ptr()
+        _check(self._lib.spec_tree_attend(self.h, a, self._stream(stream)), "spec_tree_attend")
         return res
 
     def keep(self, k_cache, v_cache, block_table, ctx_len, n_tokens, path, path_len, *,
@@ -342,18 +351,20 @@ class TreeCache:
         layers of [layers, num_pages, page_size, kv_heads, head_dim] caches (or
         in one layer's); returns the new ctx_len and row_status."""
         import torch
+        i32, a = torch.int32, self._keep_args
         B, T = path.shape
-        out = out or {}
-        res = dict(ctx_len=self._out(out.get("ctx_len"), (B,), torch.int32, "out['ctx_len']"),
-                   row_status=self._out(out.get("row_status"), (B,), torch.int32,
-                                        "out['row_status']"))
-        args = spec_tree_keep_args(
-            self._cache(k_cache, v_cache, True),
-            self._ints(block_table, (B, self.cfg.table_width), "block_table"),
-            self._ints(ctx_len, (B,), "ctx_len"), self._ints(n_tokens, (B,), "n_tokens"),
-            self._ints(path, (B, T), "path"), self._ints(path_len, (B,), "path_len"), B, T,
-            res["ctx_len"].data_ptr(), res["row_status"].data_ptr())
-        spec_tree_keep(self.h, args, self._stream(stream))
+        b = (B,)
+        self._cache(a.cache, k_cache, v_cache, True)
+        a.block_table = self._tensor(block_table, (B, self._width), i32, "block_table")
+        a.ctx_len = self._tensor(ctx_len, b, i32, "ctx_len")
+        a.n_tokens = None if n_tokens is None else self._tensor(n_tokens, b, i32, "n_tokens")
+        a.path = self._tensor(path, (B, T), i32, "path")
+        a.path_len = self._tensor(path_len, b, i32, "path_len")
+        a.batch, a.tokens = B, T
+        res = {"ctx_len": self._out(out, "ctx_len", b, i32),
+               "row_status": self._out(out, "row_status", b, i32)}
+        a.ctx_out, a.row_status = res["ctx_len"].data_ptr(), res["row_status"].data_ptr()
+        _check(self._lib.spec_tree_keep(self.h, a, self._stream(stream)), "spec_tree_keep")
         return res
 
     def check(self, stream=None) -> int:
