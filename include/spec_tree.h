@@ -198,7 +198,7 @@ spec_status spec_tree_append(spec_tree_t h, const spec_tree_append_args* a, void
  * SPEC_ERR_UNSUPPORTED when q, the cache, out or lse is not on 16 bytes, a
  * stride is not a multiple of 8 elements (or is beyond 2^36), or is 0 for a
  * dimension larger than 1; or when the key tiles of the call could pass 2^31
- * (B * kv_heads * T / (256 / G) * table_width * page_size / 128). */
+ * (B * kv_heads * T / (256 / G) * table_width * page_size / 64). */
 typedef struct {
     spec_tree_rows q;
     spec_tree_cache cache;

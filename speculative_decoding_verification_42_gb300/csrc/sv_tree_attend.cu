@@ -4,7 +4,7 @@
 // For a key head the query rows of one sequence are its nodes times the G
 // query heads that share the head: out[r] = sum_k p[r][k] V[k] / sum_k p[r][k],
 // p = exp(scale q[r] . K[k]) over the keys row r sees.  One pass over the keys
-// with the running maximum m and sum l of each row: a tile of KT keys gives
+// with the running maximum m and sum l of each row: a tile of 64 keys gives
 // S = Q K^T (tensor cores, fp32), p = 2^(c S - c m) with c = scale log2(e),
 // l += sum p and O += P V (tensor cores, P rounded to the 16-bit type, O fp32
 // in tensor memory); when m grows by more than 2^8 would allow, O and l are
@@ -25,14 +25,16 @@
 //  * A CTA has a scheduling warp (it walks the range and hands the others one
 //    segment of an item at a time, which keeps that state out of their
 //    registers), two producer warps (tensor-map copies of whole pages into
-//    rings of 128-byte-swizzled key and value tiles), an MMA warp and one or
-//    two softmax warpgroups, a thread per row.  With heads up
-//    to 128 elements two streams of (S, O) share tensor memory's 512 columns:
-//    an item of one row tile gives its even key tiles to one and its odd ones
-//    to the other (own m, l, O; joined at the end), an item of two row tiles
-//    gives each stream a row tile and reads the keys once for both; either way
-//    one stream's exponentials hide behind the other's MMAs.  Larger heads
-//    fill tensor memory with one stream of 64-key tiles.
+//    rings of 128-byte-swizzled key and value tiles), two MMA issuers (scores,
+//    values) and one or two softmax warpgroups, a thread per row.
+//  * A stream (an O in tensor memory and its warpgroup) has two buffers for the
+//    scores of a 64-key tile: while the warpgroup turns one into probabilities,
+//    which take the place of its scores, the MMAs fill the other, so neither
+//    waits for the other's round trip.  Heads up to 128
+//    elements have two streams: an item of one row tile gives its even key
+//    tiles to one and its odd ones to the other (own m, l, O; joined at the
+//    end), an item of two row tiles gives each stream a row tile and reads the
+//    keys once for both.  Larger heads fill tensor memory with one stream.
 //
 // What a row does not see must not touch it, whatever it holds: scores are
 // replaced by -inf before the maximum, but P V multiplies hidden values by a
@@ -43,6 +45,7 @@
 #include <math.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "sv_tcgen.cuh"
 #include "sv_tree.cuh"
@@ -58,20 +61,19 @@ constexpr uint32_t ATT_WAIT_POLLS = 1u << 17;  // limit of a wait: some seconds 
 constexpr uint32_t ATT_STALL_POLLS = 4096;    // SPEC_FAULT_STALL_STREAM
 constexpr float ATT_LAZY = 8.f;               // log2 growth of the maximum that O takes unscaled
 
+constexpr int ATT_KT = 64;                    // keys of a tile
+constexpr int ATT_STAGES = 11;                // most stages of a ring
+
 template <int DP>
 struct Att {                                  // DP: head size rounded up to 64
     static constexpr int NH = DP / 64;        // 64-column (128-byte) boxes of a row
     static constexpr int NS = DP <= 128 ? 2 : 1;     // streams (softmax warpgroups)
-    static constexpr int KT = DP <= 128 ? 128 : 64;  // keys per tile
-    static constexpr int UNIT = KT * DP * 2;         // bytes of a K or V tile
-    static constexpr int QB = ATT_ROWS * DP * 2;     // bytes of a row tile of Q
-    static constexpr int STAGES = (ATT_SMEM - 1024 - ATT_MISC - NS * QB) / UNIT;
-    static constexpr int KS = (STAGES + 1) / 2, VS = STAGES / 2;  // of them for keys, for values
-    static constexpr int SMEM = 1024 + NS * QB + STAGES * UNIT + ATT_MISC;
-    static constexpr int THREADS = 128 + 128 * NS;
-    __host__ __device__ static constexpr uint32_t s_col(int s) { return 128u * s; }
+    static constexpr int UNIT = ATT_KT * DP * 2;     // bytes of a K or V tile
+    static constexpr int ROOM = ATT_SMEM - 1024 - ATT_MISC;  // bytes for Q and the rings
+    static constexpr int THREADS = 160 + 128 * NS;   // four warps, the softmax warpgroups, one warp more
+    __host__ __device__ static constexpr uint32_t s_col(int s, int buf) { return 128u * s + 64u * buf; }
     __host__ __device__ static constexpr uint32_t o_col(int s) { return NS == 2 ? 256u + 128u * s : 128u; }
-    static_assert(STAGES >= 4 && SMEM <= ATT_SMEM, "the ring fits");
+    static_assert((ROOM - NS * ATT_ROWS * DP * 2) / UNIT >= 4, "the rings fit");
 };
 
 // one segment: the key tiles tile0 .. tile0 + nt - 1 of an item (nt = 0: the range's end)
@@ -87,20 +89,23 @@ struct __align__(16) AttSeg {
 };
 
 struct __align__(16) AttMisc {
-    uint64_t k_full[8], k_empty[8];  // key tiles: copied; read by the MMAs
-    uint64_t v_full[8], v_empty[8];  // value tiles
-    uint64_t v_clean[8];             // a masked value tile may meet the MMAs
+    uint64_t k_full[ATT_STAGES], k_empty[ATT_STAGES];  // key tiles: copied; read by the MMAs
+    uint64_t v_full[ATT_STAGES], v_empty[ATT_STAGES];  // value tiles
+    uint64_t v_clean[ATT_STAGES];    // a masked value tile may meet the MMAs
     uint64_t q_full[2], q_empty[2];
-    uint64_t s_full[2];            // scores of the stream's unit are in tensor memory
-    uint64_t p_ready[2];           // its probabilities are (and O is scaled)
+    uint64_t s_full[2][2];         // [stream][buffer] the unit's scores are in tensor memory
+    uint64_t p_ready[2][2];        // its probabilities are (and O is scaled)
+    uint64_t pv_done[2][2];        // its P V is complete
     uint64_t o_full[2], o_empty[2];  // the segment's O is complete; has been read
     uint64_t ml_full, ml_empty;    // stream 1's (m, l) for the join
     uint64_t seg_full[ATT_SEGS], seg_empty[ATT_SEGS];
-    uint64_t drain;
+    uint64_t drain[2];
     AttSeg seg[ATT_SEGS];
-    uint32_t nf[8][4];             // (masked) value rows of the tile with non-finite elements
-    float2 ml[ATT_ROWS];
-    int32_t scan[16];
+    uint32_t nf[ATT_STAGES][2];    // (masked) value rows of the tile with non-finite elements
+    union {
+        float2 ml[ATT_ROWS];       // stream 1's (m, l) of a row
+        int32_t scan[16];          // before the roles part: the warps' sums of costs
+    };
     int32_t first, first_b;        // the range's first sequence, and its cost before the range
     uint32_t tmem;
     int32_t failed;
@@ -117,7 +122,7 @@ struct AttGeom {
 
 // The ranges are equal in cost, not in tiles: an item costs its key tiles and
 // ATT_ITEM_COST more (its first scores, its masked tile and its output).
-constexpr int ATT_ITEM_COST = 1;
+constexpr int ATT_ITEM_COST = 2;
 
 // keys that some row of item `rp` of a sequence sees: a chain's rows see
 // nothing past their last node
@@ -125,20 +130,18 @@ __device__ __forceinline__ int att_limit(const TreeAttendParams& p, const AttGeo
 {
     return ctx + (p.mask ? n : min(n, (rp + 1) * g.group));
 }
-template <int KT>
 __device__ __forceinline__ int att_cost(const TreeAttendParams& p, const AttGeom& g, int ctx, int n, int rp)
 {
-    return (att_limit(p, g, ctx, n, rp) + KT - 1) / KT + ATT_ITEM_COST;
+    return (att_limit(p, g, ctx, n, rp) + ATT_KT - 1) / ATT_KT + ATT_ITEM_COST;
 }
 // cost of all items of one key head of a sequence
-template <int KT>
 __device__ __forceinline__ int att_head_cost(const TreeAttendParams& p, const AttGeom& g, int ctx, int n)
 {
-    if (n <= g.group) return n ? att_cost<KT>(p, g, ctx, n, 0) : 0;
+    if (n <= g.group) return n ? att_cost(p, g, ctx, n, 0) : 0;
     const int nrp = (n + g.group - 1) / g.group;
-    if (p.mask) return nrp * att_cost<KT>(p, g, ctx, n, 0);
+    if (p.mask) return nrp * att_cost(p, g, ctx, n, 0);
     int t = 0;
-    for (int rp = 0; rp < nrp; ++rp) t += att_cost<KT>(p, g, ctx, n, rp);
+    for (int rp = 0; rp < nrp; ++rp) t += att_cost(p, g, ctx, n, rp);
     return t;
 }
 
@@ -159,7 +162,6 @@ struct AttSplit {
 };
 
 // the segments of a CTA: parts of items, in order of (key head, sequence, group)
-template <int KT>
 struct AttIter {
     int pos, end;               // cost positions in the order of all items
     int b, hk, rp;              // the item
@@ -175,7 +177,7 @@ struct AttIter {
         t0 = rp * g.group;
         ntok = min(g.group, n - t0);
         limit = att_limit(p, g, ctx, n, rp);
-        ntiles = (limit + KT - 1) / KT;
+        ntiles = (limit + ATT_KT - 1) / ATT_KT;
         tile0 = max(pos - at - ATT_ITEM_COST, 0);
         tile1 = min(end - at - ATT_ITEM_COST, ntiles);
     }
@@ -197,7 +199,7 @@ struct AttIter {
         load_seq(p);
         rp = 0;
         if (n > g.group)
-            for (int t; off >= (t = att_cost<KT>(p, g, ctx, n, rp)); ++rp) off -= t;
+            for (int t; off >= (t = att_cost(p, g, ctx, n, rp)); ++rp) off -= t;
         at = pos - off;
         load_item(p, g);
         if (tile0 >= tile1) next(p, g);
@@ -248,7 +250,9 @@ struct AttWork {
     unsigned* n_joins;  // their number; back at 0 after it
     unsigned* n_done;   // its CTAs that are done
     unsigned* err;
-    int32_t page_box;   // tokens of one copied box: min(page, KT)
+    int32_t page_box;   // tokens of one copied box: min(page, ATT_KT)
+    int32_t k_stages, v_stages;
+    int32_t q_rows;     // rows of Q a buffer holds, a multiple of 8 (the MMA's other rows are never used)
     int32_t q_box;      // nodes of one copied box of Q
     int32_t stall;
 };
@@ -288,10 +292,9 @@ __device__ __forceinline__ bool att_nonfinite(uint16_t h)
 }
 
 // the segment's first tile that some row sees only in part
-template <int KT>
 __device__ __forceinline__ int att_first_masked(const AttSeg& sg)
 {
-    return max(0, sg.mask_from / KT - sg.tile0);
+    return max(0, sg.mask_from / ATT_KT - sg.tile0);
 }
 
 // zeroes the non-finite ones of a word's two values; true when there was one
@@ -309,20 +312,20 @@ __device__ __forceinline__ bool clean_word(uint32_t& v)
 // that both warpgroups read is shared between them.  Eight lanes per 128-byte
 // row of a box.
 template <bool F16, int DP>
-__device__ __forceinline__ void att_clean(AttMisc& ms, unsigned char* v_smem, uint32_t st, int kb, int from, int end,
+__device__ __forceinline__ void att_clean(AttMisc& ms, unsigned char* tile, uint32_t st, int kb, int from, int end,
                                           bool shared, int s, int quarter, int lane)
 {
     using A = Att<DP>;
-    const int per = shared ? A::KT / 8 : A::KT / 4, r0 = ((shared ? s * 4 : 0) + quarter) * per;
+    const int per = shared ? ATT_KT / 8 : ATT_KT / 4, r0 = ((shared ? s * 4 : 0) + quarter) * per;
     uint32_t bits = 0;
-#pragma unroll 4
+#pragma unroll 2
     for (int i = 0; i < per; i += 4) {
         const int r = r0 + i + (lane >> 3), key = kb + r;
         bool found = false;
         if (key >= from) {
 #pragma unroll
             for (int h = 0; h < A::NH; ++h) {
-                uint4* a = (uint4*)(v_smem + st * A::UNIT + (h * A::KT + r) * 128) + (lane & 7);
+                uint4* a = (uint4*)(tile + (h * ATT_KT + r) * 128) + (lane & 7);
                 if (key >= end) {
                     *a = make_uint4(0, 0, 0, 0);
                     continue;
@@ -340,19 +343,19 @@ __device__ __forceinline__ void att_clean(AttMisc& ms, unsigned char* v_smem, ui
             if ((v >> (8 * j)) & 0xFFu) bits |= 1u << (i + j);
     }
     fence_async_smem();
-    if (lane < per / 16) ((uint16_t*)ms.nf[st])[r0 / 16 + lane] = (uint16_t)(bits >> (16 * lane));
+    if (lane < per / 8) ((uint8_t*)ms.nf[st])[r0 / 8 + lane] = (uint8_t)(bits >> (8 * lane));
     __syncwarp();
     if (lane == 0) mbar_arrive_n(&ms.v_clean[st], A::NS == 2 && !shared ? 2 : 1);
 }
 
-// O += the non-finite values of the keys kb + i whose bits i are set in rows' words
-template <bool F16, int KT>
-__device__ __noinline__ void att_add_nonfinite(const TreeAttendParams& p, uint4 rows, int b, int hk, int kb,
-                                               uint32_t o_addr)
+// O += the non-finite values of the keys kb + i whose bits i are set in see0, see1
+template <bool F16>
+__device__ __noinline__ void att_add_nonfinite(const TreeAttendParams& p, uint32_t see0, uint32_t see1, int b, int hk,
+                                               int kb, uint32_t o_addr)
 {
 #pragma unroll 1
-    for (int y = 0; y < KT / 32; ++y) {
-        const uint32_t mine = y == 0 ? rows.x : y == 1 ? rows.y : y == 2 ? rows.z : rows.w;
+    for (int y = 0; y < 2; ++y) {
+        const uint32_t mine = y ? see1 : see0;
         for (uint32_t any = __reduce_or_sync(0xffffffffu, mine); any; any &= any - 1) {
             const int bit = __ffs(any) - 1, key = kb + 32 * y + bit;
             const int page = __ldg(p.table + (int64_t)b * p.s.width + (key >> p.s.page_log2));
@@ -383,13 +386,16 @@ __global__ void __launch_bounds__(Att<DP>::THREADS, 1)
 {
     using A = Att<DP>;
     using H = Half2<F16>;
-    constexpr int KT = A::KT, NS = A::NS, NH = A::NH, KS = A::KS, VS = A::VS;
+    constexpr int KT = ATT_KT, NS = A::NS, NH = A::NH;
+    const uint32_t KS = w.k_stages, VS = w.v_stages;
     extern __shared__ unsigned char att_raw[];
     const uint32_t raw = smem_u32(att_raw);
+    // tables, Q buffers, rings; Q's unused rows reach into the rings
     unsigned char* const q_smem = att_raw + (((raw + 1023u) & ~1023u) - raw);
-    unsigned char* const k_smem = q_smem + NS * A::QB;
+    const uint32_t q_bytes = w.q_rows * DP * 2;
+    unsigned char* const k_smem = q_smem + NS * q_bytes;
     unsigned char* const v_smem = k_smem + KS * A::UNIT;
-    AttMisc& ms = *reinterpret_cast<AttMisc*>(v_smem + VS * A::UNIT);
+    AttMisc& ms = *reinterpret_cast<AttMisc*>(q_smem + A::ROOM);
     const TreeAttendParams& p = w.p;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t limit = w.stall ? ATT_STALL_POLLS : ATT_WAIT_POLLS;
@@ -402,32 +408,36 @@ __global__ void __launch_bounds__(Att<DP>::THREADS, 1)
         tma_prefetch_map(&map_v);
     }
     if (warp == 0) tmem_alloc(&ms.tmem, ATT_TMEM_COLS);
-    if (tid == 32) {
-        for (int i = 0; i < KS; ++i) {
-            mbar_init(&ms.k_full[i], 1);
-            mbar_init(&ms.k_empty[i], 1);
+    if (warp == 1) {
+        if (lane < ATT_STAGES) {
+            mbar_init(&ms.k_full[lane], 1);
+            mbar_init(&ms.k_empty[lane], 1);
+            mbar_init(&ms.v_full[lane], 1);
+            mbar_init(&ms.v_empty[lane], 1);
+            mbar_init(&ms.v_clean[lane], 4 * NS);
         }
-        for (int i = 0; i < VS; ++i) {
-            mbar_init(&ms.v_full[i], 1);
-            mbar_init(&ms.v_empty[i], 1);
-            mbar_init(&ms.v_clean[i], 4 * NS);
+        if (lane < 2) {
+            mbar_init(&ms.q_full[lane], 1);
+            mbar_init(&ms.q_empty[lane], 1);
+            for (int j = 0; j < 2; ++j) {
+                mbar_init(&ms.s_full[lane][j], 1);
+                mbar_init(&ms.p_ready[lane][j], 4);
+                mbar_init(&ms.pv_done[lane][j], 1);
+            }
+            mbar_init(&ms.o_full[lane], 1);
+            mbar_init(&ms.o_empty[lane], 4);
         }
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&ms.q_full[i], 1);
-            mbar_init(&ms.q_empty[i], 1);
-            mbar_init(&ms.s_full[i], 1);
-            mbar_init(&ms.p_ready[i], 4);
-            mbar_init(&ms.o_full[i], 1);
-            mbar_init(&ms.o_empty[i], 4);
+        if (lane < ATT_SEGS) {
+            mbar_init(&ms.seg_full[lane], 1);
+            mbar_init(&ms.seg_empty[lane], 4 + 4 * NS);
         }
-        for (int i = 0; i < ATT_SEGS; ++i) {
-            mbar_init(&ms.seg_full[i], 1);
-            mbar_init(&ms.seg_empty[i], 3 + 4 * NS);
+        if (lane == 0) {
+            mbar_init(&ms.ml_full, 4);
+            mbar_init(&ms.ml_empty, 4);
+            mbar_init(&ms.drain[0], 1);
+            mbar_init(&ms.drain[1], 1);
+            ms.failed = 0;
         }
-        mbar_init(&ms.ml_full, 4);
-        mbar_init(&ms.ml_empty, 4);
-        mbar_init(&ms.drain, 1);
-        ms.failed = 0;
         fence_barrier_init();
     }
     // ---- this CTA's range: a scan of the sequences' costs
@@ -438,7 +448,7 @@ __global__ void __launch_bounds__(Att<DP>::THREADS, 1)
         int sum = 0;
         for (int b = s0; b < s1; ++b) {
             const SeqLen l = tree_len(p.s, b);
-            sum += att_head_cost<KT>(p, w.g, l.ctx, l.n);
+            sum += att_head_cost(p, w.g, l.ctx, l.n);
         }
         int inc = sum;
 #pragma unroll
@@ -464,7 +474,7 @@ __global__ void __launch_bounds__(Att<DP>::THREADS, 1)
             int b = s0, off = in_head - before;
             for (;; ++b) {
                 const SeqLen l = tree_len(p.s, b);
-                const int t = att_head_cost<KT>(p, w.g, l.ctx, l.n);
+                const int t = att_head_cost(p, w.g, l.ctx, l.n);
                 if (off < t) break;
                 off -= t;
             }
@@ -478,7 +488,18 @@ __global__ void __launch_bounds__(Att<DP>::THREADS, 1)
     const uint32_t tmem = ms.tmem;
     bool ok = true;
     auto wait = [&](uint64_t* bar, uint32_t parity) {  // whole warp
-        ok = ok && __all_sync(0xffffffffu, att_wait(bar, parity & 1u, failed, limit));
+        if (!__all_sync(0xffffffffu, mbar_try_wait(bar, parity & 1u)))
+            ok = ok && __all_sync(0xffffffffu, att_wait(bar, parity & 1u, failed, limit));
+    };
+    auto until = [&](uint64_t* bar, uint32_t parity) {  // one thread
+        if (!mbar_try_wait(bar, parity & 1u)) ok = ok && att_wait(bar, parity & 1u, failed, limit);
+    };
+    // an MMA issuer that gave up: none of its MMAs is in flight when the CTA leaves
+    auto drained = [&](uint64_t* bar) {
+        if (ok) return;
+        ms.failed = 1;
+        umma_commit(bar);
+        mbar_wait_n(bar, 0, limit);
     };
     // the k-th segment; done with it
     auto segment = [&](uint32_t k) -> const AttSeg& {
@@ -494,7 +515,7 @@ __global__ void __launch_bounds__(Att<DP>::THREADS, 1)
         // ---------------- scheduler
         const AttSplit split(total, gridDim.x);
         const bool busy = (int)blockIdx.x < split.ctas;
-        AttIter<KT> it;
+        AttIter it;
         it.start(p, w.g, busy ? split.start(blockIdx.x) : 0, busy ? split.start(blockIdx.x + 1) : 0, head0,
                  ms.first_b, ms.first);
         for (uint32_t k = 0; ok; ++k) {
@@ -568,11 +589,11 @@ __global__ void __launch_bounds__(Att<DP>::THREADS, 1)
                     cur = ahead;
                     ahead = ids(blk + 1);
                 }
-                if (n >= stages) wait(&empty[st], round - 1);
+                wait(&empty[st], round + 1);  // at once in the first round
                 if (!ok) break;
                 const int boxes = (min(KT, last_key - kb) + w.page_box - 1) / w.page_box;
                 if (lane == 0) mbar_arrive_expect_tx(&full[st], (uint32_t)(boxes * w.page_box * 128 * NH));
-                // a tile's pages (at most 16) lie in one block
+                // a tile's pages (at most 8) lie in one block
                 const int key = kb + lane * w.page_box;
                 const int page = __shfl_sync(0xffffffffu, cur, (key >> p.s.page_log2) & 31);
                 unsigned char* dst = ring + st * A::UNIT + lane * w.page_box * 128;
@@ -584,13 +605,13 @@ __global__ void __launch_bounds__(Att<DP>::THREADS, 1)
                 if (t > 0 || !is_k) continue;
                 for (int s = 0; s <= sg.dual; ++s) {
                     const uint32_t qb = qi % NS;
-                    if (qi >= NS) wait(&ms.q_empty[qb], qi / NS - 1);
+                    wait(&ms.q_empty[qb], qi / NS + 1);
                     if (!ok) break;
                     ++qi;
                     if (lane == 0) {
                         mbar_arrive_expect_tx(&ms.q_full[qb], (uint32_t)(w.q_box * w.g.G * 128 * NH));
                         for (int h = 0; h < NH; ++h)
-                            tma_4d(q_smem + qb * A::QB + h * ATT_ROWS * 128, &map_q, h * 64, hk * w.g.G,
+                            tma_4d(q_smem + qb * q_bytes + h * w.q_rows * 128, &map_q, h * 64, hk * w.g.G,
                                    sg.t0 + s * w.g.tpt, b, &ms.q_full[qb]);
                     }
                 }
@@ -609,93 +630,123 @@ __global__ void __launch_bounds__(Att<DP>::THREADS, 1)
             for (uint32_t i = q0; i < qi; ++i) mbar_wait_n(&ms.q_full[i % NS], (i / NS) & 1, limit);
         }
     } else if (warp == 1) {
-        // ---------------- MMA issuer: the whole warp waits, one lane issues
-        constexpr uint32_t ID_S = umma_idesc(F16, false, ATT_ROWS, KT);
-        constexpr uint32_t ID_O = umma_idesc(F16, true, ATT_ROWS, DP);
-        uint32_t base = 0, qi = 0, cleaned = 0;  // cleaned: bit per stage, phases of v_clean so far
-        uint32_t n_unit[2] = {0, 0}, n_seg[2] = {0, 0};  // units and segments of each stream so far
-        // descriptors: Q and K are K-major with 8-row groups 1024 bytes apart; V is
-        // N-major, 64-column boxes KT rows apart, 8-row groups 1024 bytes apart
-        const uint64_t q_desc = umma_desc(smem_u32(q_smem), 16, 1024), k_desc = umma_desc(smem_u32(k_smem), 16, 1024);
-        const uint64_t v_desc = umma_desc(smem_u32(v_smem), KT * 128, 1024);
-        for (uint32_t k = 0; ok; ++k) {
-            const AttSeg& sg = segment(k);
-            const int nt = sg.nt;
-            if (!ok || nt == 0) break;
-            const bool dual = sg.dual != 0;
-            const int units = dual ? 2 * nt : nt, masked = att_first_masked<KT>(sg);
-            release(k);
-            auto scores = [&](int u) {
-                const int s = NS == 2 ? u & 1 : 0, t = dual ? u >> 1 : u;
-                const uint32_t i = base + t, st = i % KS;
-                const uint32_t q = qi + (dual ? s : 0), qb = q % NS;
-                if (!dual || s == 0) wait(&ms.k_full[st], i / KS);
-                if (t == 0 && (dual || u == 0)) wait(&ms.q_full[qb], q / NS);
-                if (!ok) return;
-                tmem_fence_after();
-                if (elect_one()) {
-                    const uint64_t a = q_desc + qb * (A::QB / 16), b = k_desc + st * (A::UNIT / 16);
+        // ---------------- MMA issuer of the scores: one thread.  Each of its steps
+        // (a poll, a commit, an MMA) takes some 50 cycles, and so do those of the
+        // values' issuer: as two threads they keep the tensor cores busy between them.
+        if (lane == 0) {
+            constexpr uint32_t ID_S = umma_idesc(F16, false, ATT_ROWS, KT);
+            const int dk = p.s.D / 16;  // k-steps
+            uint32_t st = 0, round = 0, qi = 0, n[2] = {0, 0};  // key ring; row tiles of Q; units of each stream
+            // Q and K are K-major with 8-row groups 1024 bytes apart
+            const uint64_t q_desc = umma_desc(smem_u32(q_smem), 16, 1024);
+            const uint64_t k_desc = umma_desc(smem_u32(k_smem), 16, 1024);
+            const uint32_t q_half = w.q_rows * 8;  // a box of Q, in 16 bytes
+            for (uint32_t k = 0; ok; ++k) {
+                const AttSeg& sg = ms.seg[k % ATT_SEGS];
+                until(&ms.seg_full[k % ATT_SEGS], k / ATT_SEGS);
+                if (!ok || sg.nt == 0) break;
+                const int nt = sg.nt;
+                const bool dual = sg.dual != 0;
+                mbar_arrive(&ms.seg_empty[k % ATT_SEGS]);
+                auto scores = [&](auto stream, int t) {
+                    constexpr int s = decltype(stream)::value;
+                    const uint32_t q = qi + (dual ? s : 0), qb = q % NS, buf = n[s] & 1;
+                    if (!dual || s == 0) until(&ms.k_full[st], round);
+                    if (t == 0) until(&ms.q_full[qb], q / NS);
+                    // the buffer's last probabilities have met their values
+                    if (n[s] >= 2) until(&ms.pv_done[s][buf], (n[s] >> 1) - 1);
+                    if (!ok) return;
+                    tmem_fence_after();
+                    const uint64_t a = q_desc + qb * (q_bytes / 16), b = k_desc + st * (A::UNIT / 16);
+                    if (dk == DP / 16) {
 #pragma unroll
-                    for (int x = 0; x < DP / 16; ++x)
-                        umma_ss(tmem + A::s_col(s), a + ((x / 4) * ATT_ROWS * 128 + (x % 4) * 32) / 16,
-                                b + ((x / 4) * KT * 128 + (x % 4) * 32) / 16, ID_S, x > 0);
-                    umma_commit(&ms.s_full[s]);
-                    if (!dual || s == 1) umma_commit(&ms.k_empty[st]);
-                    if (t == nt - 1) umma_commit(&ms.q_empty[qb]);
-                }
-                __syncwarp();
-            };
-            auto values = [&](int u) {
-                const int s = NS == 2 ? u & 1 : 0, t = dual ? u >> 1 : u;
-                const uint32_t i = base + t, st = i % VS;
-                const bool first = u < NS;
-                if (!dual || s == 0) {
-                    if (t >= masked) {
-                        wait(&ms.v_clean[st], cleaned >> st);
-                        cleaned ^= 1u << st;
+                        for (int x = 0; x < DP / 16; ++x)
+                            umma_ss(tmem + A::s_col(s, buf), a + (x / 4) * q_half + (x % 4) * 2,
+                                    b + ((x / 4) * KT * 128 + (x % 4) * 32) / 16, ID_S, x > 0);
                     } else {
-                        wait(&ms.v_full[st], i / VS);
+                        for (int x = 0; x < dk; ++x)
+                            umma_ss(tmem + A::s_col(s, buf), a + (x / 4) * q_half + (x % 4) * 2,
+                                    b + ((x / 4) * KT * 128 + (x % 4) * 32) / 16, ID_S, x > 0);
                     }
+                    umma_commit(&ms.s_full[s][buf]);
+                    ++n[s];
+                    if (t == nt - 1) umma_commit(&ms.q_empty[qb]);
+                    if (!dual || s == 1) {
+                        umma_commit(&ms.k_empty[st]);
+                        if (++st == KS) st = 0, ++round;
+                    }
+                };
+                // stream s takes every tile (two row tiles, or one stream), or the tiles
+                // s, s + 2, ... (two streams on alternate tiles)
+                const int step = NS == 1 || dual ? 1 : 2;
+                for (int t = 0; ok && t < nt; t += step) {
+                    scores(std::integral_constant<int, 0>{}, t);
+                    if (NS == 2 && ok && t + step - 1 < nt) scores(std::integral_constant<int, NS - 1>{}, t + step - 1);
                 }
-                if (first && n_seg[s] > 0) wait(&ms.o_empty[s], n_seg[s] - 1);
-                wait(&ms.p_ready[s], n_unit[s]);
-                if (!ok) return;
-                ++n_unit[s];
-                if (first) ++n_seg[s];
-                tmem_fence_after();
-                if (elect_one()) {
+                qi += dual ? 2 : 1;
+            }
+            drained(&ms.drain[0]);
+        }
+        __syncwarp();
+    } else if (warp == 4 + 4 * NS) {
+        // ---------------- MMA issuer of the values: one thread
+        if (lane == 0) {
+            const uint32_t id_o = umma_idesc(F16, true, ATT_ROWS, 0) | ((uint32_t)(p.s.D >> 3) << 17);
+            uint32_t st = 0, round = 0, n[2] = {0, 0}, segs[2] = {0, 0};  // value ring; units and segments of each stream
+            uint32_t cleaned = 0;  // bit per stage, phases of v_clean so far
+            // V is N-major, 64-column boxes KT rows apart, 8-row groups 1024 bytes apart
+            const uint64_t v_desc = umma_desc(smem_u32(v_smem), KT * 128, 1024);
+            for (uint32_t k = 0; ok; ++k) {
+                const AttSeg& sg = ms.seg[k % ATT_SEGS];
+                until(&ms.seg_full[k % ATT_SEGS], k / ATT_SEGS);
+                if (!ok || sg.nt == 0) break;
+                const int nt = sg.nt, masked = att_first_masked(sg);
+                const bool dual = sg.dual != 0;
+                mbar_arrive(&ms.seg_empty[k % ATT_SEGS]);
+                const int step = NS == 1 || dual ? 1 : 2;
+                auto values = [&](auto stream, int t) {
+                    constexpr int s = decltype(stream)::value;
+                    const uint32_t buf = n[s] & 1;
+                    const bool first = t < step;
+                    if (!dual || s == 0) {
+                        if (t >= masked) {
+                            until(&ms.v_clean[st], cleaned >> st);
+                            cleaned ^= 1u << st;
+                        } else {
+                            until(&ms.v_full[st], round);
+                        }
+                    }
+                    if (first && segs[s] > 0) until(&ms.o_empty[s], segs[s] - 1);
+                    until(&ms.p_ready[s][buf], n[s] >> 1);
+                    if (!ok) return;
+                    tmem_fence_after();
                     const uint64_t b = v_desc + st * (A::UNIT / 16);
 #pragma unroll
                     for (int x = 0; x < KT / 16; ++x)
-                        umma_ts(tmem + A::o_col(s), tmem + A::s_col(s) + x * 8, b + x * 128, ID_O, !first || x > 0);
-                    if (!dual || s == 1) umma_commit(&ms.v_empty[st]);
-                    if (u + NS >= units) umma_commit(&ms.o_full[s]);
+                        umma_ts(tmem + A::o_col(s), tmem + A::s_col(s, buf) + x * 8, b + x * 128, id_o,
+                                !first || x > 0);
+                    umma_commit(&ms.pv_done[s][buf]);
+                    ++n[s];
+                    segs[s] += first;
+                    if (t + step >= nt) umma_commit(&ms.o_full[s]);
+                    if (!dual || s == 1) {
+                        umma_commit(&ms.v_empty[st]);
+                        if (++st == VS) st = 0, ++round;
+                    }
+                };
+                for (int t = 0; ok && t < nt; t += step) {
+                    values(std::integral_constant<int, 0>{}, t);
+                    if (NS == 2 && ok && t + step - 1 < nt) values(std::integral_constant<int, NS - 1>{}, t + step - 1);
                 }
-                __syncwarp();
-            };
-            for (int u = 0; ok && u < min(NS, units); ++u) scores(u);
-            for (int u = 0; ok && u < units; ++u) {
-                values(u);
-                if (ok && u + NS < units) scores(u + NS);
             }
-            base += nt;
-            qi += dual ? 2 : 1;
+            drained(&ms.drain[1]);
         }
-        if (!ok) {
-            // no MMA is in flight when the CTA leaves (one lane issued them all: the
-            // election takes the same lane of a full warp every time)
-            if (elect_one()) {
-                ms.failed = 1;
-                umma_commit(&ms.drain);
-                mbar_wait_n(&ms.drain, 0, limit);
-            }
-            __syncwarp();
-        }
+        __syncwarp();
     } else {
         // ---------------- softmax: warpgroup s, thread = row
         const int s = (warp - 4) >> 2, row = (warp & 3) * 32 + lane;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-        const uint32_t o_addr = tmem + A::o_col(s) + lanes, s_addr = tmem + A::s_col(s) + lanes;
+        const uint32_t o_addr = tmem + A::o_col(s) + lanes;
         const float c = p.scale * 1.4426950408889634f;
         const int T = p.s.T, Hq = p.s.Hq, D = p.s.D, G = w.g.G;
         // nodes that do not exist: zero rows
@@ -722,68 +773,67 @@ __global__ void __launch_bounds__(Att<DP>::THREADS, 1)
             const int rows = min(w.g.tpt, sg.t0 + sg.ntok - t_first) * G;
             const bool active = (warp & 3) * 32 < rows;
             float m = -INFINITY, l = 0.f;
-            int masked = att_first_masked<KT>(sg);  // later: the first masked tile not counted in `cleaned`
+            int masked = att_first_masked(sg);  // later: the first masked tile not counted in `cleaned`
 
-            for (int tile = dual ? 0 : s; tile < nt && ok; tile += dual ? 1 : NS) {
-                const bool part = tile >= masked;
+            const int stride = dual ? 1 : NS;
+            for (int tile = dual ? 0 : s; tile < nt && ok; tile += stride) {
+                const bool part = tile >= masked;  // some row sees the tile only in part
                 const int kb = (sg.tile0 + tile) * KT;
-                uint32_t see[KT / 32];
+                const uint32_t buf = n_unit & 1;
+                const uint32_t s_addr = tmem + A::s_col(s, buf) + lanes;
+                uint32_t see0 = 0, see1 = 0;
                 if (part) {
                     // on their way while the scores are computed
                     const int t = min(t_first + row / G, sg.n - 1);  // rows past the last are never stored
-#pragma unroll
-                    for (int y = 0; y < KT / 32; ++y) see[y] = att_sees(p, sg.b, t, sg.ctx, sg.n, kb + 32 * y);
+                    see0 = att_sees(p, sg.b, t, sg.ctx, sg.n, kb);
+                    see1 = att_sees(p, sg.b, t, sg.ctx, sg.n, kb + 32);
                 }
-                wait(&ms.s_full[s], n_unit);
-                ++n_unit;
+                wait(&ms.s_full[s][buf], n_unit >> 1);
                 if (!ok) break;
                 tmem_fence_after();
+                uint32_t vst = 0;
                 if (part) {
                     // phases of v_clean of the tiles before this one (the other stream's)
                     for (; masked < tile; ++masked) cleaned ^= 1u << ((base + masked) % VS);
                     ++masked;
-                    const uint32_t vi = base + tile, vst = vi % VS;
-                    wait(&ms.v_full[vst], vi / VS);
+                    vst = (base + tile) % VS;
+                    wait(&ms.v_full[vst], (base + tile) / VS);
                     if (!ok) break;
-                    att_clean<F16, DP>(ms, v_smem, vst, kb, sg.mask_from, sg.ctx + sg.n, dual, s, warp & 3, lane);
+                    att_clean<F16, DP>(ms, v_smem + vst * A::UNIT, vst, kb, sg.mask_from, sg.ctx + sg.n, dual, s,
+                                       warp & 3, lane);
                     wait(&ms.v_clean[vst], cleaned >> vst);
                     if (!ok) break;
                     cleaned ^= 1u << vst;
                 }
                 if (active) {
-                    // hidden scores become -inf in tensor memory; then the row's maximum,
-                    // found by the loads, and its exponentials.  Loops and two passes over
-                    // tensor memory keep the code and the registers few: the first pass of
-                    // a CTA through every path waits for its instructions.
+                    // the row's scores and their maximum; hidden ones become -inf
+                    uint32_t x[KT];
+                    float top;
                     if (part) {
-#pragma unroll 1
-                        for (int y = 0; y < KT / 32; ++y) {
-                            const uint32_t sees = y == 0 ? see[0] : y == 1 ? see[1] : y == 2 ? see[KT / 32 - 2]
-                                                                                          : see[KT / 32 - 1];
-                            uint32_t x[32];
-                            tmem_ld<32>(s_addr + 32 * y, x);
+                        tmem_ld<KT>(s_addr, x);
+                        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                            for (int i = 0; i < 32; ++i)
-                                if (!((sees >> i) & 1u)) x[i] = 0xFF800000u;
-                            tmem_st<32>(s_addr + 32 * y, x);
+                        for (int i = 0; i < KT; ++i) {
+                            if (!(((i < 32 ? see0 : see1) >> (i & 31)) & 1u)) x[i] = 0xFF800000u;
+                            mx[i & 3] = fmaxf(mx[i & 3], __uint_as_float(x[i]));
                         }
-                        tmem_wait_st();
-                    }
-                    float top = -INFINITY;
-#pragma unroll 1
-                    for (int y = 0; y < KT; y += 64) {
-                        uint32_t x[64];
-                        top = fmaxf(top, tmem_ld_max<64>(s_addr + y, x));
+                        top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                    } else {
+                        top = tmem_ld_max<KT>(s_addr, x);
                     }
                     // O and l stay in units of the old maximum while the new one is
-                    // less than 2^8 above it: p then stays below 2^8.  Every earlier
-                    // P V of the stream is complete: the scores were issued after it.
+                    // less than 2^8 above it: p then stays below 2^8
                     const bool grow = top * c > m * c + ATT_LAZY || (m == -INFINITY && top > m);
                     if (__any_sync(0xffffffffu, grow)) {
                         const float f = grow ? ex2_fast((m - top) * c) : 1.f;
                         if (grow) m = top;
                         l *= f;
-                        if (tile >= (dual ? 1 : NS)) {
+                        if (tile >= stride) {
+                            // the P V before this unit's has to be complete (those before it
+                            // are: this buffer's scores were issued after them)
+                            wait(&ms.pv_done[s][(n_unit - 1) & 1], (n_unit - 1) >> 1);
+                            if (!ok) break;
+                            tmem_fence_after();
 #pragma unroll 1
                             for (int d = 0; d < D; d += 16) {
                                 uint32_t o[16];
@@ -797,42 +847,37 @@ __global__ void __launch_bounds__(Att<DP>::THREADS, 1)
                     const float mc = m == -INFINITY ? 0.f : m * c;
                     const uint64_t c2 = pack2(c, c), mc2 = pack2(-mc, -mc);
                     uint64_t sum[2] = {0ull, 0ull};  // two pairs of partial sums
-#pragma unroll 1
-                    for (int y = 0; y < KT; y += 64) {
-                        uint32_t x[64];
-                        tmem_ld<64>(s_addr + y, x);
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) {
-                            float2 e = unpack2(fma2(pack2u(x[2 * i], x[2 * i + 1]), c2, mc2));
-                            e.x = ex2_fast(e.x);
-                            e.y = ex2_fast(e.y);
-                            sum[i & 1] = add2(sum[i & 1], pack2(e.x, e.y));
-                            x[i] = H::pack(e.x, e.y);
-                        }
-                        tmem_st<32>(s_addr + y / 2, *reinterpret_cast<uint32_t(*)[32]>(&x));
+                    for (int i = 0; i < KT / 2; ++i) {
+                        float2 e = unpack2(fma2(pack2u(x[2 * i], x[2 * i + 1]), c2, mc2));
+                        e.x = ex2_fast(e.x);
+                        e.y = ex2_fast(e.y);
+                        sum[i & 1] = add2(sum[i & 1], pack2(e.x, e.y));
+                        x[i] = H::pack(e.x, e.y);
                     }
+                    tmem_st<32>(s_addr, *reinterpret_cast<uint32_t(*)[32]>(&x));
                     const float2 sums = unpack2(add2(sum[0], sum[1]));
                     l += sums.x + sums.y;
                     tmem_wait_st();
                 }
-                uint32_t some = 0;  // seen keys with non-finite values
+                bool some = false;  // seen keys with non-finite values
                 if (part) {
-#pragma unroll
-                    for (int y = 0; y < KT / 32; ++y)
-                        some |= see[y] &= *(volatile uint32_t*)&ms.nf[(base + tile) % VS][y];
+                    const volatile uint32_t* nf = ms.nf[vst];
+                    see0 &= nf[0];
+                    see1 &= nf[1];
+                    some = active && (see0 | see1);
                 }
                 tmem_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&ms.p_ready[s]);
-                if (part && __any_sync(0xffffffffu, active && some)) {
+                if (lane == 0) mbar_arrive(&ms.p_ready[s][buf]);
+                if (part && __any_sync(0xffffffffu, some)) {
                     // rare: once P V is done (it saw zeros there), O += those values
-                    const uint32_t vi = base + tile;
-                    wait(&ms.v_empty[vi % VS], vi / VS);
+                    wait(&ms.pv_done[s][buf], n_unit >> 1);
                     if (!ok) break;
                     tmem_fence_after();
-                    att_add_nonfinite<F16, KT>(p, make_uint4(see[0], see[1], see[KT / 32 - 2], see[KT / 32 - 1]), sg.b,
-                                               sg.hk, kb, o_addr);
+                    att_add_nonfinite<F16>(p, see0, see1, sg.b, sg.hk, kb, o_addr);
                 }
+                ++n_unit;
             }
             for (; masked < nt; ++masked) cleaned ^= 1u << ((base + masked) % VS);
             base += nt;
@@ -1112,13 +1157,18 @@ static cudaError_t att_launch(AttWork w, int num_sms, cudaStream_t s)
     using A = Att<DP>;
     static DeviceOnce once;  // per device: the shared-memory opt-in
     cudaError_t e = cuda_once(once, nullptr, [](int, int*) {
-        return cudaFuncSetAttribute(k_tree_attend<F16, DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, A::SMEM);
+        return cudaFuncSetAttribute(k_tree_attend<F16, DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, ATT_SMEM);
     });
     if (e != cudaSuccess) return e;
     const TreeShape& sh = w.p.s;
     w.g.group = A::NS * w.g.tpt;
-    w.page_box = min(1 << sh.page_log2, A::KT);
+    w.page_box = min(1 << sh.page_log2, ATT_KT);
     w.q_box = min(w.g.tpt, sh.T);
+    // what Q does not need is for the rings: few rows leave room for more tiles on their way
+    w.q_rows = (w.q_box * w.g.G + 7) / 8 * 8;
+    const int stages = (A::ROOM - A::NS * w.q_rows * DP * 2) / A::UNIT;
+    w.k_stages = min((stages + 1) / 2, ATT_STAGES);
+    w.v_stages = min(stages / 2, ATT_STAGES);
     CUtensorMap mq, mk, mv;
     const int64_t qd[3] = {sh.Hq, sh.T, sh.B}, qs[3] = {w.p.q.head, w.p.q.token, w.p.q.seq};
     const int64_t cd[3] = {sh.Hkv, 1 << sh.page_log2, sh.num_pages}, cs[3] = {w.p.c.head, w.p.c.token, w.p.c.page};
@@ -1126,7 +1176,7 @@ static cudaError_t att_launch(AttWork w, int num_sms, cudaStream_t s)
         !att_map(&mk, F16, w.p.c.k, sh.D, cd, cs, 1, w.page_box) ||
         !att_map(&mv, F16, w.p.c.v, sh.D, cd, cs, 1, w.page_box))
         return cudaErrorInvalidValue;
-    k_tree_attend<F16, DP><<<num_sms, A::THREADS, A::SMEM, s>>>(mq, mk, mv, w);
+    k_tree_attend<F16, DP><<<num_sms, A::THREADS, ATT_SMEM, s>>>(mq, mk, mv, w);
     if ((e = cudaGetLastError()) != cudaSuccess || num_sms == 1) return e;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute at[1];
@@ -1144,9 +1194,9 @@ static cudaError_t att_launch(AttWork w, int num_sms, cudaStream_t s)
 
 bool tree_attend_fits(const TreeShape& sh)
 {
-    const int64_t kt = sh.D <= 128 ? 128 : 64, group = (sh.D <= 128 ? 2 : 1) * (ATT_ROWS / (sh.Hq / sh.Hkv));
+    const int64_t group = (sh.D <= 128 ? 2 : 1) * (ATT_ROWS / (sh.Hq / sh.Hkv));
     const int64_t groups = (sh.T + group - 1) / group;
-    const int64_t tiles = (((int64_t)sh.width << sh.page_log2) + kt - 1) / kt + ATT_ITEM_COST;
+    const int64_t tiles = (((int64_t)sh.width << sh.page_log2) + ATT_KT - 1) / ATT_KT + ATT_ITEM_COST;
     return (double)sh.B * sh.Hkv * groups * tiles < 2147483648.0;
 }
 
