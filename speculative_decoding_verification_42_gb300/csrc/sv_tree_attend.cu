@@ -25,12 +25,13 @@
 //  * A CTA has a scheduling warp (it walks the range and hands the others one
 //    segment of an item at a time, which keeps that state out of their
 //    registers), two producer warps (tensor-map copies of whole pages into
-//    rings of 128-byte-swizzled key and value tiles), two MMA issuers (scores,
-//    values) and one or two softmax warpgroups, a thread per row.
+//    rings of 128-byte-swizzled key and value tiles), an MMA issuer and one or
+//    two softmax warpgroups, a thread per row.
 //  * A stream (an O in tensor memory and its warpgroup) has two buffers for the
-//    scores of a 64-key tile: while the warpgroup turns one into probabilities,
-//    which take the place of its scores, the MMAs fill the other, so neither
-//    waits for the other's round trip.  Heads up to 128
+//    scores of a 64-key tile; probabilities take the place of their scores.
+//    The values of one meet their probabilities while the warpgroup is at the
+//    other.  Heads up to 128 elements fill both with one MMA of 128 keys, which
+//    reads less shared memory than two of 64 (Q is read for each).  Heads up to 128
 //    elements have two streams: an item of one row tile gives its even key
 //    tiles to one and its odd ones to the other (own m, l, O; joined at the
 //    end), an item of two row tiles gives each stream a row tile and reads the
@@ -69,8 +70,9 @@ struct Att {                                  // DP: head size rounded up to 64
     static constexpr int NH = DP / 64;        // 64-column (128-byte) boxes of a row
     static constexpr int NS = DP <= 128 ? 2 : 1;     // streams (softmax warpgroups)
     static constexpr int UNIT = ATT_KT * DP * 2;     // bytes of a K or V tile
+    static constexpr int KB = NS;             // tiles of a block of keys: the N of the scores' MMAs is 64 KB
     static constexpr int ROOM = ATT_SMEM - 1024 - ATT_MISC;  // bytes for Q and the rings
-    static constexpr int THREADS = 160 + 128 * NS;   // four warps, the softmax warpgroups, one warp more
+    static constexpr int THREADS = 128 + 128 * NS;   // four warps, and the softmax warpgroups
     __host__ __device__ static constexpr uint32_t s_col(int s, int buf) { return 128u * s + 64u * buf; }
     __host__ __device__ static constexpr uint32_t o_col(int s) { return NS == 2 ? 256u + 128u * s : 128u; }
     static_assert((ROOM - NS * ATT_ROWS * DP * 2) / UNIT >= 4, "the rings fit");
@@ -93,20 +95,15 @@ struct __align__(16) AttMisc {
     uint64_t v_full[ATT_STAGES], v_empty[ATT_STAGES];  // value tiles
     uint64_t v_clean[ATT_STAGES];    // a masked value tile may meet the MMAs
     uint64_t q_full[2], q_empty[2];
-    uint64_t s_full[2][2];         // [stream][buffer] the unit's scores are in tensor memory
-    uint64_t p_ready[2][2];        // its probabilities are (and O is scaled)
-    uint64_t pv_done[2][2];        // its P V is complete
+    uint64_t s_full[2][2];         // [stream][buffer] scores are in tensor memory (a block's: buffer 0)
+    uint64_t p_ready[2][2];        // a tile's probabilities are (and O is scaled)
     uint64_t o_full[2], o_empty[2];  // the segment's O is complete; has been read
     uint64_t ml_full, ml_empty;    // stream 1's (m, l) for the join
     uint64_t seg_full[ATT_SEGS], seg_empty[ATT_SEGS];
-    uint64_t drain[2];
+    uint64_t drain;
     AttSeg seg[ATT_SEGS];
     uint32_t nf[ATT_STAGES][2];    // (masked) value rows of the tile with non-finite elements
-    union {
-        float2 ml[ATT_ROWS];       // stream 1's (m, l) of a row
-        int32_t scan[16];          // before the roles part: the warps' sums of costs
-    };
-    int32_t first, first_b;        // the range's first sequence, and its cost before the range
+    float2 ml[ATT_ROWS];           // stream 1's (m, l) of a row
     uint32_t tmem;
     int32_t failed;
 };
@@ -394,7 +391,7 @@ __global__ void __launch_bounds__(Att<DP>::THREADS, 1)
     unsigned char* const q_smem = att_raw + (((raw + 1023u) & ~1023u) - raw);
     const uint32_t q_bytes = w.q_rows * DP * 2;
     unsigned char* const k_smem = q_smem + NS * q_bytes;
-    unsigned char* const v_smem = k_smem + KS * A::UNIT;
+    unsigned char* const v_smem = k_smem + KS * A::KB * A::UNIT;
     AttMisc& ms = *reinterpret_cast<AttMisc*>(q_smem + A::ROOM);
     const TreeAttendParams& p = w.p;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -402,12 +399,12 @@ __global__ void __launch_bounds__(Att<DP>::THREADS, 1)
     const volatile int32_t* failed = &ms.failed;
 
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    if (tid == 64) {
+    if (tid == 0) {
         tma_prefetch_map(&map_k);
         tma_prefetch_map(&map_q);
         tma_prefetch_map(&map_v);
     }
-    if (warp == 0) tmem_alloc(&ms.tmem, ATT_TMEM_COLS);
+    if (warp == 2) tmem_alloc(&ms.tmem, ATT_TMEM_COLS);
     if (warp == 1) {
         if (lane < ATT_STAGES) {
             mbar_init(&ms.k_full[lane], 1);
@@ -422,65 +419,21 @@ __global__ void __launch_bounds__(Att<DP>::THREADS, 1)
             for (int j = 0; j < 2; ++j) {
                 mbar_init(&ms.s_full[lane][j], 1);
                 mbar_init(&ms.p_ready[lane][j], 4);
-                mbar_init(&ms.pv_done[lane][j], 1);
             }
             mbar_init(&ms.o_full[lane], 1);
             mbar_init(&ms.o_empty[lane], 4);
         }
         if (lane < ATT_SEGS) {
             mbar_init(&ms.seg_full[lane], 1);
-            mbar_init(&ms.seg_empty[lane], 4 + 4 * NS);
+            mbar_init(&ms.seg_empty[lane], 3 + 4 * NS);
         }
         if (lane == 0) {
             mbar_init(&ms.ml_full, 4);
             mbar_init(&ms.ml_empty, 4);
-            mbar_init(&ms.drain[0], 1);
-            mbar_init(&ms.drain[1], 1);
+            mbar_init(&ms.drain, 1);
             ms.failed = 0;
         }
         fence_barrier_init();
-    }
-    // ---- this CTA's range: a scan of the sequences' costs
-    int total = 0, per_head = 0, head0 = 0;
-    {
-        const int per = (p.s.B + A::THREADS - 1) / A::THREADS;
-        const int s0 = min(p.s.B, tid * per), s1 = min(p.s.B, s0 + per);
-        int sum = 0;
-        for (int b = s0; b < s1; ++b) {
-            const SeqLen l = tree_len(p.s, b);
-            sum += att_head_cost(p, w.g, l.ctx, l.n);
-        }
-        int inc = sum;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int v = __shfl_up_sync(0xffffffffu, inc, o);
-            if (lane >= o) inc += v;
-        }
-        if (lane == 31) ms.scan[warp] = inc;
-        __syncthreads();
-        int before = inc - sum;
-#pragma unroll
-        for (int i = 0; i < A::THREADS / 32; ++i) {
-            const int v = ms.scan[i];
-            if (i < warp) before += v;
-            total += v;
-        }
-        per_head = total;
-        total *= w.g.Hkv;
-        const int pos0 = AttSplit(total, gridDim.x).start(blockIdx.x);
-        head0 = per_head ? pos0 / per_head : 0;
-        const int in_head = pos0 - head0 * per_head;
-        if (sum > 0 && in_head >= before && in_head < before + sum) {
-            int b = s0, off = in_head - before;
-            for (;; ++b) {
-                const SeqLen l = tree_len(p.s, b);
-                const int t = att_head_cost(p, w.g, l.ctx, l.n);
-                if (off < t) break;
-                off -= t;
-            }
-            ms.first_b = b;
-            ms.first = off;
-        }
     }
     tmem_fence_before();
     __syncthreads();
@@ -494,13 +447,6 @@ __global__ void __launch_bounds__(Att<DP>::THREADS, 1)
     auto until = [&](uint64_t* bar, uint32_t parity) {  // one thread
         if (!mbar_try_wait(bar, parity & 1u)) ok = ok && att_wait(bar, parity & 1u, failed, limit);
     };
-    // an MMA issuer that gave up: none of its MMAs is in flight when the CTA leaves
-    auto drained = [&](uint64_t* bar) {
-        if (ok) return;
-        ms.failed = 1;
-        umma_commit(bar);
-        mbar_wait_n(bar, 0, limit);
-    };
     // the k-th segment; done with it
     auto segment = [&](uint32_t k) -> const AttSeg& {
         wait(&ms.seg_full[k % ATT_SEGS], k / ATT_SEGS);
@@ -512,12 +458,40 @@ __global__ void __launch_bounds__(Att<DP>::THREADS, 1)
     };
 
     if (warp == 3) {
-        // ---------------- scheduler
-        const AttSplit split(total, gridDim.x);
+        // ---------------- scheduler: finds the range by a scan of the sequences' costs,
+        // a run of sequences per lane (in one warp: the others need no barrier for it)
+        const int per = (p.s.B + 31) / 32, seq0 = min(p.s.B, lane * per), seq1 = min(p.s.B, seq0 + per);
+        int sum = 0;
+#pragma unroll 4
+        for (int b = seq0; b < seq1; ++b) {
+            const SeqLen l = tree_len(p.s, b);
+            sum += att_head_cost(p, w.g, l.ctx, l.n);
+        }
+        int before = sum;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, before, o);
+            if (lane >= o) before += v;
+        }
+        const int per_head = __shfl_sync(0xffffffffu, before, 31);
+        before -= sum;
+        const AttSplit split(per_head * w.g.Hkv, gridDim.x);
         const bool busy = (int)blockIdx.x < split.ctas;
+        const int pos0 = split.start(blockIdx.x), head0 = busy ? pos0 / per_head : 0, in_head = pos0 - head0 * per_head;
+        int first_b = seq0, off = in_head - before;
+        const bool mine = busy && off >= 0 && off < sum;
+        if (mine)
+            for (;; ++first_b) {
+                const SeqLen l = tree_len(p.s, first_b);
+                const int t = att_head_cost(p, w.g, l.ctx, l.n);
+                if (off < t) break;
+                off -= t;
+            }
+        const int who = __ffs(__ballot_sync(0xffffffffu, mine)) - 1;
+        first_b = __shfl_sync(0xffffffffu, first_b, max(who, 0));
+        off = __shfl_sync(0xffffffffu, off, max(who, 0));
         AttIter it;
-        it.start(p, w.g, busy ? split.start(blockIdx.x) : 0, busy ? split.start(blockIdx.x + 1) : 0, head0,
-                 ms.first_b, ms.first);
+        it.start(p, w.g, busy ? pos0 : 0, busy ? split.start(blockIdx.x + 1) : 0, head0, first_b, off);
         for (uint32_t k = 0; ok; ++k) {
             const uint32_t slot = k % ATT_SEGS;
             if (k >= ATT_SEGS) wait(&ms.seg_empty[slot], k / ATT_SEGS - 1);
@@ -568,11 +542,13 @@ __global__ void __launch_bounds__(Att<DP>::THREADS, 1)
         uint64_t *const full = is_k ? ms.k_full : ms.v_full, *const empty = is_k ? ms.k_empty : ms.v_empty;
         const uint32_t stages = is_k ? KS : VS;
         const int page_mask = (1 << p.s.page_log2) - 1;
-        uint32_t n = 0, st = 0, round = 0, qi = 0;  // tiles so far, the next one's stage; row tiles of Q
+        const int per = is_k ? A::KB : 1, rows = per * KT;  // tiles, and keys, of a stage
+        uint32_t n = 0, st = 0, round = 0, qi = 0;  // stages filled, the next one; row tiles of Q
         for (uint32_t k = 0; ok && !w.stall; ++k) {
             const AttSeg& sg = segment(k);
-            const int nt = sg.nt, b = sg.b, hk = sg.hk, tile0 = sg.tile0, last_key = sg.limit;
+            const int nt = sg.nt, b = sg.b, hk = sg.hk, tile0 = sg.tile0;
             if (!ok || nt == 0) break;
+            const int last_key = min(sg.limit, (tile0 + nt) * KT);
             // page ids come 32 at a time, one load per block of the table row and one
             // block ahead: a lookup per tile would put its latency between the copies
             const int32_t* table = p.table + (int64_t)b * p.s.width;
@@ -582,7 +558,7 @@ __global__ void __launch_bounds__(Att<DP>::THREADS, 1)
                 return i < pages ? __ldg(table + i) : -1;
             };
             int blk = (tile0 * KT >> p.s.page_log2) >> 5, cur = ids(blk), ahead = ids(blk + 1);
-            for (int t = 0; t < nt; ++t) {
+            for (int t = 0; t < nt; t += per) {
                 const int kb = (tile0 + t) * KT, first = kb >> p.s.page_log2;
                 if ((first >> 5) != blk) {
                     ++blk;
@@ -591,15 +567,17 @@ __global__ void __launch_bounds__(Att<DP>::THREADS, 1)
                 }
                 wait(&empty[st], round + 1);  // at once in the first round
                 if (!ok) break;
-                const int boxes = (min(KT, last_key - kb) + w.page_box - 1) / w.page_box;
-                if (lane == 0) mbar_arrive_expect_tx(&full[st], (uint32_t)(boxes * w.page_box * 128 * NH));
-                // a tile's pages (at most 8) lie in one block
-                const int key = kb + lane * w.page_box;
-                const int page = __shfl_sync(0xffffffffu, cur, (key >> p.s.page_log2) & 31);
-                unsigned char* dst = ring + st * A::UNIT + lane * w.page_box * 128;
+                const int boxes = (min(rows, last_key - kb) + w.page_box - 1) / w.page_box;
+                if (elect_one()) mbar_arrive_expect_tx(&full[st], (uint32_t)(boxes * w.page_box * 128 * NH));
+                // at most 16 pages, so in this block of ids or the next
+                const int key = kb + lane * w.page_box, at = key >> p.s.page_log2;
+                const int page0 = __shfl_sync(0xffffffffu, cur, at & 31);
+                const int page1 = __shfl_sync(0xffffffffu, ahead, at & 31);
+                unsigned char* dst = ring + st * per * A::UNIT + lane * w.page_box * 128;
                 if (lane < boxes)
                     for (int h = 0; h < NH; ++h)
-                        tma_4d(dst + h * KT * 128, map, h * 64, hk, key & page_mask, page, &full[st]);
+                        tma_4d(dst + h * rows * 128, map, h * 64, hk, key & page_mask,
+                               (at >> 5) == blk ? page0 : page1, &full[st]);
                 ++n;
                 if (++st == stages) st = 0, ++round;
                 if (t > 0 || !is_k) continue;
@@ -608,7 +586,7 @@ __global__ void __launch_bounds__(Att<DP>::THREADS, 1)
                     wait(&ms.q_empty[qb], qi / NS + 1);
                     if (!ok) break;
                     ++qi;
-                    if (lane == 0) {
+                    if (elect_one()) {
                         mbar_arrive_expect_tx(&ms.q_full[qb], (uint32_t)(w.q_box * w.g.G * 128 * NH));
                         for (int h = 0; h < NH; ++h)
                             tma_4d(q_smem + qb * q_bytes + h * w.q_rows * 128, &map_q, h * 64, hk * w.g.G,
@@ -630,72 +608,24 @@ __global__ void __launch_bounds__(Att<DP>::THREADS, 1)
             for (uint32_t i = q0; i < qi; ++i) mbar_wait_n(&ms.q_full[i % NS], (i / NS) & 1, limit);
         }
     } else if (warp == 1) {
-        // ---------------- MMA issuer of the scores: one thread.  Each of its steps
-        // (a poll, a commit, an MMA) takes some 50 cycles, and so do those of the
-        // values' issuer: as two threads they keep the tensor cores busy between them.
-        if (lane == 0) {
-            constexpr uint32_t ID_S = umma_idesc(F16, false, ATT_ROWS, KT);
-            const int dk = p.s.D / 16;  // k-steps
-            uint32_t st = 0, round = 0, qi = 0, n[2] = {0, 0};  // key ring; row tiles of Q; units of each stream
-            // Q and K are K-major with 8-row groups 1024 bytes apart
+        // ---------------- MMA issuer: one thread, whose every step (a poll, a commit)
+        // keeps the tensor cores waiting: few commits, state in registers, and code
+        // that fits the first instruction fetches.  Elected, not picked by its number:
+        // the MMAs of a branch that the compiler knows to be one thread's issue in half
+        // the cycles (17 against 52 each, measured).
+        if (elect_one()) {
+            const uint32_t id_o = umma_idesc(F16, true, ATT_ROWS, 0) | ((uint32_t)(p.s.D >> 3) << 17);
+            const int dk = p.s.D / 16;  // k-steps of the scores
+            uint32_t k_st = 0, k_round = 0, v_st = 0, v_round = 0, qi = 0;  // rings; row tiles of Q
+            uint32_t cleaned = 0;             // bit per stage, phases of v_clean so far
+            uint32_t ready = 0;               // bit 2 s + buffer: phases of p_ready
+            uint32_t emptied = 0, used = 0;   // bit s: phases of o_empty; the stream has had a segment
+            // Q and K are K-major with 8-row groups 1024 bytes apart; V is N-major,
+            // 64-column boxes KT rows apart, 8-row groups 1024 bytes apart
             const uint64_t q_desc = umma_desc(smem_u32(q_smem), 16, 1024);
             const uint64_t k_desc = umma_desc(smem_u32(k_smem), 16, 1024);
-            const uint32_t q_half = w.q_rows * 8;  // a box of Q, in 16 bytes
-            for (uint32_t k = 0; ok; ++k) {
-                const AttSeg& sg = ms.seg[k % ATT_SEGS];
-                until(&ms.seg_full[k % ATT_SEGS], k / ATT_SEGS);
-                if (!ok || sg.nt == 0) break;
-                const int nt = sg.nt;
-                const bool dual = sg.dual != 0;
-                mbar_arrive(&ms.seg_empty[k % ATT_SEGS]);
-                auto scores = [&](auto stream, int t) {
-                    constexpr int s = decltype(stream)::value;
-                    const uint32_t q = qi + (dual ? s : 0), qb = q % NS, buf = n[s] & 1;
-                    if (!dual || s == 0) until(&ms.k_full[st], round);
-                    if (t == 0) until(&ms.q_full[qb], q / NS);
-                    // the buffer's last probabilities have met their values
-                    if (n[s] >= 2) until(&ms.pv_done[s][buf], (n[s] >> 1) - 1);
-                    if (!ok) return;
-                    tmem_fence_after();
-                    const uint64_t a = q_desc + qb * (q_bytes / 16), b = k_desc + st * (A::UNIT / 16);
-                    if (dk == DP / 16) {
-#pragma unroll
-                        for (int x = 0; x < DP / 16; ++x)
-                            umma_ss(tmem + A::s_col(s, buf), a + (x / 4) * q_half + (x % 4) * 2,
-                                    b + ((x / 4) * KT * 128 + (x % 4) * 32) / 16, ID_S, x > 0);
-                    } else {
-                        for (int x = 0; x < dk; ++x)
-                            umma_ss(tmem + A::s_col(s, buf), a + (x / 4) * q_half + (x % 4) * 2,
-                                    b + ((x / 4) * KT * 128 + (x % 4) * 32) / 16, ID_S, x > 0);
-                    }
-                    umma_commit(&ms.s_full[s][buf]);
-                    ++n[s];
-                    if (t == nt - 1) umma_commit(&ms.q_empty[qb]);
-                    if (!dual || s == 1) {
-                        umma_commit(&ms.k_empty[st]);
-                        if (++st == KS) st = 0, ++round;
-                    }
-                };
-                // stream s takes every tile (two row tiles, or one stream), or the tiles
-                // s, s + 2, ... (two streams on alternate tiles)
-                const int step = NS == 1 || dual ? 1 : 2;
-                for (int t = 0; ok && t < nt; t += step) {
-                    scores(std::integral_constant<int, 0>{}, t);
-                    if (NS == 2 && ok && t + step - 1 < nt) scores(std::integral_constant<int, NS - 1>{}, t + step - 1);
-                }
-                qi += dual ? 2 : 1;
-            }
-            drained(&ms.drain[0]);
-        }
-        __syncwarp();
-    } else if (warp == 4 + 4 * NS) {
-        // ---------------- MMA issuer of the values: one thread
-        if (lane == 0) {
-            const uint32_t id_o = umma_idesc(F16, true, ATT_ROWS, 0) | ((uint32_t)(p.s.D >> 3) << 17);
-            uint32_t st = 0, round = 0, n[2] = {0, 0}, segs[2] = {0, 0};  // value ring; units and segments of each stream
-            uint32_t cleaned = 0;  // bit per stage, phases of v_clean so far
-            // V is N-major, 64-column boxes KT rows apart, 8-row groups 1024 bytes apart
             const uint64_t v_desc = umma_desc(smem_u32(v_smem), KT * 128, 1024);
+            const uint32_t q_half = w.q_rows * 8;  // a box of Q, in 16 bytes
             for (uint32_t k = 0; ok; ++k) {
                 const AttSeg& sg = ms.seg[k % ATT_SEGS];
                 until(&ms.seg_full[k % ATT_SEGS], k / ATT_SEGS);
@@ -703,43 +633,88 @@ __global__ void __launch_bounds__(Att<DP>::THREADS, 1)
                 const int nt = sg.nt, masked = att_first_masked(sg);
                 const bool dual = sg.dual != 0;
                 mbar_arrive(&ms.seg_empty[k % ATT_SEGS]);
-                const int step = NS == 1 || dual ? 1 : 2;
-                auto values = [&](auto stream, int t) {
-                    constexpr int s = decltype(stream)::value;
-                    const uint32_t buf = n[s] & 1;
-                    const bool first = t < step;
-                    if (!dual || s == 0) {
-                        if (t >= masked) {
-                            until(&ms.v_clean[st], cleaned >> st);
-                            cleaned ^= 1u << st;
-                        } else {
-                            until(&ms.v_full[st], round);
-                        }
-                    }
-                    if (first && segs[s] > 0) until(&ms.o_empty[s], segs[s] - 1);
-                    until(&ms.p_ready[s][buf], n[s] >> 1);
+                // stream s's scores of the block from tile t on, into its buffers from
+                // `buf` on (both, of a block of two tiles)
+                auto scores = [&](int s, int buf, int t) {
+                    if (t >= nt || !ok) return;
+                    const uint32_t q = qi + (dual ? s : 0), qb = q % NS;
+                    if (!dual || s == 0) until(&ms.k_full[k_st], k_round);
+                    if (t == 0) until(&ms.q_full[qb], q / NS);
                     if (!ok) return;
                     tmem_fence_after();
-                    const uint64_t b = v_desc + st * (A::UNIT / 16);
+                    const uint64_t a = q_desc + qb * (q_bytes / 16), b = k_desc + k_st * (A::KB * A::UNIT / 16);
+                    const uint32_t id = umma_idesc(F16, false, ATT_ROWS, A::KB == 2 && t + 1 < nt ? 2 * KT : KT);
+                    const uint32_t d = tmem + 128 * s + 64 * buf;
+                    auto mma = [&](int x) {
+                        umma_ss(d, a + (x / 4) * q_half + (x % 4) * 2,
+                                b + ((x / 4) * A::KB * KT * 128 + (x % 4) * 32) / 16, id, x > 0);
+                    };
+                    if (dk == DP / 16) {
 #pragma unroll
-                    for (int x = 0; x < KT / 16; ++x)
-                        umma_ts(tmem + A::o_col(s), tmem + A::s_col(s, buf) + x * 8, b + x * 128, id_o,
-                                !first || x > 0);
-                    umma_commit(&ms.pv_done[s][buf]);
-                    ++n[s];
-                    segs[s] += first;
-                    if (t + step >= nt) umma_commit(&ms.o_full[s]);
+                        for (int x = 0; x < DP / 16; ++x) mma(x);
+                    } else {
+                        for (int x = 0; x < dk; ++x) mma(x);
+                    }
+                    umma_commit(&ms.s_full[s][buf]);
+                    if (t + A::KB >= nt) umma_commit(&ms.q_empty[qb]);
                     if (!dual || s == 1) {
-                        umma_commit(&ms.v_empty[st]);
-                        if (++st == VS) st = 0, ++round;
+                        umma_commit(&ms.k_empty[k_st]);
+                        if (++k_st == KS) k_st = 0, ++k_round;
                     }
                 };
-                for (int t = 0; ok && t < nt; t += step) {
-                    values(std::integral_constant<int, 0>{}, t);
-                    if (NS == 2 && ok && t + step - 1 < nt) values(std::integral_constant<int, NS - 1>{}, t + step - 1);
+                // with two streams on alternate blocks, the one without the last tile ends
+                // with the block before
+                const int other_end = NS == 2 && !dual ? (nt - 1) / 2 * 2 - 1 : -1;
+                // t = 0: the scores of all buffers; then tile by tile, the values and the
+                // scores that take the place of what they read.  A tile's values in both
+                // streams come before the next tile's: a warpgroup may wait for the
+                // first (v_empty) before it hands over its next.
+                scores(0, 0, 0);
+                scores(NS - 1, 2 - NS, NS == 1 ? 1 : dual ? 0 : 2);
+                for (int t = 0; ok && t < nt; ++t) {
+                    const int buf = t & 1;
+                    const bool even = NS == 1 || dual || (t & 2) == 0;  // stream 0 has the tile
+                    if (t >= masked) {
+                        until(&ms.v_clean[v_st], cleaned >> v_st);
+                        cleaned ^= 1u << v_st;
+                    } else {
+                        until(&ms.v_full[v_st], v_round);
+                    }
+                    const uint64_t b = v_desc + v_st * (A::UNIT / 16);
+                    auto unit = [&](auto stream) {
+                        constexpr int s = decltype(stream)::value;
+                        const bool first = t == (NS == 2 && !dual ? 2 * s : 0);
+                        if (first) {
+                            if ((used >> s) & 1u) {
+                                until(&ms.o_empty[s], emptied >> s);
+                                emptied ^= 1u << s;
+                            }
+                            used |= 1u << s;
+                        }
+                        until(&ms.p_ready[s][buf], ready >> (2 * s + buf));
+                        ready ^= 1u << (2 * s + buf);
+                        if (!ok) return;
+                        tmem_fence_after();
+                        const uint32_t a = tmem + A::s_col(s, 0) + 64 * buf;
+#pragma unroll
+                        for (int x = 0; x < KT / 16; ++x)
+                            umma_ts(tmem + A::o_col(s), a + x * 8, b + x * 128, id_o, !first || x > 0);
+                        if (!dual || s == 1) umma_commit(&ms.v_empty[v_st]);
+                        if (t == nt - 1 || t == other_end) umma_commit(&ms.o_full[s]);
+                        if (NS == 1) scores(0, buf, t + 2);
+                        else if (buf == 1) scores(s, 0, dual ? t + 1 : t + 3);
+                    };
+                    if (even) unit(std::integral_constant<int, 0>{});
+                    if (NS == 2 && (dual || !even)) unit(std::integral_constant<int, NS - 1>{});
+                    if (++v_st == VS) v_st = 0, ++v_round;
                 }
+                qi += dual ? 2 : 1;
             }
-            drained(&ms.drain[1]);
+            if (!ok) {
+                ms.failed = 1;
+                umma_commit(&ms.drain);  // no MMA is in flight when the CTA leaves
+                mbar_wait_n(&ms.drain, 0, limit);
+            }
         }
         __syncwarp();
     } else {
@@ -762,7 +737,8 @@ __global__ void __launch_bounds__(Att<DP>::THREADS, 1)
                     for (int i = lane; i < Hq; i += 32) p.lse[(int64_t)r * Hq + i] = -INFINITY;
             }
         }
-        uint32_t base = 0, n_unit = 0, cleaned = 0;  // tiles, own units, phases of v_clean (bit per stage)
+        uint32_t base = 0, cleaned = 0;              // tiles, phases of v_clean (bit per stage)
+        uint32_t n_full = 0, n_full1 = 0;            // phases of s_full (and of a second buffer's)
         uint32_t n_seg0 = 0, n_seg1 = 0, n_ml = 0;   // segments of each stream, joins
         for (uint32_t k = 0; ok; ++k) {
             const AttSeg& sg = segment(k);
@@ -775,11 +751,12 @@ __global__ void __launch_bounds__(Att<DP>::THREADS, 1)
             float m = -INFINITY, l = 0.f;
             int masked = att_first_masked(sg);  // later: the first masked tile not counted in `cleaned`
 
-            const int stride = dual ? 1 : NS;
-            for (int tile = dual ? 0 : s; tile < nt && ok; tile += stride) {
+            // two streams on alternate blocks of two tiles, or all tiles
+            const int t_begin = NS == 2 && !dual ? 2 * s : 0, skip = NS == 2 && !dual ? 2 : 0;
+            for (int tile = t_begin; tile < nt && ok; tile += (tile & 1) ? 1 + skip : 1) {
                 const bool part = tile >= masked;  // some row sees the tile only in part
                 const int kb = (sg.tile0 + tile) * KT;
-                const uint32_t buf = n_unit & 1;
+                const uint32_t buf = tile & 1;
                 const uint32_t s_addr = tmem + A::s_col(s, buf) + lanes;
                 uint32_t see0 = 0, see1 = 0;
                 if (part) {
@@ -788,7 +765,8 @@ __global__ void __launch_bounds__(Att<DP>::THREADS, 1)
                     see0 = att_sees(p, sg.b, t, sg.ctx, sg.n, kb);
                     see1 = att_sees(p, sg.b, t, sg.ctx, sg.n, kb + 32);
                 }
-                wait(&ms.s_full[s][buf], n_unit >> 1);
+                if (NS == 1 && buf == 1) wait(&ms.s_full[s][1], n_full1++);
+                else if (NS == 1 || buf == 0) wait(&ms.s_full[s][0], n_full++);
                 if (!ok) break;
                 tmem_fence_after();
                 uint32_t vst = 0;
@@ -828,10 +806,11 @@ __global__ void __launch_bounds__(Att<DP>::THREADS, 1)
                         const float f = grow ? ex2_fast((m - top) * c) : 1.f;
                         if (grow) m = top;
                         l *= f;
-                        if (tile >= stride) {
-                            // the P V before this unit's has to be complete (those before it
-                            // are: this buffer's scores were issued after them)
-                            wait(&ms.pv_done[s][(n_unit - 1) & 1], (n_unit - 1) >> 1);
+                        if (tile > t_begin) {
+                            // the P V of the tile before has to be complete (those before these
+                            // scores' block are: the scores were issued after them)
+                            const uint32_t vi = base + tile - 1;
+                            if (NS == 1 || buf == 1) wait(&ms.v_empty[vi % VS], vi / VS);
                             if (!ok) break;
                             tmem_fence_after();
 #pragma unroll 1
@@ -872,19 +851,19 @@ __global__ void __launch_bounds__(Att<DP>::THREADS, 1)
                 if (lane == 0) mbar_arrive(&ms.p_ready[s][buf]);
                 if (part && __any_sync(0xffffffffu, some)) {
                     // rare: once P V is done (it saw zeros there), O += those values
-                    wait(&ms.pv_done[s][buf], n_unit >> 1);
+                    const uint32_t vi = base + tile;
+                    wait(&ms.v_empty[vi % VS], vi / VS);
                     if (!ok) break;
                     tmem_fence_after();
                     att_add_nonfinite<F16>(p, see0, see1, sg.b, sg.hk, kb, o_addr);
                 }
-                ++n_unit;
             }
             for (; masked < nt; ++masked) cleaned ^= 1u << ((base + masked) % VS);
             base += nt;
             if (!ok) break;
 
             // ---- the segment's end: O of the streams with units
-            const bool two = dual || nt > 1;           // stream 1 has some
+            const bool two = dual || nt > A::KB;       // stream 1 has some
             const bool join = NS == 2 && !dual && two;  // one row tile in two streams
             if (s == 0 || two) wait(&ms.o_full[s], s == 0 ? n_seg0 : n_seg1);
             if (!ok) break;
@@ -983,7 +962,7 @@ __global__ void __launch_bounds__(Att<DP>::THREADS, 1)
     __syncthreads();
     if (tid == 0 && ms.failed) atomicOr(w.err, 1u);
     tmem_fence_after();
-    if (warp == 0) tmem_free(tmem, ATT_TMEM_COLS);
+    if (warp == 2) tmem_free(tmem, ATT_TMEM_COLS);
 }
 
 // ------------------------------------------------------------------------- //
@@ -997,7 +976,7 @@ __global__ void __launch_bounds__(Att<DP>::THREADS, 1)
 // shared memory.  The tasks are those that k_tree_attend announced: only the
 // GPU knows which ranges cut items.  Parts are summed in their order, whatever
 // the order of the tasks.
-constexpr int COMB_THREADS = 256, COMB_CTAS_PER_SM = 4;
+constexpr int COMB_THREADS = 256, COMB_CTAS_PER_SM = 2;
 
 template <bool F16>
 __global__ void __launch_bounds__(COMB_THREADS, COMB_CTAS_PER_SM)
@@ -1012,9 +991,11 @@ __global__ void __launch_bounds__(COMB_THREADS, COMB_CTAS_PER_SM)
     const float c = p.scale * 1.4426950408889634f;
     auto weight = [&](float m, float ref) { return m == -INFINITY ? 0.f : ex2_fast((m - ref) * c); };
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    AttJoin next = w.joins[blockIdx.x];  // of no meaning past the tasks' number
     const int tasks = (int)__ldcg(w.n_joins);
     for (int task = blockIdx.x; task < tasks; task += gridDim.x) {
-        const AttJoin jn = w.joins[task];
+        const AttJoin jn = next;
+        if (task + (int)gridDim.x < tasks) next = w.joins[task + gridDim.x];
         const int n = jn.last - jn.first + 1;
         auto slot = [&](int i) { return (int64_t)(jn.first + i) * 2 + (i == 0 ? 1 : 0); };
         // rows of the second row tile lie behind the first's 128
@@ -1027,25 +1008,34 @@ __global__ void __launch_bounds__(COMB_THREADS, COMB_CTAS_PER_SM)
             const int c32 = (D + 31) / 32, sub = jn.sub * 8 + g, rb = sub / c32, col4 = (sub - rb * c32) * 8;
             const int r = rb * 32 + lane, pr = part_row(r);
             if (r >= jn.rows) continue;
-            float top = -INFINITY, l = 0.f;
-            for (int i = 0; i < n; ++i) top = fmaxf(top, w.part_ml[slot(i) * prows + pr].x);
-            const float ref = top == -INFINITY ? 0.f : top;
+            // the parts' maxima, sums and columns are loaded together; the running
+            // maximum keeps the sums in its units
+            float ref = -INFINITY, l = 0.f;
             float4 acc[8];
 #pragma unroll
             for (int k = 0; k < 8; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 1
+#pragma unroll 2
             for (int i = 0; i < n; ++i) {
                 const float2 v = w.part_ml[slot(i) * prows + pr];
-                const float f = weight(v.x, ref);
-                l += v.y * f;
                 const float4* src = (const float4*)w.part_o + (slot(i) * (DP / 4) + col4) * prows + pr;
+                float4 o[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    if ((col4 + k) * 4 < D) o[k] = src[k * prows];
+                const float top = fmaxf(ref, v.x), m = top == -INFINITY ? 0.f : top;
+                const float f = weight(ref, m), e = weight(v.x, m);
+                ref = top;
+                l = l * f + v.y * e;
 #pragma unroll
                 for (int k = 0; k < 8; ++k)
                     if ((col4 + k) * 4 < D) {
-                        const float4 o = src[k * prows];
-                        acc[k].x += f * o.x, acc[k].y += f * o.y, acc[k].z += f * o.z, acc[k].w += f * o.w;
+                        acc[k].x = acc[k].x * f + o[k].x * e;
+                        acc[k].y = acc[k].y * f + o[k].y * e;
+                        acc[k].z = acc[k].z * f + o[k].z * e;
+                        acc[k].w = acc[k].w * f + o[k].w * e;
                     }
             }
+            if (ref == -INFINITY) ref = 0.f;
             const bool none = l == 0.f;
             const float inv = none ? 0.f : 1.f / l;
             const int64_t orow = out_row(r);
@@ -1167,8 +1157,9 @@ static cudaError_t att_launch(AttWork w, int num_sms, cudaStream_t s)
     // what Q does not need is for the rings: few rows leave room for more tiles on their way
     w.q_rows = (w.q_box * w.g.G + 7) / 8 * 8;
     const int stages = (A::ROOM - A::NS * w.q_rows * DP * 2) / A::UNIT;
-    w.k_stages = min((stages + 1) / 2, ATT_STAGES);
-    w.v_stages = min(stages / 2, ATT_STAGES);
+    // a stage of keys is a block; the values, which wait for the probabilities, get more
+    w.k_stages = min(A::KB == 2 ? max(2, stages / 4) : (stages + 1) / 2, ATT_STAGES);
+    w.v_stages = min(stages - A::KB * w.k_stages, ATT_STAGES);
     CUtensorMap mq, mk, mv;
     const int64_t qd[3] = {sh.Hq, sh.T, sh.B}, qs[3] = {w.p.q.head, w.p.q.token, w.p.q.seq};
     const int64_t cd[3] = {sh.Hkv, 1 << sh.page_log2, sh.num_pages}, cs[3] = {w.p.c.head, w.p.c.token, w.p.c.page};
@@ -1182,7 +1173,11 @@ static cudaError_t att_launch(AttWork w, int num_sms, cudaStream_t s)
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = dim3((unsigned)(num_sms * COMB_CTAS_PER_SM));
+    // no more CTAs than there can be tasks: the items', each with parts in all ranges
+    const int64_t items = (int64_t)sh.B * sh.Hkv * ((sh.T + w.g.group - 1) / w.g.group);
+    const int most = std::max(att_join_tasks(ATT_FEW, w.q_rows * A::NS, sh.D),
+                              att_join_tasks(ATT_FEW + 1, w.q_rows * A::NS, sh.D));
+    cfg.gridDim = dim3((unsigned)std::min<int64_t>(items * most, num_sms * COMB_CTAS_PER_SM));
     cfg.blockDim = dim3(COMB_THREADS);
     cfg.stream = s;
     cfg.attrs = at;
