@@ -12,15 +12,16 @@ namespace sv {
 
 struct DeviceGuard {
     int prev = -1;
-    bool ok = false;
+    bool ok = false, changed = false;
     explicit DeviceGuard(int dev)
     {
         if (cudaGetDevice(&prev) != cudaSuccess) return;
-        ok = (prev == dev) || cudaSetDevice(dev) == cudaSuccess;
+        changed = prev != dev;
+        ok = !changed || cudaSetDevice(dev) == cudaSuccess;
     }
     ~DeviceGuard()
     {
-        if (prev >= 0) cudaSetDevice(prev);
+        if (changed) cudaSetDevice(prev);
     }
 };
 

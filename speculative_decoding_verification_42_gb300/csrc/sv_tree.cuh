@@ -109,7 +109,7 @@ struct TreeKeepParams {
 };
 
 cudaError_t launch_tree_plan(TreePlanParams p, int num_sms, cudaStream_t s);
-cudaError_t launch_tree_append(const TreeAppendParams& p, int dtype, cudaStream_t s);
+cudaError_t launch_tree_append(const TreeAppendParams& p, int dtype, int num_sms, cudaStream_t s);
 // bytes of workspace (zeroed before the first call) for `ctas` CTAs, and where
 // in it the (m, l) and the joins begin
 size_t tree_attend_bytes(int D, int ctas, size_t* ml_at, size_t* join_at);

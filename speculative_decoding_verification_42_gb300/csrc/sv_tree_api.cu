@@ -186,7 +186,7 @@ spec_status spec_tree_append(spec_tree_t h, const spec_tree_append_args* a, void
     p.interleaved = a->interleaved ? 1 : 0;
     p.eps = a->eps;
     p.q_out = a->q_out;
-    return launched(launch_tree_append(p, h->cfg.dtype, (cudaStream_t)stream));
+    return launched(launch_tree_append(p, h->cfg.dtype, h->num_sms, (cudaStream_t)stream));
 }
 
 spec_status spec_tree_attend(spec_tree_t h, const spec_tree_attend_args* a, void* stream)

@@ -147,112 +147,146 @@ cudaError_t launch_tree_plan(TreePlanParams p, int num_sms, cudaStream_t s)
 // ------------------------------------------------------------------------- //
 // k_tree_append                                                             //
 // ------------------------------------------------------------------------- //
-// One CTA per token; LANES threads hold one head, 8 elements (16 bytes) each.
-constexpr int APP_THREADS = 256;
+// LANES threads hold one head, 8 elements (16 bytes) each.  With x the head, z
+// each element's mate in its pair, w the weights and r = 1 / sqrt(mean(x^2) +
+// eps), the norm and the rotation are y = r (x A + z B) with A = w cos and B =
+// -+ w(mate) sin, which a thread forms once per token for all query heads and
+// once for all key heads.  HBM bound by its bytes (each element read and
+// written once), but near the issue rate: so few instructions per element, and
+// a token's heads on as few warps as still fill the machine (1, 2, 4 or 8; the
+// angles and weights are per thread).  Loads of APP_UNROLL heads are in flight
+// together.
+constexpr int APP_THREADS = 256, APP_UNROLL = 4;
 
 template <bool F16, int LANES>
-__global__ void __launch_bounds__(APP_THREADS) k_tree_append(const TreeAppendParams p)
+__global__ void __launch_bounds__(APP_THREADS, 3) k_tree_append(const TreeAppendParams p, int warps_log2)
 {
     using H = Half2<F16>;
-    const int tok = blockIdx.x, b = tok / p.s.T, j = tok - b * p.s.T;
-    const int li = threadIdx.x % LANES, gid = threadIdx.x / LANES;
-    constexpr int GROUPS = APP_THREADS / LANES;
-    const int Hq = p.s.Hq, Hkv = p.s.Hkv, D = p.s.D;
-    const bool lane_on = li * 8 < D;
-    const int slot = __ldg(p.slot_map + tok);
+    const int gwarp = blockIdx.x * (APP_THREADS / 32) + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    const int tok = gwarp >> warps_log2;
+    if (tok >= p.s.B * p.s.T) return;  // whole warps
+    const int b = tok / p.s.T, j = tok - b * p.s.T;
+    const int li = lane % LANES, e0 = li * 8, D = p.s.D;
+    const float inv_d = 1.f / (float)D;
+    const int groups = (32 / LANES) << warps_log2;  // heads of the token at a time
+    const int gid = (gwarp & ((1 << warps_log2) - 1)) * (32 / LANES) + lane / LANES;
+    const bool lane_on = e0 < D;
+    const int slot = __ldg(p.slot_map + tok), pos = p.cos_sin ? __ldg(p.positions + tok) : 0;
     const bool live = j < tree_nodes(p.s, b) && slot >= 0 && (slot >> p.s.page_log2) < p.s.num_pages;
-    char* qo = (char*)p.q_out + ((int64_t)tok * Hq * D + li * 8) * 2;
-    if (!live) {
-        if (lane_on)
-            for (int h = gid; h < Hq; h += GROUPS) *(uint4*)(qo + (int64_t)h * D * 2) = make_uint4(0, 0, 0, 0);
-        return;
-    }
-    // the pair of element e sits rot / 2 away (halves) or beside it (interleaved)
-    const int half = p.rot / 2, e0 = li * 8;
-    const bool turn = p.cos_sin && e0 < p.rot;
-    const bool lower = e0 < half;
-    const int partner = (lower ? e0 + half : e0 - half) / 8;
-    float cs[8], sn[8];  // angles of this thread's elements (interleaved: 4 pairs)
+    const int64_t row = (int64_t)(slot >> p.s.page_log2) * p.c.page +
+                        (int64_t)(slot & ((1 << p.s.page_log2) - 1)) * p.c.token + e0;
+    // the mate of element e is rot / 2 away (halves) or beside it (interleaved)
+    const int half = p.rot / 2;
+    const bool turn = lane_on && e0 < p.rot, lower = e0 < half, far = p.cos_sin && !p.interleaved;
+    const int mate = turn && far ? (lower ? e0 + half : e0 - half) : e0;  // first element of the mates' lane
+    float c[8], sn[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) cs[i] = 1.f, sn[i] = 0.f;
+    for (int i = 0; i < 8; ++i) c[i] = 1.f, sn[i] = 0.f;
     if (turn) {
-        const int pos = __ldg(p.positions + tok);
         if (pos < 0 || pos >= p.table_len) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) cs[i] = sn[i] = __int_as_float(0x7fc00000);
+            for (int i = 0; i < 8; ++i) c[i] = sn[i] = __int_as_float(0x7fc00000);
+        } else if (p.interleaved) {
+            const float* t = p.cos_sin + (int64_t)pos * p.rot + e0 / 2;
+            const float4 x = __ldg((const float4*)t), y = __ldg((const float4*)(t + half));
+            c[0] = c[1] = x.x, c[2] = c[3] = x.y, c[4] = c[5] = x.z, c[6] = c[7] = x.w;
+            sn[1] = y.x, sn[3] = y.y, sn[5] = y.z, sn[7] = y.w;
+            sn[0] = -y.x, sn[2] = -y.y, sn[4] = -y.z, sn[6] = -y.w;
         } else {
-            const float* t = p.cos_sin + (int64_t)pos * p.rot;
-            const int i0 = p.interleaved ? e0 / 2 : lower ? e0 : e0 - half;
+            const float* t = p.cos_sin + (int64_t)pos * p.rot + (lower ? e0 : e0 - half);
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (i < (p.interleaved ? 4 : 8)) cs[i] = __ldg(t + i0 + i), sn[i] = __ldg(t + half + i0 + i);
+            for (int i = 0; i < 8; i += 4) {
+                const float4 x = __ldg((const float4*)(t + i)), y = __ldg((const float4*)(t + half + i));
+                c[i] = x.x, c[i + 1] = x.y, c[i + 2] = x.z, c[i + 3] = x.w;
+                sn[i] = lower ? -y.x : y.x, sn[i + 1] = lower ? -y.y : y.y;
+                sn[i + 2] = lower ? -y.z : y.z, sn[i + 3] = lower ? -y.w : y.w;
+            }
         }
     }
-    const int64_t row = (int64_t)(slot >> p.s.page_log2) * p.c.page +
-                        (int64_t)(slot & ((1 << p.s.page_log2) - 1)) * p.c.token;
-    const int total = Hq + 2 * Hkv;
-    for (int h0 = 0; h0 < total; h0 += GROUPS) {
-        const int h = h0 + gid;
-        const bool on = h < total && lane_on;
-        const int kind = h < Hq ? 0 : h < Hq + Hkv ? 1 : 2;
-        const int hh = kind == 0 ? h : kind == 1 ? h - Hq : h - Hq - Hkv;
+
+#pragma unroll 1
+    for (int kind = 0; kind < 3; ++kind) {
         const TreeRows& src = kind == 0 ? p.q : kind == 1 ? p.k : p.v;
-        uint4 x = make_uint4(0, 0, 0, 0);
-        if (on)
-            x = ld_stream16((const char*)src.ptr +
-                            (b * src.seq + (int64_t)j * src.token + hh * src.head + e0) * 2);
-        float y[8];
-        const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float2 f = H::unpack(xs[i]);
-            y[2 * i] = f.x, y[2 * i + 1] = f.y;
-        }
-        const void* w = kind == 0 ? p.qw : p.kw;
-        float ss = 0.f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) ss += y[i] * y[i];
-#pragma unroll
-        for (int o = LANES / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        if (kind < 2 && w && on) {
-            const float r = 1.f / sqrtf(ss / (float)D + p.eps);
-            const uint4 wv = __ldg((const uint4*)((const char*)w + e0 * 2));
-            const uint32_t ws[4] = {wv.x, wv.y, wv.z, wv.w};
+        const void* w = kind == 0 ? p.qw : kind == 1 ? p.kw : nullptr;
+        const int heads = kind == 0 ? p.s.Hq : p.s.Hkv;
+        const char* from = (const char*)src.ptr + (b * src.seq + (int64_t)j * src.token + e0) * 2;
+        char* to = kind == 0 ? (char*)p.q_out + ((int64_t)tok * p.s.Hq * D + e0) * 2
+                             : (char*)(kind == 1 ? p.c.k : p.c.v) + row * 2;
+        const int64_t from_head = src.head * 2, to_head = kind == 0 ? (int64_t)D * 2 : p.c.head * 2;
+        float A[8], Bm[8];
+        if (kind < 2) {
+            uint4 wa = make_uint4(0, 0, 0, 0), wb = wa;
+            if (w && lane_on) wa = __ldg((const uint4*)((const char*)w + e0 * 2)), wb = __ldg((const uint4*)((const char*)w + mate * 2));
+            const uint32_t was[4] = {wa.x, wa.y, wa.z, wa.w}, wbs[4] = {wb.x, wb.y, wb.z, wb.w};
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const float2 f = H::unpack(ws[i]);
-                y[2 * i] *= r * f.x, y[2 * i + 1] *= r * f.y;
+                const float2 own = w ? H::unpack(was[i]) : make_float2(1.f, 1.f);
+                float2 other = w ? H::unpack(wbs[i]) : make_float2(1.f, 1.f);
+                if (!far) other = make_float2(other.y, other.x);
+                A[2 * i] = own.x * c[2 * i], A[2 * i + 1] = own.y * c[2 * i + 1];
+                Bm[2 * i] = other.x * sn[2 * i], Bm[2 * i + 1] = other.y * sn[2 * i + 1];
             }
         }
-        float z[8];
+#pragma unroll 1
+        for (int h0 = 0; h0 < heads; h0 += groups * APP_UNROLL) {
+            uint4 x[APP_UNROLL];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) z[i] = __shfl_sync(0xffffffffu, y[i], partner, LANES);
-        if (kind < 2 && turn) {
-            if (p.interleaved) {
+            for (int u = 0; u < APP_UNROLL; ++u) {
+                const int h = h0 + u * groups + gid;
+                x[u] = make_uint4(0, 0, 0, 0);
+                if (h < heads && lane_on && live) x[u] = ld_stream16(from + h * from_head);
+            }
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float a = y[2 * i], c = y[2 * i + 1];
-                    y[2 * i] = a * cs[i] - c * sn[i];
-                    y[2 * i + 1] = c * cs[i] + a * sn[i];
+            for (int u = 0; u < APP_UNROLL; ++u) {
+                if (h0 + u * groups >= heads) break;  // the same for the whole warp
+                const int h = h0 + u * groups + gid;
+                uint4 v = x[u];
+                if (kind < 2) {
+                    const uint32_t xs[4] = {v.x, v.y, v.z, v.w};
+                    float y[8];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float2 f = H::unpack(xs[i]);
+                        y[2 * i] = f.x, y[2 * i + 1] = f.y;
+                    }
+                    float r = 1.f;
+                    if (w) {
+                        float ss = 0.f;
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) ss += y[i] * y[i];
+#pragma unroll
+                        for (int o = LANES / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+                        r = rsqrtf(ss * inv_d + p.eps);
+                    }
+                    uint32_t out[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        float2 z = make_float2(y[2 * i + 1], y[2 * i]);
+                        if (far) z = H::unpack(__shfl_sync(0xffffffffu, xs[i], mate / 8, LANES));
+                        float a0 = y[2 * i] * A[2 * i], a1 = y[2 * i + 1] * A[2 * i + 1];
+                        if (p.cos_sin) a0 += z.x * Bm[2 * i], a1 += z.y * Bm[2 * i + 1];
+                        out[i] = H::pack(a0 * r, a1 * r);
+                    }
+                    v = make_uint4(out[0], out[1], out[2], out[3]);
                 }
-            } else {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) y[i] = y[i] * cs[i] + (lower ? -z[i] : z[i]) * sn[i];
+                if (!live) v = make_uint4(0, 0, 0, 0);
+                if (h < heads && lane_on && (live || kind == 0)) *(uint4*)(to + h * to_head) = v;
             }
         }
-        if (!on) continue;
-        if (kind < 2)
-            x = make_uint4(H::pack(y[0], y[1]), H::pack(y[2], y[3]), H::pack(y[4], y[5]), H::pack(y[6], y[7]));
-        char* dst = kind == 0 ? qo + (int64_t)hh * D * 2
-                              : (char*)(kind == 1 ? p.c.k : p.c.v) + (row + hh * p.c.head + e0) * 2;
-        *(uint4*)dst = x;
+        if (!live) break;  // only q_out is written, with zeros
     }
 }
 
-cudaError_t launch_tree_append(const TreeAppendParams& p, int dtype, cudaStream_t s)
+cudaError_t launch_tree_append(const TreeAppendParams& p, int dtype, int num_sms, cudaStream_t s)
 {
-    const int tokens = p.s.B * p.s.T;
-    auto go = [&](auto kernel) { kernel<<<tokens, APP_THREADS, 0, s>>>(p); };
+    const int64_t tokens = (int64_t)p.s.B * p.s.T;
+    // as many warps per token, up to 8, as leave no more than 24 to an SM (what its registers hold): one
+    // token of 80 heads takes 8.4 us with eight warps and 20.6 with one, 576 such tokens 12.5 us with
+    // four, 16.5 with eight and 24.7 with one, 6000 tokens of 36 heads 31 us with one and 68 with eight
+    int log2 = 0;
+    while (log2 < 3 && (tokens << (log2 + 1)) <= 24 * (int64_t)num_sms) ++log2;
+    const unsigned grid = (unsigned)(((tokens << log2) + APP_THREADS / 32 - 1) / (APP_THREADS / 32));
+    auto go = [&](auto kernel) { kernel<<<grid, APP_THREADS, 0, s>>>(p, log2); };
     const bool f16 = dtype == SPEC_F16;
     if (p.s.D <= 64) f16 ? go(k_tree_append<true, 8>) : go(k_tree_append<false, 8>);
     else if (p.s.D <= 128) f16 ? go(k_tree_append<true, 16>) : go(k_tree_append<false, 16>);

@@ -168,6 +168,8 @@ class TreeCache:
         self._pages, self._width, self._max_tokens = num_pages, table_width, max_tokens
         self._cache_shape = (num_pages, page_size, kv_heads, head_dim)
         self._scale = head_dim ** -0.5
+        self._current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+            (lambda device: torch.cuda.current_stream(device).cuda_stream)
         # the argument records of the calls, filled anew by each (one handle, one caller at a time)
         self._plan_args, self._append_args = spec_tree_plan_args(), spec_tree_append_args()
         self._attend_args, self._keep_args = spec_tree_attend_args(), spec_tree_keep_args()
@@ -227,15 +229,25 @@ class TreeCache:
         rec.layer_stride = st[0] if many and shape[0] > 1 else 0
 
     def _stream(self, stream):
+        # the address of the current stream, without an object for it where torch can tell
         if stream is None:
-            import torch
-            stream = torch.cuda.current_stream(self.device)
+            return self._current_stream(self.device)
         return stream.cuda_stream
 
-    def _out(self, out, key, shape, dtype):
-        """The caller's output tensor (checked), or a new one."""
+    @staticmethod
+    def _used_on(stream, tensors):
+        # allocated on the current stream, written on another: their memory must not be
+        # reused before that stream is done with it
+        for t in tensors:
+            t.record_stream(stream)
+
+    def _out(self, out, key, shape, dtype, like=None):
+        """The caller's output tensor (checked), or a new one (like `like`, a contiguous
+        tensor of that shape and type, when given)."""
         if out is None or key not in out:
             import torch
+            if like is not None:
+                return torch.empty_like(like)
             return torch.empty(shape, dtype=dtype, device=self._dev)
         self._tensor(out[key], shape, dtype, f"out['{key}']")
         return out[key]
@@ -262,25 +274,30 @@ class TreeCache:
         B = ctx_len.shape[0]
         T = parents.shape[1] if parents is not None else int(max_tokens or self._max_tokens)
         b, bt = (B,), (B, T)
-        res = dict(held=self._out(out, "held", b, i32), ring=self._out(out, "ring", (2,), torch.int64),
-                   slot_map=self._out(out, "slot_map", bt, i32),
-                   positions=self._out(out, "positions", bt, i32),
-                   row_status=self._out(out, "row_status", b, i32))
-        a.parents = a.tree_mask = None
-        if parents is not None:
-            mask = res["tree_mask"] = self._out(out, "tree_mask", (B, T, (T + 31) // 32), i32)
-            a.parents, a.tree_mask = self._tensor(parents, bt, i32, "parents"), mask.data_ptr()
         a.ctx_len = self._tensor(ctx_len, b, i32, "ctx_len")
         a.n_tokens = None if n_tokens is None else self._tensor(n_tokens, b, i32, "n_tokens")
         a.held = self._tensor(held, b, i32, "held")
         a.ring = self._tensor(ring, (2,), torch.int64, "ring")
         a.free_pages = self._tensor(free_pages, (self._pages,), i32, "free_pages")
         a.block_table = self._tensor(block_table, (B, self._width), i32, "block_table")
+        a.parents = a.tree_mask = None
+        if parents is not None:
+            a.parents = self._tensor(parents, bt, i32, "parents")
+        res = {"held": self._out(out, "held", b, i32, held),
+               "ring": self._out(out, "ring", (2,), torch.int64, ring),
+               "slot_map": self._out(out, "slot_map", bt, i32, parents),
+               "positions": self._out(out, "positions", bt, i32, parents),
+               "row_status": self._out(out, "row_status", b, i32, held)}
+        if parents is not None:
+            mask = res["tree_mask"] = self._out(out, "tree_mask", (B, T, (T + 31) // 32), i32)
+            a.tree_mask = mask.data_ptr()
         a.batch, a.tokens = B, T
         a.held_out, a.ring_out = res["held"].data_ptr(), res["ring"].data_ptr()
         a.slot_map, a.positions = res["slot_map"].data_ptr(), res["positions"].data_ptr()
         a.row_status = res["row_status"].data_ptr()
         _check(self._lib.spec_tree_plan(self.h, a, self._stream(stream)), "spec_tree_plan")
+        if stream is not None:
+            self._used_on(stream, res.values())
         return res
 
     def append(self, q, k, v, k_cache, v_cache, slot_map, positions=None, n_tokens=None, *,
@@ -316,6 +333,8 @@ class TreeCache:
         else:
             a.q_out = self._tensor(out, shape, self.dtype, "out")
         _check(self._lib.spec_tree_append(self.h, a, self._stream(stream)), "spec_tree_append")
+        if stream is not None:
+            self._used_on(stream, (out,))
         return out
 
     def attend(self, q, k_cache, v_cache, block_table, ctx_len, n_tokens=None, *, tree_mask=None,
@@ -343,6 +362,8 @@ class TreeCache:
             e = res["lse"] = self._out(out, "lse", shape[:3], torch.float32)
             a.lse = e.data_ptr()
         _check(self._lib.spec_tree_attend(self.h, a, self._stream(stream)), "spec_tree_attend")
+        if stream is not None:
+            self._used_on(stream, res.values())
         return res
 
     def keep(self, k_cache, v_cache, block_table, ctx_len, n_tokens, path, path_len, *,
@@ -361,10 +382,12 @@ class TreeCache:
         a.path = self._tensor(path, (B, T), i32, "path")
         a.path_len = self._tensor(path_len, b, i32, "path_len")
         a.batch, a.tokens = B, T
-        res = {"ctx_len": self._out(out, "ctx_len", b, i32),
-               "row_status": self._out(out, "row_status", b, i32)}
+        res = {"ctx_len": self._out(out, "ctx_len", b, i32, ctx_len),
+               "row_status": self._out(out, "row_status", b, i32, ctx_len)}
         a.ctx_out, a.row_status = res["ctx_len"].data_ptr(), res["row_status"].data_ptr()
         _check(self._lib.spec_tree_keep(self.h, a, self._stream(stream)), "spec_tree_keep")
+        if stream is not None:
+            self._used_on(stream, res.values())
         return res
 
     def check(self, stream=None) -> int:
