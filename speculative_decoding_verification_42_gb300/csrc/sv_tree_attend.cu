@@ -62,18 +62,18 @@ constexpr uint32_t ATT_WAIT_POLLS = 1u << 17;  // limit of a wait: some seconds 
 constexpr uint32_t ATT_STALL_POLLS = 4096;    // SPEC_FAULT_STALL_STREAM
 constexpr float ATT_LAZY = 8.f;               // log2 growth of the maximum that O takes unscaled
 
-constexpr int ATT_KT = 64;                    // keys of a tile
-constexpr int ATT_STAGES = 11;                // most stages of a ring
+constexpr int ATT_STAGES = 8;                 // most stages of a ring
 
 template <int DP>
 struct Att {                                  // DP: head size rounded up to 64
     static constexpr int NH = DP / 64;        // 64-column (128-byte) boxes of a row
     static constexpr int NS = DP <= 128 ? 2 : 1;     // streams (softmax warpgroups)
-    static constexpr int UNIT = ATT_KT * DP * 2;     // bytes of a K or V tile
-    static constexpr int KB = NS;             // tiles of a block of keys: the N of the scores' MMAs is 64 KB
+    static constexpr int KT = 64 * NS;        // keys of a tile: two halves of 64, or one
+    static constexpr int UNIT = KT * DP * 2;  // bytes of a K or V tile
     static constexpr int ROOM = ATT_SMEM - 1024 - ATT_MISC;  // bytes for Q and the rings
     static constexpr int THREADS = 128 + 128 * NS;   // four warps, and the softmax warpgroups
-    __host__ __device__ static constexpr uint32_t s_col(int s, int buf) { return 128u * s + 64u * buf; }
+    // scores of stream s: 128 columns, a tile's or (one stream) two buffers of a tile
+    __host__ __device__ static constexpr uint32_t s_col(int s) { return 128u * s; }
     __host__ __device__ static constexpr uint32_t o_col(int s) { return NS == 2 ? 256u + 128u * s : 128u; }
     static_assert((ROOM - NS * ATT_ROWS * DP * 2) / UNIT >= 4, "the rings fit");
 };
@@ -95,14 +95,14 @@ struct __align__(16) AttMisc {
     uint64_t v_full[ATT_STAGES], v_empty[ATT_STAGES];  // value tiles
     uint64_t v_clean[ATT_STAGES];    // a masked value tile may meet the MMAs
     uint64_t q_full[2], q_empty[2];
-    uint64_t s_full[2][2];         // [stream][buffer] scores are in tensor memory (a block's: buffer 0)
-    uint64_t p_ready[2][2];        // a tile's probabilities are (and O is scaled)
+    uint64_t s_full[2][2];         // [stream][buffer] a tile's scores are in tensor memory
+    uint64_t p_ready[2][2];        // [stream][half or buffer] probabilities are (and O is scaled)
     uint64_t o_full[2], o_empty[2];  // the segment's O is complete; has been read
     uint64_t ml_full, ml_empty;    // stream 1's (m, l) for the join
     uint64_t seg_full[ATT_SEGS], seg_empty[ATT_SEGS];
     uint64_t drain;
     AttSeg seg[ATT_SEGS];
-    uint32_t nf[ATT_STAGES][2];    // (masked) value rows of the tile with non-finite elements
+    uint32_t nf[ATT_STAGES][4];    // (masked) value rows of the tile with non-finite elements
     float2 ml[ATT_ROWS];           // stream 1's (m, l) of a row
     uint32_t tmem;
     int32_t failed;
@@ -119,7 +119,7 @@ struct AttGeom {
 
 // The ranges are equal in cost, not in tiles: an item costs its key tiles and
 // ATT_ITEM_COST more (its first scores, its masked tile and its output).
-constexpr int ATT_ITEM_COST = 2;
+constexpr int ATT_ITEM_COST = 4;
 
 // keys that some row of item `rp` of a sequence sees: a chain's rows see
 // nothing past their last node
@@ -127,18 +127,20 @@ __device__ __forceinline__ int att_limit(const TreeAttendParams& p, const AttGeo
 {
     return ctx + (p.mask ? n : min(n, (rp + 1) * g.group));
 }
+template <int KT>
 __device__ __forceinline__ int att_cost(const TreeAttendParams& p, const AttGeom& g, int ctx, int n, int rp)
 {
-    return (att_limit(p, g, ctx, n, rp) + ATT_KT - 1) / ATT_KT + ATT_ITEM_COST;
+    return (att_limit(p, g, ctx, n, rp) + KT - 1) / KT + ATT_ITEM_COST;
 }
 // cost of all items of one key head of a sequence
+template <int KT>
 __device__ __forceinline__ int att_head_cost(const TreeAttendParams& p, const AttGeom& g, int ctx, int n)
 {
-    if (n <= g.group) return n ? att_cost(p, g, ctx, n, 0) : 0;
+    if (n <= g.group) return n ? att_cost<KT>(p, g, ctx, n, 0) : 0;
     const int nrp = (n + g.group - 1) / g.group;
-    if (p.mask) return nrp * att_cost(p, g, ctx, n, 0);
+    if (p.mask) return nrp * att_cost<KT>(p, g, ctx, n, 0);
     int t = 0;
-    for (int rp = 0; rp < nrp; ++rp) t += att_cost(p, g, ctx, n, rp);
+    for (int rp = 0; rp < nrp; ++rp) t += att_cost<KT>(p, g, ctx, n, rp);
     return t;
 }
 
@@ -159,6 +161,7 @@ struct AttSplit {
 };
 
 // the segments of a CTA: parts of items, in order of (key head, sequence, group)
+template <int KT>
 struct AttIter {
     int pos, end;               // cost positions in the order of all items
     int b, hk, rp;              // the item
@@ -174,7 +177,7 @@ struct AttIter {
         t0 = rp * g.group;
         ntok = min(g.group, n - t0);
         limit = att_limit(p, g, ctx, n, rp);
-        ntiles = (limit + ATT_KT - 1) / ATT_KT;
+        ntiles = (limit + KT - 1) / KT;
         tile0 = max(pos - at - ATT_ITEM_COST, 0);
         tile1 = min(end - at - ATT_ITEM_COST, ntiles);
     }
@@ -196,7 +199,7 @@ struct AttIter {
         load_seq(p);
         rp = 0;
         if (n > g.group)
-            for (int t; off >= (t = att_cost(p, g, ctx, n, rp)); ++rp) off -= t;
+            for (int t; off >= (t = att_cost<KT>(p, g, ctx, n, rp)); ++rp) off -= t;
         at = pos - off;
         load_item(p, g);
         if (tile0 >= tile1) next(p, g);
@@ -247,7 +250,7 @@ struct AttWork {
     unsigned* n_joins;  // their number; back at 0 after it
     unsigned* n_done;   // its CTAs that are done
     unsigned* err;
-    int32_t page_box;   // tokens of one copied box: min(page, ATT_KT)
+    int32_t page_box;   // tokens of one copied box: min(page, KT)
     int32_t k_stages, v_stages;
     int32_t q_rows;     // rows of Q a buffer holds, a multiple of 8 (the MMA's other rows are never used)
     int32_t q_box;      // nodes of one copied box of Q
@@ -289,9 +292,10 @@ __device__ __forceinline__ bool att_nonfinite(uint16_t h)
 }
 
 // the segment's first tile that some row sees only in part
+template <int KT>
 __device__ __forceinline__ int att_first_masked(const AttSeg& sg)
 {
-    return max(0, sg.mask_from / ATT_KT - sg.tile0);
+    return max(0, sg.mask_from / KT - sg.tile0);
 }
 
 // zeroes the non-finite ones of a word's two values; true when there was one
@@ -313,7 +317,7 @@ __device__ __forceinline__ void att_clean(AttMisc& ms, unsigned char* tile, uint
                                           bool shared, int s, int quarter, int lane)
 {
     using A = Att<DP>;
-    const int per = shared ? ATT_KT / 8 : ATT_KT / 4, r0 = ((shared ? s * 4 : 0) + quarter) * per;
+    const int per = shared ? A::KT / 8 : A::KT / 4, r0 = ((shared ? s * 4 : 0) + quarter) * per;
     uint32_t bits = 0;
 #pragma unroll 2
     for (int i = 0; i < per; i += 4) {
@@ -322,7 +326,7 @@ __device__ __forceinline__ void att_clean(AttMisc& ms, unsigned char* tile, uint
         if (key >= from) {
 #pragma unroll
             for (int h = 0; h < A::NH; ++h) {
-                uint4* a = (uint4*)(tile + (h * ATT_KT + r) * 128) + (lane & 7);
+                uint4* a = (uint4*)(tile + (h * A::KT + r) * 128) + (lane & 7);
                 if (key >= end) {
                     *a = make_uint4(0, 0, 0, 0);
                     continue;
@@ -383,7 +387,7 @@ __global__ void __launch_bounds__(Att<DP>::THREADS, 1)
 {
     using A = Att<DP>;
     using H = Half2<F16>;
-    constexpr int KT = ATT_KT, NS = A::NS, NH = A::NH;
+    constexpr int KT = A::KT, NS = A::NS, NH = A::NH;
     const uint32_t KS = w.k_stages, VS = w.v_stages;
     extern __shared__ unsigned char att_raw[];
     const uint32_t raw = smem_u32(att_raw);
@@ -391,7 +395,7 @@ __global__ void __launch_bounds__(Att<DP>::THREADS, 1)
     unsigned char* const q_smem = att_raw + (((raw + 1023u) & ~1023u) - raw);
     const uint32_t q_bytes = w.q_rows * DP * 2;
     unsigned char* const k_smem = q_smem + NS * q_bytes;
-    unsigned char* const v_smem = k_smem + KS * A::KB * A::UNIT;
+    unsigned char* const v_smem = k_smem + KS * A::UNIT;
     AttMisc& ms = *reinterpret_cast<AttMisc*>(q_smem + A::ROOM);
     const TreeAttendParams& p = w.p;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -408,7 +412,7 @@ __global__ void __launch_bounds__(Att<DP>::THREADS, 1)
     if (warp == 1) {
         if (lane < ATT_STAGES) {
             mbar_init(&ms.k_full[lane], 1);
-            mbar_init(&ms.k_empty[lane], 1);
+            mbar_init(&ms.k_empty[lane], NS);
             mbar_init(&ms.v_full[lane], 1);
             mbar_init(&ms.v_empty[lane], 1);
             mbar_init(&ms.v_clean[lane], 4 * NS);
@@ -465,7 +469,7 @@ __global__ void __launch_bounds__(Att<DP>::THREADS, 1)
 #pragma unroll 4
         for (int b = seq0; b < seq1; ++b) {
             const SeqLen l = tree_len(p.s, b);
-            sum += att_head_cost(p, w.g, l.ctx, l.n);
+            sum += att_head_cost<KT>(p, w.g, l.ctx, l.n);
         }
         int before = sum;
 #pragma unroll
@@ -483,14 +487,14 @@ __global__ void __launch_bounds__(Att<DP>::THREADS, 1)
         if (mine)
             for (;; ++first_b) {
                 const SeqLen l = tree_len(p.s, first_b);
-                const int t = att_head_cost(p, w.g, l.ctx, l.n);
+                const int t = att_head_cost<KT>(p, w.g, l.ctx, l.n);
                 if (off < t) break;
                 off -= t;
             }
         const int who = __ffs(__ballot_sync(0xffffffffu, mine)) - 1;
         first_b = __shfl_sync(0xffffffffu, first_b, max(who, 0));
         off = __shfl_sync(0xffffffffu, off, max(who, 0));
-        AttIter it;
+        AttIter<KT> it;
         it.start(p, w.g, busy ? pos0 : 0, busy ? split.start(blockIdx.x + 1) : 0, head0, first_b, off);
         for (uint32_t k = 0; ok; ++k) {
             const uint32_t slot = k % ATT_SEGS;
@@ -542,13 +546,12 @@ __global__ void __launch_bounds__(Att<DP>::THREADS, 1)
         uint64_t *const full = is_k ? ms.k_full : ms.v_full, *const empty = is_k ? ms.k_empty : ms.v_empty;
         const uint32_t stages = is_k ? KS : VS;
         const int page_mask = (1 << p.s.page_log2) - 1;
-        const int per = is_k ? A::KB : 1, rows = per * KT;  // tiles, and keys, of a stage
         uint32_t n = 0, st = 0, round = 0, qi = 0;  // stages filled, the next one; row tiles of Q
         for (uint32_t k = 0; ok && !w.stall; ++k) {
             const AttSeg& sg = segment(k);
             const int nt = sg.nt, b = sg.b, hk = sg.hk, tile0 = sg.tile0;
             if (!ok || nt == 0) break;
-            const int last_key = min(sg.limit, (tile0 + nt) * KT);
+            const int last_key = sg.limit;
             // page ids come 32 at a time, one load per block of the table row and one
             // block ahead: a lookup per tile would put its latency between the copies
             const int32_t* table = p.table + (int64_t)b * p.s.width;
@@ -558,7 +561,7 @@ __global__ void __launch_bounds__(Att<DP>::THREADS, 1)
                 return i < pages ? __ldg(table + i) : -1;
             };
             int blk = (tile0 * KT >> p.s.page_log2) >> 5, cur = ids(blk), ahead = ids(blk + 1);
-            for (int t = 0; t < nt; t += per) {
+            for (int t = 0; t < nt; ++t) {
                 const int kb = (tile0 + t) * KT, first = kb >> p.s.page_log2;
                 if ((first >> 5) != blk) {
                     ++blk;
@@ -567,17 +570,15 @@ __global__ void __launch_bounds__(Att<DP>::THREADS, 1)
                 }
                 wait(&empty[st], round + 1);  // at once in the first round
                 if (!ok) break;
-                const int boxes = (min(rows, last_key - kb) + w.page_box - 1) / w.page_box;
+                const int boxes = (min(KT, last_key - kb) + w.page_box - 1) / w.page_box;
                 if (elect_one()) mbar_arrive_expect_tx(&full[st], (uint32_t)(boxes * w.page_box * 128 * NH));
-                // at most 16 pages, so in this block of ids or the next
-                const int key = kb + lane * w.page_box, at = key >> p.s.page_log2;
-                const int page0 = __shfl_sync(0xffffffffu, cur, at & 31);
-                const int page1 = __shfl_sync(0xffffffffu, ahead, at & 31);
-                unsigned char* dst = ring + st * per * A::UNIT + lane * w.page_box * 128;
+                // a tile's pages (at most 16) lie in one block
+                const int key = kb + lane * w.page_box;
+                const int page = __shfl_sync(0xffffffffu, cur, (key >> p.s.page_log2) & 31);
+                unsigned char* dst = ring + st * A::UNIT + lane * w.page_box * 128;
                 if (lane < boxes)
                     for (int h = 0; h < NH; ++h)
-                        tma_4d(dst + h * rows * 128, map, h * 64, hk, key & page_mask,
-                               (at >> 5) == blk ? page0 : page1, &full[st]);
+                        tma_4d(dst + h * KT * 128, map, h * 64, hk, key & page_mask, page, &full[st]);
                 ++n;
                 if (++st == stages) st = 0, ++round;
                 if (t > 0 || !is_k) continue;
@@ -618,7 +619,7 @@ __global__ void __launch_bounds__(Att<DP>::THREADS, 1)
             const int dk = p.s.D / 16;  // k-steps of the scores
             uint32_t k_st = 0, k_round = 0, v_st = 0, v_round = 0, qi = 0;  // rings; row tiles of Q
             uint32_t cleaned = 0;             // bit per stage, phases of v_clean so far
-            uint32_t ready = 0;               // bit 2 s + buffer: phases of p_ready
+            uint32_t n[2] = {0, 0};           // tiles of each stream so far
             uint32_t emptied = 0, used = 0;   // bit s: phases of o_empty; the stream has had a segment
             // Q and K are K-major with 8-row groups 1024 bytes apart; V is N-major,
             // 64-column boxes KT rows apart, 8-row groups 1024 bytes apart
@@ -630,50 +631,43 @@ __global__ void __launch_bounds__(Att<DP>::THREADS, 1)
                 const AttSeg& sg = ms.seg[k % ATT_SEGS];
                 until(&ms.seg_full[k % ATT_SEGS], k / ATT_SEGS);
                 if (!ok || sg.nt == 0) break;
-                const int nt = sg.nt, masked = att_first_masked(sg);
+                const int nt = sg.nt, masked = att_first_masked<KT>(sg);
                 const bool dual = sg.dual != 0;
                 mbar_arrive(&ms.seg_empty[k % ATT_SEGS]);
-                // stream s's scores of the block from tile t on, into its buffers from
-                // `buf` on (both, of a block of two tiles)
-                auto scores = [&](int s, int buf, int t) {
+                // the scores of tile t, stream s's i-th from its next
+                auto scores = [&](auto stream, int t, uint32_t i) {
+                    constexpr int s = decltype(stream)::value;
                     if (t >= nt || !ok) return;
-                    const uint32_t q = qi + (dual ? s : 0), qb = q % NS;
+                    const uint32_t q = qi + (dual ? s : 0), qb = q % NS, buf = NS == 1 ? (n[s] + i) & 1 : 0;
                     if (!dual || s == 0) until(&ms.k_full[k_st], k_round);
                     if (t == 0) until(&ms.q_full[qb], q / NS);
                     if (!ok) return;
                     tmem_fence_after();
-                    const uint64_t a = q_desc + qb * (q_bytes / 16), b = k_desc + k_st * (A::KB * A::UNIT / 16);
-                    const uint32_t id = umma_idesc(F16, false, ATT_ROWS, A::KB == 2 && t + 1 < nt ? 2 * KT : KT);
-                    const uint32_t d = tmem + 128 * s + 64 * buf;
+                    const uint64_t a = q_desc + qb * (q_bytes / 16), b = k_desc + k_st * (A::UNIT / 16);
+                    const uint32_t d = tmem + A::s_col(s) + 64 * buf;
+                    constexpr uint32_t ID = umma_idesc(F16, false, ATT_ROWS, KT);
                     auto mma = [&](int x) {
-                        umma_ss(d, a + (x / 4) * q_half + (x % 4) * 2,
-                                b + ((x / 4) * A::KB * KT * 128 + (x % 4) * 32) / 16, id, x > 0);
+                        umma_ss(d, a + (x / 4) * q_half + (x % 4) * 2, b + ((x / 4) * KT * 128 + (x % 4) * 32) / 16, ID,
+                                x > 0);
                     };
-                    if (dk == DP / 16) {
+                    // at most 3 k-steps of the padded head are past the head's own
 #pragma unroll
-                        for (int x = 0; x < DP / 16; ++x) mma(x);
-                    } else {
-                        for (int x = 0; x < dk; ++x) mma(x);
-                    }
-                    umma_commit(&ms.s_full[s][buf]);
-                    if (t + A::KB >= nt) umma_commit(&ms.q_empty[qb]);
-                    if (!dual || s == 1) {
-                        umma_commit(&ms.k_empty[k_st]);
-                        if (++k_st == KS) k_st = 0, ++k_round;
-                    }
+                    for (int x = 0; x < DP / 16 - 3; ++x) mma(x);
+                    if (dk > DP / 16 - 3) mma(DP / 16 - 3);
+                    if (dk > DP / 16 - 2) mma(DP / 16 - 2);
+                    if (dk > DP / 16 - 1) mma(DP / 16 - 1);
+                    umma_commit(&ms.s_full[s][buf]);  // the warpgroup releases the key stage
+                    if (t == nt - 1) umma_commit(&ms.q_empty[qb]);
+                    if ((!dual || s == 1) && ++k_st == KS) k_st = 0, ++k_round;
                 };
-                // with two streams on alternate blocks, the one without the last tile ends
-                // with the block before
-                const int other_end = NS == 2 && !dual ? (nt - 1) / 2 * 2 - 1 : -1;
-                // t = 0: the scores of all buffers; then tile by tile, the values and the
-                // scores that take the place of what they read.  A tile's values in both
-                // streams come before the next tile's: a warpgroup may wait for the
-                // first (v_empty) before it hands over its next.
-                scores(0, 0, 0);
-                scores(NS - 1, 2 - NS, NS == 1 ? 1 : dual ? 0 : 2);
+                // scores of all buffers, then tile by tile the values and the scores that
+                // take the place of what they read
+                const std::integral_constant<int, 0> c0{};
+                const std::integral_constant<int, NS - 1> c1{};
+                scores(c0, 0, 0);
+                if (NS == 1) scores(c0, 1, 1);
+                else scores(c1, dual ? 0 : 1, 0);
                 for (int t = 0; ok && t < nt; ++t) {
-                    const int buf = t & 1;
-                    const bool even = NS == 1 || dual || (t & 2) == 0;  // stream 0 has the tile
                     if (t >= masked) {
                         until(&ms.v_clean[v_st], cleaned >> v_st);
                         cleaned ^= 1u << v_st;
@@ -681,9 +675,9 @@ __global__ void __launch_bounds__(Att<DP>::THREADS, 1)
                         until(&ms.v_full[v_st], v_round);
                     }
                     const uint64_t b = v_desc + v_st * (A::UNIT / 16);
-                    auto unit = [&](auto stream) {
+                    auto values = [&](auto stream) {
                         constexpr int s = decltype(stream)::value;
-                        const bool first = t == (NS == 2 && !dual ? 2 * s : 0);
+                        const bool first = t == (NS == 2 && !dual ? s : 0);
                         if (first) {
                             if ((used >> s) & 1u) {
                                 until(&ms.o_empty[s], emptied >> s);
@@ -691,21 +685,27 @@ __global__ void __launch_bounds__(Att<DP>::THREADS, 1)
                             }
                             used |= 1u << s;
                         }
-                        until(&ms.p_ready[s][buf], ready >> (2 * s + buf));
-                        ready ^= 1u << (2 * s + buf);
-                        if (!ok) return;
-                        tmem_fence_after();
-                        const uint32_t a = tmem + A::s_col(s, 0) + 64 * buf;
+                        const uint32_t buf = NS == 1 ? n[s] & 1 : 0, a = tmem + A::s_col(s) + 64 * buf;
+                        // half by half: the first meets its values while the warpgroup is at
+                        // the second
 #pragma unroll
-                        for (int x = 0; x < KT / 16; ++x)
-                            umma_ts(tmem + A::o_col(s), a + x * 8, b + x * 128, id_o, !first || x > 0);
+                        for (int h = 0; h < NS; ++h) {
+                            until(&ms.p_ready[s][NS == 1 ? buf : h], NS == 1 ? n[s] >> 1 : n[s]);
+                            if (!ok) return;
+                            tmem_fence_after();
+#pragma unroll
+                            for (int x = 0; x < 4; ++x)
+                                umma_ts(tmem + A::o_col(s), a + 64 * h + x * 8, b + (4 * h + x) * 128, id_o,
+                                        !first || h + x > 0);
+                        }
+                        ++n[s];
                         if (!dual || s == 1) umma_commit(&ms.v_empty[v_st]);
-                        if (t == nt - 1 || t == other_end) umma_commit(&ms.o_full[s]);
-                        if (NS == 1) scores(0, buf, t + 2);
-                        else if (buf == 1) scores(s, 0, dual ? t + 1 : t + 3);
+                        if (t + (NS == 2 && !dual ? 2 : 1) >= nt) umma_commit(&ms.o_full[s]);
+                        if (NS == 1) scores(c0, t + 2, 1);
+                        else scores(stream, dual ? t + 1 : t + 2, 0);
                     };
-                    if (even) unit(std::integral_constant<int, 0>{});
-                    if (NS == 2 && (dual || !even)) unit(std::integral_constant<int, NS - 1>{});
+                    if (NS == 1 || dual || !(t & 1)) values(c0);
+                    if (NS == 2 && (dual || (t & 1))) values(c1);
                     if (++v_st == VS) v_st = 0, ++v_round;
                 }
                 qi += dual ? 2 : 1;
@@ -738,7 +738,7 @@ __global__ void __launch_bounds__(Att<DP>::THREADS, 1)
             }
         }
         uint32_t base = 0, cleaned = 0;              // tiles, phases of v_clean (bit per stage)
-        uint32_t n_full = 0, n_full1 = 0;            // phases of s_full (and of a second buffer's)
+        uint32_t n_unit = 0;                         // own tiles
         uint32_t n_seg0 = 0, n_seg1 = 0, n_ml = 0;   // segments of each stream, joins
         for (uint32_t k = 0; ok; ++k) {
             const AttSeg& sg = segment(k);
@@ -749,56 +749,65 @@ __global__ void __launch_bounds__(Att<DP>::THREADS, 1)
             const int rows = min(w.g.tpt, sg.t0 + sg.ntok - t_first) * G;
             const bool active = (warp & 3) * 32 < rows;
             float m = -INFINITY, l = 0.f;
-            int masked = att_first_masked(sg);  // later: the first masked tile not counted in `cleaned`
+            int masked = att_first_masked<KT>(sg);  // later: the first masked tile not counted in `cleaned`
 
-            // two streams on alternate blocks of two tiles, or all tiles
-            const int t_begin = NS == 2 && !dual ? 2 * s : 0, skip = NS == 2 && !dual ? 2 : 0;
-            for (int tile = t_begin; tile < nt && ok; tile += (tile & 1) ? 1 + skip : 1) {
+            const int t_begin = dual ? 0 : s, stride = dual ? 1 : NS;  // all tiles, or alternate ones
+            for (int tile = t_begin; tile < nt && ok; tile += stride, ++n_unit) {
                 const bool part = tile >= masked;  // some row sees the tile only in part
                 const int kb = (sg.tile0 + tile) * KT;
-                const uint32_t buf = tile & 1;
-                const uint32_t s_addr = tmem + A::s_col(s, buf) + lanes;
-                uint32_t see0 = 0, see1 = 0;
+                const uint32_t buf = NS == 1 ? n_unit & 1 : 0, phase = NS == 1 ? n_unit >> 1 : n_unit;
+                const uint32_t s_addr = tmem + A::s_col(s) + lanes + 64 * buf;
+                uint32_t see[KT / 32], some = 0;
                 if (part) {
                     // on their way while the scores are computed
                     const int t = min(t_first + row / G, sg.n - 1);  // rows past the last are never stored
-                    see0 = att_sees(p, sg.b, t, sg.ctx, sg.n, kb);
-                    see1 = att_sees(p, sg.b, t, sg.ctx, sg.n, kb + 32);
+#pragma unroll
+                    for (int y = 0; y < KT / 32; ++y) see[y] = att_sees(p, sg.b, t, sg.ctx, sg.n, kb + 32 * y);
                 }
-                if (NS == 1 && buf == 1) wait(&ms.s_full[s][1], n_full1++);
-                else if (NS == 1 || buf == 0) wait(&ms.s_full[s][0], n_full++);
+                wait(&ms.s_full[s][buf], phase);
                 if (!ok) break;
                 tmem_fence_after();
-                uint32_t vst = 0;
+                // the scores are there, so their keys have been read
+                if (warp == 4 + 4 * s && lane == 0)
+                    mbar_arrive_n(&ms.k_empty[(base + tile) % KS], NS == 2 && !dual ? 2 : 1);
+                const uint32_t vi = base + tile, vst = vi % VS;
                 if (part) {
                     // phases of v_clean of the tiles before this one (the other stream's)
                     for (; masked < tile; ++masked) cleaned ^= 1u << ((base + masked) % VS);
                     ++masked;
-                    vst = (base + tile) % VS;
-                    wait(&ms.v_full[vst], (base + tile) / VS);
+                    wait(&ms.v_full[vst], vi / VS);
                     if (!ok) break;
                     att_clean<F16, DP>(ms, v_smem + vst * A::UNIT, vst, kb, sg.mask_from, sg.ctx + sg.n, dual, s,
                                        warp & 3, lane);
                     wait(&ms.v_clean[vst], cleaned >> vst);
                     if (!ok) break;
                     cleaned ^= 1u << vst;
+                    // hidden scores become -inf in tensor memory
+                    if (active) {
+#pragma unroll 1
+                        for (int y = 0; y < KT / 32; ++y) {
+                            const uint32_t sees = y == 0 ? see[0] : y == 1 ? see[1] : y == 2 ? see[KT / 32 - 2]
+                                                                                          : see[KT / 32 - 1];
+                            if (__all_sync(0xffffffffu, sees == ~0u)) continue;
+                            uint32_t x[32];
+                            tmem_ld<32>(s_addr + 32 * y, x);
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                if (!((sees >> i) & 1u)) x[i] = 0xFF800000u;
+                            tmem_st<32>(s_addr + 32 * y, x);
+                        }
+                        tmem_wait_st();
+                    }
+                    // seen keys with non-finite values (before the tile is handed over: its
+                    // stage may be filled anew after that)
+#pragma unroll
+                    for (int y = 0; y < KT / 32; ++y) some |= see[y] &= *(volatile uint32_t*)&ms.nf[vst][y];
                 }
                 if (active) {
-                    // the row's scores and their maximum; hidden ones become -inf
-                    uint32_t x[KT];
-                    float top;
-                    if (part) {
-                        tmem_ld<KT>(s_addr, x);
-                        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                        for (int i = 0; i < KT; ++i) {
-                            if (!(((i < 32 ? see0 : see1) >> (i & 31)) & 1u)) x[i] = 0xFF800000u;
-                            mx[i & 3] = fmaxf(mx[i & 3], __uint_as_float(x[i]));
-                        }
-                        top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-                    } else {
-                        top = tmem_ld_max<KT>(s_addr, x);
-                    }
+                    // the row's maximum, found by the loads
+                    uint32_t x[64];
+                    float top = tmem_ld_max<64>(s_addr + KT - 64, x);
+                    if (NS == 2) top = fmaxf(top, tmem_ld_max<64>(s_addr, x));
                     // O and l stay in units of the old maximum while the new one is
                     // less than 2^8 above it: p then stays below 2^8
                     const bool grow = top * c > m * c + ATT_LAZY || (m == -INFINITY && top > m);
@@ -807,10 +816,9 @@ __global__ void __launch_bounds__(Att<DP>::THREADS, 1)
                         if (grow) m = top;
                         l *= f;
                         if (tile > t_begin) {
-                            // the P V of the tile before has to be complete (those before these
-                            // scores' block are: the scores were issued after them)
-                            const uint32_t vi = base + tile - 1;
-                            if (NS == 1 || buf == 1) wait(&ms.v_empty[vi % VS], vi / VS);
+                            // every P V before has to be complete.  With two streams it is:
+                            // these scores were issued after the stream's last.
+                            if (NS == 1) wait(&ms.v_empty[(vi - 1) % VS], (vi - 1) / VS);
                             if (!ok) break;
                             tmem_fence_after();
 #pragma unroll 1
@@ -826,36 +834,37 @@ __global__ void __launch_bounds__(Att<DP>::THREADS, 1)
                     const float mc = m == -INFINITY ? 0.f : m * c;
                     const uint64_t c2 = pack2(c, c), mc2 = pack2(-mc, -mc);
                     uint64_t sum[2] = {0ull, 0ull};  // two pairs of partial sums
+#pragma unroll 1
+                    for (int h = 0; h < NS; ++h) {
+                        if (h > 0) tmem_ld<64>(s_addr + 64 * h, x);
 #pragma unroll
-                    for (int i = 0; i < KT / 2; ++i) {
-                        float2 e = unpack2(fma2(pack2u(x[2 * i], x[2 * i + 1]), c2, mc2));
-                        e.x = ex2_fast(e.x);
-                        e.y = ex2_fast(e.y);
-                        sum[i & 1] = add2(sum[i & 1], pack2(e.x, e.y));
-                        x[i] = H::pack(e.x, e.y);
+                        for (int i = 0; i < 32; ++i) {
+                            float2 e = unpack2(fma2(pack2u(x[2 * i], x[2 * i + 1]), c2, mc2));
+                            e.x = ex2_fast(e.x);
+                            e.y = ex2_fast(e.y);
+                            sum[i & 1] = add2(sum[i & 1], pack2(e.x, e.y));
+                            x[i] = H::pack(e.x, e.y);
+                        }
+                        tmem_st<32>(s_addr + 64 * h, *reinterpret_cast<uint32_t(*)[32]>(&x));
+                        tmem_wait_st();
+                        tmem_fence_before();
+                        __syncwarp();
+                        if (lane == 0 && (NS == 1 || h == 0)) mbar_arrive(&ms.p_ready[s][NS == 1 ? buf : 0]);
                     }
-                    tmem_st<32>(s_addr, *reinterpret_cast<uint32_t(*)[32]>(&x));
                     const float2 sums = unpack2(add2(sum[0], sum[1]));
                     l += sums.x + sums.y;
-                    tmem_wait_st();
+                } else if (lane == 0) {
+                    mbar_arrive(&ms.p_ready[s][buf]);
                 }
-                bool some = false;  // seen keys with non-finite values
-                if (part) {
-                    const volatile uint32_t* nf = ms.nf[vst];
-                    see0 &= nf[0];
-                    see1 &= nf[1];
-                    some = active && (see0 | see1);
-                }
-                tmem_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&ms.p_ready[s][buf]);
-                if (part && __any_sync(0xffffffffu, some)) {
+                if (NS == 2 && lane == 0) mbar_arrive(&ms.p_ready[s][1]);
+                if (part && __any_sync(0xffffffffu, active && some)) {
                     // rare: once P V is done (it saw zeros there), O += those values
-                    const uint32_t vi = base + tile;
-                    wait(&ms.v_empty[vi % VS], vi / VS);
+                    wait(&ms.v_empty[vst], vi / VS);
                     if (!ok) break;
                     tmem_fence_after();
-                    att_add_nonfinite<F16>(p, see0, see1, sg.b, sg.hk, kb, o_addr);
+                    att_add_nonfinite<F16>(p, see[0], see[1], sg.b, sg.hk, kb, o_addr);
+                    if (NS == 2)
+                        att_add_nonfinite<F16>(p, see[KT / 32 - 2], see[KT / 32 - 1], sg.b, sg.hk, kb + 64, o_addr);
                 }
             }
             for (; masked < nt; ++masked) cleaned ^= 1u << ((base + masked) % VS);
@@ -863,7 +872,7 @@ __global__ void __launch_bounds__(Att<DP>::THREADS, 1)
             if (!ok) break;
 
             // ---- the segment's end: O of the streams with units
-            const bool two = dual || nt > A::KB;       // stream 1 has some
+            const bool two = dual || nt > 1;           // stream 1 has some
             const bool join = NS == 2 && !dual && two;  // one row tile in two streams
             if (s == 0 || two) wait(&ms.o_full[s], s == 0 ? n_seg0 : n_seg1);
             if (!ok) break;
@@ -1152,14 +1161,13 @@ static cudaError_t att_launch(AttWork w, int num_sms, cudaStream_t s)
     if (e != cudaSuccess) return e;
     const TreeShape& sh = w.p.s;
     w.g.group = A::NS * w.g.tpt;
-    w.page_box = min(1 << sh.page_log2, ATT_KT);
+    w.page_box = min(1 << sh.page_log2, A::KT);
     w.q_box = min(w.g.tpt, sh.T);
     // what Q does not need is for the rings: few rows leave room for more tiles on their way
     w.q_rows = (w.q_box * w.g.G + 7) / 8 * 8;
     const int stages = (A::ROOM - A::NS * w.q_rows * DP * 2) / A::UNIT;
-    // a stage of keys is a block; the values, which wait for the probabilities, get more
-    w.k_stages = min(A::KB == 2 ? max(2, stages / 4) : (stages + 1) / 2, ATT_STAGES);
-    w.v_stages = min(stages - A::KB * w.k_stages, ATT_STAGES);
+    w.k_stages = min((stages + 1) / 2, ATT_STAGES);
+    w.v_stages = min(stages / 2, ATT_STAGES);
     CUtensorMap mq, mk, mv;
     const int64_t qd[3] = {sh.Hq, sh.T, sh.B}, qs[3] = {w.p.q.head, w.p.q.token, w.p.q.seq};
     const int64_t cd[3] = {sh.Hkv, 1 << sh.page_log2, sh.num_pages}, cs[3] = {w.p.c.head, w.p.c.token, w.p.c.page};
@@ -1191,7 +1199,7 @@ bool tree_attend_fits(const TreeShape& sh)
 {
     const int64_t group = (sh.D <= 128 ? 2 : 1) * (ATT_ROWS / (sh.Hq / sh.Hkv));
     const int64_t groups = (sh.T + group - 1) / group;
-    const int64_t tiles = (((int64_t)sh.width << sh.page_log2) + ATT_KT - 1) / ATT_KT + ATT_ITEM_COST;
+    const int64_t tiles = (((int64_t)sh.width << sh.page_log2) + 63) / 64 + ATT_ITEM_COST;
     return (double)sh.B * sh.Hkv * groups * tiles < 2147483648.0;
 }
 
