@@ -195,27 +195,20 @@ template <> __device__ __forceinline__ float tmem_ld_max<64>(uint32_t a, uint32_
     return __uint_as_float(m[0]);
 }
 
-// 32 columns at each of two addresses, one wait for both
-__device__ __forceinline__ void tmem_ld_2x32(uint32_t a, uint32_t b, uint32_t (&v)[32], uint32_t (&u)[32])
+// 16 columns at each of two addresses, one wait for both
+__device__ __forceinline__ void tmem_ld_2x16(uint32_t a, uint32_t b, uint32_t (&v)[16], uint32_t (&u)[16])
 {
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {"
-                 "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-                 "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%64];\n\t"
-                 "tcgen05.ld.sync.aligned.32x32b.x32.b32 {"
-                 "%32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, "
-                 "%48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63}, [%65];\n\t"
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {"
+                 "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%32];\n\t"
+                 "tcgen05.ld.sync.aligned.32x32b.x16.b32 {"
+                 "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%33];\n\t"
                  "tcgen05.wait::ld.sync.aligned;"
                  : "=&r"(v[0]), "=&r"(v[1]), "=&r"(v[2]), "=&r"(v[3]), "=&r"(v[4]), "=&r"(v[5]),
                    "=&r"(v[6]), "=&r"(v[7]), "=&r"(v[8]), "=&r"(v[9]), "=&r"(v[10]), "=&r"(v[11]),
-                   "=&r"(v[12]), "=&r"(v[13]), "=&r"(v[14]), "=&r"(v[15]), "=&r"(v[16]), "=&r"(v[17]),
-                   "=&r"(v[18]), "=&r"(v[19]), "=&r"(v[20]), "=&r"(v[21]), "=&r"(v[22]), "=&r"(v[23]),
-                   "=&r"(v[24]), "=&r"(v[25]), "=&r"(v[26]), "=&r"(v[27]), "=&r"(v[28]), "=&r"(v[29]),
-                   "=&r"(v[30]), "=&r"(v[31]), "=&r"(u[0]), "=&r"(u[1]), "=&r"(u[2]), "=&r"(u[3]),
-                   "=&r"(u[4]), "=&r"(u[5]), "=&r"(u[6]), "=&r"(u[7]), "=&r"(u[8]), "=&r"(u[9]),
-                   "=&r"(u[10]), "=&r"(u[11]), "=&r"(u[12]), "=&r"(u[13]), "=&r"(u[14]), "=&r"(u[15]),
-                   "=&r"(u[16]), "=&r"(u[17]), "=&r"(u[18]), "=&r"(u[19]), "=&r"(u[20]), "=&r"(u[21]),
-                   "=&r"(u[22]), "=&r"(u[23]), "=&r"(u[24]), "=&r"(u[25]), "=&r"(u[26]), "=&r"(u[27]),
-                   "=&r"(u[28]), "=&r"(u[29]), "=&r"(u[30]), "=&r"(u[31])
+                   "=&r"(v[12]), "=&r"(v[13]), "=&r"(v[14]), "=&r"(v[15]), "=&r"(u[0]), "=&r"(u[1]),
+                   "=&r"(u[2]), "=&r"(u[3]), "=&r"(u[4]), "=&r"(u[5]), "=&r"(u[6]), "=&r"(u[7]),
+                   "=&r"(u[8]), "=&r"(u[9]), "=&r"(u[10]), "=&r"(u[11]), "=&r"(u[12]), "=&r"(u[13]),
+                   "=&r"(u[14]), "=&r"(u[15])
                  : "r"(a), "r"(b) : "memory");
 }
 

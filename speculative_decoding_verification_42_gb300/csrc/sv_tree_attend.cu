@@ -55,7 +55,7 @@ namespace sv {
 
 constexpr int ATT_ROWS = 128;                 // rows of a row tile: M of the MMA
 constexpr int ATT_SMEM = 227 * 1024;          // shared memory of a CTA
-constexpr int ATT_MISC = 2048;                // of it: barriers and small tables
+constexpr int ATT_MISC = 3072;                // of it: barriers and small tables
 constexpr uint32_t ATT_TMEM_COLS = 512;
 constexpr int ATT_SEGS = 4;                   // segments handed out ahead
 constexpr uint32_t ATT_WAIT_POLLS = 1u << 17;  // limit of a wait: some seconds (a poll sleeps for microseconds)
@@ -98,12 +98,12 @@ struct __align__(16) AttMisc {
     uint64_t s_full[2][2];         // [stream][buffer] a tile's scores are in tensor memory
     uint64_t p_ready[2][2];        // [stream][half or buffer] probabilities are (and O is scaled)
     uint64_t o_full[2], o_empty[2];  // the segment's O is complete; has been read
-    uint64_t ml_full, ml_empty;    // stream 1's (m, l) for the join
+    uint64_t j_full[4];            // [quarter] both streams' (m, l) are in ml
     uint64_t seg_full[ATT_SEGS], seg_empty[ATT_SEGS];
     uint64_t drain;
     AttSeg seg[ATT_SEGS];
     uint32_t nf[ATT_STAGES][4];    // (masked) value rows of the tile with non-finite elements
-    float2 ml[ATT_ROWS];           // stream 1's (m, l) of a row
+    float2 ml[2][ATT_ROWS];        // [stream] (m, l) of a row, for the join
     uint32_t tmem;
     int32_t failed;
 };
@@ -252,6 +252,8 @@ struct AttWork {
     unsigned* err;
     int32_t page_box;   // tokens of one copied box: min(page, KT)
     int32_t k_stages, v_stages;
+    uint32_t k_inv, v_inv;  // 2^32 over them, rounded up: a product's upper word is the quotient (tiles < 2^29)
+    uint32_t g_inv;         // 2^16 over G, rounded up (row numbers are below 128)
     int32_t q_rows;     // rows of Q a buffer holds, a multiple of 8 (the MMA's other rows are never used)
     int32_t q_box;      // nodes of one copied box of Q
     int32_t stall;
@@ -308,43 +310,66 @@ __device__ __forceinline__ bool clean_word(uint32_t& v)
     return lo || hi;
 }
 
+// + 0 x v in both halves: what is not finite makes the sum NaN
+template <bool F16>
+__device__ __forceinline__ uint32_t add_zero_times(uint32_t v, uint32_t sum)
+{
+    if (F16) asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(sum) : "r"(v), "r"(0u), "r"(sum));
+    else asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(sum) : "r"(v), "r"(0u), "r"(sum));
+    return sum;
+}
+
 // One warp's part of cleaning a masked value tile (keys from kb on): rows from
 // key `end` on become 0, and so does what is not finite, noted in nf.  A tile
-// that both warpgroups read is shared between them.  Eight lanes per 128-byte
-// row of a box.
+// that both warpgroups read is shared between them.  Eight rows at a time, every
+// fourth or eighth eight a warp's, eight lanes per 128-byte row of a box.
 template <bool F16, int DP>
 __device__ __forceinline__ void att_clean(AttMisc& ms, unsigned char* tile, uint32_t st, int kb, int from, int end,
                                           bool shared, int s, int quarter, int lane)
 {
     using A = Att<DP>;
-    const int per = shared ? A::KT / 8 : A::KT / 4, r0 = ((shared ? s * 4 : 0) + quarter) * per;
-    uint32_t bits = 0;
-#pragma unroll 2
-    for (int i = 0; i < per; i += 4) {
-        const int r = r0 + i + (lane >> 3), key = kb + r;
-        bool found = false;
-        if (key >= from) {
+#pragma unroll 1
+    for (int g = (shared ? s * 4 : 0) + quarter; g < A::KT / 8; g += shared ? 8 : 4) {
+        uint32_t bits = 0;
+        if (kb + 8 * g + 7 >= from) {
+            uint4* const a0 = (uint4*)(tile + (8 * g + (lane >> 3)) * 128) + (lane & 7);
+            auto at = [&](int i, int h) { return a0 + (h * A::KT + 4 * i) * 8; };
+            const int key0 = kb + 8 * g + (lane >> 3);
+            uint32_t sum = 0;
 #pragma unroll
-            for (int h = 0; h < A::NH; ++h) {
-                uint4* a = (uint4*)(tile + (h * A::KT + r) * 128) + (lane & 7);
-                if (key >= end) {
-                    *a = make_uint4(0, 0, 0, 0);
-                    continue;
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int h = 0; h < A::NH; ++h) {
+                    uint4 v = make_uint4(0, 0, 0, 0);
+                    if (key0 + 4 * i >= end) *at(i, h) = v;
+                    else if (key0 + 4 * i >= from) v = *at(i, h);
+                    sum = add_zero_times<F16>(v.x, sum);
+                    sum = add_zero_times<F16>(v.y, sum);
+                    sum = add_zero_times<F16>(v.z, sum);
+                    sum = add_zero_times<F16>(v.w, sum);
                 }
-                uint4 x = *a;
-                const bool bad = clean_word<F16>(x.x) | clean_word<F16>(x.y) | clean_word<F16>(x.z) |
-                                 clean_word<F16>(x.w);
-                if (bad) *a = x;
-                found = found || bad;
+            if (__any_sync(0xffffffffu, sum != 0)) {  // rare
+#pragma unroll 1
+                for (int i = 0; i < 2; ++i) {
+                    bool found = false;
+#pragma unroll 1
+                    for (int h = 0; h < A::NH && key0 + 4 * i >= from; ++h) {
+                        uint4 v = *at(i, h);
+                        const bool bad = clean_word<F16>(v.x) | clean_word<F16>(v.y) | clean_word<F16>(v.z) |
+                                         clean_word<F16>(v.w);
+                        if (bad) *at(i, h) = v;
+                        found = found || bad;
+                    }
+                    const uint32_t v = __ballot_sync(0xffffffffu, found);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if ((v >> (8 * j)) & 0xFFu) bits |= 1u << (4 * i + j);
+                }
             }
         }
-        const uint32_t v = __ballot_sync(0xffffffffu, found);
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            if ((v >> (8 * j)) & 0xFFu) bits |= 1u << (i + j);
+        if (lane == 0) ((uint8_t*)ms.nf[st])[g] = (uint8_t)bits;
     }
     fence_async_smem();
-    if (lane < per / 8) ((uint8_t*)ms.nf[st])[r0 / 8 + lane] = (uint8_t)(bits >> (8 * lane));
     __syncwarp();
     if (lane == 0) mbar_arrive_n(&ms.v_clean[st], A::NS == 2 && !shared ? 2 : 1);
 }
@@ -389,6 +414,9 @@ __global__ void __launch_bounds__(Att<DP>::THREADS, 1)
     using H = Half2<F16>;
     constexpr int KT = A::KT, NS = A::NS, NH = A::NH;
     const uint32_t KS = w.k_stages, VS = w.v_stages;
+    auto k_round_of = [&](uint32_t i) { return __umulhi(i, w.k_inv); };
+    auto v_round_of = [&](uint32_t i) { return __umulhi(i, w.v_inv); };
+    auto v_stage_of = [&](uint32_t i) { return i - v_round_of(i) * VS; };
     extern __shared__ unsigned char att_raw[];
     const uint32_t raw = smem_u32(att_raw);
     // tables, Q buffers, rings; Q's unused rows reach into the rings
@@ -425,15 +453,14 @@ __global__ void __launch_bounds__(Att<DP>::THREADS, 1)
                 mbar_init(&ms.p_ready[lane][j], 4);
             }
             mbar_init(&ms.o_full[lane], 1);
-            mbar_init(&ms.o_empty[lane], 4);
+            mbar_init(&ms.o_empty[lane], 4 * NS);
         }
         if (lane < ATT_SEGS) {
             mbar_init(&ms.seg_full[lane], 1);
             mbar_init(&ms.seg_empty[lane], 3 + 4 * NS);
+            mbar_init(&ms.j_full[lane], 2);
         }
         if (lane == 0) {
-            mbar_init(&ms.ml_full, 4);
-            mbar_init(&ms.ml_empty, 4);
             mbar_init(&ms.drain, 1);
             ms.failed = 0;
         }
@@ -724,6 +751,7 @@ __global__ void __launch_bounds__(Att<DP>::THREADS, 1)
         const uint32_t o_addr = tmem + A::o_col(s) + lanes;
         const float c = p.scale * 1.4426950408889634f;
         const int T = p.s.T, Hq = p.s.Hq, D = p.s.D, G = w.g.G;
+        auto node_of = [&]() { return (int)((uint32_t)row * w.g_inv >> 16); };  // row / G
         // nodes that do not exist: zero rows
         {
             const int rows = p.s.B * T, ws = gridDim.x * NS * 4, per = (rows + ws - 1) / ws;
@@ -739,7 +767,7 @@ __global__ void __launch_bounds__(Att<DP>::THREADS, 1)
         }
         uint32_t base = 0, cleaned = 0;              // tiles, phases of v_clean (bit per stage)
         uint32_t n_unit = 0;                         // own tiles
-        uint32_t n_seg0 = 0, n_seg1 = 0, n_ml = 0;   // segments of each stream, joins
+        uint32_t n_o = 0, n_join = 0;                // segments of the stream, joins
         for (uint32_t k = 0; ok; ++k) {
             const AttSeg& sg = segment(k);
             const int nt = sg.nt;
@@ -760,7 +788,7 @@ __global__ void __launch_bounds__(Att<DP>::THREADS, 1)
                 uint32_t see[KT / 32], some = 0;
                 if (part) {
                     // on their way while the scores are computed
-                    const int t = min(t_first + row / G, sg.n - 1);  // rows past the last are never stored
+                    const int t = min(t_first + node_of(), sg.n - 1);  // rows past the last are never stored
 #pragma unroll
                     for (int y = 0; y < KT / 32; ++y) see[y] = att_sees(p, sg.b, t, sg.ctx, sg.n, kb + 32 * y);
                 }
@@ -769,13 +797,13 @@ __global__ void __launch_bounds__(Att<DP>::THREADS, 1)
                 tmem_fence_after();
                 // the scores are there, so their keys have been read
                 if (warp == 4 + 4 * s && lane == 0)
-                    mbar_arrive_n(&ms.k_empty[(base + tile) % KS], NS == 2 && !dual ? 2 : 1);
-                const uint32_t vi = base + tile, vst = vi % VS;
+                    mbar_arrive_n(&ms.k_empty[base + tile - k_round_of(base + tile) * KS], NS == 2 && !dual ? 2 : 1);
+                const uint32_t vi = base + tile, v_round = v_round_of(vi), vst = v_stage_of(vi);
                 if (part) {
                     // phases of v_clean of the tiles before this one (the other stream's)
-                    for (; masked < tile; ++masked) cleaned ^= 1u << ((base + masked) % VS);
+                    for (; masked < tile; ++masked) cleaned ^= 1u << v_stage_of(base + masked);
                     ++masked;
-                    wait(&ms.v_full[vst], vi / VS);
+                    wait(&ms.v_full[vst], v_round);
                     if (!ok) break;
                     att_clean<F16, DP>(ms, v_smem + vst * A::UNIT, vst, kb, sg.mask_from, sg.ctx + sg.n, dual, s,
                                        warp & 3, lane);
@@ -818,7 +846,7 @@ __global__ void __launch_bounds__(Att<DP>::THREADS, 1)
                         if (tile > t_begin) {
                             // every P V before has to be complete.  With two streams it is:
                             // these scores were issued after the stream's last.
-                            if (NS == 1) wait(&ms.v_empty[(vi - 1) % VS], (vi - 1) / VS);
+                            if (NS == 1) wait(&ms.v_empty[v_stage_of(vi - 1)], v_round_of(vi - 1));
                             if (!ok) break;
                             tmem_fence_after();
 #pragma unroll 1
@@ -859,7 +887,7 @@ __global__ void __launch_bounds__(Att<DP>::THREADS, 1)
                 if (NS == 2 && lane == 0) mbar_arrive(&ms.p_ready[s][1]);
                 if (part && __any_sync(0xffffffffu, active && some)) {
                     // rare: once P V is done (it saw zeros there), O += those values
-                    wait(&ms.v_empty[vst], vi / VS);
+                    wait(&ms.v_empty[vst], v_round);
                     if (!ok) break;
                     tmem_fence_after();
                     att_add_nonfinite<F16>(p, see[0], see[1], sg.b, sg.hk, kb, o_addr);
@@ -867,41 +895,36 @@ __global__ void __launch_bounds__(Att<DP>::THREADS, 1)
                         att_add_nonfinite<F16>(p, see[KT / 32 - 2], see[KT / 32 - 1], sg.b, sg.hk, kb + 64, o_addr);
                 }
             }
-            for (; masked < nt; ++masked) cleaned ^= 1u << ((base + masked) % VS);
+            for (; masked < nt; ++masked) cleaned ^= 1u << v_stage_of(base + masked);
             base += nt;
             if (!ok) break;
 
-            // ---- the segment's end: O of the streams with units
-            const bool two = dual || nt > 1;           // stream 1 has some
+            // ---- the segment's end: O of the streams that had tiles
+            const bool two = dual || nt > 1;            // stream 1 had some
             const bool join = NS == 2 && !dual && two;  // one row tile in two streams
-            if (s == 0 || two) wait(&ms.o_full[s], s == 0 ? n_seg0 : n_seg1);
-            if (!ok) break;
-            tmem_fence_after();
-            float m1 = -INFINITY, l1 = 0.f;
-            if (join && s == 1) {
-                // stream 1 hands its maximum and sum over; its O stays until stream 0 has read it
-                if (n_ml > 0) wait(&ms.ml_empty, n_ml - 1);
-                if (!ok) break;
-                ms.ml[row] = make_float2(m, l);
-                tmem_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&ms.ml_full);
-            }
-            if (join && s == 0) {
-                wait(&ms.o_full[1], n_seg1);
-                wait(&ms.ml_full, n_ml);
+            if (s == 0 || two) {
+                wait(&ms.o_full[s], n_o++);
                 if (!ok) break;
                 tmem_fence_after();
-                const float2 o = ms.ml[row];
-                m1 = o.x;
-                l1 = o.y;
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&ms.ml_empty);
-            }
-            n_ml += join;
-            n_seg0 += 1;
-            n_seg1 += two;
-            if (s == 0 || dual) {
+                float m1 = -INFINITY, l1 = 0.f;
+                int d0 = 0, d1 = D;
+                if (join) {
+                    // the streams' maxima and sums meet, and each gives out half of the
+                    // columns.  ml is free again: its readers' o_empty came before this o_full
+                    ms.ml[s][row] = make_float2(m, l);
+                    tmem_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&ms.j_full[warp & 3]);
+                    wait(&ms.j_full[warp & 3], n_join++);
+                    if (!ok) break;
+                    tmem_fence_after();
+                    m = ms.ml[0][row].x;
+                    l = ms.ml[0][row].y;
+                    m1 = ms.ml[1][row].x;
+                    l1 = ms.ml[1][row].y;
+                    const int half = (D / 16 + 1) / 2 * 16;
+                    (s ? d0 : d1) = half;
+                }
                 if (active) {
                     const float mm = fmaxf(m, m1), mr = mm == -INFINITY ? 0.f : mm;
                     float f0 = m == -INFINITY ? 0.f : ex2_fast((m - mr) * c);
@@ -914,53 +937,51 @@ __global__ void __launch_bounds__(Att<DP>::THREADS, 1)
                         f0 *= inv;
                         f1 *= inv;
                     }
-                    const int node = row / G;
-                    const int64_t orow = ((int64_t)sg.b * T + t_first + node) * Hq + sg.hk * G + row - node * G;
+                    const int64_t orow = ((int64_t)sg.b * T + t_first + node_of()) * Hq + sg.hk * G + row - node_of() * G;
                     const int64_t slot = (int64_t)blockIdx.x * 2 + (sg.tile0 > 0 ? 0 : 1);
                     const int prow = (dual ? s * ATT_ROWS : 0) + row;
 #pragma unroll 1
-                    for (int d = 0; d < D; d += 32) {
-                        uint32_t o[32];
+                    for (int d = d0; d < d1; d += 16) {
+                        uint32_t o[16];
                         if (join) {
-                            uint32_t o1[32];
-                            tmem_ld_2x32(o_addr + d, tmem + A::o_col(NS - 1) + lanes + d, o, o1);
+                            uint32_t o1[16];
+                            tmem_ld_2x16(tmem + A::o_col(0) + lanes + d, tmem + A::o_col(NS - 1) + lanes + d, o, o1);
 #pragma unroll
-                            for (int i = 0; i < 32; ++i)
+                            for (int i = 0; i < 16; ++i)
                                 o[i] = __float_as_uint(__uint_as_float(o[i]) * f0 + __uint_as_float(o1[i]) * f1);
                         } else {
-                            tmem_ld<32>(o_addr + d, o);
+                            tmem_ld<16>(o_addr + d, o);
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f0);
+                            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f0);
                         }
                         auto y = [&](int i) { return __uint_as_float(o[i]); };
                         if (!mine) continue;
                         if (whole) {
                             uint4* o16 = (uint4*)((char*)p.out + (orow * D + d) * 2);
 #pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                if (d + 8 * i < D)
-                                    o16[i] = none ? make_uint4(0, 0, 0, 0)
-                                                  : make_uint4(H::pack(y(8 * i), y(8 * i + 1)),
-                                                               H::pack(y(8 * i + 2), y(8 * i + 3)),
-                                                               H::pack(y(8 * i + 4), y(8 * i + 5)),
-                                                               H::pack(y(8 * i + 6), y(8 * i + 7)));
+                            for (int i = 0; i < 2; ++i)
+                                o16[i] = none ? make_uint4(0, 0, 0, 0)
+                                              : make_uint4(H::pack(y(8 * i), y(8 * i + 1)),
+                                                           H::pack(y(8 * i + 2), y(8 * i + 3)),
+                                                           H::pack(y(8 * i + 4), y(8 * i + 5)),
+                                                           H::pack(y(8 * i + 6), y(8 * i + 7)));
                         } else {
                             float4* o32 = (float4*)w.part_o + (slot * (DP / 4) + d / 4) * (NS * ATT_ROWS) + prow;
 #pragma unroll
-                            for (int i = 0; i < 8; ++i)
-                                if (d + 4 * i < D)
-                                    o32[i * NS * ATT_ROWS] =
-                                        make_float4(y(4 * i), y(4 * i + 1), y(4 * i + 2), y(4 * i + 3));
+                            for (int i = 0; i < 4; ++i)
+                                o32[i * NS * ATT_ROWS] =
+                                    make_float4(y(4 * i), y(4 * i + 1), y(4 * i + 2), y(4 * i + 3));
                         }
                     }
-                    if (mine && whole && p.lse) p.lse[orow] = none ? -INFINITY : fmaf(mr, p.scale, logf(ll));
-                    if (mine && !whole) w.part_ml[slot * NS * ATT_ROWS + prow] = make_float2(mm, ll);
+                    const bool first = s == 0 || dual;
+                    if (first && mine && whole && p.lse) p.lse[orow] = none ? -INFINITY : fmaf(mr, p.scale, logf(ll));
+                    if (first && mine && !whole) w.part_ml[slot * NS * ATT_ROWS + prow] = make_float2(mm, ll);
                 }
                 tmem_fence_before();
                 __syncwarp();
                 if (lane == 0) {
-                    mbar_arrive(&ms.o_empty[s]);
-                    if (join) mbar_arrive(&ms.o_empty[1]);
+                    mbar_arrive_n(&ms.o_empty[s], NS == 2 && !join ? 2 : 1);
+                    if (join) mbar_arrive(&ms.o_empty[1 - s]);
                 }
             }
             release(k);
@@ -1168,6 +1189,9 @@ static cudaError_t att_launch(AttWork w, int num_sms, cudaStream_t s)
     const int stages = (A::ROOM - A::NS * w.q_rows * DP * 2) / A::UNIT;
     w.k_stages = min((stages + 1) / 2, ATT_STAGES);
     w.v_stages = min(stages / 2, ATT_STAGES);
+    w.k_inv = 0xFFFFFFFFu / w.k_stages + 1;
+    w.v_inv = 0xFFFFFFFFu / w.v_stages + 1;
+    w.g_inv = 0xFFFFu / w.g.G + 1;
     CUtensorMap mq, mk, mv;
     const int64_t qd[3] = {sh.Hq, sh.T, sh.B}, qs[3] = {w.p.q.head, w.p.q.token, w.p.q.seq};
     const int64_t cd[3] = {sh.Hkv, 1 << sh.page_log2, sh.num_pages}, cs[3] = {w.p.c.head, w.p.c.token, w.p.c.page};
