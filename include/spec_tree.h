@@ -193,7 +193,9 @@ spec_status spec_tree_append(spec_tree_t h, const spec_tree_append_args* a, void
  * its values.  lse is the natural logarithm of the sum of exp over the scores.
  * A node that sees nothing, whose finite sum is 0, or with j >= n_b has a zero
  * row and lse = -inf; so has every node of a sequence with ctx < 0, n outside
- * [0, T] or ctx + n beyond the table.  Scores, sums and outputs accumulate in
+ * [0, T] or ctx + n beyond the table.  Keys and values of a page outside the
+ * cache are zeros (a sequence that spec_tree_plan left without pages: its rows
+ * have no meaning).  Scores, sums and outputs accumulate in
  * fp32; the probabilities are rounded to the 16-bit type before they meet V.
  * SPEC_ERR_UNSUPPORTED when q, the cache, out or lse is not on 16 bytes, a
  * stride is not a multiple of 8 elements (or is beyond 2^36), or is 0 for a
@@ -221,7 +223,9 @@ spec_status spec_tree_attend(spec_tree_t h, const spec_tree_attend_args* a, void
  * is strictly ascending within [0, n_b) (a node's parent comes before it, so
  * a path from a root is).  A sequence with a path that is not, or with lengths
  * outside their ranges, keeps its cache and length and gets SPEC_ROW_BAD_TREE
- * or SPEC_ROW_BAD_LEN.  Pages of different sequences must be different.
+ * or SPEC_ROW_BAD_LEN.  Pages of different sequences must be different, and a
+ * sequence that spec_tree_plan left without pages is given path_len 0: its
+ * table row does not reach its nodes.
  * SPEC_ERR_UNSUPPORTED when the cache is not on 16 bytes or a stride is not a
  * multiple of 8 elements. */
 typedef struct {

@@ -228,18 +228,21 @@ class TreeCache:
         rec.layers = shape[0] if many else 1
         rec.layer_stride = st[0] if many and shape[0] > 1 else 0
 
-    def _stream(self, stream):
+    def _stream(self):
         # the address of the current stream, without an object for it where torch can tell
-        if stream is None:
-            return self._current_stream(self.device)
-        return stream.cuda_stream
+        return self._current_stream(self.device)
 
-    @staticmethod
-    def _used_on(stream, tensors):
-        # allocated on the current stream, written on another: their memory must not be
-        # reused before that stream is done with it
-        for t in tensors:
-            t.record_stream(stream)
+    def _on(self, stream, op, *args, **kw):
+        # A call on another stream: its new outputs come from that stream's memory (the
+        # current stream's may still be read by kernels in flight there), and are noted as
+        # used by the current stream, which the caller is likely to read them on.
+        import torch
+        with torch.cuda.stream(stream):
+            res = op(*args, **kw)
+        here = torch.cuda.current_stream(self.device)
+        for t in res.values() if isinstance(res, dict) else (res,):
+            t.record_stream(here)
+        return res
 
     def _out(self, out, key, shape, dtype, like=None):
         """The caller's output tensor (checked), or a new one (like `like`, a contiguous
@@ -269,6 +272,9 @@ class TreeCache:
         include/spec_tree.h); updates free_pages and block_table in place and
         returns held, ring, slot_map, positions, row_status (and tree_mask with
         parents).  T is parents.shape[1], or max_tokens for chains."""
+        if stream is not None:
+            return self._on(stream, self.plan, ctx_len, n_tokens, held, ring, free_pages, block_table,
+                            parents=parents, max_tokens=max_tokens, out=out)
         import torch
         i32, a = torch.int32, self._plan_args
         B = ctx_len.shape[0]
@@ -295,9 +301,7 @@ class TreeCache:
         a.held_out, a.ring_out = res["held"].data_ptr(), res["ring"].data_ptr()
         a.slot_map, a.positions = res["slot_map"].data_ptr(), res["positions"].data_ptr()
         a.row_status = res["row_status"].data_ptr()
-        _check(self._lib.spec_tree_plan(self.h, a, self._stream(stream)), "spec_tree_plan")
-        if stream is not None:
-            self._used_on(stream, res.values())
+        _check(self._lib.spec_tree_plan(self.h, a, self._stream()), "spec_tree_plan")
         return res
 
     def append(self, q, k, v, k_cache, v_cache, slot_map, positions=None, n_tokens=None, *,
@@ -306,6 +310,10 @@ class TreeCache:
         """Norm and rotation of q and k, k and v into the cache; returns the
         new q [B, T, q_heads, head_dim].  cos_sin: float32 [positions, rot_dim],
         rot_dim / 2 cosines, then as many sines."""
+        if stream is not None:
+            return self._on(stream, self.append, q, k, v, k_cache, v_cache, slot_map, positions, n_tokens,
+                            q_weight=q_weight, k_weight=k_weight, eps=eps, cos_sin=cos_sin,
+                            interleaved=interleaved, out=out)
         import torch
         i32, a, d, hkv = torch.int32, self._append_args, self._d, self._hkv
         B, T = q.shape[:2]
@@ -332,9 +340,7 @@ class TreeCache:
             a.q_out = out.data_ptr()
         else:
             a.q_out = self._tensor(out, shape, self.dtype, "out")
-        _check(self._lib.spec_tree_append(self.h, a, self._stream(stream)), "spec_tree_append")
-        if stream is not None:
-            self._used_on(stream, (out,))
+        _check(self._lib.spec_tree_append(self.h, a, self._stream()), "spec_tree_append")
         return out
 
     def attend(self, q, k_cache, v_cache, block_table, ctx_len, n_tokens=None, *, tree_mask=None,
@@ -343,6 +349,9 @@ class TreeCache:
         """Attention of the nodes over context and tree (or, without tree_mask,
         over context and chain); scale defaults to head_dim ** -0.5.  Returns
         out [B, T, q_heads, head_dim] and, with lse, lse [B, T, q_heads]."""
+        if stream is not None:
+            return self._on(stream, self.attend, q, k_cache, v_cache, block_table, ctx_len, n_tokens,
+                            tree_mask=tree_mask, scale=scale, out=out, lse=lse)
         import torch
         i32, a = torch.int32, self._attend_args
         B, T = q.shape[:2]
@@ -361,9 +370,7 @@ class TreeCache:
         if lse:
             e = res["lse"] = self._out(out, "lse", shape[:3], torch.float32)
             a.lse = e.data_ptr()
-        _check(self._lib.spec_tree_attend(self.h, a, self._stream(stream)), "spec_tree_attend")
-        if stream is not None:
-            self._used_on(stream, res.values())
+        _check(self._lib.spec_tree_attend(self.h, a, self._stream()), "spec_tree_attend")
         return res
 
     def keep(self, k_cache, v_cache, block_table, ctx_len, n_tokens, path, path_len, *,
@@ -371,6 +378,9 @@ class TreeCache:
         """Move the accepted nodes' keys and values behind the context, in all
         layers of [layers, num_pages, page_size, kv_heads, head_dim] caches (or
         in one layer's); returns the new ctx_len and row_status."""
+        if stream is not None:
+            return self._on(stream, self.keep, k_cache, v_cache, block_table, ctx_len, n_tokens, path,
+                            path_len, out=out)
         import torch
         i32, a = torch.int32, self._keep_args
         B, T = path.shape
@@ -385,14 +395,12 @@ class TreeCache:
         res = {"ctx_len": self._out(out, "ctx_len", b, i32, ctx_len),
                "row_status": self._out(out, "row_status", b, i32, ctx_len)}
         a.ctx_out, a.row_status = res["ctx_len"].data_ptr(), res["row_status"].data_ptr()
-        _check(self._lib.spec_tree_keep(self.h, a, self._stream(stream)), "spec_tree_keep")
-        if stream is not None:
-            self._used_on(stream, res.values())
+        _check(self._lib.spec_tree_keep(self.h, a, self._stream()), "spec_tree_keep")
         return res
 
     def check(self, stream=None) -> int:
         """SPEC_OK, or SPEC_ERR_TIMEOUT when a wait of an attend ran out."""
-        return spec_tree_check(self.h, self._stream(stream))
+        return spec_tree_check(self.h, self._stream() if stream is None else stream.cuda_stream)
 
 
 __all__ = [n for n in dir() if n.startswith("spec_tree_") or n.startswith("SPEC_")] + ["TreeCache"]

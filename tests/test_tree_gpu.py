@@ -395,6 +395,34 @@ def test_attend_is_deterministic_and_stream_ordered(sv):
     tc.close()
 
 
+def test_outputs_of_another_stream_take_no_memory_in_use(sv):
+    """Outputs of a call with stream= are not put where kernels in flight on the
+    current stream still read."""
+    import torch
+    rng = np.random.default_rng(15)
+    B, T, H, D = 2, 300, 16, 128
+    tc = _tc(sv, B, T, H, 4, D, 16, 80, 40)
+    kc, vc = _layout(rng, 80, 16, 4, D, "bf16", "tokens")
+    q, k, v = (_rand(rng, (B, T, h, D), "bf16") for h in (H, 4, 4))
+    table, ctx, slots = _i32(np.arange(80).reshape(2, 40)), _i32([300, 5]), _i32(np.full((B, T), -1))
+    calls = (lambda s: tc.attend(q, kc, vc, table, ctx, stream=s)["out"],
+             lambda s: tc.append(q, k, v, kc, vc, slots, stream=s))
+    side, seen = torch.cuda.Stream(), torch.empty_like(q)
+    for call in calls:
+        first = call(None)
+        torch.cuda.synchronize()
+        x = torch.full_like(q, 3.0)
+        torch.cuda.synchronize()
+        torch.cuda._sleep(20_000_000)  # some milliseconds
+        torch.add(x, 0, out=seen)
+        del x
+        second = call(side)
+        torch.cuda.synchronize()
+        assert (seen == 3.0).all()
+        assert torch.equal(first, second)
+    tc.close()
+
+
 def test_stalled_attend_reports_and_recovers(sv):
     import torch
     rng = np.random.default_rng(12)
