@@ -4,11 +4,12 @@
 // For a key head the query rows of one sequence are its nodes times the G
 // query heads that share the head: out[r] = sum_k p[r][k] V[k] / sum_k p[r][k],
 // p = exp(scale q[r] . K[k]) over the keys row r sees.  One pass over the keys
-// with the running maximum m and sum l of each row: a tile of 64 keys gives
+// with the running maximum m and sum l of each row: a tile of keys gives
 // S = Q K^T (tensor cores, fp32), p = 2^(c S - c m) with c = scale log2(e),
-// l += sum p and O += P V (tensor cores, P rounded to the 16-bit type, O fp32
-// in tensor memory); when m grows by more than 2^8 would allow, O and l are
-// scaled down first.
+// l += sum p and O += P V (tensor cores, O fp32 in tensor memory); when m grows
+// by more than 2^8 would allow, O and l are scaled down first.  P is rounded to
+// the 16-bit type, the only one that meets a 16-bit V in an MMA: half an ulp of
+// each p (2^-9 of it in bf16), while l takes p before the rounding.
 //
 // The bound is HBM for up to about 256 rows per key head (each key's 4 D bytes
 // are read once per 256 rows and cost 4 D products per row), the tensor cores
@@ -17,25 +18,41 @@
 //    MMA, whatever their number: the tensor pipe has time for 128 rows while
 //    the keys stream, so few rows need no other form.
 //  * Work items are (key head, sequence, group of row tiles).  All items' key
-//    tiles in a row are cut into equal ranges, one per SM, whatever the batch:
-//    a long cache with few rows fills the machine, a ragged batch is balanced,
-//    and the lengths are read on the GPU.  An item cut by a range's end leaves
-//    partial sums (O, m, l) that k_tree_combine joins.  The key head comes
-//    first, so that the SMs of all heads go through the same pages together.
+//    tiles in a row are cut into ranges of equal cost, one per SM, whatever the
+//    batch: a long cache with few rows fills the machine, a ragged batch is
+//    balanced, and the lengths are read on the GPU.  An item cut by a range's
+//    end leaves partial sums (O, m, l) that k_tree_combine joins.  The key head
+//    comes first, so that the SMs of all heads go through the same pages
+//    together.
 //  * A CTA has a scheduling warp (it walks the range and hands the others one
 //    segment of an item at a time, which keeps that state out of their
 //    registers), two producer warps (tensor-map copies of whole pages into
-//    rings of 128-byte-swizzled key and value tiles), an MMA issuer and one or
-//    two softmax warpgroups, a thread per row.
-//  * A stream (an O in tensor memory and its warpgroup) has two buffers for the
-//    scores of a 64-key tile; probabilities take the place of their scores.
-//    The values of one meet their probabilities while the warpgroup is at the
-//    other.  Heads up to 128 elements fill both with one MMA of 128 keys, which
-//    reads less shared memory than two of 64 (Q is read for each).  Heads up to 128
-//    elements have two streams: an item of one row tile gives its even key
-//    tiles to one and its odd ones to the other (own m, l, O; joined at the
-//    end), an item of two row tiles gives each stream a row tile and reads the
-//    keys once for both.  Larger heads fill tensor memory with one stream.
+//    rings of 128-byte-swizzled key and value tiles; what few rows of Q leave
+//    free is more stages), an MMA issuer and one or two softmax warpgroups, a
+//    thread per row.
+//  * Heads up to 128 elements have two streams (an O in tensor memory, the
+//    scores of a tile of 128 keys, and a warpgroup): an item of one row tile
+//    gives its even key tiles to one and its odd ones to the other (own m, l, O;
+//    joined at the end, each warpgroup half of the columns), an item of two row
+//    tiles gives each stream a row tile and reads the keys once for both.
+//    Probabilities take the place of their scores and are handed over in halves:
+//    the first meets its values while the warpgroup is at the second.  Tiles of
+//    128 keys, as one MMA reads Q from shared memory once for 128 keys (64
+//    cycles against twice 48).  Larger heads fill tensor memory with one stream,
+//    whose two score buffers of 64 keys take turns.
+//
+// Measured (bf16, 8 key heads of 128 elements, L2 flushed; bytes of K and V):
+// 256 sequences of one token and 2048 keys each 345 us, 6.3 TB/s (0.92 of a
+// copy); 64 of 9 tokens, 4 heads to a key head and up to 4096 keys 122 us, 4.7
+// TB/s; one of 32 tokens, 8 heads to a key head and 260000 keys 204 us, 5.2 TB/s
+// and 1.05 PFLOP/s: the chain scores, softmax, values of 256 rows takes some
+// 3200 cycles a tile, of which the MMAs are 2048; a prompt of 4 x 1500 tokens
+// 195 us.  An item costs some four tiles beside its keys: the masked tile, the
+// output and the first softmax of the next are a chain that the rings cover in
+// part (one token and 500 keys: 20 us; 6 chains of 333 f16 tokens of 80 elements
+// 62 us).
+// Two warpgroups a stream, half of a tile's keys each, were slower (238 us where
+// this takes 204): a row's 2^x are bound by their unit, not by their chain.
 //
 // What a row does not see must not touch it, whatever it holds: scores are
 // replaced by -inf before the maximum, but P V multiplies hidden values by a
@@ -118,7 +135,9 @@ struct AttGeom {
 };
 
 // The ranges are equal in cost, not in tiles: an item costs its key tiles and
-// ATT_ITEM_COST more (its first scores, its masked tile and its output).
+// ATT_ITEM_COST more (its first scores, its masked tile and its output).  With
+// 2, 3, 4 and 5, 6 chains of 333 tokens take 65.6, 57.8, 55.5 and 57.6 us, a
+// prompt of 4 x 1500 tokens 199, 192, 191 and 189 us, long caches the same.
 constexpr int ATT_ITEM_COST = 4;
 
 // keys that some row of item `rp` of a sequence sees: a chain's rows see
@@ -233,12 +252,18 @@ struct __align__(16) AttJoin {
     int32_t sub;
     int32_t pad;
 };
-// few parts: a task is 8 warps times 32 rows by 32 columns; many: 32 rows by 8
+// Up to `few` parts: a task is 8 warps times 32 rows by 32 columns; more: 32 rows
+// by 8.  A batch's cuts leave two or three parts, whose loads a warp has in flight
+// at once; one sequence's long cache leaves up to one per SM, which one warp would
+// add one after the other.  Always the first form: 8 tokens on one key head over
+// 100000 keys take 110 us and not 25; always the second: 16 x 64 tokens over 8000
+// keys 247 us and not 168.  Where all tasks of the second form have a CTA each,
+// nothing is gained by the first (one token over 500 keys: 14.5 us, with it 16.5).
 constexpr int ATT_FEW = 8;
-__host__ __device__ __forceinline__ int att_join_tasks(int parts, int rows, int D)
+__host__ __device__ __forceinline__ int att_join_tasks(int parts, int rows, int D, int few)
 {
     const int rb = (rows + 31) / 32;
-    return parts <= ATT_FEW ? (rb * ((D + 31) / 32) + 7) / 8 : rb * (D / 8);
+    return parts <= few ? (rb * ((D + 31) / 32) + 7) / 8 : rb * (D / 8);
 }
 
 struct AttWork {
@@ -256,6 +281,7 @@ struct AttWork {
     uint32_t g_inv;         // 2^16 over G, rounded up (row numbers are below 128)
     int32_t q_rows;     // rows of Q a buffer holds, a multiple of 8 (the MMA's other rows are never used)
     int32_t q_box;      // nodes of one copied box of Q
+    int32_t few;        // most parts that are joined in the first form
     int32_t stall;
 };
 
@@ -554,7 +580,7 @@ __global__ void __launch_bounds__(Att<DP>::THREADS, 1)
                 const int first = split.owner(it.at + ATT_ITEM_COST);
                 if (first == (int)blockIdx.x - 1) {
                     const int last = split.owner(it.at + ATT_ITEM_COST + it.ntiles - 1), rows = it.ntok * w.g.G;
-                    const int tasks = att_join_tasks(last - first + 1, rows, p.s.D);
+                    const int tasks = att_join_tasks(last - first + 1, rows, p.s.D, w.few);
                     unsigned at = 0;
                     if (lane == 0) at = atomicAdd(w.n_joins, (unsigned)tasks);
                     at = __shfl_sync(0xffffffffu, at, 0);
@@ -1034,7 +1060,7 @@ __global__ void __launch_bounds__(COMB_THREADS, COMB_CTAS_PER_SM)
             const int node = r / G;
             return ((int64_t)jn.b * p.s.T + jn.t0 + node) * p.s.Hq + jn.hk * G + r - node * G;
         };
-        if (n <= ATT_FEW) {
+        if (n <= w.few) {
             const int c32 = (D + 31) / 32, sub = jn.sub * 8 + g, rb = sub / c32, col4 = (sub - rb * c32) * 8;
             const int r = rb * 32 + lane, pr = part_row(r);
             if (r >= jn.rows) continue;
@@ -1150,7 +1176,7 @@ size_t tree_attend_bytes(int D, int ctas, size_t* ml_at, size_t* join_at)
     const size_t ml = slots * att_part_rows(DP) * sizeof(float2);
     *ml_at = o;
     *join_at = o + ml;
-    const int most = att_join_tasks(ATT_FEW + 1, att_part_rows(DP), DP);  // of a cut
+    const int most = att_join_tasks(1, att_part_rows(DP), DP, 0);  // of a cut
     return o + ml + 16 + (size_t)ctas * most * sizeof(AttJoin);
 }
 
@@ -1199,17 +1225,17 @@ static cudaError_t att_launch(AttWork w, int num_sms, cudaStream_t s)
         !att_map(&mk, F16, w.p.c.k, sh.D, cd, cs, 1, w.page_box) ||
         !att_map(&mv, F16, w.p.c.v, sh.D, cd, cs, 1, w.page_box))
         return cudaErrorInvalidValue;
+    // an item's parts may lie in all ranges; the second form has the more tasks
+    const int64_t items = (int64_t)sh.B * sh.Hkv * ((sh.T + w.g.group - 1) / w.g.group);
+    const int64_t tasks = items * att_join_tasks(1, w.q_rows * A::NS, sh.D, 0), ctas = num_sms * COMB_CTAS_PER_SM;
+    w.few = tasks <= ctas ? 0 : ATT_FEW;
     k_tree_attend<F16, DP><<<num_sms, A::THREADS, ATT_SMEM, s>>>(mq, mk, mv, w);
-    if ((e = cudaGetLastError()) != cudaSuccess || num_sms == 1) return e;
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
-    // no more CTAs than there can be tasks: the items', each with parts in all ranges
-    const int64_t items = (int64_t)sh.B * sh.Hkv * ((sh.T + w.g.group - 1) / w.g.group);
-    const int most = std::max(att_join_tasks(ATT_FEW, w.q_rows * A::NS, sh.D),
-                              att_join_tasks(ATT_FEW + 1, w.q_rows * A::NS, sh.D));
-    cfg.gridDim = dim3((unsigned)std::min<int64_t>(items * most, num_sms * COMB_CTAS_PER_SM));
+    cfg.gridDim = dim3((unsigned)std::min(tasks, ctas));  // no more CTAs than there can be tasks
     cfg.blockDim = dim3(COMB_THREADS);
     cfg.stream = s;
     cfg.attrs = at;
