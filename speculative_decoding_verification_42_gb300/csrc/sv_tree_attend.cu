@@ -41,16 +41,20 @@
 //    cycles against twice 48).  Larger heads fill tensor memory with one stream,
 //    whose two score buffers of 64 keys take turns.
 //
-// Measured (bf16, 8 key heads of 128 elements, L2 flushed; bytes of K and V):
-// 256 sequences of one token and 2048 keys each 345 us, 6.3 TB/s (0.92 of a
-// copy); 64 of 9 tokens, 4 heads to a key head and up to 4096 keys 122 us, 4.7
-// TB/s; one of 32 tokens, 8 heads to a key head and 260000 keys 204 us, 5.2 TB/s
-// and 1.05 PFLOP/s: the chain scores, softmax, values of 256 rows takes some
-// 3200 cycles a tile, of which the MMAs are 2048; a prompt of 4 x 1500 tokens
-// 195 us.  An item costs some four tiles beside its keys: the masked tile, the
-// output and the first softmax of the next are a chain that the rings cover in
-// part (one token and 500 keys: 20 us; 6 chains of 333 f16 tokens of 80 elements
-// 62 us).
+// Measured (bf16, 8 key heads of 128 elements, 8 query heads to each where
+// nothing else is said, L2 flushed; bytes of K and V once):
+//   256 sequences of one token over 2048 keys each: 347-355 us, 6.1-6.2 TB/s
+//     (0.91 of a copy);
+//   64 of up to 9 tokens over 100 to 4100 keys: 122-124 us, 4.6 TB/s;
+//   one of 32 tokens over 260000 keys: 202-212 us, 5.2 TB/s and 1.3 PFLOP/s.
+//     The chain scores, softmax, values of 256 rows takes some 3200 cycles a tile,
+//     of which the MMAs are 2048;
+//   16 of up to 64 tokens (two items each) over 4000 to 8191 keys: 175 us, 1.0
+//     PFLOP/s;
+//   6 chains of up to 333 f16 tokens of 7 heads of 80 elements: 61 us;
+//   one token of 4 heads to a key head over 500 keys: 17.5 us.
+// An item costs some four tiles beside its keys: its masked tile, its output and
+// the first softmax of the next item are a chain that the rings cover in part.
 // Two warpgroups a stream, half of a tile's keys each, were slower (238 us where
 // this takes 204): a row's 2^x are bound by their unit, not by their chain.
 //
