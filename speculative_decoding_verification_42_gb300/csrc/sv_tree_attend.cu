@@ -43,7 +43,7 @@
 //
 // Measured (bf16, 8 key heads of 128 elements, 8 query heads to each where
 // nothing else is said, L2 flushed; bytes of K and V once):
-//   256 sequences of one token over 2048 keys each: 347-355 us, 6.1-6.2 TB/s
+//   256 sequences of one token over 100 to 4000 keys: 347-355 us, 6.1-6.2 TB/s
 //     (0.91 of a copy);
 //   64 of up to 9 tokens over 100 to 4100 keys: 122-124 us, 4.6 TB/s;
 //   one of 32 tokens over 260000 keys: 202-212 us, 5.2 TB/s and 1.3 PFLOP/s.
@@ -76,7 +76,7 @@ namespace sv {
 
 constexpr int ATT_ROWS = 128;                 // rows of a row tile: M of the MMA
 constexpr int ATT_SMEM = 227 * 1024;          // shared memory of a CTA
-constexpr int ATT_MISC = 3072;                // of it: barriers and small tables
+constexpr int ATT_MISC = 4096;                // of it: barriers and small tables
 constexpr uint32_t ATT_TMEM_COLS = 512;
 constexpr int ATT_SEGS = 4;                   // segments handed out ahead
 constexpr uint32_t ATT_WAIT_POLLS = 1u << 17;  // limit of a wait: some seconds (a poll sleeps for microseconds)
@@ -1195,10 +1195,15 @@ static bool att_map(CUtensorMap* map, bool f16, const void* ptr, int D, const in
     cuuint64_t st[3];
     // the stride of a dimension of size 1 is never used, but may not be 0
     for (int i = 0; i < 3; ++i) st[i] = dims[i] == 1 ? 16 * (cuuint64_t)((D + 7) / 8) : (cuuint64_t)strides[i] * 2;
+    // L2 fetches 256 bytes at a time where a head's row is a multiple of that (256
+    // sequences of one token, D = 128: 343 us, by 64 bytes 354), else by 64: the rest
+    // of a wider fetch is other heads' (22 x 2 tokens over 7000 keys, 4 key heads, L2
+    // flushed: D = 64 62 -> 52 us, 80 81 -> 67, 96 85 -> 73, 112 99 -> 86, 192 118 -> 110)
+    const auto promotion = D % 128 ? CU_TENSOR_MAP_L2_PROMOTION_L2_64B : CU_TENSOR_MAP_L2_PROMOTION_L2_256B;
     const cuuint32_t box[4] = {64, (cuuint32_t)box1, (cuuint32_t)box2, 1}, one[4] = {1, 1, 1, 1};
     return enc(map, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
                const_cast<void*>(ptr), d, st, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+               promotion, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <bool F16, int DP>
