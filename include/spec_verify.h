@@ -288,8 +288,9 @@ spec_status spec_verify_inject_fault(spec_verify_t h, int32_t fault);
  * alloc / release here: spec_verify_create then calls alloc(ctx, bytes,
  * device, &ptr) with `device` current, which returns 0 and a device pointer
  * aligned to 256 bytes on success and nonzero on failure (create then returns
- * SPEC_ERR_OOM); spec_verify_destroy calls release(ctx, ptr, device).  A
- * handle keeps the functions it was created with.  Passing NULL for both
+ * SPEC_ERR_OOM); spec_verify_destroy calls release(ctx, ptr, device).  Create
+ * zeroes the block on the legacy default stream and waits for it.  A handle
+ * keeps the functions it was created with.  Passing NULL for both
  * restores cudaMalloc / cudaFree.  The setting is process-wide and applies to
  * handles created after the call.  Returns SPEC_ERR_INVALID_ARG when exactly
  * one of the two functions is NULL. */

@@ -245,7 +245,11 @@ spec_status workspace_take(Workspace* w, int device, size_t bytes)
         cudaGetLastError();
         return SPEC_ERR_OOM;
     }
-    if (cudaMemset(base, 0, bytes) != cudaSuccess) {
+    // Waited for: the memset is asynchronous to the host, and a first call on a stream that
+    // does not wait for the legacy one could run before it, or in the middle of it.
+    if (cudaMemsetAsync(base, 0, bytes, cudaStreamLegacy) != cudaSuccess ||
+        cudaStreamSynchronize(cudaStreamLegacy) != cudaSuccess) {
+        cudaGetLastError();
         if (w->alloc_fn) w->release_fn(w->ctx, base, device);
         else cudaFree(base);
         return SPEC_ERR_CUDA;

@@ -37,7 +37,7 @@ struct Workspace {
 };
 
 // `bytes` of zeroed memory on `device` (which must be current), aligned to 256
-// bytes.  SPEC_ERR_OOM, SPEC_ERR_INVALID_ARG (a misaligned block of the
+// bytes; the zeros have arrived when it returns.  SPEC_ERR_OOM, SPEC_ERR_INVALID_ARG (a misaligned block of the
 // caller's allocator) or SPEC_ERR_CUDA leave nothing allocated.
 spec_status workspace_take(Workspace* w, int device, size_t bytes);
 
