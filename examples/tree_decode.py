@@ -67,7 +67,8 @@ class Decoder:
         self.ver = sv.Verifier(vocab=model.vocab, max_batch=batch * len(PATHS), max_k=2, dtype=torch.float32)
 
     def forward(self, tokens, n_tokens, parents=None):
-        """Logits [B, T, vocab] of the nodes' tokens, their keys and values in the cache."""
+        """Logits [B, T, vocab] of the nodes' tokens, their keys and values in the cache, and
+        the plan's status: where it is not 0 the request got no pages, and its logits mean nothing."""
         m, pool = self.m, self.pool
         B, T = tokens.shape
         plan = self.tc.plan(self.ctx, n_tokens, pool["held"], pool["ring"], pool["free_pages"],
@@ -87,11 +88,13 @@ class Decoder:
         logits = torch.empty(B * T, m.vocab, device="cuda")
         sv.spec_lmhead_logits(h.data_ptr(), m.head.data_ptr(), B * T, m.hidden, m.vocab, logits.data_ptr(),
                               torch.cuda.current_stream().cuda_stream)
-        return logits.view(B, T, -1)
+        return logits.view(B, T, -1), plan["row_status"]
 
     def prompt(self, tokens, n_tokens):
         """Takes the prompts in; the token that follows each."""
-        logits = self.forward(tokens, n_tokens)
+        logits, status = self.forward(tokens, n_tokens)
+        if status.any():
+            raise RuntimeError("the cache has too few pages for these prompts")
         self.ctx = self.ctx + n_tokens
         return logits[torch.arange(self.batch), n_tokens.long() - 1].argmax(-1).int()
 
@@ -106,12 +109,13 @@ class Decoder:
         return torch.cat([root[:, None], first, top(first, 2).flatten(1)], 1)
 
     def round(self, root):
-        """One tree: the accepted tokens and the next root, [B, 3] padded with -1, and their number."""
+        """One tree: the accepted tokens and the next root, [B, 3] padded with -1, and their number
+        (0 for a request that the cache has no pages for: it waits)."""
         B, T = self.batch, len(PARENTS)
         tokens = self.draft(root)
         n = torch.full((B,), T, dtype=torch.int32, device="cuda")
         parents = torch.tensor(PARENTS, dtype=torch.int32, device="cuda").expand(B, T).contiguous()
-        logits = self.forward(tokens, n, parents)
+        logits, status = self.forward(tokens, n, parents)
         # every root-to-leaf path is a sequence of the verify step
         paths = torch.tensor(PATHS, device="cuda")
         out = self.ver.run(logits[:, paths].flatten(0, 1).contiguous(), None,
@@ -122,9 +126,10 @@ class Decoder:
         kept = accepted[rows, best] + 1  # the root is kept in any case
         path = torch.zeros(B, T, dtype=torch.int32, device="cuda")
         path[:, :3] = paths[best]
-        self.ctx = self.tc.keep(self.k, self.v, self.pool["block_table"], self.ctx, n, path, kept)["ctx_len"]
+        self.ctx = self.tc.keep(self.k, self.v, self.pool["block_table"], self.ctx, n, path, kept,
+                                plan_status=status)["ctx_len"]
         emitted = out["tokens"].view(B, len(PATHS), 3)[rows, best]
-        return emitted, kept
+        return emitted, torch.where(status == 0, kept, 0)
 
     def close(self):
         self.tc.close()
@@ -140,7 +145,8 @@ def decode(prompts, lengths, steps, model=None):
         emitted, n = dec.round(root)
         for b, (row, k) in enumerate(zip(emitted.tolist(), n.tolist())):
             texts[b] += row[:k]
-        root = emitted[torch.arange(len(texts), device="cuda"), n.long() - 1].contiguous()
+        last = emitted[torch.arange(len(texts), device="cuda"), n.long().clamp(min=1) - 1]
+        root = torch.where(n > 0, last, root)
     assert dec.tc.check() == sv.SPEC_OK
     dec.close()
     return texts

@@ -101,14 +101,16 @@ spec_status spec_tree_inject_fault(spec_tree_t h, int32_t fault);
  *  - need_b > held_b: the next need_b - held_b pages of the ring, sequences
  *    in order, are written to its table row.  A sequence whose pages, those
  *    of the sequences before it included, go past the ring's end gets none and
- *    SPEC_ROW_NO_PAGES (and so do all behind it that need any); pages
- *    returned by this call are free from the next call on.
+ *    SPEC_ROW_NO_PAGES (and so do all behind it that need any), and -1 in the
+ *    entries of its row that the missing pages would have filled: what they
+ *    held may be another sequence's page by now.  Pages returned by this call
+ *    are free from the next call on.
  *  - need_b < held_b: its last held_b - need_b pages go to the ring's end, in
  *    the order of the sequences.  ctx = n = 0 returns all pages of a sequence.
  * Inputs and outputs are separate buffers where both exist (held, ring): a
  * call whose inputs are unchanged can be repeated and gives the same result.
- * block_table and free_pages are updated in place; entries of a row beyond
- * held_out are left as they are.
+ * block_table and free_pages are updated in place; other entries of a row
+ * beyond held_out are left as they are.
  * slot_map[b][j] and positions[b][j] (ctx_b + the node's depth; a root, parent
  * -1, has depth 0) are -1 for j >= n_b and for sequences whose status is not
  * 0.  tree_mask[b][j] has bit i set iff node i is node j or an ancestor of
@@ -195,7 +197,7 @@ spec_status spec_tree_append(spec_tree_t h, const spec_tree_append_args* a, void
  * row and lse = -inf; so has every node of a sequence with ctx < 0, n outside
  * [0, T] or ctx + n beyond the table.  Keys and values of a page outside the
  * cache are zeros (a sequence that spec_tree_plan left without pages: its rows
- * have no meaning).  Scores, sums and outputs accumulate in
+ * have no meaning, and its status says so).  Scores, sums and outputs accumulate in
  * fp32; the probabilities are rounded to the 16-bit type before they meet V.
  * SPEC_ERR_UNSUPPORTED when q, the cache, out or lse is not on 16 bytes, a
  * stride is not a multiple of 8 elements (or is beyond 2^36), or is 0 for a
@@ -223,9 +225,11 @@ spec_status spec_tree_attend(spec_tree_t h, const spec_tree_attend_args* a, void
  * is strictly ascending within [0, n_b) (a node's parent comes before it, so
  * a path from a root is).  A sequence with a path that is not, or with lengths
  * outside their ranges, keeps its cache and length and gets SPEC_ROW_BAD_TREE
- * or SPEC_ROW_BAD_LEN.  Pages of different sequences must be different, and a
- * sequence that spec_tree_plan left without pages is given path_len 0: its
- * table row does not reach its nodes.
+ * or SPEC_ROW_BAD_LEN, and so does one whose table row gives no page of the
+ * cache for a token of the path or its new place, with SPEC_ROW_NO_PAGES.
+ * plan_status is the row_status of the round's spec_tree_plan: a sequence with
+ * a status there keeps its cache, its length and that status, as append has
+ * written none of its nodes.  Pages of different sequences must be different.
  * SPEC_ERR_UNSUPPORTED when the cache is not on 16 bytes or a stride is not a
  * multiple of 8 elements. */
 typedef struct {
@@ -238,6 +242,7 @@ typedef struct {
     int32_t batch, tokens;
     int32_t* ctx_out;           /* [B], not ctx_len                                   */
     int32_t* row_status;        /* [B] or NULL                                        */
+    const int32_t* plan_status; /* [B] or NULL (every sequence was planned)           */
 } spec_tree_keep_args;
 spec_status spec_tree_keep(spec_tree_t h, const spec_tree_keep_args* a, void* stream);
 

@@ -104,6 +104,7 @@ struct TreeKeepParams {
     const int32_t* table;
     const int32_t* path;
     const int32_t* path_len;
+    const int32_t* plan_status;
     int32_t* ctx_out;
     int32_t* row_status;
 };

@@ -239,6 +239,7 @@ spec_status spec_tree_keep(spec_tree_t h, const spec_tree_keep_args* a, void* st
     p.table = a->block_table;
     p.path = a->path;
     p.path_len = a->path_len;
+    p.plan_status = a->plan_status;
     p.ctx_out = a->ctx_out;
     p.row_status = a->row_status;
     return launched(launch_tree_keep(p, (cudaStream_t)stream));

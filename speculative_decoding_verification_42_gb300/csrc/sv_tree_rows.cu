@@ -90,8 +90,9 @@ __global__ void __launch_bounds__(PLAN_THREADS) k_tree_plan(const TreePlanParams
         }
         const int status = !ok ? SPEC_ROW_BAD_LEN : shortage ? SPEC_ROW_NO_PAGES : bad ? SPEC_ROW_BAD_TREE : 0;
         if (first_chunk) {
-            if (!shortage)
-                for (int i = held + tid; i < need; i += PLAN_THREADS) row[i] = ring_page(i);
+            // a sequence that gets no pages loses what these entries held before: pages it gave
+            // back, which may be another sequence's by now
+            for (int i = held + tid; i < held + w; i += PLAN_THREADS) row[i] = shortage ? -1 : ring_page(i);
             for (int i = tid; i < r; i += PLAN_THREADS)
                 p.free_pages[(tail_at + back + i) % N] = row[need + i];
             if (tid == 0) {
@@ -317,25 +318,30 @@ __global__ void __launch_bounds__(KEEP_THREADS) k_tree_keep(const TreeKeepParams
 {
     const int b = blockIdx.x, layer = blockIdx.y;
     const SeqLen l = tree_len(p.s, b);
-    const int len = __ldg(p.path_len + b);
+    const int len = __ldg(p.path_len + b), planned = p.plan_status ? __ldg(p.plan_status + b) : 0;
     const bool len_ok = l.ok && len >= 0 && len <= l.n;
     const int32_t* path = p.path + (int64_t)b * p.s.T;
-    bool bad = false;
-    if (len_ok)
-        for (int i = threadIdx.x; i < len; i += KEEP_THREADS)
-            bad = bad || path[i] <= (i ? path[i - 1] : -1) || path[i] >= l.n;
-    bad = __syncthreads_or(bad);
-    if (layer == 0 && blockIdx.z == 0 && threadIdx.x == 0) {
-        const bool moves = len_ok && !bad;
-        p.ctx_out[b] = __ldg(p.s.ctx_len + b) + (moves ? len : 0);
-        if (p.row_status) p.row_status[b] = !len_ok ? SPEC_ROW_BAD_LEN : bad ? SPEC_ROW_BAD_TREE : 0;
-    }
-    if (!len_ok || bad) return;
     const int32_t* row = p.table + (int64_t)b * p.s.width;
-    // element offset of token `at` of the sequence; -1 for a page outside the cache
-    auto offset = [&](int at) -> int64_t {
+    auto in_cache = [&](int at) { return (unsigned)__ldg(row + (at >> p.s.page_log2)) < (unsigned)p.s.num_pages; };
+    bool bad = false, lost = false;
+    if (len_ok && planned == 0)
+        for (int i = threadIdx.x; i < len; i += KEEP_THREADS) {
+            const int node = path[i];
+            if (node < 0 || node >= l.n || (i && node <= path[i - 1])) bad = true;
+            else lost = lost || !in_cache(l.ctx + node) || !in_cache(l.ctx + i);
+        }
+    bad = __syncthreads_or(bad);
+    lost = __syncthreads_or(lost);
+    const int status = planned ? planned : !len_ok ? SPEC_ROW_BAD_LEN : bad ? SPEC_ROW_BAD_TREE
+                                                                            : lost ? SPEC_ROW_NO_PAGES : 0;
+    if (layer == 0 && blockIdx.z == 0 && threadIdx.x == 0) {
+        p.ctx_out[b] = __ldg(p.s.ctx_len + b) + (status == 0 ? len : 0);
+        if (p.row_status) p.row_status[b] = status;
+    }
+    if (status != 0) return;
+    // element offset of token `at` of the sequence, whose page is in the cache
+    auto offset = [&](int at) {
         const int page = __ldg(row + (at >> p.s.page_log2));
-        if (page < 0 || page >= p.s.num_pages) return -1;
         return (int64_t)page * p.c.page + (int64_t)(at & ((1 << p.s.page_log2) - 1)) * p.c.token;
     };
     const int per_head = p.s.D / 8, cols = p.s.Hkv * per_head;
@@ -351,11 +357,8 @@ __global__ void __launch_bounds__(KEEP_THREADS) k_tree_keep(const TreeKeepParams
                 const int i = i0 + k;
                 to[k] = -1;
                 if (i < len && path[i] != i) {
-                    const int64_t from = offset(l.ctx + path[i]);
-                    if (from >= 0) {
-                        to[k] = offset(l.ctx + i);
-                        x[k] = *(const uint4*)(at + from * 2);
-                    }
+                    to[k] = offset(l.ctx + i);
+                    x[k] = *(const uint4*)(at + offset(l.ctx + path[i]) * 2);
                 }
             }
 #pragma unroll

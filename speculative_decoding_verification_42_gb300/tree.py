@@ -62,7 +62,7 @@ class spec_tree_keep_args(C.Structure):
     _fields_ = [("cache", spec_tree_cache), ("block_table", C.c_void_p), ("ctx_len", C.c_void_p),
                 ("n_tokens", C.c_void_p), ("path", C.c_void_p), ("path_len", C.c_void_p),
                 ("batch", C.c_int32), ("tokens", C.c_int32), ("ctx_out", C.c_void_p),
-                ("row_status", C.c_void_p)]
+                ("row_status", C.c_void_p), ("plan_status", C.c_void_p)]
 
 
 def bind(L: C.CDLL) -> None:
@@ -374,13 +374,15 @@ class TreeCache:
         return res
 
     def keep(self, k_cache, v_cache, block_table, ctx_len, n_tokens, path, path_len, *,
-             out: dict | None = None, stream=None) -> dict:
+             plan_status=None, out: dict | None = None, stream=None) -> dict:
         """Move the accepted nodes' keys and values behind the context, in all
         layers of [layers, num_pages, page_size, kv_heads, head_dim] caches (or
-        in one layer's); returns the new ctx_len and row_status."""
+        in one layer's); returns the new ctx_len and row_status.  plan_status is
+        the row_status of the round's plan: where it is not 0 nothing moves and
+        the length stays."""
         if stream is not None:
             return self._on(stream, self.keep, k_cache, v_cache, block_table, ctx_len, n_tokens, path,
-                            path_len, out=out)
+                            path_len, plan_status=plan_status, out=out)
         import torch
         i32, a = torch.int32, self._keep_args
         B, T = path.shape
@@ -391,6 +393,8 @@ class TreeCache:
         a.n_tokens = None if n_tokens is None else self._tensor(n_tokens, b, i32, "n_tokens")
         a.path = self._tensor(path, (B, T), i32, "path")
         a.path_len = self._tensor(path_len, b, i32, "path_len")
+        a.plan_status = None if plan_status is None else \
+            self._tensor(plan_status, b, i32, "plan_status")
         a.batch, a.tokens = B, T
         res = {"ctx_len": self._out(out, "ctx_len", b, i32, ctx_len),
                "row_status": self._out(out, "row_status", b, i32, ctx_len)}

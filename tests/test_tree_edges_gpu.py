@@ -1,0 +1,105 @@
+"""The operators around a verify step where other parts of a program meet them:
+page shortages, non-finite values, other streams, layouts that are refused, the
+ends of the ranges.  Against the plain 64-bit implementations of tree_ref.py."""
+import numpy as np
+import pytest
+
+import tree_ref as ref
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def sv():
+    torch = pytest.importorskip("torch")
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from speculative_decoding_verification_42_gb300 import build
+    build.build()
+    import speculative_decoding_verification_42_gb300 as m
+    m.load_library()
+    return m
+
+
+def _dt(name):
+    import torch
+    return {"bf16": torch.bfloat16, "f16": torch.float16}[name]
+
+
+def _i32(a):
+    import torch
+    return torch.from_numpy(np.ascontiguousarray(a, dtype=np.int32)).cuda()
+
+
+def _rand(rng, shape, dtype, scale=1.0):
+    import torch
+    return torch.from_numpy((rng.standard_normal(shape) * scale).astype(np.float32)).to(_dt(dtype)).cuda()
+
+
+def _tc(sv, B, T, Hq, Hkv, D, page, pages, width, dtype="bf16"):
+    return sv.TreeCache(max_batch=B, max_tokens=T, q_heads=Hq, kv_heads=Hkv, head_dim=D, dtype=dtype,
+                        page_size=page, num_pages=pages, table_width=width)
+
+
+def test_a_sequence_without_pages_touches_nothing(sv):
+    """Sequence 0 gave two pages back, sequence 1 holds them now, and sequence 0
+    finds the ring empty: its table row no longer leads to them, append and keep
+    leave the cache alone, and its length stays."""
+    import torch
+    rng = np.random.default_rng(21)
+    B, T, H, D, page, width, N = 2, 4, 2, 64, 8, 3, 4
+    tc = _tc(sv, B, T, 2 * H, H, D, page, N, width)
+    pool = tc.new_pool(B)
+    kc, vc = (_rand(rng, (N, page, H, D), "bf16") for _ in range(2))
+    for ctx, n in (([20, 0], [4, 0]), ([5, 0], [0, 0]), ([5, 16], [0, 4])):
+        plan = tc.plan(_i32(ctx), _i32(n), pool["held"], pool["ring"], pool["free_pages"], pool["block_table"],
+                       max_tokens=T)
+        pool["held"], pool["ring"] = plan["held"], plan["ring"]
+        assert plan["row_status"].tolist() == [0, 0]
+    rows = pool["block_table"].tolist()
+    assert sorted(rows[0][:1] + rows[1]) == list(range(N)) and rows[0][1] in rows[1]
+    ctx, n = _i32([5, 16]), _i32([4, 4])
+    for _ in range(2):  # repeatable
+        plan = tc.plan(ctx, n, pool["held"], pool["ring"], pool["free_pages"], pool["block_table"], max_tokens=T)
+        assert plan["row_status"].tolist() == [sv.SPEC_ROW_NO_PAGES, 0] and plan["held"].tolist() == [1, 3]
+        assert pool["block_table"].tolist() == [[rows[0][0], -1, rows[0][2]], rows[1]]
+        assert plan["slot_map"][0].tolist() == [-1] * T
+    q, k, v = (_rand(rng, (B, T, h, D), "bf16") for h in (2 * H, H, H))
+    before = kc.clone(), vc.clone()
+    qo = tc.append(q, k, v, kc, vc, plan["slot_map"], n_tokens=n)
+    own = [int(p) for p in rows[1]]
+    for x, y in zip((kc, vc), before):
+        assert torch.equal(x[rows[0][0]], y[rows[0][0]])
+    out = tc.attend(qo, kc, vc, pool["block_table"], ctx, n)["out"]
+    alone = _tc(sv, 1, T, 2 * H, H, D, page, N, width)
+    assert torch.equal(out[1:], alone.attend(qo[1:], kc, vc, _i32([own]), _i32([16]), _i32([4]))["out"])
+    # what the row can still see is its first page; its other keys and values are zeros
+    zk, zv = (torch.cat([x, torch.zeros_like(x[:1])]) for x in (kc, vc))
+    wide = _tc(sv, 1, T, 2 * H, H, D, page, N + 1, width)
+    assert torch.equal(out[:1], wide.attend(qo[:1], zk, zv, _i32([[rows[0][0], N, N]]), _i32([5]), _i32([4]))["out"])
+    before = kc.clone(), vc.clone()
+    path, plen = _i32([[0, 2, 3, 0], [0, 1, 2, 3]]), _i32([3, 4])
+    for status in (plan["row_status"], None):
+        got = tc.keep(kc, vc, pool["block_table"], ctx, n, path, plen,
+                      **({} if status is None else dict(plan_status=status)))
+        assert got["ctx_len"].tolist() == [5, 20] and got["row_status"].tolist() == [sv.SPEC_ROW_NO_PAGES, 0]
+        assert torch.equal(kc, before[0]) and torch.equal(vc, before[1])
+    torch.cuda.synchronize()
+    for t in (tc, alone, wide):
+        t.close()
+
+
+def test_keep_leaves_what_plan_refused(sv):
+    """A status of the plan stops the keep, also where the path would fit a page that the sequence holds."""
+    import torch
+    rng = np.random.default_rng(22)
+    tc = _tc(sv, 4, 4, 1, 1, 32, 8, 8, 2)
+    kc, vc = (_rand(rng, (8, 8, 1, 32), "bf16") for _ in range(2))
+    before = kc.clone(), vc.clone()
+    table, ctx, n = _i32(np.arange(8).reshape(4, 2)), _i32([1, 2, 3, 0]), _i32([4] * 4)
+    path, plen, status = _i32([[1, 3, 0, 0]] * 4), _i32([2, 2, 2, 2]), _i32([5, 6, 7, 0])
+    got = tc.keep(kc, vc, table, ctx, n, path, plen, plan_status=status)
+    assert got["ctx_len"].tolist() == [1, 2, 3, 2] and got["row_status"].tolist() == [5, 6, 7, 0]
+    for x, y in zip((kc, vc), before):
+        assert torch.equal(x[:6], y[:6]) and torch.equal(x[6, 0], y[6, 1]) and torch.equal(x[6, 1], y[6, 3])
+    tc.close()
