@@ -273,7 +273,8 @@ __global__ void __launch_bounds__(APP_THREADS, 3) k_tree_append(const TreeAppend
                         float2 z = make_float2(y[2 * i + 1], y[2 * i]);
                         if (far) z = H::unpack(__shfl_sync(0xffffffffu, xs[i], mate / 8, LANES));
                         float a0 = y[2 * i] * A[2 * i], a1 = y[2 * i + 1] * A[2 * i + 1];
-                        if (p.cos_sin) a0 += z.x * Bm[2 * i], a1 += z.y * Bm[2 * i + 1];
+                        // not past rot_dim, where Bm is 0: 0 times an infinite or NaN mate is NaN
+                        if (turn) a0 += z.x * Bm[2 * i], a1 += z.y * Bm[2 * i + 1];
                         out[i] = H::pack(a0 * r, a1 * r);
                     }
                     v = make_uint4(out[0], out[1], out[2], out[3]);

@@ -103,3 +103,39 @@ def test_keep_leaves_what_plan_refused(sv):
     for x, y in zip((kc, vc), before):
         assert torch.equal(x[:6], y[:6]) and torch.equal(x[6, 0], y[6, 1]) and torch.equal(x[6, 1], y[6, 3])
     tc.close()
+
+
+@pytest.mark.parametrize("D,rot,inter,norm,dtype", [
+    (64, 32, True, False, "bf16"), (64, 32, False, False, "bf16"), (80, 16, True, True, "f16"),
+    (80, 48, False, True, "f16"), (256, 64, True, False, "f16"), (128, 96, False, False, "bf16")])
+def test_append_non_finite_elements(sv, D, rot, inter, norm, dtype):
+    """Infinities and NaN reach what the formula says: their pair in the rotated
+    part, themselves past it, the whole head through a norm."""
+    import torch
+    rng = np.random.default_rng(D + rot)
+    B, T, Hq, Hkv, page, pages, P = 1, 6, 4, 2, 8, 2, 16
+    tc = _tc(sv, B, T, Hq, Hkv, D, page, pages, 2, dtype)
+    q, k, v = (_rand(rng, (B, T, h, D), dtype, 2.0) for h in (Hq, Hkv, Hkv))
+    inf, nan = float("inf"), float("nan")
+    for x in (q, k):
+        for j, (e, val) in enumerate(((rot, inf), (rot + 1, -inf), (D - 1, nan), (1, inf), (rot // 2, nan))):
+            x[0, j, j % x.shape[2], e] = val
+    v[0, 1, 0, 0], v[0, 2, 1, D - 1] = inf, nan
+    kc, vc = (_rand(rng, (pages, page, Hkv, D), dtype) for _ in range(2))
+    w = (1 + 0.3 * _rand(rng, (D,), dtype)).to(_dt(dtype)) if norm else None
+    cs, pos, slot = rng.standard_normal((P, rot)).astype(np.float32), rng.integers(0, P, (B, T)), np.arange(T)[None]
+    got = tc.append(q, k, v, kc, vc, _i32(slot), _i32(pos), q_weight=w, k_weight=w,
+                    cos_sin=torch.from_numpy(cs).cuda(), interleaved=inter)
+    torch.cuda.synchronize()
+    u, w64 = ref.UNIT[dtype], ref.to_f64(w) if norm else None
+    for j in range(T):
+        for x, y in ((q[0, j], got[0, j]), (k[0, j], kc[0, j])):
+            with np.errstate(invalid="ignore"):
+                want, tol = ref.norm_rotate(ref.to_f64(x), w64, 1e-6, cs.astype(np.float64), int(pos[0, j]), inter)
+            y, fin = ref.to_f64(y), np.isfinite(want)
+            assert (np.isnan(y) == np.isnan(want)).all(), j
+            assert (y[np.isinf(want)] == want[np.isinf(want)]).all(), j
+            err = np.abs(y[fin] - want[fin]) - (tol + u * (np.abs(want) + tol) + ref.TINY[dtype])[fin]
+            assert not (err > 0).any(), (j, err.max())
+    assert torch.equal(vc[0, :T].isnan(), v[0].isnan()) and torch.equal(vc[0, :T].nan_to_num(), v[0].nan_to_num())
+    tc.close()
