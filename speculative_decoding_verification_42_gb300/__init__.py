@@ -282,7 +282,14 @@ class Verifier:
         """Verify a batch; returns (and fills) a dict of output tensors.  With the
         LM head, ``target`` is the hidden states [B * (K + 1), H] and ``w_vocab``
         the [H, V] matrix.  alpha: also the acceptance statistic of every slot.
-        early_exit: read each sequence's rows only up to its first rejection."""
+        early_exit: read each sequence's rows only up to its first rejection.
+        stream: the one to run on, which waits for nothing by itself (default: the
+        current one); the tensors may be dropped right after the call."""
+        if stream is not None:
+            return _tree.on_stream(stream, self.device, self.run, target, draft, draft_tokens, k_per_row,
+                                   temperature=temperature, top_k=top_k, top_p=top_p, seed=seed,
+                                   round=round, out=out, debug=debug, w_vocab=w_vocab, alpha=alpha,
+                                   early_exit=early_exit)
         import torch
         if w_vocab is not None:
             B, K = draft_tokens.shape[0], draft_tokens.shape[1]
@@ -306,19 +313,24 @@ class Verifier:
         ins = spec_verify_inputs(_ptr(target), _ptr(w_vocab), _ptr(draft), _ptr(draft_tokens),
                                  _ptr(k_per_row), B, K)
         outs = spec_verify_outputs(*[_ptr(out.get(f)) for f, _ in spec_verify_outputs._fields_])
-        s = stream if stream is not None else torch.cuda.current_stream(dev)
+        s = torch.cuda.current_stream(dev)
         run = spec_verify_run_early_exit if early_exit else spec_verify_run
         run(self.h, ins, self.sampling(temperature, top_k, top_p, seed, round), outs, s.cuda_stream)
         return out
 
     def draft_sample(self, draft, k_per_row=None, *, temperature=1.0, top_k=0, top_p=1.0,
                      seed=0, round=0, probs: bool = False, stream=None):
-        """Draft tokens x ~ P_d (tag-1 uniforms); optionally the dense P_d too."""
+        """Draft tokens x ~ P_d (tag-1 uniforms); optionally the dense P_d too.
+        stream: as in run."""
+        if stream is not None:
+            return _tree.on_stream(stream, self.device, self.draft_sample, draft, k_per_row,
+                                   temperature=temperature, top_k=top_k, top_p=top_p, seed=seed,
+                                   round=round, probs=probs)
         import torch
         B, K, V = draft.shape
         toks = torch.empty((B, K), dtype=torch.int32, device=draft.device)
         pr = torch.zeros((B, K, V), dtype=torch.float32, device=draft.device) if probs else None
-        s = stream if stream is not None else torch.cuda.current_stream(draft.device)
+        s = torch.cuda.current_stream(draft.device)
         spec_draft_sample(self.h, _ptr(draft), _ptr(k_per_row), B, K,
                           self.sampling(temperature, top_k, top_p, seed, round), _ptr(toks),
                           _ptr(pr), s.cuda_stream)

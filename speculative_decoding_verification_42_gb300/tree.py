@@ -135,6 +135,36 @@ def spec_tree_keep(h, args: spec_tree_keep_args, stream: int = 0) -> None:
 # --------------------------------------------------------------------------- #
 # torch wrapper                                                               #
 # --------------------------------------------------------------------------- #
+def _tensors(values):
+    import torch
+    for t in values:
+        if isinstance(t, torch.Tensor):
+            if t.is_cuda:
+                yield t
+        elif isinstance(t, dict):
+            yield from _tensors(t.values())
+        elif isinstance(t, tuple):
+            yield from _tensors(t)
+
+
+def on_stream(stream, device, op, *args, **kw):
+    """op(*args, **kw) with ``stream`` current.  Its new outputs come from that
+    stream's memory (the current stream's may still be read by kernels in flight
+    there), and are noted as used by the current stream, which the caller is likely
+    to read them on; the tensors it is given are noted as used by ``stream``, so that
+    the caller may drop them at once.  It orders nothing: ``stream`` has to wait for
+    the work that fills the inputs."""
+    import torch
+    here = torch.cuda.current_stream(device)
+    with torch.cuda.stream(stream):
+        res = op(*args, **kw)
+    for t in _tensors((args, kw)):
+        t.record_stream(stream)
+    for t in _tensors((res,)):
+        t.record_stream(here)
+    return res
+
+
 class TreeCache:
     """One handle of the operators around a verify step, for one cache shape.
 
@@ -233,16 +263,7 @@ class TreeCache:
         return self._current_stream(self.device)
 
     def _on(self, stream, op, *args, **kw):
-        # A call on another stream: its new outputs come from that stream's memory (the
-        # current stream's may still be read by kernels in flight there), and are noted as
-        # used by the current stream, which the caller is likely to read them on.
-        import torch
-        with torch.cuda.stream(stream):
-            res = op(*args, **kw)
-        here = torch.cuda.current_stream(self.device)
-        for t in res.values() if isinstance(res, dict) else (res,):
-            t.record_stream(here)
-        return res
+        return on_stream(stream, self.device, op, *args, **kw)
 
     def _out(self, out, key, shape, dtype, like=None):
         """The caller's output tensor (checked), or a new one (like `like`, a contiguous

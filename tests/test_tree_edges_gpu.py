@@ -139,3 +139,48 @@ def test_append_non_finite_elements(sv, D, rot, inter, norm, dtype):
             assert not (err > 0).any(), (j, err.max())
     assert torch.equal(vc[0, :T].isnan(), v[0].isnan()) and torch.equal(vc[0, :T].nan_to_num(), v[0].nan_to_num())
     tc.close()
+
+
+def test_inputs_of_another_stream_may_be_dropped(sv):
+    """Tensors given to a call with stream= stay whole until that stream has read
+    them, although the caller drops them and allocates anew; the outputs take no
+    memory that the current stream still uses."""
+    import torch
+    rng = np.random.default_rng(25)
+    B, T, H, D = 2, 300, 16, 128
+    tc = _tc(sv, B, T, H, 4, D, 16, 80, 40)
+    kc, vc = (_rand(rng, (80, 16, 4, D), "bf16") for _ in range(2))
+    q, k, v = (_rand(rng, (B, T, h, D), "bf16") for h in (H, 4, 4))
+    table, ctx, slots = _i32(np.arange(80).reshape(2, 40)), _i32([300, 5]), _i32(np.full((B, T), -1))
+    path, plen = _i32(np.arange(T)[None].repeat(B, 0)), _i32([7, 9])
+    pool = tc.new_pool(B)
+    K, V = 4, 50000
+    ver = sv.Verifier(vocab=V, max_batch=8, max_k=K, dtype="bf16")
+    target, draft, probs = (_rand(rng, (8, n, V), "bf16", 3.0) for n in (K + 1, K, K))
+    drafted = _i32(rng.integers(0, V, (8, K)))
+    copy = lambda *ts: [t.clone() for t in ts]  # noqa: E731
+    calls = dict(
+        attend=lambda s: tc.attend(*copy(q, kc, vc, table, ctx), stream=s)["out"],
+        append=lambda s: tc.append(*copy(q, k, v), kc, vc, *copy(slots), stream=s),
+        plan=lambda s: tc.plan(*copy(ctx), None, *copy(pool["held"], pool["ring"], pool["free_pages"],
+                                                       pool["block_table"]), stream=s)["slot_map"],
+        keep=lambda s: tc.keep(kc, vc, *copy(table, ctx), None, *copy(path, plen), stream=s)["ctx_len"],
+        run=lambda s: ver.run(*copy(target, draft, drafted), temperature=0.9, top_k=50, stream=s)["target_lse"],
+        draft_sample=lambda s: ver.draft_sample(*copy(probs), temperature=0.9, probs=True, stream=s)[1])
+    side = torch.cuda.Stream()
+    for name, call in calls.items():
+        first = call(None)
+        torch.cuda.synchronize()
+        torch.cuda.empty_cache()  # what the call frees is the only memory of its size
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(60_000_000)  # some 30 ms: the copies are made and dropped meanwhile
+        second = call(side)
+        over = [torch.full((n,), 255, dtype=torch.uint8, device="cuda")
+                for n in [x.numel() * x.element_size() for x in (q, k, v, kc, vc, table, ctx, slots, path, target, draft,
+                                                                 drafted, probs, pool["free_pages"])] * 2]
+        torch.cuda.synchronize()
+        assert torch.equal(first, second), name
+        del over
+    tc.close()
+    ver.close()
