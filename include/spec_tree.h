@@ -165,7 +165,8 @@ typedef struct {
  * outside the cache gets a zero row in q_out and writes nothing to the cache;
  * one whose position cos_sin does not hold gets NaN in q_out and k.
  * SPEC_ERR_UNSUPPORTED when a pointer to q, k, v, q_out, the weights or the
- * cache is not on 16 bytes, a stride is not a multiple of 8 elements, or
+ * cache is not on 16 bytes, a stride is not a multiple of 8 elements (or is
+ * beyond 2^36), a stride of the cache is 0 for a dimension larger than 1, or
  * rot_dim is not a multiple of 16 within [0, head_dim]. */
 typedef struct {
     spec_tree_rows q, k, v;
@@ -230,8 +231,9 @@ spec_status spec_tree_attend(spec_tree_t h, const spec_tree_attend_args* a, void
  * plan_status is the row_status of the round's spec_tree_plan: a sequence with
  * a status there keeps its cache, its length and that status, as append has
  * written none of its nodes.  Pages of different sequences must be different.
- * SPEC_ERR_UNSUPPORTED when the cache is not on 16 bytes or a stride is not a
- * multiple of 8 elements. */
+ * SPEC_ERR_UNSUPPORTED when the cache is not on 16 bytes, a stride is not a
+ * multiple of 8 elements (or is beyond 2^36), or is 0 for a dimension larger
+ * than 1. */
 typedef struct {
     spec_tree_cache cache;
     const int32_t* block_table; /* [B, table_width]                                   */

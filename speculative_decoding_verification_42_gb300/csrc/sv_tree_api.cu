@@ -42,10 +42,12 @@ bool rows_ok(const spec_tree_rows& r)
 {
     return aligned16(r.ptr) && stride_ok(r.seq_stride) && stride_ok(r.token_stride) && stride_ok(r.head_stride);
 }
-bool cache_ok(const spec_tree_cache& c)
+// a stride of 0 only where there is one element: two writers would meet at one place, and tensor maps take none
+bool cache_ok(const spec_tree* h, const spec_tree_cache& c)
 {
     return aligned16(c.k) && aligned16(c.v) && stride_ok(c.page_stride) && stride_ok(c.token_stride) &&
-           stride_ok(c.head_stride);
+           stride_ok(c.head_stride) && (h->cfg.num_pages == 1 || c.page_stride) &&
+           (h->cfg.page_size == 1 || c.token_stride) && (h->cfg.kv_heads == 1 || c.head_stride);
 }
 TreeRows rows(const spec_tree_rows& r) { return TreeRows{r.ptr, r.seq_stride, r.token_stride, r.head_stride}; }
 TreeCachePtrs cache(const spec_tree_cache& c)
@@ -164,7 +166,7 @@ spec_status spec_tree_append(spec_tree_t h, const spec_tree_append_args* a, void
     if (!a->q.ptr || !a->k.ptr || !a->v.ptr || !a->cache.k || !a->cache.v || !a->slot_map || !a->q_out ||
         (a->cos_sin && (!a->positions || a->table_len < 1 || a->rot_dim < 0)))
         return SPEC_ERR_INVALID_ARG;
-    if (!rows_ok(a->q) || !rows_ok(a->k) || !rows_ok(a->v) || !cache_ok(a->cache) || !aligned16(a->q_out) ||
+    if (!rows_ok(a->q) || !rows_ok(a->k) || !rows_ok(a->v) || !cache_ok(h, a->cache) || !aligned16(a->q_out) ||
         !aligned16(a->q_weight) || !aligned16(a->k_weight) || !aligned16(a->cos_sin) ||
         (a->cos_sin && (a->rot_dim % 16 || a->rot_dim > h->cfg.head_dim)))
         return SPEC_ERR_UNSUPPORTED;
@@ -197,13 +199,12 @@ spec_status spec_tree_attend(spec_tree_t h, const spec_tree_attend_args* a, void
     if (!a->q.ptr || !a->cache.k || !a->cache.v || !a->block_table || !a->ctx_len || !a->out ||
         (a->tree_mask && a->tokens > SPEC_TREE_MAX_NODES))
         return SPEC_ERR_INVALID_ARG;
-    if (!rows_ok(a->q) || !cache_ok(a->cache) || !aligned16(a->out) || !aligned16(a->lse))
+    if (!rows_ok(a->q) || !cache_ok(h, a->cache) || !aligned16(a->out) || !aligned16(a->lse))
         return SPEC_ERR_UNSUPPORTED;
     // tensor maps: a stride of 0 only where there is one element
     const spec_tree_config& c = h->cfg;
     if ((a->batch > 1 && !a->q.seq_stride) || (a->tokens > 1 && !a->q.token_stride) ||
-        (c.q_heads > 1 && !a->q.head_stride) || (c.num_pages > 1 && !a->cache.page_stride) ||
-        (c.page_size > 1 && !a->cache.token_stride) || (c.kv_heads > 1 && !a->cache.head_stride))
+        (c.q_heads > 1 && !a->q.head_stride))
         return SPEC_ERR_UNSUPPORTED;
     DeviceGuard g(h->cfg.device);
     if (!g.ok) return SPEC_ERR_CUDA;
@@ -230,7 +231,9 @@ spec_status spec_tree_keep(spec_tree_t h, const spec_tree_keep_args* a, void* st
     if (!a->cache.k || !a->cache.v || a->cache.layers < 1 || a->cache.layers > 65535 || !a->block_table ||
         !a->ctx_len || !a->path || !a->path_len || !a->ctx_out || a->ctx_out == a->ctx_len)
         return SPEC_ERR_INVALID_ARG;
-    if (!cache_ok(a->cache) || !stride_ok(a->cache.layer_stride)) return SPEC_ERR_UNSUPPORTED;
+    if (!cache_ok(h, a->cache) || !stride_ok(a->cache.layer_stride) ||
+        (a->cache.layers > 1 && !a->cache.layer_stride))
+        return SPEC_ERR_UNSUPPORTED;
     DeviceGuard g(h->cfg.device);
     if (!g.ok) return SPEC_ERR_CUDA;
     TreeKeepParams p = {};

@@ -184,3 +184,30 @@ def test_inputs_of_another_stream_may_be_dropped(sv):
         del over
     tc.close()
     ver.close()
+
+
+def test_caches_with_shared_elements_are_refused(sv):
+    """A stride of 0 where there are several pages, tokens, heads or layers: append and keep write there."""
+    import torch
+    B, T, H, D, page, pages, layers = 1, 2, 2, 32, 8, 4, 3
+    tc = _tc(sv, B, T, H, H, D, page, pages, 2)
+    q = torch.zeros(B, T, H, D, dtype=torch.bfloat16, device="cuda")
+    table, ctx, n, at = _i32([[0, 1]]), _i32([3]), _i32([2]), _i32([[3, 4]])
+    whole = (layers, pages, page, H, D)
+    for dim in range(4):
+        k, v = (torch.zeros([1 if i == dim else x for i, x in enumerate(whole)], dtype=torch.bfloat16,
+                            device="cuda").expand(whole) for _ in range(2))
+        calls = [lambda: tc.keep(k, v, table, ctx, n, _i32([[0, 1]]), _i32([2]))]
+        if dim:
+            calls += [lambda: tc.append(q, q, q, k[0], v[0], at),
+                      lambda: tc.attend(q, k[0], v[0], table, ctx, n)]
+        for call in calls:
+            with pytest.raises(sv.SpecVerifyError) as e:
+                call()
+            assert e.value.code == sv.SPEC_ERR_UNSUPPORTED
+    # inputs may be broadcast: they are only read
+    k, v = (torch.zeros(pages, page, H, D, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    one = torch.ones(1, 1, 1, D, dtype=torch.bfloat16, device="cuda").expand(B, T, H, D)
+    out = tc.append(one, one, one, k, v, at)
+    assert (out == 1).all() and float(k.sum()) == float(v.sum()) == T * H * D and (k[0, 3:5] == 1).all()
+    tc.close()
