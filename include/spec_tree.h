@@ -112,10 +112,11 @@ spec_status spec_tree_inject_fault(spec_tree_t h, int32_t fault);
  * block_table and free_pages are updated in place; other entries of a row
  * beyond held_out are left as they are.
  * slot_map[b][j] and positions[b][j] (ctx_b + the node's depth; a root, parent
- * -1, has depth 0) are -1 for j >= n_b and for sequences whose status is not
- * 0.  tree_mask[b][j] has bit i set iff node i is node j or an ancestor of
- * it (bit i of a row is bit i % 32 of word i / 32), and is 0 where slot_map
- * is -1.  A sequence with SPEC_ROW_BAD_TREE has its pages as its lengths ask. */
+ * -1, has depth 0) are -1 for j >= n_b, for sequences whose status is not 0, and
+ * for a node whose page, as the table has it, is not in the cache.
+ * tree_mask[b][j] has bit i set iff node i is node j or an ancestor of it (bit i
+ * of a row is bit i % 32 of word i / 32), and is 0 where slot_map is -1.  A
+ * sequence with SPEC_ROW_BAD_TREE has its pages as its lengths ask. */
 typedef struct {
     const int32_t* ctx_len;  /* [B]                                                   */
     const int32_t* n_tokens; /* [B] or NULL (T each)                                  */

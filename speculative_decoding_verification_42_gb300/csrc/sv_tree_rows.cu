@@ -109,16 +109,17 @@ __global__ void __launch_bounds__(PLAN_THREADS) k_tree_plan(const TreePlanParams
             if (status == 0 && j < l.n) {
                 const int place = l.ctx + j, pg = place >> p.s.page_log2;
                 const int page = pg < held ? row[pg] : ring_page(pg);
-                if (page >= 0 && page < p.s.num_pages)
+                if (page >= 0 && page < p.s.num_pages) {
                     slot = (page << p.s.page_log2) + (place & ((1 << p.s.page_log2) - 1));
-                pos = l.ctx + j;
-                if (p.parents) {
-                    int depth = -1;
-                    for (int a = j; a >= 0; a = par[a], ++depth)
+                    pos = l.ctx + j;
+                    if (p.parents) {
+                        int depth = -1;
+                        for (int a = j; a >= 0; a = par[a], ++depth)
 #pragma unroll
-                        for (int x = 0; x < PLAN_WORDS; ++x)
-                            if ((a >> 5) == x) m[x] |= 1u << (a & 31);
-                    pos = l.ctx + depth;
+                            for (int x = 0; x < PLAN_WORDS; ++x)
+                                if ((a >> 5) == x) m[x] |= 1u << (a & 31);
+                        pos = l.ctx + depth;
+                    }
                 }
             }
             p.slot_map[at] = slot;

@@ -211,3 +211,21 @@ def test_caches_with_shared_elements_are_refused(sv):
     out = tc.append(one, one, one, k, v, at)
     assert (out == 1).all() and float(k.sum()) == float(v.sum()) == T * H * D and (k[0, 3:5] == 1).all()
     tc.close()
+
+
+def test_plan_entries_outside_the_cache(sv):
+    """A node whose page a table row does not give has no slot, no position and no mask."""
+    import torch
+    tc = _tc(sv, 2, 4, 2, 1, 32, 8, 4, 2)
+    table = _i32([[4, 1], [2, -1]])  # of 4 pages
+    parents, ring = _i32([[-1, 0, 0, 1]] * 2), torch.tensor([0, 0], dtype=torch.int64, device="cuda")
+    for par in (parents, None):
+        got = tc.plan(_i32([6, 6]), _i32([4, 4]), _i32([2, 2]), ring, _i32([0, 0, 0, 0]), table, parents=par,
+                      max_tokens=4)
+        assert got["row_status"].tolist() == [0, 0]
+        assert got["slot_map"].tolist() == [[-1, -1, 8, 9], [22, 23, -1, -1]]
+        assert got["positions"].tolist() == ([[-1, -1, 7, 8], [6, 7, -1, -1]] if par is not None else
+                                             [[-1, -1, 8, 9], [6, 7, -1, -1]])
+        if par is not None:
+            assert got["tree_mask"][:, :, 0].tolist() == [[0, 0, 5, 11], [1, 3, 0, 0]]
+    tc.close()
