@@ -200,7 +200,8 @@ spec_status spec_tree_append(spec_tree_t h, const spec_tree_append_args* a, void
  * [0, T] or ctx + n beyond the table.  Keys and values of a page outside the
  * cache are zeros (a sequence that spec_tree_plan left without pages: its rows
  * have no meaning, and its status says so).  Scores, sums and outputs accumulate in
- * fp32; the probabilities are rounded to the 16-bit type before they meet V.
+ * fp32; the probabilities are rounded to the 16-bit type (in f16 in units of
+ * 2^-7 of the largest so far) before they meet V.
  * SPEC_ERR_UNSUPPORTED when q, the cache, out or lse is not on 16 bytes, a
  * stride is not a multiple of 8 elements (or is beyond 2^36), or is 0 for a
  * dimension larger than 1; or when the key tiles of the call could pass 2^31

@@ -9,7 +9,9 @@
 // l += sum p and O += P V (tensor cores, O fp32 in tensor memory); when m grows
 // by more than 2^8 would allow, O and l are scaled down first.  P is rounded to
 // the 16-bit type, the only one that meets a 16-bit V in an MMA: half an ulp of
-// each p (2^-9 of it in bf16), while l takes p before the rounding.
+// each p (2^-9 of it in bf16), while l takes p before the rounding.  In f16, whose
+// smallest number is 2^-24, p and l are taken 2^7 times as large, the most that
+// leaves p below the type's end: a long context's many p of 2^-25 add up.
 //
 // The bound is HBM for up to about 256 rows per key head (each key's 4 D bytes
 // are read once per 256 rows and cost 4 D products per row), the tensor cores
@@ -82,6 +84,14 @@ constexpr int ATT_SEGS = 4;                   // segments handed out ahead
 constexpr uint32_t ATT_WAIT_POLLS = 1u << 17;  // limit of a wait: some seconds (a poll sleeps for microseconds)
 constexpr uint32_t ATT_STALL_POLLS = 4096;    // SPEC_FAULT_STALL_STREAM
 constexpr float ATT_LAZY = 8.f;               // log2 growth of the maximum that O takes unscaled
+// log2 of what p, l and O are multiplied by: f16 ends at 2^16, and p is at most 2^ATT_LAZY
+__host__ __device__ constexpr float att_up(bool f16) { return f16 ? 15.f - ATT_LAZY : 0.f; }
+// natural logarithm of a row's sum l in units of its maximum m
+template <bool F16>
+__device__ __forceinline__ float att_lse(float m, float scale, float l)
+{
+    return fmaf(m, scale, logf(l * (F16 ? 1.f / (1 << (int)att_up(true)) : 1.f)));
+}
 
 constexpr int ATT_STAGES = 8;                 // most stages of a ring
 
@@ -890,7 +900,7 @@ __global__ void __launch_bounds__(Att<DP>::THREADS, 1)
                         }
                     }
                     const float mc = m == -INFINITY ? 0.f : m * c;
-                    const uint64_t c2 = pack2(c, c), mc2 = pack2(-mc, -mc);
+                    const uint64_t c2 = pack2(c, c), mc2 = pack2(att_up(F16) - mc, att_up(F16) - mc);
                     uint64_t sum[2] = {0ull, 0ull};  // two pairs of partial sums
 #pragma unroll 1
                     for (int h = 0; h < NS; ++h) {
@@ -1004,7 +1014,7 @@ __global__ void __launch_bounds__(Att<DP>::THREADS, 1)
                         }
                     }
                     const bool first = s == 0 || dual;
-                    if (first && mine && whole && p.lse) p.lse[orow] = none ? -INFINITY : fmaf(mr, p.scale, logf(ll));
+                    if (first && mine && whole && p.lse) p.lse[orow] = none ? -INFINITY : att_lse<F16>(mr, p.scale, ll);
                     if (first && mine && !whole) w.part_ml[slot * NS * ATT_ROWS + prow] = make_float2(mm, ll);
                 }
                 tmem_fence_before();
@@ -1108,7 +1118,7 @@ __global__ void __launch_bounds__(COMB_THREADS, COMB_CTAS_PER_SM)
                                   : make_uint4(H::pack(a.x * inv, a.y * inv), H::pack(a.z * inv, a.w * inv),
                                                H::pack(b.x * inv, b.y * inv), H::pack(b.z * inv, b.w * inv));
             }
-            if (p.lse && col4 == 0) p.lse[orow] = none ? -INFINITY : fmaf(ref, p.scale, logf(l));
+            if (p.lse && col4 == 0) p.lse[orow] = none ? -INFINITY : att_lse<F16>(ref, p.scale, l);
             continue;
         }
         const int c8 = D / 8, rb = jn.sub / c8, col4 = (jn.sub - rb * c8) * 2;
@@ -1158,7 +1168,7 @@ __global__ void __launch_bounds__(COMB_THREADS, COMB_CTAS_PER_SM)
                     none ? make_uint2(0, 0)
                          : make_uint2(H::pack(y.x * inv, y.y * inv), H::pack(y.z * inv, y.w * inv));
                 if (p.lse && col4 == 0 && g == 0)
-                    p.lse[orow] = none ? -INFINITY : fmaf(ref, p.scale, logf(l));
+                    p.lse[orow] = none ? -INFINITY : att_lse<F16>(ref, p.scale, l);
             }
         }
     }

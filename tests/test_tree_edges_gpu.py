@@ -229,3 +229,57 @@ def test_plan_entries_outside_the_cache(sv):
         if par is not None:
             assert got["tree_mask"][:, :, 0].tolist() == [[0, 0, 5, 11], [1, 3, 0, 0]]
     tc.close()
+
+
+@pytest.mark.parametrize("D,T,tree", [(64, 1, False), (128, 3, True), (256, 2, True)])
+def test_attend_f16_many_small_probabilities(sv, D, T, tree):
+    """Many keys whose probabilities are far below the largest still count: each of 2^-25.5 of it, less
+    than the smallest f16.  So many sequences (of the same pages) that most are not cut."""
+    import torch
+    B, ctx, page = 400, 100000, 64
+    pages = ctx // page + 2
+    tc = _tc(sv, B, T, 2, 1, D, page, pages, pages, "f16")
+    q = torch.zeros(B, T, 2, D, dtype=torch.float16, device="cuda")
+    kc, vc = (torch.zeros(pages, page, 1, D, dtype=torch.float16, device="cuda") for _ in range(2))
+    q[..., 0] = 4.0
+    kc[0, 3, 0, 0] = 25.5 * np.log(2.0) / 4.0
+    vc[...] = 1.0
+    vc[0, 3] = 0.0
+    mask = _i32(ref.pack_mask(np.eye(T, dtype=bool)[None].repeat(B, 0))) if tree else None
+    got = tc.attend(q, kc, vc, _i32(np.arange(pages)[None].repeat(B, 0)), _i32([ctx] * B),
+                    _i32([T] * B), tree_mask=mask, scale=1.0)
+    assert tc.check() == sv.SPEC_OK
+    p = np.exp(-4.0 * float(kc[0, 3, 0, 0]))
+    N = ctx  # keys but the one: the context's others and the node itself
+    z = 1.0 + N * p
+    want, lse = N * p / z, 4.0 * float(kc[0, 3, 0, 0]) + np.log(z)
+    # each probability rounded to f16 in units of 2^7 of the largest or finer (2^-11 of itself, or half the
+    # subnormals' spacing), fp32 sums of N terms in some hundred parts of a thousand, the output's rounding
+    u = ref.UNIT["f16"]
+    tol = u * want + N * 2.0 ** -25 * 2.0 ** -7 / z + 2.0 ** -13 * want + u * want
+    assert float((got["out"].double() - want).abs().max()) <= tol, (float(got["out"].double().min()), want, tol)
+    assert float((got["lse"].double() - lse).abs().max()) <= 2.0 ** -17 * abs(lse)
+    tc.close()
+
+
+@pytest.mark.parametrize("D", [64, 256])
+def test_attend_f16_largest_probabilities(sv, D):
+    """Scores just below the growth that moves the running maximum: the largest probabilities stay finite."""
+    rng = np.random.default_rng(D)
+    B, ctx, page = 400, 1500, 64
+    pages = ctx // page + 2
+    tc = _tc(sv, B, 1, 1, 1, D, page, pages, pages, "f16")
+    q, kc, vc = (_rand(rng, s, "f16") for s in ((1, 1, 1, D), (pages, page, 1, D), (pages, page, 1, D)))
+    q[...] = 0
+    q[..., 0] = 1
+    kc[...] = 0
+    kc[6:, :, 0, 0] = 7.99 * np.log(2.0)  # from the fourth tile of 128 keys on
+    got = tc.attend(q.expand(B, 1, 1, D).contiguous(), kc, vc, _i32(np.arange(pages)[None].repeat(B, 0)),
+                    _i32([ctx] * B), _i32([1] * B), scale=1.0)
+    assert tc.check() == sv.SPEC_OK
+    at = np.arange(ctx + 1)
+    k, v = (ref.to_f64(x)[at // page, at % page, 0] for x in (kc, vc))
+    out, lse, tol, tol_l = ref.attend(ref.to_f64(q)[0, 0], k, v, np.ones((1, ctx + 1), bool), 1.0, "f16")
+    assert (np.abs(ref.to_f64(got["out"])[:, 0, 0] - out[0]) <= tol[0]).all()
+    assert (np.abs(ref.to_f64(got["lse"])[:, 0, 0] - lse[0]) <= tol_l[0]).all()
+    tc.close()
