@@ -283,3 +283,92 @@ def test_attend_f16_largest_probabilities(sv, D):
     assert (np.abs(ref.to_f64(got["out"])[:, 0, 0] - out[0]) <= tol[0]).all()
     assert (np.abs(ref.to_f64(got["lse"])[:, 0, 0] - lse[0]) <= tol_l[0]).all()
     tc.close()
+
+
+def _parts(ctx, n, G, D, Hkv, sms):
+    """How sv_tree_attend.cu cuts a call without many row tiles: (may its first joining form be used, the
+    number of parts of every item that is cut)."""
+    KT, cost_of = (128 if D <= 128 else 64), 4
+    group = (2 if D <= 128 else 1) * (128 // G)
+    assert all(x <= group for x in n)
+    cost = [-(-(c + x) // KT) + cost_of if x else 0 for c, x in zip(ctx, n)]
+    total = sum(cost) * Hkv
+    ctas = min(sms, total)
+    q, r = total // ctas, total % ctas
+    owner = lambda x: x // (q + 1) if x < r * (q + 1) else r + (x - r * (q + 1)) // q  # noqa: E731
+    parts, at = [], 0
+    for _ in range(Hkv):
+        for c in cost:
+            if c:
+                first, last = owner(at + cost_of), owner(at + c - 1)
+                if last > first:
+                    parts.append(last - first + 1)
+            at += c
+    q_rows = -(-min(128 // G, max(n)) * G // 8) * 8
+    rows = q_rows * (2 if D <= 128 else 1)
+    tasks = len(ctx) * Hkv * (-(-rows // 32)) * (D // 8)
+    return tasks > 2 * sms, parts
+
+
+@pytest.mark.parametrize("Hkv,G,D,dtype,ctx,n", [
+    (4, 8, 128, "bf16", [40011], [32]), (4, 8, 128, "f16", [40011, 3000, 2000], [32, 32, 9]),
+    (6, 8, 64, "bf16", [30, 50000, 0, 2300], [32, 31, 0, 32]), (8, 4, 256, "f16", [30001, 1700, 1500], [32, 20, 32]),
+    (4, 7, 80, "bf16", [1500, 60001, 2900], [36, 33, 35])])
+def test_attend_joins_in_both_forms(sv, Hkv, G, D, dtype, ctx, n):
+    """Items in many parts and items in few, joined by one launch whose CTAs go
+    from tasks of the one form to tasks of the other."""
+    import torch
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    first_form, parts = _parts(ctx, n, G, D, Hkv, sms)
+    assert first_form and max(parts) > 8, parts
+    if len(ctx) > 1:
+        assert min(parts) <= 8, parts
+    rng = np.random.default_rng(D + Hkv)
+    B, T, Hq, page = len(ctx), max(n), Hkv * G, 32
+    width = -(-(max(ctx) + T) // page)
+    pages = sum(-(-(c + x) // page) for c, x in zip(ctx, n))
+    tc = _tc(sv, B, T, Hq, Hkv, D, page, pages, width, dtype)
+    q, kc, vc = (_rand(rng, s, dtype, 1.3) for s in ((B, T, Hq, D), (pages, page, Hkv, D), (pages, page, Hkv, D)))
+    free, table = rng.permutation(pages).tolist(), np.full((B, width), -1, np.int32)
+    see = np.zeros((B, T, T), bool)
+    par = ref.random_parents(rng, B, T, "random")
+    for b in range(B):
+        for i in range(-(-(ctx[b] + n[b]) // page)):
+            table[b, i] = free.pop()
+            # values that change along the context: a part that is lost or taken twice shows
+            vc[int(table[b, i])] += 3 * np.cos(6.3 * i * page / (ctx[b] + n[b]))
+        see[b] = ref.ancestors(par[b], n[b])[0]
+    got = tc.attend(q, kc, vc, _i32(table), _i32(ctx), _i32(n), tree_mask=_i32(ref.pack_mask(see)))
+    assert tc.check() == sv.SPEC_OK
+    u, scale, worst = ref.UNIT[dtype], D ** -0.5, 0.0
+    for b in range(B):
+        N = ctx[b] + n[b]
+        assert (got["out"][b, n[b]:] == 0).all() and (got["lse"][b, n[b]:] == -np.inf).all()
+        if not N or not n[b]:
+            continue
+        at = np.arange(N)
+        pg, off = (torch.from_numpy(x).cuda() for x in (table[b, at // page].astype(np.int64), at % page))
+        vis = np.concatenate([np.ones((n[b], ctx[b]), bool), see[b][:n[b], :n[b]]], 1)
+        vis = torch.from_numpy(vis).cuda()[:, None, :]
+        for hk in range(Hkv):
+            k, v = kc[pg, off, hk].double(), vc[pg, off, hk].double()
+            x = q[b, :n[b], hk * G:(hk + 1) * G].double()
+            s = torch.where(vis, (x @ k.T) * scale, -np.inf)
+            lse = torch.logsumexp(s, -1)
+            p = torch.exp(s - lse[..., None])
+            want, a = p @ v, p @ v.abs()
+            # scores: D-term fp32 sums, the exponent as in tree_ref; sums: 128 keys of a tile, the tiles of a
+            # part, the parts: far fewer than 1000 additions one after another; p and the output rounded
+            ds = (D + 8) * 2.0 ** -24 * scale * (x.abs() @ k.abs().T).amax(-1, keepdim=True) + 2.0 ** -17
+            sums = 1000 * 2.0 ** -24
+            tol = (u + 2 * ds + 4 * sums) * a + u * want.abs() * 1.01 + \
+                ref.TINY[dtype] * (1 + v.abs().sum(0) * (2.0 ** -7 if dtype == "f16" else 1.0))
+            err = (got["out"][b, :n[b], hk * G:(hk + 1) * G].double() - want).abs()
+            worst = max(worst, float((err / tol).max()))
+            assert (err <= tol).all(), (b, hk, worst)
+            el = (got["lse"][b, :n[b], hk * G:(hk + 1) * G].double() - lse).abs()
+            assert (el <= ds[..., 0] + sums + 2.0 ** -22 * lse.abs()).all(), (b, hk, float(el.max()))
+    tc.close()
+    from parity_util import report
+    report(f"joins, heads {Hq}/{Hkv} D={D} {dtype}: parts {min(parts)} to {max(parts)}, worst error {worst:.2f} of "
+           "its bound")
