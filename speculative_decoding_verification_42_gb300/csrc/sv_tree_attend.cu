@@ -160,10 +160,16 @@ __device__ __forceinline__ int att_limit(const TreeAttendParams& p, const AttGeo
 {
     return ctx + (p.mask ? n : min(n, (rp + 1) * g.group));
 }
+// key tiles of an item; its keys may reach 2^31 - 1
+template <int KT>
+__device__ __forceinline__ int att_tiles(int limit)
+{
+    return (int)(((uint32_t)limit + KT - 1) / KT);
+}
 template <int KT>
 __device__ __forceinline__ int att_cost(const TreeAttendParams& p, const AttGeom& g, int ctx, int n, int rp)
 {
-    return (att_limit(p, g, ctx, n, rp) + KT - 1) / KT + ATT_ITEM_COST;
+    return att_tiles<KT>(att_limit(p, g, ctx, n, rp)) + ATT_ITEM_COST;
 }
 // cost of all items of one key head of a sequence
 template <int KT>
@@ -210,7 +216,7 @@ struct AttIter {
         t0 = rp * g.group;
         ntok = min(g.group, n - t0);
         limit = att_limit(p, g, ctx, n, rp);
-        ntiles = (limit + KT - 1) / KT;
+        ntiles = att_tiles<KT>(limit);
         tile0 = max(pos - at - ATT_ITEM_COST, 0);
         tile1 = min(end - at - ATT_ITEM_COST, ntiles);
     }
@@ -640,12 +646,12 @@ __global__ void __launch_bounds__(Att<DP>::THREADS, 1)
                 const int boxes = (min(KT, last_key - kb) + w.page_box - 1) / w.page_box;
                 if (elect_one()) mbar_arrive_expect_tx(&full[st], (uint32_t)(boxes * w.page_box * 128 * NH));
                 // a tile's pages (at most 16) lie in one block
-                const int key = kb + lane * w.page_box;
+                const uint32_t key = (uint32_t)kb + lane * w.page_box;  // of no meaning from lane `boxes` on
                 const int page = __shfl_sync(0xffffffffu, cur, (key >> p.s.page_log2) & 31);
                 unsigned char* dst = ring + st * A::UNIT + lane * w.page_box * 128;
                 if (lane < boxes)
                     for (int h = 0; h < NH; ++h)
-                        tma_4d(dst + h * KT * 128, map, h * 64, hk, key & page_mask, page, &full[st]);
+                        tma_4d(dst + h * KT * 128, map, h * 64, hk, (int)(key & page_mask), page, &full[st]);
                 ++n;
                 if (++st == stages) st = 0, ++round;
                 if (t > 0 || !is_k) continue;

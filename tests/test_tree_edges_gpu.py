@@ -372,3 +372,28 @@ def test_attend_joins_in_both_forms(sv, Hkv, G, D, dtype, ctx, n):
     from parity_util import report
     report(f"joins, heads {Hq}/{Hkv} D={D} {dtype}: parts {min(parts)} to {max(parts)}, worst error {worst:.2f} of "
            "its bound")
+
+
+@pytest.mark.parametrize("D,T", [(16, 1), (256, 2)])
+def test_attend_over_almost_two_to_the_31_keys(sv, D, T):
+    """The longest context a table may describe (pages may repeat in it), to its last key."""
+    import torch
+    page, pages, width = 64, 1001, (1 << 25) - 1
+    N = page * width
+    tc = _tc(sv, 1, T, 1, 1, D, page, pages, width)
+    table = (torch.arange(width, device="cuda", dtype=torch.int32) % (pages - 1))[None].contiguous()
+    table[0, -1] = pages - 1
+    kc, vc = (torch.zeros(pages, page, 1, D, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    vc[...] = 1.0
+    vc[-1] = 2.0 ** 24  # the last page counts for a third
+    q = torch.ones(1, T, 1, D, dtype=torch.bfloat16, device="cuda")
+    got = tc.attend(q, kc, vc, table, _i32([N - T]), _i32([T]), tree_mask=_i32([[[(1 << T) - 1]] * T]))
+    assert tc.check() == sv.SPEC_OK
+    want = (N - page + page * 2.0 ** 24) / N
+    # probabilities of 1, sums of whole numbers in parts of 2^24 keys, the output's rounding
+    assert float((got["out"].double() - want).abs().max()) <= want * (2.0 ** -8 + 2.0 ** -14)
+    assert float((got["lse"].double() - np.log(N)).abs().max()) <= 2.0 ** -14
+    # a shorter one beside the end of the range: nothing is read past it
+    got = tc.attend(q, kc, vc, table, _i32([N - T + 1]), _i32([T]))
+    assert (got["out"] == 0).all() and (got["lse"] == -np.inf).all()
+    tc.close()
