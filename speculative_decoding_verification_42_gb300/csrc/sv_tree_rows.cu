@@ -18,7 +18,8 @@ namespace sv {
 // walks up the trees.  A warm call takes 6.4 us for 64 trees of 9 nodes and 10.4
 // us for 1000 of up to 64, a launch alone some 2.5.
 constexpr int PLAN_THREADS = 256;
-constexpr int PLAN_TOKENS = 1024;  // tokens of a sequence per CTA (grid y)
+constexpr int PLAN_TOKENS = 1024;  // tokens of a sequence per CTA (grid y), more where the grid ends
+constexpr int PLAN_MAX_Y = 65535;  // most CTAs of a grid's y
 constexpr int PLAN_WORDS = SPEC_TREE_MAX_NODES / 32;
 static_assert(SPEC_TREE_MAX_NODES <= PLAN_THREADS, "one thread per node of a tree");
 
@@ -101,8 +102,8 @@ __global__ void __launch_bounds__(PLAN_THREADS) k_tree_plan(const TreePlanParams
                 if (shortage && want <= avail) p.ring_out[0] = head + want;  // the first that is short
             }
         }
-        for (int j = blockIdx.y * PLAN_TOKENS + tid; j < min(T, (int)(blockIdx.y + 1) * PLAN_TOKENS);
-             j += PLAN_THREADS) {
+        for (int64_t i = (int64_t)blockIdx.y * PLAN_THREADS + tid; i < T; i += (int64_t)gridDim.y * PLAN_THREADS) {
+            const int j = (int)i;
             const int64_t at = (int64_t)b * T + j;
             int slot = -1, pos = -1;
             uint32_t m[PLAN_WORDS] = {};
@@ -144,7 +145,7 @@ cudaError_t launch_tree_plan(TreePlanParams p, int num_sms, cudaStream_t s)
     const int want = 4 * num_sms;
     p.rows_per_cta = std::max(1, (p.s.B + want - 1) / want);
     const dim3 grid(std::max(1, (p.s.B + p.rows_per_cta - 1) / p.rows_per_cta),
-                    (p.s.T + PLAN_TOKENS - 1) / PLAN_TOKENS);
+                    std::min((p.s.T - 1) / PLAN_TOKENS + 1, PLAN_MAX_Y));
     k_tree_plan<<<grid, PLAN_THREADS, 0, s>>>(p);
     return cudaGetLastError();
 }

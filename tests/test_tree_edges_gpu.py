@@ -397,3 +397,17 @@ def test_attend_over_almost_two_to_the_31_keys(sv, D, T):
     got = tc.attend(q, kc, vc, table, _i32([N - T + 1]), _i32([T]))
     assert (got["out"] == 0).all() and (got["lse"] == -np.inf).all()
     tc.close()
+
+
+def test_plan_of_a_very_long_chain(sv):
+    """More chunks of tokens than a grid's second dimension has CTAs."""
+    import torch
+    T, page = 68_000_003, 1024
+    width = T // page + 2
+    tc = _tc(sv, 1, T, 1, 1, 16, page, width, width)
+    pool = tc.new_pool(1)
+    got = tc.plan(_i32([700]), None, pool["held"], pool["ring"], pool["free_pages"], pool["block_table"])
+    assert got["row_status"].tolist() == [0] and got["held"].tolist() == [-(-(T + 700) // page)]
+    want = torch.arange(700, 700 + T, dtype=torch.int32, device="cuda")[None]
+    assert torch.equal(got["positions"], want) and torch.equal(got["slot_map"], want)
+    tc.close()
