@@ -299,7 +299,8 @@ class TreeCache:
         import torch
         i32, a = torch.int32, self._plan_args
         B = ctx_len.shape[0]
-        T = parents.shape[1] if parents is not None else int(max_tokens or self._max_tokens)
+        T = parents.shape[1] if parents is not None else \
+            self._max_tokens if max_tokens is None else int(max_tokens)
         b, bt = (B,), (B, T)
         a.ctx_len = self._tensor(ctx_len, b, i32, "ctx_len")
         a.n_tokens = None if n_tokens is None else self._tensor(n_tokens, b, i32, "n_tokens")

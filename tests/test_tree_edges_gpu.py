@@ -411,3 +411,14 @@ def test_plan_of_a_very_long_chain(sv):
     want = torch.arange(700, 700 + T, dtype=torch.int32, device="cuda")[None]
     assert torch.equal(got["positions"], want) and torch.equal(got["slot_map"], want)
     tc.close()
+
+
+def test_plan_of_no_tokens_is_refused(sv):
+    import torch
+    tc = _tc(sv, 2, 4, 2, 1, 32, 8, 4, 2)
+    pool = tc.new_pool(2)
+    with pytest.raises(sv.SpecVerifyError) as e:
+        tc.plan(_i32([0, 0]), None, pool["held"], pool["ring"], pool["free_pages"], pool["block_table"], max_tokens=0)
+    assert e.value.code == sv.SPEC_ERR_INVALID_ARG
+    torch.cuda.synchronize()
+    tc.close()
