@@ -329,12 +329,17 @@ __global__ void __launch_bounds__(KEEP_THREADS) k_tree_keep(const TreeKeepParams
     bool bad = false, lost = false;
     if (len_ok && planned == 0)
         for (int i = threadIdx.x; i < len; i += KEEP_THREADS) {
-            const int node = path[i];
-            if (node < 0 || node >= l.n || (i && node <= path[i - 1])) bad = true;
-            else lost = lost || !in_cache(l.ctx + node) || !in_cache(l.ctx + i);
+            // two loads at a time: the path's, then the tables'
+            const int node = path[i], before = i ? path[i - 1] : -1;
+            const bool inside = node >= 0 && node < l.n, from = in_cache(l.ctx + (inside ? node : 0)),
+                       to = in_cache(l.ctx + i);
+            bad = bad || !inside || node <= before;
+            lost = lost || !from || !to;
         }
-    bad = __syncthreads_or(bad);
-    lost = __syncthreads_or(lost);
+    if (__syncthreads_or(bad || lost)) {  // rare
+        bad = __syncthreads_or(bad);
+        lost = !bad;
+    }
     const int status = planned ? planned : !len_ok ? SPEC_ROW_BAD_LEN : bad ? SPEC_ROW_BAD_TREE
                                                                             : lost ? SPEC_ROW_NO_PAGES : 0;
     if (layer == 0 && blockIdx.z == 0 && threadIdx.x == 0) {
