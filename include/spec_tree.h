@@ -164,7 +164,8 @@ typedef struct {
  * (2 i, 2 i + 1) when interleaved.  All in fp32, rounded once.  q goes to
  * q_out, k and v (as it is) to their slots.  A node j >= n_b or with a slot
  * outside the cache gets a zero row in q_out and writes nothing to the cache;
- * one whose position cos_sin does not hold gets NaN in q_out and k.
+ * one whose position cos_sin does not hold gets NaN in the first rot_dim elements
+ * of q_out and k.
  * SPEC_ERR_UNSUPPORTED when a pointer to q, k, v, q_out, the weights or the
  * cache is not on 16 bytes, a stride is not a multiple of 8 elements (or is
  * beyond 2^36), a stride of the cache is 0 for a dimension larger than 1, or
@@ -194,18 +195,21 @@ spec_status spec_tree_append(spec_tree_t h, const spec_tree_append_args* a, void
  * sees the tokens below ctx_b and those nodes i < n_b whose bit is set in
  * tree_mask[b][j] (any bits: a node need not see itself); without a mask the
  * nodes i <= j.  What a node does not see has no effect on its row, whatever
- * its values.  lse is the natural logarithm of the sum of exp over the scores.
- * A node that sees nothing, whose finite sum is 0, or with j >= n_b has a zero
- * row and lse = -inf; so has every node of a sequence with ctx < 0, n outside
- * [0, T] or ctx + n beyond the table.  Keys and values of a page outside the
- * cache are zeros (a sequence that spec_tree_plan left without pages: its rows
- * have no meaning, and its status says so).  Scores, sums and outputs accumulate in
- * fp32; the probabilities are rounded to the 16-bit type (in f16 in units of
- * 2^-7 of the largest so far) before they meet V.
+ * its values; an infinite value that it sees gives that infinity, or NaN where
+ * its probability rounds to 0.  lse is the natural logarithm of the sum of exp
+ * over the scores.  A node that sees nothing, whose finite sum is 0, or with
+ * j >= n_b has a zero row and lse = -inf; so has every node of a sequence with
+ * ctx < 0, n outside [0, T] or ctx + n beyond the table.  Keys and values of a
+ * page outside the cache are zeros (a sequence that spec_tree_plan left without
+ * pages: its rows have no meaning, and its status says so).  Scores, sums and
+ * outputs accumulate in fp32; the probabilities are rounded to the 16-bit type
+ * (in f16 in units of 2^-7 of the largest so far) before they meet V.
  * SPEC_ERR_UNSUPPORTED when q, the cache, out or lse is not on 16 bytes, a
  * stride is not a multiple of 8 elements (or is beyond 2^36), or is 0 for a
- * dimension larger than 1; or when the key tiles of the call could pass 2^31
- * (B * kv_heads * T / (256 / G) * table_width * page_size / 64). */
+ * dimension larger than 1; or when the key tiles of the call could pass 2^31:
+ * B * kv_heads * ceil(T / R) * (ceil(table_width * page_size / 64) + 4), where
+ * R = 2 floor(128 / G) nodes for head_dim <= 128 and floor(128 / G) above, G =
+ * q_heads / kv_heads.  T and the table count there, not the lengths in use. */
 typedef struct {
     spec_tree_rows q;
     spec_tree_cache cache;

@@ -46,19 +46,23 @@
 // Measured (bf16, 8 key heads of 128 elements, 8 query heads to each where
 // nothing else is said, L2 flushed; bytes of K and V once):
 //   256 sequences of one token over 100 to 4000 keys: 347-355 us, 6.1-6.2 TB/s
-//     (0.91 of a copy);
-//   64 of up to 9 tokens over 100 to 4100 keys: 122-124 us, 4.6 TB/s;
-//   one of 32 tokens over 260000 keys: 202-212 us, 5.2 TB/s and 1.3 PFLOP/s.
+//     (0.89-0.91 of a copy);
+//   64 of up to 9 tokens over 100 to 4100 keys: 123-126 us, 4.5-4.6 TB/s;
+//   one of 32 tokens over 260000 keys: 206-218 us, 4.9-5.2 TB/s and 1.3 PFLOP/s.
 //     The chain scores, softmax, values of 256 rows takes some 3200 cycles a tile,
 //     of which the MMAs are 2048;
-//   16 of up to 64 tokens (two items each) over 4000 to 8191 keys: 175 us, 1.0
-//     PFLOP/s;
-//   6 chains of up to 333 f16 tokens of 7 heads of 80 elements: 61 us;
-//   one token of 4 heads to a key head over 500 keys: 17.5 us.
+//   16 of up to 64 tokens over 4000 to 8191 keys: 175-177 us, 1.0 PFLOP/s.  Both items
+//     of a key head read the keys from HBM: 836 MB where they are 403;
+//   6 chains of up to 333 f16 tokens of 7 heads of 80 elements: 61-69 us;
+//   one token of 4 heads to a key head over 500 keys: 17.5-19.6 us (14.5 warm).
 // An item costs some four tiles beside its keys: its masked tile, its output and
 // the first softmax of the next item are a chain that the rings cover in part.
 // Two warpgroups a stream, half of a tile's keys each, were slower (238 us where
-// this takes 204): a row's 2^x are bound by their unit, not by their chain.
+// this takes 204): the softmax of 64 columns takes 421 cycles with one warp on a
+// scheduler, 704 with the two that there are now and 1350 with four.  The 2^x are
+// the largest part of it (4 cycles a warp and instruction, 512 of the 704), but the
+// chain is the bound: with two row tiles their unit works 27 % of the time, the
+// tensor cores 59 %.
 //
 // What a row does not see must not touch it, whatever it holds: scores are
 // replaced by -inf before the maximum, but P V multiplies hidden values by a
@@ -685,8 +689,8 @@ __global__ void __launch_bounds__(Att<DP>::THREADS, 1)
         // ---------------- MMA issuer: one thread, whose every step (a poll, a commit)
         // keeps the tensor cores waiting: few commits, state in registers, and code
         // that fits the first instruction fetches.  Elected, not picked by its number:
-        // the MMAs of a branch that the compiler knows to be one thread's issue in half
-        // the cycles (17 against 52 each, measured).
+        // the MMAs of a branch that the compiler knows to be one thread's issue in a
+        // third of the cycles (17 against 52 each, measured).
         if (elect_one()) {
             const uint32_t id_o = umma_idesc(F16, true, ATT_ROWS, 0) | ((uint32_t)(p.s.D >> 3) << 17);
             const int dk = p.s.D / 16;  // k-steps of the scores

@@ -157,16 +157,17 @@ cudaError_t launch_tree_plan(TreePlanParams p, int num_sms, cudaStream_t s)
 // each element's mate in its pair, w the weights and r = 1 / sqrt(mean(x^2) +
 // eps), the norm and the rotation are y = r (x A + z B) with A = w cos and B =
 // -+ w(mate) sin, which a thread forms once per token for all query heads and
-// once for all key heads.  HBM bound by its bytes (each element read and
-// written once), but near the issue rate: so few instructions per element, and
-// a token's heads on as few warps as still fill the machine (1, 2, 4 or 8; the
-// angles and weights are per thread).  Loads of APP_UNROLL heads are in flight
-// together (with eight, registers leave too few warps: 57 us for 6000 tokens).
+// once for all key heads.  Its bytes (each element read and written once) would
+// be HBM's to bound, but it is bound by latency and registers: A, B and the loads
+// take 80 of them and spill, which leaves 24 warps to an SM, and the schedulers
+// issue in half of their cycles.  So few instructions per element, and a token's
+// heads on as few warps as still fill the machine (1, 2, 4 or 8; the angles and
+// weights are per thread).  Loads of APP_UNROLL heads are in flight together (with
+// eight, registers leave too few warps: 57 us for 6000 tokens).
 // Everything is fp32 up to the one rounding of the output; rsqrtf is within two
 // ulps.  Warm: one token of 80 heads of 128 elements 8.3 us, 64 sequences of up to
 // 9 of them 12.5 us (1.6 TB/s), 100 of up to 60 f16 tokens of 36 heads of 80
-// elements 31 us (1.7 TB/s): the unpacking, products and packing of 8 elements
-// bound it, and a head of 80 leaves 6 of its 16 lanes idle.
+// elements 31 us (1.8 TB/s), where a head of 80 leaves 6 of its 16 lanes idle.
 constexpr int APP_THREADS = 256, APP_UNROLL = 4;
 
 template <bool F16, int LANES>
@@ -312,9 +313,10 @@ cudaError_t launch_tree_append(const TreeAppendParams& p, int dtype, int num_sms
 // Thread = one 16-byte column of a head row; it takes the path's rows in
 // ascending order, four at a time (loads before stores).  path is strictly
 // ascending, so path[i] >= i and a row stored at place i < path[k] for every
-// k > i: no store reaches a row that is still to be read.  Bound by the latency
-// of its dependent loads (path, table, row): warm 6.2 us for 64 sequences and 4
-// layers, 9.9 us for 200 and 8.
+// k > i: no store reaches a row that is still to be read.  The path and its pages
+// are looked over first, so that a sequence that cannot move keeps all its rows.
+// Bound by the latency of its dependent loads (path, table, row): warm 6.2 us for
+// 64 sequences and 4 layers, 10.5 us for 200 and 8 (10.1 without the pages).
 constexpr int KEEP_THREADS = 256;
 
 __global__ void __launch_bounds__(KEEP_THREADS) k_tree_keep(const TreeKeepParams p)
