@@ -53,7 +53,8 @@ enum {
     SPEC_ROW_BAD_LEN = 5,  /* ctx < 0, n outside [0, T], held outside [0, table_width], */
                            /* ctx + n beyond the table, or a path longer than n          */
     SPEC_ROW_BAD_TREE = 6, /* a parent outside [-1, j) for node j; a path not ascending  */
-    SPEC_ROW_NO_PAGES = 7  /* the ring of free pages is too short for this sequence      */
+    SPEC_ROW_NO_PAGES = 7  /* the ring of free pages is too short for this sequence;     */
+                           /* keep: a token's page is not in the cache                   */
 };
 
 /* largest T of a tree (chains, i.e. calls without parents or masks, have no
