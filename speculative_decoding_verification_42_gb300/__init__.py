@@ -9,14 +9,17 @@ raises.
 ``Verifier`` is a convenience wrapper that takes torch tensors (device memory
 and the current CUDA stream come from PyTorch) and calls the same entry points.
 ``TreeCache`` (tree.py) does the same for the operators around the verify step,
-declared in ``include/spec_tree.h``.
+declared in ``include/spec_tree.h``, and ``logprobs`` and ``distill`` (score.py)
+for those that score rows of logits, declared in ``include/spec_score.h``.
 """
 from __future__ import annotations
 
 import ctypes as C
 import os
 
+from . import score as _score
 from . import tree as _tree
+from .score import *  # noqa: F401,F403  (the operators of include/spec_score.h)
 from .tree import *  # noqa: F401,F403  (the operators of include/spec_tree.h)
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -35,7 +38,7 @@ ABI_FUNCTIONS = ("spec_verify_create", "spec_verify_run", "spec_draft_sample",
                  "spec_verify_destroy", "spec_verify_status_string", "spec_verify_run_noalloc",
                  "spec_verify_set_profiling", "spec_lmhead_logits", "spec_verify_run_early_exit",
                  "spec_verify_check", "spec_verify_inject_fault", "spec_verify_set_allocator") + \
-    _tree.TREE_FUNCTIONS
+    _tree.TREE_FUNCTIONS + _score.SCORE_FUNCTIONS
 SPEC_FAULT_NONE, SPEC_FAULT_STALL_STREAM = 0, 1
 
 # spec_alloc_fn / spec_release_fn of spec_verify_set_allocator
@@ -119,6 +122,7 @@ def load_library(path: str | None = None) -> C.CDLL:
     L.spec_verify_set_allocator.argtypes = [SPEC_ALLOC_FN, SPEC_RELEASE_FN, C.c_void_p]
     L.spec_verify_set_allocator.restype = C.c_int
     _tree.bind(L)
+    _score.bind(L)
     if path is None:
         _lib = L
     return L
@@ -278,19 +282,25 @@ class Verifier:
 
     def run(self, target, draft, draft_tokens, k_per_row=None, *, temperature=1.0, top_k=0,
             top_p=1.0, seed=0, round=0, out: dict | None = None, debug: bool = True,
-            stream=None, w_vocab=None, alpha: bool = False, early_exit: bool = False) -> dict:
+            stream=None, w_vocab=None, alpha: bool = False, early_exit: bool = False,
+            logprobs: int | None = None) -> dict:
         """Verify a batch; returns (and fills) a dict of output tensors.  With the
         LM head, ``target`` is the hidden states [B * (K + 1), H] and ``w_vocab``
         the [H, V] matrix.  alpha: also the acceptance statistic of every slot.
         early_exit: read each sequence's rows only up to its first rejection.
+        logprobs: also ``out["logprobs"]``, what ``logprobs(target, out["tokens"],
+        top_n=logprobs)`` gives: the emitted tokens under the target's rows as they
+        are, before the knobs (not with the LM head, whose logits stay inside).
         stream: the one to run on, which waits for nothing by itself (default: the
         current one); the tensors may be dropped right after the call."""
         if stream is not None:
             return _tree.on_stream(stream, self.device, self.run, target, draft, draft_tokens, k_per_row,
                                    temperature=temperature, top_k=top_k, top_p=top_p, seed=seed,
                                    round=round, out=out, debug=debug, w_vocab=w_vocab, alpha=alpha,
-                                   early_exit=early_exit)
+                                   early_exit=early_exit, logprobs=logprobs)
         import torch
+        if logprobs is not None and w_vocab is not None:
+            raise ValueError("logprobs needs the target's logits, which the LM head does not give out")
         if w_vocab is not None:
             B, K = draft_tokens.shape[0], draft_tokens.shape[1]
             V = w_vocab.shape[1]
@@ -316,6 +326,8 @@ class Verifier:
         s = torch.cuda.current_stream(dev)
         run = spec_verify_run_early_exit if early_exit else spec_verify_run
         run(self.h, ins, self.sampling(temperature, top_k, top_p, seed, round), outs, s.cuda_stream)
+        if logprobs is not None:
+            out["logprobs"] = _score.logprobs(target, out["tokens"], top_n=logprobs, out=out.get("logprobs"))
         return out
 
     def draft_sample(self, draft, k_per_row=None, *, temperature=1.0, top_k=0, top_p=1.0,

@@ -1,0 +1,50 @@
+// sv_score.cuh -- parameters of the operators that score rows of logits
+// (include/spec_score.h), and what their kernels share.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "spec_score.h"
+#include "sv_internal.cuh"
+
+namespace sv {
+
+struct ScoreParams {
+    const char* x;           // logits
+    int64_t x_seq, x_tok;    // strides, elements
+    char* grad;              // gradient rows or NULL
+    int64_t g_seq, g_tok;
+    int32_t rows, T, V;
+    float temp, inv_temp, c; // temperature, 1 / it, log2(e) / it
+    int32_t* row_status;
+    const int32_t* ids;      // logprobs: [rows] or NULL; distill: [rows, k]
+    // logprobs
+    const float* g_logprob;  // [rows] or NULL
+    const float* g_entropy;
+    int32_t top_n;
+    float* logprob;
+    int32_t* rank;
+    float* entropy;
+    float* lse;
+    int32_t* top_ids;        // [rows, top_n]
+    float* top_lp;
+    // distill
+    const void* teacher;     // [rows, k]
+    int32_t teacher_dtype;
+    int32_t k, tail;
+    float teacher_temp;
+    const float* teacher_lse;
+    const float* g_loss;
+    float* loss;
+    float* accept;
+};
+
+cudaError_t launch_score_logprobs(const ScoreParams& p, int dtype, int num_sms, cudaStream_t s);
+cudaError_t launch_score_distill(const ScoreParams& p, int dtype, int num_sms, cudaStream_t s);
+
+constexpr size_t SCORE_MAX_ROW_BYTES = 8 * 208 * 1024;  // of one row of logits
+
+}  // namespace sv
