@@ -61,7 +61,7 @@ typedef struct {
     int32_t tokens;       /* T                                                          */
     int32_t vocab;        /* V                                                          */
     int32_t top_n;        /* likeliest tokens to report, 0 <= top_n <= MAX_TOP          */
-    float temperature;    /* > 0                                                        */
+    float temperature;    /* 1e-30 to 1e30                                              */
     spec_score_rows logits;
     const int32_t* ids;        /* [B, T] tokens, -1: row not scored; or NULL            */
     const float* grad_logprob; /* [B, T] upstream gradient of logprob, or NULL: 0       */
@@ -106,8 +106,8 @@ typedef struct {
     int32_t vocab;         /* V                                                         */
     int32_t entries;       /* k teacher entries a row, 1 <= k <= MAX_ENTRIES            */
     int32_t tail;          /* 0: renormalised; 1: what is left is an outcome of its own */
-    float temperature;         /* > 0, of the student's logits                          */
-    float teacher_temperature; /* > 0, of the teacher's values                          */
+    float temperature;         /* of the student's logits, 1e-30 to 1e30                */
+    float teacher_temperature; /* of the teacher's values, 1e-30 to 1e30                */
     spec_score_rows student;
     const int32_t* ids;        /* [B, T, k] the entries' tokens, -1: no entry           */
     const void* teacher;       /* [B, T, k] the entries' logits, or log probabilities   */

@@ -18,7 +18,10 @@ struct ScoreParams {
     char* grad;              // gradient rows or NULL
     int64_t g_seq, g_tok;
     int32_t rows, T, V;
-    float temp, inv_temp, c; // temperature, 1 / it, log2(e) / it
+    float inv_temp, c, c_lo; // 1 / temperature, log2(e) / it from below, and what is left of that (> 0)
+    double inv_temp_d;
+    int32_t cluster;         // CTAs of a row (the launch fills it in)
+    int32_t top_at;          // offset of the search's scratch in shared memory (the launch)
     int32_t* row_status;
     const int32_t* ids;      // logprobs: [rows] or NULL; distill: [rows, k]
     // logprobs
@@ -35,7 +38,8 @@ struct ScoreParams {
     const void* teacher;     // [rows, k]
     int32_t teacher_dtype;
     int32_t k, tail;
-    float teacher_temp;
+    float inv_tt, inv_tt_lo; // 1 / the teacher's temperature, and what is left of it
+    double inv_tt_d;
     const float* teacher_lse;
     const float* g_loss;
     float* loss;

@@ -12,7 +12,7 @@ namespace {
 
 bool dtype_ok(int32_t d) { return d == SPEC_F32 || d == SPEC_BF16 || d == SPEC_F16; }
 size_t size_of(int32_t d) { return d == SPEC_F32 ? 4 : 2; }
-bool temp_ok(float t) { return t > 0.f && !isinf(t) && !isinf(1.4426951f / t); }
+bool temp_ok(float t) { return t >= 1e-30f && t <= 1e30f; }
 bool strides_ok(const spec_score_rows& r) { return r.seq_stride >= 0 && r.token_stride >= 0; }
 constexpr int64_t MAX_STRIDE = (int64_t)1 << 34;  // products with a number of rows stay below 2^63
 bool strides_fit(const spec_score_rows& r) { return r.seq_stride < MAX_STRIDE && r.token_stride < MAX_STRIDE; }
@@ -71,9 +71,12 @@ ScoreParams rows_of(int32_t batch, int32_t tokens, int32_t vocab, float temp, co
     p.rows = batch * tokens;
     p.T = tokens;
     p.V = vocab;
-    p.temp = temp;
     p.inv_temp = 1.f / temp;
-    p.c = (float)(1.4426950408889634 / (double)temp);
+    p.inv_temp_d = 1.0 / (double)temp;
+    const double c = 1.4426950408889634 / (double)temp;
+    p.c = (float)c;
+    if ((double)p.c >= c) p.c = nextafterf(p.c, 0.f);
+    p.c_lo = fmaxf((float)(c - (double)p.c), 1.17549435e-38f);
     p.row_status = row_status;
     return p;
 }
@@ -140,7 +143,9 @@ spec_status spec_score_distill(const spec_score_distill_args* a, void* stream)
     p.tail = a->tail ? 1 : 0;
     p.teacher = a->teacher;
     p.teacher_dtype = a->teacher_dtype;
-    p.teacher_temp = a->teacher_temperature;
+    p.inv_tt_d = 1.0 / (double)a->teacher_temperature;
+    p.inv_tt = (float)p.inv_tt_d;
+    p.inv_tt_lo = (float)(p.inv_tt_d - (double)p.inv_tt);
     p.teacher_lse = a->teacher_lse;
     p.g_loss = a->grad_loss;
     p.loss = a->loss;

@@ -76,6 +76,9 @@ def logprobs(l, tok, temp, top_n, kind, gl=0.0, gh=0.0):
     rel = bz + U * (12 + 3 * ad)
     off = p * (abs(gl) * rel + abs(gh) * (np.abs(np.where(live, lp + ent, 0)) * rel + bz + bound["entropy"]
                                           + U * (4 * ad + 4 * abs(lz) + 4 * ent)))
+    # 2^x is 0 below 2^-126: of p (gl + gh (ln p + H)) that loses what it has at p = 2^-126 at most, as p |ln p| grows
+    # with p there: 2^-126 (|gl| + |gh| (126 ln 2 + ln Z + H))
+    off = off + 2.0 ** -126 * (abs(gl) + abs(gh) * (88 + abs(lz) + ent))
     off = off + 4 * U * (abs(gl) * (0 if tok is None else (np.arange(V) == tok)))
     bound["grad"] = off / temp * 1.01 + (np.abs(res["grad"]) + off / temp) * (HALF[kind] * 1.01 + 2 * U) + 8 * LEAST[kind]
     return res, bound
