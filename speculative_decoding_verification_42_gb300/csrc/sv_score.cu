@@ -26,10 +26,11 @@ namespace sv {
 
 namespace {
 
-constexpr int SC_NT = 256;      // threads of a CTA
+constexpr int SC_NT = 128;      // threads of a CTA
 constexpr int SC_WARPS = SC_NT / 32;
 constexpr int SC_BATCH = 4;     // vectors of a thread per copy group
-constexpr int SC_MAXC = 8;      // CTAs of a cluster (portable)
+constexpr int SC_MAXC = SCORE_MAX_CTAS;  // CTAs of a cluster (portable)
+constexpr int SC_PARTS = SC_MAXC * SC_WARPS;  // warps of a cluster: one lane each where they are joined
 constexpr int SC_LIST = 1024;   // candidates for the top tokens, all CTAs of a row together
 constexpr uint32_t KEY_NEG_INF = 0x007FFFFFu;  // key_of(-inf)
 constexpr float LN2 = 0.693147180559945f;
@@ -246,6 +247,12 @@ __device__ __forceinline__ uint32_t cluster_rank()
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
     return r;
 }
+__device__ __forceinline__ int cluster_id()
+{
+    int r;
+    asm volatile("mov.u32 %0, %%clusterid.x;" : "=r"(r));
+    return r;
+}
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
 // the address of a shared variable in CTA `rank` of the cluster
@@ -266,66 +273,68 @@ template <typename E> struct Slice {
     const char* src;  // global address of the first
     int n;            // vectors
     int first;        // element of the row at the first vector's start (negative: outside the row)
-    int nb;           // copy groups of a thread
+    int lo, hi;       // vectors lo .. hi - 1 lie in the row as a whole; one before and one behind may not
     int V;
 
-    __device__ __forceinline__ Slice(const ScoreParams& p, const E* x, int rank, int C, void* smem)
+    __device__ __forceinline__ Slice(const ScoreParams& p, const E* x, int rank, void* smem)
     {
-        const int mis = (int)((uintptr_t)x & 15);
-        const int all = (int)((mis + (int64_t)p.V * (int)sizeof(E) + 15) / 16), per = (all + C - 1) / C;
-        const int v0 = min(rank * per, all);
-        n = min(per, all - v0);
+        const int mis = (int)((uintptr_t)x & 15), all = (mis + p.V * (int)sizeof(E) + 15) / 16, v0 = rank * p.per;
+        n = max(0, min(p.per, all - v0));
         first = v0 * EPV<E> - mis / (int)sizeof(E);
         src = (const char*)x - mis + (int64_t)v0 * 16;
-        nb = (n + SC_NT * SC_BATCH - 1) / (SC_NT * SC_BATCH);
         buf = (uint4*)smem;
         V = p.V;
+        lo = first < 0 ? 1 : 0;
+        hi = max(lo, first + n * EPV<E> > V ? n - 1 : n);
     }
-    // a vector that lies in the row as a whole
-    __device__ __forceinline__ bool whole(int i) const
-    {
-        const int e = first + i * EPV<E>;
-        return e >= 0 && e <= V - EPV<E>;
-    }
+    __device__ __forceinline__ int full() const { return n / (SC_NT * SC_BATCH); }  // batches of all threads
     __device__ __forceinline__ bool has(int id) const { return id >= first && id < first + n * EPV<E> && id < V; }
     __device__ __forceinline__ Bits<E>* at(int id) const { return (Bits<E>*)buf + (id - first); }
 
+    // vector i by its elements, -inf outside the row
+    __device__ __forceinline__ void copy_part(int i) const
+    {
+        const int e = first + i * EPV<E>;
+        const Bits<E>* from = (const Bits<E>*)(src + (int64_t)i * 16);
+        Bits<E> v[EPV<E>];
+#pragma unroll
+        for (int q = 0; q < EPV<E>; ++q) v[q] = e + q >= 0 && e + q < V ? from[q] : (Bits<E>)Vec<E>::NEG;
+        buf[i] = vector_of<E>(v);
+    }
+    // every thread copies what it reads: vectors tid, tid + SC_NT, ...; a group for each full batch, one for the rest
     __device__ __forceinline__ void copy() const
     {
         const uint32_t to = (uint32_t)__cvta_generic_to_shared(buf);
-        for (int b = 0; b < nb; ++b) {
+        auto one = [&](int i) {
+            if (i >= lo && i < hi)
+                asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(to + i * 16),
+                             "l"(src + (int64_t)i * 16)
+                             : "memory");
+        };
+        int i = threadIdx.x;
+        for (int b = full(); b > 0; --b) {
 #pragma unroll
-            for (int j = 0; j < SC_BATCH; ++j) {
-                const int i = (b * SC_BATCH + j) * SC_NT + threadIdx.x;
-                if (i >= n) continue;
-                if (whole(i)) {
-                    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(to + i * 16),
-                                 "l"(src + (int64_t)i * 16)
-                                 : "memory");
-                } else {
-                    const int e = first + i * EPV<E>;
-                    const Bits<E>* from = (const Bits<E>*)(src + (int64_t)i * 16);
-                    Bits<E> v[EPV<E>];
-#pragma unroll
-                    for (int q = 0; q < EPV<E>; ++q) v[q] = e + q >= 0 && e + q < V ? from[q] : (Bits<E>)Vec<E>::NEG;
-                    buf[i] = vector_of<E>(v);
-                }
-            }
+            for (int j = 0; j < SC_BATCH; ++j, i += SC_NT) one(i);
             asm volatile("cp.async.commit_group;" ::: "memory");
         }
+        for (; i < n; i += SC_NT) one(i);
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        if (lo && n && threadIdx.x == 0) copy_part(0);
+        if (hi < n && n - 1 >= lo && (n - 1) % SC_NT == threadIdx.x) copy_part(n - 1);
     }
-    // this thread's copies of groups 0 .. b have arrived (later ones may have, too)
-    __device__ __forceinline__ void arrived(int b) const
+    // this thread's copies but those of the last `left` groups have arrived (of these, some may have, too)
+    static __device__ __forceinline__ void arrived(int left)
     {
-        switch (nb - 1 - b) {
+        switch (left) {
         case 0: asm volatile("cp.async.wait_group 0;" ::: "memory"); break;
         case 1: asm volatile("cp.async.wait_group 1;" ::: "memory"); break;
         case 2: asm volatile("cp.async.wait_group 2;" ::: "memory"); break;
         case 3: asm volatile("cp.async.wait_group 3;" ::: "memory"); break;
-        default: asm volatile("cp.async.wait_group 4;" ::: "memory"); break;
+        case 4: asm volatile("cp.async.wait_group 4;" ::: "memory"); break;
+        case 5: asm volatile("cp.async.wait_group 5;" ::: "memory"); break;
+        default: asm volatile("cp.async.wait_group 6;" ::: "memory"); break;
         }
     }
-    __device__ __forceinline__ void arrived_all() const { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
 };
 
 // a running softmax: maximum, sum of 2^d, sum of d 2^d, d relative to the maximum
@@ -337,27 +346,22 @@ __device__ __forceinline__ float ref_of(float m) { return m == -INFINITY ? 0.f :
 // sums of a thread's vectors, by ENTROPY those of d 2^d too; without it c is taken in two parts (c + c_lo, c_lo > 0),
 // since a loss near its minimum shows the constant's rounding; with RANK also the number of elements above x (in
 // vectors before tvec: or equal to it, written as above the next value below x)
-template <typename E, bool ENTROPY, bool RANK>
-__device__ __forceinline__ Run sum_slice(const Slice<E>& sl, float c, float c_lo, bool waits, int tvec, float x, float x_below,
-                                         int& ahead)
-{
+template <typename E, bool ENTROPY, bool RANK> struct Summer {
     float m = -INFINITY;
-    uint64_t s2 = pair(0.f, 0.f), t2 = s2;
-    const uint64_t c2 = pair(c, c), l2 = pair(c_lo, c_lo);
-    const typename Vec<E>::Thr at = Vec<E>::thr_of(x), under = Vec<E>::thr_of(x_below);
-    for (int b = 0; b < sl.nb; ++b) {
-        if (waits) sl.arrived(b);
-        uint4 w[SC_BATCH];
-        float mx = -INFINITY;
+    uint64_t s2 = 0, t2 = 0, c2, l2;
+    typename Vec<E>::Thr at, under;
+    int tvec, ahead = 0;
+
+    template <int N> __device__ __forceinline__ void take(const uint4 (&w)[N], int i)
+    {
+        float mx = Vec<E>::top(w[0]);
 #pragma unroll
-        for (int j = 0; j < SC_BATCH; ++j) {
-            const int i = (b * SC_BATCH + j) * SC_NT + threadIdx.x;
-            w[j] = i < sl.n ? sl.buf[i] : make_uint4(Vec<E>::NEG, Vec<E>::NEG, Vec<E>::NEG, Vec<E>::NEG);
-            mx = fmax_nan(mx, Vec<E>::top(w[j]));
-        }
+        for (int j = 1; j < N; ++j) mx = fmax_nan(mx, Vec<E>::top(w[j]));
         if (!(mx <= m)) {  // a new maximum (or NaN, which stays): rescale
             mx = fmax_nan(m, mx);
             if (m > -INFINITY) {
+                float c, c_;
+                unpair(c2, c, c_);
                 const float d = fmaxf((m - mx) * c, NONE), f = ex2_fast(d);
                 const uint64_t f2 = pair(f, f);
                 if (ENTROPY) t2 = mul2(f2, fma2(pair(d, d), s2, t2));
@@ -368,7 +372,7 @@ __device__ __forceinline__ Run sum_slice(const Slice<E>& sl, float c, float c_lo
         const float ref = -ref_of(m);
         const uint64_t r2 = pair(ref, ref);
 #pragma unroll
-        for (int j = 0; j < SC_BATCH; ++j) {
+        for (int j = 0; j < N; ++j) {
             uint64_t v[EPV<E> / 2];
             Vec<E>::pairs(w[j], v);
 #pragma unroll
@@ -380,21 +384,34 @@ __device__ __forceinline__ Run sum_slice(const Slice<E>& sl, float c, float c_lo
                 s2 = add2(s2, e2);
                 if (ENTROPY) t2 = fma2(e2, pair(fmaxf(a, NONE), fmaxf(z, NONE)), t2);
             }
-            if (RANK) {
-                const int i = (b * SC_BATCH + j) * SC_NT + threadIdx.x;
-                ahead += Vec<E>::above(w[j], i < tvec ? under : at);
-            }
+            if (RANK) ahead += Vec<E>::above(w[j], i + j * SC_NT < tvec ? under : at);
         }
     }
-    float a, z;
-    Run r;
-    r.m = m;
-    unpair(s2, a, z);
-    r.s = a + z;
-    unpair(t2, a, z);
-    r.t = a + z;
-    return r;
-}
+    __device__ __forceinline__ Run run(const Slice<E>& sl, bool waits)
+    {
+        int i = threadIdx.x;
+        for (int b = sl.full(); b > 0; --b, i += SC_NT * SC_BATCH) {
+            if (waits) sl.arrived(b);
+            uint4 w[SC_BATCH];
+#pragma unroll
+            for (int j = 0; j < SC_BATCH; ++j) w[j] = sl.buf[i + j * SC_NT];
+            take(w, i);
+        }
+        if (waits) sl.arrived(0);
+        for (; i < sl.n; i += SC_NT) {
+            const uint4 w[1] = {sl.buf[i]};
+            take(w, i);
+        }
+        float a, z;
+        Run r;
+        r.m = m;
+        unpair(s2, a, z);
+        r.s = a + z;
+        unpair(t2, a, z);
+        r.t = a + z;
+        return r;
+    }
+};
 
 // rescales a run to a maximum that is no smaller
 __device__ __forceinline__ void to_max(Run& r, float m, float c)
@@ -411,35 +428,24 @@ template <typename X, typename F> __device__ __forceinline__ X warp_reduce(X x, 
     for (int d = 16; d; d >>= 1) x = op(x, __shfl_xor_sync(~0u, x, d));
     return x;
 }
-// reductions over the CTA in a fixed order; every thread gets the result
-template <typename X, typename F> __device__ __forceinline__ X block_reduce(X x, F op)
+__device__ __forceinline__ float warp_max(float x)
 {
-    __shared__ X part[SC_WARPS];
-    x = warp_reduce(x, op);
-    __syncthreads();
-    if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = x;
-    __syncthreads();
-    x = part[0];
-#pragma unroll
-    for (int i = 1; i < SC_WARPS; ++i) x = op(x, part[i]);
-    return x;
+    return warp_reduce(x, [](float a, float b) { return fmax_nan(a, b); });
 }
-template <typename X> __device__ __forceinline__ X block_sum(X x)
+template <typename X> __device__ __forceinline__ X warp_sum(X x)
 {
-    return block_reduce(x, [](X a, X b) { return a + b; });
-}
-__device__ __forceinline__ float block_max(float x)
-{
-    return block_reduce(x, [](float a, float b) { return fmax_nan(a, b); });
+    return warp_reduce(x, [](X a, X b) { return a + b; });
 }
 
-template <typename E> __device__ const E* row_of(const ScoreParams& p, int r)
+template <typename E> __device__ __forceinline__ const E* row_of(const ScoreParams& p, int r)
 {
-    return (const E*)p.x + (int64_t)(r / p.T) * p.x_seq + (int64_t)(r % p.T) * p.x_tok;
+    const int b = p.by_tokens.of(r);
+    return (const E*)p.x + (int64_t)b * p.x_seq + (int64_t)(r - b * p.T) * p.x_tok;
 }
-template <typename E> __device__ E* grad_of(const ScoreParams& p, int r)
+template <typename E> __device__ __forceinline__ E* grad_of(const ScoreParams& p, int r)
 {
-    return (E*)p.grad + (int64_t)(r / p.T) * p.g_seq + (int64_t)(r % p.T) * p.g_tok;
+    const int b = p.by_tokens.of(r);
+    return (E*)p.grad + (int64_t)b * p.g_seq + (int64_t)(r - b * p.T) * p.g_tok;
 }
 
 // a row without a gradient, by the cluster's CTAs
@@ -455,15 +461,13 @@ template <typename E> __device__ void zero_grad(const ScoreParams& p, int r, int
     if (rest < p.V) g[rest] = narrow<E>(0.f);
 }
 
-// the gradient of a slice: f(logits of a pair, as distances d from -ref times c, and 2^d) -> pair
+// the gradient of a slice: f(distances d of a pair of logits from m, times c; 2^d) -> pair
 template <typename E, typename F>
 __device__ __forceinline__ void grad_slice(const Slice<E>& sl, E* g, float m, float c, F f)
 {
     const float ref = -ref_of(m);
     const uint64_t r2 = pair(ref, ref), c2 = pair(c, c);
-    E* out = g + sl.first;  // its element at the slice's start
-    const bool straight = ((uintptr_t)out & 15) == 0;
-    for (int i = threadIdx.x; i < sl.n; i += SC_NT) {
+    auto grad = [&](int i) {
         uint64_t v[EPV<E> / 2], y[EPV<E> / 2];
         Vec<E>::pairs(sl.buf[i], v);
 #pragma unroll
@@ -473,18 +477,35 @@ __device__ __forceinline__ void grad_slice(const Slice<E>& sl, E* g, float m, fl
             unpair(d2, a, z);
             y[q] = f(a, z, pair(ex2_fast(a), ex2_fast(z)));
         }
-        const uint4 w = Vec<E>::pack(y);
-        if (straight && sl.whole(i)) ((uint4*)out)[i] = w;
-        else sl.buf[i] = w;
-        if (straight && !sl.whole(i)) {
-            const int e = sl.first + i * EPV<E>;
+        return Vec<E>::pack(y);
+    };
+    E* out = g + sl.first;  // its element at the slice's start
+    if (((uintptr_t)out & 15) == 0) {
+        uint4* to = (uint4*)out;
+        int i = threadIdx.x;
+        for (int b = sl.full(); b > 0; --b)
+#pragma unroll
+            for (int j = 0; j < SC_BATCH; ++j, i += SC_NT) {
+                const uint4 w = grad(i);
+                if (i >= sl.lo && i < sl.hi) to[i] = w;
+            }
+        for (; i < sl.n; i += SC_NT) {
+            const uint4 w = grad(i);
+            if (i >= sl.lo && i < sl.hi) to[i] = w;
+        }
+        // the vectors that are not the row's as a whole
+        const int part = threadIdx.x == 0 ? 0 : sl.n - 1;
+        if (threadIdx.x < 2 && sl.n > 0 && (part < sl.lo || part >= sl.hi)) {
+            const uint4 w = grad(part);
+            const int e = sl.first + part * EPV<E>;
 #pragma unroll
             for (int q = 0; q < EPV<E>; ++q)
                 if (e + q >= 0 && e + q < sl.V) ((Bits<E>*)g)[e + q] = bits_at<E>(w, q);
         }
+        return;
     }
-    if (straight) return;
     // the gradient's rows start elsewhere in a vector than the logits': elements change vectors on the way out
+    for (int i = threadIdx.x; i < sl.n; i += SC_NT) sl.buf[i] = grad(i);
     __syncthreads();
     const int e0 = max(sl.first, 0), e1 = min(sl.first + sl.n * EPV<E>, sl.V);
     if (e0 >= e1) return;
@@ -504,20 +525,19 @@ __device__ __forceinline__ void grad_slice(const Slice<E>& sl, E* g, float m, fl
 }
 
 // ---- log probabilities ------------------------------------------------------ //
-struct LpPart {      // what a CTA knows of the row
+struct LpPart {      // what a warp knows of the row
     float m, s, t;
     int32_t ahead;
-    uint32_t kmin;   // the smallest of its threads' largest keys, of those with an unmasked token
 };
 struct LpRow {
     float m, s, t;
     int32_t ahead;
-    uint32_t kmin;
+    uint32_t bound;  // a key that the top tokens reach, and not many others
 };
 
 // scratch of the search for the top tokens, behind the slice
 struct TopScratch {
-    uint32_t keys[SC_MAXC][SC_NT];      // the largest key of every thread of the cluster
+    uint32_t keys[SC_MAXC][32];         // the largest key of every four threads of the cluster
     unsigned long long list[SC_LIST];   // CTA 0: candidates, key and inverted id, SC_LIST / C to a CTA
     int32_t counts[SC_MAXC];            // CTA 0: candidates of each CTA
     int32_t mine;                       // candidates of this CTA
@@ -560,10 +580,18 @@ __device__ void give_candidates(const Slice<E>& sl, TopScratch& ts, uint32_t bou
             remote_st(list + at * 8 + 4, key);
         }
     };
-    if (my_key >= bound)
-        each_mine(sl, [&](uint32_t key, int id) {
-            if (key >= bound) give(key, id);
-        });
+    if (my_key >= bound) {
+        const float least = val_of(bound);
+        for (int i = threadIdx.x; i < sl.n; i += SC_NT) {
+            const uint4 w = sl.buf[i];
+            if (Vec<E>::top(w) < least) continue;
+#pragma unroll
+            for (int q = 0; q < EPV<E>; ++q) {
+                const uint32_t key = key_of(value_of<E>(bits_at<E>(w, q)));
+                if (key >= bound) give(key, sl.first + i * EPV<E> + q);
+            }
+        }
+    }
     __syncthreads();
     int found = ts.mine;
     if (found > share) {
@@ -598,26 +626,40 @@ __device__ void give_candidates(const Slice<E>& sl, TopScratch& ts, uint32_t bou
     if (threadIdx.x == 0) remote_st(remote(ts.counts + rank, 0), (uint32_t)found);
 }
 
-// a key that at least n (all, if fewer) of the row's unmasked tokens reach, and not many more: at least n threads'
-// largest do, by halving the range of keys until their number is near n
-__device__ uint32_t bound_of(TopScratch& ts, const LpRow& row, int n, int C)
+// One warp: a key that at least n (all, if fewer) of the row's unmasked tokens reach, and not many more: at least n
+// groups' largest do, by halving the range of keys until their number is near n.  Up to 256 groups, n at most half of
+// them: with n of g groups above it, a bound has g ln(g / (g - n)) tokens above it when they lie at random (n = 128,
+// g = 256: 177).
+__device__ __forceinline__ uint32_t bound_of(const TopScratch& ts, float m, int n, int C)
 {
-    uint32_t lo = row.kmin, hi = key_of(row.m), mid = lo;
-    uint32_t mine[SC_MAXC];
+    uint32_t mine[SC_MAXC], lo = ~0u;
+    int k = 0;
 #pragma unroll
-    for (int i = 0; i < SC_MAXC; ++i) mine[i] = i < C ? ts.keys[i][threadIdx.x] : 0;
-    for (int round = 0;; ++round) {
-        int k = 0;
+    for (int i = 0; i < SC_MAXC; ++i) {
+        mine[i] = i < C ? ts.keys[i][threadIdx.x % 32] : 0;
+        if (mine[i] > KEY_NEG_INF) {
+            lo = min(lo, mine[i]);
+            ++k;
+        }
+    }
+    lo = __reduce_min_sync(~0u, lo);
+    // fewer than n groups have an unmasked token at all: every unmasked token is a candidate
+    if (__reduce_add_sync(~0u, k) < n) return KEY_NEG_INF + 1;
+    uint32_t hi = key_of(m);
+    while (lo < hi) {
+        const uint32_t mid = lo + (hi - lo + 1) / 2;
+        k = 0;
 #pragma unroll
         for (int i = 0; i < SC_MAXC; ++i) k += mine[i] >= mid;
-        k = tally_of(ts, round, k);
-        // fewer than n threads have an unmasked token at all: every unmasked token is a candidate
-        if (round == 0 && k < n) return KEY_NEG_INF + 1;
-        if (k < n) hi = mid - 1;
-        else lo = mid;
-        if (lo >= hi || (k >= n && k <= n + n / 4 + 8)) return lo;
-        mid = lo + (hi - lo + 1) / 2;
+        k = __reduce_add_sync(~0u, k);
+        if (k < n) {
+            hi = mid - 1;
+        } else {
+            lo = mid;
+            if (k <= n + n / 4 + 4) break;
+        }
     }
+    return lo;
 }
 
 // CTA 0: the candidates in order
@@ -674,22 +716,19 @@ template <typename E> __device__ void no_logprobs(const ScoreParams& p, int r, i
     if (p.grad) zero_grad<E>(p, r, rank, C);
 }
 
-template <typename E, bool GRAD> __global__ void __launch_bounds__(SC_NT, 4) k_score_logprobs(const ScoreParams p)
+template <typename E, bool GRAD> __global__ void __launch_bounds__(SC_NT) k_score_logprobs(const ScoreParams p)
 {
     extern __shared__ __align__(16) unsigned char smem[];
-    __shared__ LpPart parts[SC_MAXC];
-    __shared__ float w_m[SC_WARPS], w_s[SC_WARPS], w_t[SC_WARPS];
-    __shared__ int w_a[SC_WARPS];
-    __shared__ uint32_t w_k[SC_WARPS];
+    __shared__ LpPart parts[SC_PARTS];
     __shared__ LpRow s_row;
-    const int C = p.cluster, rank = (int)cluster_rank(), r = blockIdx.x / C, tid = threadIdx.x, lane = tid % 32;
+    const int C = p.cluster, rank = (int)cluster_rank(), r = cluster_id(), tid = threadIdx.x, lane = tid % 32;
     const int id = p.ids ? p.ids[r] : 0;
     if (id < 0 || id >= p.V) {
         no_logprobs<E>(p, r, id == -1 ? SPEC_ROW_OK : SPEC_ROW_BAD_TOKEN, rank, C);
         return;
     }
     const E* x = row_of<E>(p, r);
-    const Slice<E> sl(p, x, rank, C, smem);
+    const Slice<E> sl(p, x, rank, smem);
     TopScratch& ts = *(TopScratch*)(smem + p.top_at);
     sl.copy();
     const E raw = x[id];
@@ -700,14 +739,21 @@ template <typename E, bool GRAD> __global__ void __launch_bounds__(SC_NT, 4) k_s
     int ahead = 0;
     Run run;
     if (p.rank && !GRAD) {
-        const int tvec = (id - sl.first) >> (sizeof(E) == 4 ? 2 : 3);
+        Summer<E, true, true> sum;
+        sum.c2 = pair(p.c, p.c);
+        sum.tvec = (id - sl.first) >> (sizeof(E) == 4 ? 2 : 3);
         // a masked token: those in front are the unmasked ones
-        run = sum_slice<E, true, true>(sl, p.c, 0.f, true, tvec, xt, xt == -INFINITY ? xt : below<E>(raw), ahead);
-        if (tvec >= 0 && tvec < sl.n && tvec % SC_NT == tid && xt > -INFINITY)
-            for (int q = 0; q < id - sl.first - tvec * EPV<E>; ++q)
-                ahead += value_of<E>(bits_at<E>(sl.buf[tvec], q)) == xt;
+        sum.at = Vec<E>::thr_of(xt);
+        sum.under = Vec<E>::thr_of(xt == -INFINITY ? xt : below<E>(raw));
+        run = sum.run(sl, true);
+        ahead = sum.ahead;
+        if (sum.tvec >= 0 && sum.tvec < sl.n && sum.tvec % SC_NT == tid && xt > -INFINITY)
+            for (int q = 0; q < id - sl.first - sum.tvec * EPV<E>; ++q)
+                ahead += value_of<E>(bits_at<E>(sl.buf[sum.tvec], q)) == xt;
     } else {
-        run = sum_slice<E, true, false>(sl, p.c, 0.f, true, 0, 0.f, 0.f, ahead);
+        Summer<E, true, false> sum;
+        sum.c2 = pair(p.c, p.c);
+        run = sum.run(sl, true);
         if (p.rank) {  // with a gradient, where the loop above has no room for it
             each_mine(sl, [&](uint32_t key, int v) {
                 const uint32_t k = key_of(xt);
@@ -715,48 +761,29 @@ template <typename E, bool GRAD> __global__ void __launch_bounds__(SC_NT, 4) k_s
             });
         }
     }
-    const float my_max = run.m;
-    const uint32_t my_key = key_of(my_max);
-    // threads to CTA
-    float m = warp_reduce(run.m, [](float a, float b) { return fmax_nan(a, b); });
-    if (lane == 0) w_m[tid / 32] = m;
-    __syncthreads();
-    m = w_m[0];
-#pragma unroll
-    for (int i = 1; i < SC_WARPS; ++i) m = fmax_nan(m, w_m[i]);
-    to_max(run, m, p.c);
-    run.s = warp_reduce(run.s, [](float a, float b) { return a + b; });
-    run.t = warp_reduce(run.t, [](float a, float b) { return a + b; });
-    ahead = __reduce_add_sync(~0u, ahead);
-    const uint32_t kmin = p.top_n ? __reduce_min_sync(~0u, my_key > KEY_NEG_INF ? my_key : ~0u) : 0;
-    if (lane == 0) {
-        w_s[tid / 32] = run.s;
-        w_t[tid / 32] = run.t;
-        w_a[tid / 32] = ahead;
-        w_k[tid / 32] = kmin;
-    }
-    __syncthreads();
-    // CTA to cluster: to CTA 0, or (what comes next needs the row's sum, or a bound) to all
+    const uint32_t my_key = key_of(run.m);
+    // threads to warp
+    LpPart w;
+    w.m = warp_max(run.m);
+    to_max(run, w.m, p.c);
+    w.s = warp_sum(run.s);
+    w.t = warp_sum(run.t);
+    w.ahead = __reduce_add_sync(~0u, ahead);
+    // warps to cluster: to CTA 0, or (what comes next needs the row's sum, or a bound) to all
     const bool all = GRAD || p.top_n;
     if (C > 1) cluster_wait();
-    if (tid < (all ? C : 1)) {
-        LpPart q = {m, 0.f, 0.f, 0, ~0u};
-#pragma unroll
-        for (int i = 0; i < SC_WARPS; ++i) {
-            q.s += w_s[i];
-            q.t += w_t[i];
-            q.ahead += w_a[i];
-            q.kmin = min(q.kmin, w_k[i]);
-        }
-        const uint32_t to = remote(parts + rank, tid);
-        remote_st(to, __float_as_uint(q.m));
-        remote_st(to + 4, __float_as_uint(q.s));
-        remote_st(to + 8, __float_as_uint(q.t));
-        remote_st(to + 12, (uint32_t)q.ahead);
-        remote_st(to + 16, q.kmin);
+    if (lane < (all ? C : 1)) {
+        const uint32_t to = remote(parts + rank * SC_WARPS + tid / 32, lane);
+        remote_st(to, __float_as_uint(w.m));
+        remote_st(to + 4, __float_as_uint(w.s));
+        remote_st(to + 8, __float_as_uint(w.t));
+        remote_st(to + 12, (uint32_t)w.ahead);
     }
-    if (p.top_n)
-        for (int i = 0; i < C; ++i) remote_st(remote(&ts.keys[rank][tid], i), my_key);
+    if (p.top_n) {
+        uint32_t k = max(my_key, __shfl_xor_sync(~0u, my_key, 1));
+        k = max(k, __shfl_xor_sync(~0u, k, 2));
+        for (int i = lane % 4; i < C; i += 4) remote_st(remote(&ts.keys[rank][tid / 4], i), k);
+    }
     if (C > 1) {
         cluster_arrive();
         if (!all && rank != 0) return;
@@ -765,16 +792,16 @@ template <typename E, bool GRAD> __global__ void __launch_bounds__(SC_NT, 4) k_s
         __syncthreads();
     }
     if (tid < 32) {
-        LpPart q = {-INFINITY, 0.f, 0.f, 0, ~0u};
-        if (lane < C) q = parts[lane];
+        LpPart q = {-INFINITY, 0.f, 0.f, 0};
+        if (lane < C * SC_WARPS) q = parts[lane];
         Run u = {q.m, q.s, q.t};
         LpRow row;
-        row.m = warp_reduce(u.m, [](float a, float b) { return fmax_nan(a, b); });
+        row.m = warp_max(u.m);
         to_max(u, row.m, p.c);
-        row.s = warp_reduce(u.s, [](float a, float b) { return a + b; });
-        row.t = warp_reduce(u.t, [](float a, float b) { return a + b; });
+        row.s = warp_sum(u.s);
+        row.t = warp_sum(u.t);
         row.ahead = __reduce_add_sync(~0u, q.ahead);
-        row.kmin = __reduce_min_sync(~0u, q.kmin);
+        row.bound = p.top_n ? bound_of(ts, row.m, p.top_n, C) : 0;
         if (lane == 0) s_row = row;
     }
     __syncthreads();
@@ -792,7 +819,7 @@ template <typename E, bool GRAD> __global__ void __launch_bounds__(SC_NT, 4) k_s
         if (p.lse) p.lse[r] = row.m * p.inv_temp + logz;
     }
     if (p.top_n) {
-        give_candidates(sl, ts, bound_of(ts, row, p.top_n, C), my_key, p.top_n, rank, C);
+        give_candidates(sl, ts, row.bound, my_key, p.top_n, rank, C);
         if (C > 1) cluster_arrive();
         else __syncthreads();
     }
@@ -802,9 +829,12 @@ template <typename E, bool GRAD> __global__ void __launch_bounds__(SC_NT, 4) k_s
         const float f = p.inv_temp / row.s, A = -(gl + gh * (ent - logz)) * f, B = -gh * LN2 * f;
         const uint64_t A2 = pair(A, A), B2 = pair(B, B);
         E* g = grad_of<E>(p, r);
-        grad_slice(sl, g, row.m, p.c, [&](float a, float z, uint64_t e2) {
-            return mul2(e2, fma2(B2, pair(fmaxf(a, NONE), fmaxf(z, NONE)), A2));
-        });
+        if (p.g_entropy)
+            grad_slice(sl, g, row.m, p.c, [&](float a, float z, uint64_t e2) {
+                return mul2(e2, fma2(B2, pair(fmaxf(a, NONE), fmaxf(z, NONE)), A2));
+            });
+        else
+            grad_slice(sl, g, row.m, p.c, [&](float, float, uint64_t e2) { return mul2(e2, A2); });
         if (p.g_logprob && sl.has(id)) {
             __syncthreads();
             if (tid == 0) {
@@ -813,8 +843,10 @@ template <typename E, bool GRAD> __global__ void __launch_bounds__(SC_NT, 4) k_s
             }
         }
     }
-    if (p.top_n && C > 1 && rank == 0) cluster_wait();
-    if (p.top_n && rank == 0) write_top(p, r, ts, row, logz, C);
+    if (p.top_n && rank == 0) {
+        if (C > 1) cluster_wait();
+        write_top(p, r, ts, row, logz, C);
+    }
 }
 
 // ---- distillation ------------------------------------------------------------ //
@@ -825,8 +857,8 @@ __device__ __forceinline__ float teacher_value(const ScoreParams& p, int64_t at)
                                           : __half2float(((const __half*)p.teacher)[at]);
 }
 
-// the sums of a CTA's slice: tokens without an entry (the rest) and entries, each with its own maximum, as the rest
-// of a confident row may be far below what fp32 holds beside the entries
+// the sums of a warp: tokens without an entry (the rest) and entries, each with its own maximum, as the rest of a
+// confident row may be far below what fp32 holds beside the entries
 struct KdPart {
     float mr, me, sr, se;
 };
@@ -848,77 +880,118 @@ template <typename E> __device__ void no_distill(const ScoreParams& p, int r, in
     if (p.grad) zero_grad<E>(p, r, rank, C);
 }
 
-template <typename E, bool GRAD> __global__ void __launch_bounds__(SC_NT, 4) k_score_distill(const ScoreParams p)
+constexpr int SC_EPT = SPEC_SCORE_MAX_ENTRIES / SC_NT;  // entries of a thread: tid, tid + SC_NT
+
+template <typename E, bool GRAD> __global__ void __launch_bounds__(SC_NT) k_score_distill(const ScoreParams p)
 {
     extern __shared__ __align__(16) unsigned char smem[];
     __shared__ __align__(16) int32_t ids[SPEC_SCORE_MAX_ENTRIES];
     __shared__ float vals[SPEC_SCORE_MAX_ENTRIES];  // CTA 0: the student's logits at the entries
-    __shared__ float sums[SC_MAXC][SC_WARPS];       // CTA 0: the sums of the slices' warps
-    __shared__ KdPart parts[SC_MAXC];
+    __shared__ KdPart parts[SC_PARTS];
     __shared__ KdRow s_row;
-    const int C = p.cluster, rank = (int)cluster_rank(), r = blockIdx.x / C, tid = threadIdx.x, lane = tid % 32;
+    __shared__ float w_max[SC_WARPS], w_sum[SC_WARPS], w_acc[SC_WARPS];
+    __shared__ double w_part[SC_WARPS][3];
+    const int C = p.cluster, rank = (int)cluster_rank(), r = cluster_id(), tid = threadIdx.x, lane = tid % 32;
     const int k = p.k;
-    const int64_t at = (int64_t)r * k + tid;
-    const int id = tid < k ? p.ids[at] : -1;
-    if (!__syncthreads_or(id != -1)) {
+    int id[SC_EPT];
+    bool some = false;
+#pragma unroll
+    for (int u = 0; u < SC_EPT; ++u) {
+        const int i = tid + u * SC_NT;
+        ids[i] = id[u] = i < k ? p.ids[(int64_t)r * k + i] : -1;
+        some |= id[u] != -1;
+    }
+    if (!__syncthreads_or(some)) {
         no_distill<E>(p, r, SPEC_ROW_OK, rank, C);
         return;
     }
-    const Slice<E> sl(p, row_of<E>(p, r), rank, C, smem);
+    const Slice<E> sl(p, row_of<E>(p, r), rank, smem);
     sl.copy();
     // the teacher, while the row is on its way: ln q_i = y_i - nq
-    ids[tid] = id;
-    const float tv = id >= 0 ? teacher_value(p, at) : -INFINITY, lse = p.teacher_lse ? p.teacher_lse[r] : 0.f;
-    const float tmax = block_max(tv);
-    bool bad = id < -1 || id >= p.V;
-    if (id >= 0)
-        for (int j = 0; j < tid; j += 4) {
+    const float lse = p.teacher_lse ? p.teacher_lse[r] : 0.f;
+    float tv[SC_EPT], tmax = -INFINITY;
+    bool bad = false;
+#pragma unroll
+    for (int u = 0; u < SC_EPT; ++u) {
+        const int i = tid + u * SC_NT;
+        tv[u] = -INFINITY;
+        if (id[u] == -1) continue;
+        bad |= id[u] < -1 || id[u] >= p.V;
+        tv[u] = teacher_value(p, (int64_t)r * k + i);
+        tmax = fmax_nan(tmax, tv[u]);
+        for (int j = 0; j < i; j += 4) {
             const int4 o = *(const int4*)(ids + j);
-            bad |= o.x == id || (o.y == id && j + 1 < tid) || (o.z == id && j + 2 < tid) || (o.w == id && j + 3 < tid);
+            bad |= o.x == id[u] || (o.y == id[u] && j + 1 < i) || (o.z == id[u] && j + 2 < i) ||
+                   (o.w == id[u] && j + 3 < i);
         }
+    }
+    tmax = warp_max(tmax);
+    if (lane == 0) w_max[tid / 32] = tmax;
     bad = __syncthreads_or(bad);
-    const bool dull = !(tmax < INFINITY) || (!p.tail && tmax == -INFINITY) || !(fabsf(lse) < INFINITY);
-    if (bad || dull) {
-        sl.arrived_all();
+#pragma unroll
+    for (int i = 0; i < SC_WARPS; ++i) tmax = fmax_nan(tmax, w_max[i]);
+    if (bad || !(tmax < INFINITY) || (!p.tail && tmax == -INFINITY) || !(fabsf(lse) < INFINITY)) {
+        sl.arrived(0);
         no_distill<E>(p, r, bad ? SPEC_ROW_BAD_TOKEN : SPEC_ROW_NONFINITE, rank, C);
         return;
     }
     if (C > 1) cluster_arrive();  // every CTA of the cluster runs before another stores into its shared memory
-    // ln q up to the row's sum: differences first, and 1 / t in two parts, as the values may be large
-    float w = 0.f;
-    if (tv > -INFINITY)
-        w = expf(p.tail ? fmaf(tv, p.inv_tt_lo, fmaf(tv, p.inv_tt, -lse))
-                        : fmaf(tv - tmax, p.inv_tt_lo, (tv - tmax) * p.inv_tt));
-    const float sum = block_sum(w);
-    const float q = p.tail ? w : w / sum, in_q = p.tail ? sum : 1.f, qr = p.tail ? fmaxf(0.f, 1.f - sum) : 0.f;
+    // q up to the row's sum: differences first, and 1 / t in two parts, as the values may be large
+    float q[SC_EPT], sum = 0.f;
+#pragma unroll
+    for (int u = 0; u < SC_EPT; ++u) {
+        q[u] = 0.f;
+        if (tv[u] > -INFINITY)
+            q[u] = expf(p.tail ? fmaf(tv[u], p.inv_tt_lo, fmaf(tv[u], p.inv_tt, -lse))
+                               : fmaf(tv[u] - tmax, p.inv_tt_lo, (tv[u] - tmax) * p.inv_tt));
+        sum += q[u];
+    }
+    sum = warp_sum(sum);
+    if (lane == 0) w_sum[tid / 32] = sum;
     // the entries' logits leave the row
-    sl.arrived_all();
+    sl.arrived(0);
     __syncthreads();
-    const bool mine = id >= 0 && sl.has(id);
-    float l = -INFINITY;
-    if (mine) {
-        l = value_of<E>(*sl.at(id));
-        *sl.at(id) = (Bits<E>)Vec<E>::NEG;
+    sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < SC_WARPS; ++i) sum += w_sum[i];
+    float l[SC_EPT], me = -INFINITY;
+    bool mine[SC_EPT];
+#pragma unroll
+    for (int u = 0; u < SC_EPT; ++u) {
+        mine[u] = id[u] >= 0 && sl.has(id[u]);
+        l[u] = -INFINITY;
+        if (mine[u]) {
+            l[u] = value_of<E>(*sl.at(id[u]));
+            *sl.at(id[u]) = (Bits<E>)Vec<E>::NEG;
+        }
+        me = fmax_nan(me, l[u]);
+        if (!p.tail) q[u] /= sum;
     }
     __syncthreads();
-    int none = 0;
-    Run run = sum_slice<E, false, false>(sl, p.c, p.c_lo, false, 0, 0.f, 0.f, none);
-    const float mr = block_max(run.m), me = block_max(l);
-    to_max(run, mr, p.c);
-    // (a warp's sum goes to CTA 0 as it is: there the loss takes them in 64 bits)
-    const float sw = warp_reduce(run.s, [](float a, float b) { return a + b; });
-    const float sr = block_sum(lane == 0 ? sw : 0.f);
-    const float se = block_sum(ex2_fast((l - ref_of(me)) * p.c));
+    Summer<E, false, false> rest;
+    rest.c2 = pair(p.c, p.c);
+    rest.l2 = pair(p.c_lo, p.c_lo);
+    Run run = rest.run(sl, false);
+    KdPart w;
+    w.mr = warp_max(run.m);
+    to_max(run, w.mr, p.c);
+    w.sr = warp_sum(run.s);
+    w.me = warp_max(me);
+    w.se = 0.f;
+#pragma unroll
+    for (int u = 0; u < SC_EPT; ++u) w.se += ex2_fast((l[u] - ref_of(w.me)) * p.c);
+    w.se = warp_sum(w.se);
     if (C > 1) cluster_wait();
-    if (tid < (GRAD ? C : 1)) {
-        const uint32_t to = remote(parts + rank, tid);
-        remote_st(to, __float_as_uint(mr));
-        remote_st(to + 4, __float_as_uint(me));
-        remote_st(to + 8, __float_as_uint(sr));
-        remote_st(to + 12, __float_as_uint(se));
+    if (lane < (GRAD ? C : 1)) {
+        const uint32_t to = remote(parts + rank * SC_WARPS + tid / 32, lane);
+        remote_st(to, __float_as_uint(w.mr));
+        remote_st(to + 4, __float_as_uint(w.me));
+        remote_st(to + 8, __float_as_uint(w.sr));
+        remote_st(to + 12, __float_as_uint(w.se));
     }
-    if (mine) remote_st(remote(vals + tid, 0), __float_as_uint(l));
-    if (lane == 0) remote_st(remote(&sums[rank][tid / 32], 0), __float_as_uint(sw));
+#pragma unroll
+    for (int u = 0; u < SC_EPT; ++u)
+        if (mine[u]) remote_st(remote(vals + tid + u * SC_NT, 0), __float_as_uint(l[u]));
     if (C > 1) {
         cluster_arrive();
         if (!GRAD && rank != 0) return;
@@ -928,15 +1001,12 @@ template <typename E, bool GRAD> __global__ void __launch_bounds__(SC_NT, 4) k_s
     }
     if (tid < 32) {
         KdPart u = {-INFINITY, -INFINITY, 0.f, 0.f};
-        if (lane < C) u = parts[lane];
-        auto max_of = [](float a, float b) { return fmax_nan(a, b); };
-        auto sum_of = [](float a, float b) { return a + b; };
+        if (lane < C * SC_WARPS) u = parts[lane];
         KdRow row;
-        row.mr = warp_reduce(u.mr, max_of);
-        const float e = warp_reduce(u.me, max_of);
-        row.m = fmax_nan(row.mr, e);
-        row.sr = warp_reduce(u.mr == -INFINITY ? 0.f : u.sr * exp2f((u.mr - row.mr) * p.c), sum_of);
-        const float in_e = warp_reduce(u.me == -INFINITY ? 0.f : u.se * exp2f((u.me - row.m) * p.c), sum_of);
+        row.mr = warp_max(u.mr);
+        row.m = fmax_nan(row.mr, warp_max(u.me));
+        row.sr = warp_sum(u.mr == -INFINITY ? 0.f : u.sr * exp2f((u.mr - row.mr) * p.c));
+        const float in_e = warp_sum(u.me == -INFINITY ? 0.f : u.se * exp2f((u.me - row.m) * p.c));
         row.scale = row.mr == -INFINITY ? 0.f : exp2f((row.mr - row.m) * p.c);
         row.z = row.sr * row.scale + in_e;
         row.inv_z = 1.f / row.z;
@@ -950,83 +1020,92 @@ template <typename E, bool GRAD> __global__ void __launch_bounds__(SC_NT, 4) k_s
         return;
     }
     if (GRAD) {
+        const float in_q = p.tail ? sum : 1.f, qr = p.tail ? fmaxf(0.f, 1.f - sum) : 0.f;
         const float gl = (p.g_loss ? p.g_loss[r] : 1.f) * p.inv_temp, ps = (in_q + qr) * row.inv_z;
         const float pr = gl * (ps * row.scale - qr * row.inv_sr);
         const uint64_t pr2 = pair(pr, pr);
         E* g = grad_of<E>(p, r);
         grad_slice(sl, g, row.mr, p.c, [&](float, float, uint64_t e2) { return mul2(e2, pr2); });
         __syncthreads();
-        if (mine) g[id] = narrow<E>(gl * (ps * ex2_fast((l - row.m) * p.c) - q));
+#pragma unroll
+        for (int u = 0; u < SC_EPT; ++u)
+            if (mine[u]) g[id[u]] = narrow<E>(gl * (ps * ex2_fast((l[u] - row.m) * p.c) - q[u]));
     }
     if (rank != 0) return;
     // The row's loss: near its minimum a small difference of terms of the size of ln Z, which are taken in 64 bits.
     // That pipe takes 16 cycles for a warp's instruction: the entries' warps alone use it, and exponentials and
     // logarithms are one each, of different values in a warp's lanes.
-    __shared__ double w_part[SC_WARPS][3];
-    auto sum_of = [](double a, double b) { return a + b; };
-    const float li = id >= 0 ? vals[tid] : -INFINITY;
-    const float e = exp2f(fmaf(li - row.m, p.c, (li - row.m) * p.c_lo));
-    if (tid < (k + 31) / 32 * 32) {
-        const double lq = p.tail ? (double)tv * p.inv_tt_d - (double)lse : ((double)tv - (double)tmax) * p.inv_tt_d;
-        const double part =
-            warp_reduce(q > 0.f ? q * (lq - ((double)li - (double)row.m) * p.inv_temp_d) : 0.0, sum_of);
-        const double in_q = warp_reduce((double)q, sum_of), in_e = warp_reduce((double)e, sum_of);
-        if (lane == 0) {
-            w_part[tid / 32][0] = part;
-            w_part[tid / 32][1] = in_q;
-            w_part[tid / 32][2] = in_e;
-        }
+    float acc = 0.f;
+    double part = 0.0, in_q = 0.0, in_e = 0.0;
+#pragma unroll
+    for (int u = 0; u < SC_EPT; ++u) {
+        if (tid / 32 * 32 + u * SC_NT >= k) continue;
+        const float li = id[u] >= 0 ? vals[tid + u * SC_NT] : -INFINITY;
+        const float e = exp2f(fmaf(li - row.m, p.c, (li - row.m) * p.c_lo));
+        const double lq = p.tail ? (double)tv[u] * p.inv_tt_d - (double)lse : ((double)tv[u] - (double)tmax) * p.inv_tt_d;
+        if (q[u] > 0.f) part += q[u] * (lq - ((double)li - (double)row.m) * p.inv_temp_d);
+        in_q += q[u];
+        in_e += e;
+        acc += fminf(q[u], e * row.inv_z);
     }
-    const float acc = block_sum(fminf(q, e * row.inv_z));  // (its barriers are w_part's)
+    acc = warp_sum(acc);
+    if (tid / 32 * 32 < k) {
+        part = warp_sum(part);
+        in_q = warp_sum(in_q);
+        in_e = warp_sum(in_e);
+    }
+    if (lane == 0) {
+        w_acc[tid / 32] = acc;
+        w_part[tid / 32][0] = part;
+        w_part[tid / 32][1] = in_q;
+        w_part[tid / 32][2] = in_e;
+    }
+    __syncthreads();
     if (tid >= 32) return;
-    // lane i: CTA i's share of the rest; lane SC_MAXC: the rest's of the row
-    const float from = lane < C ? parts[lane].mr : row.mr;
-    const double scale = exp(((double)from - (double)(lane < SC_MAXC ? row.mr : row.m)) * p.inv_temp_d);
-    double rest = 0.0;
-    if (lane < C && from > -INFINITY) {
-        for (int i = 0; i < SC_WARPS; ++i) rest += sums[lane][i];
-        rest *= scale;
-    }
-    for (int i = 1; i < SC_MAXC; i *= 2) rest += __shfl_xor_sync(~0u, rest, i);
-    rest = __shfl_sync(~0u, rest, 0);
-    double loss = 0.0, in = 0.0, z = rest > 0.0 ? rest * __shfl_sync(~0u, scale, SC_MAXC) : 0.0;
-    for (int i = 0; i < (k + 31) / 32; ++i) {
+    // lane i: the share that warp i's sum of the rest has
+    const KdPart u = lane < C * SC_WARPS ? parts[lane] : KdPart{-INFINITY, -INFINITY, 0.f, 0.f};
+    double in_r = 0.0;
+    if (u.mr > -INFINITY) in_r = u.sr * exp(((double)u.mr - (double)row.mr) * p.inv_temp_d);
+    in_r = warp_sum(in_r);
+    const double shift = in_r > 0.0 ? ((double)row.mr - (double)row.m) * p.inv_temp_d : 0.0;
+    double loss = 0.0, in = 0.0, z = in_r > 0.0 ? in_r * exp(shift) : 0.0;
+    for (int i = 0; i < SC_WARPS; ++i) {
         loss += w_part[i][0];
         in += w_part[i][1];
         z += w_part[i][2];
     }
     const double left = p.tail ? fmax(0.0, 1.0 - in) : 0.0;
-    const double ln = log(lane == 0 ? z : lane == 1 ? rest : lane == 2 ? left : (double)sum);
-    const double ln_rest = __shfl_sync(~0u, ln, 1), ln_left = __shfl_sync(~0u, ln, 2), ln_sum = __shfl_sync(~0u, ln, 3);
+    const double ln = log(lane == 0 ? z : lane == 1 ? in_r : lane == 2 ? left : (double)sum);
+    const double ln_r = __shfl_sync(~0u, ln, 1), ln_left = __shfl_sync(~0u, ln, 2), ln_sum = __shfl_sync(~0u, ln, 3);
     if (lane == 0) {
         loss += in * (p.tail ? ln : ln - ln_sum);
-        if (left > 0.0)
-            loss += rest > 0.0 ? left * (ln_left + ln - ln_rest - ((double)row.mr - (double)row.m) * p.inv_temp_d)
-                               : (double)INFINITY;
+        if (left > 0.0) loss += in_r > 0.0 ? left * (ln_left + ln - ln_r - shift) : (double)INFINITY;
         p.row_status[r] = SPEC_ROW_OK;
         if (p.loss) p.loss[r] = (float)loss;
-        if (p.accept) p.accept[r] = acc;
+        if (p.accept) p.accept[r] = w_acc[0] + w_acc[1] + w_acc[2] + w_acc[3];
     }
 }
 
 // ---- launches ------------------------------------------------------------------ //
 // CTAs of a row.  A slice of at most SLICE bytes leaves room for four CTAs on an SM, so that some copy while others
 // compute; rows beyond eight of them have larger slices.  Few rows are spread over up to eight CTAs, for the SMs
-// that would idle, while a thread still has a vector to itself.
-constexpr int SLICE = 52 * 1024, SLICE_TOP = 39 * 1024;
+// that would idle, while every thread still has a vector or two; and the search for the top tokens wants twice as
+// many groups of threads (32 a CTA) as tokens.
+constexpr int SLICE = 52 * 1024, SLICE_TOP = 46 * 1024;
 
 template <typename K>
 cudaError_t go(K kernel, DeviceOnce& once, ScoreParams p, size_t size, size_t scratch, int num_sms, cudaStream_t s)
 {
     const size_t limit = SCORE_MAX_ROW_BYTES / SC_MAXC + 64 + scratch;
-    const size_t row = (size_t)p.V * size + 16;
-    const int most = p.top_n ? SLICE_TOP : SLICE;
-    int C = (int)((row + most - 1) / most);
+    const int row = (int)(((size_t)p.V * size + 30) / 16);  // vectors, at any alignment
+    const int most = (p.top_n ? SLICE_TOP : SLICE) / 16;
+    int C = (row + most - 1) / most;
     C = C > SC_MAXC ? SC_MAXC : C;
-    while (C < SC_MAXC && (int64_t)p.rows * C < num_sms && row / (C + 1) >= SC_NT * 16) ++C;
-    const size_t per = ((row + 15) / 16 + C - 1) / C;
+    while (C < SC_MAXC && (C * 16 < p.top_n || ((int64_t)p.rows * C < num_sms && row / (C + 1) >= SC_NT))) ++C;
     p.cluster = C;
-    p.top_at = (int)(per * 16);
+    p.per = (row + C - 1) / C;
+    p.top_at = p.per * 16;
+    p.by_tokens = FastDiv(p.T);
     const cudaError_t e = cuda_once(once, nullptr, [&](int, int*) {
         return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)limit);
     });
@@ -1034,7 +1113,7 @@ cudaError_t go(K kernel, DeviceOnce& once, ScoreParams p, size_t size, size_t sc
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)p.rows * C);
     cfg.blockDim = dim3(SC_NT);
-    cfg.dynamicSmemBytes = per * 16 + (p.top_n ? scratch : 0);
+    cfg.dynamicSmemBytes = (size_t)p.per * 16 + (p.top_n ? scratch : 0);
     cfg.stream = s;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeClusterDimension;

@@ -12,6 +12,18 @@
 
 namespace sv {
 
+// n / d for 0 <= n < 2^28, by a product (Granlund and Montgomery's division by an invariant)
+struct FastDiv {
+    uint32_t mul = 0, shift = 0;
+    FastDiv() = default;
+    explicit FastDiv(uint32_t d)
+    {
+        while (((uint64_t)1 << shift) < d) ++shift;
+        mul = (uint32_t)((((uint64_t)1 << 32) * (((uint64_t)1 << shift) - d)) / d + 1);
+    }
+    __device__ __forceinline__ int of(int n) const { return (int)((__umulhi((uint32_t)n, mul) + (uint32_t)n) >> shift); }
+};
+
 struct ScoreParams {
     const char* x;           // logits
     int64_t x_seq, x_tok;    // strides, elements
@@ -20,8 +32,11 @@ struct ScoreParams {
     int32_t rows, T, V;
     float inv_temp, c, c_lo; // 1 / temperature, log2(e) / it from below, and what is left of that (> 0)
     double inv_temp_d;
-    int32_t cluster;         // CTAs of a row (the launch fills it in)
-    int32_t top_at;          // offset of the search's scratch in shared memory (the launch)
+    // what the launch fills in
+    FastDiv by_tokens;       // of a row: its sequence
+    int32_t cluster;         // CTAs of a row
+    int32_t per;             // vectors of 16 bytes of a CTA
+    int32_t top_at;          // offset of the search's scratch in shared memory
     int32_t* row_status;
     const int32_t* ids;      // logprobs: [rows] or NULL; distill: [rows, k]
     // logprobs
@@ -49,6 +64,7 @@ struct ScoreParams {
 cudaError_t launch_score_logprobs(const ScoreParams& p, int dtype, int num_sms, cudaStream_t s);
 cudaError_t launch_score_distill(const ScoreParams& p, int dtype, int num_sms, cudaStream_t s);
 
-constexpr size_t SCORE_MAX_ROW_BYTES = 8 * 208 * 1024;  // of one row of logits
+constexpr int SCORE_MAX_CTAS = 8;                                    // of a row
+constexpr size_t SCORE_MAX_ROW_BYTES = SCORE_MAX_CTAS * 208 * 1024;  // of one row of logits
 
 }  // namespace sv
