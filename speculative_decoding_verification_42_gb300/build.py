@@ -17,7 +17,8 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libspec_verify.so")
 BUILD_DIR = os.path.join(HERE, "_build")
 SOURCES = ["sv_rows.cu", "sv_sample.cu", "sv_api.cu", "sv_noalloc.cu", "sv_lmhead.cu",
-           "sv_tree_api.cu", "sv_tree_rows.cu", "sv_tree_attend.cu", "sv_score_api.cu", "sv_score.cu"]
+           "sv_tree_api.cu", "sv_tree_rows.cu", "sv_tree_attend.cu", "sv_score_api.cu",
+           "sv_score_logprobs.cu", "sv_score_distill.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE,
               "-Xptxas", "-warn-spills"]

@@ -30,13 +30,11 @@ struct ScoreParams {
     char* grad;              // gradient rows or NULL
     int64_t g_seq, g_tok;
     int32_t rows, T, V;
-    float inv_temp, c, c_lo; // 1 / temperature, log2(e) / it from below, and what is left of that (> 0)
-    double inv_temp_d;
+    float inv_temp, c;       // 1 / temperature, log2(e) / it
     // what the launch fills in
     FastDiv by_tokens;       // of a row: its sequence
     int32_t cluster;         // CTAs of a row
     int32_t per;             // vectors of 16 bytes of a CTA
-    int32_t top_at;          // offset of the search's scratch in shared memory
     int32_t* row_status;
     const int32_t* ids;      // logprobs: [rows] or NULL; distill: [rows, k]
     // logprobs
@@ -54,7 +52,6 @@ struct ScoreParams {
     int32_t teacher_dtype;
     int32_t k, tail;
     float inv_tt, inv_tt_lo; // 1 / the teacher's temperature, and what is left of it
-    double inv_tt_d;
     const float* teacher_lse;
     const float* g_loss;
     float* loss;
@@ -65,6 +62,7 @@ cudaError_t launch_score_logprobs(const ScoreParams& p, int dtype, int num_sms, 
 cudaError_t launch_score_distill(const ScoreParams& p, int dtype, int num_sms, cudaStream_t s);
 
 constexpr int SCORE_MAX_CTAS = 8;                                    // of a row
+constexpr int SCORE_SLICE = 52 * 1024;                               // bytes of a CTA
 constexpr size_t SCORE_MAX_ROW_BYTES = SCORE_MAX_CTAS * 208 * 1024;  // of one row of logits
 
 }  // namespace sv

@@ -72,11 +72,7 @@ ScoreParams rows_of(int32_t batch, int32_t tokens, int32_t vocab, float temp, co
     p.T = tokens;
     p.V = vocab;
     p.inv_temp = 1.f / temp;
-    p.inv_temp_d = 1.0 / (double)temp;
-    const double c = 1.4426950408889634 / (double)temp;
-    p.c = (float)c;
-    if ((double)p.c >= c) p.c = nextafterf(p.c, 0.f);
-    p.c_lo = fmaxf((float)(c - (double)p.c), 1.17549435e-38f);
+    p.c = (float)(1.4426950408889634 / (double)temp);
     p.row_status = row_status;
     return p;
 }
@@ -143,9 +139,9 @@ spec_status spec_score_distill(const spec_score_distill_args* a, void* stream)
     p.tail = a->tail ? 1 : 0;
     p.teacher = a->teacher;
     p.teacher_dtype = a->teacher_dtype;
-    p.inv_tt_d = 1.0 / (double)a->teacher_temperature;
-    p.inv_tt = (float)p.inv_tt_d;
-    p.inv_tt_lo = (float)(p.inv_tt_d - (double)p.inv_tt);
+    const double inv_tt = 1.0 / (double)a->teacher_temperature;
+    p.inv_tt = (float)inv_tt;
+    p.inv_tt_lo = (float)(inv_tt - (double)p.inv_tt);
     p.teacher_lse = a->teacher_lse;
     p.g_loss = a->grad_loss;
     p.loss = a->loss;

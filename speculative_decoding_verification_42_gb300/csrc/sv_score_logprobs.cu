@@ -1,0 +1,564 @@
+// sv_score_logprobs.cu -- log probabilities of given tokens with rank, entropy
+// and top alternatives, and the gradient of log probability and entropy.
+#include "sv_score_row.cuh"
+
+namespace sv {
+
+namespace {
+
+constexpr int SC_LIST = 1024;   // candidates for the top tokens, all CTAs of a row together
+constexpr uint32_t KEY_NEG_INF = 0x007FFFFFu;  // key_of(-inf)
+
+struct LpPart {      // what a warp knows of the row
+    float m, s, t;
+    int32_t ahead;
+};
+struct LpRow {
+    float m, s, t;
+    int32_t ahead;
+    uint32_t bound;  // a key that the top tokens reach, and not many others
+};
+
+// The search for the top tokens.  A bound first: the row's CTAs exchange 512 largest keys, of groups of a thread's
+// vectors, and take one that at least n of them reach and not many more, by halving the range of keys.  With n of g
+// groups above it, a bound has g ln(g / (g - n)) tokens above it when they lie at random (n = 128: 147).  Then the copy
+// groups whose largest element reaches the bound are read once more, and what reaches it in them are the candidates,
+// which CTA 0 puts in order.
+constexpr int SC_GROUPS = 512;
+constexpr int SC_AGAIN = 512;       // copy groups of a CTA that are read again
+struct TopScratch {
+    unsigned long long list[SC_LIST];  // CTA 0: candidates, key and inverted id, SC_LIST / C to a CTA
+    uint32_t keys[SC_GROUPS];
+    uint32_t again[SC_AGAIN];          // copy group * SC_NT + thread
+    int32_t counts[SC_MAXC];           // CTA 0: candidates of each CTA
+    int32_t mine, agains;              // candidates of this CTA, entries of `again`
+    int32_t tally[2][SC_WARPS];
+    float most[1];                     // [full + 1][SC_NT]: the largest element of each thread's copy groups
+};
+
+__device__ __forceinline__ int tally_of(TopScratch& ts, int round, int x)
+{
+    // one barrier a round: the other buffer is free again when it is passed
+    x = __reduce_add_sync(~0u, x);
+    if (threadIdx.x % 32 == 0) ts.tally[round & 1][threadIdx.x / 32] = x;
+    __syncthreads();
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < SC_WARPS; ++i) n += ts.tally[round & 1][i];
+    return n;
+}
+
+template <typename E, typename F> __device__ __forceinline__ void each_of(const uint4& w, int e, F f)
+{
+#pragma unroll
+    for (int q = 0; q < EPV<E>; ++q) f(key_of(value_of<E>(bits_at<E>(w, q))), e + q);
+}
+
+// The candidates of a CTA, whose keys reach `bound`, into the list of CTA 0.  When they are too many for its share of
+// the list (equal logits), its first n in the order (key desc, id asc), found by halving the range of keys and of ids
+// and counting.
+template <typename E>
+__device__ void give_candidates(const Slice<E>& sl, int V, int full, TopScratch& ts, uint32_t bound, int n, int rank, int C)
+{
+    const int share = SC_LIST / C, tid = threadIdx.x;
+    const uint32_t list = remote(ts.list + rank * share, 0);
+    auto give = [&](uint32_t key, int id) {
+        const int at = atomicAdd(&ts.mine, 1);
+        if (at < share) {
+            remote_st(list + at * 8, ~(uint32_t)id);
+            remote_st(list + at * 8 + 4, key);
+        }
+    };
+    const float least = val_of(bound);
+    for (int b = 0; b <= full; ++b)
+        if (ts.most[b * SC_NT + tid] >= least) {
+            const int at = atomicAdd(&ts.agains, 1);
+            if (at < SC_AGAIN) ts.again[at] = b * SC_NT + tid;
+        }
+    __syncthreads();
+    const int agains = ts.agains;
+    if (agains <= SC_AGAIN) {
+        for (int a = tid; a < agains; a += SC_NT) {
+            const int g = ts.again[a] / SC_NT, owner = ts.again[a] % SC_NT;
+            uint4 w[SC_GROUP + 1];
+            int at[SC_GROUP + 1];
+#pragma unroll
+            for (int j = 0; j < SC_GROUP; ++j) {
+                at[j] = (g * SC_GROUP + j) * SC_NT + owner;
+                w[j] = at[j] >= sl.lo && at[j] < sl.hi ? load_vector(sl, V, at[j]) : no_vector<E>();
+            }
+            // the row's ends count to the last group of threads 0 and 32
+            const bool first = owner == 0 && sl.lo && sl.n, last = owner == 32 && sl.hi < sl.n;
+            at[SC_GROUP] = first ? 0 : sl.n - 1;
+            w[SC_GROUP] = g == full && (first || last) ? load_vector(sl, V, at[SC_GROUP]) : no_vector<E>();
+#pragma unroll
+            for (int j = 0; j <= SC_GROUP; ++j)
+                if (Vec<E>::top(w[j]) >= least)
+                    each_of<E>(w[j], sl.first + at[j] * EPV<E>, [&](uint32_t key, int id) {
+                        if (key >= bound) give(key, id);
+                    });
+        }
+    }
+    __syncthreads();
+    int found = ts.mine;
+    if (found > share || agains > SC_AGAIN) {
+        __syncthreads();
+        if (tid == 0) ts.mine = 0;
+        auto number = [&](int round, auto pred) {
+            int k = 0;
+            for (int i = tid; i < sl.n; i += SC_NT)
+                each_of<E>(load_vector(sl, V, i), sl.first + i * EPV<E>, [&](uint32_t key, int id) { k += pred(key, id); });
+            return tally_of(ts, round, k);
+        };
+        int round = 0;
+        const int all = number(round++, [&](uint32_t key, int) { return key >= bound; });
+        found = min(n, all);
+        uint32_t lo = bound, hi = 0xFF800000u;
+        while (lo < hi) {  // the last of them
+            const uint32_t mid = lo + (hi - lo + 1) / 2;
+            if (number(round++, [&](uint32_t key, int) { return key >= mid; }) >= found) lo = mid;
+            else hi = mid - 1;
+        }
+        const int ties = found - number(round++, [&](uint32_t key, int) { return key > lo; });
+        int first = sl.first, last = sl.first + sl.n * EPV<E> - 1;  // the last id among its equals
+        while (first < last) {
+            const int mid = first + (last - first) / 2;
+            if (number(round++, [&](uint32_t key, int id) { return key == lo && id <= mid; }) >= ties) last = mid;
+            else first = mid + 1;
+        }
+        if (found > 0)
+            for (int i = tid; i < sl.n; i += SC_NT)
+                each_of<E>(load_vector(sl, V, i), sl.first + i * EPV<E>, [&](uint32_t key, int id) {
+                    if (key > lo || (key == lo && id <= last)) give(key, id);
+                });
+    }
+    if (tid == 0) remote_st(remote(ts.counts + rank, 0), (uint32_t)found);
+}
+
+// the keys of this thread's vectors, 512 / C from a CTA, to all CTAs
+__device__ __forceinline__ void give_keys(TopScratch& ts, int full, int rank, int C)
+{
+    const int tid = threadIdx.x, parts = max(1, 4 / C);
+    for (int q = 0; q < parts; ++q) {
+        float m = -INFINITY;
+        for (int b = q * (full + 1) / parts; b < (q + 1) * (full + 1) / parts; ++b) m = fmaxf(m, ts.most[b * SC_NT + tid]);
+        uint32_t k = key_of(m);
+        int at = (rank * parts + q) * SC_NT + tid;
+        if (C == 8) {
+            k = max(k, __shfl_xor_sync(~0u, k, 1));
+            at = (rank * SC_NT + tid) / 2;
+            for (int i = tid % 2; i < C; i += 2) remote_st(remote(ts.keys + at, i), k);
+        } else {
+            for (int i = 0; i < C; ++i) remote_st(remote(ts.keys + at, i), k);
+        }
+    }
+}
+__device__ __forceinline__ uint32_t bound_of(const TopScratch& ts, int n)
+{
+    uint32_t mine[SC_GROUPS / 32], lo = ~0u, hi = 0;
+    int k = 0;
+#pragma unroll
+    for (int i = 0; i < SC_GROUPS / 32; ++i) {
+        mine[i] = ts.keys[i * 32 + threadIdx.x % 32];
+        hi = max(hi, mine[i]);
+        if (mine[i] > KEY_NEG_INF) {
+            lo = min(lo, mine[i]);
+            ++k;
+        }
+    }
+    lo = __reduce_min_sync(~0u, lo);
+    // fewer than n groups have an unmasked token at all: every unmasked token is a candidate
+    if (__reduce_add_sync(~0u, k) < n) return KEY_NEG_INF + 1;
+    hi = __reduce_max_sync(~0u, hi);
+    while (lo < hi) {
+        const uint32_t mid = lo + (hi - lo + 1) / 2;
+        k = 0;
+#pragma unroll
+        for (int i = 0; i < SC_GROUPS / 32; ++i) k += mine[i] >= mid;
+        k = __reduce_add_sync(~0u, k);
+        if (k < n) {
+            hi = mid - 1;
+        } else {
+            lo = mid;
+            if (k <= n + n / 4 + 4) break;
+        }
+    }
+    return lo;
+}
+
+// CTA 0: the candidates in order
+__device__ void write_top(const ScoreParams& p, int r, TopScratch& ts, const LpRow& row, float logz, int C)
+{
+    const int share = SC_LIST / C;
+    int before[SC_MAXC + 1];
+    before[0] = 0;
+#pragma unroll
+    for (int i = 0; i < SC_MAXC; ++i) before[i + 1] = before[i] + (i < C ? ts.counts[i] : 0);
+    const int all = before[SC_MAXC], n = min(all, p.top_n);
+    int32_t* ids = p.top_ids + (int64_t)r * p.top_n;
+    float* lps = p.top_lp + (int64_t)r * p.top_n;
+    for (int i = threadIdx.x; i < all; i += SC_NT) {
+        int part = 0, base = 0;
+#pragma unroll
+        for (int j = 1; j < SC_MAXC; ++j)
+            if (j < C && i >= before[j]) part = j, base = before[j];
+        const unsigned long long mine = ts.list[part * share + i - base];
+        int at = 0;
+        for (int j = 0; j < C; ++j) {
+            const unsigned long long* l = ts.list + j * share;
+            const int k = ts.counts[j];
+            for (int q = 0; q < k; ++q) at += l[q] > mine;
+        }
+        if (at < n) {
+            ids[at] = (int32_t)~(uint32_t)mine;
+            lps[at] = (val_of((uint32_t)(mine >> 32)) - row.m) * p.inv_temp - logz;
+        }
+    }
+    for (int i = n + threadIdx.x; i < p.top_n; i += SC_NT) {
+        ids[i] = -1;
+        lps[i] = -INFINITY;
+    }
+}
+
+__device__ __forceinline__ void no_top(const ScoreParams& p, int r, int status)
+{
+    for (int i = threadIdx.x; i < p.top_n; i += SC_NT) {
+        p.top_ids[(int64_t)r * p.top_n + i] = -1;
+        p.top_lp[(int64_t)r * p.top_n + i] = status == SPEC_ROW_OK ? -INFINITY : __int_as_float(0x7FFFFFFF);
+    }
+}
+
+// a row that is not scored, or has a bad token
+template <typename E> __device__ void no_logprobs(const ScoreParams& p, int r, int status, int rank, int C)
+{
+    if (rank == 0) {
+        const float none = status == SPEC_ROW_OK ? 0.f : __int_as_float(0x7FFFFFFF);
+        if (threadIdx.x == 0) {
+            p.row_status[r] = status;
+            if (p.logprob) p.logprob[r] = none;
+            if (p.rank) p.rank[r] = -1;
+            if (p.entropy) p.entropy[r] = none;
+            if (p.lse) p.lse[r] = none;
+        }
+        no_top(p, r, status);
+    }
+    if (p.grad) zero_grad<E>(p, r, rank, C);
+}
+
+// one warp: the row of its warps' parts
+__device__ __forceinline__ LpRow join(const LpPart* parts, float c, int C)
+{
+    const int lane = threadIdx.x % 32;
+    LpPart q = {-INFINITY, 0.f, 0.f, 0};
+    if (lane < C * SC_WARPS) q = parts[lane];
+    Run u = {q.m, q.s, q.t};
+    LpRow row;
+    row.m = warp_max(u.m);
+    to_max(u, row.m, c);
+    row.s = warp_sum(u.s);
+    row.t = warp_sum(u.t);
+    row.ahead = __reduce_add_sync(~0u, q.ahead);
+    row.bound = 0;
+    return row;
+}
+__device__ __forceinline__ bool finite_row(float m) { return m > -INFINITY && m < INFINITY; }
+
+// one thread: the results of a row (top tokens apart)
+__device__ __forceinline__ void write_row(const ScoreParams& p, int r, const LpRow& row, float xt)
+{
+    const bool ok = finite_row(row.m);
+    const float nan = __int_as_float(0x7FFFFFFF), ln = logf(row.s), logz = ln - dist(row.m, row.m, p.c) * LN2;
+    p.row_status[r] = ok ? SPEC_ROW_OK : SPEC_ROW_NONFINITE;
+    if (p.logprob) p.logprob[r] = ok ? (xt - row.m) * p.inv_temp - logz : nan;
+    if (p.rank) p.rank[r] = ok ? row.ahead : -1;
+    if (p.entropy) p.entropy[r] = ok ? ln - LN2 * (row.t / row.s) : nan;
+    if (p.lse) p.lse[r] = ok ? row.m * p.inv_temp + logz : nan;
+}
+
+template <typename E, bool TOP> __global__ void __launch_bounds__(SC_NT, 4) k_score_logprobs(const ScoreParams p)
+{
+    extern __shared__ __align__(16) unsigned char smem[];
+    __shared__ LpPart parts[2][SC_PARTS];
+    __shared__ LpRow s_row;
+    const int C = p.cluster, rank = (int)cluster_rank(), tid = threadIdx.x, lane = tid % 32;
+    const int step = gridDim.x / C;
+    TopScratch& ts = *(TopScratch*)(smem + SC_RING_BYTES);
+    Ring<E> ring(p, rank, smem);
+    auto id_of = [&](int r) { return p.ids && r < p.rows ? p.ids[r] : 0; };
+    // the first row from r on that is scored
+    auto settle = [&](int& r, int& id) {
+        while (r < p.rows && (id < 0 || id >= p.V)) {
+            no_logprobs<E>(p, r, id == -1 ? SPEC_ROW_OK : SPEC_ROW_BAD_TOKEN, rank, C);
+            r += step;
+            id = id_of(r);
+        }
+    };
+    // a row's data that are no part of the ring
+    uint4 edge, edge2;
+    E raw, raw2;
+    bool tie = false, tie2 = false;
+    auto fetch = [&](const E* x, const Slice<E>& s, int id, E& raw, uint4& edge, bool& tie) {
+        raw = x[id];
+        edge = ring.edge(s);
+        tie = false;
+        if (p.rank && rank == 0 && tid >= 64 && tid - 64 < (int)((uintptr_t)(x + id) & 15) / (int)sizeof(E) &&
+            id - 1 - (tid - 64) >= 0)
+            tie = widen(x[id - 1 - (tid - 64)]) == widen(raw);
+    };
+    int r = cluster_id(), id = id_of(r);
+    settle(r, id);
+    if (r >= p.rows) return;
+    // every CTA of the cluster runs before another stores into its shared memory
+    if (C > 1) cluster_arrive();
+    bool owed = true;  // a barrier at which this CTA arrived and has not waited
+    const E* x = row_of<E>(p, r);
+    Slice<E> sl(p, x, rank);
+    ring.start(sl);
+    ring.copy_group();
+    fetch(x, sl, id, raw, edge, tie);
+    int r2 = r + step, id2 = id_of(r2), par = 0, was = -1;
+    float was_x = 0.f;
+    while (true) {
+        settle(r2, id2);
+        const bool more = r2 < p.rows;
+        Slice<E> next;
+        if (more) {
+            x = row_of<E>(p, r2);
+            next = Slice<E>(p, x, rank);
+            fetch(x, next, id2, raw2, edge2, tie2);
+        }
+        const int r3 = r2 + step, id3 = id_of(r3);
+        while (ring.ahead < SC_RING && ring.more(next)) {}
+        const float xt = widen(raw);
+        int ahead = 0;
+        Run run;
+        auto none = [](int) { return false; };
+        auto seen = [&](int b, float m) {
+            if (TOP) ts.most[b * SC_NT + tid] = m;
+        };
+        if (p.rank) {
+            Summer<E, true, true> sum;
+            sum.c = p.c;
+            sum.tvec = (id - sl.first) >> (sizeof(E) == 4 ? 2 : 3);
+            sum.x = xt;
+            // a masked token: those in front are the unmasked ones
+            sum.at = Vec<E>::thr_of(xt);
+            sum.under = Vec<E>::thr_of(xt == -INFINITY ? xt : below<E>(raw));
+            sum.stream(ring, sl, next, edge, none, seen);
+            run = sum.result();
+            ahead = sum.ahead + (tie && xt > -INFINITY);
+        } else {
+            Summer<E, true, false> sum;
+            sum.c = p.c;
+            sum.stream(ring, sl, next, edge, none, seen);
+            run = sum.result();
+        }
+        // threads to warp
+        LpPart w;
+        w.m = warp_max(run.m);
+        to_max(run, w.m, p.c);
+        w.s = warp_sum(run.s);
+        w.t = warp_sum(run.t);
+        w.ahead = __reduce_add_sync(~0u, ahead);
+        if (owed) row_wait(C);
+        if (!TOP && was >= 0 && rank == 0 && tid < 32) {
+            // CTA 0 finishes a row while the next one is summed: no one waits for a barrier
+            const LpRow row = join(parts[par ^ 1], p.c, C);
+            if (lane == 0) write_row(p, was, row, was_x);
+        }
+        // warps to cluster: to CTA 0, or to all
+        if (lane < (TOP ? C : 1)) {
+            const uint32_t to = remote(&parts[par][rank * SC_WARPS + tid / 32], lane);
+            remote_st(to, __float_as_uint(w.m));
+            remote_st(to + 4, __float_as_uint(w.s));
+            remote_st(to + 8, __float_as_uint(w.t));
+            remote_st(to + 12, (uint32_t)w.ahead);
+        }
+        if (TOP) give_keys(ts, ring.full, rank, C);
+        row_arrive(C);
+        owed = true;
+        if (TOP) {
+            row_wait(C);
+            owed = false;
+            if (tid < 32) {
+                LpRow row = join(parts[par], p.c, C);
+                row.bound = bound_of(ts, p.top_n);
+                if (lane == 0) {
+                    ts.mine = ts.agains = 0;
+                    s_row = row;
+                    if (rank == 0) write_row(p, r, row, xt);
+                }
+            }
+            __syncthreads();
+            const LpRow row = s_row;
+            if (finite_row(row.m)) {
+                give_candidates(sl, p.V, ring.full, ts, row.bound, p.top_n, rank, C);
+                row_arrive(C);
+                owed = true;
+                if (rank == 0) {
+                    row_wait(C);
+                    owed = false;
+                    write_top(p, r, ts, row, logf(row.s) - dist(row.m, row.m, p.c) * LN2, C);
+                }
+            } else if (rank == 0) {
+                no_top(p, r, SPEC_ROW_NONFINITE);
+            }
+        }
+        was = r;
+        was_x = xt;
+        par ^= 1;
+        if (!more) break;
+        sl = next;
+        ring.on_next = false;
+        raw = raw2;
+        edge = edge2;
+        tie = tie2;
+        r = r2;
+        id = id2;
+        r2 = r3;
+        id2 = id3;
+    }
+    if (!TOP && rank == 0) {
+        row_wait(C);
+        if (tid < 32) {
+            const LpRow row = join(parts[par ^ 1], p.c, C);
+            if (lane == 0) write_row(p, was, row, was_x);
+        }
+    }
+}
+
+template <typename E> __global__ void __launch_bounds__(SC_NT) k_score_logprobs_grad(const ScoreParams p)
+{
+    extern __shared__ __align__(16) unsigned char smem[];
+    __shared__ LpPart parts[2][SC_PARTS];
+    __shared__ LpRow s_row;
+    const int C = p.cluster, rank = (int)cluster_rank(), tid = threadIdx.x, lane = tid % 32;
+    const int step = gridDim.x / C;
+    const Buffer<E> bf(p, rank, smem);
+    auto id_of = [&](int r) { return p.ids && r < p.rows ? p.ids[r] : 0; };
+    auto settle = [&](int& r, int& id) {
+        while (r < p.rows && (id < 0 || id >= p.V)) {
+            no_logprobs<E>(p, r, id == -1 ? SPEC_ROW_OK : SPEC_ROW_BAD_TOKEN, rank, C);
+            r += step;
+            id = id_of(r);
+        }
+    };
+    int r = cluster_id(), id = id_of(r);
+    settle(r, id);
+    if (r >= p.rows) return;
+    if (C > 1) cluster_arrive();  // every CTA of the cluster runs before another stores into its shared memory
+    bool started = false;
+    const E* x = row_of<E>(p, r);
+    Slice<E> sl(p, x, rank);
+    bf.copy(sl);
+    E raw = x[id], raw2 = raw;
+    int r2 = r + step, id2 = id_of(r2), par = 0;
+    while (true) {
+        settle(r2, id2);
+        const bool more = r2 < p.rows;
+        Slice<E> next;
+        if (more) {
+            x = row_of<E>(p, r2);
+            next = Slice<E>(p, x, rank);
+            raw2 = x[id2];
+        }
+        const int r3 = r2 + step, id3 = id_of(r3);
+        const float xt = widen(raw);
+        Summer<E, true, false> sum;
+        sum.c = p.c;
+        Run run = sum.template run<true>(bf, sl);
+        LpPart w;
+        w.m = warp_max(run.m);
+        to_max(run, w.m, p.c);
+        w.s = warp_sum(run.s);
+        w.t = warp_sum(run.t);
+        if (!started) row_wait(C);
+        started = true;
+        if (lane < C) {
+            const uint32_t to = remote(&parts[par][rank * SC_WARPS + tid / 32], lane);
+            remote_st(to, __float_as_uint(w.m));
+            remote_st(to + 4, __float_as_uint(w.s));
+            remote_st(to + 8, __float_as_uint(w.t));
+            remote_st(to + 12, 0u);
+        }
+        row_arrive(C);
+        row_wait(C);
+        if (tid < 32) {
+            const LpRow row = join(parts[par], p.c, C);
+            if (lane == 0) s_row = row;
+        }
+        __syncthreads();
+        const LpRow row = s_row;
+        if (rank == 0 && tid == 0) write_row(p, r, row, xt);
+        if (finite_row(row.m)) {
+            // e (A + B d), e = 2^d: p = e / s, ln p = d ln 2 - ln s
+            const float gl = p.g_logprob ? p.g_logprob[r] : 0.f, gh = p.g_entropy ? p.g_entropy[r] : 0.f;
+            const float f = p.inv_temp / row.s, A = -(gl - gh * LN2 * (row.t / row.s)) * f, B = -gh * LN2 * f;
+            const uint64_t A2 = pair(A, A), B2 = pair(B, B);
+            E* g = grad_of<E>(p, r);
+            if (p.g_entropy)
+                grad_slice(bf, sl, next, g, row.m, p.c, sum.masked,
+                           [&](uint64_t d2, uint64_t e2) { return mul2(e2, fma2(B2, d2, A2)); });
+            else
+                grad_slice(bf, sl, next, g, row.m, p.c, 0, [&](uint64_t, uint64_t e2) { return mul2(e2, A2); });
+            if (p.g_logprob && bf.has(sl, id)) {
+                __syncthreads();
+                if (tid == 0) {
+                    const float d = dist(xt, row.m, p.c), e = ex2_fast(d);
+                    g[id] = narrow<E>(gl * p.inv_temp + e * (A + B * fmaxf(d, NONE)));
+                }
+            }
+        } else {
+            bf.copy(next);
+            zero_grad<E>(p, r, rank, C);
+        }
+        par ^= 1;
+        if (!more) break;
+        sl = next;
+        raw = raw2;
+        r = r2;
+        id = id2;
+        r2 = r3;
+        id2 = id3;
+    }
+}
+
+template <typename E, bool TOP> cudaError_t go_forward(ScoreParams p, cudaStream_t s)
+{
+    static ScoreKernel sk;
+    const auto kernel = k_score_logprobs<E, TOP>;
+    auto smem = [](size_t per) {
+        return SC_RING_BYTES + (TOP ? sizeof(TopScratch) + (per / Ring<E>::GROUP + 2) * SC_NT * 4 : 0);
+    };
+    cudaError_t e = score_ready(kernel, sk, smem(SCORE_MAX_ROW_BYTES / 16 + 2));
+    if (e == cudaSuccess) e = score_split_forward(kernel, sk, p, sizeof(E), TOP ? 48 : 16, smem);
+    return e == cudaSuccess ? score_launch(kernel, sk, p, smem(p.per), s) : e;
+}
+template <typename E> cudaError_t go(ScoreParams p, int num_sms, cudaStream_t s)
+{
+    if (!p.grad || p.top_n || p.rank) {
+        ScoreParams q = p;
+        q.grad = nullptr;
+        const cudaError_t e = p.top_n ? go_forward<E, true>(q, s) : go_forward<E, false>(q, s);
+        if (e != cudaSuccess || !p.grad) return e;
+        // the gradient's kernel writes none of that again
+        p.top_n = 0;
+        p.rank = nullptr;
+    }
+    static ScoreKernel sk;
+    const cudaError_t e = score_ready(k_score_logprobs_grad<E>, sk, SC_MOST_SLICE);
+    if (e != cudaSuccess) return e;
+    score_split_gradient(p, sizeof(E), num_sms);
+    return score_launch(k_score_logprobs_grad<E>, sk, p, (size_t)p.per * 16, s);
+}
+
+}  // namespace
+
+cudaError_t launch_score_logprobs(const ScoreParams& p, int dtype, int num_sms, cudaStream_t s)
+{
+    return dtype == SPEC_F32 ? go<float>(p, num_sms, s)
+           : dtype == SPEC_BF16 ? go<__nv_bfloat16>(p, num_sms, s)
+                                : go<__half>(p, num_sms, s);
+}
+
+}  // namespace sv

@@ -1,0 +1,912 @@
+// sv_score_row.cuh -- device-side building blocks of the operators that score
+// rows of logits: vectors of elements, slices of rows and their copies, running
+// softmax sums, gradients, and the join of a cluster's warps.
+//
+// A row is taken by a cluster of 1 to 8 CTAs, a slice each.  Clusters are
+// persistent and take every nc-th row.  A thread copies the vectors that it will
+// read itself (cp.async), so that no barrier lies between a copy and its use,
+// and a row's barriers and its end pass while the next row is on its way:
+//
+//   forward    a ring of copy groups (Ring): what a thread has used makes room
+//              for what comes, of this row or the next
+//   gradient   the slice stays in shared memory, as the row's sum comes before
+//              the gradient's first element; a vector's place goes to the next
+//              row's once its gradient is written (Buffer)
+//
+// Slices are whole 16-byte vectors of the row's addresses, so rows of any
+// alignment are copied and read alike; what a row's first and last vector have
+// outside the row is -inf, which counts nowhere.
+#pragma once
+
+#include <atomic>
+#include <type_traits>
+
+#include "sv_score.cuh"
+
+namespace sv {
+
+namespace {
+
+constexpr int SC_NT = 128;               // threads of a CTA
+constexpr int SC_WARPS = SC_NT / 32;
+constexpr int SC_BATCH = 4;              // vectors of a thread per copy group (gradient)
+constexpr int SC_GROUP = 4;              // and of the forward passes' ring
+constexpr int SC_RING = 4;               // groups of the ring
+constexpr int SC_RING_BYTES = SC_RING * SC_GROUP * SC_NT * 16;
+constexpr int SC_MAXC = SCORE_MAX_CTAS;  // CTAs of a cluster (portable)
+constexpr int SC_PARTS = SC_MAXC * SC_WARPS;  // warps of a cluster: one lane each where they are joined
+constexpr float LN2 = 0.693147180559945f;
+constexpr double LN2_D = 0.69314718055994530942;
+constexpr float NONE = -200.f;  // a power of 2 that is 0 in fp32; products with it are, too, and with -inf are not
+
+// ---- elements and vectors of 16 bytes ------------------------------------- //
+template <typename E> __device__ __forceinline__ float widen(E x);
+template <> __device__ __forceinline__ float widen(float x) { return x; }
+template <> __device__ __forceinline__ float widen(__nv_bfloat16 x) { return __bfloat162float(x); }
+template <> __device__ __forceinline__ float widen(__half x) { return __half2float(x); }
+template <typename E> __device__ __forceinline__ E narrow(float x);
+template <> __device__ __forceinline__ float narrow(float x) { return x; }
+template <> __device__ __forceinline__ __nv_bfloat16 narrow(float x) { return __float2bfloat16_rn(x); }
+template <> __device__ __forceinline__ __half narrow(float x) { return __float2half_rn(x); }
+
+template <typename E> constexpr int EPV = 16 / (int)sizeof(E);  // elements of a vector
+template <typename E> using Bits = std::conditional_t<sizeof(E) == 4, uint32_t, uint16_t>;
+
+// elements of a vector in registers (q known when the loop around it is unrolled)
+__device__ __forceinline__ uint32_t word_of(const uint4& w, int q) { return q == 0 ? w.x : q == 1 ? w.y : q == 2 ? w.z : w.w; }
+template <typename E> __device__ __forceinline__ Bits<E> bits_at(const uint4& w, int q)
+{
+    if constexpr (sizeof(E) == 4) return word_of(w, q);
+    else return (uint16_t)(word_of(w, q / 2) >> (q % 2 * 16));
+}
+template <typename E> __device__ __forceinline__ uint4 vector_of(const Bits<E> (&b)[EPV<E>])
+{
+    if constexpr (sizeof(E) == 4) return make_uint4(b[0], b[1], b[2], b[3]);
+    else return make_uint4(b[0] | (uint32_t)b[1] << 16, b[2] | (uint32_t)b[3] << 16, b[4] | (uint32_t)b[5] << 16,
+                           b[6] | (uint32_t)b[7] << 16);
+}
+template <typename E> __device__ __forceinline__ float value_of(Bits<E> b)
+{
+    if constexpr (sizeof(E) == 4) return __uint_as_float(b);
+    else return widen(*reinterpret_cast<const E*>(&b));
+}
+
+// pairs of fp32 in one 64-bit register
+__device__ __forceinline__ uint64_t pair(float a, float b)
+{
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void unpair(uint64_t x, float& a, float& b)
+{
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x));
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+
+template <typename E> struct Vec;
+template <> struct Vec<float> {
+    static constexpr uint32_t NEG = 0xFF800000u;  // -inf
+    static __device__ __forceinline__ uint64_t two(uint32_t a, uint32_t b)
+    {
+        return pair(__uint_as_float(a), __uint_as_float(b));
+    }
+    static __device__ __forceinline__ void pairs(const uint4& w, uint64_t (&x)[2])
+    {
+        x[0] = two(w.x, w.y);
+        x[1] = two(w.z, w.w);
+    }
+    // the largest element of a vector, as something to be compared further (most), and as a number
+    using Most = float;
+    static __device__ __forceinline__ Most top_of(const uint4& w)
+    {
+        return fmax_nan(fmax_nan(__uint_as_float(w.x), __uint_as_float(w.y)),
+                        fmax_nan(__uint_as_float(w.z), __uint_as_float(w.w)));
+    }
+    static __device__ __forceinline__ Most most(Most a, Most b) { return fmax_nan(a, b); }
+    static __device__ __forceinline__ float value(Most a) { return a; }
+    static __device__ __forceinline__ float top(const uint4& w) { return top_of(w); }
+    static __device__ __forceinline__ uint4 pack(const uint64_t (&y)[2])
+    {
+        float a, b, c, d;
+        unpair(y[0], a, b);
+        unpair(y[1], c, d);
+        return make_uint4(__float_as_uint(a), __float_as_uint(b), __float_as_uint(c), __float_as_uint(d));
+    }
+    using Thr = float;
+    static __device__ __forceinline__ Thr thr_of(float x) { return x; }
+    using Count = int;
+    static __device__ __forceinline__ Count more(Count a, Count b) { return a + b; }
+    static __device__ __forceinline__ int number(Count n) { return n; }
+    static __device__ __forceinline__ Count above(const uint4& w, Thr thr)
+    {
+        return (__uint_as_float(w.x) > thr) + (__uint_as_float(w.y) > thr) + (__uint_as_float(w.z) > thr) +
+               (__uint_as_float(w.w) > thr);
+    }
+};
+// 16-bit types: what differs is how a word of two becomes fp32 and back
+template <typename E> struct Vec16 {
+    static __device__ __forceinline__ void pairs(const uint4& w, uint64_t (&x)[4])
+    {
+        x[0] = Vec<E>::wide(w.x);
+        x[1] = Vec<E>::wide(w.y);
+        x[2] = Vec<E>::wide(w.z);
+        x[3] = Vec<E>::wide(w.w);
+    }
+    using Most = uint32_t;
+    static __device__ __forceinline__ Most top_of(const uint4& w)
+    {
+        return Vec<E>::max2(Vec<E>::max2(w.x, w.y), Vec<E>::max2(w.z, w.w));
+    }
+    static __device__ __forceinline__ Most most(Most a, Most b) { return Vec<E>::max2(a, b); }
+    static __device__ __forceinline__ float value(Most m)
+    {
+        float a, b;
+        unpair(Vec<E>::wide(m), a, b);
+        return fmax_nan(a, b);
+    }
+    static __device__ __forceinline__ float top(const uint4& w) { return value(top_of(w)); }
+    static __device__ __forceinline__ uint4 pack(const uint64_t (&y)[4])
+    {
+        return make_uint4(Vec<E>::thin(y[0]), Vec<E>::thin(y[1]), Vec<E>::thin(y[2]), Vec<E>::thin(y[3]));
+    }
+    using Thr = uint32_t;
+    static __device__ __forceinline__ Thr thr_of(float x) { return Vec<E>::thin(pair(x, x)); }  // x is a value of E
+    // counts in two halves of a word, exact in either type up to 256 (bf16) words
+    using Count = uint32_t;
+    static __device__ __forceinline__ Count above(const uint4& w, Thr t)
+    {
+        return Vec<E>::plus(Vec<E>::plus(Vec<E>::gt(w.x, t), Vec<E>::gt(w.y, t)),
+                            Vec<E>::plus(Vec<E>::gt(w.z, t), Vec<E>::gt(w.w, t)));
+    }
+    static __device__ __forceinline__ Count more(Count a, Count b) { return Vec<E>::plus(a, b); }
+    static __device__ __forceinline__ int number(Count n)
+    {
+        float a, b;
+        unpair(Vec<E>::wide(n), a, b);
+        return (int)(a + b);
+    }
+};
+template <> struct Vec<__nv_bfloat16> : Vec16<__nv_bfloat16> {
+    static constexpr uint32_t NEG = 0xFF80FF80u;
+    static __device__ __forceinline__ uint64_t wide(uint32_t w) { return pair(bf16_lo(w), bf16_hi(w)); }
+    static __device__ __forceinline__ uint32_t thin(uint64_t y)
+    {
+        float a, b;
+        unpair(y, a, b);
+        uint32_t r;
+        asm("cvt.rn.bf16x2.f32 %0, %2, %1;" : "=r"(r) : "f"(a), "f"(b));
+        return r;
+    }
+    static __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b)
+    {
+        uint32_t r;
+        asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+        return r;
+    }
+    static __device__ __forceinline__ uint32_t gt(uint32_t a, uint32_t b)
+    {
+        uint32_t r;
+        asm("set.gt.bf16x2.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+        return r;
+    }
+    static __device__ __forceinline__ uint32_t plus(uint32_t a, uint32_t b)
+    {
+        uint32_t r;
+        asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+        return r;
+    }
+};
+template <> struct Vec<__half> : Vec16<__half> {
+    static constexpr uint32_t NEG = 0xFC00FC00u;
+    static __device__ __forceinline__ uint64_t wide(uint32_t w)
+    {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
+        return pair(f.x, f.y);
+    }
+    static __device__ __forceinline__ uint32_t thin(uint64_t y)
+    {
+        float a, b;
+        unpair(y, a, b);
+        uint32_t r;
+        asm("cvt.rn.f16x2.f32 %0, %2, %1;" : "=r"(r) : "f"(a), "f"(b));
+        return r;
+    }
+    static __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b)
+    {
+        uint32_t r;
+        asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+        return r;
+    }
+    static __device__ __forceinline__ uint32_t gt(uint32_t a, uint32_t b)
+    {
+        uint32_t r;
+        asm("set.gt.f16x2.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+        return r;
+    }
+    static __device__ __forceinline__ uint32_t plus(uint32_t a, uint32_t b)
+    {
+        uint32_t r;
+        asm("add.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+        return r;
+    }
+};
+
+// the next value of the type below a finite x (-0 and +0 are one value)
+template <typename E> __device__ __forceinline__ float below(E x)
+{
+    if constexpr (sizeof(E) == 4) {
+        const uint32_t b = __float_as_uint(x);
+        return __uint_as_float((b << 1) == 0 ? 0x80000001u : (b >> 31) ? b + 1 : b - 1);
+    } else {
+        unsigned short b = *reinterpret_cast<unsigned short*>(&x);
+        b = (b & 0x7FFF) == 0 ? 0x8001 : (b >> 15) ? b + 1 : b - 1;
+        return widen(*reinterpret_cast<E*>(&b));
+    }
+}
+
+// ---- the cluster ----------------------------------------------------------- //
+__device__ __forceinline__ uint32_t cluster_rank()
+{
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ int cluster_id()
+{
+    int r;
+    asm volatile("mov.u32 %0, %%clusterid.x;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
+// the address of a shared variable in CTA `rank` of the cluster
+__device__ __forceinline__ uint32_t remote(const void* p, int rank)
+{
+    uint32_t a = (uint32_t)__cvta_generic_to_shared(p), r;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ void remote_st(uint32_t a, uint32_t v)
+{
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
+}
+
+// the barrier of a row's CTAs, in two halves
+__device__ __forceinline__ void row_arrive(int C)
+{
+    if (C > 1) cluster_arrive();
+    else __syncthreads();
+}
+__device__ __forceinline__ void row_wait(int C)
+{
+    if (C > 1) cluster_wait();
+}
+
+// ---- a CTA's slice of a row ------------------------------------------------ //
+template <typename E> struct Slice {
+    const char* src;  // global address of its first vector
+    int n;            // vectors
+    int first;        // element of the row at the first vector's start (negative: outside the row)
+    int lo, hi;       // vectors lo .. hi - 1 lie in the row as a whole; one before may not, and one behind is its last
+
+    __device__ __forceinline__ Slice() : src(nullptr), n(0), first(0), lo(0), hi(0) {}
+    __device__ __forceinline__ Slice(const ScoreParams& p, const E* x, int rank)
+    {
+        const int mis = (int)((uintptr_t)x & 15), all = (mis + p.V * (int)sizeof(E) + 15) / 16, v0 = rank * p.per;
+        n = max(0, min(p.per, all - v0));
+        first = v0 * EPV<E> - mis / (int)sizeof(E);
+        src = (const char*)x - mis + (int64_t)v0 * 16;
+        lo = first < 0 ? 1 : 0;
+        hi = max(lo, n > 0 && first + n * EPV<E> >= p.V ? n - 1 : n);
+    }
+};
+
+// vector i of a slice by its elements, -inf outside the row
+template <typename E> __device__ __forceinline__ uint4 part_vector(const Slice<E>& s, int V, int i)
+{
+    const int e = s.first + i * EPV<E>;
+    const Bits<E>* from = (const Bits<E>*)(s.src + (int64_t)i * 16);
+    Bits<E> v[EPV<E>];
+#pragma unroll
+    for (int q = 0; q < EPV<E>; ++q) v[q] = e + q >= 0 && e + q < V ? from[q] : (Bits<E>)Vec<E>::NEG;
+    return vector_of<E>(v);
+}
+template <typename E> __device__ __forceinline__ uint4 no_vector()
+{
+    return make_uint4(Vec<E>::NEG, Vec<E>::NEG, Vec<E>::NEG, Vec<E>::NEG);
+}
+// vector i from global memory, nothing beyond the slice
+template <typename E> __device__ __forceinline__ uint4 load_vector(const Slice<E>& s, int V, int i)
+{
+    if (i >= s.lo && i < s.hi) return *(const uint4*)(s.src + (int64_t)i * 16);
+    return i >= 0 && i < s.n ? part_vector(s, V, i) : no_vector<E>();
+}
+__device__ __forceinline__ void copy16(uint32_t to, const char* from)
+{
+    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// this thread's copies but those of the last `left` groups have arrived (of these, some may have, too)
+__device__ __forceinline__ void copy_arrived(int left)
+{
+    switch (left) {
+    case 0: asm volatile("cp.async.wait_group 0;" ::: "memory"); break;
+    case 1: asm volatile("cp.async.wait_group 1;" ::: "memory"); break;
+    case 2: asm volatile("cp.async.wait_group 2;" ::: "memory"); break;
+    case 3: asm volatile("cp.async.wait_group 3;" ::: "memory"); break;
+    case 4: asm volatile("cp.async.wait_group 4;" ::: "memory"); break;
+    case 5: asm volatile("cp.async.wait_group 5;" ::: "memory"); break;
+    case 6: asm volatile("cp.async.wait_group 6;" ::: "memory"); break;
+    default: asm volatile("cp.async.wait_group 7;" ::: "memory"); break;
+    }
+}
+
+// ---- forward: a ring of copy groups ------------------------------------------ //
+// A group is SC_GROUP vectors of every thread; a slice has `full` groups and one of what is left (up to SC_GROUP
+// vectors a thread).  The row's last vector and its first, if that is not the row's as a whole, are no part of the ring:
+// thread 32 has the last, thread 0 the first, in registers (edge).
+template <typename E> struct Ring {
+    static constexpr int GROUP = SC_NT * SC_GROUP;  // vectors
+    uint4* buf;
+    int V, full;
+    // the next group to be copied: group cb of cs, into place `to`; on_next: cs is the next row's
+    Slice<E> cs;
+    const char* src;          // this thread's first vector of it
+    int cb, to, from, ahead;  // ahead: groups copied or on their way and not used
+    bool on_next;
+
+    __device__ __forceinline__ Ring(const ScoreParams& p, int rank, void* smem)
+        : buf((uint4*)smem + threadIdx.x), V(p.V), to(0), from(0), ahead(0), on_next(false)
+    {
+        const int least = (p.V * (int)sizeof(E) + 15) / 16 - rank * p.per;
+        full = max(0, min(p.per, least) - 1) / GROUP;
+    }
+    __device__ __forceinline__ void start(const Slice<E>& s)
+    {
+        cs = s;
+        cb = 0;
+        src = s.src + threadIdx.x * 16;
+    }
+    __device__ __forceinline__ void copy_group()
+    {
+        uint4* place = buf + to;
+        const uint32_t dst = (uint32_t)__cvta_generic_to_shared(place);
+        if (cb < full) {
+            // whole vectors, but the first of the row
+            if (cb > 0 || threadIdx.x >= cs.lo) copy16(dst, src);
+            else *place = no_vector<E>();
+#pragma unroll
+            for (int j = 1; j < SC_GROUP; ++j) copy16(dst + j * SC_NT * 16, src + j * SC_NT * 16);
+        } else {
+            const int i0 = cb * GROUP + threadIdx.x;
+#pragma unroll
+            for (int j = 0; j < SC_GROUP; ++j) {
+                const int i = i0 + j * SC_NT;
+                if (i >= cs.lo && i < cs.hi) copy16(dst + j * SC_NT * 16, src + j * SC_NT * 16);
+                else if (i < cs.lo) place[j * SC_NT] = no_vector<E>();
+            }
+        }
+        copy_commit();
+        src += GROUP * 16;
+        to = to + GROUP == SC_RING * GROUP ? 0 : to + GROUP;
+        ++cb;
+        ++ahead;
+    }
+    // copies one group more, if there is one: of the row, or of the next
+    __device__ __forceinline__ bool more(const Slice<E>& next)
+    {
+        if (cb > full) {
+            if (on_next || !next.src) return false;
+            on_next = true;
+            start(next);
+        }
+        copy_group();
+        return true;
+    }
+    // the oldest group has arrived; this thread's first vector of it
+    __device__ __forceinline__ const uint4* first()
+    {
+        if (ahead == SC_RING) asm volatile("cp.async.wait_group %0;" ::"n"(SC_RING - 1) : "memory");
+        else copy_arrived(ahead - 1);
+        return buf + from;
+    }
+    __device__ __forceinline__ void used(const Slice<E>& next)
+    {
+        from = from + GROUP == SC_RING * GROUP ? 0 : from + GROUP;
+        --ahead;
+        if (cb <= full) copy_group();
+        else more(next);
+    }
+    __device__ __forceinline__ bool has_edge(const Slice<E>& s) const
+    {
+        return (threadIdx.x == 0 && s.lo && s.n) || (threadIdx.x == 32 && s.hi < s.n);
+    }
+    __device__ __forceinline__ int edge_at(const Slice<E>& s) const { return threadIdx.x == 0 ? 0 : s.n - 1; }
+    __device__ __forceinline__ uint4 edge(const Slice<E>& s) const
+    {
+        return has_edge(s) ? part_vector(s, V, edge_at(s)) : no_vector<E>();
+    }
+};
+
+// ---- gradient: the slice in shared memory ------------------------------------- //
+// the shared memory of a slice, and who copies what: thread t has vectors t, t + SC_NT, ...
+template <typename E> struct Buffer {
+    uint4* buf;
+    int V;
+    int full;  // batches that every thread has whole, at any alignment of the row, the row's last vector not among them
+
+    __device__ __forceinline__ Buffer(const ScoreParams& p, int rank, void* smem) : buf((uint4*)smem), V(p.V)
+    {
+        const int least = (p.V * (int)sizeof(E) + 15) / 16 - rank * p.per;
+        full = max(0, min(p.per, least) - 1) / (SC_NT * SC_BATCH);
+    }
+    __device__ __forceinline__ bool has(const Slice<E>& s, int id) const
+    {
+        return id >= s.first && id < s.first + s.n * EPV<E> && id < V;
+    }
+    __device__ __forceinline__ Bits<E>* at(const Slice<E>& s, int id) const { return (Bits<E>*)buf + (id - s.first); }
+
+    // a batch from this thread's vector i on
+    __device__ __forceinline__ void copy_batch(const Slice<E>& s, int i) const
+    {
+        const uint32_t to = (uint32_t)__cvta_generic_to_shared(buf + i);
+        const char* from = s.src + (int64_t)i * 16;
+        if (i >= s.lo) {
+            if (s.src) {
+#pragma unroll
+                for (int j = 0; j < SC_BATCH; ++j) copy16(to + j * SC_NT * 16, from + j * SC_NT * 16);
+            }
+        } else {  // thread 0 at a row's start
+            buf[0] = part_vector(s, V, 0);
+#pragma unroll
+            for (int j = 1; j < SC_BATCH; ++j) copy16(to + j * SC_NT * 16, from + j * SC_NT * 16);
+        }
+        copy_commit();
+    }
+    // what is left behind the batches, the vectors at the row's ends by their elements
+    __device__ __forceinline__ void copy_rest(const Slice<E>& s) const
+    {
+        for (int i = full * SC_BATCH * SC_NT + threadIdx.x; i < s.n; i += SC_NT)
+            if (i >= s.lo && i < s.hi) copy16((uint32_t)__cvta_generic_to_shared(buf + i), s.src + (int64_t)i * 16);
+            else buf[i] = part_vector(s, V, i);
+        copy_commit();
+    }
+    __device__ __forceinline__ void copy(const Slice<E>& s) const
+    {
+        for (int b = 0; b < full; ++b) copy_batch(s, b * SC_BATCH * SC_NT + threadIdx.x);
+        copy_rest(s);
+    }
+};
+
+// ---- softmax sums ------------------------------------------------------------ //
+// Terms are 2^d with d = l c - B, c = log2(e) / t and B = m c rounded to an integer, m the reference: one exact product
+// and one rounding per logit, and sums of different m differ by powers of 2, exactly.  Where m c is so large that its
+// integer is no help (a row of the type's lowest values, say, where products with c overflow), d = (l - m) c instead.
+// A thread's reference is the first largest logit that it met, and moves only when one is 2^32 times above it: fp32 has
+// room for terms of that size, and moving at every new maximum is a long chain of dependent instructions that some lane
+// of a warp would ask for at most vectors (a verify batch's rows: 35 -> 25 us per 160 MB).
+__device__ __forceinline__ bool plain_ref(float m, float c) { return fabsf(m * c) < 4194304.f; }
+__device__ __forceinline__ float dist(float l, float m, float c)
+{
+    return plain_ref(m, c) ? fmaf(l, c, -rintf(m * c)) : (l - (m == -INFINITY ? 0.f : m)) * c;
+}
+// the exponent by which terms relative to m1 become terms relative to m2 >= m1; m1 above -inf
+__device__ __forceinline__ float between(float m1, float m2, float c)
+{
+    const bool a = plain_ref(m1, c), b = plain_ref(m2, c);
+    if (a && b) return fmaxf(rintf(m1 * c) - rintf(m2 * c), NONE);
+    return fmaxf((m1 - m2) * c - (a ? dist(m1, m1, c) : 0.f) + (b ? dist(m2, m2, c) : 0.f), NONE);
+}
+// reference, sum of 2^d, sum of d 2^d
+struct Run {
+    float m, s, t;
+};
+__device__ __forceinline__ void to_max(Run& r, float m, float c)
+{
+    const bool some = r.m > -INFINITY;
+    const float d = some ? between(r.m, m, c) : 0.f, f = ex2_fast(d);
+    r.t = some ? f * (r.t + d * r.s) : 0.f;
+    r.s = some ? f * r.s : 0.f;
+    r.m = m;
+}
+
+// sums of a thread's vectors, by ENTROPY those of d 2^d too; with RANK also the number of elements above x (in vectors
+// before tvec: or equal to it, written as above the next value below x)
+template <typename E, bool ENTROPY, bool RANK> struct Summer {
+    float m = -INFINITY, limit = -INFINITY, c;
+    uint64_t s2 = 0, t2 = 0;
+    uint32_t masked = 0;  // ENTROPY: batches where d is -inf or may be relative to the row's m; the last bit has all behind 30
+    float x;
+    typename Vec<E>::Thr at, under;
+    int tvec, ahead = 0;
+
+    // the terms of some vectors; CLAMP: those of d 2^d alone, where d may be -inf
+    template <bool FAST, bool CLAMP, int N> __device__ __forceinline__ void terms(const uint4 (&w)[N])
+    {
+        const float ref = FAST ? -rintf(m * c) : m == -INFINITY ? 0.f : -m;
+        const uint64_t r2 = pair(ref, ref), c2 = pair(c, c);
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            uint64_t v[EPV<E> / 2];
+            Vec<E>::pairs(w[j], v);
+#pragma unroll
+            for (int q = 0; q < EPV<E> / 2; ++q) {
+                const uint64_t d2 = FAST ? fma2(v[q], c2, r2) : mul2(add2(v[q], r2), c2);
+                float a, z;
+                unpair(d2, a, z);
+                const uint64_t e2 = pair(ex2_fast(a), ex2_fast(z));
+                if (!CLAMP) s2 = add2(s2, e2);
+                if (ENTROPY) t2 = fma2(e2, CLAMP ? pair(fmaxf(a, NONE), fmaxf(z, NONE)) : d2, t2);
+            }
+        }
+    }
+    // vectors i, i + SC_NT, ...; returns their largest element
+    template <int N> __device__ __forceinline__ float take(const uint4 (&w)[N], int i, int batch)
+    {
+        typename Vec<E>::Most most = Vec<E>::top_of(w[0]);
+#pragma unroll
+        for (int j = 1; j < N; ++j) most = Vec<E>::most(most, Vec<E>::top_of(w[j]));
+        const float mx = Vec<E>::value(most);
+        if (!(mx <= limit)) {  // a new reference (or NaN, which stays)
+            const float mn = fmax_nan(m, mx);
+            if (m > -INFINITY) {
+                const float d = between(m, mn, c), f = ex2_fast(d);
+                const uint64_t f2 = pair(f, f);
+                if (ENTROPY) t2 = mul2(f2, fma2(pair(d, d), s2, t2));
+                s2 = mul2(f2, s2);
+            }
+            m = mn;
+            limit = mn + 32.f / c;
+        }
+        const uint64_t t0 = t2;
+        const bool fast = plain_ref(m, c);
+        if (fast) terms<true, false>(w);
+        else terms<false, false>(w);
+        if (ENTROPY) {
+            float a, z;
+            unpair(t2, a, z);
+            a += z;
+            if (a != a) {  // 0 times -inf
+                t2 = t0;
+                if (fast) terms<true, true>(w);
+                else terms<false, true>(w);
+            }
+            if (a != a || !fast) masked |= 1u << min(batch, 31);
+        }
+        if (RANK && mx >= x) {
+            typename Vec<E>::Count n = Vec<E>::above(w[0], i < tvec ? under : at);
+#pragma unroll
+            for (int j = 1; j < N; ++j) n = Vec<E>::more(n, Vec<E>::above(w[j], i + j * SC_NT < tvec ? under : at));
+            ahead += Vec<E>::number(n);
+        }
+        return mx;
+    }
+    __device__ __forceinline__ Run result() const
+    {
+        float a, z;
+        Run r;
+        r.m = m;
+        unpair(s2, a, z);
+        r.s = a + z;
+        unpair(t2, a, z);
+        r.t = a + z;
+        return r;
+    }
+    // A slice in the ring, and its edge.  skip(b): this thread leaves out its vectors of group b (full + 1: the edge);
+    // seen(b, x): their largest element.
+    template <typename Skip, typename Seen>
+    __device__ __forceinline__ void stream(Ring<E>& ring, const Slice<E>& s, const Slice<E>& next, const uint4& edge,
+                                          Skip skip, Seen seen)
+    {
+        int i = threadIdx.x;
+        for (int b = 0; b < ring.full; ++b, i += Ring<E>::GROUP) {
+            const uint4* v = ring.first();
+            uint4 w[SC_GROUP];
+#pragma unroll
+            for (int j = 0; j < SC_GROUP; ++j) w[j] = v[j * SC_NT];
+            if (skip(b)) {
+#pragma unroll
+                for (int j = 0; j < SC_GROUP; ++j) w[j] = no_vector<E>();
+            }
+            seen(b, take(w, i, b));
+            ring.used(next);
+        }
+        const uint4* v = ring.first();
+        float mx = -INFINITY;
+        const bool left_out = skip(ring.full);
+        for (; i < s.hi; i += SC_NT, v += SC_NT) {
+            const uint4 w[1] = {left_out ? no_vector<E>() : *v};
+            mx = fmax_nan(mx, take(w, i, ring.full));
+        }
+        ring.used(next);
+        if (ring.has_edge(s) && !skip(ring.full + 1)) {
+            const uint4 w[1] = {edge};
+            mx = fmax_nan(mx, take(w, ring.edge_at(s), ring.full));
+        }
+        seen(ring.full, mx);
+    }
+    // A slice in its buffer, being copied in groups (WAIT) or there.
+    template <bool WAIT> __device__ __forceinline__ Run run(const Buffer<E>& bf, const Slice<E>& s)
+    {
+        int i = threadIdx.x;
+        for (int b = 0; b < bf.full; ++b, i += SC_NT * SC_BATCH) {
+            if (WAIT) copy_arrived(bf.full - b);
+            uint4 w[SC_BATCH];
+#pragma unroll
+            for (int j = 0; j < SC_BATCH; ++j) w[j] = bf.buf[i + j * SC_NT];
+            take(w, i, b);
+        }
+        if (WAIT) copy_arrived(0);
+        for (int b = bf.full; i < s.n; i += SC_NT, ++b) {
+            const uint4 w[1] = {bf.buf[i]};
+            take(w, i, b);
+        }
+        return result();
+    }
+};
+
+template <typename X, typename F> __device__ __forceinline__ X warp_reduce(X x, F op)
+{
+#pragma unroll
+    for (int d = 16; d; d >>= 1) x = op(x, __shfl_xor_sync(~0u, x, d));
+    return x;
+}
+__device__ __forceinline__ float warp_max(float x)
+{
+    return warp_reduce(x, [](float a, float b) { return fmax_nan(a, b); });
+}
+template <typename X> __device__ __forceinline__ X warp_sum(X x)
+{
+    return warp_reduce(x, [](X a, X b) { return a + b; });
+}
+
+template <typename E> __device__ __forceinline__ const E* row_of(const ScoreParams& p, int r)
+{
+    const int b = p.by_tokens.of(r);
+    return (const E*)p.x + (int64_t)b * p.x_seq + (int64_t)(r - b * p.T) * p.x_tok;
+}
+template <typename E> __device__ __forceinline__ E* grad_of(const ScoreParams& p, int r)
+{
+    const int b = p.by_tokens.of(r);
+    return (E*)p.grad + (int64_t)b * p.g_seq + (int64_t)(r - b * p.T) * p.g_tok;
+}
+
+// ---- gradients ----------------------------------------------------------------- //
+// a row without a gradient, by the cluster's CTAs
+template <typename E> __device__ void zero_grad(const ScoreParams& p, int r, int rank, int C)
+{
+    E* g = grad_of<E>(p, r);
+    const int head = (int)min((int64_t)p.V, (int64_t)(-(intptr_t)((uintptr_t)g / sizeof(E))) & (EPV<E> - 1));
+    const int nv = (p.V - head) / EPV<E>, i0 = rank * SC_NT + threadIdx.x;
+    uint4* to = (uint4*)(g + head);
+    for (int i = i0; i < nv; i += C * SC_NT) to[i] = make_uint4(0, 0, 0, 0);
+    if (i0 < head) g[i0] = narrow<E>(0.f);
+    const int rest = head + nv * EPV<E> + i0;
+    if (rest < p.V) g[rest] = narrow<E>(0.f);
+}
+
+// The gradient of a slice, whose buffer next's slice takes: f(pair of d, 2^d; CLAMP: d may be -inf) -> pair.
+template <typename E, bool FAST, typename F>
+__device__ __forceinline__ void grad_slice_(const Buffer<E>& bf, const Slice<E>& s, const Slice<E>& next, E* g, float m,
+                                            float c, uint32_t masked, F f)
+{
+    const float ref = FAST ? -rintf(m * c) : m == -INFINITY ? 0.f : -m;
+    const uint64_t r2 = pair(ref, ref), c2 = pair(c, c);
+    auto grad = [&](int i, auto clamp) {
+        uint64_t v[EPV<E> / 2], y[EPV<E> / 2];
+        Vec<E>::pairs(bf.buf[i], v);
+#pragma unroll
+        for (int q = 0; q < EPV<E> / 2; ++q) {
+            const uint64_t d2 = FAST ? fma2(v[q], c2, r2) : mul2(add2(v[q], r2), c2);
+            float a, z;
+            unpair(d2, a, z);
+            y[q] = f(decltype(clamp)::value ? pair(fmaxf(a, NONE), fmaxf(z, NONE)) : d2, pair(ex2_fast(a), ex2_fast(z)));
+        }
+        return Vec<E>::pack(y);
+    };
+    auto any = [&](int i, int batch) {
+        return masked >> min(batch, 31) & 1 ? grad(i, std::true_type()) : grad(i, std::false_type());
+    };
+    E* out = g + s.first;  // its element at the slice's start
+    int i = threadIdx.x;
+    if (((uintptr_t)out & 15) == 0) {
+        uint4* to = (uint4*)out;
+        auto part = [&](int i, const uint4& w) {
+            const int e = s.first + i * EPV<E>;
+#pragma unroll
+            for (int q = 0; q < EPV<E>; ++q)
+                if (e + q >= 0 && e + q < bf.V) ((Bits<E>*)g)[e + q] = bits_at<E>(w, q);
+        };
+        for (int b = 0; b < bf.full; ++b, i += SC_NT * SC_BATCH) {
+            uint4 w[SC_BATCH];
+            if (masked >> min(b, 31) & 1) {
+#pragma unroll
+                for (int j = 0; j < SC_BATCH; ++j) w[j] = grad(i + j * SC_NT, std::true_type());
+            } else {
+#pragma unroll
+                for (int j = 0; j < SC_BATCH; ++j) w[j] = grad(i + j * SC_NT, std::false_type());
+            }
+            if (i >= s.lo) to[i] = w[0];
+            else part(i, w[0]);
+#pragma unroll
+            for (int j = 1; j < SC_BATCH; ++j) to[i + j * SC_NT] = w[j];
+            bf.copy_batch(next, i);
+        }
+        for (int b = bf.full; i < s.n; i += SC_NT, ++b) {
+            const uint4 w = any(i, b);
+            if (i >= s.lo && i < s.hi) to[i] = w;
+            else part(i, w);
+        }
+        bf.copy_rest(next);
+        return;
+    }
+    // the gradient's rows start elsewhere in a vector than the logits': elements change vectors on the way out
+    for (int b = 0; i < s.n; i += SC_NT, ++b)
+        bf.buf[i] = any(i, b < bf.full * SC_BATCH ? b / SC_BATCH : b - bf.full * (SC_BATCH - 1));
+    __syncthreads();
+    const int e0 = max(s.first, 0), e1 = min(s.first + s.n * EPV<E>, bf.V);
+    if (e0 < e1) {
+        const int head = min(e1 - e0, (int)((-(intptr_t)((uintptr_t)(g + e0) / sizeof(E))) & (EPV<E> - 1)));
+        const int nv = (e1 - e0 - head) / EPV<E>;
+        const Bits<E>* from = bf.at(s, e0);
+        Bits<E>* to = (Bits<E>*)g + e0;
+        for (int i = threadIdx.x; i < nv; i += SC_NT) {
+            Bits<E> v[EPV<E>];
+#pragma unroll
+            for (int q = 0; q < EPV<E>; ++q) v[q] = from[head + i * EPV<E> + q];
+            *(uint4*)(to + head + i * EPV<E>) = vector_of<E>(v);
+        }
+        if (threadIdx.x < head) to[threadIdx.x] = from[threadIdx.x];
+        const int rest = head + nv * EPV<E> + threadIdx.x;
+        if (rest < e1 - e0) to[rest] = from[rest];
+    }
+    __syncthreads();
+    bf.copy(next);
+}
+template <typename E, typename F>
+__device__ __forceinline__ void grad_slice(const Buffer<E>& bf, const Slice<E>& s, const Slice<E>& next, E* g, float m,
+                                           float c, uint32_t masked, F f)
+{
+    if (plain_ref(m, c)) grad_slice_<E, true>(bf, s, next, g, m, c, masked, f);
+    else grad_slice_<E, false>(bf, s, next, g, m, c, masked, f);
+}
+
+// ---- launches ------------------------------------------------------------------ //
+// A kernel's launch set-up on each device, and its resident clusters by CTAs of a cluster and their shared memory, as
+// last asked of the runtime: one word holds both and the answer.
+struct ScoreKernel {
+    DeviceOnce once;
+    std::atomic<uint64_t> known[SV_MAX_DEVICES][64] = {};
+};
+struct ScoreLaunch {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute at[1];
+    ScoreLaunch(int C, size_t smem, cudaStream_t s)
+    {
+        cfg.gridDim = dim3((unsigned)C);
+        cfg.blockDim = dim3(SC_NT);
+        cfg.dynamicSmemBytes = smem;
+        cfg.stream = s;
+        at[0].id = cudaLaunchAttributeClusterDimension;
+        at[0].val.clusterDim.x = C;
+        at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+        cfg.attrs = at;
+        cfg.numAttrs = 1;
+    }
+};
+
+// to be called before the others: up to `most` bytes of shared memory for the kernel
+template <typename K> cudaError_t score_ready(K kernel, ScoreKernel& sk, size_t most)
+{
+    return cuda_once(sk.once, nullptr, [&](int, int*) {
+        return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
+    });
+}
+template <typename K> cudaError_t score_resident(K kernel, ScoreKernel& sk, int C, size_t smem, int* clusters)
+{
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t key = (uint64_t)C << 24 | smem / 16;
+    std::atomic<uint64_t>& word = sk.known[dev][(smem / 16 * 9 + C) % 64];
+    const uint64_t seen = word.load(std::memory_order_relaxed);
+    if (seen >> 32 == key) {
+        *clusters = (int)(seen & 0xFFFFFFFFu);
+        return cudaSuccess;
+    }
+    const ScoreLaunch l(C, smem, nullptr);
+    e = cudaOccupancyMaxActiveClusters(clusters, kernel, &l.cfg);
+    if (e != cudaSuccess) return e;
+    if (*clusters < 1) *clusters = 1;
+    word.store(key << 32 | (uint32_t)*clusters, std::memory_order_relaxed);
+    return cudaSuccess;
+}
+
+// Launches persistent clusters of p.cluster CTAs with `smem` bytes each: as many as fit the GPU at once, since one more
+// would wait for another's last row.
+template <typename K>
+cudaError_t score_launch(K kernel, ScoreKernel& sk, ScoreParams& p, size_t smem, cudaStream_t s)
+{
+    const int C = p.cluster;
+    int nc = 0;
+    const cudaError_t e = score_resident(kernel, sk, C, smem, &nc);
+    if (e != cudaSuccess) return e;
+    p.by_tokens = FastDiv(p.T);
+    if (nc >= p.rows) {
+        nc = p.rows;
+    } else {
+        // a stride that shares no factor with the positions of a sequence: each cluster meets all of them alike,
+        // the ends of ragged sequences, which cost nothing, among them
+        auto gcd = [](int a, int b) {
+            while (b) {
+                const int t = a % b;
+                a = b;
+                b = t;
+            }
+            return a;
+        };
+        while (nc > 1 && gcd(nc, p.T) > 1) --nc;
+    }
+    ScoreLaunch l(C, smem, s);
+    l.cfg.gridDim = dim3((unsigned)nc * C);
+    return cudaLaunchKernelEx(&l.cfg, kernel, p);
+}
+
+// vectors of a row, at any alignment
+inline int score_vectors(const ScoreParams& p, size_t size) { return (int)(((size_t)p.V * size + 30) / 16); }
+
+// CTAs of a row in a forward pass, by the time that each power of two would take: rounds of rows, each of a slice's
+// vectors and a cost that does not shrink with it (`fixed`, in vectors of a thread).  smem_of: bytes for a slice.
+template <typename K, typename F>
+cudaError_t score_split_forward(K kernel, ScoreKernel& sk, ScoreParams& p, size_t size, int fixed, F smem_of)
+{
+    const int row = score_vectors(p, size);
+    double best = 0;
+    for (int C = 1; C <= SC_MAXC && (C == 1 || row / C >= SC_NT); C *= 2) {
+        const int per = (row + C - 1) / C;
+        int nc = 0;
+        const cudaError_t e = score_resident(kernel, sk, C, smem_of(per), &nc);
+        if (e != cudaSuccess) return e;
+        const double cost = (double)((p.rows + nc - 1) / nc) * ((double)per / SC_NT + fixed);
+        if (C > 1 && cost >= best) continue;
+        best = cost;
+        p.cluster = C;
+        p.per = per;
+    }
+    return cudaSuccess;
+}
+// CTAs of a row with a gradient: slices of at most SCORE_SLICE bytes, so that several CTAs share an SM and some copy
+// while others compute; rows beyond eight of them have larger slices.  Few rows are spread over up to eight CTAs, for
+// the SMs that would idle, while a thread still has a vector.
+inline void score_split_gradient(ScoreParams& p, size_t size, int num_sms)
+{
+    const int row = score_vectors(p, size), slice = SCORE_SLICE / 16;
+    int C = (row + slice - 1) / slice;
+    C = C > SC_MAXC ? SC_MAXC : C;
+    while (C < SC_MAXC && (int64_t)p.rows * C < num_sms && row / (C + 1) >= SC_NT) ++C;
+    p.cluster = C;
+    p.per = (row + C - 1) / C;
+}
+constexpr size_t SC_MOST_SLICE = SCORE_MAX_ROW_BYTES / SC_MAXC + 64;
+
+}  // namespace
+
+}  // namespace sv

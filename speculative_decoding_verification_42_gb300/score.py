@@ -7,6 +7,7 @@ library's CUDA kernels; there is no fallback.
 from __future__ import annotations
 
 import ctypes as C
+import struct
 
 from .tree import SPEC_F16, on_stream
 
@@ -65,69 +66,92 @@ def spec_score_distill(args: spec_score_distill_args, stream: int = 0) -> None:
 # --------------------------------------------------------------------------- #
 # torch wrapper                                                               #
 # --------------------------------------------------------------------------- #
-_CODES: dict = {}
+# Small calls are bound by the host, so the wrapper is kept short: the argument records are packed at once
+# (the layouts of the two structures above).
+_LOGPROBS_ARGS, _DISTILL_ARGS = struct.Struct("@6ifPqq10PPqq"), struct.Struct("@8i2fPqq7PPqq")
+_bound: dict = {}
+
+
+def _bind_wrapper() -> dict:
+    """What the wrapper looks up once: torch, the type codes, and the library's functions taking packed records."""
+    import torch
+    from . import SPEC_BF16, SPEC_F32, load_library
+    L, known = load_library(), {"torch": torch}
+    for name in SCORE_FUNCTIONS:
+        f = L[name]  # a function object of its own: the library's keeps its declared types
+        f.argtypes, f.restype = [C.c_char_p, C.c_void_p], C.c_int
+        known[name] = f
+    known["codes"] = {torch.float32: SPEC_F32, torch.bfloat16: SPEC_BF16, torch.float16: SPEC_F16}
+    known["stream"] = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+        (lambda device: torch.cuda.current_stream(device).cuda_stream)
+    _bound.update(known)  # at once, as another thread may look
+    return _bound
 
 
 def _code(dtype, what) -> int:
-    if not _CODES:
-        import torch
-        from . import SPEC_BF16, SPEC_F32
-        _CODES.update({torch.float32: SPEC_F32, torch.bfloat16: SPEC_BF16, torch.float16: SPEC_F16})
-    if dtype not in _CODES:
+    code = _bound["codes"].get(dtype)
+    if code is None:
         raise TypeError(f"{what} must be bfloat16, float16 or float32, got {dtype}")
-    return _CODES[dtype]
+    return code
 
 
-def _rows(rec, t, what):
-    """Fill a spec_score_rows with a [B, T, V] or [N, V] tensor of any strides."""
+def _rows(t, what):
+    """(address, stride of a sequence, of a position) of a [B, T, V] or [N, V] tensor of any strides."""
     st = t.stride()
-    if t.shape[-1] > 1 and st[-1] != 1:
+    if st[-1] != 1 and t.shape[-1] > 1:
         raise ValueError(f"the last dimension of {what} must be contiguous")
-    rec.ptr = t.data_ptr()
-    rec.token_stride = st[-2]
-    rec.seq_stride = st[0] if len(st) == 3 else 0
+    return t.data_ptr(), st[0] if len(st) == 3 else 0, st[-2]
 
 
-def _logits(t, what):
-    """(leading shape, B, T, V) of a tensor of rows on a CUDA device."""
+def _shape(t, what):
+    """(B, T, V) of a tensor of rows on a CUDA device."""
     shape = t.shape
-    if len(shape) == 3:
-        B, T, V = shape
-    elif len(shape) == 2:
-        (T, V), B = shape, 1
-    else:
+    if len(shape) == 2:
+        shape = (1, *shape)
+    elif len(shape) != 3:
         raise ValueError(f"{what} must be [B, T, V] or [N, V], got {tuple(shape)}")
     if not t.is_cuda:
         raise ValueError(f"{what} must be on a CUDA device, got {t.device}")
-    return shape[:-1], B, T, V
+    return shape
 
 
 def _tensor(t, shape, dtype, device, what):
     """The address of a contiguous tensor of this shape and type."""
     if t is None:
-        return None
+        return 0
     if t.shape != shape or t.dtype is not dtype or t.device != device or not t.is_contiguous():
         raise ValueError(f"{what} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}, "
                          f"got {t.dtype} {tuple(t.shape)} on {t.device}")
     return t.data_ptr()
 
 
-def _grad(rec, out, like, res):
+def _result(res, out, name, shape, dtype, device):
+    """A result into res, the caller's tensor or a new one; its address."""
+    t = None if out is None else out.get(name)
+    if t is None:
+        t = res[name] = _bound["torch"].empty(shape, dtype=dtype, device=device)
+        return t.data_ptr()
+    res[name] = t
+    return _tensor(t, shape, dtype, device, f"out['{name}']")
+
+
+def _grad(out, like, res):
     """The caller's gradient tensor (checked; the logits themselves may be given), or a new one."""
     g = None if out is None else out.get("grad")
     if g is None:
-        import torch
-        g = torch.empty(like.shape, dtype=like.dtype, device=like.device)
+        g = _bound["torch"].empty(like.shape, dtype=like.dtype, device=like.device)
     elif g.shape != like.shape or g.dtype is not like.dtype or g.device != like.device:
         raise ValueError(f"out['grad'] must be {like.dtype} {tuple(like.shape)} on {like.device}, got "
                          f"{g.dtype} {tuple(g.shape)} on {g.device}")
-    _rows(rec, g, "out['grad']")
     res["grad"] = g
+    return _rows(g, "out['grad']")
 
 
-def _stream(device) -> int:
-    import torch
-    return torch.cuda.current_stream(device).cuda_stream
+def _run(name, args, device) -> None:
+    code = _bound[name](args, _bound["stream"](device.index))
+    if code:
+        from . import SpecVerifyError
+        raise SpecVerifyError(code, name)
 
 
 def logprobs(logits, tokens=None, *, temperature: float = 1.0, top_n: int = 0, rank: bool = False,
@@ -145,40 +169,28 @@ def logprobs(logits, tokens=None, *, temperature: float = 1.0, top_n: int = 0, r
     if stream is not None:
         return on_stream(stream, logits.device, logprobs, logits, tokens, temperature=temperature, top_n=top_n,
                          rank=rank, grad_logprob=grad_logprob, grad_entropy=grad_entropy, out=out)
-    import torch
-    a, dev, f32, i32 = spec_score_logprobs_args(), logits.device, torch.float32, torch.int32
-    lead, a.batch, a.tokens, a.vocab = _logits(logits, "logits")
-    a.device, a.dtype, a.top_n, a.temperature = dev.index, _code(logits.dtype, "logits"), top_n, temperature
-    _rows(a.logits, logits, "logits")
+    torch = (_bound or _bind_wrapper())["torch"]
+    B, T, V = _shape(logits, "logits")
+    lead, dev, f32, i32 = logits.shape[:-1], logits.device, torch.float32, torch.int32
     if tokens is None and (rank or grad_logprob is not None):
         raise ValueError("rank and grad_logprob need tokens")
-    a.ids = _tensor(tokens, lead, i32, dev, "tokens")
-    a.grad_logprob = _tensor(grad_logprob, lead, f32, dev, "grad_logprob")
-    a.grad_entropy = _tensor(grad_entropy, lead, f32, dev, "grad_entropy")
-    res = {}
-
-    def result(name, shape, dtype):
-        t = None if out is None else out.get(name)
-        if t is None:
-            t = torch.empty(shape, dtype=dtype, device=dev)
-            setattr(a, name, t.data_ptr())
-        else:
-            setattr(a, name, _tensor(t, shape, dtype, dev, f"out['{name}']"))
-        res[name] = t
-
+    code, rows = _code(logits.dtype, "logits"), _rows(logits, "logits")
+    ids = _tensor(tokens, lead, i32, dev, "tokens")
+    up = _tensor(grad_logprob, lead, f32, dev, "grad_logprob"), _tensor(grad_entropy, lead, f32, dev, "grad_entropy")
+    res, lp, rk, ti, tl, grad = {}, 0, 0, 0, 0, (0, 0, 0)
     if tokens is not None:
-        result("logprob", lead, f32)
+        lp = _result(res, out, "logprob", lead, f32, dev)
         if rank:
-            result("rank", lead, i32)
-    result("entropy", lead, f32)
-    result("lse", lead, f32)
-    result("row_status", lead, i32)
+            rk = _result(res, out, "rank", lead, i32, dev)
+    ent, lse = _result(res, out, "entropy", lead, f32, dev), _result(res, out, "lse", lead, f32, dev)
+    status = _result(res, out, "row_status", lead, i32, dev)
     if top_n > 0:
-        result("top_ids", (*lead, top_n), i32)
-        result("top_logprobs", (*lead, top_n), f32)
+        ti = _result(res, out, "top_ids", (*lead, top_n), i32, dev)
+        tl = _result(res, out, "top_logprobs", (*lead, top_n), f32, dev)
     if grad_logprob is not None or grad_entropy is not None:
-        _grad(a.grad, out, logits, res)
-    spec_score_logprobs(a, _stream(dev))
+        grad = _grad(out, logits, res)
+    _run("spec_score_logprobs", _LOGPROBS_ARGS.pack(dev.index, code, B, T, V, top_n, temperature, *rows, ids, *up, lp,
+                                                    rk, ent, lse, ti, tl, status, *grad), dev)
     return res
 
 
@@ -202,30 +214,22 @@ def distill(student, top_ids, teacher, *, temperature: float = 1.0, teacher_temp
         return on_stream(stream, student.device, distill, student, top_ids, teacher, temperature=temperature,
                          teacher_temperature=teacher_temperature, tail=tail, teacher_lse=teacher_lse,
                          grad_loss=grad_loss, out=out)
-    import torch
-    a, dev, f32 = spec_score_distill_args(), student.device, torch.float32
-    lead, a.batch, a.tokens, a.vocab = _logits(student, "student")
+    torch = (_bound or _bind_wrapper())["torch"]
+    B, T, V = _shape(student, "student")
+    lead, dev, f32 = student.shape[:-1], student.device, torch.float32
     k = top_ids.shape[-1] if top_ids.dim() else 0
-    a.device, a.dtype, a.teacher_dtype = dev.index, _code(student.dtype, "student"), _code(teacher.dtype, "teacher")
-    a.entries, a.tail, a.temperature = k, bool(tail), temperature
-    a.teacher_temperature = temperature if teacher_temperature is None else teacher_temperature
-    _rows(a.student, student, "student")
-    a.ids = _tensor(top_ids, (*lead, k), torch.int32, dev, "top_ids")
-    a.teacher = _tensor(teacher, (*lead, k), teacher.dtype, dev, "teacher")
-    a.teacher_lse = _tensor(teacher_lse, lead, f32, dev, "teacher_lse")
-    a.grad_loss = _tensor(grad_loss, lead, f32, dev, "grad_loss")
-    res = {}
-    for name, dtype in (("loss", f32), ("accept", f32), ("row_status", torch.int32)):
-        t = None if out is None else out.get(name)
-        if t is None:
-            t = torch.empty(lead, dtype=dtype, device=dev)
-            setattr(a, name, t.data_ptr())
-        else:
-            setattr(a, name, _tensor(t, lead, dtype, dev, f"out['{name}']"))
-        res[name] = t
+    code, t_code, rows = _code(student.dtype, "student"), _code(teacher.dtype, "teacher"), _rows(student, "student")
+    ins = (_tensor(top_ids, (*lead, k), torch.int32, dev, "top_ids"),
+           _tensor(teacher, (*lead, k), teacher.dtype, dev, "teacher"),
+           _tensor(teacher_lse, lead, f32, dev, "teacher_lse"), _tensor(grad_loss, lead, f32, dev, "grad_loss"))
+    res, grad = {}, (0, 0, 0)
+    outs = (_result(res, out, "loss", lead, f32, dev), _result(res, out, "accept", lead, f32, dev),
+            _result(res, out, "row_status", lead, torch.int32, dev))
     if grad_loss is not None:
-        _grad(a.grad, out, student, res)
-    spec_score_distill(a, _stream(dev))
+        grad = _grad(out, student, res)
+    _run("spec_score_distill", _DISTILL_ARGS.pack(dev.index, code, t_code, B, T, V, k, bool(tail), temperature,
+                                                  temperature if teacher_temperature is None else teacher_temperature,
+                                                  *rows, *ins, *outs, *grad), dev)
     return res
 
 

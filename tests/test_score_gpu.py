@@ -298,8 +298,8 @@ def test_distill(sv, kind, V, tail, k, t_kind):
     assert set(only) == {"loss", "accept", "row_status"}
     got = sv.distill(*args, **kw, grad_loss=_dev(w))
     _check_distill(got, _f64(x), ids, _f64(t), temp, 1.0, tail, lse, w, kind)
-    for n in only:
-        assert (only[n] == got[n]).all()
+    # the forward pass alone adds in another order: each form is held to the formula, not to the other's last bit
+    _check_distill(only, _f64(x), ids, _f64(t), temp, 1.0, tail, lse, w, kind)
 
 
 @pytest.mark.parametrize("how", ["ties", "equal", "masked", "block", "one", "lowest", "all_lowest", "far", "steep"])

@@ -122,3 +122,20 @@ def test_reference_rows():
     d, _ = ref.distill(np.log(np.array([0.5, 0.2, 0.3])), np.array([1, 0]), np.log(np.array([0.2, 0.5])), 1.0, 1.0, True,
                        0.0, 1.0, "f32")
     assert abs(d["loss"]) < 1e-15 and np.isclose(d["accept"], 0.7) and np.abs(d["grad"]).max() < 1e-15
+
+
+def test_packed_records_have_the_structures_layout():
+    """The wrapper packs its arguments at once: sizes and places are those of the declared structures."""
+    import struct
+    import speculative_decoding_verification_42_gb300.score as sc
+    for cls, packed in ((sc.spec_score_logprobs_args, sc._LOGPROBS_ARGS), (sc.spec_score_distill_args, sc._DISTILL_ARGS)):
+        fields = []
+        for name, kind in cls._fields_:
+            fields += [(name, n) for n, _ in kind._fields_] if kind is sc.spec_score_rows else [(name, None)]
+        assert C.sizeof(cls) == packed.size
+        values = [i + 1 for i in range(len(fields))]
+        rec = cls.from_buffer_copy(packed.pack(*values))
+        for (name, sub), v in zip(fields, values):
+            got = getattr(rec, name) if sub is None else getattr(getattr(rec, name), sub)
+            assert got == v, (name, sub)
+    assert struct.calcsize("P") == 8
