@@ -264,168 +264,117 @@ __device__ __forceinline__ void finish(const ScoreParams& p, int r, const KdRow&
 // A thread leaves out the copy groups of its vectors in which an entry lies (flags: a bit for each group and thread, the
 // row's ends being group full + 1).  Those are read once more, each by the thread of the first entry in it (slots: group
 // and thread), which takes the entries out.
-template <typename E> __global__ void __launch_bounds__(SC_NT, 4) k_score_distill(const ScoreParams p)
+template <typename E> __global__ void __launch_bounds__(SC_NT, 5) k_score_distill(const ScoreParams p)
 {
     extern __shared__ __align__(16) unsigned char smem[];
-    __shared__ __align__(16) EntryShared shared[2];
-    __shared__ KdPart parts[2][SC_PARTS];
+    __shared__ __align__(16) EntryShared es;
+    __shared__ KdPart parts[SC_PARTS];
     __shared__ KdRow s_row;
-    const int C = p.cluster, rank = (int)cluster_rank(), tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
-    const int step = gridDim.x / C;
-    Ring<E> ring(p, rank, smem);
-    const int words = (ring.full + 2) * SC_WARPS;
-    uint32_t* const all_flags = (uint32_t*)(smem + SC_RING_BYTES);
-    // the first row from r on that has an entry
-    auto settle = [&](int& r, Entries& en) {
-        while (r < p.rows && !__syncthreads_or(en.some())) {
-            no_distill<E>(p, r, SPEC_ROW_OK, rank, C);
-            r += step;
-            en.fetch(p, r);
-        }
-    };
-    for (int i = tid; i < 2 * words; i += SC_NT) all_flags[i] = 0;
-    int r = cluster_id();
-    Entries en, en2, en3;
+    const int C = p.cluster, rank = (int)cluster_rank(), r = cluster_id(), tid = threadIdx.x, lane = tid % 32;
+    const int warp = tid / 32;
+    Entries en;
     en.fetch(p, r);
-    settle(r, en);
-    if (r >= p.rows) return;
-    if (C > 1) cluster_arrive();  // every CTA of the cluster runs before another stores into its shared memory
-    bool owed = true;             // a barrier at which this CTA arrived and has not waited
+    if (!__syncthreads_or(en.some())) {
+        no_distill<E>(p, r, SPEC_ROW_OK, rank, C);
+        return;
+    }
     const E* x = row_of<E>(p, r);
-    Slice<E> sl(p, x, rank);
-    ring.start(sl);
-    ring.copy_group();
-    uint4 edge = ring.edge(sl), edge2;
+    const Slice<E> sl(p, x, rank);
+    Ring<E> ring(p, sl, rank, smem);
     en.fetch_logits(x, p.V);
-    int r2 = r + step, par = 0, sp = 0, was = -1;
-    en2.fetch(p, r2);
-    Teacher was_te;
-    float was_l[SC_EPT];
-    EntryShared* was_es = shared;
-    auto finish_last = [&](int par) {
-        if (tid < 32) {
-            const KdRow row = join(parts[par], *was_es, p.c, C);
-            if (lane == 0) s_row = row;
-        }
-        __syncthreads();
-        finish(p, was, s_row, was_te, was_l);
-    };
-    while (true) {
-        settle(r2, en2);
-        const bool more = r2 < p.rows;
-        Slice<E> next;
-        if (more) {
-            x = row_of<E>(p, r2);
-            next = Slice<E>(p, x, rank);
-            edge2 = ring.edge(next);
-            en2.fetch_logits(x, p.V);
-        }
-        const int r3 = r2 + step;
-        en3.fetch(p, r3);
-        while (ring.ahead < SC_RING && ring.more(next)) {}
-        const float lse = p.teacher_lse ? p.teacher_lse[r] : 0.f;
-        EntryShared& es = shared[sp];
-        uint32_t *flags = all_flags + sp * words, *others = all_flags + (sp ^ 1) * words;
-        int slot[SC_EPT];
+    const uint4 edge = ring.edge();
+    const float lse = p.teacher_lse ? p.teacher_lse[r] : 0.f;
+    uint32_t* const flags = (uint32_t*)(smem + SC_RING_BYTES);
+    for (int i = tid; i < (ring.full + 2) * SC_WARPS; i += SC_NT) flags[i] = 0;
+    int slot[SC_EPT];
 #pragma unroll
-        for (int u = 0; u < SC_EPT; ++u) {
-            slot[u] = -1;
-            if (en.id[u] < sl.first || en.id[u] >= p.V || en.id[u] < 0) continue;
-            const int i = (en.id[u] - sl.first) / EPV<E>;
-            if (i >= sl.n) continue;
-            slot[u] = i >= sl.lo && i < sl.hi ? i / Ring<E>::GROUP * SC_NT + i % SC_NT
-                                              : (ring.full + 1) * SC_NT + (i < sl.lo ? 0 : 32);
-        }
-        float tmax;
-        bool first[SC_EPT];
-        bool bad = check_entries(p, es, en, slot, first, tmax, [&](int u) {
-            if (slot[u] >= 0) atomicOr(flags + slot[u] / 32, 1u << (slot[u] % 32));
-        });
-        // (all threads are past the row before)
-        for (int i = tid; i < words; i += SC_NT) others[i] = 0;
-        Teacher te;
-        begin_teacher(p, es, en, tmax, lse, te);
-        sum_entries(p, es, en);
-        bad = __syncthreads_or(bad);
-        if (bad || dull(p, tmax, lse)) {
-            no_distill<E>(p, r, bad ? SPEC_ROW_BAD_TOKEN : SPEC_ROW_NONFINITE, rank, C);
-            for (int b = 0; b <= ring.full; ++b) {
-                ring.first();
-                ring.used(next);
-            }
-            for (int i = tid; i < words; i += SC_NT) flags[i] = 0;
-        } else {
-            end_teacher(p, es, te);
-            Summer<E, false, false> rest;
-            rest.c = p.c;
-            rest.stream(
-                ring, sl, next, edge, [&](int b) { return flags[b * SC_WARPS + warp] >> lane & 1; }, [](int, float) {});
-#pragma unroll
-            for (int u = 0; u < SC_EPT; ++u) {
-                if (!first[u]) continue;
-                const int g = slot[u] / SC_NT, owner = slot[u] % SC_NT;
-                const bool end = g > ring.full;
-                uint4 w[SC_GROUP];
-                int at[SC_GROUP];
-#pragma unroll
-                for (int j = 0; j < SC_GROUP; ++j) {
-                    at[j] = end ? (owner == 0 ? 0 : sl.n - 1) : (g * SC_GROUP + j) * SC_NT + owner;
-                    w[j] = end ? (j ? no_vector<E>() : load_vector(sl, p.V, at[j]))
-                               : at[j] >= sl.lo && at[j] < sl.hi ? load_vector(sl, p.V, at[j]) : no_vector<E>();
-                }
-                uint64_t out = 0;  // the entries' elements
-                for (int j = 0; j < p.k; ++j)
-                    if (es.slots[j] == slot[u]) {
-                        const int e = es.ids[j] - sl.first;
-                        out |= (uint64_t)1 << ((end ? 0 : (e / EPV<E> - at[0]) / SC_NT) * EPV<E> + e % EPV<E>);
-                    }
-#pragma unroll
-                for (int j = 0; j < SC_GROUP; ++j) {
-                    Bits<E> v[EPV<E>];
-#pragma unroll
-                    for (int q = 0; q < EPV<E>; ++q)
-                        v[q] = out >> (j * EPV<E> + q) & 1 ? (Bits<E>)Vec<E>::NEG : bits_at<E>(w[j], q);
-                    w[j] = vector_of<E>(v);
-                }
-                rest.take(w, 0, 0);
-            }
-            Run run = rest.result();
-            KdPart w;
-            w.m = warp_max(run.m);
-            to_max(run, w.m, p.c);
-            w.s = warp_sum(run.s);
-            if (owed) row_wait(C);
-            // CTA 0 finishes a row while the next one is summed: no one waits for a barrier
-            if (was >= 0 && rank == 0) finish_last(par ^ 1);
-            if (lane == 0) {
-                const uint32_t to = remote(&parts[par][rank * SC_WARPS + warp], 0);
-                remote_st(to, __float_as_uint(w.m));
-                remote_st(to + 4, __float_as_uint(w.s));
-            }
-            row_arrive(C);
-            owed = true;
-            was = r;
-            was_te = te;
-            was_es = &es;
-#pragma unroll
-            for (int u = 0; u < SC_EPT; ++u) was_l[u] = en.l[u];
-            par ^= 1;
-        }
-        // a row's shared entries are read until it is finished, in the next good row: a bad one in between has the other's
-        if (!more) break;
-        sp = was_es == shared ? 1 : 0;
-        sl = next;
-        ring.on_next = false;
-        edge = edge2;
-        r = r2;
-        en = en2;
-        r2 = r3;
-        en2 = en3;
+    for (int u = 0; u < SC_EPT; ++u) {
+        slot[u] = -1;
+        if (en.id[u] < sl.first || en.id[u] >= p.V || en.id[u] < 0) continue;
+        const int i = (en.id[u] - sl.first) / EPV<E>;
+        if (i >= sl.n) continue;
+        slot[u] = i >= sl.lo && i < sl.hi ? i / Ring<E>::GROUP * SC_NT + i % SC_NT
+                                          : (ring.full + 1) * SC_NT + (i < sl.lo ? 0 : 32);
     }
-    if (rank == 0 && was >= 0) {
+    float tmax;
+    bool first[SC_EPT];
+    bool bad = check_entries(p, es, en, slot, first, tmax, [&](int u) {
+        if (slot[u] >= 0) atomicOr(flags + slot[u] / 32, 1u << (slot[u] % 32));
+    });
+    Teacher te;
+    begin_teacher(p, es, en, tmax, lse, te);
+    bad = __syncthreads_or(bad);
+    if (bad || dull(p, tmax, lse)) {
+        no_distill<E>(p, r, bad ? SPEC_ROW_BAD_TOKEN : SPEC_ROW_NONFINITE, rank, C);
+        copy_arrived(0);
+        return;
+    }
+    // every CTA of the cluster runs before another stores into its shared memory
+    if (C > 1) cluster_arrive();
+    Summer<E, false, false> rest;
+    rest.c = p.c;
+    rest.stream(ring, edge, [&](int b) { return flags[b * SC_WARPS + warp] >> lane & 1; }, [](int, float) {});
+#pragma unroll
+    for (int u = 0; u < SC_EPT; ++u) {
+        if (!first[u]) continue;
+        const int g = slot[u] / SC_NT, owner = slot[u] % SC_NT;
+        const bool end = g > ring.full;
+        uint4 w[SC_GROUP];
+        int at[SC_GROUP];
+#pragma unroll
+        for (int j = 0; j < SC_GROUP; ++j) {
+            at[j] = end ? (owner == 0 ? 0 : sl.n - 1) : (g * SC_GROUP + j) * SC_NT + owner;
+            w[j] = end ? (j ? no_vector<E>() : load_vector(sl, p.V, at[j]))
+                       : at[j] >= sl.lo && at[j] < sl.hi ? load_vector(sl, p.V, at[j]) : no_vector<E>();
+        }
+        uint32_t out = 0;  // the entries' elements
+        for (int j = 0; j < p.k; j += 4) {
+            const int4 o = *(const int4*)(es.slots + j);
+            auto one = [&](int s, int j) {
+                if (s != slot[u]) return;
+                const int e = es.ids[j] - sl.first;
+                out |= 1u << ((end ? 0 : (e / EPV<E> - at[0]) / SC_NT) * EPV<E> + e % EPV<E>);
+            };
+            one(o.x, j);
+            one(o.y, j + 1);
+            one(o.z, j + 2);
+            one(o.w, j + 3);
+        }
+#pragma unroll
+        for (int j = 0; j < SC_GROUP; ++j) {
+            Bits<E> v[EPV<E>];
+#pragma unroll
+            for (int q = 0; q < EPV<E>; ++q)
+                v[q] = out >> (j * EPV<E> + q) & 1 ? (Bits<E>)Vec<E>::NEG : bits_at<E>(w[j], q);
+            w[j] = vector_of<E>(v);
+        }
+        rest.take(w, 0, 0);
+    }
+    Run run = rest.result();
+    KdPart w;
+    w.m = warp_max(run.m);
+    to_max(run, w.m, p.c);
+    w.s = warp_sum(run.s);
+    if (C > 1) cluster_wait();
+    if (lane == 0) {
+        const uint32_t to = remote(parts + rank * SC_WARPS + warp, 0);
+        remote_st(to, __float_as_uint(w.m));
+        remote_st(to + 4, __float_as_uint(w.s));
+    }
+    if (rank == 0) sum_entries(p, es, en);
+    row_arrive(C);
+    if (rank != 0) return;
+    if (C > 1) {
         row_wait(C);
-        finish_last(par ^ 1);
+        __syncthreads();
     }
+    if (tid < 32) {
+        const KdRow row = join(parts, es, p.c, C);
+        if (lane == 0) s_row = row;
+    }
+    end_teacher(p, es, te);
+    __syncthreads();
+    finish(p, r, s_row, te, en.l);
 }
 
 // ---- with the gradient ------------------------------------------------------------ //
@@ -549,15 +498,15 @@ template <typename E> cudaError_t go(ScoreParams p, int num_sms, cudaStream_t s)
     static ScoreKernel sk[2];
     if (!p.grad) {
         const auto kernel = k_score_distill<E>;
-        auto smem = [](size_t per) { return SC_RING_BYTES + (per / Ring<E>::GROUP + 2) * SC_WARPS * 4 * 2; };
+        auto smem = [](size_t per) { return SC_RING_BYTES + (per / Ring<E>::GROUP + 2) * SC_WARPS * 4; };
         cudaError_t e = score_ready(kernel, sk[0], smem(SCORE_MAX_ROW_BYTES / 16 + 2));
         if (e == cudaSuccess) e = score_split_forward(kernel, sk[0], p, sizeof(E), 40, smem);
-        return e == cudaSuccess ? score_launch(kernel, sk[0], p, smem(p.per), s) : e;
+        return e == cudaSuccess ? score_launch(kernel, sk[0], p, smem(p.per), false, s) : e;
     }
     const cudaError_t e = score_ready(k_score_distill_grad<E>, sk[1], SC_MOST_SLICE);
     if (e != cudaSuccess) return e;
     score_split_gradient(p, sizeof(E), num_sms);
-    return score_launch(k_score_distill_grad<E>, sk[1], p, (size_t)p.per * 16, s);
+    return score_launch(k_score_distill_grad<E>, sk[1], p, (size_t)p.per * 16, true, s);
 }
 
 }  // namespace

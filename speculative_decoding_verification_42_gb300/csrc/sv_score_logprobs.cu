@@ -33,8 +33,8 @@ struct TopScratch {
     int32_t counts[SC_MAXC];           // CTA 0: candidates of each CTA
     int32_t mine, agains;              // candidates of this CTA, entries of `again`
     int32_t tally[2][SC_WARPS];
-    float most[1];                     // [full + 1][SC_NT]: the largest element of each thread's copy groups
-};
+    int32_t pad;
+};  // and behind it, Bits<E> [full + 1][SC_NT]: the largest element of each thread's copy groups
 
 __device__ __forceinline__ int tally_of(TopScratch& ts, int round, int x)
 {
@@ -58,7 +58,8 @@ template <typename E, typename F> __device__ __forceinline__ void each_of(const 
 // the list (equal logits), its first n in the order (key desc, id asc), found by halving the range of keys and of ids
 // and counting.
 template <typename E>
-__device__ void give_candidates(const Slice<E>& sl, int V, int full, TopScratch& ts, uint32_t bound, int n, int rank, int C)
+__device__ void give_candidates(const Slice<E>& sl, int V, int full, TopScratch& ts, const Bits<E>* most, uint32_t bound,
+                                int n, int rank, int C)
 {
     const int share = SC_LIST / C, tid = threadIdx.x;
     const uint32_t list = remote(ts.list + rank * share, 0);
@@ -71,7 +72,7 @@ __device__ void give_candidates(const Slice<E>& sl, int V, int full, TopScratch&
     };
     const float least = val_of(bound);
     for (int b = 0; b <= full; ++b)
-        if (ts.most[b * SC_NT + tid] >= least) {
+        if (value_of<E>(most[b * SC_NT + tid]) >= least) {
             const int at = atomicAdd(&ts.agains, 1);
             if (at < SC_AGAIN) ts.again[at] = b * SC_NT + tid;
         }
@@ -135,21 +136,21 @@ __device__ void give_candidates(const Slice<E>& sl, int V, int full, TopScratch&
     if (tid == 0) remote_st(remote(ts.counts + rank, 0), (uint32_t)found);
 }
 
-// the keys of this thread's vectors, 512 / C from a CTA, to all CTAs
-__device__ __forceinline__ void give_keys(TopScratch& ts, int full, int rank, int C)
+// the keys of this thread's copy groups, 512 / C from a CTA, to all CTAs
+template <typename E>
+__device__ __forceinline__ void give_keys(TopScratch& ts, const Bits<E>* most, int full, int rank, int C)
 {
-    const int tid = threadIdx.x, parts = max(1, 4 / C);
+    const int tid = threadIdx.x, parts = C == 1 ? 4 : C == 2 ? 2 : 1, per = (full + parts) / parts;
+    int b = 0;
     for (int q = 0; q < parts; ++q) {
         float m = -INFINITY;
-        for (int b = q * (full + 1) / parts; b < (q + 1) * (full + 1) / parts; ++b) m = fmaxf(m, ts.most[b * SC_NT + tid]);
+        for (const int end = min(full + 1, b + per); b < end; ++b) m = fmaxf(m, value_of<E>(most[b * SC_NT + tid]));
         uint32_t k = key_of(m);
-        int at = (rank * parts + q) * SC_NT + tid;
         if (C == 8) {
             k = max(k, __shfl_xor_sync(~0u, k, 1));
-            at = (rank * SC_NT + tid) / 2;
-            for (int i = tid % 2; i < C; i += 2) remote_st(remote(ts.keys + at, i), k);
+            for (int i = tid % 2; i < C; i += 2) remote_st(remote(ts.keys + (rank * SC_NT + tid) / 2, i), k);
         } else {
-            for (int i = 0; i < C; ++i) remote_st(remote(ts.keys + at, i), k);
+            for (int i = 0; i < C; ++i) remote_st(remote(ts.keys + (rank * parts + q) * SC_NT + tid, i), k);
         }
     }
 }
@@ -275,156 +276,97 @@ __device__ __forceinline__ void write_row(const ScoreParams& p, int r, const LpR
     if (p.lse) p.lse[r] = ok ? row.m * p.inv_temp + logz : nan;
 }
 
-template <typename E, bool TOP> __global__ void __launch_bounds__(SC_NT, 4) k_score_logprobs(const ScoreParams p)
+template <typename E, bool TOP> __global__ void __launch_bounds__(SC_NT, TOP ? 4 : 6) k_score_logprobs(const ScoreParams p)
 {
     extern __shared__ __align__(16) unsigned char smem[];
-    __shared__ LpPart parts[2][SC_PARTS];
+    __shared__ LpPart parts[SC_PARTS];
     __shared__ LpRow s_row;
-    const int C = p.cluster, rank = (int)cluster_rank(), tid = threadIdx.x, lane = tid % 32;
-    const int step = gridDim.x / C;
-    TopScratch& ts = *(TopScratch*)(smem + SC_RING_BYTES);
-    Ring<E> ring(p, rank, smem);
-    auto id_of = [&](int r) { return p.ids && r < p.rows ? p.ids[r] : 0; };
-    // the first row from r on that is scored
-    auto settle = [&](int& r, int& id) {
-        while (r < p.rows && (id < 0 || id >= p.V)) {
-            no_logprobs<E>(p, r, id == -1 ? SPEC_ROW_OK : SPEC_ROW_BAD_TOKEN, rank, C);
-            r += step;
-            id = id_of(r);
-        }
-    };
-    // a row's data that are no part of the ring
-    uint4 edge, edge2;
-    E raw, raw2;
-    bool tie = false, tie2 = false;
-    auto fetch = [&](const E* x, const Slice<E>& s, int id, E& raw, uint4& edge, bool& tie) {
-        raw = x[id];
-        edge = ring.edge(s);
-        tie = false;
-        if (p.rank && rank == 0 && tid >= 64 && tid - 64 < (int)((uintptr_t)(x + id) & 15) / (int)sizeof(E) &&
-            id - 1 - (tid - 64) >= 0)
-            tie = widen(x[id - 1 - (tid - 64)]) == widen(raw);
-    };
-    int r = cluster_id(), id = id_of(r);
-    settle(r, id);
-    if (r >= p.rows) return;
+    const int C = p.cluster, rank = (int)cluster_rank(), r = cluster_id(), tid = threadIdx.x, lane = tid % 32;
+    const int id = p.ids ? p.ids[r] : 0;
+    if (id < 0 || id >= p.V) {
+        no_logprobs<E>(p, r, id == -1 ? SPEC_ROW_OK : SPEC_ROW_BAD_TOKEN, rank, C);
+        return;
+    }
     // every CTA of the cluster runs before another stores into its shared memory
     if (C > 1) cluster_arrive();
-    bool owed = true;  // a barrier at which this CTA arrived and has not waited
     const E* x = row_of<E>(p, r);
-    Slice<E> sl(p, x, rank);
-    ring.start(sl);
-    ring.copy_group();
-    fetch(x, sl, id, raw, edge, tie);
-    int r2 = r + step, id2 = id_of(r2), par = 0, was = -1;
-    float was_x = 0.f;
-    while (true) {
-        settle(r2, id2);
-        const bool more = r2 < p.rows;
-        Slice<E> next;
-        if (more) {
-            x = row_of<E>(p, r2);
-            next = Slice<E>(p, x, rank);
-            fetch(x, next, id2, raw2, edge2, tie2);
-        }
-        const int r3 = r2 + step, id3 = id_of(r3);
-        while (ring.ahead < SC_RING && ring.more(next)) {}
-        const float xt = widen(raw);
-        int ahead = 0;
-        Run run;
-        auto none = [](int) { return false; };
-        auto seen = [&](int b, float m) {
-            if (TOP) ts.most[b * SC_NT + tid] = m;
-        };
-        if (p.rank) {
-            Summer<E, true, true> sum;
-            sum.c = p.c;
-            sum.tvec = (id - sl.first) >> (sizeof(E) == 4 ? 2 : 3);
-            sum.x = xt;
-            // a masked token: those in front are the unmasked ones
-            sum.at = Vec<E>::thr_of(xt);
-            sum.under = Vec<E>::thr_of(xt == -INFINITY ? xt : below<E>(raw));
-            sum.stream(ring, sl, next, edge, none, seen);
-            run = sum.result();
-            ahead = sum.ahead + (tie && xt > -INFINITY);
-        } else {
-            Summer<E, true, false> sum;
-            sum.c = p.c;
-            sum.stream(ring, sl, next, edge, none, seen);
-            run = sum.result();
-        }
-        // threads to warp
-        LpPart w;
-        w.m = warp_max(run.m);
-        to_max(run, w.m, p.c);
-        w.s = warp_sum(run.s);
-        w.t = warp_sum(run.t);
-        w.ahead = __reduce_add_sync(~0u, ahead);
-        if (owed) row_wait(C);
-        if (!TOP && was >= 0 && rank == 0 && tid < 32) {
-            // CTA 0 finishes a row while the next one is summed: no one waits for a barrier
-            const LpRow row = join(parts[par ^ 1], p.c, C);
-            if (lane == 0) write_row(p, was, row, was_x);
-        }
-        // warps to cluster: to CTA 0, or to all
-        if (lane < (TOP ? C : 1)) {
-            const uint32_t to = remote(&parts[par][rank * SC_WARPS + tid / 32], lane);
-            remote_st(to, __float_as_uint(w.m));
-            remote_st(to + 4, __float_as_uint(w.s));
-            remote_st(to + 8, __float_as_uint(w.t));
-            remote_st(to + 12, (uint32_t)w.ahead);
-        }
-        if (TOP) give_keys(ts, ring.full, rank, C);
-        row_arrive(C);
-        owed = true;
+    const Slice<E> sl(p, x, rank);
+    Ring<E> ring(p, sl, rank, smem);
+    const E raw = x[id];
+    const uint4 edge = ring.edge();
+    const float xt = widen(raw);
+    TopScratch& ts = *(TopScratch*)(smem + SC_RING_BYTES);
+    Bits<E>* const most = (Bits<E>*)(&ts + 1);
+    int ahead = 0;
+    Run run;
+    auto none = [](int) { return false; };
+    auto seen = [&](int b, float m) {
         if (TOP) {
-            row_wait(C);
-            owed = false;
-            if (tid < 32) {
-                LpRow row = join(parts[par], p.c, C);
-                row.bound = bound_of(ts, p.top_n);
-                if (lane == 0) {
-                    ts.mine = ts.agains = 0;
-                    s_row = row;
-                    if (rank == 0) write_row(p, r, row, xt);
-                }
-            }
-            __syncthreads();
-            const LpRow row = s_row;
-            if (finite_row(row.m)) {
-                give_candidates(sl, p.V, ring.full, ts, row.bound, p.top_n, rank, C);
-                row_arrive(C);
-                owed = true;
-                if (rank == 0) {
-                    row_wait(C);
-                    owed = false;
-                    write_top(p, r, ts, row, logf(row.s) - dist(row.m, row.m, p.c) * LN2, C);
-                }
-            } else if (rank == 0) {
-                no_top(p, r, SPEC_ROW_NONFINITE);
-            }
+            const E e = narrow<E>(m);  // exact: m is a value of E
+            most[b * SC_NT + tid] = *reinterpret_cast<const Bits<E>*>(&e);
         }
-        was = r;
-        was_x = xt;
-        par ^= 1;
-        if (!more) break;
-        sl = next;
-        ring.on_next = false;
-        raw = raw2;
-        edge = edge2;
-        tie = tie2;
-        r = r2;
-        id = id2;
-        r2 = r3;
-        id2 = id3;
+    };
+    if (p.rank) {
+        // the equal ones among the elements before x in its vector
+        if (rank == 0 && tid >= 64 && tid - 64 < (int)((uintptr_t)(x + id) & 15) / (int)sizeof(E) && tid - 64 < id)
+            ahead = widen(x[id - 1 - (tid - 64)]) == xt && xt > -INFINITY;
+        Summer<E, true, true> sum;
+        sum.c = p.c;
+        sum.x = xt;
+        sum.tvec = (id - sl.first) >> (sizeof(E) == 4 ? 2 : 3);
+        // a masked token: those in front are the unmasked ones
+        sum.at = Vec<E>::thr_of(xt);
+        sum.under = Vec<E>::thr_of(xt == -INFINITY ? xt : below<E>(raw));
+        sum.stream(ring, edge, none, seen);
+        run = sum.result();
+        ahead += sum.ahead;
+    } else {
+        Summer<E, true, false> sum;
+        sum.c = p.c;
+        sum.stream(ring, edge, none, seen);
+        run = sum.result();
     }
-    if (!TOP && rank == 0) {
-        row_wait(C);
-        if (tid < 32) {
-            const LpRow row = join(parts[par ^ 1], p.c, C);
-            if (lane == 0) write_row(p, was, row, was_x);
+    // threads to warp
+    LpPart w;
+    w.m = warp_max(run.m);
+    to_max(run, w.m, p.c);
+    w.s = warp_sum(run.s);
+    w.t = warp_sum(run.t);
+    w.ahead = __reduce_add_sync(~0u, ahead);
+    // warps to cluster: to CTA 0, or to all
+    if (C > 1) cluster_wait();
+    if (lane < (TOP ? C : 1)) {
+        const uint32_t to = remote(parts + rank * SC_WARPS + tid / 32, lane);
+        remote_st(to, __float_as_uint(w.m));
+        remote_st(to + 4, __float_as_uint(w.s));
+        remote_st(to + 8, __float_as_uint(w.t));
+        remote_st(to + 12, (uint32_t)w.ahead);
+    }
+    if (TOP) give_keys<E>(ts, most, ring.full, rank, C);
+    row_arrive(C);
+    if (!TOP && rank != 0) return;
+    row_wait(C);
+    if (tid < 32) {
+        LpRow row = join(parts, p.c, C);
+        if (TOP) row.bound = bound_of(ts, p.top_n);
+        if (lane == 0) {
+            if (rank == 0) write_row(p, r, row, xt);
+            if (TOP) ts.mine = ts.agains = 0;
+            s_row = row;
         }
     }
+    if (!TOP) return;
+    __syncthreads();
+    const LpRow row = s_row;
+    if (!finite_row(row.m)) {
+        if (rank == 0) no_top(p, r, SPEC_ROW_NONFINITE);
+        return;
+    }
+    give_candidates(sl, p.V, ring.full, ts, most, row.bound, p.top_n, rank, C);
+    row_arrive(C);
+    if (rank != 0) return;
+    row_wait(C);
+    write_top(p, r, ts, row, logf(row.s) - dist(row.m, row.m, p.c) * LN2, C);
 }
 
 template <typename E> __global__ void __launch_bounds__(SC_NT) k_score_logprobs_grad(const ScoreParams p)
@@ -528,11 +470,11 @@ template <typename E, bool TOP> cudaError_t go_forward(ScoreParams p, cudaStream
     static ScoreKernel sk;
     const auto kernel = k_score_logprobs<E, TOP>;
     auto smem = [](size_t per) {
-        return SC_RING_BYTES + (TOP ? sizeof(TopScratch) + (per / Ring<E>::GROUP + 2) * SC_NT * 4 : 0);
+        return SC_RING_BYTES + (TOP ? sizeof(TopScratch) + (per / Ring<E>::GROUP + 2) * SC_NT * sizeof(E) : 0);
     };
     cudaError_t e = score_ready(kernel, sk, smem(SCORE_MAX_ROW_BYTES / 16 + 2));
     if (e == cudaSuccess) e = score_split_forward(kernel, sk, p, sizeof(E), TOP ? 48 : 16, smem);
-    return e == cudaSuccess ? score_launch(kernel, sk, p, smem(p.per), s) : e;
+    return e == cudaSuccess ? score_launch(kernel, sk, p, smem(p.per), false, s) : e;
 }
 template <typename E> cudaError_t go(ScoreParams p, int num_sms, cudaStream_t s)
 {
@@ -549,7 +491,7 @@ template <typename E> cudaError_t go(ScoreParams p, int num_sms, cudaStream_t s)
     const cudaError_t e = score_ready(k_score_logprobs_grad<E>, sk, SC_MOST_SLICE);
     if (e != cudaSuccess) return e;
     score_split_gradient(p, sizeof(E), num_sms);
-    return score_launch(k_score_logprobs_grad<E>, sk, p, (size_t)p.per * 16, s);
+    return score_launch(k_score_logprobs_grad<E>, sk, p, (size_t)p.per * 16, true, s);
 }
 
 }  // namespace

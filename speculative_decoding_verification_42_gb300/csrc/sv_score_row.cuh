@@ -2,16 +2,18 @@
 // rows of logits: vectors of elements, slices of rows and their copies, running
 // softmax sums, gradients, and the join of a cluster's warps.
 //
-// A row is taken by a cluster of 1 to 8 CTAs, a slice each.  Clusters are
-// persistent and take every nc-th row.  A thread copies the vectors that it will
-// read itself (cp.async), so that no barrier lies between a copy and its use,
-// and a row's barriers and its end pass while the next row is on its way:
+// A row is taken by a cluster of 1 to 8 CTAs, a slice each.  A thread copies the
+// vectors that it will read itself (cp.async), so that no barrier lies between a
+// copy and its use.
 //
 //   forward    a ring of copy groups (Ring): what a thread has used makes room
-//              for what comes, of this row or the next
-//   gradient   the slice stays in shared memory, as the row's sum comes before
-//              the gradient's first element; a vector's place goes to the next
-//              row's once its gradient is written (Buffer)
+//              for what comes.  One cluster per row: four or more CTAs share an
+//              SM, and two that stream keep HBM busy while others begin or end.
+//   gradient   the slice stays in shared memory (Buffer), as the row's sum comes
+//              before the gradient's first element.  Clusters are persistent
+//              and take every nc-th row: a vector's place goes to the next row's
+//              once its gradient is written, so that a row's barriers pass while
+//              the next one is on its way.
 //
 // Slices are whole 16-byte vectors of the row's addresses, so rows of any
 // alignment are copied and read alike; what a row's first and last vector have
@@ -365,25 +367,19 @@ __device__ __forceinline__ void copy_arrived(int left)
 // thread 32 has the last, thread 0 the first, in registers (edge).
 template <typename E> struct Ring {
     static constexpr int GROUP = SC_NT * SC_GROUP;  // vectors
+    const Slice<E>& s;
     uint4* buf;
     int V, full;
-    // the next group to be copied: group cb of cs, into place `to`; on_next: cs is the next row's
-    Slice<E> cs;
-    const char* src;          // this thread's first vector of it
-    int cb, to, from, ahead;  // ahead: groups copied or on their way and not used
-    bool on_next;
+    const char* src;   // this thread's first vector of the next group to be copied,
+    int cb, to, from;  // that group and its place; the place of the next to be used
 
-    __device__ __forceinline__ Ring(const ScoreParams& p, int rank, void* smem)
-        : buf((uint4*)smem + threadIdx.x), V(p.V), to(0), from(0), ahead(0), on_next(false)
+    __device__ __forceinline__ Ring(const ScoreParams& p, const Slice<E>& sl, int rank, void* smem)
+        : s(sl), buf((uint4*)smem + threadIdx.x), V(p.V), src(sl.src + threadIdx.x * 16), cb(0), to(0), from(0)
     {
         const int least = (p.V * (int)sizeof(E) + 15) / 16 - rank * p.per;
         full = max(0, min(p.per, least) - 1) / GROUP;
-    }
-    __device__ __forceinline__ void start(const Slice<E>& s)
-    {
-        cs = s;
-        cb = 0;
-        src = s.src + threadIdx.x * 16;
+#pragma unroll
+        for (int i = 0; i < SC_RING; ++i) copy_group();
     }
     __device__ __forceinline__ void copy_group()
     {
@@ -391,58 +387,43 @@ template <typename E> struct Ring {
         const uint32_t dst = (uint32_t)__cvta_generic_to_shared(place);
         if (cb < full) {
             // whole vectors, but the first of the row
-            if (cb > 0 || threadIdx.x >= cs.lo) copy16(dst, src);
+            if (cb > 0 || threadIdx.x >= s.lo) copy16(dst, src);
             else *place = no_vector<E>();
 #pragma unroll
             for (int j = 1; j < SC_GROUP; ++j) copy16(dst + j * SC_NT * 16, src + j * SC_NT * 16);
-        } else {
+        } else if (cb == full) {
             const int i0 = cb * GROUP + threadIdx.x;
 #pragma unroll
             for (int j = 0; j < SC_GROUP; ++j) {
                 const int i = i0 + j * SC_NT;
-                if (i >= cs.lo && i < cs.hi) copy16(dst + j * SC_NT * 16, src + j * SC_NT * 16);
-                else if (i < cs.lo) place[j * SC_NT] = no_vector<E>();
+                if (i >= s.lo && i < s.hi) copy16(dst + j * SC_NT * 16, src + j * SC_NT * 16);
+                else if (i < s.lo) place[j * SC_NT] = no_vector<E>();
             }
         }
-        copy_commit();
+        copy_commit();  // (behind the last group, groups of nothing: the waits below count them)
         src += GROUP * 16;
         to = to + GROUP == SC_RING * GROUP ? 0 : to + GROUP;
         ++cb;
-        ++ahead;
-    }
-    // copies one group more, if there is one: of the row, or of the next
-    __device__ __forceinline__ bool more(const Slice<E>& next)
-    {
-        if (cb > full) {
-            if (on_next || !next.src) return false;
-            on_next = true;
-            start(next);
-        }
-        copy_group();
-        return true;
     }
     // the oldest group has arrived; this thread's first vector of it
-    __device__ __forceinline__ const uint4* first()
+    __device__ __forceinline__ const uint4* first() const
     {
-        if (ahead == SC_RING) asm volatile("cp.async.wait_group %0;" ::"n"(SC_RING - 1) : "memory");
-        else copy_arrived(ahead - 1);
+        asm volatile("cp.async.wait_group %0;" ::"n"(SC_RING - 1) : "memory");
         return buf + from;
     }
-    __device__ __forceinline__ void used(const Slice<E>& next)
+    __device__ __forceinline__ void used()
     {
         from = from + GROUP == SC_RING * GROUP ? 0 : from + GROUP;
-        --ahead;
-        if (cb <= full) copy_group();
-        else more(next);
+        copy_group();
     }
-    __device__ __forceinline__ bool has_edge(const Slice<E>& s) const
+    __device__ __forceinline__ bool has_edge() const
     {
         return (threadIdx.x == 0 && s.lo && s.n) || (threadIdx.x == 32 && s.hi < s.n);
     }
-    __device__ __forceinline__ int edge_at(const Slice<E>& s) const { return threadIdx.x == 0 ? 0 : s.n - 1; }
-    __device__ __forceinline__ uint4 edge(const Slice<E>& s) const
+    __device__ __forceinline__ int edge_at() const { return threadIdx.x == 0 ? 0 : s.n - 1; }
+    __device__ __forceinline__ uint4 edge() const
     {
-        return has_edge(s) ? part_vector(s, V, edge_at(s)) : no_vector<E>();
+        return has_edge() ? part_vector(s, V, edge_at()) : no_vector<E>();
     }
 };
 
@@ -613,10 +594,10 @@ template <typename E, bool ENTROPY, bool RANK> struct Summer {
     // A slice in the ring, and its edge.  skip(b): this thread leaves out its vectors of group b (full + 1: the edge);
     // seen(b, x): their largest element.
     template <typename Skip, typename Seen>
-    __device__ __forceinline__ void stream(Ring<E>& ring, const Slice<E>& s, const Slice<E>& next, const uint4& edge,
-                                          Skip skip, Seen seen)
+    __device__ __forceinline__ void stream(Ring<E>& ring, const uint4& edge, Skip skip, Seen seen)
     {
         int i = threadIdx.x;
+#pragma unroll 1
         for (int b = 0; b < ring.full; ++b, i += Ring<E>::GROUP) {
             const uint4* v = ring.first();
             uint4 w[SC_GROUP];
@@ -627,19 +608,19 @@ template <typename E, bool ENTROPY, bool RANK> struct Summer {
                 for (int j = 0; j < SC_GROUP; ++j) w[j] = no_vector<E>();
             }
             seen(b, take(w, i, b));
-            ring.used(next);
+            ring.used();
         }
         const uint4* v = ring.first();
         float mx = -INFINITY;
         const bool left_out = skip(ring.full);
-        for (; i < s.hi; i += SC_NT, v += SC_NT) {
+#pragma unroll 1
+        for (; i < ring.s.hi; i += SC_NT, v += SC_NT) {
             const uint4 w[1] = {left_out ? no_vector<E>() : *v};
             mx = fmax_nan(mx, take(w, i, ring.full));
         }
-        ring.used(next);
-        if (ring.has_edge(s) && !skip(ring.full + 1)) {
+        if (ring.has_edge() && !skip(ring.full + 1)) {
             const uint4 w[1] = {edge};
-            mx = fmax_nan(mx, take(w, ring.edge_at(s), ring.full));
+            mx = fmax_nan(mx, take(w, ring.edge_at(), ring.full));
         }
         seen(ring.full, mx);
     }
@@ -840,19 +821,17 @@ template <typename K> cudaError_t score_resident(K kernel, ScoreKernel& sk, int 
     return cudaSuccess;
 }
 
-// Launches persistent clusters of p.cluster CTAs with `smem` bytes each: as many as fit the GPU at once, since one more
-// would wait for another's last row.
+// Launches clusters of p.cluster CTAs with `smem` bytes each: one per row, or persistent ones, as many as fit the GPU at
+// once, since one more would wait for another's last row.
 template <typename K>
-cudaError_t score_launch(K kernel, ScoreKernel& sk, ScoreParams& p, size_t smem, cudaStream_t s)
+cudaError_t score_launch(K kernel, ScoreKernel& sk, ScoreParams& p, size_t smem, bool persistent, cudaStream_t s)
 {
     const int C = p.cluster;
-    int nc = 0;
-    const cudaError_t e = score_resident(kernel, sk, C, smem, &nc);
-    if (e != cudaSuccess) return e;
-    p.by_tokens = FastDiv(p.T);
-    if (nc >= p.rows) {
-        nc = p.rows;
-    } else {
+    int nc = p.rows;
+    if (persistent) {
+        const cudaError_t e = score_resident(kernel, sk, C, smem, &nc);
+        if (e != cudaSuccess) return e;
+        nc = nc < p.rows ? nc : p.rows;
         // a stride that shares no factor with the positions of a sequence: each cluster meets all of them alike,
         // the ends of ragged sequences, which cost nothing, among them
         auto gcd = [](int a, int b) {
@@ -863,8 +842,9 @@ cudaError_t score_launch(K kernel, ScoreKernel& sk, ScoreParams& p, size_t smem,
             }
             return a;
         };
-        while (nc > 1 && gcd(nc, p.T) > 1) --nc;
+        while (nc > 1 && nc < p.rows && gcd(nc, p.T) > 1) --nc;
     }
+    p.by_tokens = FastDiv(p.T);
     ScoreLaunch l(C, smem, s);
     l.cfg.gridDim = dim3((unsigned)nc * C);
     return cudaLaunchKernelEx(&l.cfg, kernel, p);
@@ -873,8 +853,9 @@ cudaError_t score_launch(K kernel, ScoreKernel& sk, ScoreParams& p, size_t smem,
 // vectors of a row, at any alignment
 inline int score_vectors(const ScoreParams& p, size_t size) { return (int)(((size_t)p.V * size + 30) / 16); }
 
-// CTAs of a row in a forward pass, by the time that each power of two would take: rounds of rows, each of a slice's
-// vectors and a cost that does not shrink with it (`fixed`, in vectors of a thread).  smem_of: bytes for a slice.
+// CTAs of a row in a forward pass, by the time that each power of two would take: the rows that a resident cluster has
+// one after another (and half a row for those that end last), each of a slice's vectors and a cost that does not shrink
+// with it (`fixed`, in vectors of a thread).  smem_of: bytes for a slice.
 template <typename K, typename F>
 cudaError_t score_split_forward(K kernel, ScoreKernel& sk, ScoreParams& p, size_t size, int fixed, F smem_of)
 {
@@ -885,7 +866,7 @@ cudaError_t score_split_forward(K kernel, ScoreKernel& sk, ScoreParams& p, size_
         int nc = 0;
         const cudaError_t e = score_resident(kernel, sk, C, smem_of(per), &nc);
         if (e != cudaSuccess) return e;
-        const double cost = (double)((p.rows + nc - 1) / nc) * ((double)per / SC_NT + fixed);
+        const double rounds = p.rows <= nc ? 1.0 : (double)p.rows / nc + 0.5, cost = rounds * ((double)per / SC_NT + fixed);
         if (C > 1 && cost >= best) continue;
         best = cost;
         p.cluster = C;
