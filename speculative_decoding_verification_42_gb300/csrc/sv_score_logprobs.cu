@@ -32,7 +32,7 @@ struct TopScratch {
     uint32_t again[SC_AGAIN];          // copy group * SC_NT + thread
     int32_t counts[SC_MAXC];           // CTA 0: candidates of each CTA
     int32_t mine, agains;              // candidates of this CTA, entries of `again`
-    int32_t tally[2][SC_WARPS];
+    int32_t tally[2][(SC_NT / 32)];
     int32_t pad;
 };  // and behind it, Bits<E> [full + 1][SC_NT]: the largest element of each thread's copy groups
 
@@ -44,7 +44,7 @@ __device__ __forceinline__ int tally_of(TopScratch& ts, int round, int x)
     __syncthreads();
     int n = 0;
 #pragma unroll
-    for (int i = 0; i < SC_WARPS; ++i) n += ts.tally[round & 1][i];
+    for (int i = 0; i < (SC_NT / 32); ++i) n += ts.tally[round & 1][i];
     return n;
 }
 
@@ -230,7 +230,7 @@ __device__ __forceinline__ void no_top(const ScoreParams& p, int r, int status)
 }
 
 // a row that is not scored, or has a bad token
-template <typename E> __device__ void no_logprobs(const ScoreParams& p, int r, int status, int rank, int C)
+template <typename E, int NT> __device__ void no_logprobs(const ScoreParams& p, int r, int status, int rank, int C)
 {
     if (rank == 0) {
         const float none = status == SPEC_ROW_OK ? 0.f : __int_as_float(0x7FFFFFFF);
@@ -243,23 +243,25 @@ template <typename E> __device__ void no_logprobs(const ScoreParams& p, int r, i
         }
         no_top(p, r, status);
     }
-    if (p.grad) zero_grad<E>(p, r, rank, C);
+    if (p.grad) zero_grad<E, NT>(p, r, rank, C);
 }
 
-// one warp: the row of its warps' parts
-__device__ __forceinline__ LpRow join(const LpPart* parts, float c, int C)
+// one warp: the row of the parts of n warps
+__device__ __forceinline__ LpRow join(const LpPart* parts, float c, int n)
 {
-    const int lane = threadIdx.x % 32;
-    LpPart q = {-INFINITY, 0.f, 0.f, 0};
-    if (lane < C * SC_WARPS) q = parts[lane];
-    Run u = {q.m, q.s, q.t};
-    LpRow row;
-    row.m = warp_max(u.m);
-    to_max(u, row.m, c);
-    row.s = warp_sum(u.s);
-    row.t = warp_sum(u.t);
-    row.ahead = __reduce_add_sync(~0u, q.ahead);
-    row.bound = 0;
+    LpRow row = {-INFINITY, 0.f, 0.f, 0, 0};
+    for (int i = threadIdx.x % 32; i < n; i += 32) row.m = fmax_nan(row.m, parts[i].m);
+    row.m = warp_max(row.m);
+    for (int i = threadIdx.x % 32; i < n; i += 32) {
+        Run u = {parts[i].m, parts[i].s, parts[i].t};
+        to_max(u, row.m, c);
+        row.s += u.s;
+        row.t += u.t;
+        row.ahead += parts[i].ahead;
+    }
+    row.s = warp_sum(row.s);
+    row.t = warp_sum(row.t);
+    row.ahead = __reduce_add_sync(~0u, row.ahead);
     return row;
 }
 __device__ __forceinline__ bool finite_row(float m) { return m > -INFINITY && m < INFINITY; }
@@ -279,23 +281,23 @@ __device__ __forceinline__ void write_row(const ScoreParams& p, int r, const LpR
 template <typename E, bool TOP> __global__ void __launch_bounds__(SC_NT, TOP ? 4 : 6) k_score_logprobs(const ScoreParams p)
 {
     extern __shared__ __align__(16) unsigned char smem[];
-    __shared__ LpPart parts[SC_PARTS];
+    __shared__ LpPart parts[SC_MAXC * (SC_NT / 32)];
     __shared__ LpRow s_row;
     const int C = p.cluster, rank = (int)cluster_rank(), r = cluster_id(), tid = threadIdx.x, lane = tid % 32;
     const int id = p.ids ? p.ids[r] : 0;
     if (id < 0 || id >= p.V) {
-        no_logprobs<E>(p, r, id == -1 ? SPEC_ROW_OK : SPEC_ROW_BAD_TOKEN, rank, C);
+        no_logprobs<E, SC_NT>(p, r, id == -1 ? SPEC_ROW_OK : SPEC_ROW_BAD_TOKEN, rank, C);
         return;
     }
     // every CTA of the cluster runs before another stores into its shared memory
     if (C > 1) cluster_arrive();
     const E* x = row_of<E>(p, r);
     const Slice<E> sl(p, x, rank);
-    Ring<E> ring(p, sl, rank, smem);
+    Ring<E, SC_NT, false> ring(p, sl, rank, smem);
     const E raw = x[id];
     const uint4 edge = ring.edge();
     const float xt = widen(raw);
-    TopScratch& ts = *(TopScratch*)(smem + SC_RING_BYTES);
+    TopScratch& ts = *(TopScratch*)(smem + RING_BYTES<SC_NT>);
     Bits<E>* const most = (Bits<E>*)(&ts + 1);
     int ahead = 0;
     Run run;
@@ -336,7 +338,7 @@ template <typename E, bool TOP> __global__ void __launch_bounds__(SC_NT, TOP ? 4
     // warps to cluster: to CTA 0, or to all
     if (C > 1) cluster_wait();
     if (lane < (TOP ? C : 1)) {
-        const uint32_t to = remote(parts + rank * SC_WARPS + tid / 32, lane);
+        const uint32_t to = remote(parts + rank * (SC_NT / 32) + tid / 32, lane);
         remote_st(to, __float_as_uint(w.m));
         remote_st(to + 4, __float_as_uint(w.s));
         remote_st(to + 8, __float_as_uint(w.t));
@@ -347,7 +349,7 @@ template <typename E, bool TOP> __global__ void __launch_bounds__(SC_NT, TOP ? 4
     if (!TOP && rank != 0) return;
     row_wait(C);
     if (tid < 32) {
-        LpRow row = join(parts, p.c, C);
+        LpRow row = join(parts, p.c, C * (SC_NT / 32));
         if (TOP) row.bound = bound_of(ts, p.top_n);
         if (lane == 0) {
             if (rank == 0) write_row(p, r, row, xt);
@@ -369,99 +371,74 @@ template <typename E, bool TOP> __global__ void __launch_bounds__(SC_NT, TOP ? 4
     write_top(p, r, ts, row, logf(row.s) - dist(row.m, row.m, p.c) * LN2, C);
 }
 
-template <typename E> __global__ void __launch_bounds__(SC_NT) k_score_logprobs_grad(const ScoreParams p)
+template <typename E> __global__ void __launch_bounds__(SC_NT_GRAD, 2) k_score_logprobs_grad(const ScoreParams p)
 {
+    constexpr int NT = SC_NT_GRAD, W = NT / 32;
     extern __shared__ __align__(16) unsigned char smem[];
-    __shared__ LpPart parts[2][SC_PARTS];
+    __shared__ LpPart parts[SC_MAXC * W];
     __shared__ LpRow s_row;
-    const int C = p.cluster, rank = (int)cluster_rank(), tid = threadIdx.x, lane = tid % 32;
-    const int step = gridDim.x / C;
-    const Buffer<E> bf(p, rank, smem);
-    auto id_of = [&](int r) { return p.ids && r < p.rows ? p.ids[r] : 0; };
-    auto settle = [&](int& r, int& id) {
-        while (r < p.rows && (id < 0 || id >= p.V)) {
-            no_logprobs<E>(p, r, id == -1 ? SPEC_ROW_OK : SPEC_ROW_BAD_TOKEN, rank, C);
-            r += step;
-            id = id_of(r);
-        }
-    };
-    int r = cluster_id(), id = id_of(r);
-    settle(r, id);
-    if (r >= p.rows) return;
-    if (C > 1) cluster_arrive();  // every CTA of the cluster runs before another stores into its shared memory
-    bool started = false;
+    const int C = p.cluster, rank = (int)cluster_rank(), r = cluster_id(), tid = threadIdx.x, lane = tid % 32;
+    const int id = p.ids ? p.ids[r] : 0;
+    if (id < 0 || id >= p.V) {
+        no_logprobs<E, NT>(p, r, id == -1 ? SPEC_ROW_OK : SPEC_ROW_BAD_TOKEN, rank, C);
+        return;
+    }
+    // every CTA of the cluster runs before another stores into its shared memory
+    if (C > 1) cluster_arrive();
     const E* x = row_of<E>(p, r);
-    Slice<E> sl(p, x, rank);
-    bf.copy(sl);
-    E raw = x[id], raw2 = raw;
-    int r2 = r + step, id2 = id_of(r2), par = 0;
-    while (true) {
-        settle(r2, id2);
-        const bool more = r2 < p.rows;
-        Slice<E> next;
-        if (more) {
-            x = row_of<E>(p, r2);
-            next = Slice<E>(p, x, rank);
-            raw2 = x[id2];
+    const Slice<E> sl(p, x, rank);
+    Ring<E, NT, true> ring(p, sl, rank, smem);
+    const float xt = widen(x[id]);
+    const uint4 edge = ring.edge();
+    Summer<E, true, false> sum;
+    sum.c = p.c;
+    sum.stream(ring, edge, [](int) { return false; }, [](int, float) {});
+    Run run = sum.result();
+    LpPart w;
+    w.m = warp_max(run.m);
+    to_max(run, w.m, p.c);
+    w.s = warp_sum(run.s);
+    w.t = warp_sum(run.t);
+    if (C > 1) cluster_wait();
+    if (lane < C) {
+        const uint32_t to = remote(parts + rank * W + tid / 32, lane);
+        remote_st(to, __float_as_uint(w.m));
+        remote_st(to + 4, __float_as_uint(w.s));
+        remote_st(to + 8, __float_as_uint(w.t));
+        remote_st(to + 12, 0u);
+    }
+    row_arrive(C);
+    row_wait(C);
+    if (tid < 32) {
+        const LpRow row = join(parts, p.c, C * W);
+        if (lane == 0) {
+            s_row = row;
+            if (rank == 0) write_row(p, r, row, xt);
         }
-        const int r3 = r2 + step, id3 = id_of(r3);
-        const float xt = widen(raw);
-        Summer<E, true, false> sum;
-        sum.c = p.c;
-        Run run = sum.template run<true>(bf, sl);
-        LpPart w;
-        w.m = warp_max(run.m);
-        to_max(run, w.m, p.c);
-        w.s = warp_sum(run.s);
-        w.t = warp_sum(run.t);
-        if (!started) row_wait(C);
-        started = true;
-        if (lane < C) {
-            const uint32_t to = remote(&parts[par][rank * SC_WARPS + tid / 32], lane);
-            remote_st(to, __float_as_uint(w.m));
-            remote_st(to + 4, __float_as_uint(w.s));
-            remote_st(to + 8, __float_as_uint(w.t));
-            remote_st(to + 12, 0u);
-        }
-        row_arrive(C);
-        row_wait(C);
-        if (tid < 32) {
-            const LpRow row = join(parts[par], p.c, C);
-            if (lane == 0) s_row = row;
-        }
+    }
+    __syncthreads();
+    const LpRow row = s_row;
+    if (!finite_row(row.m)) {
+        copy_done();
+        zero_grad<E, NT>(p, r, rank, C);
+        return;
+    }
+    // e (A + B d), e = 2^d: p = e / s, ln p = d ln 2 - ln s
+    const float gl = p.g_logprob ? p.g_logprob[r] : 0.f, gh = p.g_entropy ? p.g_entropy[r] : 0.f;
+    const float f = p.inv_temp / row.s, A = -(gl - gh * LN2 * (row.t / row.s)) * f, B = -gh * LN2 * f;
+    const uint64_t A2 = pair(A, A), B2 = pair(B, B);
+    E* g = grad_of<E>(p, r);
+    if (p.g_entropy)
+        grad_slice(ring, edge, g, row.m, p.c, sum.masked,
+                   [&](uint64_t d2, uint64_t e2) { return mul2(e2, fma2(B2, d2, A2)); });
+    else
+        grad_slice(ring, edge, g, row.m, p.c, 0, [&](uint64_t, uint64_t e2) { return mul2(e2, A2); });
+    if (p.g_logprob && ring.has(id)) {
         __syncthreads();
-        const LpRow row = s_row;
-        if (rank == 0 && tid == 0) write_row(p, r, row, xt);
-        if (finite_row(row.m)) {
-            // e (A + B d), e = 2^d: p = e / s, ln p = d ln 2 - ln s
-            const float gl = p.g_logprob ? p.g_logprob[r] : 0.f, gh = p.g_entropy ? p.g_entropy[r] : 0.f;
-            const float f = p.inv_temp / row.s, A = -(gl - gh * LN2 * (row.t / row.s)) * f, B = -gh * LN2 * f;
-            const uint64_t A2 = pair(A, A), B2 = pair(B, B);
-            E* g = grad_of<E>(p, r);
-            if (p.g_entropy)
-                grad_slice(bf, sl, next, g, row.m, p.c, sum.masked,
-                           [&](uint64_t d2, uint64_t e2) { return mul2(e2, fma2(B2, d2, A2)); });
-            else
-                grad_slice(bf, sl, next, g, row.m, p.c, 0, [&](uint64_t, uint64_t e2) { return mul2(e2, A2); });
-            if (p.g_logprob && bf.has(sl, id)) {
-                __syncthreads();
-                if (tid == 0) {
-                    const float d = dist(xt, row.m, p.c), e = ex2_fast(d);
-                    g[id] = narrow<E>(gl * p.inv_temp + e * (A + B * fmaxf(d, NONE)));
-                }
-            }
-        } else {
-            bf.copy(next);
-            zero_grad<E>(p, r, rank, C);
+        if (tid == 0) {
+            const float d = dist(xt, row.m, p.c), e = ex2_fast(d);
+            g[id] = narrow<E>(gl * p.inv_temp + e * (A + B * fmaxf(d, NONE)));
         }
-        par ^= 1;
-        if (!more) break;
-        sl = next;
-        raw = raw2;
-        r = r2;
-        id = id2;
-        r2 = r3;
-        id2 = id3;
     }
 }
 
@@ -470,11 +447,11 @@ template <typename E, bool TOP> cudaError_t go_forward(ScoreParams p, cudaStream
     static ScoreKernel sk;
     const auto kernel = k_score_logprobs<E, TOP>;
     auto smem = [](size_t per) {
-        return SC_RING_BYTES + (TOP ? sizeof(TopScratch) + (per / Ring<E>::GROUP + 2) * SC_NT * sizeof(E) : 0);
+        return RING_BYTES<SC_NT> + (TOP ? sizeof(TopScratch) + (per / (SC_NT * SC_GROUP) + 2) * SC_NT * sizeof(E) : 0);
     };
     cudaError_t e = score_ready(kernel, sk, smem(SCORE_MAX_ROW_BYTES / 16 + 2));
     if (e == cudaSuccess) e = score_split_forward(kernel, sk, p, sizeof(E), TOP ? 48 : 16, smem);
-    return e == cudaSuccess ? score_launch(kernel, sk, p, smem(p.per), false, s) : e;
+    return e == cudaSuccess ? score_launch(kernel, p, SC_NT, smem(p.per), s) : e;
 }
 template <typename E> cudaError_t go(ScoreParams p, int num_sms, cudaStream_t s)
 {
@@ -488,10 +465,10 @@ template <typename E> cudaError_t go(ScoreParams p, int num_sms, cudaStream_t s)
         p.rank = nullptr;
     }
     static ScoreKernel sk;
-    const cudaError_t e = score_ready(k_score_logprobs_grad<E>, sk, SC_MOST_SLICE);
+    const cudaError_t e = score_ready(k_score_logprobs_grad<E>, sk, SC_GRAD_BYTES);
     if (e != cudaSuccess) return e;
     score_split_gradient(p, sizeof(E), num_sms);
-    return score_launch(k_score_logprobs_grad<E>, sk, p, (size_t)p.per * 16, true, s);
+    return score_launch(k_score_logprobs_grad<E>, p, SC_NT_GRAD, SC_GRAD_BYTES, s);
 }
 
 }  // namespace

@@ -4,16 +4,14 @@
 //
 // A row is taken by a cluster of 1 to 8 CTAs, a slice each.  A thread copies the
 // vectors that it will read itself (cp.async), so that no barrier lies between a
-// copy and its use.
+// copy and its use: a ring of copy groups, where what it has used makes room for
+// what comes.
 //
-//   forward    a ring of copy groups (Ring): what a thread has used makes room
-//              for what comes.  One cluster per row: four or more CTAs share an
-//              SM, and two that stream keep HBM busy while others begin or end.
-//   gradient   the slice stays in shared memory (Buffer), as the row's sum comes
-//              before the gradient's first element.  Clusters are persistent
-//              and take every nc-th row: a vector's place goes to the next row's
-//              once its gradient is written, so that a row's barriers pass while
-//              the next one is on its way.
+//   forward    one cluster per row: four or more CTAs share an SM, and two that
+//              stream keep HBM busy while others begin or end
+//   gradient   the row's sum comes before the gradient's first element, so the
+//              row is streamed twice, the second time from L2, which is told
+//              to keep it until then: as many rows are under way as L2 holds
 //
 // Slices are whole 16-byte vectors of the row's addresses, so rows of any
 // alignment are copied and read alike; what a row's first and last vector have
@@ -29,16 +27,13 @@ namespace sv {
 
 namespace {
 
-constexpr int SC_NT = 128;               // threads of a CTA
-constexpr int SC_WARPS = SC_NT / 32;
-constexpr int SC_BATCH = 4;              // vectors of a thread per copy group (gradient)
-constexpr int SC_GROUP = 4;              // and of the forward passes' ring
-constexpr int SC_RING = 4;               // groups of the ring
-constexpr int SC_RING_BYTES = SC_RING * SC_GROUP * SC_NT * 16;
+constexpr int SC_NT = 128;               // threads of a CTA in the forward passes,
+constexpr int SC_NT_GRAD = 256;          // and with a gradient
+constexpr int SC_GROUP = 4;              // vectors of a thread in a copy group
+constexpr int SC_RING = 4;               // groups of a ring
 constexpr int SC_MAXC = SCORE_MAX_CTAS;  // CTAs of a cluster (portable)
-constexpr int SC_PARTS = SC_MAXC * SC_WARPS;  // warps of a cluster: one lane each where they are joined
+template <int NT> constexpr int RING_BYTES = SC_RING * SC_GROUP * NT * 16;
 constexpr float LN2 = 0.693147180559945f;
-constexpr double LN2_D = 0.69314718055994530942;
 constexpr float NONE = -200.f;  // a power of 2 that is 0 in fp32; products with it are, too, and with -inf are not
 
 // ---- elements and vectors of 16 bytes ------------------------------------- //
@@ -341,69 +336,96 @@ template <typename E> __device__ __forceinline__ uint4 load_vector(const Slice<E
     if (i >= s.lo && i < s.hi) return *(const uint4*)(s.src + (int64_t)i * 16);
     return i >= 0 && i < s.n ? part_vector(s, V, i) : no_vector<E>();
 }
-__device__ __forceinline__ void copy16(uint32_t to, const char* from)
+template <int OFF> __device__ __forceinline__ void copy16(uint32_t to, const char* from)
 {
-    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+    asm volatile("cp.async.cg.shared.global.L2::128B [%0+%2], [%1+%2], 16;" ::"r"(to), "l"(from), "n"(OFF) : "memory");
+}
+template <int OFF> __device__ __forceinline__ void copy16(uint32_t to, const char* from, uint64_t policy)
+{
+    asm volatile("cp.async.cg.shared.global.L2::cache_hint.L2::128B [%0+%2], [%1+%2], 16, %3;" ::"r"(to), "l"(from),
+                 "n"(OFF), "l"(policy)
+                 : "memory");
 }
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-// this thread's copies but those of the last `left` groups have arrived (of these, some may have, too)
-__device__ __forceinline__ void copy_arrived(int left)
+__device__ __forceinline__ void copy_done() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
+// what L2 is told of a line: to keep it, or that it is not needed again
+__device__ __forceinline__ uint64_t policy_keep()
 {
-    switch (left) {
-    case 0: asm volatile("cp.async.wait_group 0;" ::: "memory"); break;
-    case 1: asm volatile("cp.async.wait_group 1;" ::: "memory"); break;
-    case 2: asm volatile("cp.async.wait_group 2;" ::: "memory"); break;
-    case 3: asm volatile("cp.async.wait_group 3;" ::: "memory"); break;
-    case 4: asm volatile("cp.async.wait_group 4;" ::: "memory"); break;
-    case 5: asm volatile("cp.async.wait_group 5;" ::: "memory"); break;
-    case 6: asm volatile("cp.async.wait_group 6;" ::: "memory"); break;
-    default: asm volatile("cp.async.wait_group 7;" ::: "memory"); break;
-    }
+    uint64_t p;
+    asm volatile("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(p));
+    return p;
+}
+__device__ __forceinline__ uint64_t policy_drop()
+{
+    uint64_t p;
+    asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+    return p;
+}
+template <int OFF> __device__ __forceinline__ void store16(void* to, const uint4& w, uint64_t policy)
+{
+    asm volatile("st.global.L2::cache_hint.v4.b32 [%0+%1], {%2, %3, %4, %5}, %6;" ::"l"(to), "n"(OFF), "r"(w.x), "r"(w.y),
+                 "r"(w.z), "r"(w.w), "l"(policy)
+                 : "memory");
 }
 
-// ---- forward: a ring of copy groups ------------------------------------------ //
+// ---- a ring of copy groups ----------------------------------------------------- //
 // A group is SC_GROUP vectors of every thread; a slice has `full` groups and one of what is left (up to SC_GROUP
 // vectors a thread).  The row's last vector and its first, if that is not the row's as a whole, are no part of the ring:
-// thread 32 has the last, thread 0 the first, in registers (edge).
-template <typename E> struct Ring {
-    static constexpr int GROUP = SC_NT * SC_GROUP;  // vectors
+// thread 32 has the last, thread 0 the first, in registers (edge).  TWICE: the slice comes a second time.
+template <typename E, int NT, bool TWICE> struct Ring {
+    static constexpr int GROUP = NT * SC_GROUP;  // vectors
     const Slice<E>& s;
     uint4* buf;
     int V, full;
     const char* src;   // this thread's first vector of the next group to be copied,
     int cb, to, from;  // that group and its place; the place of the next to be used
+    bool again;        // TWICE: the copies are those of the second time
+    uint64_t policy;
 
     __device__ __forceinline__ Ring(const ScoreParams& p, const Slice<E>& sl, int rank, void* smem)
-        : s(sl), buf((uint4*)smem + threadIdx.x), V(p.V), src(sl.src + threadIdx.x * 16), cb(0), to(0), from(0)
+        : s(sl), buf((uint4*)smem + threadIdx.x), V(p.V), src(sl.src + threadIdx.x * 16), cb(0), to(0), from(0),
+          again(false), policy(TWICE ? policy_keep() : 0)
     {
         const int least = (p.V * (int)sizeof(E) + 15) / 16 - rank * p.per;
         full = max(0, min(p.per, least) - 1) / GROUP;
 #pragma unroll
         for (int i = 0; i < SC_RING; ++i) copy_group();
     }
+    template <int J> __device__ __forceinline__ void copy_vector(uint32_t dst)
+    {
+        if (TWICE) copy16<J * NT * 16>(dst, src, policy);
+        else copy16<J * NT * 16>(dst, src);
+    }
     __device__ __forceinline__ void copy_group()
     {
+        static_assert(SC_GROUP == 4, "the calls below");
         uint4* place = buf + to;
         const uint32_t dst = (uint32_t)__cvta_generic_to_shared(place);
         if (cb < full) {
             // whole vectors, but the first of the row
-            if (cb > 0 || threadIdx.x >= s.lo) copy16(dst, src);
+            if (cb > 0 || threadIdx.x >= s.lo) copy_vector<0>(dst);
             else *place = no_vector<E>();
-#pragma unroll
-            for (int j = 1; j < SC_GROUP; ++j) copy16(dst + j * SC_NT * 16, src + j * SC_NT * 16);
+            copy_vector<1>(dst);
+            copy_vector<2>(dst);
+            copy_vector<3>(dst);
         } else if (cb == full) {
-            const int i0 = cb * GROUP + threadIdx.x;
-#pragma unroll
-            for (int j = 0; j < SC_GROUP; ++j) {
-                const int i = i0 + j * SC_NT;
-                if (i >= s.lo && i < s.hi) copy16(dst + j * SC_NT * 16, src + j * SC_NT * 16);
-                else if (i < s.lo) place[j * SC_NT] = no_vector<E>();
-            }
+            const int i = cb * GROUP + threadIdx.x;
+            if (i < s.lo) *place = no_vector<E>();
+            else if (i < s.hi) copy_vector<0>(dst);
+            if (i + NT < s.hi) copy_vector<1>(dst);
+            if (i + 2 * NT < s.hi) copy_vector<2>(dst);
+            if (i + 3 * NT < s.hi) copy_vector<3>(dst);
         }
         copy_commit();  // (behind the last group, groups of nothing: the waits below count them)
         src += GROUP * 16;
         to = to + GROUP == SC_RING * GROUP ? 0 : to + GROUP;
         ++cb;
+        if (TWICE && !again && cb > full) {
+            again = true;
+            cb = 0;
+            src = s.src + threadIdx.x * 16;
+            policy = policy_drop();
+        }
     }
     // the oldest group has arrived; this thread's first vector of it
     __device__ __forceinline__ const uint4* first() const
@@ -425,55 +447,9 @@ template <typename E> struct Ring {
     {
         return has_edge() ? part_vector(s, V, edge_at()) : no_vector<E>();
     }
-};
-
-// ---- gradient: the slice in shared memory ------------------------------------- //
-// the shared memory of a slice, and who copies what: thread t has vectors t, t + SC_NT, ...
-template <typename E> struct Buffer {
-    uint4* buf;
-    int V;
-    int full;  // batches that every thread has whole, at any alignment of the row, the row's last vector not among them
-
-    __device__ __forceinline__ Buffer(const ScoreParams& p, int rank, void* smem) : buf((uint4*)smem), V(p.V)
-    {
-        const int least = (p.V * (int)sizeof(E) + 15) / 16 - rank * p.per;
-        full = max(0, min(p.per, least) - 1) / (SC_NT * SC_BATCH);
-    }
-    __device__ __forceinline__ bool has(const Slice<E>& s, int id) const
+    __device__ __forceinline__ bool has(int id) const
     {
         return id >= s.first && id < s.first + s.n * EPV<E> && id < V;
-    }
-    __device__ __forceinline__ Bits<E>* at(const Slice<E>& s, int id) const { return (Bits<E>*)buf + (id - s.first); }
-
-    // a batch from this thread's vector i on
-    __device__ __forceinline__ void copy_batch(const Slice<E>& s, int i) const
-    {
-        const uint32_t to = (uint32_t)__cvta_generic_to_shared(buf + i);
-        const char* from = s.src + (int64_t)i * 16;
-        if (i >= s.lo) {
-            if (s.src) {
-#pragma unroll
-                for (int j = 0; j < SC_BATCH; ++j) copy16(to + j * SC_NT * 16, from + j * SC_NT * 16);
-            }
-        } else {  // thread 0 at a row's start
-            buf[0] = part_vector(s, V, 0);
-#pragma unroll
-            for (int j = 1; j < SC_BATCH; ++j) copy16(to + j * SC_NT * 16, from + j * SC_NT * 16);
-        }
-        copy_commit();
-    }
-    // what is left behind the batches, the vectors at the row's ends by their elements
-    __device__ __forceinline__ void copy_rest(const Slice<E>& s) const
-    {
-        for (int i = full * SC_BATCH * SC_NT + threadIdx.x; i < s.n; i += SC_NT)
-            if (i >= s.lo && i < s.hi) copy16((uint32_t)__cvta_generic_to_shared(buf + i), s.src + (int64_t)i * 16);
-            else buf[i] = part_vector(s, V, i);
-        copy_commit();
-    }
-    __device__ __forceinline__ void copy(const Slice<E>& s) const
-    {
-        for (int b = 0; b < full; ++b) copy_batch(s, b * SC_BATCH * SC_NT + threadIdx.x);
-        copy_rest(s);
     }
 };
 
@@ -539,8 +515,8 @@ template <typename E, bool ENTROPY, bool RANK> struct Summer {
             }
         }
     }
-    // vectors i, i + SC_NT, ...; returns their largest element
-    template <int N> __device__ __forceinline__ float take(const uint4 (&w)[N], int i, int batch)
+    // vectors i, i + NT, ...; returns their largest element
+    template <int NT, int N> __device__ __forceinline__ float take(const uint4 (&w)[N], int i, int batch)
     {
         typename Vec<E>::Most most = Vec<E>::top_of(w[0]);
 #pragma unroll
@@ -575,7 +551,7 @@ template <typename E, bool ENTROPY, bool RANK> struct Summer {
         if (RANK && mx >= x) {
             typename Vec<E>::Count n = Vec<E>::above(w[0], i < tvec ? under : at);
 #pragma unroll
-            for (int j = 1; j < N; ++j) n = Vec<E>::more(n, Vec<E>::above(w[j], i + j * SC_NT < tvec ? under : at));
+            for (int j = 1; j < N; ++j) n = Vec<E>::more(n, Vec<E>::above(w[j], i + j * NT < tvec ? under : at));
             ahead += Vec<E>::number(n);
         }
         return mx;
@@ -593,54 +569,38 @@ template <typename E, bool ENTROPY, bool RANK> struct Summer {
     }
     // A slice in the ring, and its edge.  skip(b): this thread leaves out its vectors of group b (full + 1: the edge);
     // seen(b, x): their largest element.
-    template <typename Skip, typename Seen>
-    __device__ __forceinline__ void stream(Ring<E>& ring, const uint4& edge, Skip skip, Seen seen)
+    template <typename R, typename Skip, typename Seen>
+    __device__ __forceinline__ void stream(R& ring, const uint4& edge, Skip skip, Seen seen)
     {
+        constexpr int NT = R::GROUP / SC_GROUP;
         int i = threadIdx.x;
 #pragma unroll 1
-        for (int b = 0; b < ring.full; ++b, i += Ring<E>::GROUP) {
+        for (int b = 0; b < ring.full; ++b, i += R::GROUP) {
             const uint4* v = ring.first();
             uint4 w[SC_GROUP];
 #pragma unroll
-            for (int j = 0; j < SC_GROUP; ++j) w[j] = v[j * SC_NT];
+            for (int j = 0; j < SC_GROUP; ++j) w[j] = v[j * NT];
             if (skip(b)) {
 #pragma unroll
                 for (int j = 0; j < SC_GROUP; ++j) w[j] = no_vector<E>();
             }
-            seen(b, take(w, i, b));
+            seen(b, take<NT>(w, i, b));
             ring.used();
         }
         const uint4* v = ring.first();
         float mx = -INFINITY;
         const bool left_out = skip(ring.full);
 #pragma unroll 1
-        for (; i < ring.s.hi; i += SC_NT, v += SC_NT) {
+        for (; i < ring.s.hi; i += NT, v += NT) {
             const uint4 w[1] = {left_out ? no_vector<E>() : *v};
-            mx = fmax_nan(mx, take(w, i, ring.full));
+            mx = fmax_nan(mx, take<NT>(w, i, ring.full));
         }
+        ring.used();
         if (ring.has_edge() && !skip(ring.full + 1)) {
             const uint4 w[1] = {edge};
-            mx = fmax_nan(mx, take(w, ring.edge_at(), ring.full));
+            mx = fmax_nan(mx, take<NT>(w, ring.edge_at(), ring.full));
         }
         seen(ring.full, mx);
-    }
-    // A slice in its buffer, being copied in groups (WAIT) or there.
-    template <bool WAIT> __device__ __forceinline__ Run run(const Buffer<E>& bf, const Slice<E>& s)
-    {
-        int i = threadIdx.x;
-        for (int b = 0; b < bf.full; ++b, i += SC_NT * SC_BATCH) {
-            if (WAIT) copy_arrived(bf.full - b);
-            uint4 w[SC_BATCH];
-#pragma unroll
-            for (int j = 0; j < SC_BATCH; ++j) w[j] = bf.buf[i + j * SC_NT];
-            take(w, i, b);
-        }
-        if (WAIT) copy_arrived(0);
-        for (int b = bf.full; i < s.n; i += SC_NT, ++b) {
-            const uint4 w[1] = {bf.buf[i]};
-            take(w, i, b);
-        }
-        return result();
     }
 };
 
@@ -672,28 +632,51 @@ template <typename E> __device__ __forceinline__ E* grad_of(const ScoreParams& p
 
 // ---- gradients ----------------------------------------------------------------- //
 // a row without a gradient, by the cluster's CTAs
-template <typename E> __device__ void zero_grad(const ScoreParams& p, int r, int rank, int C)
+template <typename E, int NT> __device__ void zero_grad(const ScoreParams& p, int r, int rank, int C)
 {
     E* g = grad_of<E>(p, r);
     const int head = (int)min((int64_t)p.V, (int64_t)(-(intptr_t)((uintptr_t)g / sizeof(E))) & (EPV<E> - 1));
-    const int nv = (p.V - head) / EPV<E>, i0 = rank * SC_NT + threadIdx.x;
+    const int nv = (p.V - head) / EPV<E>, i0 = rank * NT + threadIdx.x;
     uint4* to = (uint4*)(g + head);
-    for (int i = i0; i < nv; i += C * SC_NT) to[i] = make_uint4(0, 0, 0, 0);
+    for (int i = i0; i < nv; i += C * NT) to[i] = make_uint4(0, 0, 0, 0);
     if (i0 < head) g[i0] = narrow<E>(0.f);
     const int rest = head + nv * EPV<E> + i0;
     if (rest < p.V) g[rest] = narrow<E>(0.f);
 }
 
-// The gradient of a slice, whose buffer next's slice takes: f(pair of d, 2^d; CLAMP: d may be -inf) -> pair.
-template <typename E, bool FAST, typename F>
-__device__ __forceinline__ void grad_slice_(const Buffer<E>& bf, const Slice<E>& s, const Slice<E>& next, E* g, float m,
-                                            float c, uint32_t masked, F f)
+// 16 bytes of a row that begin at byte a of this lane's vector: of it and of the next lane's
+__device__ __forceinline__ uint4 joined(const uint4& w, int a)
 {
+    uint4 n;
+    n.x = __shfl_down_sync(~0u, w.x, 1);
+    n.y = __shfl_down_sync(~0u, w.y, 1);
+    n.z = __shfl_down_sync(~0u, w.z, 1);
+    n.w = __shfl_down_sync(~0u, w.w, 1);
+    // by words, then by the bytes left
+    const int words = a / 4, bits = a % 4 * 8;
+    uint32_t v[5];
+#pragma unroll
+    for (int q = 0; q < 5; ++q) {
+        const uint32_t two = q < 4 ? word_of(w, q) : n.x, three = q < 3 ? word_of(w, q + 1) : word_of(n, q - 3),
+                       four = q < 2 ? word_of(w, q + 2) : word_of(n, q - 2), five = q < 1 ? w.w : word_of(n, q - 1);
+        v[q] = words == 0 ? two : words == 1 ? three : words == 2 ? four : five;
+    }
+    return make_uint4(__funnelshift_r(v[0], v[1], bits), __funnelshift_r(v[1], v[2], bits),
+                      __funnelshift_r(v[2], v[3], bits), __funnelshift_r(v[3], v[4], bits));
+}
+
+// The gradient of a slice whose ring comes to it the second time: f(pair of d, 2^d; d may be -inf in the groups that
+// `masked` names, where it is clamped) -> pair.  Threads write what they read, so it may go over the logits.
+template <typename E, bool FAST, typename R, typename F>
+__device__ __forceinline__ void grad_slice_(R& ring, const uint4& edge, E* g, float m, float c, uint32_t masked, F f)
+{
+    constexpr int NT = R::GROUP / SC_GROUP;
+    const Slice<E>& s = ring.s;
     const float ref = FAST ? -rintf(m * c) : m == -INFINITY ? 0.f : -m;
-    const uint64_t r2 = pair(ref, ref), c2 = pair(c, c);
-    auto grad = [&](int i, auto clamp) {
+    const uint64_t r2 = pair(ref, ref), c2 = pair(c, c), policy = policy_drop();
+    auto grad = [&](const uint4& x, auto clamp) {
         uint64_t v[EPV<E> / 2], y[EPV<E> / 2];
-        Vec<E>::pairs(bf.buf[i], v);
+        Vec<E>::pairs(x, v);
 #pragma unroll
         for (int q = 0; q < EPV<E> / 2; ++q) {
             const uint64_t d2 = FAST ? fma2(v[q], c2, r2) : mul2(add2(v[q], r2), c2);
@@ -703,71 +686,67 @@ __device__ __forceinline__ void grad_slice_(const Buffer<E>& bf, const Slice<E>&
         }
         return Vec<E>::pack(y);
     };
-    auto any = [&](int i, int batch) {
-        return masked >> min(batch, 31) & 1 ? grad(i, std::true_type()) : grad(i, std::false_type());
+    auto is_masked = [&](int b) { return masked >> min(b, 31) & 1; };
+    auto any = [&](const uint4& x, int b) {
+        return is_masked(b) ? grad(x, std::true_type()) : grad(x, std::false_type());
     };
-    E* out = g + s.first;  // its element at the slice's start
+    char* const out = (char*)(g + s.first);  // its element at the slice's start
+    // elements q0 .. q1 - 1 of vector i
+    auto elements = [&](const uint4& w, int i, int q0, int q1) {
+        const int e = s.first + i * EPV<E>;
+#pragma unroll
+        for (int q = 0; q < EPV<E>; ++q)
+            if (q >= q0 && q < q1 && e + q >= 0 && e + q < ring.V) ((Bits<E>*)g)[e + q] = bits_at<E>(w, q);
+    };
+    const int a = (int)((-(intptr_t)out) & 15);  // bytes from a vector's place to the next 16-byte boundary
     int i = threadIdx.x;
-    if (((uintptr_t)out & 15) == 0) {
-        uint4* to = (uint4*)out;
-        auto part = [&](int i, const uint4& w) {
-            const int e = s.first + i * EPV<E>;
+    if (a == 0) {
+        char* to = out + (int64_t)i * 16;
+#pragma unroll 1
+        for (int b = 0; b < ring.full; ++b, i += R::GROUP, to += R::GROUP * 16) {
+            const uint4* v = ring.first();
+            uint4 w[SC_GROUP];
+            if (is_masked(b)) {
 #pragma unroll
-            for (int q = 0; q < EPV<E>; ++q)
-                if (e + q >= 0 && e + q < bf.V) ((Bits<E>*)g)[e + q] = bits_at<E>(w, q);
-        };
-        for (int b = 0; b < bf.full; ++b, i += SC_NT * SC_BATCH) {
-            uint4 w[SC_BATCH];
-            if (masked >> min(b, 31) & 1) {
-#pragma unroll
-                for (int j = 0; j < SC_BATCH; ++j) w[j] = grad(i + j * SC_NT, std::true_type());
+                for (int j = 0; j < SC_GROUP; ++j) w[j] = grad(v[j * NT], std::true_type());
             } else {
 #pragma unroll
-                for (int j = 0; j < SC_BATCH; ++j) w[j] = grad(i + j * SC_NT, std::false_type());
+                for (int j = 0; j < SC_GROUP; ++j) w[j] = grad(v[j * NT], std::false_type());
             }
-            if (i >= s.lo) to[i] = w[0];
-            else part(i, w[0]);
-#pragma unroll
-            for (int j = 1; j < SC_BATCH; ++j) to[i + j * SC_NT] = w[j];
-            bf.copy_batch(next, i);
+            if (b > 0 || i >= s.lo) store16<0>(to, w[0], policy);
+            store16<NT * 16>(to, w[1], policy);
+            store16<2 * NT * 16>(to, w[2], policy);
+            store16<3 * NT * 16>(to, w[3], policy);
+            ring.used();
         }
-        for (int b = bf.full; i < s.n; i += SC_NT, ++b) {
-            const uint4 w = any(i, b);
-            if (i >= s.lo && i < s.hi) to[i] = w;
-            else part(i, w);
+        const uint4* v = ring.first();
+        for (; i < s.hi; i += NT, v += NT, to += NT * 16)
+            if (i >= s.lo) store16<0>(to, any(*v, ring.full), policy);
+    } else {
+        // the gradient's rows begin elsewhere in a vector than the logits': lanes have neighbouring vectors, and join
+        // them two by two to what lies between boundaries
+        const int lane = threadIdx.x % 32, q = a / (int)sizeof(E);
+        for (int b = 0; b <= ring.full; ++b) {
+            const uint4* v = ring.first();
+            for (int j = 0; j < SC_GROUP; ++j, i += NT) {
+                if (i - lane >= s.hi) continue;  // none of the warp's
+                const bool in = i >= s.lo && i < s.hi;
+                const uint4 w = in ? any(v[j * NT], b) : no_vector<E>(), two = joined(w, a);
+                if (!in) continue;
+                if (lane < 31 && i + 1 < s.hi) store16<0>(out + (int64_t)i * 16 + a, two, policy);
+                else elements(w, i, q, EPV<E>);
+                if (lane == 0 || i == s.lo) elements(w, i, 0, q);
+            }
+            ring.used();
         }
-        bf.copy_rest(next);
-        return;
     }
-    // the gradient's rows start elsewhere in a vector than the logits': elements change vectors on the way out
-    for (int b = 0; i < s.n; i += SC_NT, ++b)
-        bf.buf[i] = any(i, b < bf.full * SC_BATCH ? b / SC_BATCH : b - bf.full * (SC_BATCH - 1));
-    __syncthreads();
-    const int e0 = max(s.first, 0), e1 = min(s.first + s.n * EPV<E>, bf.V);
-    if (e0 < e1) {
-        const int head = min(e1 - e0, (int)((-(intptr_t)((uintptr_t)(g + e0) / sizeof(E))) & (EPV<E> - 1)));
-        const int nv = (e1 - e0 - head) / EPV<E>;
-        const Bits<E>* from = bf.at(s, e0);
-        Bits<E>* to = (Bits<E>*)g + e0;
-        for (int i = threadIdx.x; i < nv; i += SC_NT) {
-            Bits<E> v[EPV<E>];
-#pragma unroll
-            for (int q = 0; q < EPV<E>; ++q) v[q] = from[head + i * EPV<E> + q];
-            *(uint4*)(to + head + i * EPV<E>) = vector_of<E>(v);
-        }
-        if (threadIdx.x < head) to[threadIdx.x] = from[threadIdx.x];
-        const int rest = head + nv * EPV<E> + threadIdx.x;
-        if (rest < e1 - e0) to[rest] = from[rest];
-    }
-    __syncthreads();
-    bf.copy(next);
+    if (ring.has_edge()) elements(any(edge, ring.full), ring.edge_at(), 0, EPV<E>);
 }
-template <typename E, typename F>
-__device__ __forceinline__ void grad_slice(const Buffer<E>& bf, const Slice<E>& s, const Slice<E>& next, E* g, float m,
-                                           float c, uint32_t masked, F f)
+template <typename E, typename R, typename F>
+__device__ __forceinline__ void grad_slice(R& ring, const uint4& edge, E* g, float m, float c, uint32_t masked, F f)
 {
-    if (plain_ref(m, c)) grad_slice_<E, true>(bf, s, next, g, m, c, masked, f);
-    else grad_slice_<E, false>(bf, s, next, g, m, c, masked, f);
+    if (plain_ref(m, c)) grad_slice_<E, true>(ring, edge, g, m, c, masked, f);
+    else grad_slice_<E, false>(ring, edge, g, m, c, masked, f);
 }
 
 // ---- launches ------------------------------------------------------------------ //
@@ -780,10 +759,10 @@ struct ScoreKernel {
 struct ScoreLaunch {
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute at[1];
-    ScoreLaunch(int C, size_t smem, cudaStream_t s)
+    ScoreLaunch(int C, int threads, size_t smem, cudaStream_t s)
     {
         cfg.gridDim = dim3((unsigned)C);
-        cfg.blockDim = dim3(SC_NT);
+        cfg.blockDim = dim3(threads);
         cfg.dynamicSmemBytes = smem;
         cfg.stream = s;
         at[0].id = cudaLaunchAttributeClusterDimension;
@@ -801,7 +780,8 @@ template <typename K> cudaError_t score_ready(K kernel, ScoreKernel& sk, size_t 
         return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
     });
 }
-template <typename K> cudaError_t score_resident(K kernel, ScoreKernel& sk, int C, size_t smem, int* clusters)
+template <typename K>
+cudaError_t score_resident(K kernel, ScoreKernel& sk, int C, int threads, size_t smem, int* clusters)
 {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -813,7 +793,7 @@ template <typename K> cudaError_t score_resident(K kernel, ScoreKernel& sk, int 
         *clusters = (int)(seen & 0xFFFFFFFFu);
         return cudaSuccess;
     }
-    const ScoreLaunch l(C, smem, nullptr);
+    const ScoreLaunch l(C, threads, smem, nullptr);
     e = cudaOccupancyMaxActiveClusters(clusters, kernel, &l.cfg);
     if (e != cudaSuccess) return e;
     if (*clusters < 1) *clusters = 1;
@@ -821,32 +801,12 @@ template <typename K> cudaError_t score_resident(K kernel, ScoreKernel& sk, int 
     return cudaSuccess;
 }
 
-// Launches clusters of p.cluster CTAs with `smem` bytes each: one per row, or persistent ones, as many as fit the GPU at
-// once, since one more would wait for another's last row.
-template <typename K>
-cudaError_t score_launch(K kernel, ScoreKernel& sk, ScoreParams& p, size_t smem, bool persistent, cudaStream_t s)
+// Launches a cluster of p.cluster CTAs for every row.
+template <typename K> cudaError_t score_launch(K kernel, ScoreParams& p, int threads, size_t smem, cudaStream_t s)
 {
-    const int C = p.cluster;
-    int nc = p.rows;
-    if (persistent) {
-        const cudaError_t e = score_resident(kernel, sk, C, smem, &nc);
-        if (e != cudaSuccess) return e;
-        nc = nc < p.rows ? nc : p.rows;
-        // a stride that shares no factor with the positions of a sequence: each cluster meets all of them alike,
-        // the ends of ragged sequences, which cost nothing, among them
-        auto gcd = [](int a, int b) {
-            while (b) {
-                const int t = a % b;
-                a = b;
-                b = t;
-            }
-            return a;
-        };
-        while (nc > 1 && nc < p.rows && gcd(nc, p.T) > 1) --nc;
-    }
     p.by_tokens = FastDiv(p.T);
-    ScoreLaunch l(C, smem, s);
-    l.cfg.gridDim = dim3((unsigned)nc * C);
+    ScoreLaunch l(p.cluster, threads, smem, s);
+    l.cfg.gridDim = dim3((unsigned)p.rows * p.cluster);
     return cudaLaunchKernelEx(&l.cfg, kernel, p);
 }
 
@@ -864,7 +824,7 @@ cudaError_t score_split_forward(K kernel, ScoreKernel& sk, ScoreParams& p, size_
     for (int C = 1; C <= SC_MAXC && (C == 1 || row / C >= SC_NT); C *= 2) {
         const int per = (row + C - 1) / C;
         int nc = 0;
-        const cudaError_t e = score_resident(kernel, sk, C, smem_of(per), &nc);
+        const cudaError_t e = score_resident(kernel, sk, C, SC_NT, smem_of(per), &nc);
         if (e != cudaSuccess) return e;
         const double rounds = p.rows <= nc ? 1.0 : (double)p.rows / nc + 0.5, cost = rounds * ((double)per / SC_NT + fixed);
         if (C > 1 && cost >= best) continue;
@@ -874,19 +834,21 @@ cudaError_t score_split_forward(K kernel, ScoreKernel& sk, ScoreParams& p, size_
     }
     return cudaSuccess;
 }
-// CTAs of a row with a gradient: slices of at most SCORE_SLICE bytes, so that several CTAs share an SM and some copy
-// while others compute; rows beyond eight of them have larger slices.  Few rows are spread over up to eight CTAs, for
-// the SMs that would idle, while a thread still has a vector.
+// CTAs of a row with a gradient, two of them an SM (their shared memory sees to it): as many as it takes for the rows
+// under way to stay in L2 between their two passes, with room for what else lies there; and few rows are spread over
+// more, for the SMs that would idle, while every thread has a vector or two.
+constexpr size_t SC_GRAD_BYTES = 100 * 1024;
 inline void score_split_gradient(ScoreParams& p, size_t size, int num_sms)
 {
-    const int row = score_vectors(p, size), slice = SCORE_SLICE / 16;
-    int C = (row + slice - 1) / slice;
-    C = C > SC_MAXC ? SC_MAXC : C;
-    while (C < SC_MAXC && (int64_t)p.rows * C < num_sms && row / (C + 1) >= SC_NT) ++C;
+    const int row = score_vectors(p, size);
+    const double under_way = 2.0 * num_sms < p.rows ? 2.0 * num_sms : p.rows;
+    int C = 1;
+    while (C < SC_MAXC && ((under_way / C) * row * 16 > SCORE_L2_ROWS ||
+                           ((int64_t)p.rows * C < 2 * num_sms && row / (2 * C) >= SC_NT_GRAD)))
+        C *= 2;
     p.cluster = C;
     p.per = (row + C - 1) / C;
 }
-constexpr size_t SC_MOST_SLICE = SCORE_MAX_ROW_BYTES / SC_MAXC + 64;
 
 }  // namespace
 
