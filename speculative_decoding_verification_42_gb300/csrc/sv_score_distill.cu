@@ -79,57 +79,103 @@ template <int NT> struct Teacher {
     float in, left;               // sum of q, what it leaves of 1
 };
 
-// what the threads of a CTA tell one another of a row's entries; the next row has another, as some are still at the
-// last row's end when others begin it
+// What the threads of a CTA tell one another of a row's entries.  The entries of a slice are chained by the thread whose
+// vectors they lie in (head, next), with their place there: copy group (the row's ends being group full + 1) and element
+// of the group.
+constexpr int SC_SEEN = 32768;  // places of ids
 template <int NT> struct EntryShared {
     int32_t ids[SPEC_SCORE_MAX_ENTRIES];
-    int32_t slots[SPEC_SCORE_MAX_ENTRIES];
+    int32_t next[SPEC_SCORE_MAX_ENTRIES], place[SPEC_SCORE_MAX_ENTRIES];
+    int32_t head[NT];
+    uint32_t seen[SC_SEEN / 32];
+    uint32_t state;                          // 1: a bad id; 2: two ids with one place in `seen`
     float w_max[NT / 32], w_sum[NT / 32];
     float w_me[NT / 32], w_se[NT / 32];  // the student's largest logit at a warp's entries, and the sum of their 2^d
 };
-
-// Checks a row's entries (a barrier, then the checks; the caller passes bad to the next one) and starts the teacher's
-// sums.  slots: see below; mark(u): called between the barriers.
-template <int NT, typename Mark>
-__device__ __forceinline__ bool check_entries(const ScoreParams& p, EntryShared<NT>& es, Entries<NT>& en, const int (&slot)[EPT<NT>],
-                                              bool (&first)[EPT<NT>], float& tmax, Mark mark)
+template <int NT> __device__ __forceinline__ void clear(EntryShared<NT>& es)
 {
-    const int tid = threadIdx.x, lane = tid % 32;
-    tmax = -INFINITY;
+    es.head[threadIdx.x] = -1;
+    for (int i = threadIdx.x; i < SC_SEEN / 32; i += NT) es.seen[i] = 0;
+    if (threadIdx.x == 0) es.state = 0;
+}
+
+// Enters a row's entries (es is clear, and a barrier has passed): ids out of range and, maybe, ids that are there twice
+// go to `state`; the warps' largest teacher values to w_max.
+template <typename E, int NT>
+__device__ __forceinline__ void enter(const ScoreParams& p, EntryShared<NT>& es, Entries<NT>& en, const Slice<E>& sl, int full)
+{
+    const int tid = threadIdx.x;
+    float tmax = -INFINITY;
 #pragma unroll
     for (int u = 0; u < EPT<NT>; ++u) {
-        es.ids[tid + u * NT] = en.id[u];
-        es.slots[tid + u * NT] = slot[u];
-        if (en.id[u] == -1) en.tv[u] = -INFINITY;
+        const int e = tid + u * NT, id = en.id[u];
+        es.ids[e] = id;
+        if (id == -1) {
+            en.tv[u] = -INFINITY;
+            continue;
+        }
         tmax = fmax_nan(tmax, en.tv[u]);
+        if (id < 0 || id >= p.V) {
+            atomicOr(&es.state, 1u);
+            continue;
+        }
+        const uint32_t at = (uint32_t)(id ^ id >> 15) % SC_SEEN, bit = 1u << (at % 32);
+        if (atomicOr(es.seen + at / 32, bit) & bit) atomicOr(&es.state, 2u);
+        if (id < sl.first) continue;
+        const int i = (id - sl.first) / EPV<E>, q = (id - sl.first) % EPV<E>;
+        if (i >= sl.n) continue;
+        const bool inner = i >= sl.lo && i < sl.hi;
+        const int owner = inner ? i % NT : i < sl.lo ? 0 : 32;
+        es.place[e] = inner ? i / (NT * SC_GROUP) << 8 | i / NT % SC_GROUP * EPV<E> + q : (full + 1) << 8 | q;
+        es.next[e] = atomicExch(es.head + owner, e);
     }
     tmax = warp_max(tmax);
-    if (lane == 0) es.w_max[tid / 32] = tmax;
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < NT / 32; ++i) tmax = fmax_nan(tmax, es.w_max[i]);
-    bool bad = false;
+    if (tid % 32 == 0) es.w_max[tid / 32] = tmax;
+}
+// after a barrier: whether the row is bad, for all CTAs of a cluster alike
+template <int NT> __device__ __forceinline__ bool bad_entries(const EntryShared<NT>& es, const Entries<NT>& en)
+{
+    if (es.state & 1) return true;
+    if (!(es.state & 2)) return false;
+    bool twice = false;
 #pragma unroll
     for (int u = 0; u < EPT<NT>; ++u) {
-        const int i = tid + u * NT, id = en.id[u];
-        first[u] = slot[u] >= 0;
+        const int e = threadIdx.x + u * NT, id = en.id[u];
         if (id == -1) continue;
-        bad |= id < -1 || id >= p.V;
-        for (int j = 0; j < i; j += 4) {
+        for (int j = 0; j < e; j += 4) {
             const int4 o = *(const int4*)(es.ids + j);
-            bad |= o.x == id || (o.y == id && j + 1 < i) || (o.z == id && j + 2 < i) || (o.w == id && j + 3 < i);
+            twice |= o.x == id || (o.y == id && j + 1 < e) || (o.z == id && j + 2 < e) || (o.w == id && j + 3 < e);
         }
-        if (first[u])
-            for (int j = 0; j < i; j += 4) {
-                const int4 o = *(const int4*)(es.slots + j);
-                if (o.x == slot[u] || (o.y == slot[u] && j + 1 < i) || (o.z == slot[u] && j + 2 < i) ||
-                    (o.w == slot[u] && j + 3 < i))
-                    first[u] = false;
-            }
-        mark(u);
     }
-    return bad;
+    return __syncthreads_or(twice);
 }
+// The entries of a thread's vectors leave them, group by group.  (Which of two comes first in the chain is a matter of
+// chance, but both leave.)
+template <typename E, int NT> struct Leaving {
+    const EntryShared<NT>& es;
+    int group;  // the next with an entry
+    __device__ __forceinline__ explicit Leaving(const EntryShared<NT>& s) : es(s) { after(-1); }
+    __device__ __forceinline__ void after(int b)
+    {
+        group = INT32_MAX;
+        for (int e = es.head[threadIdx.x]; e >= 0; e = es.next[e])
+            if (es.place[e] >> 8 > b) group = min(group, es.place[e] >> 8);
+    }
+    template <int STEP> __device__ __forceinline__ void from(int b, uint4* v)
+    {
+        if (b != group) return;
+        for (int e = es.head[threadIdx.x]; e >= 0; e = es.next[e]) {
+            const int at = es.place[e];
+            if (at >> 8 != b) continue;
+            // element q of vector j, by words, as the vector is read
+            const int j = (at & 255) / EPV<E>, q = (at & 255) % EPV<E>;
+            uint32_t* const w = (uint32_t*)(v + j * STEP) + q * (int)sizeof(E) / 4;
+            *w = sizeof(E) == 4 ? Vec<E>::NEG : q % 2 ? (*w & 0xFFFFu) | (Vec<E>::NEG & 0xFFFF0000u)
+                                                       : (*w & 0xFFFF0000u) | (Vec<E>::NEG & 0xFFFFu);
+        }
+        after(b);
+    }
+};
 __device__ __forceinline__ bool dull(const ScoreParams& p, float tmax, float lse)
 {
     return !(tmax < INFINITY) || (!p.tail && tmax == -INFINITY) || !(fabsf(lse) < INFINITY);
@@ -265,64 +311,6 @@ __device__ __forceinline__ void finish(const ScoreParams& p, int r, const KdRow&
     }
 }
 
-// ---- both passes' first part -------------------------------------------------------- //
-// A thread leaves out the copy groups of its vectors in which an entry lies (flags: a bit for each group and thread, the
-// row's ends being group full + 1).  Those are read once more, each by the thread of the first entry in it (slots: group
-// and thread), which takes the entries out.
-template <typename E, int NT>
-__device__ __forceinline__ void slots_of(const Slice<E>& sl, int V, int full, const Entries<NT>& en, int (&slot)[EPT<NT>])
-{
-#pragma unroll
-    for (int u = 0; u < EPT<NT>; ++u) {
-        slot[u] = -1;
-        if (en.id[u] < sl.first || en.id[u] >= V || en.id[u] < 0) continue;
-        const int i = (en.id[u] - sl.first) / EPV<E>;
-        if (i >= sl.n) continue;
-        slot[u] = i >= sl.lo && i < sl.hi ? i / (NT * SC_GROUP) * NT + i % NT : (full + 1) * NT + (i < sl.lo ? 0 : 32);
-    }
-}
-template <typename E, int NT, typename S>
-__device__ __forceinline__ void take_left_out(const ScoreParams& p, const Slice<E>& sl, int full, const EntryShared<NT>& es,
-                                              const int (&slot)[EPT<NT>], const bool (&first)[EPT<NT>], S& rest)
-{
-#pragma unroll
-    for (int u = 0; u < EPT<NT>; ++u) {
-        if (!first[u]) continue;
-        const int g = slot[u] / NT, owner = slot[u] % NT;
-        const bool end = g > full;
-        uint4 w[SC_GROUP];
-        int at[SC_GROUP];
-#pragma unroll
-        for (int j = 0; j < SC_GROUP; ++j) {
-            at[j] = end ? (owner == 0 ? 0 : sl.n - 1) : (g * SC_GROUP + j) * NT + owner;
-            w[j] = end ? (j ? no_vector<E>() : load_vector(sl, p.V, at[j]))
-                       : at[j] >= sl.lo && at[j] < sl.hi ? load_vector(sl, p.V, at[j]) : no_vector<E>();
-        }
-        uint32_t out = 0;  // the entries' elements
-        for (int j = 0; j < p.k; j += 4) {
-            const int4 o = *(const int4*)(es.slots + j);
-            auto one = [&](int s, int j) {
-                if (s != slot[u]) return;
-                const int e = es.ids[j] - sl.first;
-                out |= 1u << ((end ? 0 : (e / EPV<E> - at[0]) / NT) * EPV<E> + e % EPV<E>);
-            };
-            one(o.x, j);
-            one(o.y, j + 1);
-            one(o.z, j + 2);
-            one(o.w, j + 3);
-        }
-#pragma unroll
-        for (int j = 0; j < SC_GROUP; ++j) {
-            Bits<E> v[EPV<E>];
-#pragma unroll
-            for (int q = 0; q < EPV<E>; ++q)
-                v[q] = out >> (j * EPV<E> + q) & 1 ? (Bits<E>)Vec<E>::NEG : bits_at<E>(w[j], q);
-            w[j] = vector_of<E>(v);
-        }
-        rest.template take<NT>(w, 0, 0);
-    }
-}
-
 template <typename E, int NT, bool GRAD> __device__ __forceinline__ void distill_row(const ScoreParams& p)
 {
     constexpr int W = NT / 32;
@@ -331,9 +319,9 @@ template <typename E, int NT, bool GRAD> __device__ __forceinline__ void distill
     __shared__ KdPart parts[SC_MAXC * W];
     __shared__ KdRow s_row;
     const int C = p.cluster, rank = (int)cluster_rank(), r = cluster_id(), tid = threadIdx.x, lane = tid % 32;
-    const int warp = tid / 32;
     Entries<NT> en;
     en.fetch(p, r);
+    clear(es);
     if (!__syncthreads_or(en.some())) {
         no_distill<E, NT>(p, r, SPEC_ROW_OK, rank, C);
         return;
@@ -344,18 +332,12 @@ template <typename E, int NT, bool GRAD> __device__ __forceinline__ void distill
     en.fetch_logits(x, p.V);
     const uint4 edge = ring.edge();
     const float lse = p.teacher_lse ? p.teacher_lse[r] : 0.f;
-    uint32_t* const flags = (uint32_t*)(smem + RING_BYTES<NT>);
-    for (int i = tid; i < (ring.full + 2) * W; i += NT) flags[i] = 0;
-    int slot[EPT<NT>];
-    slots_of(sl, p.V, ring.full, en, slot);
-    float tmax;
-    bool first[EPT<NT>];
-    bool bad = check_entries(p, es, en, slot, first, tmax, [&](int u) {
-        if (slot[u] >= 0) atomicOr(flags + slot[u] / 32, 1u << (slot[u] % 32));
-    });
-    Teacher<NT> te;
-    begin_teacher(p, es, en, tmax, lse, te);
-    bad = __syncthreads_or(bad);
+    enter(p, es, en, sl, ring.full);
+    __syncthreads();
+    const bool bad = bad_entries(es, en);
+    float tmax = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < W; ++i) tmax = fmax_nan(tmax, es.w_max[i]);
     if (bad || dull(p, tmax, lse)) {
         copy_done();
         no_distill<E, NT>(p, r, bad ? SPEC_ROW_BAD_TOKEN : SPEC_ROW_NONFINITE, rank, C);
@@ -363,19 +345,27 @@ template <typename E, int NT, bool GRAD> __device__ __forceinline__ void distill
     }
     // every CTA of the cluster runs before another stores into its shared memory
     if (C > 1) cluster_arrive();
+    Teacher<NT> te;
+    begin_teacher(p, es, en, tmax, lse, te);
+    if (GRAD || rank == 0) sum_entries(p, es, en);
+    Leaving<E, NT> leaving(es);
     Summer<E, false, false> rest;
     rest.c = p.c;
-    rest.stream(ring, edge, [&](int b) { return flags[b * W + warp] >> lane & 1; }, [](int, float) {});
-    take_left_out(p, sl, ring.full, es, slot, first, rest);
+    rest.stream(
+        ring, edge,
+        [&](int b, uint4* v) {
+            if (b <= ring.full) leaving.template from<NT>(b, v);
+            else leaving.template from<1>(b, v);
+        },
+        [](int, float) {});
     Run run = rest.result();
     KdPart w;
     w.m = warp_max(run.m);
     to_max(run, w.m, p.c);
     w.s = warp_sum(run.s);
-    if (GRAD || rank == 0) sum_entries(p, es, en);
     if (C > 1) cluster_wait();
     if (lane < (GRAD ? C : 1)) {
-        const uint32_t to = remote(parts + rank * W + warp, lane);
+        const uint32_t to = remote(parts + rank * W + tid / 32, lane);
         remote_st(to, __float_as_uint(w.m));
         remote_st(to + 4, __float_as_uint(w.s));
     }
@@ -427,13 +417,11 @@ template <typename E> cudaError_t go(ScoreParams p, int num_sms, cudaStream_t s)
     static ScoreKernel sk[2];
     if (!p.grad) {
         const auto kernel = k_score_distill<E>;
-        auto smem = [](size_t per) { return RING_BYTES<SC_NT> + (per / (SC_NT * SC_GROUP) + 2) * (SC_NT / 32) * 4; };
-        cudaError_t e = score_ready(kernel, sk[0], smem(SCORE_MAX_ROW_BYTES / 16 + 2));
-        if (e == cudaSuccess) e = score_split_forward(kernel, sk[0], p, sizeof(E), 40, smem);
-        return e == cudaSuccess ? score_launch(kernel, p, SC_NT, smem(p.per), s) : e;
+        constexpr size_t smem = RING_BYTES<SC_NT>;
+        cudaError_t e = score_ready(kernel, sk[0], smem);
+        if (e == cudaSuccess) e = score_split_forward(kernel, sk[0], p, sizeof(E), 32, [](size_t) { return smem; });
+        return e == cudaSuccess ? score_launch(kernel, p, SC_NT, smem, s) : e;
     }
-    static_assert(RING_BYTES<SC_NT_GRAD> + (SCORE_MAX_ROW_BYTES / 16 / (SC_NT_GRAD * SC_GROUP) + 3) * (SC_NT_GRAD / 32) * 4 <=
-                  SC_GRAD_BYTES, "flags of the largest row");
     const cudaError_t e = score_ready(k_score_distill_grad<E>, sk[1], SC_GRAD_BYTES);
     if (e != cudaSuccess) return e;
     score_split_gradient(p, sizeof(E), num_sms);

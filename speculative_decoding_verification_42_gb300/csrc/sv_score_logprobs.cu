@@ -301,7 +301,7 @@ template <typename E, bool TOP> __global__ void __launch_bounds__(SC_NT, TOP ? 4
     Bits<E>* const most = (Bits<E>*)(&ts + 1);
     int ahead = 0;
     Run run;
-    auto none = [](int) { return false; };
+    auto none = [](int, uint4*) {};
     auto seen = [&](int b, float m) {
         if (TOP) {
             const E e = narrow<E>(m);  // exact: m is a value of E
@@ -392,7 +392,7 @@ template <typename E> __global__ void __launch_bounds__(SC_NT_GRAD, 2) k_score_l
     const uint4 edge = ring.edge();
     Summer<E, true, false> sum;
     sum.c = p.c;
-    sum.stream(ring, edge, [](int) { return false; }, [](int, float) {});
+    sum.stream(ring, edge, [](int, uint4*) {}, [](int, float) {});
     Run run = sum.result();
     LpPart w;
     w.m = warp_max(run.m);

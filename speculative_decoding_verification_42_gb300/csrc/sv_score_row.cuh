@@ -428,7 +428,7 @@ template <typename E, int NT, bool TWICE> struct Ring {
         }
     }
     // the oldest group has arrived; this thread's first vector of it
-    __device__ __forceinline__ const uint4* first() const
+    __device__ __forceinline__ uint4* first() const
     {
         asm volatile("cp.async.wait_group %0;" ::"n"(SC_RING - 1) : "memory");
         return buf + from;
@@ -567,36 +567,34 @@ template <typename E, bool ENTROPY, bool RANK> struct Summer {
         r.t = a + z;
         return r;
     }
-    // A slice in the ring, and its edge.  skip(b): this thread leaves out its vectors of group b (full + 1: the edge);
-    // seen(b, x): their largest element.
-    template <typename R, typename Skip, typename Seen>
-    __device__ __forceinline__ void stream(R& ring, const uint4& edge, Skip skip, Seen seen)
+    // A slice in the ring, and its edge.  change(b, v): before this thread's vectors v, v + NT, ... of group b are read
+    // (full + 1: the edge); seen(b, x): their largest element.
+    template <typename R, typename Change, typename Seen>
+    __device__ __forceinline__ void stream(R& ring, uint4 edge, Change change, Seen seen)
     {
         constexpr int NT = R::GROUP / SC_GROUP;
         int i = threadIdx.x;
 #pragma unroll 1
         for (int b = 0; b < ring.full; ++b, i += R::GROUP) {
-            const uint4* v = ring.first();
+            uint4* v = ring.first();
+            change(b, v);
             uint4 w[SC_GROUP];
 #pragma unroll
             for (int j = 0; j < SC_GROUP; ++j) w[j] = v[j * NT];
-            if (skip(b)) {
-#pragma unroll
-                for (int j = 0; j < SC_GROUP; ++j) w[j] = no_vector<E>();
-            }
             seen(b, take<NT>(w, i, b));
             ring.used();
         }
-        const uint4* v = ring.first();
+        uint4* v = ring.first();
+        change(ring.full, v);
         float mx = -INFINITY;
-        const bool left_out = skip(ring.full);
 #pragma unroll 1
         for (; i < ring.s.hi; i += NT, v += NT) {
-            const uint4 w[1] = {left_out ? no_vector<E>() : *v};
+            const uint4 w[1] = {*v};
             mx = fmax_nan(mx, take<NT>(w, i, ring.full));
         }
         ring.used();
-        if (ring.has_edge() && !skip(ring.full + 1)) {
+        if (ring.has_edge()) {
+            change(ring.full + 1, &edge);
             const uint4 w[1] = {edge};
             mx = fmax_nan(mx, take<NT>(w, ring.edge_at(), ring.full));
         }
