@@ -14,7 +14,7 @@ namespace sv {
 
 namespace {
 
-template <int NT> constexpr int EPT = SPEC_SCORE_MAX_ENTRIES / NT;  // entries of a thread: tid, tid + NT
+template <int NT> constexpr int EPT = (SPEC_SCORE_MAX_ENTRIES + NT - 1) / NT;  // entries of a thread: tid, tid + NT
 
 __device__ __forceinline__ float teacher_value(const ScoreParams& p, int64_t at)
 {
@@ -84,8 +84,8 @@ template <int NT> struct Teacher {
 // of the group.
 constexpr int SC_SEEN = 32768;  // places of ids
 template <int NT> struct EntryShared {
-    int32_t ids[SPEC_SCORE_MAX_ENTRIES];
-    int32_t next[SPEC_SCORE_MAX_ENTRIES], place[SPEC_SCORE_MAX_ENTRIES];
+    int32_t ids[EPT<NT> * NT];
+    int32_t next[EPT<NT> * NT], place[EPT<NT> * NT];
     int32_t head[NT];
     uint32_t seen[SC_SEEN / 32];
     uint32_t state;                          // 1: a bad id; 2: two ids with one place in `seen`
@@ -407,7 +407,7 @@ template <typename E> __global__ void __launch_bounds__(SC_NT, 5) k_score_distil
 {
     distill_row<E, SC_NT, false>(p);
 }
-template <typename E> __global__ void __launch_bounds__(SC_NT_GRAD, 2) k_score_distill_grad(const ScoreParams p)
+template <typename E> __global__ void __launch_bounds__(SC_NT_GRAD, 4) k_score_distill_grad(const ScoreParams p)
 {
     distill_row<E, SC_NT_GRAD, true>(p);
 }

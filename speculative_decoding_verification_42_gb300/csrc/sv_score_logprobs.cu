@@ -371,7 +371,7 @@ template <typename E, bool TOP> __global__ void __launch_bounds__(SC_NT, TOP ? 4
     write_top(p, r, ts, row, logf(row.s) - dist(row.m, row.m, p.c) * LN2, C);
 }
 
-template <typename E> __global__ void __launch_bounds__(SC_NT_GRAD, 2) k_score_logprobs_grad(const ScoreParams p)
+template <typename E> __global__ void __launch_bounds__(SC_NT_GRAD, 4) k_score_logprobs_grad(const ScoreParams p)
 {
     constexpr int NT = SC_NT_GRAD, W = NT / 32;
     extern __shared__ __align__(16) unsigned char smem[];

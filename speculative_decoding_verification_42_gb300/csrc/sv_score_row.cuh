@@ -10,8 +10,8 @@
 //   forward    one cluster per row: four or more CTAs share an SM, and two that
 //              stream keep HBM busy while others begin or end
 //   gradient   the row's sum comes before the gradient's first element, so the
-//              row is streamed twice, the second time from L2, which is told
-//              to keep it until then: as many rows are under way as L2 holds
+//              row is streamed twice, the second time from L2: as many rows are
+//              under way as it holds
 //
 // Slices are whole 16-byte vectors of the row's addresses, so rows of any
 // alignment are copied and read alike; what a row's first and last vector have
@@ -28,7 +28,7 @@ namespace sv {
 namespace {
 
 constexpr int SC_NT = 128;               // threads of a CTA in the forward passes,
-constexpr int SC_NT_GRAD = 256;          // and with a gradient
+constexpr int SC_NT_GRAD = 128;          // and with a gradient
 constexpr int SC_GROUP = 4;              // vectors of a thread in a copy group
 constexpr int SC_RING = 4;               // groups of a ring
 constexpr int SC_MAXC = SCORE_MAX_CTAS;  // CTAs of a cluster (portable)
@@ -340,38 +340,14 @@ template <int OFF> __device__ __forceinline__ void copy16(uint32_t to, const cha
 {
     asm volatile("cp.async.cg.shared.global.L2::128B [%0+%2], [%1+%2], 16;" ::"r"(to), "l"(from), "n"(OFF) : "memory");
 }
-template <int OFF> __device__ __forceinline__ void copy16(uint32_t to, const char* from, uint64_t policy)
-{
-    asm volatile("cp.async.cg.shared.global.L2::cache_hint.L2::128B [%0+%2], [%1+%2], 16, %3;" ::"r"(to), "l"(from),
-                 "n"(OFF), "l"(policy)
-                 : "memory");
-}
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 __device__ __forceinline__ void copy_done() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
-// what L2 is told of a line: to keep it, or that it is not needed again
-__device__ __forceinline__ uint64_t policy_keep()
-{
-    uint64_t p;
-    asm volatile("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(p));
-    return p;
-}
-__device__ __forceinline__ uint64_t policy_drop()
-{
-    uint64_t p;
-    asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
-    return p;
-}
-template <int OFF> __device__ __forceinline__ void store16(void* to, const uint4& w, uint64_t policy)
-{
-    asm volatile("st.global.L2::cache_hint.v4.b32 [%0+%1], {%2, %3, %4, %5}, %6;" ::"l"(to), "n"(OFF), "r"(w.x), "r"(w.y),
-                 "r"(w.z), "r"(w.w), "l"(policy)
-                 : "memory");
-}
-
 // ---- a ring of copy groups ----------------------------------------------------- //
 // A group is SC_GROUP vectors of every thread; a slice has `full` groups and one of what is left (up to SC_GROUP
 // vectors a thread).  The row's last vector and its first, if that is not the row's as a whole, are no part of the ring:
-// thread 32 has the last, thread 0 the first, in registers (edge).  TWICE: the slice comes a second time.
+// thread 32 has the last, thread 0 the first, in registers (edge).  TWICE: the slice comes a second time, its last group
+// first: what was read last is the likeliest to be in L2 still, where a second pass in the same order would find each
+// line just gone.
 template <typename E, int NT, bool TWICE> struct Ring {
     static constexpr int GROUP = NT * SC_GROUP;  // vectors
     const Slice<E>& s;
@@ -380,52 +356,44 @@ template <typename E, int NT, bool TWICE> struct Ring {
     const char* src;   // this thread's first vector of the next group to be copied,
     int cb, to, from;  // that group and its place; the place of the next to be used
     bool again;        // TWICE: the copies are those of the second time
-    uint64_t policy;
 
     __device__ __forceinline__ Ring(const ScoreParams& p, const Slice<E>& sl, int rank, void* smem)
         : s(sl), buf((uint4*)smem + threadIdx.x), V(p.V), src(sl.src + threadIdx.x * 16), cb(0), to(0), from(0),
-          again(false), policy(TWICE ? policy_keep() : 0)
+          again(false)
     {
         const int least = (p.V * (int)sizeof(E) + 15) / 16 - rank * p.per;
         full = max(0, min(p.per, least) - 1) / GROUP;
 #pragma unroll
         for (int i = 0; i < SC_RING; ++i) copy_group();
     }
-    template <int J> __device__ __forceinline__ void copy_vector(uint32_t dst)
-    {
-        if (TWICE) copy16<J * NT * 16>(dst, src, policy);
-        else copy16<J * NT * 16>(dst, src);
-    }
     __device__ __forceinline__ void copy_group()
     {
         static_assert(SC_GROUP == 4, "the calls below");
         uint4* place = buf + to;
         const uint32_t dst = (uint32_t)__cvta_generic_to_shared(place);
-        if (cb < full) {
+        if (cb >= 0 && cb < full) {
             // whole vectors, but the first of the row
-            if (cb > 0 || threadIdx.x >= s.lo) copy_vector<0>(dst);
+            if (cb > 0 || threadIdx.x >= s.lo) copy16<0 * NT * 16>(dst, src);
             else *place = no_vector<E>();
-            copy_vector<1>(dst);
-            copy_vector<2>(dst);
-            copy_vector<3>(dst);
+            copy16<1 * NT * 16>(dst, src);
+            copy16<2 * NT * 16>(dst, src);
+            copy16<3 * NT * 16>(dst, src);
         } else if (cb == full) {
             const int i = cb * GROUP + threadIdx.x;
             if (i < s.lo) *place = no_vector<E>();
-            else if (i < s.hi) copy_vector<0>(dst);
-            if (i + NT < s.hi) copy_vector<1>(dst);
-            if (i + 2 * NT < s.hi) copy_vector<2>(dst);
-            if (i + 3 * NT < s.hi) copy_vector<3>(dst);
+            else if (i < s.hi) copy16<0 * NT * 16>(dst, src);
+            if (i + NT < s.hi) copy16<1 * NT * 16>(dst, src);
+            if (i + 2 * NT < s.hi) copy16<2 * NT * 16>(dst, src);
+            if (i + 3 * NT < s.hi) copy16<3 * NT * 16>(dst, src);
         }
         copy_commit();  // (behind the last group, groups of nothing: the waits below count them)
-        src += GROUP * 16;
         to = to + GROUP == SC_RING * GROUP ? 0 : to + GROUP;
-        ++cb;
-        if (TWICE && !again && cb > full) {
-            again = true;
-            cb = 0;
-            src = s.src + threadIdx.x * 16;
-            policy = policy_drop();
+        if (TWICE && !again && cb == full) {
+            again = true;  // the same group once more
+            return;
         }
+        src += TWICE && again ? -GROUP * 16 : GROUP * 16;
+        cb += TWICE && again ? -1 : 1;
     }
     // the oldest group has arrived; this thread's first vector of it
     __device__ __forceinline__ uint4* first() const
@@ -457,9 +425,12 @@ template <typename E, int NT, bool TWICE> struct Ring {
 // Terms are 2^d with d = l c - B, c = log2(e) / t and B = m c rounded to an integer, m the reference: one exact product
 // and one rounding per logit, and sums of different m differ by powers of 2, exactly.  Where m c is so large that its
 // integer is no help (a row of the type's lowest values, say, where products with c overflow), d = (l - m) c instead.
-// A thread's reference is the first largest logit that it met, and moves only when one is 2^32 times above it: fp32 has
-// room for terms of that size, and moving at every new maximum is a long chain of dependent instructions that some lane
-// of a warp would ask for at most vectors (a verify batch's rows: 35 -> 25 us per 160 MB).
+// A thread's reference is the first largest logit that it met, and moves only when one is 2^AWAY times above it: fp32
+// has room for terms of that size, and moving at every new maximum is a long chain of dependent instructions that some
+// lane of a warp would ask for at most vectors (608 x 131072 bf16: 38.8 -> 30.3 us).  The sum of d 2^d is as inexact as
+// the largest d in it times an ulp of the sum of 2^d, and the entropy is what is left of ln of the one minus the other:
+// with entropies AWAY is 4, which costs up to 1.5 us of a verify batch's 38 and leaves them 2e-7 off, where 32 leaves
+// 3e-6.
 __device__ __forceinline__ bool plain_ref(float m, float c) { return fabsf(m * c) < 4194304.f; }
 __device__ __forceinline__ float dist(float l, float m, float c)
 {
@@ -488,6 +459,7 @@ __device__ __forceinline__ void to_max(Run& r, float m, float c)
 // sums of a thread's vectors, by ENTROPY those of d 2^d too; with RANK also the number of elements above x (in vectors
 // before tvec: or equal to it, written as above the next value below x)
 template <typename E, bool ENTROPY, bool RANK> struct Summer {
+    static constexpr float AWAY = ENTROPY ? 4.f : 32.f;
     float m = -INFINITY, limit = -INFINITY, c;
     uint64_t s2 = 0, t2 = 0;
     uint32_t masked = 0;  // ENTROPY: batches where d is -inf or may be relative to the row's m; the last bit has all behind 30
@@ -531,7 +503,7 @@ template <typename E, bool ENTROPY, bool RANK> struct Summer {
                 s2 = mul2(f2, s2);
             }
             m = mn;
-            limit = mn + 32.f / c;
+            limit = mn + AWAY / c;
         }
         const uint64_t t0 = t2;
         const bool fast = plain_ref(m, c);
@@ -671,7 +643,7 @@ __device__ __forceinline__ void grad_slice_(R& ring, const uint4& edge, E* g, fl
     constexpr int NT = R::GROUP / SC_GROUP;
     const Slice<E>& s = ring.s;
     const float ref = FAST ? -rintf(m * c) : m == -INFINITY ? 0.f : -m;
-    const uint64_t r2 = pair(ref, ref), c2 = pair(c, c), policy = policy_drop();
+    const uint64_t r2 = pair(ref, ref), c2 = pair(c, c);
     auto grad = [&](const uint4& x, auto clamp) {
         uint64_t v[EPV<E> / 2], y[EPV<E> / 2];
         Vec<E>::pairs(x, v);
@@ -684,6 +656,8 @@ __device__ __forceinline__ void grad_slice_(R& ring, const uint4& edge, E* g, fl
         }
         return Vec<E>::pack(y);
     };
+    // streaming stores: L2 has better use for its lines
+    auto store = [](char* to, const uint4& w) { __stcs((uint4*)to, w); };
     auto is_masked = [&](int b) { return masked >> min(b, 31) & 1; };
     auto any = [&](const uint4& x, int b) {
         return is_masked(b) ? grad(x, std::true_type()) : grad(x, std::false_type());
@@ -697,11 +671,17 @@ __device__ __forceinline__ void grad_slice_(R& ring, const uint4& edge, E* g, fl
             if (q >= q0 && q < q1 && e + q >= 0 && e + q < ring.V) ((Bits<E>*)g)[e + q] = bits_at<E>(w, q);
     };
     const int a = (int)((-(intptr_t)out) & 15);  // bytes from a vector's place to the next 16-byte boundary
-    int i = threadIdx.x;
+    int i = threadIdx.x + ring.full * R::GROUP;
     if (a == 0) {
         char* to = out + (int64_t)i * 16;
+        const uint4* last = ring.first();
+        for (int j = 0; j < SC_GROUP; ++j)
+            if (i + j * NT >= s.lo && i + j * NT < s.hi) store(to + j * NT * 16, any(last[j * NT], ring.full));
+        ring.used();
 #pragma unroll 1
-        for (int b = 0; b < ring.full; ++b, i += R::GROUP, to += R::GROUP * 16) {
+        for (int b = ring.full - 1; b >= 0; --b) {
+            i -= R::GROUP;
+            to -= R::GROUP * 16;
             const uint4* v = ring.first();
             uint4 w[SC_GROUP];
             if (is_masked(b)) {
@@ -711,27 +691,25 @@ __device__ __forceinline__ void grad_slice_(R& ring, const uint4& edge, E* g, fl
 #pragma unroll
                 for (int j = 0; j < SC_GROUP; ++j) w[j] = grad(v[j * NT], std::false_type());
             }
-            if (b > 0 || i >= s.lo) store16<0>(to, w[0], policy);
-            store16<NT * 16>(to, w[1], policy);
-            store16<2 * NT * 16>(to, w[2], policy);
-            store16<3 * NT * 16>(to, w[3], policy);
+            if (b > 0 || i >= s.lo) store(to, w[0]);
+            store(to + NT * 16, w[1]);
+            store(to + 2 * NT * 16, w[2]);
+            store(to + 3 * NT * 16, w[3]);
             ring.used();
         }
-        const uint4* v = ring.first();
-        for (; i < s.hi; i += NT, v += NT, to += NT * 16)
-            if (i >= s.lo) store16<0>(to, any(*v, ring.full), policy);
     } else {
         // the gradient's rows begin elsewhere in a vector than the logits': lanes have neighbouring vectors, and join
         // them two by two to what lies between boundaries
         const int lane = threadIdx.x % 32, q = a / (int)sizeof(E);
-        for (int b = 0; b <= ring.full; ++b) {
+        for (int b = ring.full; b >= 0; --b) {
             const uint4* v = ring.first();
-            for (int j = 0; j < SC_GROUP; ++j, i += NT) {
+            for (int j = 0; j < SC_GROUP; ++j) {
+                const int i = threadIdx.x + b * R::GROUP + j * NT;
                 if (i - lane >= s.hi) continue;  // none of the warp's
                 const bool in = i >= s.lo && i < s.hi;
                 const uint4 w = in ? any(v[j * NT], b) : no_vector<E>(), two = joined(w, a);
                 if (!in) continue;
-                if (lane < 31 && i + 1 < s.hi) store16<0>(out + (int64_t)i * 16 + a, two, policy);
+                if (lane < 31 && i + 1 < s.hi) store(out + (int64_t)i * 16 + a, two);
                 else elements(w, i, q, EPV<E>);
                 if (lane == 0 || i == s.lo) elements(w, i, 0, q);
             }
@@ -832,14 +810,18 @@ cudaError_t score_split_forward(K kernel, ScoreKernel& sk, ScoreParams& p, size_
     }
     return cudaSuccess;
 }
-// CTAs of a row with a gradient, two of them an SM (their shared memory sees to it): as many as it takes for the rows
-// under way to stay in L2 between their two passes, with room for what else lies there; and few rows are spread over
-// more, for the SMs that would idle, while every thread has a vector or two.
-constexpr size_t SC_GRAD_BYTES = 100 * 1024;
+// CTAs of a row with a gradient, four of them an SM (their shared memory sees to it): as many as it takes for the rows
+// under way to stay in L2 between their two passes, or all but a little of them, since the second pass begins with what
+// was read last; and few rows are spread over more, for the SMs that would idle, while every thread has a vector or
+// two.  2000 x 128256 bf16, 600 rows under way of 257 KB each: 208 us with two CTAs a row, 231 with one; 512 such rows
+// of a distillation loss, which one CTA each keeps under 140 MB: 62 with one, 64 with two.  Two CTAs an SM of 256
+// threads take 214 and 67, and 28 instead of 26 for 300 x 32000 fp32; 1500 x 100003 fp16 alone is faster with them
+// (138 instead of 147).
+constexpr size_t SC_GRAD_BYTES = 46 * 1024;
 inline void score_split_gradient(ScoreParams& p, size_t size, int num_sms)
 {
     const int row = score_vectors(p, size);
-    const double under_way = 2.0 * num_sms < p.rows ? 2.0 * num_sms : p.rows;
+    const double under_way = 4.0 * num_sms < p.rows ? 4.0 * num_sms : p.rows;
     int C = 1;
     while (C < SC_MAXC && ((under_way / C) * row * 16 > SCORE_L2_ROWS ||
                            ((int64_t)p.rows * C < 2 * num_sms && row / (2 * C) >= SC_NT_GRAD)))
