@@ -418,11 +418,11 @@ template <typename E> cudaError_t go(ScoreParams p, int num_sms, cudaStream_t s)
     if (!p.grad) {
         const auto kernel = k_score_distill<E>;
         constexpr size_t smem = RING_BYTES<SC_NT>;
-        cudaError_t e = score_ready(kernel, sk[0], smem);
-        if (e == cudaSuccess) e = score_split_forward(kernel, sk[0], p, sizeof(E), 32, [](size_t) { return smem; });
+        cudaError_t e = score_ready(kernel, sk[0], SC_NT, smem, smem);
+        if (e == cudaSuccess) e = score_split_forward(sk[0], p, sizeof(E), num_sms, 32, [](size_t) { return smem; });
         return e == cudaSuccess ? score_launch(kernel, p, SC_NT, smem, s) : e;
     }
-    const cudaError_t e = score_ready(k_score_distill_grad<E>, sk[1], SC_GRAD_BYTES);
+    const cudaError_t e = score_ready(k_score_distill_grad<E>, sk[1], SC_NT_GRAD, SC_GRAD_BYTES, SC_GRAD_BYTES);
     if (e != cudaSuccess) return e;
     score_split_gradient(p, sizeof(E), num_sms);
     return score_launch(k_score_distill_grad<E>, p, SC_NT_GRAD, SC_GRAD_BYTES, s);

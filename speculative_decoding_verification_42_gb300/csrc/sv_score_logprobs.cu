@@ -92,12 +92,20 @@ __device__ void give_candidates(const Slice<E>& sl, int V, int full, TopScratch&
             const bool first = owner == 0 && sl.lo && sl.n, last = owner == 32 && sl.hi < sl.n;
             at[SC_GROUP] = first ? 0 : sl.n - 1;
             w[SC_GROUP] = g == full && (first || last) ? load_vector(sl, V, at[SC_GROUP]) : no_vector<E>();
+            // first which elements they are, then one of each lane's at a time: lanes have them at different places
+            unsigned long long hits = 0;
 #pragma unroll
             for (int j = 0; j <= SC_GROUP; ++j)
-                if (Vec<E>::top(w[j]) >= least)
-                    each_of<E>(w[j], sl.first + at[j] * EPV<E>, [&](uint32_t key, int id) {
-                        if (key >= bound) give(key, id);
-                    });
+#pragma unroll
+                for (int q = 0; q < EPV<E>; ++q)
+                    if (value_of<E>(bits_at<E>(w[j], q)) >= least) hits |= 1ull << (j * EPV<E> + q);
+            while (hits) {
+                const int h = __ffsll(hits) - 1, j = h / EPV<E>;
+                hits &= hits - 1;
+                const int e = (j == SC_GROUP ? at[SC_GROUP] : (g * SC_GROUP + j) * SC_NT + owner) * EPV<E> + h % EPV<E>;
+                const uint32_t key = key_of(widen(((const E*)sl.src)[e]));
+                if (key >= bound) give(key, sl.first + e);
+            }
         }
     }
     __syncthreads();
@@ -442,15 +450,15 @@ template <typename E> __global__ void __launch_bounds__(SC_NT_GRAD, 4) k_score_l
     }
 }
 
-template <typename E, bool TOP> cudaError_t go_forward(ScoreParams p, cudaStream_t s)
+template <typename E, bool TOP> cudaError_t go_forward(ScoreParams p, int num_sms, cudaStream_t s)
 {
     static ScoreKernel sk;
     const auto kernel = k_score_logprobs<E, TOP>;
     auto smem = [](size_t per) {
         return RING_BYTES<SC_NT> + (TOP ? sizeof(TopScratch) + (per / (SC_NT * SC_GROUP) + 2) * SC_NT * sizeof(E) : 0);
     };
-    cudaError_t e = score_ready(kernel, sk, smem(SCORE_MAX_ROW_BYTES / 16 + 2));
-    if (e == cudaSuccess) e = score_split_forward(kernel, sk, p, sizeof(E), TOP ? 48 : 16, smem);
+    cudaError_t e = score_ready(kernel, sk, SC_NT, smem(0), smem(SCORE_MAX_ROW_BYTES / 16 + 2));
+    if (e == cudaSuccess) e = score_split_forward(sk, p, sizeof(E), num_sms, TOP ? 48 : 16, smem);
     return e == cudaSuccess ? score_launch(kernel, p, SC_NT, smem(p.per), s) : e;
 }
 template <typename E> cudaError_t go(ScoreParams p, int num_sms, cudaStream_t s)
@@ -458,14 +466,14 @@ template <typename E> cudaError_t go(ScoreParams p, int num_sms, cudaStream_t s)
     if (!p.grad || p.top_n || p.rank) {
         ScoreParams q = p;
         q.grad = nullptr;
-        const cudaError_t e = p.top_n ? go_forward<E, true>(q, s) : go_forward<E, false>(q, s);
+        const cudaError_t e = p.top_n ? go_forward<E, true>(q, num_sms, s) : go_forward<E, false>(q, num_sms, s);
         if (e != cudaSuccess || !p.grad) return e;
         // the gradient's kernel writes none of that again
         p.top_n = 0;
         p.rank = nullptr;
     }
     static ScoreKernel sk;
-    const cudaError_t e = score_ready(k_score_logprobs_grad<E>, sk, SC_GRAD_BYTES);
+    const cudaError_t e = score_ready(k_score_logprobs_grad<E>, sk, SC_NT_GRAD, SC_GRAD_BYTES, SC_GRAD_BYTES);
     if (e != cudaSuccess) return e;
     score_split_gradient(p, sizeof(E), num_sms);
     return score_launch(k_score_logprobs_grad<E>, p, SC_NT_GRAD, SC_GRAD_BYTES, s);

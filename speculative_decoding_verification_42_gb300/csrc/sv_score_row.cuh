@@ -18,7 +18,6 @@
 // outside the row is -inf, which counts nowhere.
 #pragma once
 
-#include <atomic>
 #include <type_traits>
 
 #include "sv_score.cuh"
@@ -726,11 +725,11 @@ __device__ __forceinline__ void grad_slice(R& ring, const uint4& edge, E* g, flo
 }
 
 // ---- launches ------------------------------------------------------------------ //
-// A kernel's launch set-up on each device, and its resident clusters by CTAs of a cluster and their shared memory, as
-// last asked of the runtime: one word holds both and the answer.
+// A kernel's launch set-up on each device, and the clusters of 1, 2, 4 .. CTAs that are resident there with the least of
+// shared memory that it takes.
 struct ScoreKernel {
     DeviceOnce once;
-    std::atomic<uint64_t> known[SV_MAX_DEVICES][64] = {};
+    int clusters[SV_MAX_DEVICES][4] = {};
 };
 struct ScoreLaunch {
     cudaLaunchConfig_t cfg = {};
@@ -749,32 +748,19 @@ struct ScoreLaunch {
     }
 };
 
-// to be called before the others: up to `most` bytes of shared memory for the kernel
-template <typename K> cudaError_t score_ready(K kernel, ScoreKernel& sk, size_t most)
-{
-    return cuda_once(sk.once, nullptr, [&](int, int*) {
-        return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
-    });
-}
+// to be called before the others: `least` to `most` bytes of shared memory for the kernel
 template <typename K>
-cudaError_t score_resident(K kernel, ScoreKernel& sk, int C, int threads, size_t smem, int* clusters)
+cudaError_t score_ready(K kernel, ScoreKernel& sk, int threads, size_t least, size_t most)
 {
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    const uint64_t key = (uint64_t)C << 24 | smem / 16;
-    std::atomic<uint64_t>& word = sk.known[dev][(smem / 16 * 9 + C) % 64];
-    const uint64_t seen = word.load(std::memory_order_relaxed);
-    if (seen >> 32 == key) {
-        *clusters = (int)(seen & 0xFFFFFFFFu);
-        return cudaSuccess;
-    }
-    const ScoreLaunch l(C, threads, smem, nullptr);
-    e = cudaOccupancyMaxActiveClusters(clusters, kernel, &l.cfg);
-    if (e != cudaSuccess) return e;
-    if (*clusters < 1) *clusters = 1;
-    word.store(key << 32 | (uint32_t)*clusters, std::memory_order_relaxed);
-    return cudaSuccess;
+    static_assert(SC_MAXC == 8, "four powers of two");
+    return cuda_once(sk.once, nullptr, [&](int dev, int*) {
+        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
+        for (int i = 0; i < 4 && e == cudaSuccess; ++i) {
+            const ScoreLaunch l(1 << i, threads, least, nullptr);
+            e = cudaOccupancyMaxActiveClusters(&sk.clusters[dev][i], kernel, &l.cfg);
+        }
+        return e;
+    });
 }
 
 // Launches a cluster of p.cluster CTAs for every row.
@@ -791,17 +777,20 @@ inline int score_vectors(const ScoreParams& p, size_t size) { return (int)(((siz
 
 // CTAs of a row in a forward pass, by the time that each power of two would take: the rows that a resident cluster has
 // one after another (and half a row for those that end last), each of a slice's vectors and a cost that does not shrink
-// with it (`fixed`, in vectors of a thread).  smem_of: bytes for a slice.
-template <typename K, typename F>
-cudaError_t score_split_forward(K kernel, ScoreKernel& sk, ScoreParams& p, size_t size, int fixed, F smem_of)
+// with it (`fixed`, in vectors of a thread).  smem_of: bytes for a slice, which may leave room for fewer CTAs on an SM.
+template <typename F>
+cudaError_t score_split_forward(const ScoreKernel& sk, ScoreParams& p, size_t size, int num_sms, int fixed, F smem_of)
 {
+    constexpr size_t SM_BYTES = 228 * 1024, AROUND = 2048;  // of an SM, and what a CTA takes besides
     const int row = score_vectors(p, size);
+    int dev = 0;
+    const cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
     double best = 0;
-    for (int C = 1; C <= SC_MAXC && (C == 1 || row / C >= SC_NT); C *= 2) {
-        const int per = (row + C - 1) / C;
-        int nc = 0;
-        const cudaError_t e = score_resident(kernel, sk, C, SC_NT, smem_of(per), &nc);
-        if (e != cudaSuccess) return e;
+    for (int i = 0; i < 4 && (i == 0 || row >> i >= SC_NT); ++i) {
+        const int C = 1 << i, per = (row + C - 1) / C;
+        const int fit = num_sms * (int)(SM_BYTES / (smem_of(per) + AROUND)) / C;
+        const int nc = max(1, min(sk.clusters[dev][i], fit));
         const double rounds = p.rows <= nc ? 1.0 : (double)p.rows / nc + 0.5, cost = rounds * ((double)per / SC_NT + fixed);
         if (C > 1 && cost >= best) continue;
         best = cost;
