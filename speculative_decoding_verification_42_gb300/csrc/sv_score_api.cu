@@ -89,7 +89,7 @@ spec_status spec_score_logprobs(const spec_score_logprobs_args* a, void* stream)
                                       a->grad, a->row_status, &empty);
     if (st != SPEC_OK) return st;
     if (a->top_n < 0 || ((a->logprob || a->rank || a->grad_logprob) && !a->ids && !empty) ||
-        (a->top_n > 0 && (!a->top_ids || !a->top_logprobs) && !empty) ||
+        (a->top_n > 0 && a->top_n <= SPEC_SCORE_MAX_TOP && (!a->top_ids || !a->top_logprobs) && !empty) ||
         (!empty && (a->grad.ptr != nullptr) != (a->grad_logprob || a->grad_entropy)))
         return SPEC_ERR_INVALID_ARG;
     if (a->top_n > SPEC_SCORE_MAX_TOP || !on(a->ids, 4) || !on(a->grad_logprob, 4) || !on(a->grad_entropy, 4) ||

@@ -256,11 +256,12 @@ __device__ __forceinline__ KdRow join(const KdPart* parts, const EntryShared<NT>
     return row;
 }
 
-// h(q, p); lr: ln(q / p), for a p too small for a quotient
-__device__ __forceinline__ float divergence(float q, float p, float lr)
+// h(q, p); for a p too small for a quotient, ln(q / p) = a - b inv_temp, b the distance of a logit, which its product
+// with 1 / t may take out of range where that with q too is in it
+__device__ __forceinline__ float divergence(float q, float p, float a, float b, float inv_temp)
 {
     if (q == 0.f) return p;
-    if (!(p > 1e-30f)) return q * lr - q + p;
+    if (!(p > 1e-30f)) return q * a - q * b * inv_temp - q + p;
     const float d = (q - p) / p;
     return fabsf(d) < 0.5f ? p * ((1.f + d) * log1pf(d) - d) : q * logf(q / p) - q + p;
 }
@@ -277,7 +278,7 @@ __device__ __forceinline__ void finish(const ScoreParams& p, int r, const KdRow&
 #pragma unroll
     for (int u = 0; u < EPT<NT>; ++u) {
         const float pi = ex2_fast(dist(l[u], row.m, p.c)) * row.inv_z;
-        h += divergence(te.q[u], pi, te.lq[u] - ((l[u] - row.m) * p.inv_temp - ln_z));
+        h += divergence(te.q[u], pi, te.lq[u] + ln_z, l[u] - row.m, p.inv_temp);
         acc += fminf(te.q[u], pi);
     }
     h = warp_sum(h);
@@ -296,10 +297,9 @@ __device__ __forceinline__ void finish(const ScoreParams& p, int r, const KdRow&
         const float pr = row.sr * row.scale * row.inv_z;
         if (p.tail) {
             // ln of the rest's share, from the logarithms of both sums and the distance of their references
-            const float ln_pr = row.sr > 0.f ? (row.mr - row.m) * p.inv_temp + logf(row.sr) -
-                                                   dist(row.mr, row.mr, p.c) * LN2 - ln_z
-                                             : -INFINITY;
-            h += divergence(te.left, pr, logf(te.left) - ln_pr) + fmaxf(0.f, te.in - 1.f);
+            const float ln_r = row.sr > 0.f ? logf(row.sr) - dist(row.mr, row.mr, p.c) * LN2 : 0.f;
+            h += divergence(te.left, pr, logf(te.left) - ln_r + ln_z, row.sr > 0.f ? row.mr - row.m : -INFINITY,
+                            p.inv_temp) + fmaxf(0.f, te.in - 1.f);
         } else {
             h += pr;
         }

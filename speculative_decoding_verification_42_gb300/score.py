@@ -112,7 +112,15 @@ def _shape(t, what):
         raise ValueError(f"{what} must be [B, T, V] or [N, V], got {tuple(shape)}")
     if not t.is_cuda:
         raise ValueError(f"{what} must be on a CUDA device, got {t.device}")
+    if max(shape) > 0x7FFFFFFF:  # (an expanded tensor may well be)
+        raise ValueError(f"{what} must have sizes below 2^31, got {tuple(shape)}")
     return shape
+
+
+def _temperature(t) -> float:
+    """A number that fp32 holds, where there is one; the library refuses the others."""
+    t = float(t)
+    return t if -1e38 < t < 1e38 else float("nan")
 
 
 def _tensor(t, shape, dtype, device, what):
@@ -184,13 +192,14 @@ def logprobs(logits, tokens=None, *, temperature: float = 1.0, top_n: int = 0, r
             rk = _result(res, out, "rank", lead, i32, dev)
     ent, lse = _result(res, out, "entropy", lead, f32, dev), _result(res, out, "lse", lead, f32, dev)
     status = _result(res, out, "row_status", lead, i32, dev)
-    if top_n > 0:
+    top_n = max(-1, min(top_n, SPEC_SCORE_MAX_TOP + 1))  # the library refuses both, and nothing is allocated for them
+    if 0 < top_n <= SPEC_SCORE_MAX_TOP:
         ti = _result(res, out, "top_ids", (*lead, top_n), i32, dev)
         tl = _result(res, out, "top_logprobs", (*lead, top_n), f32, dev)
     if grad_logprob is not None or grad_entropy is not None:
         grad = _grad(out, logits, res)
-    _run("spec_score_logprobs", _LOGPROBS_ARGS.pack(dev.index, code, B, T, V, top_n, temperature, *rows, ids, *up, lp,
-                                                    rk, ent, lse, ti, tl, status, *grad), dev)
+    _run("spec_score_logprobs", _LOGPROBS_ARGS.pack(dev.index, code, B, T, V, top_n, _temperature(temperature), *rows,
+                                                    ids, *up, lp, rk, ent, lse, ti, tl, status, *grad), dev)
     return res
 
 
@@ -227,8 +236,9 @@ def distill(student, top_ids, teacher, *, temperature: float = 1.0, teacher_temp
             _result(res, out, "row_status", lead, torch.int32, dev))
     if grad_loss is not None:
         grad = _grad(out, student, res)
-    _run("spec_score_distill", _DISTILL_ARGS.pack(dev.index, code, t_code, B, T, V, k, bool(tail), temperature,
-                                                  temperature if teacher_temperature is None else teacher_temperature,
+    temp = _temperature(temperature)
+    t_temp = temp if teacher_temperature is None else _temperature(teacher_temperature)
+    _run("spec_score_distill", _DISTILL_ARGS.pack(dev.index, code, t_code, B, T, V, k, bool(tail), temp, t_temp,
                                                   *rows, *ins, *outs, *grad), dev)
     return res
 

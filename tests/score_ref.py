@@ -19,8 +19,8 @@ def softmax(l, temp):
 
 
 def adds(V):
-    """The longest chain of fp32 additions that a sum over a row may take: a CTA's
-    256 threads share at least an eighth of the row, or all of it, and tens join them."""
+    """The longest chain of fp32 additions that a sum over a row may take: the 128
+    threads of a CTA, with two sums each, share all of it at most, and tens join them."""
     return -(-V // 256) + 48
 
 

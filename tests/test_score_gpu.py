@@ -512,6 +512,47 @@ def test_refusals(sv):
     torch.cuda.synchronize()
 
 
+def test_numbers_out_of_range(sv):
+    """Numbers that a record of the library cannot hold are refused like its other bad ones, before anything is
+    allocated for them."""
+    import torch
+    x = torch.zeros(2, 8, device="cuda")
+    ids, val = torch.zeros(2, 1, dtype=torch.int32, device="cuda"), torch.zeros(2, 1, device="cuda")
+    torch.cuda.reset_peak_memory_stats()
+    before = torch.cuda.memory_allocated()
+    for code, call in [
+        (1, lambda: sv.logprobs(x, temperature=1e300)), (1, lambda: sv.distill(x, ids, val, temperature=1e300)),
+        (1, lambda: sv.distill(x, ids, val, teacher_temperature=-1e39)),
+        (2, lambda: sv.logprobs(x, top_n=2 ** 40)), (1, lambda: sv.logprobs(x, top_n=-2 ** 40)),
+    ]:
+        with pytest.raises(sv.SpecVerifyError) as e:
+            call()
+        assert e.value.code == code
+    for call in (lambda: sv.logprobs(x[:1].expand(2 ** 33, 8)),
+                 lambda: sv.distill(x[:1].expand(2 ** 33, 8), ids[:1].expand(2 ** 33, 1), val[:1].expand(2 ** 33, 1))):
+        with pytest.raises(ValueError):
+            call()
+    assert torch.cuda.max_memory_allocated() - before < 2 ** 20  # a few results of two rows
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("temp", [0.8, 0.25])
+def test_distill_losses_next_to_the_end_of_fp32(sv, kind, temp):
+    """Entries on tokens masked with the type's lowest value: their distance over the temperature is beyond fp32, the
+    teacher's small share of it is not."""
+    import torch
+    rng = np.random.default_rng(6)
+    N, V, k = 3, 500, 2
+    x = _logits(rng, N, V, kind)
+    ids = np.stack([rng.permutation(V)[:k] for _ in range(N)]).astype(np.int32)
+    for r in range(N):
+        x[r, ids[r].tolist()] = torch.finfo(x.dtype).min
+    t = (rng.standard_normal((N, k)) * 0.1 - 5).astype(np.float32)
+    got = sv.distill(x, _dev(ids), _dev(t), temperature=temp, teacher_temperature=1.0, tail=True)
+    assert got["loss"].isfinite().all() and (got["loss"] > 1e36).all()
+    _check_distill(got, _f64(x), ids, t.astype(np.float64), float(np.float32(temp)), 1.0, True, None, None, kind)
+
+
 def test_verify_then_score_then_distill(sv):
     """The operators as they are used together: a verify step with the log probabilities of
     what it emitted, the target's top logits recorded, and the draft's loss against them, whose
