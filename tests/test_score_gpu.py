@@ -1,6 +1,8 @@
 """The operators that score rows of logits on the GPU, against the plain 64-bit
 implementations of score_ref.py, at the sizes, values and layouts where they can
 go wrong.  Bounds come from the roundings the operators make (score_ref.py)."""
+import os
+
 import numpy as np
 import pytest
 
@@ -433,6 +435,32 @@ def test_repeatable_on_any_stream_and_captured(sv, kind, V):
         torch.cuda.synchronize()
         for n in want[i]:
             assert torch.equal(held[n], want[i][n]), n
+
+
+def test_first_calls_of_a_process_may_be_captured(sv):
+    import subprocess
+    import sys
+    code = """
+import torch
+import speculative_decoding_verification_42_gb300 as sv
+x = torch.randn(6, 5000, device="cuda")
+tok, w = torch.arange(6, device="cuda", dtype=torch.int32), torch.ones(6, device="cuda")
+def calls():
+    a = sv.logprobs(x, tok, top_n=4, rank=True, grad_logprob=w, grad_entropy=w)
+    return {**a, **sv.distill(x, a["top_ids"], a["top_logprobs"], tail=True, grad_loss=w)}
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    held = calls()
+graph.replay()
+torch.cuda.synchronize()
+now = calls()
+assert all(torch.equal(held[n], now[n]) for n in now)
+print("ok")
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.stdout.strip() == "ok", r.stderr[-2000:]
 
 
 def test_rows_beyond_two_to_the_31(sv):
