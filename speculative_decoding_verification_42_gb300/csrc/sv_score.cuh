@@ -62,7 +62,7 @@ cudaError_t launch_score_logprobs(const ScoreParams& p, int dtype, int num_sms, 
 cudaError_t launch_score_distill(const ScoreParams& p, int dtype, int num_sms, cudaStream_t s);
 
 constexpr int SCORE_MAX_CTAS = 8;                                    // of a row
-constexpr double SCORE_L2_ROWS = 140e6;                             // bytes of rows under way between two passes
+constexpr double SCORE_L2_ROWS = 100e6;                             // bytes of rows under way between two passes
 constexpr size_t SCORE_MAX_ROW_BYTES = SCORE_MAX_CTAS * 208 * 1024;  // of one row of logits
 
 }  // namespace sv

@@ -14,7 +14,7 @@ namespace sv {
 
 namespace {
 
-template <int NT> constexpr int EPT = (SPEC_SCORE_MAX_ENTRIES + NT - 1) / NT;  // entries of a thread: tid, tid + NT
+constexpr int EPT = (SPEC_SCORE_MAX_ENTRIES + SC_NT - 1) / SC_NT;  // entries of a thread: tid, tid + SC_NT
 
 __device__ __forceinline__ float teacher_value(const ScoreParams& p, int64_t at)
 {
@@ -34,7 +34,7 @@ struct KdRow {
 };
 __device__ __forceinline__ bool finite_row(float m) { return m > -INFINITY && m < INFINITY; }
 
-template <typename E, int NT> __device__ void no_distill(const ScoreParams& p, int r, int status, int rank, int C)
+template <typename E> __device__ void no_distill(const ScoreParams& p, int r, int status, int rank, int C)
 {
     if (rank == 0 && threadIdx.x == 0) {
         const float none = status == SPEC_ROW_OK ? 0.f : __int_as_float(0x7FFFFFFF);
@@ -42,18 +42,18 @@ template <typename E, int NT> __device__ void no_distill(const ScoreParams& p, i
         if (p.loss) p.loss[r] = none;
         if (p.accept) p.accept[r] = none;
     }
-    if (p.grad) zero_grad<E, NT>(p, r, rank, C);
+    if (p.grad) zero_grad<E>(p, r, rank, C);
 }
 
 // a row's entries, this thread's: token, teacher's value, the student's logit
-template <int NT> struct Entries {
-    int id[EPT<NT>];
-    float tv[EPT<NT>], l[EPT<NT>];
+struct Entries {
+    int id[EPT];
+    float tv[EPT], l[EPT];
     __device__ __forceinline__ void fetch(const ScoreParams& p, int r)
     {
 #pragma unroll
-        for (int u = 0; u < EPT<NT>; ++u) {
-            const int i = threadIdx.x + u * NT;
+        for (int u = 0; u < EPT; ++u) {
+            const int i = threadIdx.x + u * SC_NT;
             const bool in = r < p.rows && i < p.k;
             id[u] = in ? p.ids[(int64_t)r * p.k + i] : -1;
             tv[u] = in ? teacher_value(p, (int64_t)r * p.k + i) : -INFINITY;
@@ -62,20 +62,20 @@ template <int NT> struct Entries {
     template <typename E> __device__ __forceinline__ void fetch_logits(const E* x, int V)
     {
 #pragma unroll
-        for (int u = 0; u < EPT<NT>; ++u) l[u] = id[u] >= 0 && id[u] < V ? widen(x[id[u]]) : -INFINITY;
+        for (int u = 0; u < EPT; ++u) l[u] = id[u] >= 0 && id[u] < V ? widen(x[id[u]]) : -INFINITY;
     }
     __device__ __forceinline__ bool some() const
     {
         bool s = false;
 #pragma unroll
-        for (int u = 0; u < EPT<NT>; ++u) s |= id[u] != -1;
+        for (int u = 0; u < EPT; ++u) s |= id[u] != -1;
         return s;
     }
 };
 
 // the teacher's distribution over a row's entries, this thread's
-template <int NT> struct Teacher {
-    float q[EPT<NT>], lq[EPT<NT>];  // lq: ln q
+struct Teacher {
+    float q[EPT], lq[EPT];  // lq: ln q
     float in, left;               // sum of q, what it leaves of 1
 };
 
@@ -83,32 +83,32 @@ template <int NT> struct Teacher {
 // vectors they lie in (head, next), with their place there: copy group (the row's ends being group full + 1) and element
 // of the group.
 constexpr int SC_SEEN = 32768;  // places of ids
-template <int NT> struct EntryShared {
-    int32_t ids[EPT<NT> * NT];
-    int32_t next[EPT<NT> * NT], place[EPT<NT> * NT];
-    int32_t head[NT];
+struct EntryShared {
+    int32_t ids[EPT * SC_NT];
+    int32_t next[EPT * SC_NT], place[EPT * SC_NT];
+    int32_t head[SC_NT];
     uint32_t seen[SC_SEEN / 32];
     uint32_t state;                          // 1: a bad id; 2: two ids with one place in `seen`
-    float w_max[NT / 32], w_sum[NT / 32];
-    float w_me[NT / 32], w_se[NT / 32];  // the student's largest logit at a warp's entries, and the sum of their 2^d
+    float w_max[SC_NT / 32], w_sum[SC_NT / 32];
+    float w_me[SC_NT / 32], w_se[SC_NT / 32];  // the student's largest logit at a warp's entries, and the sum of their 2^d
 };
-template <int NT> __device__ __forceinline__ void clear(EntryShared<NT>& es)
+__device__ __forceinline__ void clear(EntryShared& es)
 {
     es.head[threadIdx.x] = -1;
-    for (int i = threadIdx.x; i < SC_SEEN / 32; i += NT) es.seen[i] = 0;
+    for (int i = threadIdx.x; i < SC_SEEN / 32; i += SC_NT) es.seen[i] = 0;
     if (threadIdx.x == 0) es.state = 0;
 }
 
 // Enters a row's entries (es is clear, and a barrier has passed): ids out of range and, maybe, ids that are there twice
 // go to `state`; the warps' largest teacher values to w_max.
-template <typename E, int NT>
-__device__ __forceinline__ void enter(const ScoreParams& p, EntryShared<NT>& es, Entries<NT>& en, const Slice<E>& sl, int full)
+template <typename E>
+__device__ __forceinline__ void enter(const ScoreParams& p, EntryShared& es, Entries& en, const Slice<E>& sl, int full)
 {
     const int tid = threadIdx.x;
     float tmax = -INFINITY;
 #pragma unroll
-    for (int u = 0; u < EPT<NT>; ++u) {
-        const int e = tid + u * NT, id = en.id[u];
+    for (int u = 0; u < EPT; ++u) {
+        const int e = tid + u * SC_NT, id = en.id[u];
         es.ids[e] = id;
         if (id == -1) {
             en.tv[u] = -INFINITY;
@@ -125,22 +125,22 @@ __device__ __forceinline__ void enter(const ScoreParams& p, EntryShared<NT>& es,
         const int i = (id - sl.first) / EPV<E>, q = (id - sl.first) % EPV<E>;
         if (i >= sl.n) continue;
         const bool inner = i >= sl.lo && i < sl.hi;
-        const int owner = inner ? i % NT : i < sl.lo ? 0 : 32;
-        es.place[e] = inner ? i / (NT * SC_GROUP) << 8 | i / NT % SC_GROUP * EPV<E> + q : (full + 1) << 8 | q;
+        const int owner = inner ? i % SC_NT : i < sl.lo ? 0 : 32;
+        es.place[e] = inner ? i / (SC_NT * SC_GROUP) << 8 | i / SC_NT % SC_GROUP * EPV<E> + q : (full + 1) << 8 | q;
         es.next[e] = atomicExch(es.head + owner, e);
     }
     tmax = warp_max(tmax);
     if (tid % 32 == 0) es.w_max[tid / 32] = tmax;
 }
 // after a barrier: whether the row is bad, for all CTAs of a cluster alike
-template <int NT> __device__ __forceinline__ bool bad_entries(const EntryShared<NT>& es, const Entries<NT>& en)
+__device__ __forceinline__ bool bad_entries(const EntryShared& es, const Entries& en)
 {
     if (es.state & 1) return true;
     if (!(es.state & 2)) return false;
     bool twice = false;
 #pragma unroll
-    for (int u = 0; u < EPT<NT>; ++u) {
-        const int e = threadIdx.x + u * NT, id = en.id[u];
+    for (int u = 0; u < EPT; ++u) {
+        const int e = threadIdx.x + u * SC_NT, id = en.id[u];
         if (id == -1) continue;
         for (int j = 0; j < e; j += 4) {
             const int4 o = *(const int4*)(es.ids + j);
@@ -151,10 +151,10 @@ template <int NT> __device__ __forceinline__ bool bad_entries(const EntryShared<
 }
 // The entries of a thread's vectors leave them, group by group.  (Which of two comes first in the chain is a matter of
 // chance, but both leave.)
-template <typename E, int NT> struct Leaving {
-    const EntryShared<NT>& es;
+template <typename E> struct Leaving {
+    const EntryShared& es;
     int group;  // the next with an entry
-    __device__ __forceinline__ explicit Leaving(const EntryShared<NT>& s) : es(s) { after(-1); }
+    __device__ __forceinline__ explicit Leaving(const EntryShared& s) : es(s) { after(-1); }
     __device__ __forceinline__ void after(int b)
     {
         group = INT32_MAX;
@@ -181,13 +181,12 @@ __device__ __forceinline__ bool dull(const ScoreParams& p, float tmax, float lse
     return !(tmax < INFINITY) || (!p.tail && tmax == -INFINITY) || !(fabsf(lse) < INFINITY);
 }
 // q up to the row's sum: differences first, and 1 / t in two parts, as the values may be large
-template <int NT>
-__device__ __forceinline__ void begin_teacher(const ScoreParams& p, EntryShared<NT>& es, const Entries<NT>& en, float tmax,
-                                              float lse, Teacher<NT>& te)
+__device__ __forceinline__ void begin_teacher(const ScoreParams& p, EntryShared& es, const Entries& en, float tmax,
+                                              float lse, Teacher& te)
 {
     float sum = 0.f;
 #pragma unroll
-    for (int u = 0; u < EPT<NT>; ++u) {
+    for (int u = 0; u < EPT; ++u) {
         te.q[u] = 0.f;
         te.lq[u] = -INFINITY;
         if (en.tv[u] > -INFINITY) {
@@ -200,33 +199,31 @@ __device__ __forceinline__ void begin_teacher(const ScoreParams& p, EntryShared<
     sum = warp_sum(sum);
     if (threadIdx.x % 32 == 0) es.w_sum[threadIdx.x / 32] = sum;
 }
-template <int NT>
-__device__ __forceinline__ void end_teacher(const ScoreParams& p, const EntryShared<NT>& es, Teacher<NT>& te)
+__device__ __forceinline__ void end_teacher(const ScoreParams& p, const EntryShared& es, Teacher& te)
 {
     float sum = 0.f;
 #pragma unroll
-    for (int i = 0; i < NT / 32; ++i) sum += es.w_sum[i];
+    for (int i = 0; i < SC_NT / 32; ++i) sum += es.w_sum[i];
     te.in = p.tail ? sum : 1.f;
     te.left = p.tail ? fmaxf(0.f, 1.f - sum) : 0.f;
     if (!p.tail) {
         const float ln = logf(sum), inv = 1.f / sum;
 #pragma unroll
-        for (int u = 0; u < EPT<NT>; ++u) {
+        for (int u = 0; u < EPT; ++u) {
             te.q[u] *= inv;
             te.lq[u] -= ln;
         }
     }
 }
 // the entries' sums of a warp
-template <int NT>
-__device__ __forceinline__ void sum_entries(const ScoreParams& p, EntryShared<NT>& es, const Entries<NT>& en)
+__device__ __forceinline__ void sum_entries(const ScoreParams& p, EntryShared& es, const Entries& en)
 {
     float me = -INFINITY, se = 0.f;
 #pragma unroll
-    for (int u = 0; u < EPT<NT>; ++u) me = fmax_nan(me, en.l[u]);
+    for (int u = 0; u < EPT; ++u) me = fmax_nan(me, en.l[u]);
     me = warp_max(me);
 #pragma unroll
-    for (int u = 0; u < EPT<NT>; ++u) se += ex2_fast(dist(en.l[u], me, p.c));
+    for (int u = 0; u < EPT; ++u) se += ex2_fast(dist(en.l[u], me, p.c));
     se = warp_sum(se);
     if (threadIdx.x % 32 == 0) {
         es.w_me[threadIdx.x / 32] = me;
@@ -234,22 +231,21 @@ __device__ __forceinline__ void sum_entries(const ScoreParams& p, EntryShared<NT
     }
 }
 // one warp: the row of the parts of n warps and of its entries
-template <int NT>
-__device__ __forceinline__ KdRow join(const KdPart* parts, const EntryShared<NT>& es, float c, int n)
+__device__ __forceinline__ KdRow join(const KdPart* parts, const EntryShared& es, float c, int n)
 {
     KdRow row = {-INFINITY, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     for (int i = threadIdx.x % 32; i < n; i += 32) row.mr = fmax_nan(row.mr, parts[i].m);
     row.mr = warp_max(row.mr);
     row.m = row.mr;
 #pragma unroll
-    for (int i = 0; i < NT / 32; ++i) row.m = fmax_nan(row.m, es.w_me[i]);
+    for (int i = 0; i < SC_NT / 32; ++i) row.m = fmax_nan(row.m, es.w_me[i]);
     for (int i = threadIdx.x % 32; i < n; i += 32)
         if (parts[i].m > -INFINITY) row.sr += parts[i].s * ex2_fast(between(parts[i].m, row.mr, c));
     row.sr = warp_sum(row.sr);
     row.scale = row.mr == -INFINITY ? 0.f : ex2_fast(between(row.mr, row.m, c));
     row.z = row.sr * row.scale;
 #pragma unroll
-    for (int i = 0; i < NT / 32; ++i)
+    for (int i = 0; i < SC_NT / 32; ++i)
         if (es.w_me[i] > -INFINITY) row.z += es.w_se[i] * ex2_fast(between(es.w_me[i], row.m, c));
     row.inv_z = 1.f / row.z;
     row.inv_sr = row.sr > 0.f ? 1.f / row.sr : 0.f;
@@ -267,16 +263,15 @@ __device__ __forceinline__ float divergence(float q, float p, float a, float b, 
 }
 
 // CTA 0: a row's loss and acceptance
-template <int NT>
-__device__ __forceinline__ void finish(const ScoreParams& p, int r, const KdRow& row, const Teacher<NT>& te,
-                                       const float (&l)[EPT<NT>])
+__device__ __forceinline__ void finish(const ScoreParams& p, int r, const KdRow& row, const Teacher& te,
+                                       const float (&l)[EPT])
 {
-    __shared__ float w_h[NT / 32], w_acc[NT / 32];
+    __shared__ float w_h[SC_NT / 32], w_acc[SC_NT / 32];
     const int tid = threadIdx.x, lane = tid % 32;
     const float ln_z = logf(row.z) - dist(row.m, row.m, p.c) * LN2;  // relative to m
     float h = 0.f, acc = 0.f;
 #pragma unroll
-    for (int u = 0; u < EPT<NT>; ++u) {
+    for (int u = 0; u < EPT; ++u) {
         const float pi = ex2_fast(dist(l[u], row.m, p.c)) * row.inv_z;
         h += divergence(te.q[u], pi, te.lq[u] + ln_z, l[u] - row.m, p.inv_temp);
         acc += fminf(te.q[u], pi);
@@ -290,7 +285,7 @@ __device__ __forceinline__ void finish(const ScoreParams& p, int r, const KdRow&
     __syncthreads();
     if (tid == 0) {
         h = acc = 0.f;
-        for (int i = 0; i < NT / 32; ++i) {
+        for (int i = 0; i < SC_NT / 32; ++i) {
             h += w_h[i];
             acc += w_acc[i];
         }
@@ -311,24 +306,24 @@ __device__ __forceinline__ void finish(const ScoreParams& p, int r, const KdRow&
     }
 }
 
-template <typename E, int NT, bool GRAD> __device__ __forceinline__ void distill_row(const ScoreParams& p)
+template <typename E, bool GRAD> __device__ __forceinline__ void distill_row(const ScoreParams& p)
 {
-    constexpr int W = NT / 32;
+    constexpr int W = SC_NT / 32;
     extern __shared__ __align__(16) unsigned char smem[];
-    __shared__ __align__(16) EntryShared<NT> es;
+    __shared__ __align__(16) EntryShared es;
     __shared__ KdPart parts[SC_MAXC * W];
     __shared__ KdRow s_row;
     const int C = p.cluster, rank = (int)cluster_rank(), r = cluster_id(), tid = threadIdx.x, lane = tid % 32;
-    Entries<NT> en;
+    Entries en;
     en.fetch(p, r);
     clear(es);
     if (!__syncthreads_or(en.some())) {
-        no_distill<E, NT>(p, r, SPEC_ROW_OK, rank, C);
+        no_distill<E>(p, r, SPEC_ROW_OK, rank, C);
         return;
     }
     const E* x = row_of<E>(p, r);
     const Slice<E> sl(p, x, rank);
-    Ring<E, NT, GRAD> ring(p, sl, rank, smem);
+    Ring<E, GRAD ? SC_RING_GRAD : SC_RING> ring(p, sl, rank, smem);
     en.fetch_logits(x, p.V);
     const uint4 edge = ring.edge();
     const float lse = p.teacher_lse ? p.teacher_lse[r] : 0.f;
@@ -340,21 +335,21 @@ template <typename E, int NT, bool GRAD> __device__ __forceinline__ void distill
     for (int i = 0; i < W; ++i) tmax = fmax_nan(tmax, es.w_max[i]);
     if (bad || dull(p, tmax, lse)) {
         copy_done();
-        no_distill<E, NT>(p, r, bad ? SPEC_ROW_BAD_TOKEN : SPEC_ROW_NONFINITE, rank, C);
+        no_distill<E>(p, r, bad ? SPEC_ROW_BAD_TOKEN : SPEC_ROW_NONFINITE, rank, C);
         return;
     }
     // every CTA of the cluster runs before another stores into its shared memory
     if (C > 1) cluster_arrive();
-    Teacher<NT> te;
+    Teacher te;
     begin_teacher(p, es, en, tmax, lse, te);
     if (GRAD || rank == 0) sum_entries(p, es, en);
-    Leaving<E, NT> leaving(es);
+    Leaving<E> leaving(es);
     Summer<E, false, false> rest;
     rest.c = p.c;
     rest.stream(
         ring, edge,
         [&](int b, uint4* v) {
-            if (b <= ring.full) leaving.template from<NT>(b, v);
+            if (b <= ring.full) leaving.template from<SC_NT>(b, v);
             else leaving.template from<1>(b, v);
         },
         [](int, float) {});
@@ -391,12 +386,12 @@ template <typename E, int NT, bool GRAD> __device__ __forceinline__ void distill
             grad_slice(ring, edge, g, row.mr, p.c, 0, [&](uint64_t, uint64_t e2) { return mul2(e2, pr2); });
             __syncthreads();  // the entries' elements are written last
 #pragma unroll
-            for (int u = 0; u < EPT<NT>; ++u)
+            for (int u = 0; u < EPT; ++u)
                 if (en.id[u] >= 0 && ring.has(en.id[u]))
                     g[en.id[u]] = narrow<E>(gl * (ps * ex2_fast(dist(en.l[u], row.m, p.c)) - te.q[u]));
         } else {
             copy_done();
-            zero_grad<E, NT>(p, r, rank, C);
+            zero_grad<E>(p, r, rank, C);
         }
         if (rank != 0) return;
     }
@@ -405,11 +400,11 @@ template <typename E, int NT, bool GRAD> __device__ __forceinline__ void distill
 
 template <typename E> __global__ void __launch_bounds__(SC_NT, 5) k_score_distill(const ScoreParams p)
 {
-    distill_row<E, SC_NT, false>(p);
+    distill_row<E, false>(p);
 }
-template <typename E> __global__ void __launch_bounds__(SC_NT_GRAD, 4) k_score_distill_grad(const ScoreParams p)
+template <typename E> __global__ void __launch_bounds__(SC_NT, 4) k_score_distill_grad(const ScoreParams p)
 {
-    distill_row<E, SC_NT_GRAD, true>(p);
+    distill_row<E, true>(p);
 }
 
 template <typename E> cudaError_t go(ScoreParams p, int num_sms, cudaStream_t s)
@@ -417,15 +412,15 @@ template <typename E> cudaError_t go(ScoreParams p, int num_sms, cudaStream_t s)
     static ScoreKernel sk[2];
     if (!p.grad) {
         const auto kernel = k_score_distill<E>;
-        constexpr size_t smem = RING_BYTES<SC_NT>;
-        cudaError_t e = score_ready(kernel, sk[0], SC_NT, smem, smem);
+        constexpr size_t smem = SC_RING * SC_GROUP_BYTES;
+        cudaError_t e = score_ready(kernel, sk[0], smem, smem);
         if (e == cudaSuccess) e = score_split_forward(sk[0], p, sizeof(E), num_sms, 32, [](size_t) { return smem; });
-        return e == cudaSuccess ? score_launch(kernel, p, SC_NT, smem, s) : e;
+        return e == cudaSuccess ? score_launch(kernel, p, smem, s) : e;
     }
-    const cudaError_t e = score_ready(k_score_distill_grad<E>, sk[1], SC_NT_GRAD, SC_GRAD_BYTES, SC_GRAD_BYTES);
+    const cudaError_t e = score_ready(k_score_distill_grad<E>, sk[1], SC_GRAD_BYTES, SC_GRAD_BYTES);
     if (e != cudaSuccess) return e;
     score_split_gradient(p, sizeof(E), num_sms);
-    return score_launch(k_score_distill_grad<E>, p, SC_NT_GRAD, SC_GRAD_BYTES, s);
+    return score_launch(k_score_distill_grad<E>, p, SC_GRAD_BYTES, s);
 }
 
 }  // namespace

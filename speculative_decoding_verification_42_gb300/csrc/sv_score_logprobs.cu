@@ -238,7 +238,7 @@ __device__ __forceinline__ void no_top(const ScoreParams& p, int r, int status)
 }
 
 // a row that is not scored, or has a bad token
-template <typename E, int NT> __device__ void no_logprobs(const ScoreParams& p, int r, int status, int rank, int C)
+template <typename E> __device__ void no_logprobs(const ScoreParams& p, int r, int status, int rank, int C)
 {
     if (rank == 0) {
         const float none = status == SPEC_ROW_OK ? 0.f : __int_as_float(0x7FFFFFFF);
@@ -251,7 +251,7 @@ template <typename E, int NT> __device__ void no_logprobs(const ScoreParams& p, 
         }
         no_top(p, r, status);
     }
-    if (p.grad) zero_grad<E, NT>(p, r, rank, C);
+    if (p.grad) zero_grad<E>(p, r, rank, C);
 }
 
 // one warp: the row of the parts of n warps
@@ -294,18 +294,18 @@ template <typename E, bool TOP> __global__ void __launch_bounds__(SC_NT, TOP ? 4
     const int C = p.cluster, rank = (int)cluster_rank(), r = cluster_id(), tid = threadIdx.x, lane = tid % 32;
     const int id = p.ids ? p.ids[r] : 0;
     if (id < 0 || id >= p.V) {
-        no_logprobs<E, SC_NT>(p, r, id == -1 ? SPEC_ROW_OK : SPEC_ROW_BAD_TOKEN, rank, C);
+        no_logprobs<E>(p, r, id == -1 ? SPEC_ROW_OK : SPEC_ROW_BAD_TOKEN, rank, C);
         return;
     }
     // every CTA of the cluster runs before another stores into its shared memory
     if (C > 1) cluster_arrive();
     const E* x = row_of<E>(p, r);
     const Slice<E> sl(p, x, rank);
-    Ring<E, SC_NT, false> ring(p, sl, rank, smem);
+    Ring<E, SC_RING> ring(p, sl, rank, smem);
     const E raw = x[id];
     const uint4 edge = ring.edge();
     const float xt = widen(raw);
-    TopScratch& ts = *(TopScratch*)(smem + RING_BYTES<SC_NT>);
+    TopScratch& ts = *(TopScratch*)(smem + SC_RING * SC_GROUP_BYTES);
     Bits<E>* const most = (Bits<E>*)(&ts + 1);
     int ahead = 0;
     Run run;
@@ -379,23 +379,23 @@ template <typename E, bool TOP> __global__ void __launch_bounds__(SC_NT, TOP ? 4
     write_top(p, r, ts, row, logf(row.s) - dist(row.m, row.m, p.c) * LN2, C);
 }
 
-template <typename E> __global__ void __launch_bounds__(SC_NT_GRAD, 4) k_score_logprobs_grad(const ScoreParams p)
+template <typename E> __global__ void __launch_bounds__(SC_NT, 4) k_score_logprobs_grad(const ScoreParams p)
 {
-    constexpr int NT = SC_NT_GRAD, W = NT / 32;
+    constexpr int W = SC_NT / 32;
     extern __shared__ __align__(16) unsigned char smem[];
     __shared__ LpPart parts[SC_MAXC * W];
     __shared__ LpRow s_row;
     const int C = p.cluster, rank = (int)cluster_rank(), r = cluster_id(), tid = threadIdx.x, lane = tid % 32;
     const int id = p.ids ? p.ids[r] : 0;
     if (id < 0 || id >= p.V) {
-        no_logprobs<E, NT>(p, r, id == -1 ? SPEC_ROW_OK : SPEC_ROW_BAD_TOKEN, rank, C);
+        no_logprobs<E>(p, r, id == -1 ? SPEC_ROW_OK : SPEC_ROW_BAD_TOKEN, rank, C);
         return;
     }
     // every CTA of the cluster runs before another stores into its shared memory
     if (C > 1) cluster_arrive();
     const E* x = row_of<E>(p, r);
     const Slice<E> sl(p, x, rank);
-    Ring<E, NT, true> ring(p, sl, rank, smem);
+    Ring<E, SC_RING_GRAD> ring(p, sl, rank, smem);
     const float xt = widen(x[id]);
     const uint4 edge = ring.edge();
     Summer<E, true, false> sum;
@@ -428,7 +428,7 @@ template <typename E> __global__ void __launch_bounds__(SC_NT_GRAD, 4) k_score_l
     const LpRow row = s_row;
     if (!finite_row(row.m)) {
         copy_done();
-        zero_grad<E, NT>(p, r, rank, C);
+        zero_grad<E>(p, r, rank, C);
         return;
     }
     // e (A + B d), e = 2^d: p = e / s, ln p = d ln 2 - ln s
@@ -455,11 +455,11 @@ template <typename E, bool TOP> cudaError_t go_forward(ScoreParams p, int num_sm
     static ScoreKernel sk;
     const auto kernel = k_score_logprobs<E, TOP>;
     auto smem = [](size_t per) {
-        return RING_BYTES<SC_NT> + (TOP ? sizeof(TopScratch) + (per / (SC_NT * SC_GROUP) + 2) * SC_NT * sizeof(E) : 0);
+        return SC_RING * SC_GROUP_BYTES + (TOP ? sizeof(TopScratch) + (per / (SC_NT * SC_GROUP) + 2) * SC_NT * sizeof(E) : 0);
     };
-    cudaError_t e = score_ready(kernel, sk, SC_NT, smem(0), smem(SCORE_MAX_ROW_BYTES / 16 + 2));
+    cudaError_t e = score_ready(kernel, sk, smem(0), smem(SCORE_MAX_ROW_BYTES / 16 + 2));
     if (e == cudaSuccess) e = score_split_forward(sk, p, sizeof(E), num_sms, TOP ? 48 : 16, smem);
-    return e == cudaSuccess ? score_launch(kernel, p, SC_NT, smem(p.per), s) : e;
+    return e == cudaSuccess ? score_launch(kernel, p, smem(p.per), s) : e;
 }
 template <typename E> cudaError_t go(ScoreParams p, int num_sms, cudaStream_t s)
 {
@@ -473,10 +473,10 @@ template <typename E> cudaError_t go(ScoreParams p, int num_sms, cudaStream_t s)
         p.rank = nullptr;
     }
     static ScoreKernel sk;
-    const cudaError_t e = score_ready(k_score_logprobs_grad<E>, sk, SC_NT_GRAD, SC_GRAD_BYTES, SC_GRAD_BYTES);
+    const cudaError_t e = score_ready(k_score_logprobs_grad<E>, sk, SC_GRAD_BYTES, SC_GRAD_BYTES);
     if (e != cudaSuccess) return e;
     score_split_gradient(p, sizeof(E), num_sms);
-    return score_launch(k_score_logprobs_grad<E>, p, SC_NT_GRAD, SC_GRAD_BYTES, s);
+    return score_launch(k_score_logprobs_grad<E>, p, SC_GRAD_BYTES, s);
 }
 
 }  // namespace

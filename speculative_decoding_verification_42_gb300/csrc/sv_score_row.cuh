@@ -10,8 +10,9 @@
 //   forward    one cluster per row: four or more CTAs share an SM, and two that
 //              stream keep HBM busy while others begin or end
 //   gradient   the row's sum comes before the gradient's first element, so the
-//              row is streamed twice, the second time from L2: as many rows are
-//              under way as it holds
+//              row is streamed twice, the second time in reverse: first what the
+//              rings still hold, then the rest from L2, where as many rows are
+//              under way as it has room for
 //
 // Slices are whole 16-byte vectors of the row's addresses, so rows of any
 // alignment are copied and read alike; what a row's first and last vector have
@@ -26,12 +27,12 @@ namespace sv {
 
 namespace {
 
-constexpr int SC_NT = 128;               // threads of a CTA in the forward passes,
-constexpr int SC_NT_GRAD = 128;          // and with a gradient
+constexpr int SC_NT = 128;               // threads of a CTA
 constexpr int SC_GROUP = 4;              // vectors of a thread in a copy group
-constexpr int SC_RING = 4;               // groups of a ring
+constexpr int SC_RING = 4;               // groups of a ring in the forward passes,
+constexpr int SC_RING_GRAD = 6;          // and with a gradient
 constexpr int SC_MAXC = SCORE_MAX_CTAS;  // CTAs of a cluster (portable)
-template <int NT> constexpr int RING_BYTES = SC_RING * SC_GROUP * NT * 16;
+constexpr int SC_GROUP_BYTES = SC_GROUP * SC_NT * 16;
 constexpr float LN2 = 0.693147180559945f;
 constexpr float NONE = -200.f;  // a power of 2 that is 0 in fp32; products with it are, too, and with -inf are not
 
@@ -344,26 +345,23 @@ __device__ __forceinline__ void copy_done() { asm volatile("cp.async.wait_group 
 // ---- a ring of copy groups ----------------------------------------------------- //
 // A group is SC_GROUP vectors of every thread; a slice has `full` groups and one of what is left (up to SC_GROUP
 // vectors a thread).  The row's last vector and its first, if that is not the row's as a whole, are no part of the ring:
-// thread 32 has the last, thread 0 the first, in registers (edge).  TWICE: the slice comes a second time, its last group
-// first: what was read last is the likeliest to be in L2 still, where a second pass in the same order would find each
-// line just gone.
-template <typename E, int NT, bool TWICE> struct Ring {
-    static constexpr int GROUP = NT * SC_GROUP;  // vectors
+// thread 32 has the last, thread 0 the first, in registers (edge).  After turn() the slice comes a second time, its last
+// group first: the ring has the last ones still, and of the others what was read last is the likeliest to be in L2.
+template <typename E, int RING> struct Ring {
+    static constexpr int GROUP = SC_NT * SC_GROUP;  // vectors
     const Slice<E>& s;
     uint4* buf;
     int V, full;
     const char* src;   // this thread's first vector of the next group to be copied,
     int cb, to, from;  // that group and its place; the place of the next to be used
-    bool again;        // TWICE: the copies are those of the second time
 
     __device__ __forceinline__ Ring(const ScoreParams& p, const Slice<E>& sl, int rank, void* smem)
-        : s(sl), buf((uint4*)smem + threadIdx.x), V(p.V), src(sl.src + threadIdx.x * 16), cb(0), to(0), from(0),
-          again(false)
+        : s(sl), buf((uint4*)smem + threadIdx.x), V(p.V), src(sl.src + threadIdx.x * 16), cb(0), to(0), from(0)
     {
         const int least = (p.V * (int)sizeof(E) + 15) / 16 - rank * p.per;
         full = max(0, min(p.per, least) - 1) / GROUP;
 #pragma unroll
-        for (int i = 0; i < SC_RING; ++i) copy_group();
+        for (int i = 0; i < RING; ++i) copy_next();
     }
     __device__ __forceinline__ void copy_group()
     {
@@ -372,38 +370,53 @@ template <typename E, int NT, bool TWICE> struct Ring {
         const uint32_t dst = (uint32_t)__cvta_generic_to_shared(place);
         if (cb >= 0 && cb < full) {
             // whole vectors, but the first of the row
-            if (cb > 0 || threadIdx.x >= s.lo) copy16<0 * NT * 16>(dst, src);
+            if (cb > 0 || threadIdx.x >= s.lo) copy16<0 * SC_NT * 16>(dst, src);
             else *place = no_vector<E>();
-            copy16<1 * NT * 16>(dst, src);
-            copy16<2 * NT * 16>(dst, src);
-            copy16<3 * NT * 16>(dst, src);
+            copy16<1 * SC_NT * 16>(dst, src);
+            copy16<2 * SC_NT * 16>(dst, src);
+            copy16<3 * SC_NT * 16>(dst, src);
         } else if (cb == full) {
             const int i = cb * GROUP + threadIdx.x;
             if (i < s.lo) *place = no_vector<E>();
-            else if (i < s.hi) copy16<0 * NT * 16>(dst, src);
-            if (i + NT < s.hi) copy16<1 * NT * 16>(dst, src);
-            if (i + 2 * NT < s.hi) copy16<2 * NT * 16>(dst, src);
-            if (i + 3 * NT < s.hi) copy16<3 * NT * 16>(dst, src);
+            else if (i < s.hi) copy16<0 * SC_NT * 16>(dst, src);
+            if (i + SC_NT < s.hi) copy16<1 * SC_NT * 16>(dst, src);
+            if (i + 2 * SC_NT < s.hi) copy16<2 * SC_NT * 16>(dst, src);
+            if (i + 3 * SC_NT < s.hi) copy16<3 * SC_NT * 16>(dst, src);
         }
         copy_commit();  // (behind the last group, groups of nothing: the waits below count them)
-        to = to + GROUP == SC_RING * GROUP ? 0 : to + GROUP;
-        if (TWICE && !again && cb == full) {
-            again = true;  // the same group once more
-            return;
-        }
-        src += TWICE && again ? -GROUP * 16 : GROUP * 16;
-        cb += TWICE && again ? -1 : 1;
     }
     // the oldest group has arrived; this thread's first vector of it
     __device__ __forceinline__ uint4* first() const
     {
-        asm volatile("cp.async.wait_group %0;" ::"n"(SC_RING - 1) : "memory");
+        asm volatile("cp.async.wait_group %0;" ::"n"(RING - 1) : "memory");
         return buf + from;
+    }
+    __device__ __forceinline__ void copy_next()
+    {
+        copy_group();
+        to = to + GROUP == RING * GROUP ? 0 : to + GROUP;
+        src += GROUP * 16;
+        ++cb;
     }
     __device__ __forceinline__ void used()
     {
-        from = from + GROUP == SC_RING * GROUP ? 0 : from + GROUP;
+        from = from + GROUP == RING * GROUP ? 0 : from + GROUP;
+        copy_next();
+    }
+    // the second time: groups in reverse, the last of them from where they are
+    __device__ __forceinline__ void turn()
+    {
+        cb = full - RING;
+        src = s.src + ((int64_t)cb * GROUP + threadIdx.x) * 16;
+        from = full % RING * GROUP;
+    }
+    __device__ __forceinline__ void used_again()
+    {
+        to = from;
         copy_group();
+        from = from == 0 ? (RING - 1) * GROUP : from - GROUP;
+        src -= GROUP * 16;
+        --cb;
     }
     __device__ __forceinline__ bool has_edge() const
     {
@@ -486,8 +499,8 @@ template <typename E, bool ENTROPY, bool RANK> struct Summer {
             }
         }
     }
-    // vectors i, i + NT, ...; returns their largest element
-    template <int NT, int N> __device__ __forceinline__ float take(const uint4 (&w)[N], int i, int batch)
+    // vectors i, i + SC_NT, ...; returns their largest element
+    template <int N> __device__ __forceinline__ float take(const uint4 (&w)[N], int i, int batch)
     {
         typename Vec<E>::Most most = Vec<E>::top_of(w[0]);
 #pragma unroll
@@ -522,7 +535,7 @@ template <typename E, bool ENTROPY, bool RANK> struct Summer {
         if (RANK && mx >= x) {
             typename Vec<E>::Count n = Vec<E>::above(w[0], i < tvec ? under : at);
 #pragma unroll
-            for (int j = 1; j < N; ++j) n = Vec<E>::more(n, Vec<E>::above(w[j], i + j * NT < tvec ? under : at));
+            for (int j = 1; j < N; ++j) n = Vec<E>::more(n, Vec<E>::above(w[j], i + j * SC_NT < tvec ? under : at));
             ahead += Vec<E>::number(n);
         }
         return mx;
@@ -538,12 +551,11 @@ template <typename E, bool ENTROPY, bool RANK> struct Summer {
         r.t = a + z;
         return r;
     }
-    // A slice in the ring, and its edge.  change(b, v): before this thread's vectors v, v + NT, ... of group b are read
+    // A slice in the ring, and its edge.  change(b, v): before this thread's vectors v, v + SC_NT, ... of group b are read
     // (full + 1: the edge); seen(b, x): their largest element.
     template <typename R, typename Change, typename Seen>
     __device__ __forceinline__ void stream(R& ring, uint4 edge, Change change, Seen seen)
     {
-        constexpr int NT = R::GROUP / SC_GROUP;
         int i = threadIdx.x;
 #pragma unroll 1
         for (int b = 0; b < ring.full; ++b, i += R::GROUP) {
@@ -551,23 +563,23 @@ template <typename E, bool ENTROPY, bool RANK> struct Summer {
             change(b, v);
             uint4 w[SC_GROUP];
 #pragma unroll
-            for (int j = 0; j < SC_GROUP; ++j) w[j] = v[j * NT];
-            seen(b, take<NT>(w, i, b));
+            for (int j = 0; j < SC_GROUP; ++j) w[j] = v[j * SC_NT];
+            seen(b, take(w, i, b));
             ring.used();
         }
         uint4* v = ring.first();
         change(ring.full, v);
         float mx = -INFINITY;
 #pragma unroll 1
-        for (; i < ring.s.hi; i += NT, v += NT) {
+        for (; i < ring.s.hi; i += SC_NT, v += SC_NT) {
             const uint4 w[1] = {*v};
-            mx = fmax_nan(mx, take<NT>(w, i, ring.full));
+            mx = fmax_nan(mx, take(w, i, ring.full));
         }
         ring.used();
         if (ring.has_edge()) {
             change(ring.full + 1, &edge);
             const uint4 w[1] = {edge};
-            mx = fmax_nan(mx, take<NT>(w, ring.edge_at(), ring.full));
+            mx = fmax_nan(mx, take(w, ring.edge_at(), ring.full));
         }
         seen(ring.full, mx);
     }
@@ -601,13 +613,13 @@ template <typename E> __device__ __forceinline__ E* grad_of(const ScoreParams& p
 
 // ---- gradients ----------------------------------------------------------------- //
 // a row without a gradient, by the cluster's CTAs
-template <typename E, int NT> __device__ void zero_grad(const ScoreParams& p, int r, int rank, int C)
+template <typename E> __device__ void zero_grad(const ScoreParams& p, int r, int rank, int C)
 {
     E* g = grad_of<E>(p, r);
     const int head = (int)min((int64_t)p.V, (int64_t)(-(intptr_t)((uintptr_t)g / sizeof(E))) & (EPV<E> - 1));
-    const int nv = (p.V - head) / EPV<E>, i0 = rank * NT + threadIdx.x;
+    const int nv = (p.V - head) / EPV<E>, i0 = rank * SC_NT + threadIdx.x;
     uint4* to = (uint4*)(g + head);
-    for (int i = i0; i < nv; i += C * NT) to[i] = make_uint4(0, 0, 0, 0);
+    for (int i = i0; i < nv; i += C * SC_NT) to[i] = make_uint4(0, 0, 0, 0);
     if (i0 < head) g[i0] = narrow<E>(0.f);
     const int rest = head + nv * EPV<E> + i0;
     if (rest < p.V) g[rest] = narrow<E>(0.f);
@@ -639,7 +651,6 @@ __device__ __forceinline__ uint4 joined(const uint4& w, int a)
 template <typename E, bool FAST, typename R, typename F>
 __device__ __forceinline__ void grad_slice_(R& ring, const uint4& edge, E* g, float m, float c, uint32_t masked, F f)
 {
-    constexpr int NT = R::GROUP / SC_GROUP;
     const Slice<E>& s = ring.s;
     const float ref = FAST ? -rintf(m * c) : m == -INFINITY ? 0.f : -m;
     const uint64_t r2 = pair(ref, ref), c2 = pair(c, c);
@@ -671,12 +682,13 @@ __device__ __forceinline__ void grad_slice_(R& ring, const uint4& edge, E* g, fl
     };
     const int a = (int)((-(intptr_t)out) & 15);  // bytes from a vector's place to the next 16-byte boundary
     int i = threadIdx.x + ring.full * R::GROUP;
+    ring.turn();
     if (a == 0) {
         char* to = out + (int64_t)i * 16;
         const uint4* last = ring.first();
         for (int j = 0; j < SC_GROUP; ++j)
-            if (i + j * NT >= s.lo && i + j * NT < s.hi) store(to + j * NT * 16, any(last[j * NT], ring.full));
-        ring.used();
+            if (i + j * SC_NT >= s.lo && i + j * SC_NT < s.hi) store(to + j * SC_NT * 16, any(last[j * SC_NT], ring.full));
+        ring.used_again();
 #pragma unroll 1
         for (int b = ring.full - 1; b >= 0; --b) {
             i -= R::GROUP;
@@ -685,16 +697,16 @@ __device__ __forceinline__ void grad_slice_(R& ring, const uint4& edge, E* g, fl
             uint4 w[SC_GROUP];
             if (is_masked(b)) {
 #pragma unroll
-                for (int j = 0; j < SC_GROUP; ++j) w[j] = grad(v[j * NT], std::true_type());
+                for (int j = 0; j < SC_GROUP; ++j) w[j] = grad(v[j * SC_NT], std::true_type());
             } else {
 #pragma unroll
-                for (int j = 0; j < SC_GROUP; ++j) w[j] = grad(v[j * NT], std::false_type());
+                for (int j = 0; j < SC_GROUP; ++j) w[j] = grad(v[j * SC_NT], std::false_type());
             }
             if (b > 0 || i >= s.lo) store(to, w[0]);
-            store(to + NT * 16, w[1]);
-            store(to + 2 * NT * 16, w[2]);
-            store(to + 3 * NT * 16, w[3]);
-            ring.used();
+            store(to + SC_NT * 16, w[1]);
+            store(to + 2 * SC_NT * 16, w[2]);
+            store(to + 3 * SC_NT * 16, w[3]);
+            ring.used_again();
         }
     } else {
         // the gradient's rows begin elsewhere in a vector than the logits': lanes have neighbouring vectors, and join
@@ -703,16 +715,16 @@ __device__ __forceinline__ void grad_slice_(R& ring, const uint4& edge, E* g, fl
         for (int b = ring.full; b >= 0; --b) {
             const uint4* v = ring.first();
             for (int j = 0; j < SC_GROUP; ++j) {
-                const int i = threadIdx.x + b * R::GROUP + j * NT;
+                const int i = threadIdx.x + b * R::GROUP + j * SC_NT;
                 if (i - lane >= s.hi) continue;  // none of the warp's
                 const bool in = i >= s.lo && i < s.hi;
-                const uint4 w = in ? any(v[j * NT], b) : no_vector<E>(), two = joined(w, a);
+                const uint4 w = in ? any(v[j * SC_NT], b) : no_vector<E>(), two = joined(w, a);
                 if (!in) continue;
                 if (lane < 31 && i + 1 < s.hi) store(out + (int64_t)i * 16 + a, two);
                 else elements(w, i, q, EPV<E>);
                 if (lane == 0 || i == s.lo) elements(w, i, 0, q);
             }
-            ring.used();
+            ring.used_again();
         }
     }
     if (ring.has_edge()) elements(any(edge, ring.full), ring.edge_at(), 0, EPV<E>);
@@ -734,10 +746,10 @@ struct ScoreKernel {
 struct ScoreLaunch {
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute at[1];
-    ScoreLaunch(int C, int threads, size_t smem, cudaStream_t s)
+    ScoreLaunch(int C, size_t smem, cudaStream_t s)
     {
         cfg.gridDim = dim3((unsigned)C);
-        cfg.blockDim = dim3(threads);
+        cfg.blockDim = dim3(SC_NT);
         cfg.dynamicSmemBytes = smem;
         cfg.stream = s;
         at[0].id = cudaLaunchAttributeClusterDimension;
@@ -750,13 +762,13 @@ struct ScoreLaunch {
 
 // to be called before the others: `least` to `most` bytes of shared memory for the kernel
 template <typename K>
-cudaError_t score_ready(K kernel, ScoreKernel& sk, int threads, size_t least, size_t most)
+cudaError_t score_ready(K kernel, ScoreKernel& sk, size_t least, size_t most)
 {
     static_assert(SC_MAXC == 8, "four powers of two");
     return cuda_once(sk.once, nullptr, [&](int dev, int*) {
         cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
         for (int i = 0; i < 4 && e == cudaSuccess; ++i) {
-            const ScoreLaunch l(1 << i, threads, least, nullptr);
+            const ScoreLaunch l(1 << i, least, nullptr);
             e = cudaOccupancyMaxActiveClusters(&sk.clusters[dev][i], kernel, &l.cfg);
         }
         return e;
@@ -764,10 +776,10 @@ cudaError_t score_ready(K kernel, ScoreKernel& sk, int threads, size_t least, si
 }
 
 // Launches a cluster of p.cluster CTAs for every row.
-template <typename K> cudaError_t score_launch(K kernel, ScoreParams& p, int threads, size_t smem, cudaStream_t s)
+template <typename K> cudaError_t score_launch(K kernel, ScoreParams& p, size_t smem, cudaStream_t s)
 {
     p.by_tokens = FastDiv(p.T);
-    ScoreLaunch l(p.cluster, threads, smem, s);
+    ScoreLaunch l(p.cluster, smem, s);
     l.cfg.gridDim = dim3((unsigned)p.rows * p.cluster);
     return cudaLaunchKernelEx(&l.cfg, kernel, p);
 }
@@ -799,21 +811,20 @@ cudaError_t score_split_forward(const ScoreKernel& sk, ScoreParams& p, size_t si
     }
     return cudaSuccess;
 }
-// CTAs of a row with a gradient, four of them an SM (their shared memory sees to it): as many as it takes for the rows
-// under way to stay in L2 between their two passes, or all but a little of them, since the second pass begins with what
-// was read last; and few rows are spread over more, for the SMs that would idle, while every thread has a vector or
-// two.  2000 x 128256 bf16, 600 rows under way of 257 KB each: 208 us with two CTAs a row, 231 with one; 512 such rows
-// of a distillation loss, which one CTA each keeps under 140 MB: 62 with one, 64 with two.  Two CTAs an SM of 256
-// threads take 214 and 67, and 28 instead of 26 for 300 x 32000 fp32; 1500 x 100003 fp16 alone is faster with them
-// (138 instead of 147).
-constexpr size_t SC_GRAD_BYTES = 46 * 1024;
+// CTAs of a row with a gradient, four of them an SM (their rings see to it): as many as it takes for the rows under way,
+// as long as they are two passes over, to have room in L2 beside what else goes through it; and few rows are spread over
+// more, for the SMs that would idle, while every thread has a vector or two.  What a ring holds at the turn, a third or
+// more of a slice, is not read again at all: rings of 4, 5, 6 groups take 204, 201, 200 us for 2000 x 128256 bf16 and
+// 174, 171, 169 for 777 x 128256 fp32.  With 140 MB instead of 100 under way 1500 x 100003 fp16 take 136 us, not 124 (a
+// row of L2's misses to one of hits), with 60 MB 151 (more CTAs a row, each with its entries and joins).
+constexpr size_t SC_GRAD_BYTES = SC_RING_GRAD * SC_GROUP_BYTES;
 inline void score_split_gradient(ScoreParams& p, size_t size, int num_sms)
 {
     const int row = score_vectors(p, size);
     const double under_way = 4.0 * num_sms < p.rows ? 4.0 * num_sms : p.rows;
     int C = 1;
     while (C < SC_MAXC && ((under_way / C) * row * 16 > SCORE_L2_ROWS ||
-                           ((int64_t)p.rows * C < 2 * num_sms && row / (2 * C) >= SC_NT_GRAD)))
+                           ((int64_t)p.rows * C < 2 * num_sms && row / (2 * C) >= SC_NT)))
         C *= 2;
     p.cluster = C;
     p.per = (row + C - 1) / C;
