@@ -339,10 +339,9 @@ template <typename E, bool GRAD> __device__ __forceinline__ void distill_row(con
         return;
     }
     // every CTA of the cluster runs before another stores into its shared memory
-    if (C > 1) cluster_arrive();
+    if (C > 1) cluster_begin();
     Teacher te;
     begin_teacher(p, es, en, tmax, lse, te);
-    if (GRAD || rank == 0) sum_entries(p, es, en);
     Leaving<E> leaving(es);
     Summer<E, false, false> rest;
     rest.c = p.c;
@@ -354,6 +353,7 @@ template <typename E, bool GRAD> __device__ __forceinline__ void distill_row(con
         },
         [](int, float) {});
     Run run = rest.result();
+    if (GRAD || rank == 0) sum_entries(p, es, en);  // (their logits have come by now)
     KdPart w;
     w.m = warp_max(run.m);
     to_max(run, w.m, p.c);

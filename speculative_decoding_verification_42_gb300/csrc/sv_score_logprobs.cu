@@ -298,7 +298,7 @@ template <typename E, bool TOP> __global__ void __launch_bounds__(SC_NT, TOP ? 4
         return;
     }
     // every CTA of the cluster runs before another stores into its shared memory
-    if (C > 1) cluster_arrive();
+    if (C > 1) cluster_begin();
     const E* x = row_of<E>(p, r);
     const Slice<E> sl(p, x, rank);
     Ring<E, SC_RING> ring(p, sl, rank, smem);
@@ -392,11 +392,11 @@ template <typename E> __global__ void __launch_bounds__(SC_NT, 4) k_score_logpro
         return;
     }
     // every CTA of the cluster runs before another stores into its shared memory
-    if (C > 1) cluster_arrive();
+    if (C > 1) cluster_begin();
     const E* x = row_of<E>(p, r);
     const Slice<E> sl(p, x, rank);
     Ring<E, SC_RING_GRAD> ring(p, sl, rank, smem);
-    const float xt = widen(x[id]);
+    const E xt = x[id];  // (waited for where it is used)
     const uint4 edge = ring.edge();
     Summer<E, true, false> sum;
     sum.c = p.c;
@@ -421,7 +421,7 @@ template <typename E> __global__ void __launch_bounds__(SC_NT, 4) k_score_logpro
         const LpRow row = join(parts, p.c, C * W);
         if (lane == 0) {
             s_row = row;
-            if (rank == 0) write_row(p, r, row, xt);
+            if (rank == 0) write_row(p, r, row, widen(xt));
         }
     }
     __syncthreads();

@@ -272,6 +272,8 @@ __device__ __forceinline__ int cluster_id()
     asm volatile("mov.u32 %0, %%clusterid.x;" : "=r"(r));
     return r;
 }
+// (nothing is written before it that the others read)
+__device__ __forceinline__ void cluster_begin() { asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory"); }
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
 // the address of a shared variable in CTA `rank` of the cluster
@@ -814,9 +816,10 @@ cudaError_t score_split_forward(const ScoreKernel& sk, ScoreParams& p, size_t si
 // CTAs of a row with a gradient, four of them an SM (their rings see to it): as many as it takes for the rows under way,
 // as long as they are two passes over, to have room in L2 beside what else goes through it; and few rows are spread over
 // more, for the SMs that would idle, while every thread has a vector or two.  What a ring holds at the turn, a third or
-// more of a slice, is not read again at all: rings of 4, 5, 6 groups take 204, 201, 200 us for 2000 x 128256 bf16 and
-// 174, 171, 169 for 777 x 128256 fp32.  With 140 MB instead of 100 under way 1500 x 100003 fp16 take 136 us, not 124 (a
-// row of L2's misses to one of hits), with 60 MB 151 (more CTAs a row, each with its entries and joins).
+// more of a slice, is not read again at all: rings of 4, 5, 6 groups took 204, 201, 200 us for 2000 x 128256 bf16 and
+// 174, 171, 169 for 777 x 128256 fp32.  With 140 MB instead of 100 under way 1500 x 100003 fp16 take 136 us, not 124
+// (L2 loses more of what comes again), with 60 MB 143, and 777 x 128256 fp32 178, not 169 (more CTAs a row, each with
+// its entries and joins).  Three CTAs an SM with rings of 8 take 190, 135, 169, and 28, not 24, for 300 x 32000 fp32.
 constexpr size_t SC_GRAD_BYTES = SC_RING_GRAD * SC_GROUP_BYTES;
 inline void score_split_gradient(ScoreParams& p, size_t size, int num_sms)
 {
