@@ -82,10 +82,11 @@ struct Teacher {
 // What the threads of a CTA tell one another of a row's entries.  The entries of a slice are chained by the thread whose
 // vectors they lie in (head, next), with their place there: copy group (the row's ends being group full + 1) and element
 // of the group.
-constexpr int SC_SEEN = 32768;  // places of ids
+constexpr int SC_SEEN = 16384;  // places of ids
 struct EntryShared {
     int32_t ids[EPT * SC_NT];
-    int32_t next[EPT * SC_NT], place[EPT * SC_NT];
+    int16_t next[EPT * SC_NT];
+    uint16_t place[EPT * SC_NT];  // a slice has fewer than 256 groups
     int32_t head[SC_NT];
     uint32_t seen[SC_SEEN / 32];
     uint32_t state;                          // 1: a bad id; 2: two ids with one place in `seen`
@@ -119,15 +120,16 @@ __device__ __forceinline__ void enter(const ScoreParams& p, EntryShared& es, Ent
             atomicOr(&es.state, 1u);
             continue;
         }
-        const uint32_t at = (uint32_t)(id ^ id >> 15) % SC_SEEN, bit = 1u << (at % 32);
+        const uint32_t at = (uint32_t)(id ^ id >> 14) % SC_SEEN, bit = 1u << (at % 32);
         if (atomicOr(es.seen + at / 32, bit) & bit) atomicOr(&es.state, 2u);
         if (id < sl.first) continue;
         const int i = (id - sl.first) / EPV<E>, q = (id - sl.first) % EPV<E>;
         if (i >= sl.n) continue;
         const bool inner = i >= sl.lo && i < sl.hi;
         const int owner = inner ? i % SC_NT : i < sl.lo ? 0 : 32;
+        static_assert(SCORE_MAX_ROW_BYTES / SC_GROUP_BYTES + 3 < 256, "a place's group");
         es.place[e] = inner ? i / (SC_NT * SC_GROUP) << 8 | i / SC_NT % SC_GROUP * EPV<E> + q : (full + 1) << 8 | q;
-        es.next[e] = atomicExch(es.head + owner, e);
+        es.next[e] = (int16_t)atomicExch(es.head + owner, e);
     }
     tmax = warp_max(tmax);
     if (tid % 32 == 0) es.w_max[tid / 32] = tmax;
@@ -398,7 +400,7 @@ template <typename E, bool GRAD> __device__ __forceinline__ void distill_row(con
     finish(p, r, row, te, en.l);
 }
 
-template <typename E> __global__ void __launch_bounds__(SC_NT, 5) k_score_distill(const ScoreParams p)
+template <typename E> __global__ void __launch_bounds__(SC_NT, 6) k_score_distill(const ScoreParams p)
 {
     distill_row<E, false>(p);
 }
