@@ -26,15 +26,17 @@ struct LpRow {
 // which CTA 0 puts in order.
 constexpr int SC_GROUPS = 512;
 constexpr int SC_AGAIN = 512;       // copy groups of a CTA that are read again
+// It is where the ring was: used when every CTA of the row is through with its slice.  Behind the ring are the keys that
+// the CTAs exchange, which may come earlier, and Bits<E> [full + 1][SC_NT]: the largest element of each thread's copy
+// groups.
 struct TopScratch {
     unsigned long long list[SC_LIST];  // CTA 0: candidates, key and inverted id, SC_LIST / C to a CTA
-    uint32_t keys[SC_GROUPS];
     uint32_t again[SC_AGAIN];          // copy group * SC_NT + thread
     int32_t counts[SC_MAXC];           // CTA 0: candidates of each CTA
     int32_t mine, agains;              // candidates of this CTA, entries of `again`
     int32_t tally[2][(SC_NT / 32)];
-    int32_t pad;
-};  // and behind it, Bits<E> [full + 1][SC_NT]: the largest element of each thread's copy groups
+};
+static_assert(sizeof(TopScratch) <= SC_RING * SC_GROUP_BYTES, "where the ring was");
 
 __device__ __forceinline__ int tally_of(TopScratch& ts, int round, int x)
 {
@@ -146,7 +148,7 @@ __device__ void give_candidates(const Slice<E>& sl, int V, int full, TopScratch&
 
 // the keys of this thread's copy groups, 512 / C from a CTA, to all CTAs
 template <typename E>
-__device__ __forceinline__ void give_keys(TopScratch& ts, const Bits<E>* most, int full, int rank, int C)
+__device__ __forceinline__ void give_keys(const uint32_t* keys, const Bits<E>* most, int full, int rank, int C)
 {
     const int tid = threadIdx.x, parts = C == 1 ? 4 : C == 2 ? 2 : 1, per = (full + parts) / parts;
     int b = 0;
@@ -156,19 +158,19 @@ __device__ __forceinline__ void give_keys(TopScratch& ts, const Bits<E>* most, i
         uint32_t k = key_of(m);
         if (C == 8) {
             k = max(k, __shfl_xor_sync(~0u, k, 1));
-            for (int i = tid % 2; i < C; i += 2) remote_st(remote(ts.keys + (rank * SC_NT + tid) / 2, i), k);
+            for (int i = tid % 2; i < C; i += 2) remote_st(remote(keys + (rank * SC_NT + tid) / 2, i), k);
         } else {
-            for (int i = 0; i < C; ++i) remote_st(remote(ts.keys + (rank * parts + q) * SC_NT + tid, i), k);
+            for (int i = 0; i < C; ++i) remote_st(remote(keys + (rank * parts + q) * SC_NT + tid, i), k);
         }
     }
 }
-__device__ __forceinline__ uint32_t bound_of(const TopScratch& ts, int n)
+__device__ __forceinline__ uint32_t bound_of(const uint32_t* keys, int n)
 {
     uint32_t mine[SC_GROUPS / 32], lo = ~0u, hi = 0;
     int k = 0;
 #pragma unroll
     for (int i = 0; i < SC_GROUPS / 32; ++i) {
-        mine[i] = ts.keys[i * 32 + threadIdx.x % 32];
+        mine[i] = keys[i * 32 + threadIdx.x % 32];
         hi = max(hi, mine[i]);
         if (mine[i] > KEY_NEG_INF) {
             lo = min(lo, mine[i]);
@@ -286,7 +288,7 @@ __device__ __forceinline__ void write_row(const ScoreParams& p, int r, const LpR
     if (p.lse) p.lse[r] = ok ? row.m * p.inv_temp + logz : nan;
 }
 
-template <typename E, bool TOP> __global__ void __launch_bounds__(SC_NT, TOP ? 4 : 6) k_score_logprobs(const ScoreParams p)
+template <typename E, bool TOP> __global__ void __launch_bounds__(SC_NT, TOP ? 5 : 6) k_score_logprobs(const ScoreParams p)
 {
     extern __shared__ __align__(16) unsigned char smem[];
     __shared__ LpPart parts[SC_MAXC * (SC_NT / 32)];
@@ -305,8 +307,9 @@ template <typename E, bool TOP> __global__ void __launch_bounds__(SC_NT, TOP ? 4
     const E raw = x[id];
     const uint4 edge = ring.edge();
     const float xt = widen(raw);
-    TopScratch& ts = *(TopScratch*)(smem + SC_RING * SC_GROUP_BYTES);
-    Bits<E>* const most = (Bits<E>*)(&ts + 1);
+    TopScratch& ts = *(TopScratch*)smem;
+    uint32_t* const keys = (uint32_t*)(smem + SC_RING * SC_GROUP_BYTES);
+    Bits<E>* const most = (Bits<E>*)(keys + SC_GROUPS);
     int ahead = 0;
     Run run;
     auto none = [](int, uint4*) {};
@@ -352,13 +355,13 @@ template <typename E, bool TOP> __global__ void __launch_bounds__(SC_NT, TOP ? 4
         remote_st(to + 8, __float_as_uint(w.t));
         remote_st(to + 12, (uint32_t)w.ahead);
     }
-    if (TOP) give_keys<E>(ts, most, ring.full, rank, C);
+    if (TOP) give_keys<E>(keys, most, ring.full, rank, C);
     row_arrive(C);
     if (!TOP && rank != 0) return;
     row_wait(C);
     if (tid < 32) {
         LpRow row = join(parts, p.c, C * (SC_NT / 32));
-        if (TOP) row.bound = bound_of(ts, p.top_n);
+        if (TOP) row.bound = bound_of(keys, p.top_n);
         if (lane == 0) {
             if (rank == 0) write_row(p, r, row, xt);
             if (TOP) ts.mine = ts.agains = 0;
@@ -455,7 +458,7 @@ template <typename E, bool TOP> cudaError_t go_forward(ScoreParams p, int num_sm
     static ScoreKernel sk;
     const auto kernel = k_score_logprobs<E, TOP>;
     auto smem = [](size_t per) {
-        return SC_RING * SC_GROUP_BYTES + (TOP ? sizeof(TopScratch) + (per / (SC_NT * SC_GROUP) + 2) * SC_NT * sizeof(E) : 0);
+        return SC_RING * SC_GROUP_BYTES + (TOP ? SC_GROUPS * 4 + (per / (SC_NT * SC_GROUP) + 2) * SC_NT * sizeof(E) : 0);
     };
     cudaError_t e = score_ready(kernel, sk, smem(0), smem(SCORE_MAX_ROW_BYTES / 16 + 2));
     if (e == cudaSuccess) e = score_split_forward(sk, p, sizeof(E), num_sms, TOP ? 48 : 16, smem);
