@@ -323,6 +323,7 @@ template <typename E, bool GRAD> __device__ __forceinline__ void distill_row(con
     const int C = p.cluster, rank = (int)cluster_rank(), r = cluster_id(), tid = threadIdx.x, lane = tid % 32;
     Entries en;
     en.fetch(p, r);
+    const float lse = p.teacher_lse ? p.teacher_lse[r] : 0.f, g_loss = GRAD && p.g_loss ? p.g_loss[r] : 1.f;
     clear(es);
     if (!__syncthreads_or(en.some())) {
         no_distill<E>(p, r, SPEC_ROW_OK, rank, C);
@@ -333,7 +334,6 @@ template <typename E, bool GRAD> __device__ __forceinline__ void distill_row(con
     Ring<E, GRAD ? SC_RING_GRAD : SC_RING> ring(p, sl, rank, smem);
     en.fetch_logits(x, p.V);
     const uint4 edge = ring.edge();
-    const float lse = p.teacher_lse ? p.teacher_lse[r] : 0.f;
     enter(p, es, en, sl, ring.full);
     __syncthreads();
     const bool bad = bad_entries(es, en);
@@ -386,7 +386,7 @@ template <typename E, bool GRAD> __device__ __forceinline__ void distill_row(con
     const KdRow row = s_row;
     if (GRAD) {
         if (finite_row(row.m)) {
-            const float gl = (p.g_loss ? p.g_loss[r] : 1.f) * p.inv_temp, ps = (te.in + te.left) * row.inv_z;
+            const float gl = g_loss * p.inv_temp, ps = (te.in + te.left) * row.inv_z;
             const float pr = gl * (ps * row.scale - te.left * row.inv_sr);
             const uint64_t pr2 = pair(pr, pr);
             E* g = grad_of<E>(p, r);

@@ -409,7 +409,9 @@ template <typename E> __global__ void __launch_bounds__(SC_NT, 4) k_score_logpro
     const E* x = row_of<E>(p, r);
     const Slice<E> sl(p, x, rank);
     Ring<E, SC_RING_GRAD> ring(p, sl, rank, smem);
-    const E xt = x[id];  // (waited for where it is used)
+    // (waited for where they are used)
+    const E xt = x[id];
+    const float gl = p.g_logprob ? p.g_logprob[r] : 0.f, gh = p.g_entropy ? p.g_entropy[r] : 0.f;
     const uint4 edge = ring.edge();
     Summer<E, true, false> sum;
     sum.c = p.c;
@@ -445,7 +447,6 @@ template <typename E> __global__ void __launch_bounds__(SC_NT, 4) k_score_logpro
         return;
     }
     // e (A + B d), e = 2^d: p = e / s, ln p = d ln 2 - ln s
-    const float gl = p.g_logprob ? p.g_logprob[r] : 0.f, gh = p.g_entropy ? p.g_entropy[r] : 0.f;
     const float f = p.inv_temp / row.s, A = -(gl - gh * LN2 * (row.t / row.s)) * f, B = -gh * LN2 * f;
     const uint64_t A2 = pair(A, A), B2 = pair(B, B);
     E* g = grad_of<E>(p, r);
@@ -457,7 +458,7 @@ template <typename E> __global__ void __launch_bounds__(SC_NT, 4) k_score_logpro
     if (p.g_logprob && ring.has(id)) {
         __syncthreads();
         if (tid == 0) {
-            const float d = dist(xt, row.m, p.c), e = ex2_fast(d);
+            const float d = dist(widen(xt), row.m, p.c), e = ex2_fast(d);
             g[id] = narrow<E>(gl * p.inv_temp + e * (A + B * fmaxf(d, NONE)));
         }
     }
