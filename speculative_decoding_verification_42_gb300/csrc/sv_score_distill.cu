@@ -12,7 +12,7 @@
 // Entries leave the ring before their thread reads it (a chain per thread), so the
 // pass is the plain one.  Measured with L2 flushed: 2048 x 152064 bf16 with 64
 // entries 105 us (six CTAs an SM, 0.71 of a copy; five took 112), gradients of
-// 777 x 128256 fp32 with 128 entries 169 us and of 1500 x 100003 fp16 124 us (0.7).
+// 777 x 128256 fp32 with 128 entries 167 us and of 1500 x 100003 fp16 122 us (0.7).
 #include "sv_score_row.cuh"
 
 namespace sv {
