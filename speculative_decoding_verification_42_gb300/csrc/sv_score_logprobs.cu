@@ -446,13 +446,14 @@ template <typename E> __global__ void __launch_bounds__(SC_NT, 4) k_score_logpro
         zero_grad<E>(p, r, rank, C);
         return;
     }
-    // e (A + B d), e = 2^d: p = e / s, ln p = d ln 2 - ln s
+    // e (A + B d), e = 2^d: p = e / s, ln p = d ln 2 - ln s.  The product e d comes first, which is 0 where e is; B d may
+    // be out of range there.
     const float f = p.inv_temp / row.s, A = -(gl - gh * LN2 * (row.t / row.s)) * f, B = -gh * LN2 * f;
     const uint64_t A2 = pair(A, A), B2 = pair(B, B);
     E* g = grad_of<E>(p, r);
     if (p.g_entropy)
         grad_slice(ring, edge, g, row.m, p.c, sum.masked,
-                   [&](uint64_t d2, uint64_t e2) { return mul2(e2, fma2(B2, d2, A2)); });
+                   [&](uint64_t d2, uint64_t e2) { return fma2(mul2(e2, d2), B2, mul2(e2, A2)); });
     else
         grad_slice(ring, edge, g, row.m, p.c, 0, [&](uint64_t, uint64_t e2) { return mul2(e2, A2); });
     if (p.g_logprob && ring.has(id)) {

@@ -164,6 +164,21 @@ def test_logprobs_gradient(sv, kind, V):
     _check_logprobs(alone, _f64(x), None, temp, 0, kind, None, gh)
 
 
+@pytest.mark.parametrize("kind,V", [("bf16", 13), ("f32", 13), ("bf16", 5003), ("f32", 40001)])
+@pytest.mark.parametrize("temp", [1.46, 3.0, 40.0])
+def test_entropy_gradient_of_masks_of_the_lowest_value(sv, kind, V, temp):
+    """The distance of such a token over the temperature is in range, its product with an upstream gradient is not."""
+    rng = np.random.default_rng(V)
+    N, temp = 6, float(np.float32(temp))
+    x = _logits(rng, N, V, kind, "lowest")
+    tok = rng.integers(0, V, N)
+    gh = np.array([2.9, -7, 300, -1e4, 1e6, 0.1], np.float32)
+    gl = np.array([0, 1, -2, 0, 5, 1], np.float32)
+    got = sv.logprobs(x, _dev(tok.astype(np.int32)), temperature=temp, grad_logprob=_dev(gl), grad_entropy=_dev(gh))
+    assert not got["grad"].isnan().any()
+    _check_logprobs(got, _f64(x), tok, temp, 0, kind, gl, gh)
+
+
 def test_logprobs_without_tokens_and_row_statuses(sv):
     import torch
     rng = np.random.default_rng(3)
