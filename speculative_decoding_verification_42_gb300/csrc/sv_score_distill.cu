@@ -37,7 +37,6 @@ struct KdRow {
     float scale;      // of the rest's in the row's
     float inv_z, inv_sr;
 };
-__device__ __forceinline__ bool finite_row(float m) { return m > -INFINITY && m < INFINITY; }
 
 template <typename E> __device__ void no_distill(const ScoreParams& p, int r, int status, int rank, int C)
 {

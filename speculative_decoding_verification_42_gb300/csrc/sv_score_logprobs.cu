@@ -284,7 +284,6 @@ __device__ __forceinline__ LpRow join(const LpPart* parts, float c, int n)
     row.ahead = __reduce_add_sync(~0u, row.ahead);
     return row;
 }
-__device__ __forceinline__ bool finite_row(float m) { return m > -INFINITY && m < INFINITY; }
 
 // one thread: the results of a row (top tokens apart)
 __device__ __forceinline__ void write_row(const ScoreParams& p, int r, const LpRow& row, float xt)

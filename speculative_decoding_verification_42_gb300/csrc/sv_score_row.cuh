@@ -7,7 +7,7 @@
 // copy and its use: a ring of copy groups, where what it has used makes room for
 // what comes.
 //
-//   forward    one cluster per row: four or more CTAs share an SM, and two that
+//   forward    one cluster per row: five or six CTAs share an SM, and those that
 //              stream keep HBM busy while others begin or end
 //   gradient   the row's sum comes before the gradient's first element, so the
 //              row is streamed twice, the second time in reverse: first what the
@@ -601,6 +601,9 @@ template <typename X> __device__ __forceinline__ X warp_sum(X x)
 {
     return warp_reduce(x, [](X a, X b) { return a + b; });
 }
+
+// a row's largest logit, NaN where one is
+__device__ __forceinline__ bool finite_row(float m) { return m > -INFINITY && m < INFINITY; }
 
 template <typename E> __device__ __forceinline__ const E* row_of(const ScoreParams& p, int r)
 {
