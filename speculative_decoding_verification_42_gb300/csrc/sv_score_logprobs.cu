@@ -1,7 +1,7 @@
 // sv_score_logprobs.cu -- log probabilities of given tokens with rank, entropy
 // and top alternatives, and the gradient of log probability and entropy.
 //
-// ln p_x = (x - m) / t - ln s and H = ln s - ln 2 (sum d 2^d) / s, relative to m,
+// ln p_x = (x - m) / t - ln s and H = ln s - ln 2 (sum d 2^d) / s, relative to 2^B,
 // from one pass; the gradient p_v (A + B d_v) needs both and takes a second.
 // Measured with L2 flushed: 608 x 131072 bf16 30 us (5.3 TB/s; a pass is 5.9
 // instructions an element, issue 59 % where rows are short), fp32 53 us (6 TB/s);
@@ -285,15 +285,25 @@ __device__ __forceinline__ LpRow join(const LpPart* parts, float c, int n)
     return row;
 }
 
+// ln Z relative to the largest logit m, whose term in the sum is e = 2^d.  Of a row that m dominates ln Z is what the other
+// terms are to e: so e is taken off as the instruction gave it, and its error is no part of the result.
+__device__ __forceinline__ float log_z(const LpRow& row, float c)
+{
+    const float e = ex2_fast(dist(row.m, row.m, c));
+    return log1pf((row.s - e) / e);
+}
+
 // one thread: the results of a row (top tokens apart)
 __device__ __forceinline__ void write_row(const ScoreParams& p, int r, const LpRow& row, float xt)
 {
     const bool ok = finite_row(row.m);
-    const float nan = __int_as_float(0x7FFFFFFF), ln = logf(row.s), logz = ln - dist(row.m, row.m, p.c) * LN2;
+    const float nan = __int_as_float(0x7FFFFFFF), logz = log_z(row, p.c);
     p.row_status[r] = ok ? SPEC_ROW_OK : SPEC_ROW_NONFINITE;
     if (p.logprob) p.logprob[r] = ok ? (xt - row.m) * p.inv_temp - logz : nan;
     if (p.rank) p.rank[r] = ok ? row.ahead : -1;
-    if (p.entropy) p.entropy[r] = ok ? ln - LN2 * (row.t / row.s) : nan;
+    // ln Z - sum p ln(p Z), the sum relative to m's term
+    if (p.entropy)
+        p.entropy[r] = ok ? fmaxf(0.f, logz + LN2 * (fmaf(dist(row.m, row.m, p.c), row.s, -row.t) / row.s)) : nan;
     if (p.lse) p.lse[r] = ok ? row.m * p.inv_temp + logz : nan;
 }
 
@@ -388,7 +398,7 @@ template <typename E, bool TOP> __global__ void __launch_bounds__(SC_NT, TOP ? 5
     row_arrive(C);
     if (rank != 0) return;
     row_wait(C);
-    write_top(p, r, ts, row, logf(row.s) - dist(row.m, row.m, p.c) * LN2, C);
+    write_top(p, r, ts, row, log_z(row, p.c), C);
 }
 
 template <typename E> __global__ void __launch_bounds__(SC_NT, 4) k_score_logprobs_grad(const ScoreParams p)
